@@ -15,7 +15,9 @@ _BINDING_NAMES = ("kda_status_string", "kda_plan_segments", "kda_plan_check", "k
                   "kda_workspace_bytes", "kda_segment_forward", "kda_compose_summaries", "kda_apply_boundary",
                   "kda_forward_segmented", "kda_forward_two_pass", "kda_forward_segmented_noalloc",
                   "kda_device_status", "kda_selftest_wait_expiry", "kda_compose_summaries_blocked",
-                  "kda_scan_workspace_bytes", "kda_backward_segmented", "kda_backward_workspace_bytes", "upload_plan", "KDAError", "LIB_PATH")
+                  "kda_scan_workspace_bytes", "kda_backward_segmented", "kda_backward_workspace_bytes", "kda_gated_scan_forward",
+                  "kda_gated_scan_backward", "kda_gated_scan_workspace_bytes", "kda_gated_scan_step", "kda_block_norm_forward",
+                  "kda_block_norm_backward", "kda_block_norm_workspace_bytes", "kda_decode_step", "upload_plan", "KDAError", "LIB_PATH")
 
 
 def __getattr__(name):

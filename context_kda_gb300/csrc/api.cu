@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "elem.cuh"
 #include "kda_internal.cuh"
 
 namespace {
@@ -176,7 +177,8 @@ extern "C" int kda_device_status(void)
     }
     int worst = KDA_OK;
     for (int st : {kda::take_prep_status(), kda::take_state_status(), kda::take_compose_status(),
-                   kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status()})
+                   kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status(),
+                   kda::take_scan_status(), kda::take_decode_status()})
         if (st != KDA_OK && worst == KDA_OK) worst = st;
     return worst;
 }
@@ -509,4 +511,177 @@ extern "C" int kda_backward_segmented(const int32_t *plan, const int32_t *plan_d
         reinterpret_cast<const float *>(b + off[1]), reinterpret_cast<float *>(b + off[7]),
         reinterpret_cast<unsigned char *>(b + off[8]),
         reinterpret_cast<float *>(b + off[6]), kBackwardGrid, dq, dk, dv, dg, dbeta, dh0, s));
+}
+
+// ---- the operators around the KDA layer ------------------------------------------------------------
+
+namespace {
+
+// A tensor of rows: present, aligned to its elements, its rows at least 'width' apart.
+bool rows_ok(const void *p, int64_t ld, int64_t width, int bytes)
+{
+    return p && (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes)) == 0 && ld >= width;
+}
+bool rows_ok_or_null(const void *p, int64_t ld, int64_t width, int bytes) { return !p || rows_ok(p, ld, width, bytes); }
+bool floats_ok_or_null(const float *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool scan_in_ok(int32_t D, int32_t type, const kda::ScanIn &in)
+{
+    const int e = kda::elem_bytes(type);
+    return D >= 1 && e && rows_ok(in.x, in.ldx, D, e) && rows_ok_or_null(in.i, in.ldi, D, e) &&
+           rows_ok(in.g, in.ldg, D, 4) && floats_ok_or_null(in.h0);
+}
+
+// The workspace, where the call needs one.
+int scan_ws_ok(const int32_t *plan, int32_t D, const void *ws, size_t ws_bytes)
+{
+    const size_t need = kda::scan_workspace_bytes(plan[KDA_PH_T], D);
+    if (need && (!ws || !aligned16(ws))) return KDA_ERR_INVALID_ARG;
+    return ws_bytes < need ? KDA_ERR_WORKSPACE : KDA_OK;
+}
+
+bool norm_group_ok(int32_t D, int32_t group)
+{
+    return group == 0 || group == D ||
+           ((group == 32 || group == 64 || group == 128 || group == 256) && D % group == 0);
+}
+
+// What both directions of the block norm check of the arguments they share.
+int norm_in_ok(int64_t T, int32_t D, int32_t rtype, int32_t type, const kda::NormIn &a, float eps)
+{
+    const int e = kda::elem_bytes(type), re = kda::elem_bytes(rtype);
+    if (T < 0 || D < 1 || !e || !re || !(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (rtype != type && rtype != KDA_TYPE_F32) return KDA_ERR_UNSUPPORTED;
+    if (D > kda::NORM_MAX_D || !norm_group_ok(D, a.group)) return KDA_ERR_UNSUPPORTED;
+    if (a.gate != KDA_GATE_NONE && a.gate != KDA_GATE_SIGMOID && a.gate != KDA_GATE_SILU) return KDA_ERR_INVALID_ARG;
+    if (T == 0) return KDA_OK;   // no rows: their addresses do not matter
+    if ((a.gate != KDA_GATE_NONE) != (a.z != nullptr)) return KDA_ERR_INVALID_ARG;
+    if (!a.o && (a.z || a.w_post || a.ls)) return KDA_ERR_INVALID_ARG;
+    if (!rows_ok_or_null(a.r, a.ldr, D, re) || !rows_ok_or_null(a.o, a.ldo, D, e) || !rows_ok_or_null(a.z, a.ldz, D, e))
+        return KDA_ERR_INVALID_ARG;
+    if (!floats_ok_or_null(a.w_post) || !floats_ok_or_null(a.ls) || !floats_ok_or_null(a.w_pre)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kda_gated_scan_workspace_bytes(const int32_t *plan, int32_t D)
+{
+    return plan_ok(plan) && D >= 1 ? kda::scan_workspace_bytes(plan[KDA_PH_T], D) : 0;
+}
+
+extern "C" int kda_gated_scan_forward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
+                                      const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                                      const float *h0, void *h, int64_t ldh, float *final_state, float *states,
+                                      void *ws, size_t ws_bytes, void *stream)
+{
+    const kda::ScanIn in{x, i, g, h0, ldx, ldi, ldg};
+    if (!plan_ok(plan) || !plan_dev || !scan_in_ok(D, type, in)) return KDA_ERR_INVALID_ARG;
+    if (!rows_ok(h, ldh, D, kda::elem_bytes(type)) || !floats_ok_or_null(final_state) || !floats_ok_or_null(states))
+        return KDA_ERR_INVALID_ARG;
+    if (const int rc = scan_ws_ok(plan, D, ws, ws_bytes)) return rc;
+    return cuda_status(kda::launch_scan_forward(plan, plan_dev, D, type, in, h, ldh, final_state, states, ws,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_gated_scan_backward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
+                                       const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                                       const float *h0, const float *states, const void *dh, int64_t lddh,
+                                       const float *dfinal, void *dx, int64_t lddx, void *di, int64_t lddi, float *dg,
+                                       int64_t lddg, float *dh0, void *ws, size_t ws_bytes, void *stream)
+{
+    const kda::ScanIn in{x, i, g, h0, ldx, ldi, ldg};
+    const kda::ScanGrads out{dx, di, dg, dh0, lddx, lddi, lddg};
+    if (!plan_ok(plan) || !plan_dev || !scan_in_ok(D, type, in)) return KDA_ERR_INVALID_ARG;
+    const int e = kda::elem_bytes(type);
+    if (!states || !floats_ok_or_null(states) || !rows_ok(dh, lddh, D, e) || !floats_ok_or_null(dfinal))
+        return KDA_ERR_INVALID_ARG;
+    if (!rows_ok(dx, lddx, D, e) || !rows_ok_or_null(di, lddi, D, e) || !rows_ok(dg, lddg, D, 4) || !floats_ok_or_null(dh0))
+        return KDA_ERR_INVALID_ARG;
+    if (di && !i) return KDA_ERR_INVALID_ARG;
+    if (const int rc = scan_ws_ok(plan, D, ws, ws_bytes)) return rc;
+    return cuda_status(kda::launch_scan_backward(plan, plan_dev, D, type, in, states, dh, lddh, dfinal, out, ws,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_gated_scan_step(int32_t B, int32_t D, int32_t type, const int32_t *slots, int32_t num_slots,
+                                   const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                                   float *state, void *h, int64_t ldh, void *stream)
+{
+    const kda::ScanIn in{x, i, g, nullptr, ldx, ldi, ldg};
+    if (B < 0 || num_slots < 0 || (!slots && B > num_slots)) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return D >= 1 && kda::elem_bytes(type) ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (!scan_in_ok(D, type, in) || !state || !floats_ok_or_null(state) || !rows_ok(h, ldh, D, kda::elem_bytes(type)) ||
+        (reinterpret_cast<uintptr_t>(slots) & 3u))
+        return KDA_ERR_INVALID_ARG;
+    return cuda_status(kda::launch_scan_step(B, D, type, slots, num_slots, in, state, h, ldh,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t kda_block_norm_workspace_bytes(int32_t D)
+{
+    return D >= 1 && D <= kda::NORM_MAX_D ? kda::norm_workspace_bytes(D) : 0;
+}
+
+extern "C" int kda_block_norm_forward(int64_t T, int32_t D, int32_t res_type, int32_t type, const void *r, int64_t ldr,
+                                      const void *o, int64_t ldo, const void *z, int64_t ldz, int32_t gate, int32_t group,
+                                      const float *w_post, float scale, const float *ls, const float *w_pre, float eps,
+                                      void *r_out, int64_t ldr_out, void *y, int64_t ldy, void *stream)
+{
+    const kda::NormIn a{r, o, z, ldr, ldo, ldz, w_post, ls, w_pre, gate, group, scale, eps};
+    const int rc = norm_in_ok(T, D, res_type, type, a, eps);
+    if (rc != KDA_OK || T == 0) return rc;
+    if ((y != nullptr) != (w_pre != nullptr) || (!y && !r_out)) return KDA_ERR_INVALID_ARG;
+    if (!r && !o) return KDA_ERR_INVALID_ARG;
+    if (!rows_ok_or_null(r_out, ldr_out, D, kda::elem_bytes(res_type)) || !rows_ok_or_null(y, ldy, D, kda::elem_bytes(type)))
+        return KDA_ERR_INVALID_ARG;
+    return cuda_status(kda::launch_norm_forward(T, D, res_type, type, a, r_out, ldr_out, y, ldy,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_block_norm_backward(int64_t T, int32_t D, int32_t res_type, int32_t type, const void *r_out,
+                                       int64_t ldr_out, const void *o, int64_t ldo, const void *z, int64_t ldz,
+                                       int32_t gate, int32_t group, const float *w_post, float scale, const float *ls,
+                                       const float *w_pre, float eps, const void *dr_out, int64_t lddr_out, const void *dy,
+                                       int64_t lddy, void *dr, int64_t lddr, void *d_o, int64_t lddo, void *dz,
+                                       int64_t lddz, float *dw_post, float *dls, float *dw_pre, void *ws, size_t ws_bytes,
+                                       void *stream)
+{
+    const kda::NormIn a{r_out, o, z, ldr_out, ldo, ldz, w_post, ls, w_pre, gate, group, scale, eps};
+    const kda::NormGrads g{dr, d_o, dz, lddr, lddo, lddz, dw_post, dls, dw_pre};
+    if (const int rc = norm_in_ok(T, D, res_type, type, a, eps)) return rc;
+    const int e = kda::elem_bytes(type), re = kda::elem_bytes(res_type);
+    if ((dw_post && !w_post) || (dls && !ls) || (dw_pre && !w_pre)) return KDA_ERR_INVALID_ARG;
+    if (!floats_ok_or_null(dw_post) || !floats_ok_or_null(dls) || !floats_ok_or_null(dw_pre)) return KDA_ERR_INVALID_ARG;
+    if (T > 0) {
+        if ((dy != nullptr) != (w_pre != nullptr) || (!dy && !dr_out) || (w_pre && !r_out)) return KDA_ERR_INVALID_ARG;
+        if ((d_o != nullptr) != (o != nullptr) || (!dr && !d_o) || (dz && !z))
+            return KDA_ERR_INVALID_ARG;
+        if (!rows_ok_or_null(dr_out, lddr_out, D, re) || !rows_ok_or_null(dy, lddy, D, e) || !rows_ok_or_null(dr, lddr, D, re) ||
+            !rows_ok_or_null(d_o, lddo, D, e) || !rows_ok_or_null(dz, lddz, D, e))
+            return KDA_ERR_INVALID_ARG;
+    }
+    if (!ws || !aligned16(ws)) return KDA_ERR_INVALID_ARG;
+    if (ws_bytes < kda::norm_workspace_bytes(D)) return KDA_ERR_WORKSPACE;
+    return cuda_status(kda::launch_norm_backward(T, D, res_type, type, a, dr_out, lddr_out, dy, lddy, g, ws,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_decode_step(int32_t B, int32_t H, int32_t type, const int32_t *slots, int32_t num_slots, const void *q,
+                               int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const float *g,
+                               int64_t ldg, const float *beta, int64_t ldb, float scale, float *state, void *o, int64_t ldo,
+                               void *stream)
+{
+    const int e = kda::elem_bytes(type);
+    if (B < 0 || H < 1 || !e || num_slots < 0 || (!slots && B > num_slots)) return KDA_ERR_INVALID_ARG;
+    if (H > 65535) return KDA_ERR_UNSUPPORTED;
+    if (B == 0) return KDA_OK;
+    const int64_t w = static_cast<int64_t>(H) * kda::KD;
+    if (!rows_ok(q, ldq, w, e) || !rows_ok(k, ldk, w, e) || !rows_ok(v, ldv, w, e) || !rows_ok(g, ldg, w, 4) ||
+        !rows_ok(beta, ldb, H, 4) || !rows_ok(o, ldo, w, e) || !state || !aligned16(state) ||
+        (reinterpret_cast<uintptr_t>(slots) & 3u))
+        return KDA_ERR_INVALID_ARG;
+    const kda::DecodeIn in{q, k, v, g, beta, ldq, ldk, ldv, ldg, ldb};
+    return cuda_status(kda::launch_decode_step(B, H, type, slots, num_slots, in, scale, state, o, ldo,
+                                               static_cast<cudaStream_t>(stream)));
 }

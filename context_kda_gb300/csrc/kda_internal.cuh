@@ -214,4 +214,54 @@ cudaError_t launch_two_pass(const int32_t *plan_host, const int32_t *plan_dev, i
                             uint16_t *o, float *A, float *B, float *S_in, float *final_state,
                             unsigned char *pkg, cudaStream_t stream);
 
+// The operators around the KDA layer (gated_scan.cu, block_norm.cu, decode.cu).  Rows are [rows][D] with
+// a row stride (ld, in elements); null pointers stand for absent tensors as in kda.h.
+struct ScanIn {
+    const void *x, *i;     // [T][D] activations; i null: 1
+    const float *g, *h0;   // [T][D] log-decays; [N][D], null: zeros
+    int64_t ldx, ldi, ldg;
+};
+struct ScanGrads {
+    void *dx, *di;         // [T][D]; di null: not written
+    float *dg, *dh0;       // [T][D]; [N][D], null: not written
+    int64_t lddx, lddi, lddg;
+};
+size_t scan_workspace_bytes(int64_t T, int D);
+cudaError_t launch_scan_forward(const int32_t *plan_host, const int32_t *plan_dev, int D, int type, const ScanIn &in,
+                                void *h, int64_t ldh, float *final_state, float *states, void *ws, cudaStream_t stream);
+cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_dev, int D, int type, const ScanIn &in,
+                                 const float *states, const void *dh, int64_t lddh, const float *dfinal,
+                                 const ScanGrads &out, void *ws, cudaStream_t stream);
+cudaError_t launch_scan_step(int B, int D, int type, const int32_t *slots, int num_slots, const ScanIn &in,
+                             float *state, void *h, int64_t ldh, cudaStream_t stream);
+int take_scan_status();
+
+struct NormIn {
+    const void *r, *o, *z;            // residual (the forward's input, the backward's r'), branch, gate logits
+    int64_t ldr, ldo, ldz;
+    const float *w_post, *ls, *w_pre; // [group], [D], [D]
+    int gate, group;                  // group 0: the whole row
+    float scale, eps;
+};
+struct NormGrads {
+    void *dr, *d_o, *dz;              // null: not written
+    int64_t lddr, lddo, lddz;
+    float *dw_post, *dls, *dw_pre;
+};
+constexpr int NORM_MAX_D = 16384;
+size_t norm_workspace_bytes(int D);
+cudaError_t launch_norm_forward(int64_t T, int D, int rtype, int type, const NormIn &a, void *r_out, int64_t ldro, void *y,
+                                int64_t ldy, cudaStream_t stream);
+cudaError_t launch_norm_backward(int64_t T, int D, int rtype, int type, const NormIn &a, const void *dr_out, int64_t lddro,
+                                 const void *dy, int64_t lddy, const NormGrads &g, void *ws, cudaStream_t stream);
+
+struct DecodeIn {
+    const void *q, *k, *v;            // [B][H][128] with token strides
+    const float *g, *beta;            // [B][H][128], [B][H]
+    int64_t ldq, ldk, ldv, ldg, ldb;
+};
+cudaError_t launch_decode_step(int B, int H, int type, const int32_t *slots, int num_slots, const DecodeIn &in, float scale,
+                               float *state, void *o, int64_t ldo, cudaStream_t stream);
+int take_decode_status();
+
 }  // namespace kda

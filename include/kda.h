@@ -475,6 +475,145 @@ int kda_forward_segmented_noalloc(const int32_t *plan, const int32_t *plan_dev, 
                                   const float *g, const float *beta, const float *h0, float scale,
                                   kda_bf16 *o, float *final_state, void *stream);
 
+/* ---- The operators around the KDA layer --------------------------------------------------------------
+ *
+ * A decoder built on KDA interleaves it with a per-channel gated linear recurrence, puts norms around
+ * both, and serves both a token at a time.  These entry points follow the conventions above (host
+ * checks first, no allocation, the caller's stream), with their own about tensors:
+ *   - 'type' is the type of the activations, KDA_TYPE_*; everything is computed and summed in fp32 and
+ *     rounded to it once, at the store.  Decays, states, weights and weight gradients are fp32.
+ *   - A tensor of rows, [rows][D], comes with its row stride 'ld' in elements (ld >= D; consecutive
+ *     channels are adjacent), so it may be a column range of a wider matrix; such a tensor is aligned
+ *     to its element type only.  Widths, strides and addresses that keep every row on 16 bytes take
+ *     wide copies; others run too, slower.  Everything else is contiguous.
+ *   - Outputs must not overlap inputs unless said otherwise.
+ * A bad pointer, size, type code or stride returns KDA_ERR_INVALID_ARG and enqueues nothing. */
+enum { KDA_TYPE_BF16 = 0, KDA_TYPE_F16 = 1, KDA_TYPE_F32 = 2 };
+
+/* Tokens between two saved states of the gated recurrence. */
+enum { KDA_SCAN_TILE = 128 };
+
+/*
+ * kda_gated_scan_forward -- the gated linear recurrence of every sequence of the plan, per channel,
+ *     h_t = exp(g_t) h_{t-1} + i_t x_t,     h before a sequence's first token = its h0.
+ *   plan, plan_dev  a plan of kda_plan_segments and its device copy; its segments do not matter here.
+ *   D               channels (any number).
+ *   x, i            activations [T][D]; i (the input gate's value) NULL: 1.
+ *   g               fp32 [T][D] log-decays; any value (exp(g) is taken as it is).
+ *   h0              fp32 [N][D] or NULL (zeros).
+ *   h           out [T][D].
+ *   final_state out fp32 [N][D] (h after each sequence's last token) or NULL.
+ *   states      out fp32 [ceil(T / KDA_SCAN_TILE)][D] or NULL: what the backward needs, h in fp32 after
+ *                   token j KDA_SCAN_TILE - 1 of the packed stream (row 0: zeros).
+ *   ws, ws_bytes    device workspace of at least kda_gated_scan_workspace_bytes(plan, D) bytes (may be
+ *                   NULL where that is 0).
+ * A sequence never sees another's values, whatever they are.  Results do not depend on timing: the
+ * same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_WORKSPACE or KDA_ERR_CUDA.
+ */
+int kda_gated_scan_forward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
+                           const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                           const float *h0, void *h, int64_t ldh, float *final_state, float *states,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * kda_gated_scan_backward -- the gradients of kda_gated_scan_forward for
+ * L = sum <dh, h> + sum <dfinal, final_state>.  With G_t = dh_t + exp(g_{t+1}) G_{t+1} (dfinal in place
+ * of the second term at a sequence's last token):
+ *     dx = i G, di = x G, dg = exp(g) h_{t-1} G, dh0 = exp(g) G at the first token.
+ *   x, i, g, h0     the forward's inputs.    states  what the forward saved.
+ *   dh              [T][D].                  dfinal  fp32 [N][D] or NULL (zeros).
+ *   dx          out [T][D].                  di  out [T][D] or NULL (NULL when i is).
+ *   dg          out fp32 [T][D].             dh0 out fp32 [N][D] or NULL (defined also when h0 is NULL).
+ * Workspace, errors and the guarantees of the forward.
+ */
+int kda_gated_scan_backward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
+                            const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                            const float *h0, const float *states, const void *dh, int64_t lddh,
+                            const float *dfinal, void *dx, int64_t lddx, void *di, int64_t lddi, float *dg,
+                            int64_t lddg, float *dh0, void *ws, size_t ws_bytes, void *stream);
+
+/* Device workspace bytes of the two calls above (0: none needed, or the plan or D is invalid). */
+size_t kda_gated_scan_workspace_bytes(const int32_t *plan, int32_t D);
+
+/*
+ * kda_gated_scan_step -- one token of the recurrence for each of B rows: row b updates the state of its
+ * slot in place, s = exp(g_b) s + i_b x_b, and returns it as h_b.
+ *   slots           device int32 [B], or NULL (row b's slot is b; then B <= num_slots).  No slot may
+ *                   occur twice.  A negative slot marks padding: its h row is zeros, no state is touched.
+ *                   A slot >= num_slots is treated as padding and recorded: kda_device_status() then
+ *                   returns KDA_ERR_INVALID_ARG.
+ *   state           in/out fp32 [num_slots][D].
+ *   x, i, g, h      [B][D], as in the forward.
+ * B = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG or KDA_ERR_CUDA.
+ */
+int kda_gated_scan_step(int32_t B, int32_t D, int32_t type, const int32_t *slots, int32_t num_slots,
+                        const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
+                        float *state, void *h, int64_t ldh, void *stream);
+
+enum { KDA_GATE_NONE = 0, KDA_GATE_SIGMOID = 1, KDA_GATE_SILU = 2 };
+
+/*
+ * kda_block_norm_forward -- the norms after and before a block with the block's gate and the residual,
+ * in one pass over T rows:
+ *     n  = o / rms_group(o) * w_post      (n = o when w_post is NULL)
+ *     u  = act(z) * n                     (act: 1, sigmoid or silu, by 'gate'; z is given iff there is one)
+ *     r' = r + scale * ls * u             (r NULL: 0; ls NULL: 1)
+ *     y  = r' / rms_row(r') * w_pre       (only when w_pre is given; of r' before its rounding)
+ * rms(v) = sqrt(mean(v^2) + eps).  Parts of it stand alone: o NULL is the first block's norm alone
+ * (y from r); r and w_pre NULL a gated norm of the block's output into r_out; w_pre NULL the last
+ * block's residual.
+ *   T, D            rows and channels (D <= 16384, else KDA_ERR_UNSUPPORTED).
+ *   res_type, type  types of r, r_out and of o, z, y: equal, or res_type KDA_TYPE_F32 (others:
+ *                   KDA_ERR_UNSUPPORTED).
+ *   group           channels normed together after the block: 0 or D for the whole row, or a head's 32, 64,
+ *                   128 or 256 where that divides D (others: KDA_ERR_UNSUPPORTED).
+ *   w_post [group], ls [D], w_pre [D]   fp32 or NULL.
+ *   r_out       out [T][D] r', or NULL.  May be r itself (same address and stride).
+ *   y           out [T][D], given iff w_pre is.
+ * T = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
+ */
+int kda_block_norm_forward(int64_t T, int32_t D, int32_t res_type, int32_t type, const void *r, int64_t ldr,
+                           const void *o, int64_t ldo, const void *z, int64_t ldz, int32_t gate, int32_t group,
+                           const float *w_post, float scale, const float *ls, const float *w_pre, float eps,
+                           void *r_out, int64_t ldr_out, void *y, int64_t ldy, void *stream);
+
+/*
+ * kda_block_norm_backward -- the gradients of kda_block_norm_forward from those of r' (dr_out, NULL:
+ * zeros) and y (dy, given iff w_pre is).
+ *   r_out           the forward's r' (needed iff w_pre is given).  o, z, the weights, scale: the forward's.
+ *   dr          out [T][D] gradient of r (and of r'), or NULL.    d_o  out [T][D], given iff o is.
+ *   dz          out [T][D] or NULL (not written).
+ *   dw_post     out fp32 [group], dls, dw_pre out fp32 [D], or NULL (not written).  Sums over the rows in
+ *                   an order that depends on T and D only: the same call gives the same bits.
+ *   ws, ws_bytes    device workspace of at least kda_block_norm_workspace_bytes(D) bytes.
+ * T = 0 writes zeros to the weight gradients.  dr may be dr_out itself (same address and stride).
+ * Returns as the forward, or KDA_ERR_WORKSPACE.
+ */
+int kda_block_norm_backward(int64_t T, int32_t D, int32_t res_type, int32_t type, const void *r_out,
+                            int64_t ldr_out, const void *o, int64_t ldo, const void *z, int64_t ldz,
+                            int32_t gate, int32_t group, const float *w_post, float scale, const float *ls,
+                            const float *w_pre, float eps, const void *dr_out, int64_t lddr_out, const void *dy,
+                            int64_t lddy, void *dr, int64_t lddr, void *d_o, int64_t lddo, void *dz, int64_t lddz,
+                            float *dw_post, float *dls, float *dw_pre, void *ws, size_t ws_bytes, void *stream);
+
+/* Device workspace bytes of kda_block_norm_backward (0: D is out of range). */
+size_t kda_block_norm_workspace_bytes(int32_t D);
+
+/*
+ * kda_decode_step -- one KDA token for each of B slots and H heads, the recurrence at the top of this
+ * file with the state of a slot updated in place:
+ *     S~ = Diag(exp g) S,  S = S~ + k (beta (v - S~^T k))^T,  o = scale S^T q.
+ * It continues what kda_forward_segmented leaves in final_state (the same layout), token by token.
+ *   q, k, v, o      [B][H][128] of 'type', token strides ldq.. in elements (>= H * 128).
+ *   g               fp32 [B][H][128], any value; beta fp32 [B][H]; token strides ldg, ldb.
+ *   slots, num_slots  as in kda_gated_scan_step; a padding row's o is zeros.
+ *   state           in/out fp32 [num_slots][H][K][V], 16-byte aligned.
+ * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (H > 65535) or KDA_ERR_CUDA.
+ */
+int kda_decode_step(int32_t B, int32_t H, int32_t type, const int32_t *slots, int32_t num_slots, const void *q,
+                    int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const float *g, int64_t ldg,
+                    const float *beta, int64_t ldb, float scale, float *state, void *o, int64_t ldo, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

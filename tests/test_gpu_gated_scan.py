@@ -1,0 +1,315 @@
+"""GPU tests of the gated linear recurrence (forward, gradients, one-token step) against its 64-bit
+definition (tests/ops_reference.py, whose tolerances apply)."""
+import numpy as np
+import pytest
+
+import ops_reference as ref
+from ops_reference import check, torch_type
+
+pytestmark = pytest.mark.gpu
+
+LENGTHS = [[1], [2], [127], [128], [129], [1, 1, 1], [128, 128], [100, 1, 156, 300], [1500], [60, 1, 700, 64, 5, 128, 640, 3]]
+
+
+def _draw(lens, D, kind, with_i=True, with_h0=True, split=False, seed=0, g_lo=-0.2, g_hi=-0.001):
+    """Device tensors and their exact 64-bit values."""
+    import torch
+    t = torch_type(kind)
+    gen = torch.Generator().manual_seed(seed)
+    T, N = sum(lens), len(lens)
+    cu = [0] + [int(c) for c in np.cumsum(lens)]
+    normal = lambda *s: torch.randn(*s, generator=gen)
+    x, i, g = normal(T, D).to(t), torch.rand(T, D, generator=gen).to(t), g_lo + (g_hi - g_lo) * torch.rand(T, D, generator=gen)
+    h0 = normal(N, D) if with_h0 else None
+    dh, dfinal = normal(T, D).to(t), normal(N, D)
+    if split:     # x, i and g as column ranges of wider rows, at an odd offset
+        wide = torch.zeros(T, 2 * D + 3, dtype=t)
+        wide[:, 1:D + 1], wide[:, D + 2:2 * D + 2] = x, i
+        wide = wide.cuda()
+        xd, idv = wide[:, 1:D + 1], wide[:, D + 2:2 * D + 2]
+        gw = torch.zeros(T, D + 5)
+        gw[:, 2:D + 2] = g
+        gd = gw.cuda()[:, 2:D + 2]
+    else:
+        xd, idv, gd = x.cuda(), i.cuda(), g.cuda()
+    dev = {"x": xd, "i": idv if with_i else None, "g": gd, "h0": None if h0 is None else h0.cuda(), "dh": dh.cuda(),
+           "dfinal": dfinal.cuda()}
+    f64 = lambda v: None if v is None else v.double().numpy()
+    return cu, dev, {"x": f64(x), "i": f64(i) if with_i else None, "g": f64(g), "h0": f64(h0), "dh": f64(dh), "dfinal": f64(dfinal)}
+
+
+def _forward(cu, dev, stream=None, plan=None):
+    import torch
+    from context_kda_gb300 import binding as kda
+    x = dev["x"]
+    T, D, N = cu[-1], x.shape[1], len(cu) - 1
+    plan = kda.kda_plan_segments(cu, 1) if plan is None else plan
+    plan_dev = kda.upload_plan(plan)
+    nan = float("nan")
+    h = torch.full((T, D), nan, dtype=x.dtype, device="cuda")
+    final = torch.full((N, D), nan, device="cuda")
+    states = torch.full((-(-T // 128), D), nan, device="cuda")
+    ws = torch.full((kda.kda_gated_scan_workspace_bytes(plan, D) + 16,), 85, dtype=torch.uint8, device="cuda")[:-16]
+    kda.kda_gated_scan_forward(plan, plan_dev, x, dev["i"], dev["g"], dev["h0"], h, final, states, ws, stream)
+    return h, final, states
+
+
+def _backward(cu, dev, states, with_dfinal=True):
+    import torch
+    from context_kda_gb300 import binding as kda
+    x = dev["x"]
+    T, D, N = cu[-1], x.shape[1], len(cu) - 1
+    plan = kda.kda_plan_segments(cu, 1)
+    plan_dev = kda.upload_plan(plan)
+    nan = float("nan")
+    dx = torch.full((T, D), nan, dtype=x.dtype, device="cuda")
+    di = None if dev["i"] is None else torch.full((T, D), nan, dtype=x.dtype, device="cuda")
+    dg, dh0 = torch.full((T, D), nan, device="cuda"), torch.full((N, D), nan, device="cuda")
+    ws = torch.full((kda.kda_gated_scan_workspace_bytes(plan, D) + 16,), 85, dtype=torch.uint8, device="cuda")[:-16]
+    kda.kda_gated_scan_backward(plan, plan_dev, x, dev["i"], dev["g"], dev["h0"], states, dev["dh"],
+                                dev["dfinal"] if with_dfinal else None, dx, di, dg, dh0, ws)
+    return dx, di, dg, dh0
+
+
+def _check_all(lens, D, kind, with_dfinal=True, **how):
+    import torch
+    from context_kda_gb300 import binding as kda
+    cu, dev, w = _draw(lens, D, kind, **how)
+    h, final, states = _forward(cu, dev)
+    got = _backward(cu, dev, states, with_dfinal)
+    assert kda.kda_device_status() == kda.KDA_OK
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    check(h, h_ref, kind, "h")
+    check(final, f_ref, "f32", "final")
+    check(states, ref.saved_states(h_ref), "f32", "states")
+    want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"] if with_dfinal else None)
+    for name, a, b, k in zip(("dx", "di", "dg", "dh0"), got, want, (kind, kind, "f32", "f32")):
+        if a is not None:
+            check(a, b, k, name)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", LENGTHS, ids=lambda v: "-".join(map(str, v)))
+def test_lengths(lens, kind):
+    _check_all(lens, 64, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 2, 3, 31, 33, 63, 65, 72, 128, 200, 1001, 2048])
+def test_widths(D, kind):
+    _check_all([90, 1, 300], D, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [64, 65, 320])
+def test_column_ranges_of_wider_rows(D, kind):
+    _check_all([200, 3, 180], D, kind, split=True)
+
+
+@pytest.mark.parametrize("with_i,with_h0,with_dfinal", [(False, True, True), (True, False, True), (True, True, False), (False, False, False)])
+def test_absent_tensors(with_i, with_h0, with_dfinal):
+    for D in (64, 33):
+        _check_all([70, 260, 1], D, "bf16", with_i=with_i, with_h0=with_h0, with_dfinal=with_dfinal)
+
+
+def test_many_tiles_in_one_sequence():
+    _check_all([128 * 45 + 17], 64, "bf16")
+    _check_all([128 * 45 + 17], 200, "f32", seed=3)
+
+
+def test_many_short_sequences():
+    rng = np.random.default_rng(4)
+    _check_all([int(n) for n in rng.integers(1, 9, 700)], 64, "bf16")
+    _check_all([1] * 900, 40, "f16")
+
+
+def test_long_memory():
+    """Decays of 1 - 2^-12 to 1: sums over thousands of tokens; exp(g) is one rounding from exact, so
+    n tokens of memory leave at most n 2^-24 relative, 4000 * 6e-8 = 2.4e-4, as a bound."""
+    cu, dev, w = _draw([5000], 64, "f32", g_lo=-2.0 ** -12, g_hi=0.0)
+    h, final, _ = _forward(cu, dev)
+    h_ref, _ = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    x = h.double().cpu().numpy()
+    assert np.linalg.norm(x - h_ref) <= 2.4e-4 * np.linalg.norm(h_ref)
+
+
+def test_strong_and_total_decay():
+    """g down to -200 (exp underflows) and minus infinity: h is then the token's own term."""
+    import torch
+    cu, dev, w = _draw([300, 40], 64, "f32", g_lo=-200.0, g_hi=0.0)
+    dev["g"][::7] = float("-inf")
+    w["g"][::7] = -np.inf
+    h, final, states = _forward(cu, dev)
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    check(h, h_ref, "f32", "h")
+    got = _backward(cu, dev, states)
+    for name, a, b in zip(("dx", "di", "dg", "dh0"), got, ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])):
+        check(a, b, "f32", name)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_sequences_do_not_see_each_other(bad):
+    """Infinities and NaN in one sequence leave every other sequence's results as they were, bit for bit."""
+    import torch
+    lens = [130, 300, 5, 260]
+    cu, dev, _ = _draw(lens, 72, "bf16")
+    h, final, states = _forward(cu, dev)
+    grads = _backward(cu, dev, states)
+    dev["x"][cu[1] + 20, :] = bad
+    dev["dh"][cu[1] + 20, :] = bad
+    dev["h0"][1] = bad
+    dev["dfinal"][1] = bad
+    h2, final2, states2 = _forward(cu, dev)
+    grads2 = _backward(cu, dev, states2)
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for n in (0, 2, 3):
+        rows = slice(cu[n], cu[n + 1])
+        assert same(h[rows], h2[rows]) and same(final[n], final2[n])
+        for a, b in zip(grads[:3], grads2[:3]):
+            assert same(a[rows], b[rows])
+        assert same(grads[3][n], grads2[3][n])
+    assert not bool(torch.isfinite(h2[cu[1] + 20:cu[2]]).any())
+
+
+def test_same_call_same_bits():
+    import torch
+    cu, dev, _ = _draw([4000, 100, 3000], 200, "bf16")
+    a = _forward(cu, dev)
+    ga = _backward(cu, dev, a[2])
+    for _ in range(3):
+        b = _forward(cu, dev)
+        gb = _backward(cu, dev, b[2])
+        for x, y in zip(a + ga, b + gb):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_another_stream():
+    import torch
+    cu, dev, w = _draw([700, 30], 64, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        h, _, _ = _forward(cu, dev)
+    side.synchronize()
+    check(h, ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])[0], "bf16", "h")
+    torch.cuda.synchronize()
+    h, _, _ = _forward(cu, dev, stream=side)
+    torch.cuda.synchronize()
+    check(h, ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])[0], "bf16", "h")
+
+
+def test_graph_capture_replays():
+    """The calls can be captured: nothing is allocated or synchronised, and a replay redoes the work."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    cu, dev, w = _draw([1000, 200], 64, "bf16")
+    plan = kda.kda_plan_segments(cu, 1)
+    plan_dev = kda.upload_plan(plan)
+    h = torch.zeros(cu[-1], 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kda.kda_gated_scan_workspace_bytes(plan, 64), dtype=torch.uint8, device="cuda")
+    call = lambda: kda.kda_gated_scan_forward(plan, plan_dev, dev["x"], dev["i"], dev["g"], dev["h0"], h, None, None, ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        h.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(h, ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])[0], "bf16", "h")
+
+
+def test_offsets_beyond_32_bits():
+    """Rows far apart: element offsets pass 2^31 and byte offsets 2^32."""
+    import torch
+    T, D, wide = 70000, 64, 40000
+    cu, dev, w = _draw([T], D, "bf16", seed=9)
+    big = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")
+    x = big[:, wide - D:]
+    x.copy_(dev["x"])
+    assert (T - 1) * wide > 2 ** 31
+    dev["x"] = x
+    h, final, states = _forward(cu, dev)
+    h_ref, _ = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    check(h, h_ref, "bf16", "h")
+    got = _backward(cu, dev, states)
+    want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])
+    for name, a, b, k in zip(("dx", "di", "dg", "dh0"), got, want, ("bf16", "bf16", "f32", "f32")):
+        check(a, b, k, name)
+
+
+def test_a_device_plan_of_another_problem_is_refused():
+    import torch
+    from context_kda_gb300 import binding as kda
+    assert kda.kda_device_status() == kda.KDA_OK
+    cu, dev, _ = _draw([500], 64, "bf16")
+    plan, other = kda.kda_plan_segments(cu, 1), kda.upload_plan(kda.kda_plan_segments([0, 100, 500], 1))
+    h = torch.full((500, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kda.kda_gated_scan_workspace_bytes(plan, 64), dtype=torch.uint8, device="cuda")
+    kda.kda_gated_scan_forward(plan, other, dev["x"], dev["i"], dev["g"], dev["h0"], h, None, None, ws)
+    assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
+    assert kda.kda_device_status() == kda.KDA_OK
+    assert bool((h == 7.0).all())
+
+
+# ---- one token ------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("B,D,with_i", [(1, 1, True), (1, 2048, True), (5, 33, False), (64, 2048, True), (300, 65, True), (70000, 8, True)])
+def test_step(B, D, with_i, kind):
+    import torch
+    from context_kda_gb300 import binding as kda
+    gen = torch.Generator().manual_seed(B + D)
+    t = torch_type(kind)
+    x, i = torch.randn(B, D, generator=gen).to(t), torch.rand(B, D, generator=gen).to(t)
+    g, state = -0.2 * torch.rand(B, D, generator=gen), torch.randn(B + 4, D, generator=gen)
+    slots = torch.randperm(B + 4, generator=gen)[:B].to(torch.int32)
+    slots[::5] = -1                                  # padding rows
+    got_state = state.cuda()
+    h = torch.full((B, D), float("nan"), dtype=t, device="cuda")
+    kda.kda_gated_scan_step(slots.cuda(), x.cuda(), i.cuda() if with_i else None, g.cuda(), got_state, h)
+    live = (slots >= 0).numpy()
+    sl = slots.numpy()[live]
+    want = state.double().numpy()
+    u = x.double().numpy() * (i.double().numpy() if with_i else 1.0)
+    want[sl] = np.exp(g.double().numpy())[live] * want[sl] + u[live]
+    out = np.zeros((B, D))
+    out[live] = want[sl]
+    check(got_state, want, "f32", "state")
+    check(h, out, kind, "h")
+    untouched = np.setdiff1d(np.arange(B + 4), sl)
+    assert torch.equal(got_state.cpu()[untouched], state[untouched])
+    assert bool((h.cpu()[~torch.from_numpy(live)] == 0).all())
+
+
+def test_step_continues_a_forward():
+    """A forward over n tokens equals a forward over n - 1 and one step, per sequence."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    lens = [130, 2, 257]
+    cu, dev, w = _draw(lens, 72, "bf16")
+    h, final, _ = _forward(cu, dev)
+    keep = [t for n in range(3) for t in range(cu[n], cu[n + 1] - 1)]
+    last = [cu[n + 1] - 1 for n in range(3)]
+    cut = {k: (None if v is None else v[keep] if k in ("x", "i", "g", "dh") else v) for k, v in dev.items()}
+    _, state, _ = _forward([0] + [int(c) for c in np.cumsum([n - 1 for n in lens])], cut)
+    out = torch.empty(3, 72, dtype=torch.bfloat16, device="cuda")
+    kda.kda_gated_scan_step(None, dev["x"][last], dev["i"][last], dev["g"][last], state, out)
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    check(state, f_ref, "f32", "state")
+    check(out, h_ref[last], "bf16", "h")
+
+
+def test_step_records_a_slot_out_of_range():
+    import torch
+    from context_kda_gb300 import binding as kda
+    assert kda.kda_device_status() == kda.KDA_OK
+    state = torch.ones(2, 8, device="cuda")
+    h = torch.full((2, 8), 5.0, device="cuda")
+    slots = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    kda.kda_gated_scan_step(slots, torch.ones(2, 8, device="cuda"), None, torch.zeros(2, 8, device="cuda"), state, h)
+    assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
+    assert kda.kda_device_status() == kda.KDA_OK
+    assert state.tolist() == [[1.0] * 8, [2.0] * 8] and h.tolist() == [[2.0] * 8, [0.0] * 8]
