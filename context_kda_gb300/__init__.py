@@ -22,5 +22,6 @@ _BINDING_NAMES = ("kda_status_string", "kda_plan_segments", "kda_plan_check", "k
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        value = globals()[name] = getattr(importlib.import_module(".binding", __name__), name)
+        return value
     raise AttributeError(name)

@@ -16,7 +16,9 @@ LIB = os.path.join(PKG, "libkda.so")
 ROOT = os.path.dirname(PKG)
 
 CUDA_SOURCES = ["api.cu", "chunk_prep.cu", "chunk_state.cu", "compose.cu", "boundary.cu", "noalloc.cu", "backward.cu", "reverse.cu",
-                "gated_scan.cu", "block_norm.cu", "decode.cu"]
+                "gated_scan.cu", "decode.cu", "block_norm.cu",
+                "block_norm_forward_bf16.cu", "block_norm_forward_f16.cu", "block_norm_backward_bf16.cu",
+                "block_norm_backward_f16.cu"]
 CXX_SOURCES = ["plan.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

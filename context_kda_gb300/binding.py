@@ -138,7 +138,7 @@ def _nbytes(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # of the current device
     return ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
 
 
@@ -286,6 +286,10 @@ SCAN_TILE = 128
 _TYPES = {}
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _refuse(fn: str):
     raise KDAError(fn, KDA_ERR_INVALID_ARG, _lib.kda_status_string(KDA_ERR_INVALID_ARG).decode())
 
@@ -305,9 +309,13 @@ def _rows(fn: str, t, rows: int, width: int, dtype):
     trailing axes count as one); (None, 0) for None."""
     if t is None:
         return None, 0
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or len(shape) < 2 or shape[0] != rows or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda or t.shape[0] != rows:
         _refuse(fn)
+    if t.is_contiguous():
+        if t.numel() != rows * width:
+            _refuse(fn)
+        return t.data_ptr(), width
+    shape, stride = t.shape, t.stride()
     n = 1
     for size, step in zip(reversed(shape[1:]), reversed(stride[1:])):
         if size != 1 and step != n:
@@ -315,7 +323,7 @@ def _rows(fn: str, t, rows: int, width: int, dtype):
         n *= size
     if n != width:
         _refuse(fn)
-    return t.data_ptr(), (stride[0] if rows > 1 else max(stride[0], width))
+    return t.data_ptr(), (stride[0] if rows > 1 else width)
 
 
 def _flat(fn: str, t, numel: int, dtype=None):
@@ -350,9 +358,9 @@ def kda_gated_scan_forward(plan, plan_dev, x, i, g, h0, h, final_state, states, 
     T, N, D = int(p[3]), int(p[4]), x.shape[-1]
     ty = _type(fn, x)
     _check(fn, _lib.kda_gated_scan_forward(
-        _hp(p), _dp(plan_dev), D, ty, *_rows(fn, x, T, D, x.dtype), *_rows(fn, i, T, D, x.dtype),
+        p.ctypes.data, plan_dev.data_ptr(), D, ty, *_rows(fn, x, T, D, x.dtype), *_rows(fn, i, T, D, x.dtype),
         *_rows(fn, g, T, D, _f32()), _flat(fn, h0, N * D), *_rows(fn, h, T, D, x.dtype), _flat(fn, final_state, N * D),
-        _flat(fn, states, -(-T // SCAN_TILE) * D), _dp(ws), _nbytes(ws), _stream(stream)))
+        _flat(fn, states, -(-T // SCAN_TILE) * D), _addr(ws), _nbytes(ws), _stream(stream)))
 
 
 def kda_gated_scan_backward(plan, plan_dev, x, i, g, h0, states, dh, dfinal, dx, di, dg, dh0, ws, stream=None):
@@ -361,9 +369,9 @@ def kda_gated_scan_backward(plan, plan_dev, x, i, g, h0, states, dh, dfinal, dx,
     T, N, D = int(p[3]), int(p[4]), x.shape[-1]
     ty, t, f32 = _type(fn, x), x.dtype, _f32()
     _check(fn, _lib.kda_gated_scan_backward(
-        _hp(p), _dp(plan_dev), D, ty, *_rows(fn, x, T, D, t), *_rows(fn, i, T, D, t), *_rows(fn, g, T, D, f32),
+        p.ctypes.data, plan_dev.data_ptr(), D, ty, *_rows(fn, x, T, D, t), *_rows(fn, i, T, D, t), *_rows(fn, g, T, D, f32),
         _flat(fn, h0, N * D), _flat(fn, states, -(-T // SCAN_TILE) * D), *_rows(fn, dh, T, D, t), _flat(fn, dfinal, N * D),
-        *_rows(fn, dx, T, D, t), *_rows(fn, di, T, D, t), *_rows(fn, dg, T, D, f32), _flat(fn, dh0, N * D), _dp(ws),
+        *_rows(fn, dx, T, D, t), *_rows(fn, di, T, D, t), *_rows(fn, dg, T, D, f32), _flat(fn, dh0, N * D), _addr(ws),
         _nbytes(ws), _stream(stream)))
 
 
@@ -418,7 +426,7 @@ def kda_block_norm_backward(r_out, o, z, gate, group, w_post, scale, ls, w_pre, 
         _gate_code(fn, gate), int(group), _flat(fn, w_post, G), float(scale), _flat(fn, ls, D), _flat(fn, w_pre, D),
         float(eps), *_rows(fn, dr_out, T, D, rt), *_rows(fn, dy, T, D, t), *_rows(fn, dr, T, D, rt),
         *_rows(fn, do, T, D, t), *_rows(fn, dz, T, D, t), _flat(fn, dw_post, G), _flat(fn, dls, D), _flat(fn, dw_pre, D),
-        _dp(ws), _nbytes(ws), _stream(stream)))
+        _addr(ws), _nbytes(ws), _stream(stream)))
 
 
 def kda_decode_step(slots, q, k, v, g, beta, scale, state, o, stream=None):

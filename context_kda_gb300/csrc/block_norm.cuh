@@ -1,0 +1,674 @@
+// The norms around a block, fused with the block's gate and the residual:
+//     n = o * inv_o * w_post,   inv_o = 1 / sqrt(mean_group(o^2) + eps)     (n = o without w_post)
+//     u = act(z) * n,           act = 1, sigmoid or silu
+//     r' = r + scale * ls * u                                                (stored in the residual's type)
+//     y = r' * inv_r * w_pre,   inv_r = 1 / sqrt(mean_row(r'^2) + eps)       (of r' before it is rounded)
+// and the gradients of r, o, z, w_post, ls and w_pre from those of r' and y.  Bound by memory: a row is
+// read once and stays in registers between its two norms.
+//
+// The gradient through v -> v / rms(v) is inv (e - hat mean(e hat)) for e = the gradient of hat = v inv.  In a group
+// of one channel the two terms cancel down to inv^3 eps e, which is then what is computed.
+// Reciprocals and square roots are the hardware's approximations (about 2^-22 relative): fp32 results keep 1e-6.
+//
+// A CTA of BLOCK threads takes R rows at a time (NT threads a row, 8 NC channels a thread) and walks over
+// all its rows.  Every thread copies what it will read itself into its own slots of a ring in shared memory
+// (cp.async), one to three steps ahead, so the copies need no barrier; sums over a row take one barrier each
+// (none when a row is a warp or less).  U is the run of adjacent channels that a thread copies: 8 where rows
+// start on 16 bytes, otherwise 2 (2-byte types whose rows start on pairs) or 1; single 2-byte elements,
+// which no asynchronous copy moves, are read directly.
+// Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
+// and its groups at the end, and a second kernel adds up the CTAs in order.
+#pragma once
+
+#include "elem.cuh"
+#include "kda_internal.cuh"
+#include "tc.cuh"
+
+namespace kda {
+namespace norm {
+
+constexpr int MAX_GRID = 304;   // CTAs of a launch: rows of the backward's column sums
+
+// What both directions take besides NormIn.
+struct Shape {
+    int64_t T;
+    int D, G, NT;                // channels, channels of a group, threads of a row
+    bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes (or on pairs): residual, the others
+};
+
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.
+template <typename X, int BLOCK, int NC, int U> struct Row {
+    static constexpr int NE = 8 * NC, NU = NE / U, RUN = U * static_cast<int>(sizeof(X));
+    static constexpr bool COPY = RUN >= 4;                // there is an asynchronous copy of this size
+    static constexpr int PB = RUN >= 16 ? 16 : 4, PIECES = COPY ? RUN / PB : 0, EPP = PB / static_cast<int>(sizeof(X));
+    static constexpr int BYTES = COPY ? NE * static_cast<int>(sizeof(X)) * BLOCK : 0;   // of the CTA, per step
+
+    // Copies the row's channels below D to the slots at 'base' (nothing is read when 'in' is false).
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *any, int ti, int NT, int D, bool in)
+    {
+        if constexpr (COPY) {
+#pragma unroll
+            for (int q = 0; q < NU; ++q)
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+                    const int c = (ti + q * NT) * U + p * EPP;
+                    const int left = in ? (D - c) * static_cast<int>(sizeof(X)) : 0;
+                    const int bytes = left < 0 ? 0 : left > PB ? PB : left;
+                    const X *src = bytes ? row + c : any;
+                    const uint32_t dst = base + ((q * PIECES + p) * BLOCK + threadIdx.x) * PB;
+                    if constexpr (PB == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+                    else
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+                }
+        }
+    }
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v, __nv_bfloat16 *)
+    {
+        v[0] = __uint_as_float(w << 16);
+        v[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v, __half *)
+    {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        v[0] = f.x;
+        v[1] = f.y;
+    }
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v, float *) { v[0] = __uint_as_float(w); }
+
+    // The channels as fp32 (zeros from D on): from the slots, or from the row where there is no copy.
+    template <bool RING>
+    static __device__ __forceinline__ void read(const unsigned char *base, const X *row, int ti, int NT, int D, bool in, float (&v)[NE])
+    {
+        if constexpr (RING && COPY) {
+            constexpr int EPW = 4 / static_cast<int>(sizeof(X));
+#pragma unroll
+            for (int j = 0; j < NU * PIECES; ++j) {
+                if constexpr (PB == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(base + (j * BLOCK + threadIdx.x) * 16);
+                    unpack(w.x, v + j * EPP, static_cast<X *>(nullptr));
+                    unpack(w.y, v + j * EPP + EPW, static_cast<X *>(nullptr));
+                    unpack(w.z, v + j * EPP + 2 * EPW, static_cast<X *>(nullptr));
+                    unpack(w.w, v + j * EPP + 3 * EPW, static_cast<X *>(nullptr));
+                } else {
+                    unpack(*reinterpret_cast<const uint32_t *>(base + (j * BLOCK + threadIdx.x) * 4), v + j * EPP, static_cast<X *>(nullptr));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < NU; ++q)
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int c = (ti + q * NT) * U + j;
+                    v[q * U + j] = in && c < D ? to_f32(row[c]) : 0.f;
+                }
+        }
+    }
+    static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool wide, const float (&v)[NE])
+    {
+#pragma unroll
+        for (int q = 0; q < NU; ++q) {
+            const int c = (ti + q * NT) * U;
+            X e[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) e[j] = from_f32<X>(v[q * U + j]);
+            if (U > 1 && wide && c + U <= D) {
+                if constexpr (RUN >= 16) {
+#pragma unroll
+                    for (int p = 0; p < RUN / 16; ++p)
+                        reinterpret_cast<uint4 *>(row + c)[p] = reinterpret_cast<const uint4 *>(e)[p];
+                } else if constexpr (RUN == 4) {
+                    *reinterpret_cast<uint32_t *>(row + c) = *reinterpret_cast<const uint32_t *>(e);
+                } else if constexpr (RUN == 8) {
+                    *reinterpret_cast<uint2 *>(row + c) = *reinterpret_cast<const uint2 *>(e);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (c + j < D) row[c + j] = e[j];
+        }
+    }
+};
+
+// Sums of N values over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp
+// take one barrier: the partial sums go to one of two buffers in turn.
+template <int N, int BLOCK> struct Sums {
+    float part[2][N][BLOCK / 32];
+    __device__ __forceinline__ void over_row(float (&v)[N], int NT, int turn)
+    {
+#pragma unroll
+        for (int m = 16; m; m >>= 1)
+            if (m < NT)
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
+        if (NT <= 32) return;
+        const int warp = threadIdx.x >> 5, n = NT >> 5, w0 = warp & ~(n - 1);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int j = 0; j < N; ++j) part[turn & 1][j][warp] = v[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float s = 0.f;
+            for (int w = 0; w < n; ++w) s += part[turn & 1][j][w0 + w];
+            v[j] = s;
+        }
+    }
+};
+
+// Sums over each run's group of G channels (G < D), in place.  G spans G / U lanes of consecutive threads,
+// which may be several warps when runs are short (NT U is then at least G).
+template <int BLOCK, int NU, int U> struct GroupSums {
+    float part[U < 8 ? 2 : 1][U < 8 ? NU : 1][BLOCK / 32];
+    __device__ __forceinline__ void over_group(float (&v)[NU], int G, int turn)
+    {
+        const int lanes = G / U;
+#pragma unroll
+        for (int m = 16; m; m >>= 1)
+            if (m < lanes)
+#pragma unroll
+                for (int q = 0; q < NU; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], m);
+        if constexpr (U < 8) {
+            if (lanes <= 32) return;
+            const int warp = threadIdx.x >> 5, n = lanes >> 5, w0 = warp & ~(n - 1);
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int q = 0; q < NU; ++q) part[turn & 1][q][warp] = v[q];
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < NU; ++q) {
+                float s = 0.f;
+                for (int w = 0; w < n; ++w) s += part[turn & 1][q][w0 + w];
+                v[q] = s;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float inv_rms(float mean_sq, float eps) { return rsqrtf(mean_sq + eps); }
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + tc::ex2_ftz(z * -1.4426950408889634f)); }   // exp = infinity: 0
+
+// The gradient of v from e, the gradient of hat = v inv; mean = mean(e hat) over the group.
+__device__ __forceinline__ float unit_grad(float e, float hat, float inv, float mean, bool one, float eps)
+{
+    return inv * (one ? e * (eps * inv * inv) : fmaf(-hat, mean, e));
+}
+
+// A weight's values at a thread's channels (1 where it is absent): kept in registers when they are few.
+template <int NE, int U, typename I>
+__device__ __forceinline__ void weights(const float *w, float scale, I index, int ti, int NT, int D, float (&v)[NE])
+{
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        const int c = (ti + (j / U) * NT) * U + j % U;
+        v[j] = c < D ? scale * (w ? __ldg(w + index(c)) : 1.f) : 0.f;
+    }
+}
+
+// ---- forward ----------------------------------------------------------------------------------------------
+
+template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
+    using RowR = Row<R, BLOCK, NC, U>;
+    using RowE = Row<E, BLOCK, NC, U>;
+    static constexpr int NE = 8 * NC, NU = NE / U;
+    static constexpr int STEP = RowR::BYTES + 2 * RowE::BYTES;
+    static constexpr int FIT = STEP ? (NC == 1 ? 112 : 200) * 1024 / STEP : 0;    // two CTAs an SM when NC = 1
+    static constexpr int S = FIT > 3 ? 3 : FIT;      // steps in the ring; 0: no ring
+    static constexpr int SMEM = S * STEP;
+};
+
+template <typename R, typename E, int BLOCK, int NC, int U>
+__global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
+{
+    using F = Forward<R, E, BLOCK, NC, U>;
+    using RowR = typename F::RowR;
+    using RowE = typename F::RowE;
+    constexpr int NE = F::NE, NU = F::NU, S = F::S;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ Sums<1, BLOCK> sums;
+    __shared__ GroupSums<BLOCK, NU, U> groups;
+    const R *r = static_cast<const R *>(a.r);
+    const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
+    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT;
+    const float inv_d = 1.f / D, inv_g = 1.f / G;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, row0 = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / NT;
+    const uint32_t base = tc::smem_u32(ring);
+
+    auto fetch = [&](int slot, int64_t t) {
+        const bool in = t < s.T;
+        const uint32_t b = base + slot * F::STEP;
+        if (r) RowR::fetch(b, r + t * a.ldr, r, ti, NT, D, in);
+        if (o) RowE::fetch(b + RowR::BYTES, o + t * a.ldo, o, ti, NT, D, in);
+        if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, z + t * a.ldz, z, ti, NT, D, in);
+    };
+    auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
+    auto in_row = [&](int c) { return c; };
+    float wl[NE], wr[NE];      // scale * ls * w_post, w_pre
+    auto branch_weights = [&] {
+        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
+        if (a.w_post) {
+            float wg[NE];
+            weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
+#pragma unroll
+            for (int j = 0; j < NE; ++j) wl[j] *= wg[j];
+        }
+    };
+    if constexpr (NC == 1) {
+        branch_weights();
+        if (y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+    }
+    for (int k = 0; k < S - 1; ++k) {
+        fetch(k, row0 + k * step);
+        cp_commit();
+    }
+    int slot = 0, turn = 0;
+    for (int64_t t = row0; t - threadIdx.x / NT < s.T; t += step) {
+        const bool in = t < s.T;
+        if constexpr (S > 0) {
+            fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
+            cp_commit();
+            cp_wait<S - 1>();
+        }
+        const unsigned char *b = ring + slot * F::STEP;
+        float v[NE];
+        if (r) {
+            RowR::template read<(S > 0)>(b, r + t * a.ldr, ti, NT, D, in, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NE; ++j) v[j] = 0.f;
+        }
+        if (o) {
+            float n[NE];
+            RowE::template read<(S > 0)>(b + RowR::BYTES, o + t * a.ldo, ti, NT, D, in, n);
+            float g[NE];
+            if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, z + t * a.ldz, ti, NT, D, in, g);
+            if (a.w_post) {
+                float ss[NU];
+#pragma unroll
+                for (int q = 0; q < NU; ++q) {
+                    ss[q] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < U; ++j) ss[q] += n[q * U + j] * n[q * U + j];
+                }
+                if (G == D) {
+                    float one[1] = {0.f};
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) one[0] += ss[q];
+                    sums.over_row(one, NT, turn++);
+                    const float inv = inv_rms(one[0] * inv_g, a.eps);
+#pragma unroll
+                    for (int j = 0; j < NE; ++j) n[j] *= inv;
+                } else {
+                    groups.over_group(ss, G, turn);
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) {
+                        const float inv = inv_rms(ss[q] * inv_g, a.eps);
+#pragma unroll
+                        for (int j = 0; j < U; ++j) n[q * U + j] *= inv;
+                    }
+                }
+            }
+            if (a.gate == KDA_GATE_SIGMOID) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) n[j] *= sigmoid(g[j]);
+            } else if (a.gate == KDA_GATE_SILU) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) n[j] *= g[j] * sigmoid(g[j]);
+            }
+            if constexpr (NC > 1) branch_weights();
+#pragma unroll
+            for (int j = 0; j < NE; ++j) v[j] = fmaf(wl[j], n[j], v[j]);
+        }
+        if (r_out && in) RowR::write(r_out + t * ldro, ti, NT, D, s.wide_r, v);
+        if (y) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int j = 0; j < NE; ++j) ss[0] += v[j] * v[j];
+            sums.over_row(ss, NT, turn);
+            const float inv = inv_rms(ss[0] * inv_d, a.eps);
+            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+#pragma unroll
+            for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
+            if (in) RowE::write(y + t * ldy, ti, NT, D, s.wide_a, v);
+        }
+        ++turn;
+        if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
+    }
+}
+
+// ---- backward ---------------------------------------------------------------------------------------------
+
+template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
+    using RowR = Row<R, BLOCK, NC, U>;
+    using RowE = Row<E, BLOCK, NC, U>;
+    static constexpr int NE = 8 * NC, NU = NE / U;
+    static constexpr int STEP = 2 * RowR::BYTES + 3 * RowE::BYTES;
+    static constexpr int FIT = STEP ? 200 * 1024 / STEP : 0;
+    static constexpr int S = FIT > 3 ? 3 : FIT;
+    static constexpr int FOLD = BLOCK * NE * 4;      // the column sums of the CTA, folded at the end
+    static constexpr int SMEM = S * STEP > FOLD ? S * STEP : FOLD;
+};
+
+// part: [grid][G + 2 D], the CTA's sums for w_post, ls and w_pre.
+template <typename R, typename E, int BLOCK, int NC, int U>
+__global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R *dro, int64_t lddro, const E *dy, int64_t lddy,
+                                                     NormGrads g, float *part)
+{
+    using B = Backward<R, E, BLOCK, NC, U>;
+    using RowR = typename B::RowR;
+    using RowE = typename B::RowE;
+    constexpr int NE = B::NE, NU = B::NU, S = B::S;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ Sums<3, BLOCK> sums;
+    __shared__ Sums<1, BLOCK> sum1;
+    __shared__ GroupSums<BLOCK, NU, U> groups;
+    const R *r = static_cast<const R *>(a.r);
+    const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
+    R *dr = static_cast<R *>(g.dr);
+    E *d_o = static_cast<E *>(g.d_o), *dz = static_cast<E *>(g.dz);
+    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT;
+    const float inv_d = 1.f / D, inv_g = 1.f / G;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, row0 = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / NT;
+    const uint32_t base = tc::smem_u32(ring);
+    constexpr int O_DRO = RowR::BYTES, O_DY = 2 * RowR::BYTES, O_O = O_DY + RowE::BYTES, O_Z = O_O + RowE::BYTES;
+
+    auto fetch = [&](int slot, int64_t t) {
+        const bool in = t < s.T;
+        const uint32_t b = base + slot * B::STEP;
+        if (a.w_pre) {
+            RowR::fetch(b, r + t * a.ldr, r, ti, NT, D, in);
+            RowE::fetch(b + O_DY, dy + t * lddy, dy, ti, NT, D, in);
+        }
+        if (dro) RowR::fetch(b + O_DRO, dro + t * lddro, dro, ti, NT, D, in);
+        if (o) RowE::fetch(b + O_O, o + t * a.ldo, o, ti, NT, D, in);
+        if (z) RowE::fetch(b + O_Z, z + t * a.ldz, z, ti, NT, D, in);
+    };
+    auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
+    auto in_row = [&](int c) { return c; };
+    float acc_g[NE], acc_l[NE], acc_r[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) acc_g[j] = acc_l[j] = acc_r[j] = 0.f;
+    float wg[NE], wl[NE], wr[NE];
+    if constexpr (NC == 1) {
+        weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
+        weights<NE, U>(a.ls, 1.f, in_row, ti, NT, D, wl);
+        weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+    }
+    for (int k = 0; k < S - 1; ++k) {
+        fetch(k, row0 + k * step);
+        cp_commit();
+    }
+    int slot = 0, turn = 0;
+    for (int64_t t = row0; t - threadIdx.x / NT < s.T; t += step) {
+        const bool in = t < s.T;
+        if constexpr (S > 0) {
+            fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
+            cp_commit();
+            cp_wait<S - 1>();
+        }
+        const unsigned char *b = ring + slot * B::STEP;
+        float ov[NE], rv[NE], e[NE];
+        float total[3] = {0.f, 0.f, 0.f};       // sums of r^2, e r, o^2 over the row
+        float so[NU];                           // of o^2 over the groups
+        if (a.w_pre) {
+            RowR::template read<(S > 0)>(b, r + t * a.ldr, ti, NT, D, in, rv);
+            RowE::template read<(S > 0)>(b + O_DY, dy + t * lddy, ti, NT, D, in, e);
+            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                total[0] += rv[j] * rv[j];
+                total[1] += e[j] * wr[j] * rv[j];
+            }
+        }
+        if (o) {
+            RowE::template read<(S > 0)>(b + O_O, o + t * a.ldo, ti, NT, D, in, ov);
+#pragma unroll
+            for (int q = 0; q < NU; ++q) {
+                so[q] = 0.f;
+#pragma unroll
+                for (int j = 0; j < U; ++j) so[q] += ov[q * U + j] * ov[q * U + j];
+                total[2] += so[q];
+            }
+        }
+        sums.over_row(total, NT, turn);
+        float v[NE];                            // the gradient of r', then that of o
+        if (dro) {
+            RowR::template read<(S > 0)>(b + O_DRO, dro + t * lddro, ti, NT, D, in, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NE; ++j) v[j] = 0.f;
+        }
+        if (a.w_pre) {
+            const float inv = inv_rms(total[0] * inv_d, a.eps), mean = total[1] * inv_d * inv;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                const float hat = rv[j] * inv;
+                acc_r[j] = fmaf(e[j], hat, acc_r[j]);
+                v[j] += unit_grad(e[j] * wr[j], hat, inv, mean, D == 1, a.eps);
+            }
+        }
+        if (dr && in) RowR::write(dr + t * g.lddr, ti, NT, D, s.wide_r, v);
+        if (o) {
+            if (a.w_post) {
+                if (G == D) {
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) so[q] = total[2];
+                } else {
+                    groups.over_group(so, G, turn);
+                }
+            }
+            float gz[NE];
+            if (z) RowE::template read<(S > 0)>(b + O_Z, z + t * a.ldz, ti, NT, D, in, gz);
+            if constexpr (NC > 1) {
+                weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
+                weights<NE, U>(a.ls, 1.f, in_row, ti, NT, D, wl);
+            }
+            float ev[NU], inv[NU];
+#pragma unroll
+            for (int q = 0; q < NU; ++q) {
+                inv[q] = a.w_post ? inv_rms(so[q] * inv_g, a.eps) : 1.f;
+                ev[q] = 0.f;
+            }
+            // channel j with the gate's value and derivative: v becomes the gradient of hat, ov becomes hat
+            auto channel = [&](int j, float act, float slope) {
+                const float hat = ov[j] * inv[j / U], n = hat * wg[j], tt = a.scale * v[j], ta = tt * act;
+                acc_l[j] = fmaf(ta, n, acc_l[j]);
+                gz[j] = tt * wl[j] * n * slope;
+                const float dn = ta * wl[j];
+                acc_g[j] = fmaf(dn, hat, acc_g[j]);
+                v[j] = dn * wg[j];
+                ov[j] = hat;
+                ev[j / U] = fmaf(v[j], hat, ev[j / U]);
+            };
+            if (a.gate == KDA_GATE_SIGMOID) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    const float p = sigmoid(gz[j]);
+                    channel(j, p, fmaf(-p, p, p));
+                }
+            } else if (a.gate == KDA_GATE_SILU) {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    const float p = sigmoid(gz[j]), act = gz[j] * p;
+                    channel(j, act, fmaf(act, 1.f - p, p));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NE; ++j) channel(j, 1.f, 0.f);
+            }
+            if (dz && in) RowE::write(dz + t * g.lddz, ti, NT, D, s.wide_b, gz);
+            if (a.w_post) {
+                if (G == D) {
+                    float one[1] = {0.f};
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) one[0] += ev[q];
+                    sum1.over_row(one, NT, turn);
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) ev[q] = one[0];
+                } else {
+                    groups.over_group(ev, G, turn + 1);
+                }
+#pragma unroll
+                for (int j = 0; j < NE; ++j) v[j] = unit_grad(v[j], ov[j], inv[j / U], ev[j / U] * inv_g, G == 1, a.eps);
+            }
+            if (in) RowE::write(d_o + t * g.lddo, ti, NT, D, s.wide_a, v);
+        }
+        ++turn;
+        if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    // the CTA's column sums, over its rows (and over the groups for w_post)
+    cp_wait<0>();
+    float *fold = reinterpret_cast<float *>(ring);     // [rows][8 NC NT]
+    const int width = NT * NE;
+    part += static_cast<size_t>(blockIdx.x) * (G + 2 * static_cast<size_t>(D));
+    auto put = [&](const float (&acc)[NE]) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NE; ++j) fold[(threadIdx.x / NT) * width + (ti + (j / U) * NT) * U + j % U] = acc[j];
+        __syncthreads();
+    };
+    if (g.dw_post) {
+        put(acc_g);
+        for (int c = threadIdx.x; c < G; c += BLOCK) {
+            float v = 0.f;
+            for (int k = 0; k < rows; ++k)
+                for (int j = c; j < D; j += G) v += fold[k * width + j];
+            part[c] = v;
+        }
+    }
+    auto out = [&](float *p) {
+        for (int c = threadIdx.x; c < D; c += BLOCK) {
+            float v = 0.f;
+            for (int k = 0; k < rows; ++k) v += fold[k * width + c];
+            p[c] = v;
+        }
+    };
+    if (g.dls) {
+        put(acc_l);
+        out(part + G);
+    }
+    if (g.dw_pre) {
+        put(acc_r);
+        out(part + G + D);
+    }
+}
+
+// ---- launches ---------------------------------------------------------------------------------------------
+
+// Every row of the tensor starts on 'bytes'.
+inline bool rows_on(const void *p, int64_t ld, int elem, int bytes)
+{
+    return !p || ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && (ld * elem & (bytes - 1)) == 0);
+}
+
+// Threads of a row: as many as hold it in 8 nc channels each, and a group's where runs are short.
+inline int threads_of_row(int D, int G, int nc, int U)
+{
+    int nt = 4;
+    while (static_cast<int64_t>(nt) * 8 * nc < D) nt *= 2;
+    if (G < D)
+        while (nt * U < G) nt *= 2;
+    return nt;
+}
+
+template <typename R, typename E, int BLOCK, int NC, int U>
+cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
+{
+    using F = Forward<R, E, BLOCK, NC, U>;
+    s.NT = threads_of_row(s.D, s.G, NC, U);
+    auto fn = forward<R, E, BLOCK, NC, U>;
+    if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), F::SMEM)) return e;
+    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = (BLOCK == 512 && NC == 1 ? 2 : 1) * sm_count();
+    fn<<<static_cast<unsigned>(want < most ? want : most), BLOCK, F::SMEM, stream>>>(s, a, static_cast<R *>(r_out), ldro,
+                                                                                      static_cast<E *>(y), ldy);
+    return cudaGetLastError();
+}
+
+template <typename R, typename E, int BLOCK, int NC, int U>
+cudaError_t run_backward(Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy, const NormGrads &g,
+                         float *part, int *grid, cudaStream_t stream)
+{
+    using B = Backward<R, E, BLOCK, NC, U>;
+    s.NT = threads_of_row(s.D, s.G, NC, U);
+    auto fn = backward<R, E, BLOCK, NC, U>;
+    if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), B::SMEM)) return e;
+    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = sm_count() < MAX_GRID ? sm_count() : MAX_GRID;
+    *grid = static_cast<int>(want < most ? want : most);
+    fn<<<*grid, BLOCK, B::SMEM, stream>>>(s, a, static_cast<const R *>(dro), lddro, static_cast<const E *>(dy), lddy, g, part);
+    return cudaGetLastError();
+}
+
+// The instance for a width and a run: rows of up to 4096 channels take 512 threads with 8 channels each, up to 8192
+// twice the channels, up to 16384 twice the threads.
+#define KDA_NORM_PICK(FN, R, E, U, ...)                                          \
+    (s.D <= 4096 ? FN<R, E, 512, 1, U>(__VA_ARGS__)                              \
+                 : s.D <= 8192 ? FN<R, E, 512, 2, U>(__VA_ARGS__) : FN<R, E, 1024, 2, U>(__VA_ARGS__))
+
+template <typename R, typename E>
+cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
+{
+    constexpr int re = sizeof(R), e = sizeof(E);
+    if (rows_on(a.r, a.ldr, re, 16) && rows_on(a.o, a.ldo, e, 16) && rows_on(a.z, a.ldz, e, 16)) {
+        s.wide_r = rows_on(r_out, ldro, re, 16);
+        s.wide_a = rows_on(y, ldy, e, 16);
+        return KDA_NORM_PICK(run_forward, R, E, 8, s, a, r_out, ldro, y, ldy, stream);
+    }
+    if constexpr (e == 2) {
+        if (rows_on(a.r, a.ldr, re, 4) && rows_on(a.o, a.ldo, e, 4) && rows_on(a.z, a.ldz, e, 4)) {
+            s.wide_r = rows_on(r_out, ldro, re, 2 * re);
+            s.wide_a = rows_on(y, ldy, e, 4);
+            return KDA_NORM_PICK(run_forward, R, E, 2, s, a, r_out, ldro, y, ldy, stream);
+        }
+    }
+    return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
+}
+
+template <typename R, typename E>
+cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy, const NormGrads &g,
+                          float *part, int *grid, cudaStream_t stream)
+{
+    constexpr int re = sizeof(R), e = sizeof(E);
+    auto on = [&](int r_bytes, int e_bytes) {
+        return (!a.w_pre || (rows_on(a.r, a.ldr, re, r_bytes) && rows_on(dy, lddy, e, e_bytes))) && rows_on(dro, lddro, re, r_bytes) &&
+               rows_on(a.o, a.ldo, e, e_bytes) && rows_on(a.z, a.ldz, e, e_bytes);
+    };
+    if (on(16, 16)) {
+        s.wide_r = rows_on(g.dr, g.lddr, re, 16);
+        s.wide_a = rows_on(g.d_o, g.lddo, e, 16);
+        s.wide_b = rows_on(g.dz, g.lddz, e, 16);
+        return KDA_NORM_PICK(run_backward, R, E, 8, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+    }
+    if constexpr (e == 2) {
+        if (on(4, 4)) {
+            s.wide_r = rows_on(g.dr, g.lddr, re, 2 * re);
+            s.wide_a = rows_on(g.d_o, g.lddo, e, 4);
+            s.wide_b = rows_on(g.dz, g.lddz, e, 4);
+            return KDA_NORM_PICK(run_backward, R, E, 2, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+        }
+    }
+    return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+}
+
+// One translation unit per activation type.
+cudaError_t forward_bf16(int rtype, Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream);
+cudaError_t forward_f16(int rtype, Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream);
+cudaError_t forward_f32(int rtype, Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream);
+cudaError_t backward_bf16(int rtype, Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy,
+                          const NormGrads &g, float *part, int *grid, cudaStream_t stream);
+cudaError_t backward_f16(int rtype, Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy,
+                         const NormGrads &g, float *part, int *grid, cudaStream_t stream);
+cudaError_t backward_f32(int rtype, Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy,
+                         const NormGrads &g, float *part, int *grid, cudaStream_t stream);
+
+}  // namespace norm
+}  // namespace kda

@@ -1,0 +1,14 @@
+// Block norms, forward, activations in f16 (kernels in block_norm.cuh).
+#include "block_norm.cuh"
+
+namespace kda {
+namespace norm {
+
+cudaError_t forward_f16(int rtype, Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
+{
+    return rtype == KDA_TYPE_F32 ? pick_forward<float, __half>(s, a, r_out, ldro, y, ldy, stream)
+                                 : pick_forward<__half, __half>(s, a, r_out, ldro, y, ldy, stream);
+}
+
+}  // namespace norm
+}  // namespace kda

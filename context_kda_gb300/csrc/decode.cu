@@ -1,45 +1,136 @@
 // One KDA token per slot, from and into the slot's fp32 state (K x V per head):
 //     S~ = Diag(exp g) S,  d = beta (v - S~^T k),  S = S~ + k d^T,  o = scale S^T q.
 //
-// One CTA per (token, head), one thread per value column: it reads its column twice (for S~^T k, then
-// for the update) and writes it once.
+// The state is 64 KiB a head and is read and written once; nothing else matters, so the kernel is a copy
+// with a product on the way.  Value columns do not depend on one another: a CTA takes CT columns of
+// one (token, head), its 256 threads load them in 16-byte pieces (all before the first use) and hold
+// them in registers.  S~^T k and S~^T q come from one pass over the registers, and
+//     o = scale (S~^T q + (q . k) d),
+// so that the columns are summed once, before the update.
 #include "elem.cuh"
 #include "kda_internal.cuh"
 
 namespace kda {
 namespace {
 
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+
 __device__ int g_decode_status;
 
-template <typename E>
-__global__ void __launch_bounds__(VD) decode_step(int B, int H, const int32_t *slots, int num_slots, DecodeIn in, float scale,
-                                                  float *state, void *o_, int64_t ldo)
+template <typename E, int CT>
+__global__ void __launch_bounds__(THREADS) decode_step(int H, const int32_t *slots, int num_slots, DecodeIn in, float scale,
+                                                       float *state, void *o_, int64_t ldo)
 {
-    __shared__ float s_a[KD], s_k[KD], s_q[KD];
-    const int h = blockIdx.y, c = threadIdx.x;
-    const int64_t b = blockIdx.x;
+    constexpr int LANES = CT / 4;            // lanes of a row's columns
+    constexpr int ROWS = THREADS / LANES;    // rows of one load of the CTA
+    constexpr int R = KD / ROWS;             // rows of a thread
+    __shared__ float4 s_row[KD];             // exp g, k, q of a row
+    __shared__ float s_sum[2][WARPS][CT];
+    __shared__ float s_dot[KD / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c0 = blockIdx.x * CT, h = blockIdx.y;
+    const int64_t b = blockIdx.z;
     const int slot = slots ? slots[b] : static_cast<int>(b);
-    E *o = static_cast<E *>(o_) + b * ldo + h * VD + c;
+    E *o = static_cast<E *>(o_) + b * ldo + h * VD + c0;
     if (slot < 0 || slot >= num_slots) {
-        *o = from_f32<E>(0.f);
-        if (slot >= num_slots && c == 0) record_status(&g_decode_status, KDA_ERR_INVALID_ARG);
+        if (tid < CT) o[tid] = from_f32<E>(0.f);
+        if (slot >= num_slots && tid == 0) record_status(&g_decode_status, KDA_ERR_INVALID_ARG);
         return;
     }
-    s_a[c] = expf(in.g[b * in.ldg + h * KD + c]);
-    s_k[c] = to_f32(static_cast<const E *>(in.k)[b * in.ldk + h * KD + c]);
-    s_q[c] = to_f32(static_cast<const E *>(in.q)[b * in.ldq + h * KD + c]);
-    __syncthreads();
-    float *S = state + (static_cast<int64_t>(slot) * H + h) * KD * VD + c;
-    float u = 0.f;
-    for (int k = 0; k < KD; ++k) u = fmaf(s_k[k], s_a[k] * S[k * VD], u);
-    const float d = in.beta[b * in.ldb + h] * (to_f32(static_cast<const E *>(in.v)[b * in.ldv + h * VD + c]) - u);
-    float y = 0.f;
-    for (int k = 0; k < KD; ++k) {
-        const float v = fmaf(s_k[k], d, s_a[k] * S[k * VD]);
-        S[k * VD] = v;
-        y = fmaf(s_q[k], v, y);
+    const int col = (tid % LANES) * 4, row0 = tid / LANES;
+    float *S = state + ((static_cast<int64_t>(slot) * H + h) * KD + row0) * VD + c0 + col;
+    float4 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = *reinterpret_cast<const float4 *>(S + r * ROWS * VD);
+    if (tid < KD) {
+        const float a = expf(in.g[b * in.ldg + h * KD + tid]);
+        const float k = to_f32(static_cast<const E *>(in.k)[b * in.ldk + h * KD + tid]);
+        const float q = to_f32(static_cast<const E *>(in.q)[b * in.ldq + h * KD + tid]);
+        s_row[tid] = make_float4(a, k, q, 0.f);
+        float dot = q * k;
+        for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        if (lane == 0) s_dot[warp] = dot;
     }
-    *o = from_f32<E>(scale * y);
+    float v = 0.f, beta = 0.f;
+    if (tid < CT) {
+        v = to_f32(static_cast<const E *>(in.v)[b * in.ldv + h * VD + c0 + tid]);
+        beta = in.beta[b * in.ldb + h];
+    }
+    __syncthreads();
+    float u[4] = {}, w[4] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float4 p = s_row[row0 + r * ROWS];
+        s[r].x *= p.x;
+        s[r].y *= p.x;
+        s[r].z *= p.x;
+        s[r].w *= p.x;
+        u[0] = fmaf(p.y, s[r].x, u[0]);
+        u[1] = fmaf(p.y, s[r].y, u[1]);
+        u[2] = fmaf(p.y, s[r].z, u[2]);
+        u[3] = fmaf(p.y, s[r].w, u[3]);
+        w[0] = fmaf(p.z, s[r].x, w[0]);
+        w[1] = fmaf(p.z, s[r].y, w[1]);
+        w[2] = fmaf(p.z, s[r].z, w[2]);
+        w[3] = fmaf(p.z, s[r].w, w[3]);
+    }
+#pragma unroll
+    for (int m = LANES; m < 32; m *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u[j] += __shfl_xor_sync(0xffffffffu, u[j], m);
+            w[j] += __shfl_xor_sync(0xffffffffu, w[j], m);
+        }
+    if (lane < LANES) {
+        *reinterpret_cast<float4 *>(&s_sum[0][warp][col]) = make_float4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<float4 *>(&s_sum[1][warp][col]) = make_float4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();
+    if (tid < CT) {
+        float su = 0.f, sw = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < WARPS; ++j) {
+            su += s_sum[0][j][tid];
+            sw += s_sum[1][j][tid];
+        }
+#pragma unroll
+        for (int j = 0; j < KD / 32; ++j) dot += s_dot[j];
+        const float d = beta * (v - su);
+        o[tid] = from_f32<E>(scale * fmaf(dot, d, sw));
+        s_sum[0][0][tid] = d;      // read above by this thread alone
+    }
+    __syncthreads();
+    const float4 d = *reinterpret_cast<const float4 *>(&s_sum[0][0][col]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float k = s_row[row0 + r * ROWS].y;
+        s[r].x = fmaf(k, d.x, s[r].x);
+        s[r].y = fmaf(k, d.y, s[r].y);
+        s[r].z = fmaf(k, d.z, s[r].z);
+        s[r].w = fmaf(k, d.w, s[r].w);
+        *reinterpret_cast<float4 *>(S + r * ROWS * VD) = s[r];
+    }
+}
+
+template <typename E>
+cudaError_t launch(int B, int H, const int32_t *slots, int num_slots, const DecodeIn &in, float scale, float *state, void *o,
+                   int64_t ldo, cudaStream_t stream)
+{
+    // grid.z is at most 65535: more tokens go in several launches
+    for (int64_t b = 0; b < B; b += 65535) {
+        const int n = static_cast<int>(B - b < 65535 ? B - b : 65535);
+        DecodeIn p = in;
+        p.q = static_cast<const E *>(in.q) + b * in.ldq;
+        p.k = static_cast<const E *>(in.k) + b * in.ldk;
+        p.v = static_cast<const E *>(in.v) + b * in.ldv;
+        p.g = in.g + b * in.ldg;
+        p.beta = in.beta + b * in.ldb;
+        const int32_t *sl = slots ? slots + b : nullptr;
+        float *st = slots ? state : state + b * H * KD * VD;
+        E *out = static_cast<E *>(o) + b * ldo;
+        decode_step<E, 64><<<dim3(2, H, n), THREADS, 0, stream>>>(H, sl, num_slots, p, scale, st, out, ldo);
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -47,11 +138,9 @@ __global__ void __launch_bounds__(VD) decode_step(int B, int H, const int32_t *s
 cudaError_t launch_decode_step(int B, int H, int type, const int32_t *slots, int num_slots, const DecodeIn &in, float scale,
                                float *state, void *o, int64_t ldo, cudaStream_t stream)
 {
-    const dim3 grid(B, H);
-    if (type == KDA_TYPE_F32) decode_step<float><<<grid, VD, 0, stream>>>(B, H, slots, num_slots, in, scale, state, o, ldo);
-    else if (type == KDA_TYPE_F16) decode_step<__half><<<grid, VD, 0, stream>>>(B, H, slots, num_slots, in, scale, state, o, ldo);
-    else decode_step<__nv_bfloat16><<<grid, VD, 0, stream>>>(B, H, slots, num_slots, in, scale, state, o, ldo);
-    return cudaGetLastError();
+    if (type == KDA_TYPE_F32) return launch<float>(B, H, slots, num_slots, in, scale, state, o, ldo, stream);
+    if (type == KDA_TYPE_F16) return launch<__half>(B, H, slots, num_slots, in, scale, state, o, ldo, stream);
+    return launch<__nv_bfloat16>(B, H, slots, num_slots, in, scale, state, o, ldo, stream);
 }
 
 int take_decode_status()
