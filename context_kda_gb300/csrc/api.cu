@@ -5,7 +5,9 @@
 // fallback path (cuLA PR #110, "feat(cp): add opt-in NVSHMEM CP state handoff",
 // §Supported configuration: request an error instead of fallback).
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "elem.cuh"
 #include "kda_internal.cuh"
@@ -546,6 +548,14 @@ bool norm_group_ok(int32_t D, int32_t group)
            ((group == 32 || group == 64 || group == 128 || group == 256) && D % group == 0);
 }
 
+// The block norm's kernels count rows in 32 bits and step between them by a 32-bit number of bytes.
+bool norm_steps_ok(int64_t T, std::initializer_list<std::pair<int64_t, int>> strides)
+{
+    for (const auto &s : strides)
+        if (s.first > INT32_MAX / s.second) return false;
+    return T <= INT32_MAX;
+}
+
 // What both directions of the block norm check of the arguments they share.
 int norm_in_ok(int64_t T, int32_t D, int32_t rtype, int32_t type, const kda::NormIn &a, float eps)
 {
@@ -635,6 +645,9 @@ extern "C" int kda_block_norm_forward(int64_t T, int32_t D, int32_t res_type, in
     if (!r && !o) return KDA_ERR_INVALID_ARG;
     if (!rows_ok_or_null(r_out, ldr_out, D, kda::elem_bytes(res_type)) || !rows_ok_or_null(y, ldy, D, kda::elem_bytes(type)))
         return KDA_ERR_INVALID_ARG;
+    const int e = kda::elem_bytes(type), re = kda::elem_bytes(res_type);
+    if (!norm_steps_ok(T, {{r ? ldr : 0, re}, {o ? ldo : 0, e}, {z ? ldz : 0, e}, {r_out ? ldr_out : 0, re}, {y ? ldy : 0, e}}))
+        return KDA_ERR_UNSUPPORTED;
     return cuda_status(kda::launch_norm_forward(T, D, res_type, type, a, r_out, ldr_out, y, ldy,
                                                 static_cast<cudaStream_t>(stream)));
 }
@@ -661,6 +674,9 @@ extern "C" int kda_block_norm_backward(int64_t T, int32_t D, int32_t res_type, i
             !rows_ok_or_null(d_o, lddo, D, e) || !rows_ok_or_null(dz, lddz, D, e))
             return KDA_ERR_INVALID_ARG;
     }
+    if (!norm_steps_ok(T, {{r_out ? ldr_out : 0, re}, {o ? ldo : 0, e}, {z ? ldz : 0, e}, {dr_out ? lddr_out : 0, re},
+                           {dy ? lddy : 0, e}, {dr ? lddr : 0, re}, {d_o ? lddo : 0, e}, {dz ? lddz : 0, e}}))
+        return KDA_ERR_UNSUPPORTED;
     if (!ws || !aligned16(ws)) return KDA_ERR_INVALID_ARG;
     if (ws_bytes < kda::norm_workspace_bytes(D)) return KDA_ERR_WORKSPACE;
     return cuda_status(kda::launch_norm_backward(T, D, res_type, type, a, dr_out, lddr_out, dy, lddy, g, ws,

@@ -52,7 +52,7 @@ cudaError_t launch_norm_forward(int64_t T, int D, int rtype, int type, const Nor
                                 int64_t ldy, cudaStream_t stream)
 {
     norm::Shape s = {};
-    s.T = T;
+    s.T = static_cast<uint32_t>(T);
     s.D = D;
     s.G = a.group ? a.group : D;
     if (type == KDA_TYPE_F32) return norm::forward_f32(rtype, s, a, r_out, ldro, y, ldy, stream);
@@ -64,7 +64,7 @@ cudaError_t launch_norm_backward(int64_t T, int D, int rtype, int type, const No
                                  const void *dy, int64_t lddy, const NormGrads &g, void *ws, cudaStream_t stream)
 {
     norm::Shape s = {};
-    s.T = T;
+    s.T = static_cast<uint32_t>(T);
     s.D = D;
     s.G = a.group ? a.group : D;
     float *part = static_cast<float *>(ws);

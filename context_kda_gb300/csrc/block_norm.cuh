@@ -20,6 +20,8 @@
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 #pragma once
 
+#include <type_traits>
+
 #include "elem.cuh"
 #include "kda_internal.cuh"
 #include "tc.cuh"
@@ -31,7 +33,7 @@ constexpr int MAX_GRID = 304;   // CTAs of a launch: rows of the backward's colu
 
 // What both directions take besides NormIn.
 struct Shape {
-    int64_t T;
+    uint32_t T;
     int D, G, NT;                // channels, channels of a group, threads of a row
     bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes (or on pairs): residual, the others
 };
@@ -46,24 +48,33 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
     static constexpr int PB = RUN >= 16 ? 16 : 4, PIECES = COPY ? RUN / PB : 0, EPP = PB / static_cast<int>(sizeof(X));
     static constexpr int BYTES = COPY ? NE * static_cast<int>(sizeof(X)) * BLOCK : 0;   // of the CTA, per step
 
-    // Copies the row's channels below D to the slots at 'base' (nothing is read when 'in' is false).
-    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *any, int ti, int NT, int D, bool in)
+    static __device__ __forceinline__ void copy(uint32_t dst, const X *src, int bytes)
+    {
+        if constexpr (PB == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    }
+    // Copies the row's channels below D to the slots at 'base' + the thread's; 'row' is at the thread's first channel.
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, int ti, int NT, int D)
     {
         if constexpr (COPY) {
 #pragma unroll
             for (int q = 0; q < NU; ++q)
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) {
-                    const int c = (ti + q * NT) * U + p * EPP;
-                    const int left = in ? (D - c) * static_cast<int>(sizeof(X)) : 0;
+                    const int left = (D - (ti + q * NT) * U - p * EPP) * static_cast<int>(sizeof(X));
                     const int bytes = left < 0 ? 0 : left > PB ? PB : left;
-                    const X *src = bytes ? row + c : any;
-                    const uint32_t dst = base + ((q * PIECES + p) * BLOCK + threadIdx.x) * PB;
-                    if constexpr (PB == 16)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-                    else
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+                    copy(base + ((q * PIECES + p) * BLOCK + threadIdx.x) * PB, bytes ? row + q * NT * U + p * EPP : row, bytes);
                 }
+        }
+    }
+    // Zeros in place of a row past the end ('any': some address of the tensor).
+    static __device__ __forceinline__ void fetch_none(uint32_t base, const X *any)
+    {
+        if constexpr (COPY) {
+#pragma unroll
+            for (int j = 0; j < NU * PIECES; ++j) copy(base + (j * BLOCK + threadIdx.x) * PB, any, 0);
         }
     }
     static __device__ __forceinline__ void unpack(uint32_t w, float *v, __nv_bfloat16 *)
@@ -134,44 +145,82 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
     }
 };
 
-// Sums of N values over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp
-// take one barrier: the partial sums go to one of two buffers in turn.
-template <int N, int BLOCK> struct Sums {
-    float part[2][N][BLOCK / 32];
-    __device__ __forceinline__ void over_row(float (&v)[N], int NT, int turn)
+// Sums over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp take one barrier: the
+// warps' sums go to one of two buffers in turn.
+template <int BLOCK> struct Sums {
+    float part[2][2][BLOCK / 32];
+    static __device__ __forceinline__ float xor_add(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
+    // A sum over the lanes that differ in the bits of n - 1 (n a power of two).
+    static __device__ __forceinline__ float lanes(float v, int n)
     {
-#pragma unroll
-        for (int m = 16; m; m >>= 1)
-            if (m < NT)
-#pragma unroll
-                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
-        if (NT <= 32) return;
+        if (n > 16) v = xor_add(v, 16);
+        if (n > 8) v = xor_add(v, 8);
+        if (n > 4) v = xor_add(v, 4);
+        if (n > 2) v = xor_add(v, 2);
+        if (n > 1) v = xor_add(v, 1);
+        return v;
+    }
+    __device__ __forceinline__ float over_row(float v, int NT, int turn)
+    {
+        v = lanes(v, NT < 32 ? NT : 32);
+        if (NT <= 32) return v;
         const int warp = threadIdx.x >> 5, n = NT >> 5, w0 = warp & ~(n - 1);
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int j = 0; j < N; ++j) part[turn & 1][j][warp] = v[j];
+        if ((threadIdx.x & 31) == 0) part[turn & 1][0][warp] = v;
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float s = 0.f;
-            for (int w = 0; w < n; ++w) s += part[turn & 1][j][w0 + w];
-            v[j] = s;
+        return lanes(part[turn & 1][0][w0 + (threadIdx.x & (n - 1))], n);
+    }
+    // Two sums at once: each half of a warp takes one of them.
+    __device__ __forceinline__ void over_row(float &u, float &v, int NT, int turn)
+    {
+        if (NT < 32) {
+            u = lanes(u, NT);
+            v = lanes(v, NT);
+            return;
         }
+        const bool upper = threadIdx.x & 16;
+        float w = (upper ? v : u) + __shfl_xor_sync(0xffffffffu, upper ? u : v, 16);
+        w = lanes(w, 16);
+        if (NT > 32) {
+            const int warp = threadIdx.x >> 5, n = NT >> 5, w0 = warp & ~(n - 1);
+            if ((threadIdx.x & 15) == 0) part[turn & 1][upper][warp] = w;
+            __syncthreads();
+            if (n == 32) {       // more partial sums than lanes of a half
+                u = lanes(part[turn & 1][0][threadIdx.x & 31], 32);
+                v = lanes(part[turn & 1][1][threadIdx.x & 31], 32);
+                return;
+            }
+            w = lanes(part[turn & 1][upper][w0 + (threadIdx.x & (n - 1))], n);
+        }
+        u = __shfl_sync(0xffffffffu, w, 0);
+        v = __shfl_sync(0xffffffffu, w, 16);
     }
 };
+
+// Row t of a tensor of rows 'ld' bytes apart, at the channels from 'first' on.
+template <typename X> __device__ __forceinline__ X *row_at(X *p, uint32_t t, uint32_t ld, int first)
+{
+    using Byte = typename std::conditional<std::is_const<X>::value, const char, char>::type;
+    return reinterpret_cast<X *>(reinterpret_cast<Byte *>(p + first) + static_cast<uint64_t>(t) * ld);
+}
 
 // Sums over each run's group of G channels (G < D), in place.  G spans G / U lanes of consecutive threads,
 // which may be several warps when runs are short (NT U is then at least G).
 template <int BLOCK, int NU, int U> struct GroupSums {
     float part[U < 8 ? 2 : 1][U < 8 ? NU : 1][BLOCK / 32];
+    static __device__ __forceinline__ void fold(float (&v)[NU], int m)
+    {
+#pragma unroll
+        for (int q = 0; q < NU; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], m);
+    }
     __device__ __forceinline__ void over_group(float (&v)[NU], int G, int turn)
     {
         const int lanes = G / U;
-#pragma unroll
-        for (int m = 16; m; m >>= 1)
-            if (m < lanes)
-#pragma unroll
-                for (int q = 0; q < NU; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], m);
+#pragma unroll 1
+        for (int m = (lanes < 32 ? lanes : 32) >> 1; m > 8; m >>= 1) fold(v, m);
+        if (lanes >= 16) fold(v, 8);
+        if (lanes >= 8) fold(v, 4);
+        fold(v, 2);        // a group is four lanes at least
+        fold(v, 1);
         if constexpr (U < 8) {
             if (lanes <= 32) return;
             const int warp = threadIdx.x >> 5, n = lanes >> 5, w0 = warp & ~(n - 1);
@@ -198,11 +247,8 @@ __device__ __forceinline__ float rcp(float x)
 __device__ __forceinline__ float inv_rms(float mean_sq, float eps) { return rsqrtf(mean_sq + eps); }
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + tc::ex2_ftz(z * -1.4426950408889634f)); }   // exp = infinity: 0
 
-// The gradient of v from e, the gradient of hat = v inv; mean = mean(e hat) over the group.
-__device__ __forceinline__ float unit_grad(float e, float hat, float inv, float mean, bool one, float eps)
-{
-    return inv * (one ? e * (eps * inv * inv) : fmaf(-hat, mean, e));
-}
+// The gradient of a group of one channel from e, the gradient of hat = v inv.
+__device__ __forceinline__ float unit_grad_of_one(float e, float inv, float eps) { return e * (eps * inv) * (inv * inv); }
 
 // A weight's values at a thread's channels (1 where it is absent): kept in registers when they are few.
 template <int NE, int U, typename I>
@@ -222,34 +268,43 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
     using RowE = Row<E, BLOCK, NC, U>;
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = RowR::BYTES + 2 * RowE::BYTES;
-    static constexpr int FIT = STEP ? (NC == 1 ? 112 : 200) * 1024 / STEP : 0;    // two CTAs an SM when NC = 1
+    static constexpr int CTAS = NC == 1 ? 1024 / BLOCK : 1;                       // of an SM
+    static constexpr int FIT = STEP ? 220 / CTAS * 1024 / STEP : 0;
     static constexpr int S = FIT > 3 ? 3 : FIT;      // steps in the ring; 0: no ring
     static constexpr int SMEM = S * STEP;
 };
 
 template <typename R, typename E, int BLOCK, int NC, int U>
-__global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
+__global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
 {
     using F = Forward<R, E, BLOCK, NC, U>;
     using RowR = typename F::RowR;
     using RowE = typename F::RowE;
     constexpr int NE = F::NE, NU = F::NU, S = F::S;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ Sums<1, BLOCK> sums;
+    __shared__ Sums<BLOCK> sums;
     __shared__ GroupSums<BLOCK, NU, U> groups;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
-    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT;
+    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT, rr = threadIdx.x / NT;
     const float inv_d = 1.f / D, inv_g = 1.f / G;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, row0 = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / NT;
+    const uint32_t step = gridDim.x * rows;
+    const uint32_t lr = a.ldr * sizeof(R), lo = a.ldo * sizeof(E), lz = a.ldz * sizeof(E);
     const uint32_t base = tc::smem_u32(ring);
 
-    auto fetch = [&](int slot, int64_t t) {
-        const bool in = t < s.T;
+    // channels past D are not read: the row's first address stands in for theirs
+    const int first = ti * U < D ? ti * U : 0;
+    auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * F::STEP;
-        if (r) RowR::fetch(b, r + t * a.ldr, r, ti, NT, D, in);
-        if (o) RowE::fetch(b + RowR::BYTES, o + t * a.ldo, o, ti, NT, D, in);
-        if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, z + t * a.ldz, z, ti, NT, D, in);
+        if (t < s.T) {
+            if (r) RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
+            if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, first), ti, NT, D);
+            if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first), ti, NT, D);
+        } else {
+            if (r) RowR::fetch_none(b, r);
+            if (o) RowE::fetch_none(b + RowR::BYTES, o);
+            if (z) RowE::fetch_none(b + RowR::BYTES + RowE::BYTES, z);
+        }
     };
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
@@ -267,12 +322,14 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forwar
         branch_weights();
         if (y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
     }
+    uint32_t t0 = blockIdx.x * rows;
     for (int k = 0; k < S - 1; ++k) {
-        fetch(k, row0 + k * step);
+        fetch(k, t0 + rr + k * step);
         cp_commit();
     }
     int slot = 0, turn = 0;
-    for (int64_t t = row0; t - threadIdx.x / NT < s.T; t += step) {
+    for (; t0 < s.T; t0 += step) {
+        const uint32_t t = t0 + rr;
         const bool in = t < s.T;
         if constexpr (S > 0) {
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
@@ -282,16 +339,16 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forwar
         const unsigned char *b = ring + slot * F::STEP;
         float v[NE];
         if (r) {
-            RowR::template read<(S > 0)>(b, r + t * a.ldr, ti, NT, D, in, v);
+            RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
         }
         if (o) {
             float n[NE];
-            RowE::template read<(S > 0)>(b + RowR::BYTES, o + t * a.ldo, ti, NT, D, in, n);
+            RowE::template read<(S > 0)>(b + RowR::BYTES, row_at(o, t, lo, 0), ti, NT, D, in, n);
             float g[NE];
-            if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, z + t * a.ldz, ti, NT, D, in, g);
+            if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), ti, NT, D, in, g);
             if (a.w_post) {
                 float ss[NU];
 #pragma unroll
@@ -301,11 +358,10 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forwar
                     for (int j = 0; j < U; ++j) ss[q] += n[q * U + j] * n[q * U + j];
                 }
                 if (G == D) {
-                    float one[1] = {0.f};
+                    float all = 0.f;
 #pragma unroll
-                    for (int q = 0; q < NU; ++q) one[0] += ss[q];
-                    sums.over_row(one, NT, turn++);
-                    const float inv = inv_rms(one[0] * inv_g, a.eps);
+                    for (int q = 0; q < NU; ++q) all += ss[q];
+                    const float inv = inv_rms(sums.over_row(all, NT, turn++) * inv_g, a.eps);
 #pragma unroll
                     for (int j = 0; j < NE; ++j) n[j] *= inv;
                 } else {
@@ -329,17 +385,16 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 && NC == 1 ? 2 : 1) forwar
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = fmaf(wl[j], n[j], v[j]);
         }
-        if (r_out && in) RowR::write(r_out + t * ldro, ti, NT, D, s.wide_r, v);
+        if (r_out && in) RowR::write(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
         if (y) {
-            float ss[1] = {0.f};
+            float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < NE; ++j) ss[0] += v[j] * v[j];
-            sums.over_row(ss, NT, turn);
-            const float inv = inv_rms(ss[0] * inv_d, a.eps);
+            for (int j = 0; j < NE; ++j) ss += v[j] * v[j];
+            const float inv = inv_rms(sums.over_row(ss, NT, turn) * inv_d, a.eps);
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
-            if (in) RowE::write(y + t * ldy, ti, NT, D, s.wide_a, v);
+            if (in) RowE::write(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -353,7 +408,8 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
     using RowE = Row<E, BLOCK, NC, U>;
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = 2 * RowR::BYTES + 3 * RowE::BYTES;
-    static constexpr int FIT = STEP ? 200 * 1024 / STEP : 0;
+    static constexpr int CTAS = BLOCK == 256 ? 2 : 1;                             // of an SM
+    static constexpr int FIT = STEP ? 220 / CTAS * 1024 / STEP : 0;
     static constexpr int S = FIT > 3 ? 3 : FIT;
     static constexpr int FOLD = BLOCK * NE * 4;      // the column sums of the CTA, folded at the end
     static constexpr int SMEM = S * STEP > FOLD ? S * STEP : FOLD;
@@ -361,7 +417,7 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
 
 // part: [grid][G + 2 D], the CTA's sums for w_post, ls and w_pre.
 template <typename R, typename E, int BLOCK, int NC, int U>
-__global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R *dro, int64_t lddro, const E *dy, int64_t lddy,
+__global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) backward(Shape s, NormIn a, const R *dro, int64_t lddro, const E *dy, int64_t lddy,
                                                      NormGrads g, float *part)
 {
     using B = Backward<R, E, BLOCK, NC, U>;
@@ -369,29 +425,40 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
     using RowE = typename B::RowE;
     constexpr int NE = B::NE, NU = B::NU, S = B::S;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ Sums<3, BLOCK> sums;
-    __shared__ Sums<1, BLOCK> sum1;
+    __shared__ Sums<BLOCK> sums, sums_o, sums_e;
     __shared__ GroupSums<BLOCK, NU, U> groups;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
     R *dr = static_cast<R *>(g.dr);
     E *d_o = static_cast<E *>(g.d_o), *dz = static_cast<E *>(g.dz);
-    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT;
+    const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT, rr = threadIdx.x / NT;
     const float inv_d = 1.f / D, inv_g = 1.f / G;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, row0 = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / NT;
+    const uint32_t step = gridDim.x * rows;
+    const uint32_t lr = a.ldr * sizeof(R), lo = a.ldo * sizeof(E), lz = a.ldz * sizeof(E);
+    const uint32_t ldr = lddro * sizeof(R), ldy = lddy * sizeof(E);
     const uint32_t base = tc::smem_u32(ring);
     constexpr int O_DRO = RowR::BYTES, O_DY = 2 * RowR::BYTES, O_O = O_DY + RowE::BYTES, O_Z = O_O + RowE::BYTES;
 
-    auto fetch = [&](int slot, int64_t t) {
-        const bool in = t < s.T;
+    const int first = ti * U < D ? ti * U : 0;
+    auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * B::STEP;
-        if (a.w_pre) {
-            RowR::fetch(b, r + t * a.ldr, r, ti, NT, D, in);
-            RowE::fetch(b + O_DY, dy + t * lddy, dy, ti, NT, D, in);
+        if (t < s.T) {
+            if (a.w_pre) {
+                RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
+                RowE::fetch(b + O_DY, row_at(dy, t, ldy, first), ti, NT, D);
+            }
+            if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, first), ti, NT, D);
+            if (o) RowE::fetch(b + O_O, row_at(o, t, lo, first), ti, NT, D);
+            if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, first), ti, NT, D);
+        } else {
+            if (a.w_pre) {
+                RowR::fetch_none(b, r);
+                RowE::fetch_none(b + O_DY, dy);
+            }
+            if (dro) RowR::fetch_none(b + O_DRO, dro);
+            if (o) RowE::fetch_none(b + O_O, o);
+            if (z) RowE::fetch_none(b + O_Z, z);
         }
-        if (dro) RowR::fetch(b + O_DRO, dro + t * lddro, dro, ti, NT, D, in);
-        if (o) RowE::fetch(b + O_O, o + t * a.ldo, o, ti, NT, D, in);
-        if (z) RowE::fetch(b + O_Z, z + t * a.ldz, z, ti, NT, D, in);
     };
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
@@ -401,15 +468,17 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
     float wg[NE], wl[NE], wr[NE];
     if constexpr (NC == 1) {
         weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
-        weights<NE, U>(a.ls, 1.f, in_row, ti, NT, D, wl);
+        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
         weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
     }
+    uint32_t t0 = blockIdx.x * rows;
     for (int k = 0; k < S - 1; ++k) {
-        fetch(k, row0 + k * step);
+        fetch(k, t0 + rr + k * step);
         cp_commit();
     }
     int slot = 0, turn = 0;
-    for (int64_t t = row0; t - threadIdx.x / NT < s.T; t += step) {
+    for (; t0 < s.T; t0 += step) {
+        const uint32_t t = t0 + rr;
         const bool in = t < s.T;
         if constexpr (S > 0) {
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
@@ -418,60 +487,67 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
         }
         const unsigned char *b = ring + slot * B::STEP;
         float ov[NE], rv[NE], e[NE];
-        float total[3] = {0.f, 0.f, 0.f};       // sums of r^2, e r, o^2 over the row
+        float ss = 0.f, ev_r = 0.f;             // sums of r^2 and of e r over the row
         float so[NU];                           // of o^2 over the groups
         if (a.w_pre) {
-            RowR::template read<(S > 0)>(b, r + t * a.ldr, ti, NT, D, in, rv);
-            RowE::template read<(S > 0)>(b + O_DY, dy + t * lddy, ti, NT, D, in, e);
+            RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, rv);
+            RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy, 0), ti, NT, D, in, e);
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                total[0] += rv[j] * rv[j];
-                total[1] += e[j] * wr[j] * rv[j];
+                ss = fmaf(rv[j], rv[j], ss);
+                ev_r = fmaf(e[j] * wr[j], rv[j], ev_r);
             }
         }
         if (o) {
-            RowE::template read<(S > 0)>(b + O_O, o + t * a.ldo, ti, NT, D, in, ov);
+            RowE::template read<(S > 0)>(b + O_O, row_at(o, t, lo, 0), ti, NT, D, in, ov);
+            if (a.w_post) {
+                float all = 0.f;
 #pragma unroll
-            for (int q = 0; q < NU; ++q) {
-                so[q] = 0.f;
+                for (int q = 0; q < NU; ++q) {
+                    so[q] = 0.f;
 #pragma unroll
-                for (int j = 0; j < U; ++j) so[q] += ov[q * U + j] * ov[q * U + j];
-                total[2] += so[q];
+                    for (int j = 0; j < U; ++j) so[q] = fmaf(ov[q * U + j], ov[q * U + j], so[q]);
+                    all += so[q];
+                }
+                if (G == D) {
+                    all = sums_o.over_row(all, NT, turn);
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) so[q] = all;
+                } else {
+                    groups.over_group(so, G, turn);
+                }
             }
         }
-        sums.over_row(total, NT, turn);
         float v[NE];                            // the gradient of r', then that of o
         if (dro) {
-            RowR::template read<(S > 0)>(b + O_DRO, dro + t * lddro, ti, NT, D, in, v);
+            RowR::template read<(S > 0)>(b + O_DRO, row_at(dro, t, ldr, 0), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
         }
         if (a.w_pre) {
-            const float inv = inv_rms(total[0] * inv_d, a.eps), mean = total[1] * inv_d * inv;
+            sums.over_row(ss, ev_r, NT, turn);
+            const float inv = inv_rms(ss * inv_d, a.eps), mean = ev_r * inv_d * inv;
+            if (D == 1) {
+                v[0] += unit_grad_of_one(e[0] * wr[0], inv, a.eps);
+                acc_r[0] = fmaf(e[0], rv[0] * inv, acc_r[0]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                const float hat = rv[j] * inv;
-                acc_r[j] = fmaf(e[j], hat, acc_r[j]);
-                v[j] += unit_grad(e[j] * wr[j], hat, inv, mean, D == 1, a.eps);
-            }
-        }
-        if (dr && in) RowR::write(dr + t * g.lddr, ti, NT, D, s.wide_r, v);
-        if (o) {
-            if (a.w_post) {
-                if (G == D) {
-#pragma unroll
-                    for (int q = 0; q < NU; ++q) so[q] = total[2];
-                } else {
-                    groups.over_group(so, G, turn);
+                for (int j = 0; j < NE; ++j) {
+                    const float hat = rv[j] * inv;
+                    acc_r[j] = fmaf(e[j], hat, acc_r[j]);
+                    v[j] = fmaf(inv, fmaf(-hat, mean, e[j] * wr[j]), v[j]);
                 }
             }
+        }
+        if (dr && in) RowR::write(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
+        if (o) {
             float gz[NE];
-            if (z) RowE::template read<(S > 0)>(b + O_Z, z + t * a.ldz, ti, NT, D, in, gz);
+            if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz, 0), ti, NT, D, in, gz);
             if constexpr (NC > 1) {
                 weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
-                weights<NE, U>(a.ls, 1.f, in_row, ti, NT, D, wl);
+                weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
             }
             float ev[NU], inv[NU];
 #pragma unroll
@@ -479,13 +555,12 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
                 inv[q] = a.w_post ? inv_rms(so[q] * inv_g, a.eps) : 1.f;
                 ev[q] = 0.f;
             }
-            // channel j with the gate's value and derivative: v becomes the gradient of hat, ov becomes hat
-            auto channel = [&](int j, float act, float slope) {
-                const float hat = ov[j] * inv[j / U], n = hat * wg[j], tt = a.scale * v[j], ta = tt * act;
-                acc_l[j] = fmaf(ta, n, acc_l[j]);
-                gz[j] = tt * wl[j] * n * slope;
-                const float dn = ta * wl[j];
+            // channel j with the gate's value and derivative times v: v becomes the gradient of hat, ov becomes hat
+            auto channel = [&](int j, float va, float vs) {
+                const float hat = ov[j] * inv[j / U], n = hat * wg[j], dn = va * wl[j];
+                acc_l[j] = fmaf(va, n, acc_l[j]);      // times the scale, at the end
                 acc_g[j] = fmaf(dn, hat, acc_g[j]);
+                gz[j] = vs * wl[j] * n;
                 v[j] = dn * wg[j];
                 ov[j] = hat;
                 ev[j / U] = fmaf(v[j], hat, ev[j / U]);
@@ -493,35 +568,39 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
             if (a.gate == KDA_GATE_SIGMOID) {
 #pragma unroll
                 for (int j = 0; j < NE; ++j) {
-                    const float p = sigmoid(gz[j]);
-                    channel(j, p, fmaf(-p, p, p));
+                    const float p = sigmoid(gz[j]), va = v[j] * p;
+                    channel(j, va, fmaf(-va, p, va));
                 }
             } else if (a.gate == KDA_GATE_SILU) {
 #pragma unroll
                 for (int j = 0; j < NE; ++j) {
-                    const float p = sigmoid(gz[j]), act = gz[j] * p;
-                    channel(j, act, fmaf(act, 1.f - p, p));
+                    const float p = sigmoid(gz[j]), va = v[j] * p;
+                    channel(j, va * gz[j], va * fmaf(gz[j], 1.f - p, 1.f));
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) channel(j, 1.f, 0.f);
+                for (int j = 0; j < NE; ++j) channel(j, v[j], 0.f);
             }
-            if (dz && in) RowE::write(dz + t * g.lddz, ti, NT, D, s.wide_b, gz);
+            if (dz && in) RowE::write(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), 0), ti, NT, D, s.wide_b, gz);
             if (a.w_post) {
                 if (G == D) {
-                    float one[1] = {0.f};
+                    float all = 0.f;
 #pragma unroll
-                    for (int q = 0; q < NU; ++q) one[0] += ev[q];
-                    sum1.over_row(one, NT, turn);
+                    for (int q = 0; q < NU; ++q) all += ev[q];
+                    all = sums_e.over_row(all, NT, turn);
 #pragma unroll
-                    for (int q = 0; q < NU; ++q) ev[q] = one[0];
+                    for (int q = 0; q < NU; ++q) ev[q] = all;
                 } else {
                     groups.over_group(ev, G, turn + 1);
                 }
+                if (G == 1) {
+                    v[0] = unit_grad_of_one(v[0], inv[0], a.eps);
+                } else {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) v[j] = unit_grad(v[j], ov[j], inv[j / U], ev[j / U] * inv_g, G == 1, a.eps);
+                    for (int j = 0; j < NE; ++j) v[j] = inv[j / U] * fmaf(-ov[j], ev[j / U] * inv_g, v[j]);
+                }
             }
-            if (in) RowE::write(d_o + t * g.lddo, ti, NT, D, s.wide_a, v);
+            if (in) RowE::write(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -546,20 +625,20 @@ __global__ void __launch_bounds__(BLOCK, 1) backward(Shape s, NormIn a, const R 
             part[c] = v;
         }
     }
-    auto out = [&](float *p) {
+    auto out = [&](float *p, float by) {
         for (int c = threadIdx.x; c < D; c += BLOCK) {
             float v = 0.f;
             for (int k = 0; k < rows; ++k) v += fold[k * width + c];
-            p[c] = v;
+            p[c] = by * v;
         }
     };
     if (g.dls) {
         put(acc_l);
-        out(part + G);
+        out(part + G, a.scale);
     }
     if (g.dw_pre) {
         put(acc_r);
-        out(part + G + D);
+        out(part + G + D, 1.f);
     }
 }
 
@@ -588,7 +667,7 @@ cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, voi
     s.NT = threads_of_row(s.D, s.G, NC, U);
     auto fn = forward<R, E, BLOCK, NC, U>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), F::SMEM)) return e;
-    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = (BLOCK == 512 && NC == 1 ? 2 : 1) * sm_count();
+    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = F::CTAS * sm_count();
     fn<<<static_cast<unsigned>(want < most ? want : most), BLOCK, F::SMEM, stream>>>(s, a, static_cast<R *>(r_out), ldro,
                                                                                       static_cast<E *>(y), ldy);
     return cudaGetLastError();
@@ -602,17 +681,19 @@ cudaError_t run_backward(Shape s, const NormIn &a, const void *dro, int64_t lddr
     s.NT = threads_of_row(s.D, s.G, NC, U);
     auto fn = backward<R, E, BLOCK, NC, U>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), B::SMEM)) return e;
-    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = sm_count() < MAX_GRID ? sm_count() : MAX_GRID;
+    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, full = B::CTAS * sm_count(), most = full < MAX_GRID ? full : MAX_GRID;
     *grid = static_cast<int>(want < most ? want : most);
     fn<<<*grid, BLOCK, B::SMEM, stream>>>(s, a, static_cast<const R *>(dro), lddro, static_cast<const E *>(dy), lddy, g, part);
     return cudaGetLastError();
 }
 
-// The instance for a width and a run: rows of up to 4096 channels take 512 threads with 8 channels each, up to 8192
-// twice the channels, up to 16384 twice the threads.
-#define KDA_NORM_PICK(FN, R, E, U, ...)                                          \
-    (s.D <= 4096 ? FN<R, E, 512, 1, U>(__VA_ARGS__)                              \
-                 : s.D <= 8192 ? FN<R, E, 512, 2, U>(__VA_ARGS__) : FN<R, E, 1024, 2, U>(__VA_ARGS__))
+// The instance for a width and a run: CTAs of 256 threads for rows of up to 2048 channels, 512 up to 4096, 512 with
+// twice the channels a thread up to 8192, 1024 with those up to 16384.
+#define KDA_NORM_PICK(FN, R, E, U, ...)                \
+    (s.D <= 2048   ? FN<R, E, 256, 1, U>(__VA_ARGS__)  \
+     : s.D <= 4096 ? FN<R, E, 512, 1, U>(__VA_ARGS__)  \
+     : s.D <= 8192 ? FN<R, E, 512, 2, U>(__VA_ARGS__)  \
+                   : FN<R, E, 1024, 2, U>(__VA_ARGS__))
 
 template <typename R, typename E>
 cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)

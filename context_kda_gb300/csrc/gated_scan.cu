@@ -19,7 +19,7 @@
 //     tiles); the group's last tile publishes the next group's state.  Only that last step is serial in time,
 //     once in 2048 tokens.  Published words carry their own validity (they are all ones until written,
 //     which no published value is), so that one 8-byte store and one load pass a map on.  A kernel before
-//     the main one sets them, the ticket and each tile's first sequence.
+//     the main one sets them, the ticket and each tile's sequence starts.
 //   - Waits give up after about two seconds (KDA_ERR_TIMEOUT through kda_device_status).
 //
 // The backward takes the states before every 128th token that the forward saved, so a tile recomputes its
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int L = KDA_SCAN_TILE;    // tokens of a tile
 constexpr int THREADS = 256, WARPS = THREADS / 32, W = L / WARPS;   // W: tokens of a warp
-constexpr int GROUP = 16;           // tiles of a group
+constexpr int MIN_GROUP = 8, MAX_GROUP = 16;   // tiles of a group: see run()
 constexpr int MAX_CLUSTER = 8;      // tiles that a cluster covers
 constexpr int DPAD = 64;            // channels are padded to this in the workspace
 constexpr long long SPIN = 4000000000LL;   // clocks of a wait: about two seconds
@@ -47,36 +47,43 @@ __device__ int g_scan_status;
 
 // Workspace of the chain (bytes).
 struct Layout {
-    size_t first, state, map, end;   // each tile's first sequence; groups' states; tiles' maps
+    size_t starts, state, map, end;   // each tile's sequence starts; groups' states; tiles' maps
 };
+// The sequence starts of a tile: bit j: a sequence starts at its token j; 'first': the lowest such sequence.
+// The end of the stream counts as the start of sequence N.
+struct __align__(16) Starts {
+    uint32_t bits[L / 32];
+    int first, pad[3];
+};
+static_assert(sizeof(Starts) == 32, "two 16-byte loads");
 __host__ __device__ inline int tiles_of(int T) { return (T + L - 1) / L; }
 inline Layout layout_of(int64_t T, int D)
 {
     const size_t nT = static_cast<size_t>(T + L - 1) / L, Dp = static_cast<size_t>(D + DPAD - 1) / DPAD * DPAD;
     auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
     Layout l;
-    l.first = 256;                                   // the ticket comes first
-    l.state = up(l.first + (nT + 1) * 4);
-    l.map = up(l.state + (nT + GROUP - 1) / GROUP * Dp * 4);
+    l.starts = 256;                                  // the ticket comes first
+    l.state = up(l.starts + (nT + 1) * sizeof(Starts));
+    l.map = up(l.state + (nT / MIN_GROUP + 1) * Dp * 4);
     l.end = l.map + nT * Dp * 8;
     return l;
 }
 struct Chain {
     int *ticket;
-    const int *first;
+    Starts *starts;       // [tiles + 1]
     uint32_t *state;      // [groups][Dp], all ones until published
     uint64_t *map;        // [tiles][Dp], low word A, high word B
-    int Dp;
+    int Dp, group;        // padded channels; tiles of a group
 };
 inline Chain chain_of(void *ws, int64_t T, int D)
 {
     char *b = static_cast<char *>(ws);
     const Layout l = layout_of(T, D);
-    return Chain{reinterpret_cast<int *>(b), reinterpret_cast<int *>(b + l.first), reinterpret_cast<uint32_t *>(b + l.state),
-                 reinterpret_cast<uint64_t *>(b + l.map), (D + DPAD - 1) / DPAD * DPAD};
+    return Chain{reinterpret_cast<int *>(b), reinterpret_cast<Starts *>(b + l.starts), reinterpret_cast<uint32_t *>(b + l.state),
+                 reinterpret_cast<uint64_t *>(b + l.map), (D + DPAD - 1) / DPAD * DPAD, MAX_GROUP};
 }
 
-__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int *ticket, int *first, uint4 *words,
+__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int *ticket, Starts *starts, uint4 *words,
                                                   size_t n)
 {
     tc::grid_dep_launch();
@@ -86,15 +93,32 @@ __global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig s
     if (id == 0) *ticket = 0;
     const PlanView pv{plan};
     const int32_t *cu = pv.cu();
-    for (size_t j = id; j <= static_cast<size_t>(nT); j += step) {
-        const int64_t t = static_cast<int64_t>(j) * L;     // first n with cu[n] >= t (N + 1: none)
-        int lo = 0, hi = pv.N() + 1;
+    const int lane = threadIdx.x & 31, N = pv.N();
+    for (size_t j = id / 32; j <= static_cast<size_t>(nT); j += step / 32) {     // a warp a tile
+        const int64_t t0 = static_cast<int64_t>(j) * L;
+        int lo = 0, hi = N + 1;                                // first n with cu[n] >= t0 (N + 1: none)
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (cu[mid] < t) lo = mid + 1;
+            if (cu[mid] < t0) lo = mid + 1;
             else hi = mid;
         }
-        first[j] = lo;
+        uint32_t mine[L / 32] = {};
+        for (int k = 0; k < L / 32; ++k) {                     // at most a start a token
+            const int m = lo + k * 32 + lane;
+            const int64_t t = m <= N ? cu[m] - t0 : L;
+#pragma unroll
+            for (int w = 0; w < L / 32; ++w)
+                if (t >> 5 == w) mine[w] |= 1u << (t & 31);
+        }
+#pragma unroll
+        for (int w = 0; w < L / 32; ++w) mine[w] = __reduce_or_sync(0xffffffffu, mine[w]);
+        if (lane == 0) {
+            Starts st = {};
+#pragma unroll
+            for (int w = 0; w < L / 32; ++w) st.bits[w] = mine[w];
+            st.first = lo;
+            starts[j] = st;
+        }
     }
 }
 
@@ -103,6 +127,10 @@ __global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig s
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16_all(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void *src, int bytes)
 {
@@ -123,7 +151,16 @@ __device__ __forceinline__ void fill(X *dst, const X *src, int64_t ld, int t0, i
         const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
         const X *p = src + (t0 + row) * ld + c0 + ch * EPC;
         const uint32_t s = tc::smem_u32(dst + row * C + ch * EPC);
+        if (t0 + L <= T && c0 + C <= D) {
+            const int64_t hop = STEP * ld;
 #pragma unroll
+            for (int k = 0; k < L / STEP; ++k) {
+                cp16_all(s + k * STEP * C * sizeof(X), p);
+                p += hop;
+            }
+            return;
+        }
+#pragma unroll 4
         for (int k = 0; k < L / STEP; ++k) {
             const bool in = t0 + row + k * STEP < T && bytes > 0;
             cp16(s + k * STEP * C * sizeof(X), in ? p + k * STEP * ld : src, in ? bytes : 0);
@@ -280,9 +317,9 @@ template <int V, typename U> __device__ __forceinline__ bool poll(const U *p, U 
 // What the tiles of a channel range pass on: shared memory of both directions.
 template <int C> struct Shared {
     float2 map[WARPS][C];          // the warps' maps
-    float2 before[GROUP][C];       // maps of the tiles before this one (cluster: this tile's in [0])
+    float2 before[MAX_GROUP - 1][C];       // maps of the tiles before this one (cluster: this tile's in [0])
     float state[C];                // the tile's incoming state
-    int seq[2][L + 4];             // per token (one more than the tile's): the sequence that starts there, or -1
+    int seq[L + 4];                // cluster, per token (one more than the tile's): the sequence that starts there, or -1
     int next, bad;
 };
 
@@ -301,34 +338,52 @@ __device__ __forceinline__ float2 ld_cluster(uint32_t addr)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The state that enters tile 'rt' (tiles numbered in the direction of the recurrence), left in sh.state for all
-// threads.  (Am, Bm): this tile's map, in the warp 'last_warp', the last one of the tile in that direction.  False: a
-// wait ran out.
-template <int C, int V, bool WIDE, bool CHAIN>
-__device__ __forceinline__ bool incoming(Shared<C> &sh, const Chain &ch, int rt, int col0, bool last, int last_warp,
-                                         const float (&Am)[V], const float (&Bm)[V])
+// The state that enters each warp's tokens of tile 'rt' (tiles numbered in the direction of the recurrence), from the
+// warps' maps in sh.map; warps are counted in that direction too.  Warp 'last', the tile's last, does what one
+// warp can: it folds the maps (each becomes that of the warps before it), passes the tile's on and folds the state
+// that enters the tile, left in sh.state.  False: a wait ran out.  All threads call it, behind a barrier after the
+// maps were written; meanwhile() runs once this tile's map is on its way and before others are waited for.
+template <int C, int V, bool WIDE, bool CHAIN, bool REVERSE, typename Meanwhile>
+__device__ __forceinline__ bool incoming(Shared<C> &sh, const Chain &ch, int rt, int col0, bool last, float (&h)[V], Meanwhile meanwhile)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = REVERSE ? WARPS - 1 - (threadIdx.x >> 5) : threadIdx.x >> 5;
+    constexpr int last_warp = WARPS - 1;
     int at[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) at[v] = chan<V, WIDE>(lane, v);
+    float Am[V], Bm[V];
+    if (warp == last_warp) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Am[v] = 1.f;
+            Bm[v] = 0.f;
+        }
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float2 m = sh.map[w][at[v]];
+                sh.map[w][at[v]] = make_float2(Am[v], Bm[v]);
+                then(Am[v], Bm[v], m.x, m.y);
+            }
+    }
     if constexpr (CHAIN) {
-        const int pos = rt % GROUP, grp = rt / GROUP;
-        if (warp == last_warp && pos < GROUP - 1 && !last) {   // the group's last tile publishes a state instead
+        const int grp = rt / ch.group, pos = rt - grp * ch.group;
+        if (warp == last_warp && pos < ch.group - 1 && !last) {   // the group's last tile publishes a state instead
             uint64_t *p = ch.map + static_cast<size_t>(rt) * ch.Dp + col0;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 st_relaxed(p + at[v], static_cast<uint64_t>(word(Bm[v])) << 32 | __float_as_uint(Am[v]));
         }
+        meanwhile();
         bool ok = true;
         for (int p = warp; p < pos && ok; p += WARPS) {
             uint64_t w[V];
-            ok = poll<V>(ch.map + static_cast<size_t>(grp * GROUP + p) * ch.Dp + col0, w, at);
+            ok = poll<V>(ch.map + static_cast<size_t>(grp * ch.group + p) * ch.Dp + col0, w, at);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 sh.before[p][at[v]] = make_float2(__uint_as_float(static_cast<uint32_t>(w[v])), __uint_as_float(static_cast<uint32_t>(w[v] >> 32)));
         }
-        float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = 0.f;
         if (warp == last_warp && grp > 0 && ok) {
@@ -348,7 +403,7 @@ __device__ __forceinline__ bool incoming(Shared<C> &sh, const Chain &ch, int rt,
                     const float2 m = sh.before[p][at[v]];
                     h[v] = apply(m.x, m.y, h[v]);
                 }
-            if (pos == GROUP - 1 && !last) {
+            if (pos == ch.group - 1 && !last) {
                 uint32_t *p = ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0;
 #pragma unroll
                 for (int v = 0; v < V; ++v) st_relaxed(p + at[v], word(apply(Am[v], Bm[v], h[v])));
@@ -361,6 +416,7 @@ __device__ __forceinline__ bool incoming(Shared<C> &sh, const Chain &ch, int rt,
 #pragma unroll
             for (int v = 0; v < V; ++v) sh.before[0][at[v]] = make_float2(Am[v], Bm[v]);
         cluster_arrive();
+        meanwhile();
         cluster_wait();
         if (warp == last_warp) {
             float2 m[MAX_CLUSTER - 1][V];
@@ -371,36 +427,77 @@ __device__ __forceinline__ bool incoming(Shared<C> &sh, const Chain &ch, int rt,
                     m[p][v] = p < rt ? ld_cluster(mapa(tc::smem_u32(&sh.before[0][at[v]]), p)) : make_float2(1.f, 0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float h = 0.f;
+                float s = 0.f;
 #pragma unroll
-                for (int p = 0; p < MAX_CLUSTER - 1; ++p) h = p < rt ? apply(m[p][v].x, m[p][v].y, h) : h;
-                sh.state[at[v]] = h;
+                for (int p = 0; p < MAX_CLUSTER - 1; ++p) s = p < rt ? apply(m[p][v].x, m[p][v].y, s) : s;
+                sh.state[at[v]] = s;
             }
         }
         cluster_arrive();   // paired with the wait at the kernel's end: no CTA leaves while its map is read
     }
     __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float2 m = sh.map[warp][at[v]];
+        h[v] = apply(m.x, m.y, sh.state[at[v]]);
+    }
     return true;
 }
 
-// Marks the tile's sequence starts: seq[j] = n where token t0 + j is sequence n's first (n = N at token T).
-// 'first': the first n with cu[n] >= t0, or -1 to look at all of them.  seq must hold -1 everywhere.
-__device__ __forceinline__ void mark_starts(int *seq, const PlanView &pv, int first, int t0)
+// The sequence starts among a warp's tokens and the token after them: bit j of 'mask'; the start at bit j is that of
+// sequence first + (number of bits below j).
+struct Bounds {
+    uint32_t mask;
+    int first;
+    __device__ __forceinline__ int64_t seq(int j) const { return first + __popc(mask & ((1u << j) - 1)); }
+};
+// Chain: from the tile's words and the next tile's first bit (a tile ahead of their use).
+struct Words {
+    uint4 bits;
+    uint32_t after;
+    int first;
+    __device__ __forceinline__ void load(const Starts *st, int tt)
+    {
+        bits = *reinterpret_cast<const uint4 *>(st[tt].bits);
+        first = st[tt].first;
+        after = st[tt + 1].bits[0];
+    }
+    __device__ __forceinline__ Bounds of_warp(int warp) const
+    {
+        constexpr int PER = 32 / W;            // warps of a word
+        const int w = warp / PER, at = warp % PER * W;
+        const uint32_t b[6] = {bits.x, bits.y, bits.z, bits.w, after, 0u};
+        uint32_t cur = 0, next = 0;
+        int below = 0;
+#pragma unroll
+        for (int k = 0; k < L / 32; ++k) {
+            if (k == w) cur = b[k], next = b[k + 1];
+            if (k < w) below += __popc(b[k]);
+        }
+        Bounds r;
+        r.mask = __funnelshift_r(cur, next, at) & ((2u << W) - 1);
+        r.first = first + below + __popc(cur & ((1u << at) - 1));
+        return r;
+    }
+};
+static_assert(32 % W == 0 && L == 128, "whole warps a word, four words a tile");
+// Cluster: the starts are marked in shared memory (seq holds -1 everywhere) and read a warp at a time.
+__device__ __forceinline__ void mark_starts(int *seq, const PlanView &pv, int t0)
 {
     const int32_t *cu = pv.cu();
-    const int N = pv.N();
-    if (first >= 0) {
-        const int n = first + threadIdx.x;    // a start a token at most: L + 1 of them
-        if (threadIdx.x <= L && n <= N) {
-            const int t = cu[n] - t0;
-            if (t <= L) seq[t] = n;
-        }
-        return;
-    }
-    for (int n = threadIdx.x; n <= N; n += THREADS) {
+    for (int n = threadIdx.x; n <= pv.N(); n += THREADS) {
         const int t = cu[n] - t0;
         if (t >= 0 && t <= L) seq[t] = n;
     }
+}
+__device__ __forceinline__ Bounds marked(const int *seq)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = lane <= W ? seq[warp * W + lane] : -1;
+    Bounds r;
+    r.mask = __ballot_sync(0xffffffffu, n >= 0);
+    r.first = __shfl_sync(0xffffffffu, n, r.mask ? __ffs(r.mask) - 1 : 0);
+    return r;
 }
 
 // The tile whose number in the direction of the recurrence is rt and whose channels start at col0.
@@ -417,28 +514,32 @@ template <int C, bool REVERSE> __device__ __forceinline__ Tile tile_of(int k, in
     return t;
 }
 
-// Walks the tiles of a CTA: load(tile) starts the copies of a tile, work(tile, seq, release) computes it and calls
-// release() once the copied data may be overwritten.  work returns false when a wait ran out.
+// Walks the tiles of a CTA: load(tile, part) starts the copies of a tile in two parts, work(tile, bounds, release)
+// computes it; release runs within it, once part 0's copies may be overwritten, part 1's may when it is done.  work
+// returns false when a wait ran out.
 template <int C, bool CHAIN, bool REVERSE, typename Load, typename Work>
 __device__ __forceinline__ void walk(Shared<C> &sh, const Chain &ch, const PlanView &pv, int D, Load load, Work work)
 {
     const int T = pv.T(), nT = tiles_of(T), nC = (D + C - 1) / C;
-    for (int j = threadIdx.x; j < 2 * (L + 4); j += THREADS) (&sh.seq[0][0])[j] = -1;
     if (threadIdx.x == 0) sh.bad = 0;
     if constexpr (!CHAIN) {
+        for (int j = threadIdx.x; j < L + 4; j += THREADS) sh.seq[j] = -1;
         uint32_t cs, rank;
         asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         const int cc = blockIdx.x / cs;
         const Tile t = tile_of<C, REVERSE>(static_cast<int>(rank) * nC + cc, nT, nC);
         const bool real = t.rt < nT;      // clusters are a power of two: some CTAs may be past the end
-        if (real) load(t);
+        if (real) {
+            load(t, 0);
+            load(t, 1);
+        }
         __syncthreads();
-        if (real) mark_starts(sh.seq[0], pv, -1, t.t0);
+        if (real) mark_starts(sh.seq, pv, t.t0);
         cp_wait();
         __syncthreads();
         if (real) {
-            work(t, sh.seq[0], [] {});
+            work(t, marked(sh.seq), [] {});
         } else {
             cluster_arrive();
             cluster_wait();
@@ -446,37 +547,47 @@ __device__ __forceinline__ void walk(Shared<C> &sh, const Chain &ch, const PlanV
         }
         cluster_wait();
     } else {
-        tc::grid_dep_wait();
+        // Tickets are drawn ahead (k: in work, k2: next, then the one drawn while k is in work), so that neither the
+        // draw nor a tile's starts are waited for; the second only once the first tile's copies are on their way, when
+        // all CTAs have drawn their first.  A CTA works its tiles in the order drawn, so the lowest unfinished tile is
+        // always in work with nothing to wait for.
         const int n = nT * nC;
+        tc::grid_dep_wait();
+        int drawn = 0;
         if (threadIdx.x == 0) sh.next = atomicAdd(ch.ticket, 1);
         __syncthreads();
-        int k = sh.next, at = 0;
+        int k = sh.next;
+        Words words = {};
         if (k < n) {
             const Tile t = tile_of<C, REVERSE>(k, nT, nC);
-            load(t);
-            mark_starts(sh.seq[0], pv, ch.first[t.tt], t.t0);
+            load(t, 0);
+            load(t, 1);
+            words.load(ch.starts, t.tt);
+            if (threadIdx.x == 0) drawn = atomicAdd(ch.ticket, 1);
         }
         while (k < n) {
             const Tile t = tile_of<C, REVERSE>(k, nT, nC);
             __syncthreads();                 // everyone has read 'next'
-            if (threadIdx.x == 0) sh.next = atomicAdd(ch.ticket, 1);
+            if (threadIdx.x == 0) sh.next = drawn;
             cp_wait();
             __syncthreads();
             const int k2 = sh.next;
-            const bool ok = work(t, sh.seq[at], [&] {
-                // called between two barriers of the CTA: the copies' buffers are free
-                if (k2 < n) load(tile_of<C, REVERSE>(k2, nT, nC));
+            const Bounds bounds = words.of_warp(threadIdx.x >> 5);
+            const bool ok = work(t, bounds, [&] {
+                // called behind a barrier of the CTA: the copies' buffers are free
+                if (threadIdx.x == 0 && k2 < n) drawn = atomicAdd(ch.ticket, 1);
+                if (k2 < n) {
+                    const Tile u = tile_of<C, REVERSE>(k2, nT, nC);
+                    load(u, 0);
+                    words.load(ch.starts, u.tt);
+                }
             });
             if (!ok) {
                 cp_wait();
                 if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_TIMEOUT);
                 return;
             }
-            at ^= 1;
-            if (k2 < n) {
-                const Tile u = tile_of<C, REVERSE>(k2, nT, nC);
-                mark_starts(sh.seq[at], pv, ch.first[u.tt], u.t0);
-            }
+            if (k2 < n) load(tile_of<C, REVERSE>(k2, nT, nC), 1);
             k = k2;
         }
     }
@@ -507,12 +618,13 @@ __global__ void __launch_bounds__(THREADS, 2) scan_forward(const int32_t *plan, 
     E *h_out = static_cast<E *>(h_);
     const bool pair = V == 1 || !WIDE || pairs(h_out, ldh);
 
-    auto load = [&](const Tile &t) {
+    auto load = [&](const Tile &t, int part) {
+        if (part == 1) return;
         fill<E, C, WIDE>(&sm.x[0][0], x, in.ldx, t.t0, T, t.col0, D);
         if (ig) fill<E, C, WIDE>(&sm.i[0][0], ig, in.ldi, t.t0, T, t.col0, D);
         fill<float, C, WIDE>(&sm.g[0][0], in.g, in.ldg, t.t0, T, t.col0, D);
     };
-    auto work = [&](const Tile &t, int *seq, auto release) {
+    auto work = [&](const Tile &t, const Bounds &bounds, auto release) {
         const int r0 = warp * W, left = D - t.col0;
         float a[W][V], u[W][V];
 #pragma unroll
@@ -533,8 +645,7 @@ __global__ void __launch_bounds__(THREADS, 2) scan_forward(const int32_t *plan, 
             }
         }
         // bit j: a sequence starts at the warp's token j (bit W: at the token after its last)
-        const int sv = lane <= W ? seq[r0 + lane] : -1;
-        const uint32_t mask = __ballot_sync(0xffffffffu, sv >= 0);
+        const uint32_t mask = bounds.mask;
         const int rows = T - t.t0 - r0;      // tokens from the warp's first on
         const uint32_t starts = mask & (rows >= W ? (1u << W) - 1 : rows > 0 ? (1u << rows) - 1 : 0u);
         float A[V], B[V];
@@ -547,8 +658,8 @@ __global__ void __launch_bounds__(THREADS, 2) scan_forward(const int32_t *plan, 
             const float *h0 = in.h0 ? in.h0 + t.col0 : nullptr;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j);
                 if (!(starts >> j & 1)) continue;
+                const int64_t n = bounds.seq(j);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (h0 && chan<V, WIDE>(lane, v) < left) u[j][v] = fmaf(a[j][v], h0[n * D + chan<V, WIDE>(lane, v)], u[j][v]);
@@ -560,59 +671,61 @@ __global__ void __launch_bounds__(THREADS, 2) scan_forward(const int32_t *plan, 
 #pragma unroll
             for (int v = 0; v < V; ++v) A[v] = -1.f;
         } else {
+            // a becomes the product of the decays up to the token, u the state from zero
 #pragma unroll
             for (int j = 1; j < W; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    A[v] *= a[j][v];
-                    B[v] = fmaf(a[j][v], B[v], u[j][v]);
+                    u[j][v] = B[v] = fmaf(a[j][v], B[v], u[j][v]);
+                    a[j][v] = A[v] *= a[j][v];
                 }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) sm.s.map[warp][chan<V, WIDE>(lane, v)] = make_float2(A[v], B[v]);
         __syncthreads();
-        release();
-        if (threadIdx.x <= L) seq[threadIdx.x] = -1;
-        float pa[V], pb[V], h[V];      // the map of the warps before this one
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            pa[v] = 1.f;
-            pb[v] = 0.f;
-        }
-        for (int w = 0; w < warp; ++w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 m = sm.s.map[w][chan<V, WIDE>(lane, v)];
-                then(pa[v], pb[v], m.x, m.y);
-            }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {      // and with it: the tile's in the last warp
-            const float b = A[v] < 0.f ? B[v] : fmaf(A[v], pb[v], B[v]);
-            A[v] = A[v] < 0.f || pa[v] < 0.f ? -1.f : A[v] * pa[v];
-            B[v] = b;
-        }
-        if (!incoming<C, V, WIDE, CHAIN>(sm.s, ch, t.rt, t.col0, t.tt == nT - 1, WARPS - 1, A, B)) return false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = apply(pa[v], pb[v], sm.s.state[chan<V, WIDE>(lane, v)]);
+        float h[V];
+        if (!incoming<C, V, WIDE, CHAIN, false>(sm.s, ch, t.rt, t.col0, t.tt == nT - 1, h, release)) return false;
         E *row = h_out + (t.t0 + r0) * ldh + t.col0;
-        if (mask == 0 && rows >= W && left >= C && pair) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], u[j][v]);
-                put_all<V, WIDE>(row, lane, h);
-                row += ldh;
-            }
-        } else {
+        if (starts) {
 #pragma unroll
             for (int j = 0; j < W; ++j) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) h[v] = starts >> j & 1 ? u[j][v] : fmaf(a[j][v], h[v], u[j][v]);
                 if (j < rows) put<V, WIDE>(row, lane, h, left, pair);
                 row += ldh;
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j + 1) - 1;
-                if ((mask >> (j + 1) & 1) && final_state) put<V, WIDE>(final_state + n * D + t.col0, lane, h, left, false);
+                if ((mask >> (j + 1) & 1) && final_state)
+                    put<V, WIDE>(final_state + (bounds.seq(j + 1) - 1) * D + t.col0, lane, h, left, false);
             }
+        } else {
+            float s[V];
+            if (rows >= W && left >= C && pair) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[v] = fmaf(a[j][v], h[v], u[j][v]);
+                    put_all<V, WIDE>(row, lane, s);
+                    row += ldh;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[v] = fmaf(a[j][v], h[v], u[j][v]);
+                    if (j < rows) put<V, WIDE>(row, lane, s, left, pair);
+                    row += ldh;
+                }
+            }
+            if (mask && final_state) {         // no start among the warp's tokens: the one behind the last, or the stream's end
+                const int j = __ffs(mask) - 2;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    if (k == j)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) s[v] = fmaf(a[k][v], h[v], u[k][v]);
+                if (j >= 0) put<V, WIDE>(final_state + (bounds.seq(j + 1) - 1) * D + t.col0, lane, s, left, false);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = fmaf(a[W - 1][v], h[v], u[W - 1][v]);
         }
         if (states) {
             if (warp == WARPS - 1 && t.tt + 1 < nT)
@@ -654,16 +767,19 @@ __global__ void __launch_bounds__(THREADS, 2) scan_backward(const int32_t *plan,
     E *dx = static_cast<E *>(out.dx), *di = static_cast<E *>(out.di);
     const bool pair = V == 1 || !WIDE || (pairs(dx, out.lddx) && pairs(di, out.lddi) && pairs(out.dg, out.lddg));
 
-    auto load = [&](const Tile &t) {
-        fill<float, C, WIDE>(&sm.g[0][0], in.g, in.ldg, t.t0, T, t.col0, D);
+    // part 0: the decays, which a tile takes to registers; part 1: what it reads again for the gradients
+    auto load = [&](const Tile &t, int part) {
+        if (part == 0) {
+            fill<float, C, WIDE>(&sm.g[0][0], in.g, in.ldg, t.t0, T, t.col0, D);
+            return;
+        }
         fill<E, C, WIDE>(&sm.dh[0][0], dh, lddh, t.t0, T, t.col0, D);
         fill<E, C, WIDE>(&sm.x[0][0], x, in.ldx, t.t0, T, t.col0, D);
         if (ig) fill<E, C, WIDE>(&sm.i[0][0], ig, in.ldi, t.t0, T, t.col0, D);
     };
-    auto work = [&](const Tile &t, int *seq, auto release) {
+    auto work = [&](const Tile &t, const Bounds &bounds, auto release) {
         const int r0 = warp * W, left = D - t.col0, rows = T - t.t0 - r0;
-        const int sv = lane <= W ? seq[r0 + lane] : -1;
-        const uint32_t mask = __ballot_sync(0xffffffffu, sv >= 0);
+        const uint32_t mask = bounds.mask;
         const uint32_t starts = mask & (rows >= W ? (1u << W) - 1 : rows > 0 ? (1u << rows) - 1 : 0u);
         const uint32_t ends = mask >> 1;
         const bool plain = mask == 0 && rows >= W && left >= C && pair;
@@ -672,24 +788,25 @@ __global__ void __launch_bounds__(THREADS, 2) scan_backward(const int32_t *plan,
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] = p && chan<V, WIDE>(lane, v) < left ? p[n * D + t.col0 + chan<V, WIDE>(lane, v)] : 0.f;
         };
-        auto u_of = [&](int j, float (&u)[V]) {
-            get<V, WIDE>(sm.x[r0 + j], lane, u);
-            if (ig) {
-                float iv[V];
-                get<V, WIDE>(sm.i[r0 + j], lane, iv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) u[v] *= iv[v];
-            }
-        };
         float hin[V];                    // the state before the tile
         seq_row(states, t.tt, hin);
-        float a[W][V];
+        float a[W][V], u[W][V];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             float gv[V];
             get<V, WIDE>(sm.g[r0 + j], lane, gv);
+            get<V, WIDE>(sm.x[r0 + j], lane, u[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
+        }
+        if (ig) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                float iv[V];
+                get<V, WIDE>(sm.i[r0 + j], lane, iv);
+#pragma unroll
+                for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
+            }
         }
         float P[V], fb[V], B[V];         // maps of the states (P, fb; forwards) and of the gradients (P, B; backwards)
 #pragma unroll
@@ -697,160 +814,120 @@ __global__ void __launch_bounds__(THREADS, 2) scan_backward(const int32_t *plan,
             P[v] = 1.f;
             fb[v] = B[v] = 0.f;
         }
-        if (mask == 0) {
+        auto maps = [&](auto bounded) {
+            constexpr bool bnd = decltype(bounded)::value;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                float u[V];
-                u_of(j, u);
+                if constexpr (bnd)
+                    if (starts >> j & 1) seq_row(in.h0, bounds.seq(j), fb);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     P[v] *= a[j][v];
-                    fb[v] = fmaf(a[j][v], fb[v], u[v]);
+                    fb[v] = fmaf(a[j][v], fb[v], u[j][v]);
                 }
             }
 #pragma unroll
             for (int j = W - 1; j >= 0; --j) {
                 float d[V];
                 get<V, WIDE>(sm.dh[r0 + j], lane, d);
+                if constexpr (bnd)
+                    if (ends >> j & 1) seq_row(dfinal, bounds.seq(j + 1) - 1, B);
 #pragma unroll
                 for (int v = 0; v < V; ++v) B[v] = a[j][v] * (d[v] + B[v]);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                float u[V];
-                u_of(j, u);
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j);
-                if (starts >> j & 1) seq_row(in.h0, n, fb);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    P[v] *= a[j][v];
-                    fb[v] = fmaf(a[j][v], fb[v], u[v]);
-                }
-            }
-#pragma unroll
-            for (int j = W - 1; j >= 0; --j) {
-                float d[V];
-                get<V, WIDE>(sm.dh[r0 + j], lane, d);
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j + 1) - 1;
-                if (ends >> j & 1) seq_row(dfinal, n, B);
-#pragma unroll
-                for (int v = 0; v < V; ++v) B[v] = a[j][v] * (d[v] + B[v]);
-            }
-        }
-        float A[V];
+        };
+        if (mask == 0) maps(std::false_type{});
+        else maps(std::true_type{});
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = chan<V, WIDE>(lane, v);
-            A[v] = ends ? -1.f : P[v];
             sm.fmap[warp][c] = make_float2(starts ? -1.f : P[v], fb[v]);
-            sm.s.map[warp][c] = make_float2(A[v], B[v]);
+            sm.s.map[WARPS - 1 - warp][c] = make_float2(ends ? -1.f : P[v], B[v]);
         }
         __syncthreads();
-        if (threadIdx.x <= L) seq[threadIdx.x] = -1;
-        float pa[V], pb[V], e[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            pa[v] = 1.f;
-            pb[v] = 0.f;
-        }
-        for (int w = WARPS - 1; w > warp; --w)
+        // the last warp in time has nothing to wait for: it folds the maps of the states (each becomes that of the
+        // warps before it)
+        if (warp == WARPS - 1) {
+            float A[V], S[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float2 m = sm.s.map[w][chan<V, WIDE>(lane, v)];
-                then(pa[v], pb[v], m.x, m.y);
+                A[v] = 1.f;
+                S[v] = 0.f;
             }
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int c = chan<V, WIDE>(lane, v);
+                    const float2 m = sm.fmap[w][c];
+                    sm.fmap[w][c] = make_float2(A[v], S[v]);
+                    then(A[v], S[v], m.x, m.y);
+                }
+        }
+        float e[V];
+        if (!incoming<C, V, WIDE, CHAIN, true>(sm.s, ch, t.rt, t.col0, t.tt == 0, e, release)) return false;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float b = A[v] < 0.f ? B[v] : fmaf(A[v], pb[v], B[v]);
-            A[v] = A[v] < 0.f || pa[v] < 0.f ? -1.f : A[v] * pa[v];
-            B[v] = b;
+            const float2 m = sm.fmap[warp][chan<V, WIDE>(lane, v)];
+            hin[v] = apply(m.x, m.y, hin[v]);
         }
-        if (!incoming<C, V, WIDE, CHAIN>(sm.s, ch, t.rt, t.col0, t.tt == 0, 0, A, B)) return false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = apply(pa[v], pb[v], sm.s.state[chan<V, WIDE>(lane, v)]);
-        for (int w = 0; w < warp; ++w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 m = sm.fmap[w][chan<V, WIDE>(lane, v)];
-                hin[v] = apply(m.x, m.y, hin[v]);
-            }
-        float before[W][V];              // the state before each token
         const int64_t last = t.t0 + r0 + W - 1;
         E *px = dx + last * out.lddx + t.col0, *pi = di ? di + last * out.lddi + t.col0 : nullptr;
         float *pg = out.dg + last * out.lddg + t.col0;
-        // token j's gradients from that of the next state; e becomes that of the one before
-        auto grads = [&](int j, float (&gx)[V], float (&gi)[V], float (&gg)[V]) {
-            float d[V], iv[V];
-            get<V, WIDE>(sm.dh[r0 + j], lane, d);
-            get<V, WIDE>(sm.x[r0 + j], lane, gi);
-            if (ig) get<V, WIDE>(sm.i[r0 + j], lane, iv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float G = d[v] + e[v];
-                e[v] = a[j][v] * G;
-                gx[v] = ig ? iv[v] * G : G;
-                gi[v] *= G;
-                gg[v] = before[j][v] * e[v];
-            }
-        };
-        if (plain) {
+        // the states before each token (in place of u), then the gradients of each token from that of the next state
+        auto finish = [&](auto bounded) {
+            constexpr bool bnd = decltype(bounded)::value;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                float u[V];
-                u_of(j, u);
+                if constexpr (bnd)
+                    if (starts >> j & 1) seq_row(in.h0, bounds.seq(j), hin);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    before[j][v] = hin[v];
-                    hin[v] = fmaf(a[j][v], hin[v], u[v]);
+                    const float h = fmaf(a[j][v], hin[v], u[j][v]);
+                    u[j][v] = hin[v];
+                    hin[v] = h;
                 }
             }
 #pragma unroll
             for (int j = W - 1; j >= 0; --j) {
-                float gx[V], gi[V], gg[V];
-                grads(j, gx, gi, gg);
-                put_all<V, WIDE>(px, lane, gx);
-                put_all<V, WIDE>(pg, lane, gg);
-                px -= out.lddx;
-                pg -= out.lddg;
-                if (di) {
-                    put_all<V, WIDE>(pi, lane, gi);
-                    pi -= out.lddi;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                float u[V];
-                u_of(j, u);
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j);
-                if (starts >> j & 1) seq_row(in.h0, n, hin);
+                float G[V], gx[V], gi[V], gg[V];
+                get<V, WIDE>(sm.dh[r0 + j], lane, G);
+                get<V, WIDE>(sm.x[r0 + j], lane, gi);
+                if constexpr (bnd)
+                    if (ends >> j & 1) seq_row(dfinal, bounds.seq(j + 1) - 1, e);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    before[j][v] = hin[v];
-                    hin[v] = fmaf(a[j][v], hin[v], u[v]);
+                    G[v] += e[v];
+                    e[v] = a[j][v] * G[v];
+                    gi[v] *= G[v];
+                    gg[v] = u[j][v] * e[v];
+                    gx[v] = G[v];
                 }
-            }
+                if (ig) {
+                    get<V, WIDE>(sm.i[r0 + j], lane, gx);
 #pragma unroll
-            for (int j = W - 1; j >= 0; --j) {
-                float gx[V], gi[V], gg[V];
-                const int64_t n = __shfl_sync(0xffffffffu, sv, j + 1) - 1;
-                if (ends >> j & 1) seq_row(dfinal, n, e);
-                grads(j, gx, gi, gg);
-                if (j < rows) {
-                    put<V, WIDE>(px, lane, gx, left, pair);
-                    if (di) put<V, WIDE>(pi, lane, gi, left, pair);
-                    put<V, WIDE>(pg, lane, gg, left, pair);
+                    for (int v = 0; v < V; ++v) gx[v] *= G[v];
+                }
+                if constexpr (bnd) {
+                    if (j < rows) {
+                        put<V, WIDE>(px, lane, gx, left, pair);
+                        if (di) put<V, WIDE>(pi, lane, gi, left, pair);
+                        put<V, WIDE>(pg, lane, gg, left, pair);
+                    }
+                    if ((starts >> j & 1) && out.dh0) put<V, WIDE>(out.dh0 + bounds.seq(j) * D + t.col0, lane, e, left, false);
+                } else {
+                    put_all<V, WIDE>(px, lane, gx);
+                    if (di) put_all<V, WIDE>(pi, lane, gi);
+                    put_all<V, WIDE>(pg, lane, gg);
                 }
                 px -= out.lddx;
                 pi -= out.lddi;
                 pg -= out.lddg;
-                const int64_t m = __shfl_sync(0xffffffffu, sv, j);
-                if ((starts >> j & 1) && out.dh0) put<V, WIDE>(out.dh0 + m * D + t.col0, lane, e, left, false);
             }
-        }
+        };
+        if (plain) finish(std::false_type{});
+        else finish(std::true_type{});
         __syncthreads();
-        release();
         return true;
     };
     walk<C, CHAIN, true>(sm.s, ch, pv, D, load, work);
@@ -924,11 +1001,14 @@ cudaError_t run(K cluster, K chain, int C, int smem, const int32_t *plan_host, c
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     } else {
         ch = chain_of(ws, T, D);
+        // A short group folds fewer maps a tile (measured at 64 channel ranges: 115.0 us with 8, 117.0 us with 16); a
+        // long one passes the state on less often, which is what bounds narrow inputs.
+        ch.group = nC >= 32 ? MIN_GROUP : MAX_GROUP;
         const Layout l = layout_of(T, D);
         const size_t words = (l.end - l.state) / 16;
         const size_t want = (words + 4 * 256 - 1) / (4 * 256), most = 4 * static_cast<size_t>(sm_count());
         chain_init<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
-            plan_dev, sig, nT, ch.ticket, const_cast<int *>(ch.first), reinterpret_cast<uint4 *>(ch.state), words);
+            plan_dev, sig, nT, ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
         if (cudaError_t e = cudaGetLastError()) return e;
         const int64_t tiles = static_cast<int64_t>(nT) * nC, grid = 2 * static_cast<int64_t>(sm_count());
         cfg.gridDim = dim3(static_cast<unsigned>(tiles < grid ? tiles : grid));

@@ -562,7 +562,8 @@ enum { KDA_GATE_NONE = 0, KDA_GATE_SIGMOID = 1, KDA_GATE_SILU = 2 };
  * rms(v) = sqrt(mean(v^2) + eps).  Parts of it stand alone: o NULL is the first block's norm alone
  * (y from r); r and w_pre NULL a gated norm of the block's output into r_out; w_pre NULL the last
  * block's residual.
- *   T, D            rows and channels (D <= 16384, else KDA_ERR_UNSUPPORTED).
+ *   T, D            rows and channels (D <= 16384, T and the bytes between rows < 2^31, else
+ *                   KDA_ERR_UNSUPPORTED).
  *   res_type, type  types of r, r_out and of o, z, y: equal, or res_type KDA_TYPE_F32 (others:
  *                   KDA_ERR_UNSUPPORTED).
  *   group           channels normed together after the block: 0 or D for the whole row, or a head's 32, 64,
