@@ -5,14 +5,17 @@ Loaded by file path from __graft_entry__.build(), so it imports nothing from the
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+OPS = os.path.join(PKG, "_ops.so")     # the marshalling module of binding.py (csrc/torch_ops.cpp)
 ROOT = os.path.dirname(PKG)
 
 CUDA_SOURCES = ["api.cu", "chunk_prep.cu", "chunk_state.cu", "compose.cu", "boundary.cu", "noalloc.cu", "backward.cu", "reverse.cu",
@@ -38,7 +41,7 @@ def _newest_input() -> float:
 
 def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
     """Compile csrc/ into context_kda_gb300/libkda.so unless it is up to date."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (LIB, OPS)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -51,6 +54,14 @@ def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
     for src in CXX_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", *inc, "-c", os.path.join(CSRC, src), "-o", obj])
+
+    # torch's headers, found without importing it; its libraries are already loaded when the module is
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    ops_obj = os.path.join(BUILD, "torch_ops.cpp.o")
+    jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", os.path.join(torch, "include"), "-I",
+                 os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
+                 sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", ops_obj])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -66,4 +77,8 @@ def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    tmp = OPS + f".tmp{os.getpid()}"
+    run(["g++", "-shared", "-o", tmp, ops_obj, "-L", PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
+         "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, OPS)
     return LIB

@@ -283,68 +283,19 @@ def kda_forward_segmented_noalloc(plan, plan_dev, H, q, k, v, g, beta, h0, scale
 TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
 GATES = {"none": 0, "sigmoid": 1, "silu": 2}
 SCAN_TILE = 128
-_TYPES = {}
+_ops = None
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _refuse(fn: str):
-    raise KDAError(fn, KDA_ERR_INVALID_ARG, _lib.kda_status_string(KDA_ERR_INVALID_ARG).decode())
-
-
-def _type(fn: str, t) -> int:
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float32: TYPE_F32})
-    code = _TYPES.get(t.dtype)
-    if code is None:
-        _refuse(fn)
-    return code
-
-
-def _rows(fn: str, t, rows: int, width: int, dtype):
-    """Address and row stride of a [rows, width] tensor of 'dtype' whose channels are adjacent (any
-    trailing axes count as one); (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype or not t.is_cuda or t.shape[0] != rows:
-        _refuse(fn)
-    if t.is_contiguous():
-        if t.numel() != rows * width:
-            _refuse(fn)
-        return t.data_ptr(), width
-    shape, stride = t.shape, t.stride()
-    n = 1
-    for size, step in zip(reversed(shape[1:]), reversed(stride[1:])):
-        if size != 1 and step != n:
-            _refuse(fn)
-        n *= size
-    if n != width:
-        _refuse(fn)
-    return t.data_ptr(), (stride[0] if rows > 1 else width)
-
-
-def _flat(fn: str, t, numel: int, dtype=None):
-    """Address of a contiguous fp32 (or 'dtype') tensor of 'numel' elements; None for None."""
-    if t is None:
-        return None
-    if dtype is None:
-        _type(fn, t)
-        bad = _TYPES[t.dtype] != TYPE_F32
-    else:
-        bad = t.dtype is not dtype
-    if bad or t.numel() != numel or not t.is_contiguous() or not t.is_cuda:
-        _refuse(fn)
-    return t.data_ptr()
-
-
-def _slots(fn: str, slots, B: int):
-    if slots is None:
-        return None
-    import torch
-    return _flat(fn, slots, B, torch.int32)
+def _marshal():
+    """The native module that unpacks these operators' tensors (csrc/torch_ops.cpp), loaded on first use (it needs
+    torch, which the rest of this module does without)."""
+    global _ops
+    if _ops is None:
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        from . import _ops as module
+        module.set_error(KDAError)
+        _ops = module
+    return _ops
 
 
 def kda_gated_scan_workspace_bytes(plan, D: int) -> int:
@@ -354,93 +305,41 @@ def kda_gated_scan_workspace_bytes(plan, D: int) -> int:
 def kda_gated_scan_forward(plan, plan_dev, x, i, g, h0, h, final_state, states, ws, stream=None):
     """The gated linear recurrence of every sequence of the plan (see include/kda.h): x, i, h [T, D] in one
     activation type, g [T, D] fp32; i, h0, final_state, states and ws (where its size is 0) may be None."""
-    fn, p = "kda_gated_scan_forward", _words(plan)
-    T, N, D = int(p[3]), int(p[4]), x.shape[-1]
-    ty = _type(fn, x)
-    _check(fn, _lib.kda_gated_scan_forward(
-        p.ctypes.data, plan_dev.data_ptr(), D, ty, *_rows(fn, x, T, D, x.dtype), *_rows(fn, i, T, D, x.dtype),
-        *_rows(fn, g, T, D, _f32()), _flat(fn, h0, N * D), *_rows(fn, h, T, D, x.dtype), _flat(fn, final_state, N * D),
-        _flat(fn, states, -(-T // SCAN_TILE) * D), _addr(ws), _nbytes(ws), _stream(stream)))
+    (_ops or _marshal()).gated_scan_forward(_words(plan), plan_dev, x, i, g, h0, h, final_state, states, ws, stream)
 
 
 def kda_gated_scan_backward(plan, plan_dev, x, i, g, h0, states, dh, dfinal, dx, di, dg, dh0, ws, stream=None):
     """The gradients of kda_gated_scan_forward (see include/kda.h); i, h0, dfinal, di and dh0 may be None."""
-    fn, p = "kda_gated_scan_backward", _words(plan)
-    T, N, D = int(p[3]), int(p[4]), x.shape[-1]
-    ty, t, f32 = _type(fn, x), x.dtype, _f32()
-    _check(fn, _lib.kda_gated_scan_backward(
-        p.ctypes.data, plan_dev.data_ptr(), D, ty, *_rows(fn, x, T, D, t), *_rows(fn, i, T, D, t), *_rows(fn, g, T, D, f32),
-        _flat(fn, h0, N * D), _flat(fn, states, -(-T // SCAN_TILE) * D), *_rows(fn, dh, T, D, t), _flat(fn, dfinal, N * D),
-        *_rows(fn, dx, T, D, t), *_rows(fn, di, T, D, t), *_rows(fn, dg, T, D, f32), _flat(fn, dh0, N * D), _addr(ws),
-        _nbytes(ws), _stream(stream)))
+    (_ops or _marshal()).gated_scan_backward(_words(plan), plan_dev, x, i, g, h0, states, dh, dfinal, dx, di, dg, dh0, ws, stream)
 
 
 def kda_gated_scan_step(slots, x, i, g, state, h, stream=None):
     """One token of the recurrence for each row of x [B, D], the states [num_slots, D] updated in place
     (see include/kda.h); slots (int32 [B], negative: padding) and i may be None."""
-    fn, (B, D) = "kda_gated_scan_step", x.shape
-    t, n = x.dtype, state.shape[0]
-    _check(fn, _lib.kda_gated_scan_step(
-        B, D, _type(fn, x), _slots(fn, slots, B), n, *_rows(fn, x, B, D, t), *_rows(fn, i, B, D, t),
-        *_rows(fn, g, B, D, _f32()), _flat(fn, state, n * D), *_rows(fn, h, B, D, t), _stream(stream)))
+    (_ops or _marshal()).gated_scan_step(slots, x, i, g, state, h, stream)
 
 
 def kda_block_norm_workspace_bytes(D: int) -> int:
     return int(_lib.kda_block_norm_workspace_bytes(int(D)))
 
 
-def _gate_code(fn, gate):
-    return GATES[gate] if gate in GATES else _refuse(fn)
-
-
 def kda_block_norm_forward(r, o, z, gate, group, w_post, scale, ls, w_pre, eps, r_out, y, stream=None):
     """The norms after and before a block with its gate and the residual (see include/kda.h): r, r_out [T, D]
     in the residual's type, o, z, y [T, D] in the activations' type, gate "none", "sigmoid" or "silu",
     weights fp32; absent parts are None."""
-    fn = "kda_block_norm_forward"
-    a = r if r is not None else r_out if r_out is not None else o
-    b = o if o is not None else y if y is not None else a
-    if a is None:
-        _refuse(fn)
-    T, D, rt, t = a.shape[0], a.numel() // max(1, a.shape[0]) if a.shape[0] else a.shape[-1], a.dtype, b.dtype
-    G = group or D
-    _check(fn, _lib.kda_block_norm_forward(
-        T, D, _type(fn, a), _type(fn, b), *_rows(fn, r, T, D, rt), *_rows(fn, o, T, D, t), *_rows(fn, z, T, D, t),
-        _gate_code(fn, gate), int(group), _flat(fn, w_post, G), float(scale), _flat(fn, ls, D), _flat(fn, w_pre, D),
-        float(eps), *_rows(fn, r_out, T, D, rt), *_rows(fn, y, T, D, t), _stream(stream)))
+    (_ops or _marshal()).block_norm_forward(r, o, z, GATES.get(gate, -1), group, w_post, scale, ls, w_pre, eps, r_out, y, stream)
 
 
 def kda_block_norm_backward(r_out, o, z, gate, group, w_post, scale, ls, w_pre, eps, dr_out, dy, dr, do, dz, dw_post, dls,
                             dw_pre, ws, stream=None):
     """The gradients of kda_block_norm_forward from those of r_out and y (see include/kda.h); absent parts and
     gradients that are not wanted are None."""
-    fn = "kda_block_norm_backward"
-    a = next((v for v in (dr_out, dr, r_out, dy, o) if v is not None), None)
-    b = next((v for v in (o, dy, do, a) if v is not None), None)
-    if a is None:
-        _refuse(fn)
-    T, D, rt, t = a.shape[0], a.numel() // max(1, a.shape[0]) if a.shape[0] else a.shape[-1], a.dtype, b.dtype
-    G = group or D
-    _check(fn, _lib.kda_block_norm_backward(
-        T, D, _type(fn, a), _type(fn, b), *_rows(fn, r_out, T, D, rt), *_rows(fn, o, T, D, t), *_rows(fn, z, T, D, t),
-        _gate_code(fn, gate), int(group), _flat(fn, w_post, G), float(scale), _flat(fn, ls, D), _flat(fn, w_pre, D),
-        float(eps), *_rows(fn, dr_out, T, D, rt), *_rows(fn, dy, T, D, t), *_rows(fn, dr, T, D, rt),
-        *_rows(fn, do, T, D, t), *_rows(fn, dz, T, D, t), _flat(fn, dw_post, G), _flat(fn, dls, D), _flat(fn, dw_pre, D),
-        _addr(ws), _nbytes(ws), _stream(stream)))
+    (_ops or _marshal()).block_norm_backward(r_out, o, z, GATES.get(gate, -1), group, w_post, scale, ls, w_pre, eps, dr_out, dy, dr,
+                                             do, dz, dw_post, dls, dw_pre, ws, stream)
 
 
 def kda_decode_step(slots, q, k, v, g, beta, scale, state, o, stream=None):
     """One KDA token for each of B slots (see include/kda.h): q, k, v, o [B, H, 128] in one activation type,
     g [B, H, 128] and beta [B, H] fp32, state [num_slots, H, 128, 128] fp32 updated in place; slots (int32
     [B], negative: padding) may be None."""
-    fn, (B, H, K) = "kda_decode_step", q.shape
-    t, n, W, f32 = q.dtype, state.shape[0], H * HEAD_DIM_K, _f32()
-    _check(fn, _lib.kda_decode_step(
-        B, H, _type(fn, q), _slots(fn, slots, B), n, *_rows(fn, q, B, W, t), *_rows(fn, k, B, W, t), *_rows(fn, v, B, W, t),
-        *_rows(fn, g, B, W, f32), *_rows(fn, beta, B, H, f32), float(scale), _flat(fn, state, n * W * HEAD_DIM_V),
-        *_rows(fn, o, B, W, t), _stream(stream)))
-
-
-def _f32():
-    import torch
-    return torch.float32
+    (_ops or _marshal()).decode_step(slots, q, k, v, g, beta, scale, state, o, stream)
