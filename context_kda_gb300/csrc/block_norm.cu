@@ -55,6 +55,8 @@ cudaError_t launch_norm_forward(int64_t T, int D, int rtype, int type, const Nor
     s.T = static_cast<uint32_t>(T);
     s.D = D;
     s.G = a.group ? a.group : D;
+    s.inv_d = 1.f / D;
+    s.inv_g = 1.f / s.G;
     if (type == KDA_TYPE_F32) return norm::forward_f32(rtype, s, a, r_out, ldro, y, ldy, stream);
     if (type == KDA_TYPE_F16) return norm::forward_f16(rtype, s, a, r_out, ldro, y, ldy, stream);
     return norm::forward_bf16(rtype, s, a, r_out, ldro, y, ldy, stream);
@@ -67,6 +69,8 @@ cudaError_t launch_norm_backward(int64_t T, int D, int rtype, int type, const No
     s.T = static_cast<uint32_t>(T);
     s.D = D;
     s.G = a.group ? a.group : D;
+    s.inv_d = 1.f / D;
+    s.inv_g = 1.f / s.G;
     float *part = static_cast<float *>(ws);
     int grid = 0;
     if (T > 0) {

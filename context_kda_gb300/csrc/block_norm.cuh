@@ -16,6 +16,9 @@
 // (none when a row is a warp or less).  U is the run of adjacent channels that a thread copies: 8 where rows
 // start on 16 bytes, otherwise 2 (2-byte types whose rows start on pairs) or 1; single 2-byte elements,
 // which no asynchronous copy moves, are read directly.
+// FULL instances are for the usual call: every part but the gate is there, D is a multiple of 8 and all rows start on
+// 16 bytes.  They decide nothing about that per row (a third of the instructions of the others, which bound
+// them: 16384 x 2048 gradients in bf16 115 us without, see below with).
 // Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 #pragma once
@@ -36,6 +39,7 @@ struct Shape {
     uint32_t T;
     int D, G, NT;                // channels, channels of a group, threads of a row
     bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes (or on pairs): residual, the others
+    float inv_d, inv_g;          // 1 / D, 1 / G
 };
 
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -68,6 +72,16 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
                     copy(base + ((q * PIECES + p) * BLOCK + threadIdx.x) * PB, bytes ? row + q * NT * U + p * EPP : row, bytes);
                 }
         }
+    }
+    // The same where the thread's channels all exist.
+    static __device__ __forceinline__ void fetch_all(uint32_t base, const X *row)
+    {
+#pragma unroll
+        for (int p = 0; p < NU * PIECES; ++p) copy_all(base + (p * BLOCK + threadIdx.x) * PB, row + p * EPP);
+    }
+    static __device__ __forceinline__ void copy_all(uint32_t dst, const X *src)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     }
     // Zeros in place of a row past the end ('any': some address of the tensor).
     static __device__ __forceinline__ void fetch_none(uint32_t base, const X *any)
@@ -117,6 +131,15 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
                     v[q * U + j] = in && c < D ? to_f32(row[c]) : 0.f;
                 }
         }
+    }
+    // A thread's eight channels from 'at' on, aligned.
+    static __device__ __forceinline__ void write_all(X *at, const float (&v)[NE])
+    {
+        X e[NE];
+#pragma unroll
+        for (int j = 0; j < NE; ++j) e[j] = from_f32<X>(v[j]);
+#pragma unroll
+        for (int p = 0; p < NE * static_cast<int>(sizeof(X)) / 16; ++p) reinterpret_cast<uint4 *>(at)[p] = reinterpret_cast<const uint4 *>(e)[p];
     }
     static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool wide, const float (&v)[NE])
     {
@@ -274,7 +297,7 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
     static constexpr int SMEM = S * STEP;
 };
 
-template <typename R, typename E, int BLOCK, int NC, int U>
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL>
 __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
 {
     using F = Forward<R, E, BLOCK, NC, U>;
@@ -287,31 +310,44 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
     const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT, rr = threadIdx.x / NT;
-    const float inv_d = 1.f / D, inv_g = 1.f / G;
+    const float inv_d = s.inv_d, inv_g = s.inv_g;
     const uint32_t step = gridDim.x * rows;
     const uint32_t lr = a.ldr * sizeof(R), lo = a.ldo * sizeof(E), lz = a.ldz * sizeof(E);
     const uint32_t base = tc::smem_u32(ring);
+    const bool has_r = FULL || r, has_o = FULL || o, has_post = FULL || a.w_post, has_out = FULL || r_out, has_y = FULL || y;
 
     // channels past D are not read: the row's first address stands in for theirs
-    const int first = ti * U < D ? ti * U : 0;
+    const bool active = ti * U < D;
+    const int first = active ? ti * U : 0;
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * F::STEP;
-        if (t < s.T) {
-            if (r) RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
-            if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, first), ti, NT, D);
-            if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first), ti, NT, D);
+        if (t < s.T && (!FULL || active)) {
+            if constexpr (FULL) {
+                RowR::fetch_all(b, row_at(r, t, lr, first));
+                RowE::fetch_all(b + RowR::BYTES, row_at(o, t, lo, first));
+                if (z) RowE::fetch_all(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first));
+            } else {
+                if (r) RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
+                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, first), ti, NT, D);
+                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first), ti, NT, D);
+            }
         } else {
-            if (r) RowR::fetch_none(b, r);
-            if (o) RowE::fetch_none(b + RowR::BYTES, o);
+            if (has_r) RowR::fetch_none(b, r);
+            if (has_o) RowE::fetch_none(b + RowR::BYTES, o);
             if (z) RowE::fetch_none(b + RowR::BYTES + RowE::BYTES, z);
         }
     };
+    uint32_t t0 = blockIdx.x * rows;
+    for (int k = 0; k < S - 1; ++k) {
+        fetch(k, t0 + rr + k * step);
+        cp_commit();
+    }
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
     float wl[NE], wr[NE];      // scale * ls * w_post, w_pre
     auto branch_weights = [&] {
         weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
-        if (a.w_post) {
+        if (has_post) {
             float wg[NE];
             weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
 #pragma unroll
@@ -320,12 +356,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     };
     if constexpr (NC == 1) {
         branch_weights();
-        if (y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
-    }
-    uint32_t t0 = blockIdx.x * rows;
-    for (int k = 0; k < S - 1; ++k) {
-        fetch(k, t0 + rr + k * step);
-        cp_commit();
+        if (has_y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -338,18 +369,18 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
         }
         const unsigned char *b = ring + slot * F::STEP;
         float v[NE];
-        if (r) {
+        if (has_r) {
             RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
         }
-        if (o) {
+        if (has_o) {
             float n[NE];
             RowE::template read<(S > 0)>(b + RowR::BYTES, row_at(o, t, lo, 0), ti, NT, D, in, n);
             float g[NE];
             if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), ti, NT, D, in, g);
-            if (a.w_post) {
+            if (has_post) {
                 float ss[NU];
 #pragma unroll
                 for (int q = 0; q < NU; ++q) {
@@ -385,8 +416,12 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = fmaf(wl[j], n[j], v[j]);
         }
-        if (r_out && in) RowR::write(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
-        if (y) {
+        if constexpr (FULL) {
+            if (in && active) RowR::write_all(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), first), v);
+        } else {
+            if (r_out && in) RowR::write(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
+        }
+        if (has_y) {
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < NE; ++j) ss += v[j] * v[j];
@@ -394,7 +429,11 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
-            if (in) RowE::write(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
+            if constexpr (FULL) {
+                if (in && active) RowE::write_all(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), first), v);
+            } else {
+                if (in) RowE::write(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
+            }
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -416,9 +455,9 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
 };
 
 // part: [grid][G + 2 D], the CTA's sums for w_post, ls and w_pre.
-template <typename R, typename E, int BLOCK, int NC, int U>
-__global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) backward(Shape s, NormIn a, const R *dro, int64_t lddro, const E *dy, int64_t lddy,
-                                                     NormGrads g, float *part)
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL>
+__global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) backward(Shape s, NormIn a, const R *dro, int64_t lddro,
+                                                                                      const E *dy, int64_t lddy, NormGrads g, float *part)
 {
     using B = Backward<R, E, BLOCK, NC, U>;
     using RowR = typename B::RowR;
@@ -432,34 +471,49 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     R *dr = static_cast<R *>(g.dr);
     E *d_o = static_cast<E *>(g.d_o), *dz = static_cast<E *>(g.dz);
     const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT, rr = threadIdx.x / NT;
-    const float inv_d = 1.f / D, inv_g = 1.f / G;
+    const float inv_d = s.inv_d, inv_g = s.inv_g;
     const uint32_t step = gridDim.x * rows;
     const uint32_t lr = a.ldr * sizeof(R), lo = a.ldo * sizeof(E), lz = a.ldz * sizeof(E);
     const uint32_t ldr = lddro * sizeof(R), ldy = lddy * sizeof(E);
     const uint32_t base = tc::smem_u32(ring);
     constexpr int O_DRO = RowR::BYTES, O_DY = 2 * RowR::BYTES, O_O = O_DY + RowE::BYTES, O_Z = O_O + RowE::BYTES;
+    const bool has_pre = FULL || a.w_pre, has_dro = FULL || dro, has_o = FULL || o, has_post = FULL || a.w_post;
 
-    const int first = ti * U < D ? ti * U : 0;
+    const bool active = ti * U < D;
+    const int first = active ? ti * U : 0;
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * B::STEP;
-        if (t < s.T) {
-            if (a.w_pre) {
-                RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
-                RowE::fetch(b + O_DY, row_at(dy, t, ldy, first), ti, NT, D);
+        if (t < s.T && (!FULL || active)) {
+            if constexpr (FULL) {
+                RowR::fetch_all(b, row_at(r, t, lr, first));
+                RowE::fetch_all(b + O_DY, row_at(dy, t, ldy, first));
+                RowR::fetch_all(b + O_DRO, row_at(dro, t, ldr, first));
+                RowE::fetch_all(b + O_O, row_at(o, t, lo, first));
+                if (z) RowE::fetch_all(b + O_Z, row_at(z, t, lz, first));
+            } else {
+                if (a.w_pre) {
+                    RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
+                    RowE::fetch(b + O_DY, row_at(dy, t, ldy, first), ti, NT, D);
+                }
+                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, first), ti, NT, D);
+                if (o) RowE::fetch(b + O_O, row_at(o, t, lo, first), ti, NT, D);
+                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, first), ti, NT, D);
             }
-            if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, first), ti, NT, D);
-            if (o) RowE::fetch(b + O_O, row_at(o, t, lo, first), ti, NT, D);
-            if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, first), ti, NT, D);
         } else {
-            if (a.w_pre) {
+            if (has_pre) {
                 RowR::fetch_none(b, r);
                 RowE::fetch_none(b + O_DY, dy);
             }
-            if (dro) RowR::fetch_none(b + O_DRO, dro);
-            if (o) RowE::fetch_none(b + O_O, o);
+            if (has_dro) RowR::fetch_none(b + O_DRO, dro);
+            if (has_o) RowE::fetch_none(b + O_O, o);
             if (z) RowE::fetch_none(b + O_Z, z);
         }
     };
+    uint32_t t0 = blockIdx.x * rows;
+    for (int k = 0; k < S - 1; ++k) {
+        fetch(k, t0 + rr + k * step);
+        cp_commit();
+    }
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
     float acc_g[NE], acc_l[NE], acc_r[NE];
@@ -470,11 +524,6 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
         weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
         weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
-    }
-    uint32_t t0 = blockIdx.x * rows;
-    for (int k = 0; k < S - 1; ++k) {
-        fetch(k, t0 + rr + k * step);
-        cp_commit();
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -489,7 +538,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         float ov[NE], rv[NE], e[NE];
         float ss = 0.f, ev_r = 0.f;             // sums of r^2 and of e r over the row
         float so[NU];                           // of o^2 over the groups
-        if (a.w_pre) {
+        if (has_pre) {
             RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, rv);
             RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy, 0), ti, NT, D, in, e);
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
@@ -499,9 +548,9 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 ev_r = fmaf(e[j] * wr[j], rv[j], ev_r);
             }
         }
-        if (o) {
+        if (has_o) {
             RowE::template read<(S > 0)>(b + O_O, row_at(o, t, lo, 0), ti, NT, D, in, ov);
-            if (a.w_post) {
+            if (has_post) {
                 float all = 0.f;
 #pragma unroll
                 for (int q = 0; q < NU; ++q) {
@@ -520,16 +569,16 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             }
         }
         float v[NE];                            // the gradient of r', then that of o
-        if (dro) {
+        if (has_dro) {
             RowR::template read<(S > 0)>(b + O_DRO, row_at(dro, t, ldr, 0), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
         }
-        if (a.w_pre) {
+        if (has_pre) {
             sums.over_row(ss, ev_r, NT, turn);
-            const float inv = inv_rms(ss * inv_d, a.eps), mean = ev_r * inv_d * inv;
-            if (D == 1) {
+            const float inv = in ? inv_rms(ss * inv_d, a.eps) : 0.f, mean = ev_r * inv_d * inv;   // no row: zeros, also with eps = 0
+            if (!FULL && D == 1) {
                 v[0] += unit_grad_of_one(e[0] * wr[0], inv, a.eps);
                 acc_r[0] = fmaf(e[0], rv[0] * inv, acc_r[0]);
             } else {
@@ -541,8 +590,11 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 }
             }
         }
-        if (dr && in) RowR::write(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
-        if (o) {
+        if (dr && in && (!FULL || active)) {
+                if constexpr (FULL) RowR::write_all(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), first), v);
+                else RowR::write(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
+            }
+        if (has_o) {
             float gz[NE];
             if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz, 0), ti, NT, D, in, gz);
             if constexpr (NC > 1) {
@@ -552,7 +604,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             float ev[NU], inv[NU];
 #pragma unroll
             for (int q = 0; q < NU; ++q) {
-                inv[q] = a.w_post ? inv_rms(so[q] * inv_g, a.eps) : 1.f;
+                inv[q] = !has_post ? 1.f : in ? inv_rms(so[q] * inv_g, a.eps) : 0.f;
                 ev[q] = 0.f;
             }
             // channel j with the gate's value and derivative times v: v becomes the gradient of hat, ov becomes hat
@@ -581,8 +633,11 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 #pragma unroll
                 for (int j = 0; j < NE; ++j) channel(j, v[j], 0.f);
             }
-            if (dz && in) RowE::write(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), 0), ti, NT, D, s.wide_b, gz);
-            if (a.w_post) {
+            if (dz && in && (!FULL || active)) {
+                if constexpr (FULL) RowE::write_all(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), first), gz);
+                else RowE::write(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), 0), ti, NT, D, s.wide_b, gz);
+            }
+            if (has_post) {
                 if (G == D) {
                     float all = 0.f;
 #pragma unroll
@@ -593,14 +648,17 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 } else {
                     groups.over_group(ev, G, turn + 1);
                 }
-                if (G == 1) {
+                if (!FULL && G == 1) {
                     v[0] = unit_grad_of_one(v[0], inv[0], a.eps);
                 } else {
 #pragma unroll
                     for (int j = 0; j < NE; ++j) v[j] = inv[j / U] * fmaf(-ov[j], ev[j / U] * inv_g, v[j]);
                 }
             }
-            if (in) RowE::write(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
+            if (in && (!FULL || active)) {
+                if constexpr (FULL) RowE::write_all(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), first), v);
+                else RowE::write(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
+            }
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -660,12 +718,12 @@ inline int threads_of_row(int D, int G, int nc, int U)
     return nt;
 }
 
-template <typename R, typename E, int BLOCK, int NC, int U>
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false>
 cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
 {
     using F = Forward<R, E, BLOCK, NC, U>;
     s.NT = threads_of_row(s.D, s.G, NC, U);
-    auto fn = forward<R, E, BLOCK, NC, U>;
+    auto fn = forward<R, E, BLOCK, NC, U, FULL>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), F::SMEM)) return e;
     const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = F::CTAS * sm_count();
     fn<<<static_cast<unsigned>(want < most ? want : most), BLOCK, F::SMEM, stream>>>(s, a, static_cast<R *>(r_out), ldro,
@@ -673,13 +731,13 @@ cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, voi
     return cudaGetLastError();
 }
 
-template <typename R, typename E, int BLOCK, int NC, int U>
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false>
 cudaError_t run_backward(Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy, const NormGrads &g,
                          float *part, int *grid, cudaStream_t stream)
 {
     using B = Backward<R, E, BLOCK, NC, U>;
     s.NT = threads_of_row(s.D, s.G, NC, U);
-    auto fn = backward<R, E, BLOCK, NC, U>;
+    auto fn = backward<R, E, BLOCK, NC, U, FULL>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), B::SMEM)) return e;
     const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, full = B::CTAS * sm_count(), most = full < MAX_GRID ? full : MAX_GRID;
     *grid = static_cast<int>(want < most ? want : most);
@@ -702,6 +760,9 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
     if (rows_on(a.r, a.ldr, re, 16) && rows_on(a.o, a.ldo, e, 16) && rows_on(a.z, a.ldz, e, 16)) {
         s.wide_r = rows_on(r_out, ldro, re, 16);
         s.wide_a = rows_on(y, ldy, e, 16);
+        if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 4096)
+            return s.D <= 2048 ? run_forward<R, E, 256, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream)
+                               : run_forward<R, E, 512, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream);
         return KDA_NORM_PICK(run_forward, R, E, 8, s, a, r_out, ldro, y, ldy, stream);
     }
     if constexpr (e == 2) {
@@ -727,6 +788,9 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
         s.wide_r = rows_on(g.dr, g.lddr, re, 16);
         s.wide_a = rows_on(g.d_o, g.lddo, e, 16);
         s.wide_b = rows_on(g.dz, g.lddz, e, 16);
+        if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 4096)
+            return s.D <= 2048 ? run_backward<R, E, 256, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                               : run_backward<R, E, 512, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return KDA_NORM_PICK(run_backward, R, E, 8, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
     if constexpr (e == 2) {

@@ -226,3 +226,23 @@ def test_another_stream():
     args = (w["o"], w["z"], "sigmoid", 128, w["w_post"], 0.7, w["ls"], w["w_pre"], EPS)
     check(y, ref.norm_forward(w["r"], *args)[1], "bf16", "y")
     check(got[1], ref.norm_backward(r_out.double().cpu().numpy(), *args, w["dr_out"], w["dy"])[1], "bf16", "do")
+
+
+def test_no_eps():
+    """eps = 0, with fewer rows than the CTAs take at once: rows that are not there leave nothing in the weights' gradients."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    for T, D, group in ((5, 128, 32), (3, 96, 0), (7, 33, 0)):
+        d, w = _draw(T, D, "bf16", "bf16", group=group)
+        r_out, y = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kda.kda_block_norm_forward(d["r"], d["o"], d["z"], "sigmoid", group, d["w_post"], 0.7, d["ls"], d["w_pre"], 0.0, r_out, y)
+        args = (w["o"], w["z"], "sigmoid", group, w["w_post"], 0.7, w["ls"], w["w_pre"], 0.0)
+        check(y, ref.norm_forward(w["r"], *args)[1], "bf16", "y")
+        dr, do, dz = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+        dw = [torch.empty(n, device="cuda") for n in (group or D, D, D)]
+        ws = torch.empty(kda.kda_block_norm_workspace_bytes(D), dtype=torch.uint8, device="cuda")
+        kda.kda_block_norm_backward(r_out, d["o"], d["z"], "sigmoid", group, d["w_post"], 0.7, d["ls"], d["w_pre"], 0.0, d["dr_out"],
+                                    d["dy"], dr, do, dz, *dw, ws)
+        want = ref.norm_backward(r_out.double().cpu().numpy(), *args, w["dr_out"], w["dy"])
+        for a, b, k in zip((dr, do, dz, *dw), want, ("bf16",) * 3 + ("f32",) * 3):
+            check(a, b, k)
