@@ -46,7 +46,8 @@ constexpr int C = 32;                        // channels of a tile
 constexpr int RUN = 16, RUNS = L / RUN;      // tokens of a run, runs of a tile
 constexpr int V = 2;                         // channels of a lane
 constexpr int WARPS = RUNS / 2, THREADS = WARPS * 32;
-constexpr int CTAS = 4;                      // of an SM
+// CTAs of an SM: four, or as many as their shared memory allows.
+template <typename Sh> constexpr int ctas_of() { return 233472 / (static_cast<int>(sizeof(Sh)) + 1024) < 4 ? 233472 / (static_cast<int>(sizeof(Sh)) + 1024) : 4; }
 constexpr int GROUP = 16, SHORT_GROUP = 8;   // tiles of a group: see run()
 constexpr int MAX_CLUSTER = 8;               // tiles that a cluster covers
 constexpr long long SPIN = 4000000000LL;     // clocks of a wait: about two seconds
@@ -93,14 +94,14 @@ inline Chain chain_of(void *ws, int64_t T, int D)
                  reinterpret_cast<uint64_t *>(b + l.map), padded(D), GROUP};
 }
 
-__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int *ticket, Starts *starts, uint4 *words,
-                                                  size_t n)
+__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int grid, int *ticket, Starts *starts,
+                                                  uint4 *words, size_t n)
 {
     tc::grid_dep_launch();
     const size_t id = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x, step = static_cast<size_t>(gridDim.x) * blockDim.x;
     if (!plan_matches(plan, sig)) return;   // the main kernel records it
     for (size_t j = id; j < n; j += step) words[j] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    if (id == 0) *ticket = 0;
+    if (id == 0) *ticket = grid;
     const PlanView pv{plan};
     const int32_t *cu = pv.cu();
     const int lane = threadIdx.x & 31, N = pv.N();
@@ -134,12 +135,32 @@ __global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig s
 
 // ---- a tile in shared memory ----------------------------------------------------------------------------
 
-// Rows of one tensor, run by run; rows of 2-byte elements are 64 bytes, and every other run is moved by as much, so
-// that the two runs a warp reads at once lie in different banks.
-template <typename X> constexpr int run_bytes() { return RUN * C * static_cast<int>(sizeof(X)) + (sizeof(X) == 2 ? 64 : 0); }
-template <typename X> struct __align__(16) Rows {
-    unsigned char b[RUNS * run_bytes<X>()];
-    __device__ __forceinline__ X *row(int run, int j) { return reinterpret_cast<X *>(b + run * run_bytes<X>()) + j * C; }
+// Rows of one tensor, run by run.  SH: rows that do not all start on 16 bytes are copied with the 16 bytes they start in,
+// so a row takes one copy more and its channels start at an offset.  Runs are moved against each other where a
+// warp, which reads two runs at once, would find both in the same banks.
+template <typename X, bool SH> struct __align__(16) Rows {
+    static constexpr int EPC = 16 / static_cast<int>(sizeof(X));            // elements of a copy
+    static constexpr int PITCH = (C + (SH ? EPC : 0)) * static_cast<int>(sizeof(X));
+    static constexpr int RUN_BYTES = RUN * PITCH + (SH || sizeof(X) == 2 ? 64 : 0);
+    unsigned char b[RUNS * RUN_BYTES];
+    __device__ __forceinline__ X *row(int run, int j) { return reinterpret_cast<X *>(b + run * RUN_BYTES + j * PITCH); }
+};
+// The row of a run's j-th token in shared memory, from its first channel on.
+template <typename X, bool SH> struct Run {
+    Rows<X, SH> &rows;
+    int run;
+    uint32_t first, ld;        // element the run's first row starts at, and between rows (modulo a copy)
+    __device__ __forceinline__ Run(Rows<X, SH> &r, int n, const X *src, int64_t stride, int t0) : rows(r), run(n), first(0), ld(0)
+    {
+        if constexpr (SH) {
+            first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) / sizeof(X)) + static_cast<uint32_t>(t0 + n * RUN) * static_cast<uint32_t>(stride);
+            ld = static_cast<uint32_t>(stride);
+        }
+    }
+    __device__ __forceinline__ const X *operator()(int j) const
+    {
+        return rows.row(run, j) + (SH ? (first + j * ld) & (Rows<X, SH>::EPC - 1) : 0u);
+    }
 };
 // What the runs and tiles of a channel range pass on.
 struct Shared {
@@ -152,61 +173,72 @@ struct Shared {
 };
 
 // ---- copies ---------------------------------------------------------------------------------------------
-// G: bytes of a copy: 16 where every row starts on 16 bytes, 4 where rows start on 4, 2 for 2-byte elements on
-// odd addresses (through registers).
 
-template <int G> __device__ __forceinline__ void copy(uint32_t dst, const void *src, int bytes)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
 {
-    if constexpr (G == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // Tokens t0.. (zeros from T on), channels c0.. (zeros from D on) of a tensor of rows.
-template <typename X, int G> __device__ __forceinline__ void fill(Rows<X> &dst, const X *src, int64_t ld, int t0, int T, int c0, int D)
+template <typename X, bool SH>
+__device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld, int t0, int T, int c0, int D)
 {
-    constexpr int PER = (G < static_cast<int>(sizeof(X)) ? static_cast<int>(sizeof(X)) : G) / static_cast<int>(sizeof(X));   // elements of a copy
-    constexpr int CPR = C / PER, STEP = THREADS / CPR;      // copies of a row, rows of a step
-    const int row = threadIdx.x / CPR, c = threadIdx.x % CPR * PER;
-    const X *p = src + (static_cast<int64_t>(t0) + row) * ld + c0 + c;
-    const int64_t hop = STEP * ld;
-    const int left = (D - c0 - c) * static_cast<int>(sizeof(X));
-    constexpr int BYTES = PER * static_cast<int>(sizeof(X));
-    const int bytes = left < 0 ? 0 : left > BYTES ? BYTES : left;
-    const int rows = bytes ? T - t0 - row : 0;               // of this thread, from its first on
-    // the k-th row's place is a constant from the first's: steps never leave the first row's place within its run
-    static_assert(STEP % RUN == 0 || RUN % STEP == 0, "whole runs a step or whole steps a run");
-    X *const to = dst.row(row / RUN, row % RUN) + c;
-    constexpr int ROW = C * static_cast<int>(sizeof(X));
-    auto place = [](int k) { return k * STEP / RUN * run_bytes<X>() + k * STEP % RUN * ROW; };
-    if constexpr (BYTES >= 4) {
+    using R = Rows<X, SH>;
+    if constexpr (!SH) {
+        constexpr int CPR = C / R::EPC, STEP = THREADS / CPR;      // copies of a row, rows of a step
+        const int row = threadIdx.x / CPR, c = threadIdx.x % CPR * R::EPC;
+        const X *p = src + (static_cast<int64_t>(t0) + row) * ld + c0 + c;
+        const int64_t hop = STEP * ld;
+        const int left = (D - c0 - c) * static_cast<int>(sizeof(X));
+        const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+        const int rows = bytes ? T - t0 - row : 0;                 // of this thread, from its first on
+        // the k-th row's place is a constant from the first's: steps never leave the first row's place within its run
+        static_assert(STEP % RUN == 0 || RUN % STEP == 0, "whole runs a step or whole steps a run");
+        const uint32_t to = smem_u32(dst.row(row / RUN, row % RUN) + c);
+        auto place = [](int k) { return k * STEP / RUN * R::RUN_BYTES + k * STEP % RUN * R::PITCH; };
         if (rows >= L) {
 #pragma unroll
             for (int k = 0; k < L / STEP; ++k) {
-                copy<BYTES>(smem_u32(to) + place(k), p, bytes);
+                copy16(to + place(k), p, bytes);
                 p += hop;
             }
         } else {
 #pragma unroll 4
             for (int k = 0; k < L / STEP; ++k) {
                 const bool in = k * STEP < rows;
-                copy<BYTES>(smem_u32(to) + place(k), in ? p : src, in ? bytes : 0);
+                copy16(to + place(k), in ? p : src, in ? bytes : 0);
                 p += hop;
             }
         }
     } else {
+        // copy k of a thread: copy ch of row 'row'; THREADS copies are DR rows and DC copies on
+        constexpr int CPR = C / R::EPC + 1, DR = THREADS / CPR, DC = THREADS % CPR;
+        static_assert(THREADS == L, "as many copies a thread as a row takes");
+        int row = threadIdx.x / CPR, ch = threadIdx.x % CPR;
+        const int width = (D - c0 < C ? D - c0 : C) * static_cast<int>(sizeof(X));
+        const char *base = reinterpret_cast<const char *>(src), *p = reinterpret_cast<const char *>(src + (static_cast<int64_t>(t0) + row) * ld + c0);
+        const int64_t pitch = ld * static_cast<int64_t>(sizeof(X));
 #pragma unroll
-        for (int k0 = 0; k0 < L / STEP; k0 += 16) {
-            X v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[k] = (k0 + k) * STEP < rows ? *p : from_f32<X>(0.f);
-                p += hop;
+        for (int k = 0; k < CPR; ++k) {
+            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+            const int left = t0 + row < T ? off + width - ch * 16 : 0;
+            const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+            const char *from = p - off + ch * 16;
+            X *to = dst.row(row / RUN, row % RUN) + ch * R::EPC;
+            if (bytes && from < base) {        // the tensor starts within this copy: nothing before it is read
+                const int skip = static_cast<int>(base - from) / static_cast<int>(sizeof(X));
+                for (int e = 0; e < R::EPC; ++e)
+                    to[e] = e >= skip && e * static_cast<int>(sizeof(X)) < bytes ? reinterpret_cast<const X *>(from)[e] : from_f32<X>(0.f);
+            } else {
+                copy16(smem_u32(to), bytes ? from : base - (reinterpret_cast<uintptr_t>(base) & 15u), bytes);
             }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                *reinterpret_cast<X *>(reinterpret_cast<unsigned char *>(to) + place(k0 + k)) = v[k];
+            row += DR;
+            ch += DC;
+            p += DR * pitch;
+            if (ch >= CPR) {
+                ch -= CPR;
+                ++row;
+                p += pitch;
             }
         }
     }
@@ -522,16 +554,13 @@ __device__ __forceinline__ void walk(Shared &sh, const Chain &ch, const PlanView
         }
         cluster_wait();
     } else {
-        // Tickets are drawn ahead (k: in work, k2: next, then the one drawn while k is in work), so that neither the
-        // draw nor a tile's starts are waited for; the second only once the first tile's copies are on their way, when
-        // all CTAs have drawn their first.  A CTA works its tiles in the order drawn, so the lowest unfinished tile is
-        // always in work with nothing to wait for.
+        // A CTA's first tile goes by its index: its copies start before the kernel that sets the workspace is waited
+        // for (blocks are dispatched in the order of their indexes, and a wait that this failed would end by its
+        // limit).  The others go by tickets, drawn ahead (k: in work, k2: next, then the one drawn while k is in work), so that neither
+        // the draw nor a tile's starts are waited for.  A CTA works its tiles in the order drawn, so the lowest
+        // unfinished tile is always in work with nothing to wait for.
         const int n = nT * nC;
-        grid_dep_wait();
-        int drawn = 0;
-        if (threadIdx.x == 0) sh.next = atomicAdd(ch.ticket, 1);
-        __syncthreads();
-        int k = sh.next;
+        int drawn = 0, k = blockIdx.x;
         uint4 bits = {};
         uint32_t after = 0;
         int first = 0;
@@ -544,6 +573,7 @@ __device__ __forceinline__ void walk(Shared &sh, const Chain &ch, const PlanView
             const Tile t = tile_of<REVERSE>(k, nT, nC);
             load(t, 0);
             load(t, 1);
+            grid_dep_wait();
             words(t);
             if (threadIdx.x == 0) drawn = atomicAdd(ch.ticket, 1);
         }
@@ -576,20 +606,18 @@ __device__ __forceinline__ void walk(Shared &sh, const Chain &ch, const PlanView
 
 // ---- forward --------------------------------------------------------------------------------------------
 
-template <typename E> struct __align__(16) ForwardShared {
-    Rows<float> g;
-    Rows<E> x, i;
+template <typename E, bool SH> struct __align__(16) ForwardShared {
+    Rows<float, SH> g;
+    Rows<E, SH> x, i;
     Shared s;
 };
 
-template <typename E, int G, bool CHAIN>
-__global__ void __launch_bounds__(THREADS, CTAS) scan_forward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch, void *h_,
+template <typename E, bool SH, bool ADJ, bool CHAIN>
+__global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan_forward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch, void *h_,
                                                               int64_t ldh, float *final_state, float *states)
 {
-    constexpr bool ADJ = G == 16 || (sizeof(E) == 2 && G == 4);
-    constexpr int G4 = G < 4 ? 4 : G;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<ForwardShared<E> *>(smem_raw);
+    auto &sm = *reinterpret_cast<ForwardShared<E, SH> *>(smem_raw);
     if (!plan_matches(plan, sig)) {
         if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         return;
@@ -602,21 +630,23 @@ __global__ void __launch_bounds__(THREADS, CTAS) scan_forward(const int32_t *pla
 
     auto load = [&](const Tile &t, int part) {
         if (part == 1) return;
-        fill<float, G4>(sm.g, in.g, in.ldg, t.t0, T, t.col0, D);
-        fill<E, G>(sm.x, x, in.ldx, t.t0, T, t.col0, D);
-        if (ig) fill<E, G>(sm.i, ig, in.ldi, t.t0, T, t.col0, D);
+        fill(sm.g, in.g, in.ldg, t.t0, T, t.col0, D);
+        fill(sm.x, x, in.ldx, t.t0, T, t.col0, D);
+        if (ig) fill(sm.i, ig, in.ldi, t.t0, T, t.col0, D);
     };
     auto work = [&](const Tile &t, const Bounds &b, auto release) {
         const int left = D - t.col0, rows = T - t.t0 - run * RUN, place = b.place();
         const int kind = kind_of(b, rows >= RUN && left >= C && pair);
         float h0[V] = {};
         if (kind == ONE) seq_row<ADJ>(in.h0, b.first, D, t.col0, l, b.starts != 0, h0);
+        const Run<float, SH> gr(sm.g, run, in.g, in.ldg, t.t0);
+        const Run<E, SH> xr(sm.x, run, x, in.ldx, t.t0), ir(sm.i, run, ig, in.ldi, t.t0);
         float a[RUN][V], u[RUN][V];
 #pragma unroll
         for (int j = 0; j < RUN; ++j) {
             float gv[V];
-            get<ADJ>(sm.g.row(run, j), l, gv);
-            get<ADJ>(sm.x.row(run, j), l, u[j]);
+            get<ADJ>(gr(j), l, gv);
+            get<ADJ>(xr(j), l, u[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
         }
@@ -624,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) scan_forward(const int32_t *pla
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 float iv[V];
-                get<ADJ>(sm.i.row(run, j), l, iv);
+                get<ADJ>(ir(j), l, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
             }
@@ -700,23 +730,21 @@ __global__ void __launch_bounds__(THREADS, CTAS) scan_forward(const int32_t *pla
 
 // ---- backward -------------------------------------------------------------------------------------------
 
-template <typename E> struct __align__(16) BackwardShared {
-    Rows<float> g;
-    Rows<E> x, i, dh;
+template <typename E, bool SH> struct __align__(16) BackwardShared {
+    Rows<float, SH> g;
+    Rows<E, SH> x, i, dh;
     float2 fmap[RUNS][C];          // the runs' maps of the states, forwards
     float fstate[RUNS][C];         // the state that enters each run
     Shared s;
 };
 
-template <typename E, int G, bool CHAIN>
-__global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch,
+template <typename E, bool SH, bool ADJ, bool CHAIN>
+__global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) scan_backward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch,
                                                                                     const float *states, const void *dh_, int64_t lddh,
                                                                                     const float *dfinal, ScanGrads out)
 {
-    constexpr bool ADJ = G == 16 || (sizeof(E) == 2 && G == 4);
-    constexpr int G4 = G < 4 ? 4 : G;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<BackwardShared<E> *>(smem_raw);
+    auto &sm = *reinterpret_cast<BackwardShared<E, SH> *>(smem_raw);
     if (!plan_matches(plan, sig)) {
         if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         return;
@@ -730,12 +758,12 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backw
     // part 0: the decays, which a tile takes to registers; part 1: what it reads again for the gradients
     auto load = [&](const Tile &t, int part) {
         if (part == 0) {
-            fill<float, G4>(sm.g, in.g, in.ldg, t.t0, T, t.col0, D);
+            fill(sm.g, in.g, in.ldg, t.t0, T, t.col0, D);
             return;
         }
-        fill<E, G>(sm.x, x, in.ldx, t.t0, T, t.col0, D);
-        if (ig) fill<E, G>(sm.i, ig, in.ldi, t.t0, T, t.col0, D);
-        fill<E, G>(sm.dh, dh, lddh, t.t0, T, t.col0, D);
+        fill(sm.x, x, in.ldx, t.t0, T, t.col0, D);
+        if (ig) fill(sm.i, ig, in.ldi, t.t0, T, t.col0, D);
+        fill(sm.dh, dh, lddh, t.t0, T, t.col0, D);
     };
     auto work = [&](const Tile &t, const Bounds &b, auto release) {
         const int left = D - t.col0, rows = T - t.t0 - run * RUN, place = b.place();
@@ -749,12 +777,14 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backw
         // the state before the tile, for the warp that folds the states' maps
         float f0 = 0.f;
         if (warp == WARPS - 1 && lane < left) f0 = states[static_cast<int64_t>(t.tt) * D + t.col0 + lane];
+        const Run<float, SH> gr(sm.g, run, in.g, in.ldg, t.t0);
+        const Run<E, SH> xr(sm.x, run, x, in.ldx, t.t0), ir(sm.i, run, ig, in.ldi, t.t0);
         float a[RUN][V], u[RUN][V];
 #pragma unroll
         for (int j = 0; j < RUN; ++j) {
             float gv[V];
-            get<ADJ>(sm.g.row(run, j), l, gv);
-            get<ADJ>(sm.x.row(run, j), l, u[j]);
+            get<ADJ>(gr(j), l, gv);
+            get<ADJ>(xr(j), l, u[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
         }
@@ -762,18 +792,19 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backw
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 float iv[V];
-                get<ADJ>(sm.i.row(run, j), l, iv);
+                get<ADJ>(ir(j), l, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
             }
         }
+        const Run<E, SH> hr(sm.dh, run, dh, lddh, t.t0);
         float P[V] = {1.f, 1.f}, F[V] = {0.f, 0.f}, B[V] = {0.f, 0.f};   // (P, F): of the states; (P, B): of the gradients
         by_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
                 float d[V];
-                get<ADJ>(sm.dh.row(run, j), l, d);
+                get<ADJ>(hr(j), l, d);
                 if constexpr (K == ANY)
                     if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, B);
 #pragma unroll
@@ -846,8 +877,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backw
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
                 float Gr[V], gx[V], gi[V], gg[V];
-                get<ADJ>(sm.dh.row(run, j), l, Gr);
-                get<ADJ>(sm.x.row(run, j), l, gi);
+                get<ADJ>(hr(j), l, Gr);
+                get<ADJ>(xr(j), l, gi);
                 if constexpr (K == ANY)
                     if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, e);
 #pragma unroll
@@ -860,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 4 ? 3 : CTAS) scan_backw
                     gx[v] = Gr[v];
                 }
                 if (ig) {
-                    get<ADJ>(sm.i.row(run, j), l, gx);
+                    get<ADJ>(ir(j), l, gx);
 #pragma unroll
                     for (int v = 0; v < V; ++v) gx[v] *= Gr[v];
                 }
@@ -928,12 +959,24 @@ template <typename F> cudaError_t by_type(int type, F f)
     return f(__nv_bfloat16{});
 }
 
-// The widest copy (16, 4 or 2 bytes) that every row of the tensor starts on; 16 for none.
-int row_copy(const void *p, int64_t ld, int bytes)
+// How a tensor's rows lie: all on 16 bytes, all on pairs of elements.
+struct Lie {
+    bool wide = true, even = true;
+    Lie &with(const void *p, int64_t ld, int bytes)
+    {
+        if (!p) return *this;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * bytes);
+        wide = wide && (at & 15) == 0;
+        even = even && (at & (2 * bytes - 1)) == 0;
+        return *this;
+    }
+};
+// Calls f(copies with an offset, channels in pairs) for how the rows lie.
+template <typename F> cudaError_t by_lie(const Lie &lie, F f)
 {
-    if (!p) return 16;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * bytes);
-    return (a & 15) == 0 ? 16 : (a & 3) == 0 ? 4 : 2;
+    if (lie.wide) return f(std::false_type{}, std::true_type{});
+    if (lie.even) return f(std::true_type{}, std::true_type{});
+    return f(std::true_type{}, std::false_type{});
 }
 
 // Runs a tile kernel in the form that the number of tiles asks for.  cluster / chain: the two instances.
@@ -968,11 +1011,11 @@ cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host
         const Layout l = layout_of(T, D);
         const size_t words = (l.end - l.state) / 16;
         const size_t want = (words + 4 * 256 - 1) / (4 * 256), most = 4 * static_cast<size_t>(sm_count());
+        const int64_t tiles = static_cast<int64_t>(nT) * nC, all = static_cast<int64_t>(ctas) * sm_count();
+        cfg.gridDim = dim3(static_cast<unsigned>(tiles < all ? tiles : all));
         chain_init<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
-            plan_dev, sig, nT, ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
+            plan_dev, sig, nT, static_cast<int>(cfg.gridDim.x), ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
         if (cudaError_t e = cudaGetLastError()) return e;
-        const int64_t tiles = static_cast<int64_t>(nT) * nC, grid = static_cast<int64_t>(ctas) * sm_count();
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles < grid ? tiles : grid));
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -988,18 +1031,12 @@ cudaError_t launch_scan_forward(const int32_t *plan_host, const int32_t *plan_de
 {
     return by_type(type, [&](auto ev) {
         using E = decltype(ev);
-        constexpr int e = sizeof(E);
-        auto with = [&](auto g) {
-            constexpr int G = decltype(g)::value;
-            return run(scan_forward<E, G, false>, scan_forward<E, G, true>, static_cast<int>(sizeof(ForwardShared<E>)), CTAS, plan_host, plan_dev,
-                       D, ws, stream, in, h, ldh, final_state, states);
-        };
-        const int x = row_copy(in.x, in.ldx, e), i = row_copy(in.i, in.ldi, e), g = row_copy(in.g, in.ldg, 4);
-        const int least = x < i ? (x < g ? x : g) : (i < g ? i : g);
-        if (least == 16) return with(std::integral_constant<int, 16>{});
-        if constexpr (e == 2)
-            if (least == 2) return with(std::integral_constant<int, 2>{});
-        return with(std::integral_constant<int, 4>{});
+        return by_lie(Lie().with(in.x, in.ldx, sizeof(E)).with(in.i, in.ldi, sizeof(E)).with(in.g, in.ldg, 4), [&](auto shift, auto adj) {
+            constexpr bool SH = decltype(shift)::value, ADJ = decltype(adj)::value;
+            using Sh = ForwardShared<E, SH>;
+            return run(scan_forward<E, SH, ADJ, false>, scan_forward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
+                       plan_dev, D, ws, stream, in, h, ldh, final_state, states);
+        });
     });
 }
 
@@ -1009,18 +1046,13 @@ cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_d
 {
     return by_type(type, [&](auto ev) {
         using E = decltype(ev);
-        constexpr int e = sizeof(E);
-        auto with = [&](auto g) {
-            constexpr int G = decltype(g)::value;
-            return run(scan_backward<E, G, false>, scan_backward<E, G, true>, static_cast<int>(sizeof(BackwardShared<E>)), e == 4 ? 3 : CTAS, plan_host,
+        const Lie lie = Lie().with(in.x, in.ldx, sizeof(E)).with(in.i, in.ldi, sizeof(E)).with(in.g, in.ldg, 4).with(dh, lddh, sizeof(E));
+        return by_lie(lie, [&](auto shift, auto adj) {
+            constexpr bool SH = decltype(shift)::value, ADJ = decltype(adj)::value;
+            using Sh = BackwardShared<E, SH>;
+            return run(scan_backward<E, SH, ADJ, false>, scan_backward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
                        plan_dev, D, ws, stream, in, states, dh, lddh, dfinal, out);
-        };
-        int least = row_copy(in.x, in.ldx, e);
-        for (const int c : {row_copy(in.i, in.ldi, e), row_copy(in.g, in.ldg, 4), row_copy(dh, lddh, e)}) least = c < least ? c : least;
-        if (least == 16) return with(std::integral_constant<int, 16>{});
-        if constexpr (e == 2)
-            if (least == 2) return with(std::integral_constant<int, 2>{});
-        return with(std::integral_constant<int, 4>{});
+        });
     });
 }
 

@@ -313,3 +313,29 @@ def test_step_records_a_slot_out_of_range():
     assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
     assert kda.kda_device_status() == kda.KDA_OK
     assert state.tolist() == [[1.0] * 8, [2.0] * 8] and h.tolist() == [[2.0] * 8, [0.0] * 8]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [5, 34, 65, 130])
+def test_every_alignment(D, kind):
+    """Tensors that start at every element of 16 bytes, with rows of every length modulo 16 bytes; the values around
+    them are NaN and stay out of the results."""
+    import torch
+    per = 16 // torch.finfo(torch_type(kind)).bits * 8
+    cu, dev, w = _draw([140, 20], D, kind, seed=D)
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])
+    for first in range(per):
+        for pad in (0, 1, 2, 3):
+            moved = dict(dev)
+            for name in ("x", "i", "g", "dh"):
+                ld = D + pad
+                flat = torch.full((cu[-1] * ld + first + 8,), float("nan"), dtype=dev[name].dtype, device="cuda")
+                rows = flat[first:first + cu[-1] * ld].view(cu[-1], ld)[:, :D]
+                rows.copy_(dev[name])
+                moved[name] = rows
+            h, final, states = _forward(cu, moved)
+            check(h, h_ref, kind, "h")
+            check(final, f_ref, "f32", "final")
+            for name, a, b, k in zip(("dx", "di", "dg", "dh0"), _backward(cu, moved, states), want, (kind, kind, "f32", "f32")):
+                check(a, b, k, name)
