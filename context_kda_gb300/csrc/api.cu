@@ -180,7 +180,7 @@ extern "C" int kda_device_status(void)
     int worst = KDA_OK;
     for (int st : {kda::take_prep_status(), kda::take_state_status(), kda::take_compose_status(),
                    kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status(),
-                   kda::take_scan_status(), kda::take_decode_status()})
+                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status()})
         if (st != KDA_OK && worst == KDA_OK) worst = st;
     return worst;
 }

@@ -11,11 +11,9 @@
 // Reciprocals and square roots are the hardware's approximations (about 2^-22 relative): fp32 results keep 1e-6.
 //
 // A CTA of BLOCK threads takes R rows at a time (NT threads a row, 8 NC channels a thread) and walks over
-// all its rows.  Every thread copies what it will read itself into its own slots of a ring in shared memory
-// (cp.async), one to three steps ahead, so the copies need no barrier; sums over a row take one barrier each
-// (none when a row is a warp or less).  U is the run of adjacent channels that a thread copies: 8 where rows
-// start on 16 bytes, otherwise 2 (2-byte types whose rows start on pairs) or 1; single 2-byte elements,
-// which no asynchronous copy moves, are read directly.
+// all its rows, which are copied to a ring in shared memory (cp.async) one to three steps ahead.  Sums over a row take
+// one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 where rows
+// start on 16 bytes (a thread copies what it reads itself, without a barrier), 1 otherwise.
 // FULL instances are for the usual call: every part but the gate is there, D is a multiple of 8 and all rows start on
 // 16 bytes.  They decide nothing about that per row (a third of the instructions of the others, which bound
 // them: 16384 x 2048 gradients in bf16 115 us without, see below with).
@@ -38,98 +36,86 @@ constexpr int MAX_GRID = 304;   // CTAs of a launch: rows of the backward's colu
 struct Shape {
     uint32_t T;
     int D, G, NT;                // channels, channels of a group, threads of a row
-    bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes (or on pairs): residual, the others
+    bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes: residual, the others
     float inv_d, inv_g;          // 1 / D, 1 / G
 };
 
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.
-template <typename X, int BLOCK, int NC, int U> struct Row {
-    static constexpr int NE = 8 * NC, NU = NE / U, RUN = U * static_cast<int>(sizeof(X));
-    static constexpr bool COPY = RUN >= 4;                // there is an asynchronous copy of this size
-    static constexpr int PB = RUN >= 16 ? 16 : 4, PIECES = COPY ? RUN / PB : 0, EPP = PB / static_cast<int>(sizeof(X));
-    static constexpr int BYTES = COPY ? NE * static_cast<int>(sizeof(X)) * BLOCK : 0;   // of the CTA, per step
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void unpack(uint32_t w, float *v, const __nv_bfloat16 *)
+{
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack(uint32_t w, float *v, const __half *)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+}
+__device__ __forceinline__ void unpack(uint32_t w, float *v, const float *) { v[0] = __uint_as_float(w); }
 
-    static __device__ __forceinline__ void copy(uint32_t dst, const X *src, int bytes)
+// A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.
+template <typename X, int BLOCK, int NC, int U> struct Row;
+
+// U = 8: rows start on 16 bytes; every thread copies its own channels into its own slots.
+template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 8> {
+    static constexpr int NE = 8 * NC, PIECES = static_cast<int>(sizeof(X)) / 2, EPP = 8 / PIECES;   // 16-byte pieces of a run
+    static constexpr int BYTES = NE * static_cast<int>(sizeof(X)) * BLOCK;                           // of the CTA, per step
+
+    // Copies the row's channels below D to the slots at 'base'; 'row' is the row's first channel.
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *, int ti, int NT, int D)
     {
-        if constexpr (PB == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    }
-    // Copies the row's channels below D to the slots at 'base' + the thread's; 'row' is at the thread's first channel.
-    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, int ti, int NT, int D)
-    {
-        if constexpr (COPY) {
 #pragma unroll
-            for (int q = 0; q < NU; ++q)
+        for (int q = 0; q < NC; ++q)
 #pragma unroll
-                for (int p = 0; p < PIECES; ++p) {
-                    const int left = (D - (ti + q * NT) * U - p * EPP) * static_cast<int>(sizeof(X));
-                    const int bytes = left < 0 ? 0 : left > PB ? PB : left;
-                    copy(base + ((q * PIECES + p) * BLOCK + threadIdx.x) * PB, bytes ? row + q * NT * U + p * EPP : row, bytes);
-                }
-        }
+            for (int p = 0; p < PIECES; ++p) {
+                const int c = (ti + q * NT) * 8 + p * EPP, left = (D - c) * static_cast<int>(sizeof(X));
+                const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+                copy16(base + ((q * PIECES + p) * BLOCK + threadIdx.x) * 16, bytes ? row + c : row, bytes);
+            }
     }
     // The same where the thread's channels all exist.
-    static __device__ __forceinline__ void fetch_all(uint32_t base, const X *row)
+    static __device__ __forceinline__ void fetch_all(uint32_t base, const X *row, int ti)
     {
 #pragma unroll
-        for (int p = 0; p < NU * PIECES; ++p) copy_all(base + (p * BLOCK + threadIdx.x) * PB, row + p * EPP);
-    }
-    static __device__ __forceinline__ void copy_all(uint32_t dst, const X *src)
-    {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        for (int p = 0; p < PIECES; ++p) copy16(base + (p * BLOCK + threadIdx.x) * 16, row + ti * 8 + p * EPP);
     }
     // Zeros in place of a row past the end ('any': some address of the tensor).
     static __device__ __forceinline__ void fetch_none(uint32_t base, const X *any)
     {
-        if constexpr (COPY) {
 #pragma unroll
-            for (int j = 0; j < NU * PIECES; ++j) copy(base + (j * BLOCK + threadIdx.x) * PB, any, 0);
-        }
+        for (int j = 0; j < NC * PIECES; ++j) copy16(base + (j * BLOCK + threadIdx.x) * 16, any, 0);
     }
-    static __device__ __forceinline__ void unpack(uint32_t w, float *v, __nv_bfloat16 *)
-    {
-        v[0] = __uint_as_float(w << 16);
-        v[1] = __uint_as_float(w & 0xFFFF0000u);
-    }
-    static __device__ __forceinline__ void unpack(uint32_t w, float *v, __half *)
-    {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-        v[0] = f.x;
-        v[1] = f.y;
-    }
-    static __device__ __forceinline__ void unpack(uint32_t w, float *v, float *) { v[0] = __uint_as_float(w); }
-
-    // The channels as fp32 (zeros from D on): from the slots, or from the row where there is no copy.
+    // The channels as fp32 (zeros from D on): from the slots, or from the row where there is no ring.
     template <bool RING>
     static __device__ __forceinline__ void read(const unsigned char *base, const X *row, int ti, int NT, int D, bool in, float (&v)[NE])
     {
-        if constexpr (RING && COPY) {
+        if constexpr (RING) {
             constexpr int EPW = 4 / static_cast<int>(sizeof(X));
 #pragma unroll
-            for (int j = 0; j < NU * PIECES; ++j) {
-                if constexpr (PB == 16) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(base + (j * BLOCK + threadIdx.x) * 16);
-                    unpack(w.x, v + j * EPP, static_cast<X *>(nullptr));
-                    unpack(w.y, v + j * EPP + EPW, static_cast<X *>(nullptr));
-                    unpack(w.z, v + j * EPP + 2 * EPW, static_cast<X *>(nullptr));
-                    unpack(w.w, v + j * EPP + 3 * EPW, static_cast<X *>(nullptr));
-                } else {
-                    unpack(*reinterpret_cast<const uint32_t *>(base + (j * BLOCK + threadIdx.x) * 4), v + j * EPP, static_cast<X *>(nullptr));
-                }
+            for (int j = 0; j < NC * PIECES; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(base + (j * BLOCK + threadIdx.x) * 16);
+                unpack(w.x, v + j * EPP, row);
+                unpack(w.y, v + j * EPP + EPW, row);
+                unpack(w.z, v + j * EPP + 2 * EPW, row);
+                unpack(w.w, v + j * EPP + 3 * EPW, row);
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < NU; ++q)
-#pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    const int c = (ti + q * NT) * U + j;
-                    v[q * U + j] = in && c < D ? to_f32(row[c]) : 0.f;
-                }
+            for (int j = 0; j < NE; ++j) {
+                const int c = (ti + j / 8 * NT) * 8 + j % 8;
+                v[j] = in && c < D ? to_f32(row[c]) : 0.f;
+            }
         }
     }
     // A thread's eight channels from 'at' on, aligned.
@@ -139,32 +125,77 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
 #pragma unroll
         for (int j = 0; j < NE; ++j) e[j] = from_f32<X>(v[j]);
 #pragma unroll
-        for (int p = 0; p < NE * static_cast<int>(sizeof(X)) / 16; ++p) reinterpret_cast<uint4 *>(at)[p] = reinterpret_cast<const uint4 *>(e)[p];
+        for (int p = 0; p < NC * PIECES; ++p) reinterpret_cast<uint4 *>(at)[p] = reinterpret_cast<const uint4 *>(e)[p];
     }
     static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool wide, const float (&v)[NE])
     {
 #pragma unroll
-        for (int q = 0; q < NU; ++q) {
-            const int c = (ti + q * NT) * U;
-            X e[U];
+        for (int q = 0; q < NC; ++q) {
+            const int c = (ti + q * NT) * 8;
+            X e[8];
 #pragma unroll
-            for (int j = 0; j < U; ++j) e[j] = from_f32<X>(v[q * U + j]);
-            if (U > 1 && wide && c + U <= D) {
-                if constexpr (RUN >= 16) {
+            for (int j = 0; j < 8; ++j) e[j] = from_f32<X>(v[q * 8 + j]);
+            if (wide && c + 8 <= D) {
 #pragma unroll
-                    for (int p = 0; p < RUN / 16; ++p)
-                        reinterpret_cast<uint4 *>(row + c)[p] = reinterpret_cast<const uint4 *>(e)[p];
-                } else if constexpr (RUN == 4) {
-                    *reinterpret_cast<uint32_t *>(row + c) = *reinterpret_cast<const uint32_t *>(e);
-                } else if constexpr (RUN == 8) {
-                    *reinterpret_cast<uint2 *>(row + c) = *reinterpret_cast<const uint2 *>(e);
-                }
+                for (int p = 0; p < PIECES; ++p) reinterpret_cast<uint4 *>(row + c)[p] = reinterpret_cast<const uint4 *>(e)[p];
                 continue;
             }
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+            for (int j = 0; j < 8; ++j)
                 if (c + j < D) row[c + j] = e[j];
         }
+    }
+};
+
+// U = 1: any rows.  A row is copied 16 bytes at a time with the 16 bytes it starts in, by all of its threads, so it is
+// read behind a barrier of them, from an offset.
+template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
+    static constexpr int NE = 8 * NC, SIZE = static_cast<int>(sizeof(X)), EPC = 16 / SIZE;
+    static constexpr int BYTES = BLOCK * (NE * SIZE + 4);     // of the CTA, per step: a row has four threads at least
+    static __device__ __forceinline__ int place(int NT) { return static_cast<int>(threadIdx.x / NT) * (NT * NE * SIZE + 16); }
+
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D)
+    {
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u), end = off + D * SIZE;
+        const char *p = reinterpret_cast<const char *>(row) - off;
+        base += place(NT);
+#pragma unroll
+        for (int k = 0; k <= NE * SIZE / 16; ++k) {
+            const int at = (ti + k * NT) * 16;
+            if (at >= end) break;
+            const int bytes = end - at > 16 ? 16 : end - at;
+            if (p + at < reinterpret_cast<const char *>(tensor)) {     // the tensor starts here: nothing before it is read
+                for (int e = off / SIZE; e < EPC && at + e * SIZE < end; ++e)
+                    store(base + at + e * SIZE, reinterpret_cast<const X *>(p + at)[e]);
+            } else {
+                copy16(base + at, p + at, bytes);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(uint32_t at, X v)
+    {
+        if constexpr (SIZE == 4)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(to_f32(v)) : "memory");
+        else
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const unsigned short *>(&v)) : "memory");
+    }
+    static __device__ __forceinline__ void fetch_none(uint32_t, const X *) {}
+    template <bool RING>
+    static __device__ __forceinline__ void read(const unsigned char *base, const X *row, int ti, int NT, int D, bool in, float (&v)[NE])
+    {
+        const X *p = RING ? reinterpret_cast<const X *>(base + place(NT) + (reinterpret_cast<uintptr_t>(row) & 15u)) : row;
+        const int some = in ? D : 0;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            const int c = ti + j * NT;
+            v[j] = c < some ? to_f32(p[c]) : 0.f;
+        }
+    }
+    static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool, const float (&v)[NE])
+    {
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            if (ti + j * NT < D) row[ti + j * NT] = from_f32<X>(v[j]);
     }
 };
 
@@ -292,8 +323,8 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = RowR::BYTES + 2 * RowE::BYTES;
     static constexpr int CTAS = NC == 1 ? 1024 / BLOCK : 1;                       // of an SM
-    static constexpr int FIT = STEP ? 220 / CTAS * 1024 / STEP : 0;
-    static constexpr int S = FIT > 3 ? 3 : FIT;      // steps in the ring; 0: no ring
+    static constexpr int FIT = 220 / CTAS * 1024 / STEP;
+    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U == 1 ? 0 : FIT;      // steps in the ring; 0: no ring
     static constexpr int SMEM = S * STEP;
 };
 
@@ -323,13 +354,13 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
         const uint32_t b = base + slot * F::STEP;
         if (t < s.T && (!FULL || active)) {
             if constexpr (FULL) {
-                RowR::fetch_all(b, row_at(r, t, lr, first));
-                RowE::fetch_all(b + RowR::BYTES, row_at(o, t, lo, first));
-                if (z) RowE::fetch_all(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first));
+                RowR::fetch_all(b, row_at(r, t, lr, 0), ti);
+                RowE::fetch_all(b + RowR::BYTES, row_at(o, t, lo, 0), ti);
+                if (z) RowE::fetch_all(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), ti);
             } else {
-                if (r) RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
-                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, first), ti, NT, D);
-                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, first), ti, NT, D);
+                if (r) RowR::fetch(b, row_at(r, t, lr, 0), r, ti, NT, D);
+                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, 0), o, ti, NT, D);
+                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), z, ti, NT, D);
             }
         } else {
             if (has_r) RowR::fetch_none(b, r);
@@ -338,10 +369,11 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
         }
     };
     uint32_t t0 = blockIdx.x * rows;
-    for (int k = 0; k < S - 1; ++k) {
-        fetch(k, t0 + rr + k * step);
-        cp_commit();
-    }
+    if constexpr (S > 0)
+        for (int k = 0; k < S - 1; ++k) {
+            fetch(k, t0 + rr + k * step);
+            cp_commit();
+        }
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
     float wl[NE], wr[NE];      // scale * ls * w_post, w_pre
@@ -362,10 +394,18 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     for (; t0 < s.T; t0 += step) {
         const uint32_t t = t0 + rr;
         const bool in = t < s.T;
-        if constexpr (S > 0) {
+        auto ahead = [&] {
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
+        };
+        if constexpr (S > 0 && U == 8) {
+            ahead();
             cp_wait<S - 1>();
+        } else if constexpr (S > 0) {
+            cp_wait<S - 2>();
+            if (NT > 32) __syncthreads();      // the row is there, and the one before it has been read
+            else __syncwarp();
+            ahead();
         }
         const unsigned char *b = ring + slot * F::STEP;
         float v[NE];
@@ -448,8 +488,8 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = 2 * RowR::BYTES + 3 * RowE::BYTES;
     static constexpr int CTAS = BLOCK == 256 ? 2 : 1;                             // of an SM
-    static constexpr int FIT = STEP ? 220 / CTAS * 1024 / STEP : 0;
-    static constexpr int S = FIT > 3 ? 3 : FIT;
+    static constexpr int FIT = 220 / CTAS * 1024 / STEP;
+    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U == 1 ? 0 : FIT;
     static constexpr int FOLD = BLOCK * NE * 4;      // the column sums of the CTA, folded at the end
     static constexpr int SMEM = S * STEP > FOLD ? S * STEP : FOLD;
 };
@@ -485,19 +525,19 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         const uint32_t b = base + slot * B::STEP;
         if (t < s.T && (!FULL || active)) {
             if constexpr (FULL) {
-                RowR::fetch_all(b, row_at(r, t, lr, first));
-                RowE::fetch_all(b + O_DY, row_at(dy, t, ldy, first));
-                RowR::fetch_all(b + O_DRO, row_at(dro, t, ldr, first));
-                RowE::fetch_all(b + O_O, row_at(o, t, lo, first));
-                if (z) RowE::fetch_all(b + O_Z, row_at(z, t, lz, first));
+                RowR::fetch_all(b, row_at(r, t, lr, 0), ti);
+                RowE::fetch_all(b + O_DY, row_at(dy, t, ldy, 0), ti);
+                RowR::fetch_all(b + O_DRO, row_at(dro, t, ldr, 0), ti);
+                RowE::fetch_all(b + O_O, row_at(o, t, lo, 0), ti);
+                if (z) RowE::fetch_all(b + O_Z, row_at(z, t, lz, 0), ti);
             } else {
                 if (a.w_pre) {
-                    RowR::fetch(b, row_at(r, t, lr, first), ti, NT, D);
-                    RowE::fetch(b + O_DY, row_at(dy, t, ldy, first), ti, NT, D);
+                    RowR::fetch(b, row_at(r, t, lr, 0), r, ti, NT, D);
+                    RowE::fetch(b + O_DY, row_at(dy, t, ldy, 0), dy, ti, NT, D);
                 }
-                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, first), ti, NT, D);
-                if (o) RowE::fetch(b + O_O, row_at(o, t, lo, first), ti, NT, D);
-                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, first), ti, NT, D);
+                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, 0), dro, ti, NT, D);
+                if (o) RowE::fetch(b + O_O, row_at(o, t, lo, 0), o, ti, NT, D);
+                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, 0), z, ti, NT, D);
             }
         } else {
             if (has_pre) {
@@ -510,10 +550,11 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         }
     };
     uint32_t t0 = blockIdx.x * rows;
-    for (int k = 0; k < S - 1; ++k) {
-        fetch(k, t0 + rr + k * step);
-        cp_commit();
-    }
+    if constexpr (S > 0)
+        for (int k = 0; k < S - 1; ++k) {
+            fetch(k, t0 + rr + k * step);
+            cp_commit();
+        }
     auto in_group = [&](int c) { return G == D ? c : c & (G - 1); };
     auto in_row = [&](int c) { return c; };
     float acc_g[NE], acc_l[NE], acc_r[NE];
@@ -529,10 +570,18 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     for (; t0 < s.T; t0 += step) {
         const uint32_t t = t0 + rr;
         const bool in = t < s.T;
-        if constexpr (S > 0) {
+        auto ahead = [&] {
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
+        };
+        if constexpr (S > 0 && U == 8) {
+            ahead();
             cp_wait<S - 1>();
+        } else if constexpr (S > 0) {
+            cp_wait<S - 2>();
+            if (NT > 32) __syncthreads();      // the row is there, and the one before it has been read
+            else __syncwarp();
+            ahead();
         }
         const unsigned char *b = ring + slot * B::STEP;
         float ov[NE], rv[NE], e[NE];
@@ -702,10 +751,10 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 
 // ---- launches ---------------------------------------------------------------------------------------------
 
-// Every row of the tensor starts on 'bytes'.
-inline bool rows_on(const void *p, int64_t ld, int elem, int bytes)
+// Every row of the tensor starts on 16 bytes.
+inline bool rows_on(const void *p, int64_t ld, int elem)
 {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && (ld * elem & (bytes - 1)) == 0);
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * elem & 15) == 0);
 }
 
 // Threads of a row: as many as hold it in 8 nc channels each, and a group's where runs are short.
@@ -757,20 +806,13 @@ template <typename R, typename E>
 cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
 {
     constexpr int re = sizeof(R), e = sizeof(E);
-    if (rows_on(a.r, a.ldr, re, 16) && rows_on(a.o, a.ldo, e, 16) && rows_on(a.z, a.ldz, e, 16)) {
-        s.wide_r = rows_on(r_out, ldro, re, 16);
-        s.wide_a = rows_on(y, ldy, e, 16);
+    if (rows_on(a.r, a.ldr, re) && rows_on(a.o, a.ldo, e) && rows_on(a.z, a.ldz, e)) {
+        s.wide_r = rows_on(r_out, ldro, re);
+        s.wide_a = rows_on(y, ldy, e);
         if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 4096)
             return s.D <= 2048 ? run_forward<R, E, 256, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream)
                                : run_forward<R, E, 512, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream);
         return KDA_NORM_PICK(run_forward, R, E, 8, s, a, r_out, ldro, y, ldy, stream);
-    }
-    if constexpr (e == 2) {
-        if (rows_on(a.r, a.ldr, re, 4) && rows_on(a.o, a.ldo, e, 4) && rows_on(a.z, a.ldz, e, 4)) {
-            s.wide_r = rows_on(r_out, ldro, re, 2 * re);
-            s.wide_a = rows_on(y, ldy, e, 4);
-            return KDA_NORM_PICK(run_forward, R, E, 2, s, a, r_out, ldro, y, ldy, stream);
-        }
     }
     return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
 }
@@ -780,26 +822,15 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
                           float *part, int *grid, cudaStream_t stream)
 {
     constexpr int re = sizeof(R), e = sizeof(E);
-    auto on = [&](int r_bytes, int e_bytes) {
-        return (!a.w_pre || (rows_on(a.r, a.ldr, re, r_bytes) && rows_on(dy, lddy, e, e_bytes))) && rows_on(dro, lddro, re, r_bytes) &&
-               rows_on(a.o, a.ldo, e, e_bytes) && rows_on(a.z, a.ldz, e, e_bytes);
-    };
-    if (on(16, 16)) {
-        s.wide_r = rows_on(g.dr, g.lddr, re, 16);
-        s.wide_a = rows_on(g.d_o, g.lddo, e, 16);
-        s.wide_b = rows_on(g.dz, g.lddz, e, 16);
+    const bool pre = !a.w_pre || (rows_on(a.r, a.ldr, re) && rows_on(dy, lddy, e));
+    if (pre && rows_on(dro, lddro, re) && rows_on(a.o, a.ldo, e) && rows_on(a.z, a.ldz, e)) {
+        s.wide_r = rows_on(g.dr, g.lddr, re);
+        s.wide_a = rows_on(g.d_o, g.lddo, e);
+        s.wide_b = rows_on(g.dz, g.lddz, e);
         if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 4096)
             return s.D <= 2048 ? run_backward<R, E, 256, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
                                : run_backward<R, E, 512, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return KDA_NORM_PICK(run_backward, R, E, 8, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
-    }
-    if constexpr (e == 2) {
-        if (on(4, 4)) {
-            s.wide_r = rows_on(g.dr, g.lddr, re, 2 * re);
-            s.wide_a = rows_on(g.d_o, g.lddo, e, 4);
-            s.wide_b = rows_on(g.dz, g.lddz, e, 4);
-            return KDA_NORM_PICK(run_backward, R, E, 2, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
-        }
     }
     return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
 }

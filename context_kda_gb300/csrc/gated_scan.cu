@@ -1,608 +1,8 @@
-// Gated linear recurrence over packed sequences, per channel:
-//     h_t = exp(g_t) h_{t-1} + i_t x_t,   h_{-1} = h0 of the sequence,
-// its gradients (the same recurrence backwards in time) and its single-token step.
-//
-// One pass over the data.  Over a run of tokens the recurrence is the map h -> A h + B with A the product
-// of the decays and B the run's state from zero, and maps compose as (A2, B2) o (A1, B1) = (A1 A2, A2 B1 + B2);
-// a run in which a sequence starts forgets what came before (h -> B, marked by A = -1: decays are not
-// negative), so nothing of another sequence, infinities and NaN included, is ever multiplied in.
-//
-// The stream is cut into tiles of 128 tokens x 32 channels, a tile into 8 runs of 16 tokens (half a warp each, two
-// channels a lane).  A CTA of four warps copies a tile to shared memory (cp.async), folds each run in
-// registers, folds the runs' maps in shared memory and publishes the tile's; with the tile's incoming state known,
-// every run is finished from registers and the results are written.  Inputs are read from memory once.  The
-// kernel waits rather than computes (for copies, for other tiles' maps), so four CTAs share an SM, each in another phase;
-// a tile's copies are requested as soon as the last tile's have gone to registers.
-//   - Up to 8 tiles of tokens ('cluster'): the CTAs of a channel range are one cluster; they exchange the
-//     maps through distributed shared memory.  One launch and no workspace, for short inputs, where
-//     latency counts.
-//   - More ('chain'): CTAs draw tiles in time order from a ticket, so that a tile waits only for tiles drawn
-//     before it by CTAs that run.  A tile's incoming state is folded, always in the same order, from the
-//     state at its group's start and the maps of the group's earlier tiles; the group's last tile publishes
-//     the next group's state.  Only that last step is serial in time, once a group.  Published words
-//     carry their own validity (they are all ones until written, which no published value is), so that one
-//     8-byte store and one load pass a map on.  A kernel before the main one sets them, the ticket and each
-//     tile's sequence starts.
-//   - Waits give up after about two seconds (KDA_ERR_TIMEOUT through kda_device_status).
-//
-// The backward takes the states before every 128th token that the forward saved, so a tile recomputes its
-// states without waiting; its own recurrence is
-//     G_t = dh_t + e_{t+1},  e_t = exp(g_t) G_t   (e_{t+1} = dfinal at the last token of a sequence),
-//     dx = i G, di = x G, dg = e_t h_{t-1}, dh0 = e at the first token,
-// with tiles taken from the last to the first.
-#include <type_traits>
-
-#include "elem.cuh"
-#include "kda_internal.cuh"
-#include "tc.cuh"
+// Gated linear recurrence: forward and single-token step (gated_scan.cuh).
+#include "gated_scan.cuh"
 
 namespace kda {
 namespace {
-
-using namespace tc;
-
-constexpr int L = KDA_SCAN_TILE;             // tokens of a tile
-constexpr int C = 32;                        // channels of a tile
-constexpr int RUN = 16, RUNS = L / RUN;      // tokens of a run, runs of a tile
-constexpr int V = 2;                         // channels of a lane
-constexpr int WARPS = RUNS / 2, THREADS = WARPS * 32;
-// CTAs of an SM: four, or as many as their shared memory allows.
-template <typename Sh> constexpr int ctas_of() { return 233472 / (static_cast<int>(sizeof(Sh)) + 1024) < 4 ? 233472 / (static_cast<int>(sizeof(Sh)) + 1024) : 4; }
-constexpr int GROUP = 16, SHORT_GROUP = 8;   // tiles of a group: see run()
-constexpr int MAX_CLUSTER = 8;               // tiles that a cluster covers
-constexpr long long SPIN = 4000000000LL;     // clocks of a wait: about two seconds
-
-__device__ int g_scan_status;
-
-// The sequence starts of a tile: bit j: a sequence starts at its token j; 'first': the lowest such sequence.
-// The end of the stream counts as the start of sequence N.
-struct __align__(16) Starts {
-    uint32_t bits[L / 32];
-    int first, pad[3];
-};
-static_assert(sizeof(Starts) == 32 && L == 128 && RUN == 16, "two runs a word, four words a tile");
-
-// Workspace of the chain (bytes).
-struct Layout {
-    size_t starts, state, map, end;   // each tile's sequence starts; groups' states; tiles' maps
-};
-__host__ __device__ inline int tiles_of(int T) { return static_cast<int>((static_cast<int64_t>(T) + L - 1) / L); }
-inline int padded(int D) { return (D + C - 1) / C * C; }
-inline Layout layout_of(int64_t T, int D)
-{
-    const size_t nT = static_cast<size_t>(T + L - 1) / L, Dp = padded(D);
-    auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
-    Layout l;
-    l.starts = 256;                                  // the ticket comes first
-    l.state = up(l.starts + (nT + 1) * sizeof(Starts));
-    l.map = up(l.state + (nT / SHORT_GROUP + 1) * Dp * 4);
-    l.end = l.map + nT * Dp * 8;
-    return l;
-}
-struct Chain {
-    int *ticket;
-    Starts *starts;       // [tiles + 1]
-    uint32_t *state;      // [groups][Dp], all ones until published
-    uint64_t *map;        // [tiles][Dp], low word A, high word B
-    int Dp, group;        // padded channels; tiles of a group
-};
-inline Chain chain_of(void *ws, int64_t T, int D)
-{
-    char *b = static_cast<char *>(ws);
-    const Layout l = layout_of(T, D);
-    return Chain{reinterpret_cast<int *>(b), reinterpret_cast<Starts *>(b + l.starts), reinterpret_cast<uint32_t *>(b + l.state),
-                 reinterpret_cast<uint64_t *>(b + l.map), padded(D), GROUP};
-}
-
-__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int grid, int *ticket, Starts *starts,
-                                                  uint4 *words, size_t n)
-{
-    tc::grid_dep_launch();
-    const size_t id = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x, step = static_cast<size_t>(gridDim.x) * blockDim.x;
-    if (!plan_matches(plan, sig)) return;   // the main kernel records it
-    for (size_t j = id; j < n; j += step) words[j] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    if (id == 0) *ticket = grid;
-    const PlanView pv{plan};
-    const int32_t *cu = pv.cu();
-    const int lane = threadIdx.x & 31, N = pv.N();
-    for (size_t j = id / 32; j <= static_cast<size_t>(nT); j += step / 32) {     // a warp a tile
-        const int64_t t0 = static_cast<int64_t>(j) * L;
-        int lo = 0, hi = N + 1;                                // first n with cu[n] >= t0 (N + 1: none)
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] < t0) lo = mid + 1;
-            else hi = mid;
-        }
-        uint32_t mine[L / 32] = {};
-        for (int k = 0; k < L / 32; ++k) {                     // at most a start a token
-            const int m = lo + k * 32 + lane;
-            const int64_t t = m <= N ? cu[m] - t0 : L;
-#pragma unroll
-            for (int w = 0; w < L / 32; ++w)
-                if (t >> 5 == w) mine[w] |= 1u << (t & 31);
-        }
-#pragma unroll
-        for (int w = 0; w < L / 32; ++w) mine[w] = __reduce_or_sync(0xffffffffu, mine[w]);
-        if (lane == 0) {
-            Starts st = {};
-#pragma unroll
-            for (int w = 0; w < L / 32; ++w) st.bits[w] = mine[w];
-            st.first = lo;
-            starts[j] = st;
-        }
-    }
-}
-
-// ---- a tile in shared memory ----------------------------------------------------------------------------
-
-// Rows of one tensor, run by run.  SH: rows that do not all start on 16 bytes are copied with the 16 bytes they start in,
-// so a row takes one copy more and its channels start at an offset.  Runs are moved against each other where a
-// warp, which reads two runs at once, would find both in the same banks.
-template <typename X, bool SH> struct __align__(16) Rows {
-    static constexpr int EPC = 16 / static_cast<int>(sizeof(X));            // elements of a copy
-    static constexpr int PITCH = (C + (SH ? EPC : 0)) * static_cast<int>(sizeof(X));
-    static constexpr int RUN_BYTES = RUN * PITCH + (SH || sizeof(X) == 2 ? 64 : 0);
-    unsigned char b[RUNS * RUN_BYTES];
-    __device__ __forceinline__ X *row(int run, int j) { return reinterpret_cast<X *>(b + run * RUN_BYTES + j * PITCH); }
-};
-// The row of a run's j-th token in shared memory, from its first channel on.
-template <typename X, bool SH> struct Run {
-    Rows<X, SH> &rows;
-    int run;
-    uint32_t first, ld;        // element the run's first row starts at, and between rows (modulo a copy)
-    __device__ __forceinline__ Run(Rows<X, SH> &r, int n, const X *src, int64_t stride, int t0) : rows(r), run(n), first(0), ld(0)
-    {
-        if constexpr (SH) {
-            first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) / sizeof(X)) + static_cast<uint32_t>(t0 + n * RUN) * static_cast<uint32_t>(stride);
-            ld = static_cast<uint32_t>(stride);
-        }
-    }
-    __device__ __forceinline__ const X *operator()(int j) const
-    {
-        return rows.row(run, j) + (SH ? (first + j * ld) & (Rows<X, SH>::EPC - 1) : 0u);
-    }
-};
-// What the runs and tiles of a channel range pass on.
-struct Shared {
-    float2 map[RUNS][C];           // the runs' maps
-    float state[RUNS][C];          // the state that enters each run
-    float2 before[GROUP - 1][C];   // maps of the group's tiles before this one (cluster: this tile's in [0])
-    Starts starts;                 // cluster: the tile's sequence starts
-    uint32_t after;
-    int next, bad;
-};
-
-// ---- copies ---------------------------------------------------------------------------------------------
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// Tokens t0.. (zeros from T on), channels c0.. (zeros from D on) of a tensor of rows.
-template <typename X, bool SH>
-__device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld, int t0, int T, int c0, int D)
-{
-    using R = Rows<X, SH>;
-    if constexpr (!SH) {
-        constexpr int CPR = C / R::EPC, STEP = THREADS / CPR;      // copies of a row, rows of a step
-        const int row = threadIdx.x / CPR, c = threadIdx.x % CPR * R::EPC;
-        const X *p = src + (static_cast<int64_t>(t0) + row) * ld + c0 + c;
-        const int64_t hop = STEP * ld;
-        const int left = (D - c0 - c) * static_cast<int>(sizeof(X));
-        const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-        const int rows = bytes ? T - t0 - row : 0;                 // of this thread, from its first on
-        // the k-th row's place is a constant from the first's: steps never leave the first row's place within its run
-        static_assert(STEP % RUN == 0 || RUN % STEP == 0, "whole runs a step or whole steps a run");
-        const uint32_t to = smem_u32(dst.row(row / RUN, row % RUN) + c);
-        auto place = [](int k) { return k * STEP / RUN * R::RUN_BYTES + k * STEP % RUN * R::PITCH; };
-        if (rows >= L) {
-#pragma unroll
-            for (int k = 0; k < L / STEP; ++k) {
-                copy16(to + place(k), p, bytes);
-                p += hop;
-            }
-        } else {
-#pragma unroll 4
-            for (int k = 0; k < L / STEP; ++k) {
-                const bool in = k * STEP < rows;
-                copy16(to + place(k), in ? p : src, in ? bytes : 0);
-                p += hop;
-            }
-        }
-    } else {
-        // copy k of a thread: copy ch of row 'row'; THREADS copies are DR rows and DC copies on
-        constexpr int CPR = C / R::EPC + 1, DR = THREADS / CPR, DC = THREADS % CPR;
-        static_assert(THREADS == L, "as many copies a thread as a row takes");
-        int row = threadIdx.x / CPR, ch = threadIdx.x % CPR;
-        const int width = (D - c0 < C ? D - c0 : C) * static_cast<int>(sizeof(X));
-        const char *base = reinterpret_cast<const char *>(src), *p = reinterpret_cast<const char *>(src + (static_cast<int64_t>(t0) + row) * ld + c0);
-        const int64_t pitch = ld * static_cast<int64_t>(sizeof(X));
-#pragma unroll
-        for (int k = 0; k < CPR; ++k) {
-            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-            const int left = t0 + row < T ? off + width - ch * 16 : 0;
-            const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-            const char *from = p - off + ch * 16;
-            X *to = dst.row(row / RUN, row % RUN) + ch * R::EPC;
-            if (bytes && from < base) {        // the tensor starts within this copy: nothing before it is read
-                const int skip = static_cast<int>(base - from) / static_cast<int>(sizeof(X));
-                for (int e = 0; e < R::EPC; ++e)
-                    to[e] = e >= skip && e * static_cast<int>(sizeof(X)) < bytes ? reinterpret_cast<const X *>(from)[e] : from_f32<X>(0.f);
-            } else {
-                copy16(smem_u32(to), bytes ? from : base - (reinterpret_cast<uintptr_t>(base) & 15u), bytes);
-            }
-            row += DR;
-            ch += DC;
-            p += DR * pitch;
-            if (ch >= CPR) {
-                ch -= CPR;
-                ++row;
-                p += pitch;
-            }
-        }
-    }
-}
-
-// ---- channels of a lane ---------------------------------------------------------------------------------
-// Adjacent ones where a pair can be loaded and stored as one (ADJ), 16 apart otherwise (single elements of half a
-// warp are adjacent).
-template <bool ADJ> __device__ __forceinline__ int chan(int lane, int v) { return ADJ ? lane * 2 + v : lane + 16 * v; }
-
-__device__ __forceinline__ void unpack(uint32_t w, float (&o)[V], const __nv_bfloat16 *)
-{
-    o[0] = __uint_as_float(w << 16);
-    o[1] = __uint_as_float(w & 0xFFFF0000u);
-}
-__device__ __forceinline__ void unpack(uint32_t w, float (&o)[V], const __half *)
-{
-    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    o[0] = p.x;
-    o[1] = p.y;
-}
-template <bool ADJ, typename X> __device__ __forceinline__ void get(const X *row, int lane, float (&o)[V])
-{
-    if constexpr (ADJ && sizeof(X) == 4) {
-        const float2 p = reinterpret_cast<const float2 *>(row)[lane];
-        o[0] = p.x;
-        o[1] = p.y;
-    } else if constexpr (ADJ) {
-        unpack(reinterpret_cast<const uint32_t *>(row)[lane], o, row);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = to_f32(row[chan<ADJ>(lane, v)]);
-    }
-}
-
-__device__ __forceinline__ void put2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
-__device__ __forceinline__ void put2(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
-__device__ __forceinline__ void put2(__nv_bfloat16 *p, float a, float b)
-{
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
-}
-// A lane's channels of one row, from its first one's address, where all of the tile's channels exist and, if adjacent,
-// rows start on pairs.
-template <bool ADJ, typename X> __device__ __forceinline__ void put_all(X *at, const float (&o)[V])
-{
-    if constexpr (ADJ) {
-        put2(at, o[0], o[1]);
-    } else {
-        at[0] = from_f32<X>(o[0]);
-        at[16] = from_f32<X>(o[1]);
-    }
-}
-// The same where 'left' channels exist.
-template <bool ADJ, typename X> __device__ __forceinline__ void put(X *row, int lane, const float (&o)[V], int left)
-{
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (chan<ADJ>(lane, v) < left) row[chan<ADJ>(lane, v)] = from_f32<X>(o[v]);
-}
-template <typename X> __device__ __forceinline__ bool pairs(const X *p, int64_t ld)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (2 * sizeof(X) - 1)) == 0 && (ld & 1) == 0;
-}
-
-// exp(g) as 2^(g log2 e): the product's rounding moves the result by |g| 2^-24 relative, which is below the
-// exponential's own 2^-22 for every g that leaves anything to remember.
-__device__ __forceinline__ float decay(float g) { return ex2_ftz(g * 1.4426950408889634f); }
-
-// ---- maps -----------------------------------------------------------------------------------------------
-
-// One map more: (A, B) becomes (a, b) o (A, B).
-__device__ __forceinline__ void then(float &A, float &B, float a, float b)
-{
-    B = a < 0.f ? b : fmaf(a, B, b);
-    A = a < 0.f || A < 0.f ? -1.f : A * a;
-}
-__device__ __forceinline__ float apply(float2 m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
-
-// A float as a word that is not all ones (one NaN pattern gives way to another).
-__device__ __forceinline__ uint32_t word(float x)
-{
-    const uint32_t u = __float_as_uint(x);
-    return u == ~0u ? 0x7FFFFFFFu : u;
-}
-__device__ __forceinline__ uint64_t ld_relaxed(const uint64_t *p)
-{
-    uint64_t v;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t *p)
-{
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_relaxed(uint64_t *p, uint64_t v)
-{
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-__device__ __forceinline__ void st_relaxed(uint32_t *p, uint32_t v)
-{
-    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// The tile whose number in the direction of the recurrence is rt and whose channels start at col0.
-struct Tile {
-    int rt, tt, t0, col0;
-};
-template <bool REVERSE> __device__ __forceinline__ Tile tile_of(int k, int nT, int nC)
-{
-    Tile t;
-    t.rt = k / nC;
-    t.tt = REVERSE ? nT - 1 - t.rt : t.rt;
-    t.t0 = t.tt * L;
-    t.col0 = (k - t.rt * nC) * C;
-    return t;
-}
-
-// The sequence starts among a run's tokens and the token after them: bit j of 'mask'; the start at bit j is that of
-// sequence first + (number of bits below j).  'starts': those among the run's tokens.
-struct Bounds {
-    uint32_t mask, starts;
-    int first;
-    __device__ __forceinline__ Bounds(const uint4 &bits, int first_seq, uint32_t after, int run, int rows)
-    {
-        const int w = run / 2;             // = the warp
-        const uint32_t b[6] = {bits.x, bits.y, bits.z, bits.w, after, 0u};
-        uint32_t cur = 0, next = 0;
-        int below = first_seq;
-#pragma unroll
-        for (int k = 0; k < L / 32; ++k) {
-            if (k == w) cur = b[k], next = b[k + 1];
-            if (k < w) below += __popc(b[k]);
-        }
-        const int at = run % 2 * RUN;
-        mask = __funnelshift_r(cur, next, at) & ((2u << RUN) - 1);
-        first = below + __popc(cur & ((1u << at) - 1));
-        starts = mask & (rows >= RUN ? (1u << RUN) - 1 : rows > 0 ? (1u << rows) - 1 : 0u);
-    }
-    __device__ __forceinline__ int64_t seq(int j) const { return first + __popc(mask & ((1u << j) - 1)); }
-    // the first boundary's place, beyond the run if there is none
-    __device__ __forceinline__ int place() const { return mask ? __ffs(mask) - 1 : 2 * RUN; }
-};
-// How a warp's two runs are worked.  Boundaries between sequences are rare, but later tiles wait for the tiles that
-// hold them: a run with one takes it by selections (its rows of h0 and dfinal are requested before anything else),
-// only runs with several, and those at the tensor's edges, look at every token.
-enum { PLAIN = 0, ONE = 1, ANY = 2 };
-__device__ __forceinline__ int kind_of(const Bounds &b, bool inside)
-{
-    if (__any_sync(0xffffffffu, !inside || __popc(b.mask) > 1)) return ANY;
-    return __any_sync(0xffffffffu, b.mask != 0) ? ONE : PLAIN;
-}
-template <int K> using Kind = std::integral_constant<int, K>;
-template <typename F> __device__ __forceinline__ void by_kind(int kind, F f)
-{
-    if (kind == PLAIN) f(Kind<PLAIN>{});
-    else if (kind == ONE) f(Kind<ONE>{});
-    else f(Kind<ANY>{});
-}
-// Row n of [N][D] at a lane's channels (zeros past D, without the tensor, or where it is not wanted).
-template <bool ADJ> __device__ __forceinline__ void seq_row(const float *p, int64_t n, int D, int col0, int l, bool wanted, float (&o)[V])
-{
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = p && wanted && col0 + chan<ADJ>(l, v) < D ? p[n * D + col0 + chan<ADJ>(l, v)] : 0.f;
-}
-
-// ---- tiles in turn ----------------------------------------------------------------------------------------
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float2 ld_cluster(uint32_t addr)
-{
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ float2 map_of(uint64_t w)
-{
-    return make_float2(__uint_as_float(static_cast<uint32_t>(w)), __uint_as_float(static_cast<uint32_t>(w >> 32)));
-}
-
-// The state that enters each run of tile 'rt' (tiles and runs numbered in the direction of the recurrence), from the
-// runs' maps in sh.map, left in sh.state.  The warp 'one' does what one warp can, a channel a lane: it folds the maps, passes the
-// tile's on and folds the state that enters the tile.  meanwhile() runs once this tile's map is on its way and before
-// others are waited for.  False: a wait ran out.  All threads call it, behind a barrier after the maps were written.
-template <bool CHAIN, bool REVERSE, typename Meanwhile>
-__device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, int col0, bool last, Meanwhile meanwhile)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int one = REVERSE ? 0 : WARPS - 1;
-    float A = 1.f, B = 0.f, h = 0.f;
-    if (warp == one) {
-#pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            const float2 m = sh.map[REVERSE ? RUNS - 1 - r : r][lane];
-            then(A, B, m.x, m.y);
-        }
-    }
-    if constexpr (CHAIN) {
-        const int grp = rt / ch.group, pos = rt - grp * ch.group;
-        uint64_t *own = ch.map + static_cast<size_t>(rt) * ch.Dp + col0 + lane;
-        if (warp == one && pos < ch.group - 1 && !last)      // the group's last tile publishes a state instead
-            st_relaxed(own, static_cast<uint64_t>(word(B)) << 32 | __float_as_uint(A));
-        meanwhile();
-        constexpr int MOST = (GROUP - 1 + WARPS - 1) / WARPS;
-        uint64_t w[MOST];
-        uint32_t from = 0;
-        bool ok = true;
-        // only what has not come yet is read again: words that many CTAs wait for are few enough as it is
-#pragma unroll
-        for (int k = 0; k < MOST; ++k) w[k] = warp + k * WARPS < pos ? ~0ull : 0ull;
-        if (warp == one && grp > 0) from = ~0u;
-        const long long began = clock64();
-        while (true) {
-            bool all = true;
-#pragma unroll
-            for (int k = 0; k < MOST; ++k)
-                if (__any_sync(0xffffffffu, w[k] == ~0ull)) w[k] = ld_relaxed(own - static_cast<size_t>(pos - warp - k * WARPS) * ch.Dp);
-            if (__any_sync(0xffffffffu, from == ~0u)) from = ld_relaxed(ch.state + static_cast<size_t>(grp) * ch.Dp + col0 + lane);
-#pragma unroll
-            for (int k = 0; k < MOST; ++k) all = all && w[k] != ~0ull;
-            all = all && from != ~0u;
-            if (__all_sync(0xffffffffu, all)) break;
-            if (__any_sync(0xffffffffu, clock64() - began > SPIN)) {
-                ok = false;
-                break;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < MOST; ++k)
-            if (warp + k * WARPS < pos) sh.before[warp + k * WARPS][lane] = map_of(w[k]);
-        if (!ok) sh.bad = 1;
-        __syncthreads();
-        if (sh.bad) return false;
-        if (warp == one) {
-            h = __uint_as_float(from);
-#pragma unroll 5
-            for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
-            if (pos == ch.group - 1 && !last)
-                st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(apply(make_float2(A, B), h)));
-        }
-    } else {
-        if (warp == one) sh.before[0][lane] = make_float2(A, B);
-        cluster_arrive();
-        meanwhile();
-        cluster_wait();
-        if (warp == one) {
-            float2 m[MAX_CLUSTER - 1];
-#pragma unroll
-            for (int p = 0; p < MAX_CLUSTER - 1; ++p)
-                m[p] = p < rt ? ld_cluster(mapa(smem_u32(&sh.before[0][lane]), p)) : make_float2(1.f, 0.f);
-#pragma unroll
-            for (int p = 0; p < MAX_CLUSTER - 1; ++p) h = p < rt ? apply(m[p], h) : h;
-        }
-        cluster_arrive();   // paired with the wait at the kernel's end: no CTA leaves while its map is read
-    }
-    if (warp == one) {
-#pragma unroll
-        for (int k = 0; k < RUNS; ++k) {
-            const int r = REVERSE ? RUNS - 1 - k : k;
-            const float2 m = sh.map[r][lane];
-            sh.state[r][lane] = h;
-            h = apply(m, h);
-        }
-    }
-    __syncthreads();
-    return true;
-}
-
-// Walks the tiles of a CTA: load(tile, part) starts the copies of a tile in two parts, work(tile, bounds, release)
-// computes it; release runs within it, once part 0's copies may be overwritten, part 1's may when it is done.  work
-// returns false when a wait ran out.
-template <bool CHAIN, bool REVERSE, typename Load, typename Work>
-__device__ __forceinline__ void walk(Shared &sh, const Chain &ch, const PlanView &pv, int D, Load load, Work work)
-{
-    const int T = pv.T(), nT = tiles_of(T), nC = (D + C - 1) / C;
-    const int run = threadIdx.x / 16;
-    if (threadIdx.x == 0) sh.bad = 0;
-    if constexpr (!CHAIN) {
-        uint32_t cs, rank;
-        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
-        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        const Tile t = tile_of<REVERSE>(static_cast<int>(rank) * nC + static_cast<int>(blockIdx.x / cs), nT, nC);
-        if (t.rt < nT) {
-            load(t, 0);
-            load(t, 1);
-            if (threadIdx.x < L / 32) sh.starts.bits[threadIdx.x] = 0;
-            if (threadIdx.x == 32) sh.starts.first = 0x7FFFFFFF;
-            if (threadIdx.x == 33) sh.after = 0;
-            __syncthreads();
-            for (int n = threadIdx.x; n <= pv.N(); n += THREADS) {
-                const int pos = pv.cu()[n] - t.t0;
-                if (pos < 0 || pos > L) continue;
-                if (pos < L) atomicOr(&sh.starts.bits[pos >> 5], 1u << (pos & 31));
-                else sh.after = 1;
-                atomicMin(&sh.starts.first, n);
-            }
-            cp_wait_all();
-            __syncthreads();
-            work(t, Bounds(*reinterpret_cast<const uint4 *>(sh.starts.bits), sh.starts.first, sh.after, run, T - t.t0 - run * RUN), [] {});
-        } else {                    // clusters are a power of two: some CTAs may be past the end
-            cluster_arrive();
-            cluster_wait();
-            cluster_arrive();
-        }
-        cluster_wait();
-    } else {
-        // A CTA's first tile goes by its index: its copies start before the kernel that sets the workspace is waited
-        // for (blocks are dispatched in the order of their indexes, and a wait that this failed would end by its
-        // limit).  The others go by tickets, drawn ahead (k: in work, k2: next, then the one drawn while k is in work), so that neither
-        // the draw nor a tile's starts are waited for.  A CTA works its tiles in the order drawn, so the lowest
-        // unfinished tile is always in work with nothing to wait for.
-        const int n = nT * nC;
-        int drawn = 0, k = blockIdx.x;
-        uint4 bits = {};
-        uint32_t after = 0;
-        int first = 0;
-        auto words = [&](const Tile &t) {
-            bits = *reinterpret_cast<const uint4 *>(ch.starts[t.tt].bits);
-            first = ch.starts[t.tt].first;
-            after = ch.starts[t.tt + 1].bits[0];
-        };
-        if (k < n) {
-            const Tile t = tile_of<REVERSE>(k, nT, nC);
-            load(t, 0);
-            load(t, 1);
-            grid_dep_wait();
-            words(t);
-            if (threadIdx.x == 0) drawn = atomicAdd(ch.ticket, 1);
-        }
-        while (k < n) {
-            const Tile t = tile_of<REVERSE>(k, nT, nC);
-            __syncthreads();                 // everyone has read 'next'
-            if (threadIdx.x == 0) sh.next = drawn;
-            cp_wait_all();
-            __syncthreads();
-            const int k2 = sh.next;
-            const bool ok = work(t, Bounds(bits, first, after, run, T - t.t0 - run * RUN), [&] {
-                // called behind a barrier of the CTA: part 0's buffers are free
-                if (threadIdx.x == 0 && k2 < n) drawn = atomicAdd(ch.ticket, 1);
-                if (k2 < n) {
-                    const Tile u = tile_of<REVERSE>(k2, nT, nC);
-                    load(u, 0);
-                    words(u);
-                }
-            });
-            if (!ok) {
-                cp_wait_all();
-                if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_TIMEOUT);
-                return;
-            }
-            if (k2 < n) load(tile_of<REVERSE>(k2, nT, nC), 1);
-            k = k2;
-        }
-    }
-}
 
 // ---- forward --------------------------------------------------------------------------------------------
 
@@ -728,201 +128,6 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
     walk<CHAIN, false>(sm.s, ch, pv, D, load, work);
 }
 
-// ---- backward -------------------------------------------------------------------------------------------
-
-template <typename E, bool SH> struct __align__(16) BackwardShared {
-    Rows<float, SH> g;
-    Rows<E, SH> x, i, dh;
-    float2 fmap[RUNS][C];          // the runs' maps of the states, forwards
-    float fstate[RUNS][C];         // the state that enters each run
-    Shared s;
-};
-
-template <typename E, bool SH, bool ADJ, bool CHAIN>
-__global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) scan_backward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch,
-                                                                                    const float *states, const void *dh_, int64_t lddh,
-                                                                                    const float *dfinal, ScanGrads out)
-{
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<BackwardShared<E, SH> *>(smem_raw);
-    if (!plan_matches(plan, sig)) {
-        if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
-        return;
-    }
-    const PlanView pv{plan};
-    const int T = pv.T(), run = threadIdx.x / 16, l = threadIdx.x % 16, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const E *x = static_cast<const E *>(in.x), *ig = static_cast<const E *>(in.i), *dh = static_cast<const E *>(dh_);
-    E *dx = static_cast<E *>(out.dx), *di = static_cast<E *>(out.di);
-    const bool pair = !ADJ || (pairs(dx, out.lddx) && (!di || pairs(di, out.lddi)) && pairs(out.dg, out.lddg));
-
-    // part 0: the decays, which a tile takes to registers; part 1: what it reads again for the gradients
-    auto load = [&](const Tile &t, int part) {
-        if (part == 0) {
-            fill(sm.g, in.g, in.ldg, t.t0, T, t.col0, D);
-            return;
-        }
-        fill(sm.x, x, in.ldx, t.t0, T, t.col0, D);
-        if (ig) fill(sm.i, ig, in.ldi, t.t0, T, t.col0, D);
-        fill(sm.dh, dh, lddh, t.t0, T, t.col0, D);
-    };
-    auto work = [&](const Tile &t, const Bounds &b, auto release) {
-        const int left = D - t.col0, rows = T - t.t0 - run * RUN, place = b.place();
-        const uint32_t ends = b.mask >> 1;
-        const int kind = kind_of(b, rows >= RUN && left >= C && pair);
-        float h0[V] = {}, df[V] = {};
-        if (kind == ONE) {
-            seq_row<ADJ>(in.h0, b.first, D, t.col0, l, b.starts != 0, h0);
-            seq_row<ADJ>(dfinal, b.first - 1, D, t.col0, l, ends != 0, df);
-        }
-        // the state before the tile, for the warp that folds the states' maps
-        float f0 = 0.f;
-        if (warp == WARPS - 1 && lane < left) f0 = states[static_cast<int64_t>(t.tt) * D + t.col0 + lane];
-        const Run<float, SH> gr(sm.g, run, in.g, in.ldg, t.t0);
-        const Run<E, SH> xr(sm.x, run, x, in.ldx, t.t0), ir(sm.i, run, ig, in.ldi, t.t0);
-        float a[RUN][V], u[RUN][V];
-#pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-            float gv[V];
-            get<ADJ>(gr(j), l, gv);
-            get<ADJ>(xr(j), l, u[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
-        }
-        if (ig) {
-#pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                float iv[V];
-                get<ADJ>(ir(j), l, iv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
-            }
-        }
-        const Run<E, SH> hr(sm.dh, run, dh, lddh, t.t0);
-        float P[V] = {1.f, 1.f}, F[V] = {0.f, 0.f}, B[V] = {0.f, 0.f};   // (P, F): of the states; (P, B): of the gradients
-        by_kind(kind, [&](auto k) {
-            constexpr int K = decltype(k)::value;
-#pragma unroll
-            for (int j = RUN - 1; j >= 0; --j) {
-                float d[V];
-                get<ADJ>(hr(j), l, d);
-                if constexpr (K == ANY)
-                    if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, B);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) B[v] = j + 1 == place ? df[v] : B[v];
-                    B[v] = a[j][v] * (d[v] + B[v]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                if constexpr (K == ANY)
-                    if (b.starts >> j & 1) seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, F);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) F[v] = j == place ? h0[v] : F[v];
-                    P[v] *= a[j][v];
-                    F[v] = fmaf(a[j][v], F[v], u[j][v]);
-                }
-            }
-        });
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            sm.s.map[run][chan<ADJ>(l, v)] = make_float2(ends ? -1.f : P[v], B[v]);
-            sm.fmap[run][chan<ADJ>(l, v)] = make_float2(b.starts ? -1.f : P[v], F[v]);
-        }
-        __syncthreads();
-        // While the tile's map travels: the states before each token, in place of the tokens' own terms.
-        auto meanwhile = [&] {
-            release();
-            if (warp == WARPS - 1) {
-#pragma unroll
-                for (int r = 0; r < RUNS; ++r) {
-                    sm.fstate[r][lane] = f0;
-                    f0 = apply(sm.fmap[r][lane], f0);
-                }
-            }
-            __syncthreads();
-            float f[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = sm.fstate[run][chan<ADJ>(l, v)];
-            by_kind(kind, [&](auto k) {
-                constexpr int K = decltype(k)::value;
-#pragma unroll
-                for (int j = 0; j < RUN; ++j) {
-                    if constexpr (K == ANY)
-                        if (b.starts >> j & 1) seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if constexpr (K == ONE) f[v] = j == place ? h0[v] : f[v];
-                        const float next = fmaf(a[j][v], f[v], u[j][v]);
-                        u[j][v] = f[v];
-                        f[v] = next;
-                    }
-                }
-            });
-        };
-        if (!incoming<CHAIN, true>(sm.s, ch, t.rt, t.col0, t.tt == 0, meanwhile)) return false;
-        float e[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = sm.s.state[run][chan<ADJ>(l, v)];
-        const int64_t last = static_cast<int64_t>(t.t0) + run * RUN + RUN - 1;
-        const int c0 = t.col0 + chan<ADJ>(l, 0);
-        E *px = dx + last * out.lddx + c0, *pi = di ? di + last * out.lddi + c0 : nullptr;
-        float *pg = out.dg + last * out.lddg + c0;
-        by_kind(kind, [&](auto k) {
-            constexpr int K = decltype(k)::value;
-            float *first = nullptr;
-            if constexpr (K == ONE)
-                if (out.dh0 && b.starts) first = out.dh0 + static_cast<int64_t>(b.first) * D + t.col0;
-#pragma unroll
-            for (int j = RUN - 1; j >= 0; --j) {
-                float Gr[V], gx[V], gi[V], gg[V];
-                get<ADJ>(hr(j), l, Gr);
-                get<ADJ>(xr(j), l, gi);
-                if constexpr (K == ANY)
-                    if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, e);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) e[v] = j + 1 == place ? df[v] : e[v];
-                    Gr[v] += e[v];
-                    e[v] = a[j][v] * Gr[v];
-                    gi[v] *= Gr[v];
-                    gg[v] = u[j][v] * e[v];
-                    gx[v] = Gr[v];
-                }
-                if (ig) {
-                    get<ADJ>(ir(j), l, gx);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) gx[v] *= Gr[v];
-                }
-                if constexpr (K == ANY) {
-                    if (j < rows) {
-                        put<ADJ>(px - chan<ADJ>(l, 0), l, gx, left);
-                        if (di) put<ADJ>(pi - chan<ADJ>(l, 0), l, gi, left);
-                        put<ADJ>(pg - chan<ADJ>(l, 0), l, gg, left);
-                    }
-                    if ((b.starts >> j & 1) && out.dh0) put<ADJ>(out.dh0 + b.seq(j) * D + t.col0, l, e, left);
-                } else {
-                    put_all<ADJ>(px, gx);
-                    if (di) put_all<ADJ>(pi, gi);
-                    put_all<ADJ>(pg, gg);
-                    if constexpr (K == ONE)
-                        if (first && j == place) {
-                            first[chan<ADJ>(l, 0)] = e[0];
-                            first[chan<ADJ>(l, 1)] = e[1];
-                        }
-                }
-                px -= out.lddx;
-                pi -= out.lddi;
-                pg -= out.lddg;
-            }
-        });
-        __syncthreads();
-        return true;
-    };
-    walk<CHAIN, true>(sm.s, ch, pv, D, load, work);
-}
-
 // ---- one token --------------------------------------------------------------------------------------------
 
 // One token per row, each the next one of its slot's state (updated in place).
@@ -950,78 +155,6 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int D, const in
     }
 }
 
-// ---- launches ---------------------------------------------------------------------------------------------
-
-template <typename F> cudaError_t by_type(int type, F f)
-{
-    if (type == KDA_TYPE_F32) return f(float{});
-    if (type == KDA_TYPE_F16) return f(__half{});
-    return f(__nv_bfloat16{});
-}
-
-// How a tensor's rows lie: all on 16 bytes, all on pairs of elements.
-struct Lie {
-    bool wide = true, even = true;
-    Lie &with(const void *p, int64_t ld, int bytes)
-    {
-        if (!p) return *this;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * bytes);
-        wide = wide && (at & 15) == 0;
-        even = even && (at & (2 * bytes - 1)) == 0;
-        return *this;
-    }
-};
-// Calls f(copies with an offset, channels in pairs) for how the rows lie.
-template <typename F> cudaError_t by_lie(const Lie &lie, F f)
-{
-    if (lie.wide) return f(std::false_type{}, std::true_type{});
-    if (lie.even) return f(std::true_type{}, std::true_type{});
-    return f(std::true_type{}, std::false_type{});
-}
-
-// Runs a tile kernel in the form that the number of tiles asks for.  cluster / chain: the two instances.
-template <typename K, typename... Args>
-cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host, const int32_t *plan_dev, int D, void *ws, cudaStream_t stream,
-                const ScanIn &in, Args... args)
-{
-    const int T = plan_host[KDA_PH_T], nT = tiles_of(T), nC = (D + C - 1) / C;
-    const PlanSig sig = plan_sig(plan_host);
-    K fn = nT <= MAX_CLUSTER ? cluster : chain;
-    if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), smem)) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    Chain ch = {};
-    if (nT <= MAX_CLUSTER) {
-        int cs = 1;
-        while (cs < nT) cs *= 2;
-        cfg.gridDim = dim3(static_cast<unsigned>(nC) * cs);
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cs;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    } else {
-        ch = chain_of(ws, T, D);
-        // A short group folds fewer maps a tile; a long one passes the state on less often, which is what bounds narrow
-        // inputs.
-        ch.group = nC >= 64 ? SHORT_GROUP : GROUP;
-        const Layout l = layout_of(T, D);
-        const size_t words = (l.end - l.state) / 16;
-        const size_t want = (words + 4 * 256 - 1) / (4 * 256), most = 4 * static_cast<size_t>(sm_count());
-        const int64_t tiles = static_cast<int64_t>(nT) * nC, all = static_cast<int64_t>(ctas) * sm_count();
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles < all ? tiles : all));
-        chain_init<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
-            plan_dev, sig, nT, static_cast<int>(cfg.gridDim.x), ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
-        if (cudaError_t e = cudaGetLastError()) return e;
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, fn, plan_dev, sig, D, in, ch, args...);
-}
-
 }  // namespace
 
 size_t scan_workspace_bytes(int64_t T, int D) { return T <= MAX_CLUSTER * L ? 0 : layout_of(T, D).end; }
@@ -1036,22 +169,6 @@ cudaError_t launch_scan_forward(const int32_t *plan_host, const int32_t *plan_de
             using Sh = ForwardShared<E, SH>;
             return run(scan_forward<E, SH, ADJ, false>, scan_forward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
                        plan_dev, D, ws, stream, in, h, ldh, final_state, states);
-        });
-    });
-}
-
-cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_dev, int D, int type, const ScanIn &in,
-                                 const float *states, const void *dh, int64_t lddh, const float *dfinal,
-                                 const ScanGrads &out, void *ws, cudaStream_t stream)
-{
-    return by_type(type, [&](auto ev) {
-        using E = decltype(ev);
-        const Lie lie = Lie().with(in.x, in.ldx, sizeof(E)).with(in.i, in.ldi, sizeof(E)).with(in.g, in.ldg, 4).with(dh, lddh, sizeof(E));
-        return by_lie(lie, [&](auto shift, auto adj) {
-            constexpr bool SH = decltype(shift)::value, ADJ = decltype(adj)::value;
-            using Sh = BackwardShared<E, SH>;
-            return run(scan_backward<E, SH, ADJ, false>, scan_backward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
-                       plan_dev, D, ws, stream, in, states, dh, lddh, dfinal, out);
         });
     });
 }

@@ -235,6 +235,7 @@ cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_d
 cudaError_t launch_scan_step(int B, int D, int type, const int32_t *slots, int num_slots, const ScanIn &in,
                              float *state, void *h, int64_t ldh, cudaStream_t stream);
 int take_scan_status();
+int take_scan_backward_status();
 
 struct NormIn {
     const void *r, *o, *z;            // residual (the forward's input, the backward's r'), branch, gate logits
