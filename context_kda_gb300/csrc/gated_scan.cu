@@ -130,28 +130,57 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
 
 // ---- one token --------------------------------------------------------------------------------------------
 
-// One token per row, each the next one of its slot's state (updated in place).
+// One token per row, each the next one of its slot's state (updated in place).  N channels a thread: four where all rows
+// start on four elements and D is a multiple of four, one otherwise; bound by memory (2048 x 4096 in bf16: see the
+// launch), or by the launch.
 constexpr int STEP_THREADS = 128;
-template <typename E>
+template <typename X> __device__ __forceinline__ void get_n(const X *p, float (&v)[1]) { v[0] = to_f32(*p); }
+__device__ __forceinline__ void get_n(const float *p, float (&v)[4])
+{
+    const float4 q = *reinterpret_cast<const float4 *>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+}
+template <typename X> __device__ __forceinline__ void get_n(const X *p, float (&v)[4])
+{
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    float w[2];
+    unpack(q.x, w, p);
+    v[0] = w[0], v[1] = w[1];
+    unpack(q.y, w, p);
+    v[2] = w[0], v[3] = w[1];
+}
+template <typename X> __device__ __forceinline__ void put_n(X *p, const float (&v)[1]) { *p = from_f32<X>(v[0]); }
+__device__ __forceinline__ void put_n(float *p, const float (&v)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+template <typename X> __device__ __forceinline__ void put_n(X *p, const float (&v)[4])
+{
+    X e[4] = {from_f32<X>(v[0]), from_f32<X>(v[1]), from_f32<X>(v[2]), from_f32<X>(v[3])};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
+}
+template <typename E, int N>
 __global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int D, const int32_t *slots, int num_slots, ScanIn in,
                                                           float *state, void *h_, int64_t ldh)
 {
-    const int d = blockIdx.x * STEP_THREADS + threadIdx.x;
+    const int d = (blockIdx.x * STEP_THREADS + threadIdx.x) * N;
     if (d >= D) return;
     for (int64_t b = blockIdx.y; b < B; b += gridDim.y) {
+        // the row's inputs are requested along with its slot, not after it
+        float g[N], u[N], i[N];
+        get_n(in.g + b * in.ldg + d, g);
+        get_n(static_cast<const E *>(in.x) + b * in.ldx + d, u);
+        if (in.i) get_n(static_cast<const E *>(in.i) + b * in.ldi + d, i);
         const int slot = slots ? slots[b] : static_cast<int>(b);
-        E *h = static_cast<E *>(h_) + b * ldh + d;
-        if (slot < 0 || slot >= num_slots) {
-            *h = from_f32<E>(0.f);
-            if (slot >= num_slots && d == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
-            continue;
+        const bool live = slot >= 0 && slot < num_slots;
+        float s[N] = {};
+        if (live) {
+            float *at = state + static_cast<int64_t>(slot) * D + d;
+            get_n(at, s);
+#pragma unroll
+            for (int j = 0; j < N; ++j) s[j] = fmaf(decay(g[j]), s[j], in.i ? u[j] * i[j] : u[j]);
+            put_n(at, s);
+        } else if (slot >= num_slots && d == 0) {
+            record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         }
-        const float x = to_f32(static_cast<const E *>(in.x)[b * in.ldx + d]);
-        const float u = in.i ? x * to_f32(static_cast<const E *>(in.i)[b * in.ldi + d]) : x;
-        float *s = state + static_cast<int64_t>(slot) * D + d;
-        const float v = fmaf(expf(in.g[b * in.ldg + d]), *s, u);
-        *s = v;
-        *h = from_f32<E>(v);
+        put_n(static_cast<E *>(h_) + b * ldh + d, s);
     }
 }
 
@@ -176,9 +205,17 @@ cudaError_t launch_scan_forward(const int32_t *plan_host, const int32_t *plan_de
 cudaError_t launch_scan_step(int B, int D, int type, const int32_t *slots, int num_slots, const ScanIn &in,
                              float *state, void *h, int64_t ldh, cudaStream_t stream)
 {
-    const dim3 grid((D + STEP_THREADS - 1) / STEP_THREADS, B < 65535 ? B : 65535);
-    return by_type(type, [&](auto e) {
-        scan_step<decltype(e)><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
+    return by_type(type, [&](auto ev) {
+        using E = decltype(ev);
+        auto on_four = [](const void *p, int64_t ld, uintptr_t bytes) {
+            return !p || ((reinterpret_cast<uintptr_t>(p) & (4 * bytes - 1)) == 0 && (ld & 3) == 0);
+        };
+        const bool four = D % 4 == 0 && on_four(in.x, in.ldx, sizeof(E)) && on_four(in.i, in.ldi, sizeof(E)) && on_four(in.g, in.ldg, 4) &&
+                          on_four(state, 0, 4) && on_four(h, ldh, sizeof(E));
+        const int n = four ? 4 : 1;
+        const dim3 grid((D + STEP_THREADS * n - 1) / (STEP_THREADS * n), B < 65535 ? B : 65535);
+        if (four) scan_step<E, 4><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
+        else scan_step<E, 1><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
         return cudaGetLastError();
     });
 }
