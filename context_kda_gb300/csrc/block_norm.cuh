@@ -12,8 +12,8 @@
 //
 // A CTA of BLOCK threads takes R rows at a time (NT threads a row, 8 NC channels a thread) and walks over
 // all its rows, which are copied to a ring in shared memory (cp.async) one to three steps ahead.  Sums over a row take
-// one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 where rows
-// start on 16 bytes (a thread copies what it reads itself, without a barrier), 1 otherwise.
+// one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
+// residual is fp32) where rows start on 16 bytes (a thread copies what it reads itself, without a barrier), 1 otherwise.
 // FULL instances are for the usual call: every part but the gate is there, D is a multiple of 8 and all rows start on
 // 16 bytes.  They decide nothing about that per row (a third of the instructions of the others, which bound
 // them: 16384 x 2048 gradients in bf16 115 us without, see below with).
@@ -47,9 +47,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, int bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void unpack(uint32_t w, float *v, const __nv_bfloat16 *)
 {
@@ -64,37 +64,44 @@ __device__ __forceinline__ void unpack(uint32_t w, float *v, const __half *)
 }
 __device__ __forceinline__ void unpack(uint32_t w, float *v, const float *) { v[0] = __uint_as_float(w); }
 
-// A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.
-template <typename X, int BLOCK, int NC, int U> struct Row;
-
-// U = 8: rows start on 16 bytes; every thread copies its own channels into its own slots.
-template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 8> {
-    static constexpr int NE = 8 * NC, PIECES = static_cast<int>(sizeof(X)) / 2, EPP = 8 / PIECES;   // 16-byte pieces of a run
-    static constexpr int BYTES = NE * static_cast<int>(sizeof(X)) * BLOCK;                           // of the CTA, per step
+// A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.  U = 8, or 4 where the
+// residual is fp32: rows start on 16 bytes; every thread copies its own channels into its own slots.  A run is one
+// copy, so that a warp's copies and stores are adjacent bytes: with 8 channels of fp32 a thread, in two pieces each,
+// every sector moved twice (16384 x 2048 in fp32: 157 us, 109 us with 4).
+template <typename X, int BLOCK, int NC, int U> struct Row {
+    static constexpr int NE = 8 * NC, NU = NE / U, RUN = U * static_cast<int>(sizeof(X));     // runs, bytes of a run
+    static constexpr int BYTES = NE * static_cast<int>(sizeof(X)) * BLOCK;                    // of the CTA, per step
+    static_assert(RUN == 16 || RUN == 8, "one copy a run");
+    static __device__ __forceinline__ void copy(uint32_t dst, const X *src, int bytes)
+    {
+        if constexpr (RUN == 16) copy16(dst, src, bytes);
+        else copy8(dst, src, bytes);
+    }
 
     // Copies the row's channels below D to the slots at 'base'; 'row' is the row's first channel.
     static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *, int ti, int NT, int D)
     {
 #pragma unroll
-        for (int q = 0; q < NC; ++q)
-#pragma unroll
-            for (int p = 0; p < PIECES; ++p) {
-                const int c = (ti + q * NT) * 8 + p * EPP, left = (D - c) * static_cast<int>(sizeof(X));
-                const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-                copy16(base + ((q * PIECES + p) * BLOCK + threadIdx.x) * 16, bytes ? row + c : row, bytes);
-            }
+        for (int q = 0; q < NU; ++q) {
+            const int c = (ti + q * NT) * U, left = (D - c) * static_cast<int>(sizeof(X));
+            const int bytes = left < 0 ? 0 : left > RUN ? RUN : left;
+            copy(base + (q * BLOCK + threadIdx.x) * RUN, bytes ? row + c : row, bytes);
+        }
     }
-    // The same where the thread's channels all exist.
-    static __device__ __forceinline__ void fetch_all(uint32_t base, const X *row, int ti)
+    // The same where D is a multiple of 8 (zeros from D on).
+    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, int ti, int NT, int D)
     {
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) copy16(base + (p * BLOCK + threadIdx.x) * 16, row + ti * 8 + p * EPP);
+        for (int q = 0; q < NU; ++q) {
+            const bool there = (ti + q * NT) * U < D;
+            copy(base + (q * BLOCK + threadIdx.x) * RUN, there ? row + (ti + q * NT) * U : row, there ? RUN : 0);
+        }
     }
     // Zeros in place of a row past the end ('any': some address of the tensor).
     static __device__ __forceinline__ void fetch_none(uint32_t base, const X *any)
     {
 #pragma unroll
-        for (int j = 0; j < NC * PIECES; ++j) copy16(base + (j * BLOCK + threadIdx.x) * 16, any, 0);
+        for (int q = 0; q < NU; ++q) copy(base + (q * BLOCK + threadIdx.x) * RUN, any, 0);
     }
     // The channels as fp32 (zeros from D on): from the slots, or from the row where there is no ring.
     template <bool RING>
@@ -103,46 +110,45 @@ template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 8> {
         if constexpr (RING) {
             constexpr int EPW = 4 / static_cast<int>(sizeof(X));
 #pragma unroll
-            for (int j = 0; j < NC * PIECES; ++j) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(base + (j * BLOCK + threadIdx.x) * 16);
-                unpack(w.x, v + j * EPP, row);
-                unpack(w.y, v + j * EPP + EPW, row);
-                unpack(w.z, v + j * EPP + 2 * EPW, row);
-                unpack(w.w, v + j * EPP + 3 * EPW, row);
+            for (int q = 0; q < NU; ++q) {
+                const unsigned char *at = base + (q * BLOCK + threadIdx.x) * RUN;
+                if constexpr (RUN == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(at);
+                    unpack(w.x, v + q * U, row);
+                    unpack(w.y, v + q * U + EPW, row);
+                    unpack(w.z, v + q * U + 2 * EPW, row);
+                    unpack(w.w, v + q * U + 3 * EPW, row);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(at);
+                    unpack(w.x, v + q * U, row);
+                    unpack(w.y, v + q * U + EPW, row);
+                }
             }
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                const int c = (ti + j / 8 * NT) * 8 + j % 8;
+                const int c = (ti + j / U * NT) * U + j % U;
                 v[j] = in && c < D ? to_f32(row[c]) : 0.f;
             }
         }
     }
-    // A thread's eight channels from 'at' on, aligned.
-    static __device__ __forceinline__ void write_all(X *at, const float (&v)[NE])
-    {
-        X e[NE];
-#pragma unroll
-        for (int j = 0; j < NE; ++j) e[j] = from_f32<X>(v[j]);
-#pragma unroll
-        for (int p = 0; p < NC * PIECES; ++p) reinterpret_cast<uint4 *>(at)[p] = reinterpret_cast<const uint4 *>(e)[p];
-    }
-    static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool wide, const float (&v)[NE])
+    // The channels below D; FULL: D is a multiple of 8 and the row starts on 16 bytes (else as 'wide' says).
+    template <bool FULL> static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool wide, const float (&v)[NE])
     {
 #pragma unroll
-        for (int q = 0; q < NC; ++q) {
-            const int c = (ti + q * NT) * 8;
-            X e[8];
+        for (int q = 0; q < NU; ++q) {
+            const int c = (ti + q * NT) * U;
+            X e[U];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = from_f32<X>(v[q * 8 + j]);
-            if (wide && c + 8 <= D) {
+            for (int j = 0; j < U; ++j) e[j] = from_f32<X>(v[q * U + j]);
+            if (FULL ? c < D : wide && c + U <= D) {
+                if constexpr (RUN == 16) *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(e);
+                else *reinterpret_cast<uint2 *>(row + c) = *reinterpret_cast<const uint2 *>(e);
+            } else if (!FULL) {
 #pragma unroll
-                for (int p = 0; p < PIECES; ++p) reinterpret_cast<uint4 *>(row + c)[p] = reinterpret_cast<const uint4 *>(e)[p];
-                continue;
+                for (int j = 0; j < U; ++j)
+                    if (c + j < D) row[c + j] = e[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < D) row[c + j] = e[j];
         }
     }
 };
@@ -191,7 +197,7 @@ template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
             v[j] = c < some ? to_f32(p[c]) : 0.f;
         }
     }
-    static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool, const float (&v)[NE])
+    template <bool> static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool, const float (&v)[NE])
     {
 #pragma unroll
         for (int j = 0; j < NE; ++j)
@@ -250,15 +256,16 @@ template <int BLOCK> struct Sums {
     }
 };
 
-// Row t of a tensor of rows 'ld' bytes apart, at the channels from 'first' on.
-template <typename X> __device__ __forceinline__ X *row_at(X *p, uint32_t t, uint32_t ld, int first)
+// Row t of a tensor of rows 'ld' bytes apart.
+template <typename X> __device__ __forceinline__ X *row_at(X *p, uint32_t t, uint32_t ld)
 {
     using Byte = typename std::conditional<std::is_const<X>::value, const char, char>::type;
-    return reinterpret_cast<X *>(reinterpret_cast<Byte *>(p + first) + static_cast<uint64_t>(t) * ld);
+    return reinterpret_cast<X *>(reinterpret_cast<Byte *>(p) + static_cast<uint64_t>(t) * ld);
 }
 
 // Sums over each run's group of G channels (G < D), in place.  G spans G / U lanes of consecutive threads,
-// which may be several warps when runs are short (NT U is then at least G).
+// which may be several warps when runs are short (NT U is then at least G; buffers in turn as above, so an object serves one
+// sum a row).
 template <int BLOCK, int NU, int U> struct GroupSums {
     float part[U < 8 ? 2 : 1][U < 8 ? NU : 1][BLOCK / 32];
     static __device__ __forceinline__ void fold(float (&v)[NU], int m)
@@ -347,20 +354,17 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     const uint32_t base = tc::smem_u32(ring);
     const bool has_r = FULL || r, has_o = FULL || o, has_post = FULL || a.w_post, has_out = FULL || r_out, has_y = FULL || y;
 
-    // channels past D are not read: the row's first address stands in for theirs
-    const bool active = ti * U < D;
-    const int first = active ? ti * U : 0;
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * F::STEP;
-        if (t < s.T && (!FULL || active)) {
+        if (t < s.T) {
             if constexpr (FULL) {
-                RowR::fetch_all(b, row_at(r, t, lr, 0), ti);
-                RowE::fetch_all(b + RowR::BYTES, row_at(o, t, lo, 0), ti);
-                if (z) RowE::fetch_all(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), ti);
+                RowR::fetch_full(b, row_at(r, t, lr), ti, NT, D);
+                RowE::fetch_full(b + RowR::BYTES, row_at(o, t, lo), ti, NT, D);
+                if (z) RowE::fetch_full(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), ti, NT, D);
             } else {
-                if (r) RowR::fetch(b, row_at(r, t, lr, 0), r, ti, NT, D);
-                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo, 0), o, ti, NT, D);
-                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), z, ti, NT, D);
+                if (r) RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
+                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D);
+                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D);
             }
         } else {
             if (has_r) RowR::fetch_none(b, r);
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
         };
-        if constexpr (S > 0 && U == 8) {
+        if constexpr (S > 0 && U > 1) {
             ahead();
             cp_wait<S - 1>();
         } else if constexpr (S > 0) {
@@ -410,16 +414,16 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
         const unsigned char *b = ring + slot * F::STEP;
         float v[NE];
         if (has_r) {
-            RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, v);
+            RowR::template read<(S > 0)>(b, row_at(r, t, lr), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
         }
         if (has_o) {
             float n[NE];
-            RowE::template read<(S > 0)>(b + RowR::BYTES, row_at(o, t, lo, 0), ti, NT, D, in, n);
+            RowE::template read<(S > 0)>(b + RowR::BYTES, row_at(o, t, lo), ti, NT, D, in, n);
             float g[NE];
-            if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz, 0), ti, NT, D, in, g);
+            if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), ti, NT, D, in, g);
             if (has_post) {
                 float ss[NU];
 #pragma unroll
@@ -456,11 +460,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = fmaf(wl[j], n[j], v[j]);
         }
-        if constexpr (FULL) {
-            if (in && active) RowR::write_all(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), first), v);
-        } else {
-            if (r_out && in) RowR::write(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
-        }
+        if (has_out && in) RowR::template write<FULL>(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R))), ti, NT, D, s.wide_r, v);
         if (has_y) {
             float ss = 0.f;
 #pragma unroll
@@ -469,11 +469,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
-            if constexpr (FULL) {
-                if (in && active) RowE::write_all(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), first), v);
-            } else {
-                if (in) RowE::write(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
-            }
+            if (in) RowE::template write<FULL>(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E))), ti, NT, D, s.wide_a, v);
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -505,7 +501,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     constexpr int NE = B::NE, NU = B::NU, S = B::S;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ Sums<BLOCK> sums, sums_o, sums_e;
-    __shared__ GroupSums<BLOCK, NU, U> groups;
+    __shared__ GroupSums<BLOCK, NU, U> groups_o, groups_e;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
     R *dr = static_cast<R *>(g.dr);
@@ -519,25 +515,23 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     constexpr int O_DRO = RowR::BYTES, O_DY = 2 * RowR::BYTES, O_O = O_DY + RowE::BYTES, O_Z = O_O + RowE::BYTES;
     const bool has_pre = FULL || a.w_pre, has_dro = FULL || dro, has_o = FULL || o, has_post = FULL || a.w_post;
 
-    const bool active = ti * U < D;
-    const int first = active ? ti * U : 0;
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * B::STEP;
-        if (t < s.T && (!FULL || active)) {
+        if (t < s.T) {
             if constexpr (FULL) {
-                RowR::fetch_all(b, row_at(r, t, lr, 0), ti);
-                RowE::fetch_all(b + O_DY, row_at(dy, t, ldy, 0), ti);
-                RowR::fetch_all(b + O_DRO, row_at(dro, t, ldr, 0), ti);
-                RowE::fetch_all(b + O_O, row_at(o, t, lo, 0), ti);
-                if (z) RowE::fetch_all(b + O_Z, row_at(z, t, lz, 0), ti);
+                RowR::fetch_full(b, row_at(r, t, lr), ti, NT, D);
+                RowE::fetch_full(b + O_DY, row_at(dy, t, ldy), ti, NT, D);
+                RowR::fetch_full(b + O_DRO, row_at(dro, t, ldr), ti, NT, D);
+                RowE::fetch_full(b + O_O, row_at(o, t, lo), ti, NT, D);
+                if (z) RowE::fetch_full(b + O_Z, row_at(z, t, lz), ti, NT, D);
             } else {
                 if (a.w_pre) {
-                    RowR::fetch(b, row_at(r, t, lr, 0), r, ti, NT, D);
-                    RowE::fetch(b + O_DY, row_at(dy, t, ldy, 0), dy, ti, NT, D);
+                    RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
+                    RowE::fetch(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D);
                 }
-                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr, 0), dro, ti, NT, D);
-                if (o) RowE::fetch(b + O_O, row_at(o, t, lo, 0), o, ti, NT, D);
-                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz, 0), z, ti, NT, D);
+                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D);
+                if (o) RowE::fetch(b + O_O, row_at(o, t, lo), o, ti, NT, D);
+                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz), z, ti, NT, D);
             }
         } else {
             if (has_pre) {
@@ -574,7 +568,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
         };
-        if constexpr (S > 0 && U == 8) {
+        if constexpr (S > 0 && U > 1) {
             ahead();
             cp_wait<S - 1>();
         } else if constexpr (S > 0) {
@@ -588,8 +582,8 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         float ss = 0.f, ev_r = 0.f;             // sums of r^2 and of e r over the row
         float so[NU];                           // of o^2 over the groups
         if (has_pre) {
-            RowR::template read<(S > 0)>(b, row_at(r, t, lr, 0), ti, NT, D, in, rv);
-            RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy, 0), ti, NT, D, in, e);
+            RowR::template read<(S > 0)>(b, row_at(r, t, lr), ti, NT, D, in, rv);
+            RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy), ti, NT, D, in, e);
             if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
@@ -598,7 +592,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             }
         }
         if (has_o) {
-            RowE::template read<(S > 0)>(b + O_O, row_at(o, t, lo, 0), ti, NT, D, in, ov);
+            RowE::template read<(S > 0)>(b + O_O, row_at(o, t, lo), ti, NT, D, in, ov);
             if (has_post) {
                 float all = 0.f;
 #pragma unroll
@@ -613,13 +607,13 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 #pragma unroll
                     for (int q = 0; q < NU; ++q) so[q] = all;
                 } else {
-                    groups.over_group(so, G, turn);
+                    groups_o.over_group(so, G, turn);
                 }
             }
         }
         float v[NE];                            // the gradient of r', then that of o
         if (has_dro) {
-            RowR::template read<(S > 0)>(b + O_DRO, row_at(dro, t, ldr, 0), ti, NT, D, in, v);
+            RowR::template read<(S > 0)>(b + O_DRO, row_at(dro, t, ldr), ti, NT, D, in, v);
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] = 0.f;
@@ -639,13 +633,10 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 }
             }
         }
-        if (dr && in && (!FULL || active)) {
-                if constexpr (FULL) RowR::write_all(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), first), v);
-                else RowR::write(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R)), 0), ti, NT, D, s.wide_r, v);
-            }
+        if (dr && in) RowR::template write<FULL>(row_at(dr, t, static_cast<uint32_t>(g.lddr * sizeof(R))), ti, NT, D, s.wide_r, v);
         if (has_o) {
             float gz[NE];
-            if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz, 0), ti, NT, D, in, gz);
+            if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz), ti, NT, D, in, gz);
             if constexpr (NC > 1) {
                 weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
                 weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
@@ -682,10 +673,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 #pragma unroll
                 for (int j = 0; j < NE; ++j) channel(j, v[j], 0.f);
             }
-            if (dz && in && (!FULL || active)) {
-                if constexpr (FULL) RowE::write_all(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), first), gz);
-                else RowE::write(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E)), 0), ti, NT, D, s.wide_b, gz);
-            }
+            if (dz && in) RowE::template write<FULL>(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E))), ti, NT, D, s.wide_b, gz);
             if (has_post) {
                 if (G == D) {
                     float all = 0.f;
@@ -695,7 +683,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 #pragma unroll
                     for (int q = 0; q < NU; ++q) ev[q] = all;
                 } else {
-                    groups.over_group(ev, G, turn + 1);
+                    groups_e.over_group(ev, G, turn);
                 }
                 if (!FULL && G == 1) {
                     v[0] = unit_grad_of_one(v[0], inv[0], a.eps);
@@ -704,10 +692,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                     for (int j = 0; j < NE; ++j) v[j] = inv[j / U] * fmaf(-ov[j], ev[j / U] * inv_g, v[j]);
                 }
             }
-            if (in && (!FULL || active)) {
-                if constexpr (FULL) RowE::write_all(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), first), v);
-                else RowE::write(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E)), 0), ti, NT, D, s.wide_a, v);
-            }
+            if (in) RowE::template write<FULL>(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E))), ti, NT, D, s.wide_a, v);
         }
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
@@ -774,7 +759,11 @@ cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, voi
     s.NT = threads_of_row(s.D, s.G, NC, U);
     auto fn = forward<R, E, BLOCK, NC, U, FULL>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), F::SMEM)) return e;
-    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = F::CTAS * sm_count();
+    // With one barrier a row, fewer CTAs read and write the rows more nearly in order and are faster (16384 x 4096 with a
+    // residual in fp32: 164 us on one CTA of 512 threads an SM, 177 us on two); with two barriers a row the second CTA
+    // is needed to fill the waits (all in bf16: 86 us on two, 109 us on one).
+    const int ctas = F::CTAS > 1 && !(a.w_post && s.G == s.D) ? F::CTAS / 2 : F::CTAS;
+    const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, most = static_cast<int64_t>(ctas) * sm_count();
     fn<<<static_cast<unsigned>(want < most ? want : most), BLOCK, F::SMEM, stream>>>(s, a, static_cast<R *>(r_out), ldro,
                                                                                       static_cast<E *>(y), ldy);
     return cudaGetLastError();
@@ -802,6 +791,9 @@ cudaError_t run_backward(Shape s, const NormIn &a, const void *dro, int64_t lddr
      : s.D <= 8192 ? FN<R, E, 512, 2, U>(__VA_ARGS__)  \
                    : FN<R, E, 1024, 2, U>(__VA_ARGS__))
 
+// Channels of a run where rows start on 16 bytes.
+template <typename R> constexpr int WIDE = sizeof(R) == 4 ? 4 : 8;
+
 template <typename R, typename E>
 cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
 {
@@ -810,9 +802,9 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
         s.wide_r = rows_on(r_out, ldro, re);
         s.wide_a = rows_on(y, ldy, e);
         if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 4096)
-            return s.D <= 2048 ? run_forward<R, E, 256, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream)
-                               : run_forward<R, E, 512, 1, 8, true>(s, a, r_out, ldro, y, ldy, stream);
-        return KDA_NORM_PICK(run_forward, R, E, 8, s, a, r_out, ldro, y, ldy, stream);
+            return s.D <= 2048 ? run_forward<R, E, 256, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
+                               : run_forward<R, E, 512, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream);
+        return KDA_NORM_PICK(run_forward, R, E, WIDE<R>, s, a, r_out, ldro, y, ldy, stream);
     }
     return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
 }
@@ -828,9 +820,9 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
         s.wide_a = rows_on(g.d_o, g.lddo, e);
         s.wide_b = rows_on(g.dz, g.lddz, e);
         if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 4096)
-            return s.D <= 2048 ? run_backward<R, E, 256, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
-                               : run_backward<R, E, 512, 1, 8, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
-        return KDA_NORM_PICK(run_backward, R, E, 8, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+            return s.D <= 2048 ? run_backward<R, E, 256, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                               : run_backward<R, E, 512, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+        return KDA_NORM_PICK(run_backward, R, E, WIDE<R>, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
     return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
 }
