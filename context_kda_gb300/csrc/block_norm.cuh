@@ -14,9 +14,9 @@
 // all its rows, which are copied to a ring in shared memory (cp.async) one to three steps ahead.  Sums over a row take
 // one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
 // residual is fp32) where rows start on 16 bytes (a thread copies what it reads itself, without a barrier), 1 otherwise.
-// FULL instances are for the usual call: every part but the gate is there, D is a multiple of 8 and all rows start on
-// 16 bytes.  They decide nothing about that per row (a third of the instructions of the others, which bound
-// them: 16384 x 2048 gradients in bf16 115 us without, see below with).
+// FULL instances are for the usual call: every part but the gate is there and, unless U = 1, D is a multiple of 8 and
+// outputs lie as inputs do.  They decide nothing about that per row, which is a third of the instructions of the
+// others and bounds them (16384 x 2048 gradients in bf16: 115 us, 95 us with FULL).
 // Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 #pragma once
@@ -89,7 +89,7 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
         }
     }
     // The same where D is a multiple of 8 (zeros from D on).
-    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, int ti, int NT, int D)
+    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *, int ti, int NT, int D)
     {
 #pragma unroll
         for (int q = 0; q < NU; ++q) {
@@ -184,6 +184,10 @@ template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(to_f32(v)) : "memory");
         else
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const unsigned short *>(&v)) : "memory");
+    }
+    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D)
+    {
+        fetch(base, row, tensor, ti, NT, D);
     }
     static __device__ __forceinline__ void fetch_none(uint32_t, const X *) {}
     template <bool RING>
@@ -358,9 +362,9 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
         const uint32_t b = base + slot * F::STEP;
         if (t < s.T) {
             if constexpr (FULL) {
-                RowR::fetch_full(b, row_at(r, t, lr), ti, NT, D);
-                RowE::fetch_full(b + RowR::BYTES, row_at(o, t, lo), ti, NT, D);
-                if (z) RowE::fetch_full(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), ti, NT, D);
+                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D);
+                RowE::fetch_full(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D);
+                if (z) RowE::fetch_full(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D);
             } else {
                 if (r) RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
                 if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D);
@@ -519,11 +523,11 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         const uint32_t b = base + slot * B::STEP;
         if (t < s.T) {
             if constexpr (FULL) {
-                RowR::fetch_full(b, row_at(r, t, lr), ti, NT, D);
-                RowE::fetch_full(b + O_DY, row_at(dy, t, ldy), ti, NT, D);
-                RowR::fetch_full(b + O_DRO, row_at(dro, t, ldr), ti, NT, D);
-                RowE::fetch_full(b + O_O, row_at(o, t, lo), ti, NT, D);
-                if (z) RowE::fetch_full(b + O_Z, row_at(z, t, lz), ti, NT, D);
+                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D);
+                RowE::fetch_full(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D);
+                RowR::fetch_full(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D);
+                RowE::fetch_full(b + O_O, row_at(o, t, lo), o, ti, NT, D);
+                if (z) RowE::fetch_full(b + O_Z, row_at(z, t, lz), z, ti, NT, D);
             } else {
                 if (a.w_pre) {
                     RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         if (has_pre) {
             sums.over_row(ss, ev_r, NT, turn);
             const float inv = in ? inv_rms(ss * inv_d, a.eps) : 0.f, mean = ev_r * inv_d * inv;   // no row: zeros, also with eps = 0
-            if (!FULL && D == 1) {
+            if ((!FULL || U == 1) && D == 1) {
                 v[0] += unit_grad_of_one(e[0] * wr[0], inv, a.eps);
                 acc_r[0] = fmaf(e[0], rv[0] * inv, acc_r[0]);
             } else {
@@ -685,7 +689,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 } else {
                     groups_e.over_group(ev, G, turn);
                 }
-                if (!FULL && G == 1) {
+                if ((!FULL || U == 1) && G == 1) {
                     v[0] = unit_grad_of_one(v[0], inv[0], a.eps);
                 } else {
 #pragma unroll
@@ -806,6 +810,9 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
                                : run_forward<R, E, 512, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream);
         return KDA_NORM_PICK(run_forward, R, E, WIDE<R>, s, a, r_out, ldro, y, ldy, stream);
     }
+    if (a.r && a.o && a.w_post && r_out && y && s.D <= 4096)
+        return s.D <= 2048 ? run_forward<R, E, 256, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream)
+                           : run_forward<R, E, 512, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream);
     return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
 }
 
@@ -824,6 +831,9 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
                                : run_backward<R, E, 512, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return KDA_NORM_PICK(run_backward, R, E, WIDE<R>, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
+    if (a.w_pre && dro && a.o && a.w_post && s.D <= 4096)
+        return s.D <= 2048 ? run_backward<R, E, 256, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                           : run_backward<R, E, 512, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
 }
 
