@@ -18,28 +18,39 @@ cudaError_t backward_f32(int, Shape s, const NormIn &a, const void *dro, int64_t
 
 namespace {
 
-constexpr int RT = 256;   // threads: 32 columns x 8 strands of rows
+constexpr int RT = 1024, STRANDS = RT / 32;   // threads: 32 columns x 32 strands of CTAs
 
-// Column c of [dw_post | dls | dw_pre] (G + 2 D of them): the CTAs' sums, eight strands added up in order.
+// Column c of [dw_post | dls | dw_pre] (G + 2 D of them): the CTAs' sums, strand by strand, the strands added up in order.
+// Its blocks are dispatched while the last of those CTAs fold their sums; every thread has all of its loads in flight.
 __global__ void __launch_bounds__(RT) reduce(int ctas, int D, int G, const float *part, float *dw_post, float *dls, float *dw_pre)
 {
-    __shared__ float s[RT / 32][32];
+    __shared__ float s[STRANDS][33];
     tc::grid_dep_wait();
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, width = G + 2 * D;
-    float v = 0.f;
-    if (c < width)
-#pragma unroll 8
-        for (int b = strand; b < ctas; b += RT / 32) v += part[static_cast<size_t>(b) * width + c];
-    s[strand][lane] = v;
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, width = G + 2 * D;
+    int c = blockIdx.x * 32 + lane;
+    float v[(MAX_GRID + STRANDS - 1) / STRANDS];
+#pragma unroll
+    for (int k = 0; k < (MAX_GRID + STRANDS - 1) / STRANDS; ++k) {
+        const int b = strand + k * STRANDS;
+        v[k] = c < width && b < ctas ? part[static_cast<size_t>(b) * width + c] : 0.f;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < (MAX_GRID + STRANDS - 1) / STRANDS; ++k) sum += v[k];
+    s[strand][lane] = sum;
     __syncthreads();
-    if (strand || c >= width) return;
-    for (int k = 1; k < RT / 32; ++k) v += s[k][lane];
+    // a warp a column now: the strands' sums, a lane each
+    sum = s[lane][strand];
+#pragma unroll
+    for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    c = blockIdx.x * 32 + strand;
+    if (lane || c >= width) return;
     if (c < G) {
-        if (dw_post) dw_post[c] = v;
+        if (dw_post) dw_post[c] = sum;
     } else if (c < G + D) {
-        if (dls) dls[c - G] = v;
+        if (dls) dls[c - G] = sum;
     } else if (dw_pre) {
-        dw_pre[c - G - D] = v;
+        dw_pre[c - G - D] = sum;
     }
 }
 

@@ -701,7 +701,8 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         ++turn;
         if constexpr (S > 0) slot = slot + 1 == S ? 0 : slot + 1;
     }
-    // the CTA's column sums, over its rows (and over the groups for w_post)
+    // the CTA's column sums, over its rows (and over the groups for w_post); the kernel that adds them up may be dispatched
+    tc::grid_dep_launch();
     cp_wait<0>();
     float *fold = reinterpret_cast<float *>(ring);     // [rows][8 NC NT]
     const int width = NT * NE;
