@@ -68,6 +68,7 @@ cudaError_t launch_norm_forward(int64_t T, int D, int rtype, int type, const Nor
     s.G = a.group ? a.group : D;
     s.inv_d = 1.f / D;
     s.inv_g = 1.f / s.G;
+    s.wide_w = norm::rows_on(a.w_post, 0, 4) && norm::rows_on(a.ls, 0, 4) && norm::rows_on(a.w_pre, 0, 4);
     if (type == KDA_TYPE_F32) return norm::forward_f32(rtype, s, a, r_out, ldro, y, ldy, stream);
     if (type == KDA_TYPE_F16) return norm::forward_f16(rtype, s, a, r_out, ldro, y, ldy, stream);
     return norm::forward_bf16(rtype, s, a, r_out, ldro, y, ldy, stream);
@@ -82,6 +83,7 @@ cudaError_t launch_norm_backward(int64_t T, int D, int rtype, int type, const No
     s.G = a.group ? a.group : D;
     s.inv_d = 1.f / D;
     s.inv_g = 1.f / s.G;
+    s.wide_w = norm::rows_on(a.w_post, 0, 4) && norm::rows_on(a.ls, 0, 4) && norm::rows_on(a.w_pre, 0, 4);
     float *part = static_cast<float *>(ws);
     int grid = 0;
     if (T > 0) {

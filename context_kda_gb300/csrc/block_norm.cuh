@@ -36,6 +36,7 @@ constexpr int MAX_GRID = 304;   // CTAs of a launch: rows of the backward's colu
 struct Shape {
     uint32_t T;
     int D, G, NT;                // channels, channels of a group, threads of a row
+    bool wide_w;                 // weights start on 16 bytes
     bool wide_r, wide_a, wide_b; // outputs whose rows start on 16 bytes: residual, the others
     float inv_d, inv_g;          // 1 / D, 1 / G
 };
@@ -315,10 +316,25 @@ __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + tc::ex2_ftz
 // The gradient of a group of one channel from e, the gradient of hat = v inv.
 __device__ __forceinline__ float unit_grad_of_one(float e, float inv, float eps) { return e * (eps * inv) * (inv * inv); }
 
-// A weight's values at a thread's channels (1 where it is absent): kept in registers when they are few.
+// A weight's values at a thread's channels (1 where it is absent), times 'scale': kept in registers when they are few,
+// read again for every row otherwise, four at a time where the weight starts on 16 bytes ('wide') and D allows.
 template <int NE, int U, typename I>
-__device__ __forceinline__ void weights(const float *w, float scale, I index, int ti, int NT, int D, float (&v)[NE])
+__device__ __forceinline__ void weights(const float *w, float scale, I index, int ti, int NT, int D, bool wide, float (&v)[NE])
 {
+    if constexpr (U >= 4) {
+        if (w && wide && D % U == 0) {
+#pragma unroll
+            for (int j = 0; j < NE; j += 4) {
+                const int c = (ti + (j / U) * NT) * U + j % U;
+                const float4 f = c < D ? __ldg(reinterpret_cast<const float4 *>(w + index(c))) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[j] = scale * f.x;
+                v[j + 1] = scale * f.y;
+                v[j + 2] = scale * f.z;
+                v[j + 3] = scale * f.w;
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
         const int c = (ti + (j / U) * NT) * U + j % U;
@@ -386,17 +402,17 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     auto in_row = [&](int c) { return c; };
     float wl[NE], wr[NE];      // scale * ls * w_post, w_pre
     auto branch_weights = [&] {
-        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
+        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
         if (has_post) {
             float wg[NE];
-            weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
+            weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
 #pragma unroll
             for (int j = 0; j < NE; ++j) wl[j] *= wg[j];
         }
     };
     if constexpr (NC == 1) {
         branch_weights();
-        if (has_y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+        if (has_y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
 #pragma unroll
             for (int j = 0; j < NE; ++j) ss += v[j] * v[j];
             const float inv = inv_rms(sums.over_row(ss, NT, turn) * inv_d, a.eps);
-            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
             if (in) RowE::template write<FULL>(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E))), ti, NT, D, s.wide_a, v);
@@ -560,9 +576,9 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     for (int j = 0; j < NE; ++j) acc_g[j] = acc_l[j] = acc_r[j] = 0.f;
     float wg[NE], wl[NE], wr[NE];
     if constexpr (NC == 1) {
-        weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
-        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
-        weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+        weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
+        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
+        weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -588,7 +604,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         if (has_pre) {
             RowR::template read<(S > 0)>(b, row_at(r, t, lr), ti, NT, D, in, rv);
             RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy), ti, NT, D, in, e);
-            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, wr);
+            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
                 ss = fmaf(rv[j], rv[j], ss);
@@ -642,8 +658,8 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             float gz[NE];
             if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz), ti, NT, D, in, gz);
             if constexpr (NC > 1) {
-                weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, wg);
-                weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, wl);
+                weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
+                weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
             }
             float ev[NU], inv[NU];
 #pragma unroll
@@ -806,9 +822,10 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
     if (rows_on(a.r, a.ldr, re) && rows_on(a.o, a.ldo, e) && rows_on(a.z, a.ldz, e)) {
         s.wide_r = rows_on(r_out, ldro, re);
         s.wide_a = rows_on(y, ldy, e);
-        if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 4096)
-            return s.D <= 2048 ? run_forward<R, E, 256, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
-                               : run_forward<R, E, 512, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream);
+        if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 8192)
+            return s.D <= 2048   ? run_forward<R, E, 256, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
+                   : s.D <= 4096 ? run_forward<R, E, 512, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
+                                 : run_forward<R, E, 1024, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream);
         return KDA_NORM_PICK(run_forward, R, E, WIDE<R>, s, a, r_out, ldro, y, ldy, stream);
     }
     if (a.r && a.o && a.w_post && r_out && y && s.D <= 4096)
@@ -827,9 +844,10 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
         s.wide_r = rows_on(g.dr, g.lddr, re);
         s.wide_a = rows_on(g.d_o, g.lddo, e);
         s.wide_b = rows_on(g.dz, g.lddz, e);
-        if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 4096)
-            return s.D <= 2048 ? run_backward<R, E, 256, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
-                               : run_backward<R, E, 512, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+        if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 8192)
+            return s.D <= 2048   ? run_backward<R, E, 256, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                   : s.D <= 4096 ? run_backward<R, E, 512, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                                 : run_backward<R, E, 512, 2, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return KDA_NORM_PICK(run_backward, R, E, WIDE<R>, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
     if (a.w_pre && dro && a.o && a.w_post && s.D <= 4096)
