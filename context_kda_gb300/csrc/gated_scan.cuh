@@ -161,7 +161,19 @@ template <typename X, bool SH> struct Run {
     }
     __device__ __forceinline__ const X *operator()(int j) const
     {
-        return rows.row(run, j) + (SH ? (first + j * ld) & (Rows<X, SH>::EPC - 1) : 0u);
+        // rows a copy's elements apart start alike
+        constexpr int EPC = Rows<X, SH>::EPC;
+        return rows.row(run, j) + (SH ? (first + (j % EPC) * ld) & (EPC - 1) : 0u);
+    }
+    // f(j, row) for all tokens, those that start alike one after the other
+    template <typename F> __device__ __forceinline__ void each(F f) const
+    {
+        constexpr int P = SH ? Rows<X, SH>::EPC : 1;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+#pragma unroll
+            for (int j = k; j < RUN; j += P) f(j, (*this)(j));
+        }
     }
 };
 // What the runs and tiles of a channel range pass on.
@@ -213,34 +225,42 @@ __device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld,
             }
         }
     } else {
-        // copy k of a thread: copy ch of row 'row'; THREADS copies are DR rows and DC copies on
-        constexpr int CPR = C / R::EPC + 1, DR = THREADS / CPR, DC = THREADS % CPR;
-        static_assert(THREADS == L, "as many copies a thread as a row takes");
-        int row = threadIdx.x / CPR, ch = threadIdx.x % CPR;
-        const int width = (D - c0 < C ? D - c0 : C) * static_cast<int>(sizeof(X));
-        const char *base = reinterpret_cast<const char *>(src), *p = reinterpret_cast<const char *>(src + (static_cast<int64_t>(t0) + row) * ld + c0);
+        constexpr int CPR = C / R::EPC, STEP = THREADS / CPR;      // whole copies of a row, rows of a step; a row takes one copy more
+        static_assert(THREADS == L, "the last copies are one a thread");
+        const char *base = reinterpret_cast<const char *>(src);
         const int64_t pitch = ld * static_cast<int64_t>(sizeof(X));
+        const char *tile = base + t0 * pitch + c0 * static_cast<int64_t>(sizeof(X));
+        if (t0 > 0 && t0 + L < T && c0 + C <= D) {
+            // rows before and after the tile's: whole copies stay within the tensor, their ends belong to other channels
+            const int row = threadIdx.x / CPR, c = threadIdx.x % CPR;
+            const uint32_t to = smem_u32(dst.row(row / RUN, row % RUN) + c * R::EPC);
+            auto from = [](const char *p) { return reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15)); };
+            const char *p = tile + row * pitch;
+            const int64_t hop = STEP * pitch;
 #pragma unroll
-        for (int k = 0; k < CPR; ++k) {
+            for (int k = 0; k < L / STEP; ++k) {
+                copy16(to + k * STEP / RUN * R::RUN_BYTES + k * STEP % RUN * R::PITCH, from(p) + c * 16, 16);
+                p += hop;
+            }
+            copy16(smem_u32(dst.row(threadIdx.x / RUN, threadIdx.x % RUN) + C), from(tile + threadIdx.x * pitch) + C * sizeof(X), 16);
+            return;
+        }
+        const int width = (D - c0 < C ? D - c0 : C) * static_cast<int>(sizeof(X));
+#pragma unroll 1
+        for (int k = threadIdx.x; k < L * (CPR + 1); k += THREADS) {
+            const int row = k / (CPR + 1), ch = k % (CPR + 1);
+            const char *p = tile + row * pitch;
             const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
             const int left = t0 + row < T ? off + width - ch * 16 : 0;
             const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-            const char *from = p - off + ch * 16;
+            const char *at = p - off + ch * 16;
             X *to = dst.row(row / RUN, row % RUN) + ch * R::EPC;
-            if (bytes && from < base) {        // the tensor starts within this copy: nothing before it is read
-                const int skip = static_cast<int>(base - from) / static_cast<int>(sizeof(X));
+            if (bytes && at < base) {        // the tensor starts within this copy: nothing before it is read
+                const int skip = static_cast<int>(base - at) / static_cast<int>(sizeof(X));
                 for (int e = 0; e < R::EPC; ++e)
-                    to[e] = e >= skip && e * static_cast<int>(sizeof(X)) < bytes ? reinterpret_cast<const X *>(from)[e] : from_f32<X>(0.f);
+                    to[e] = e >= skip && e * static_cast<int>(sizeof(X)) < bytes ? reinterpret_cast<const X *>(at)[e] : from_f32<X>(0.f);
             } else {
-                copy16(smem_u32(to), bytes ? from : base - (reinterpret_cast<uintptr_t>(base) & 15u), bytes);
-            }
-            row += DR;
-            ch += DC;
-            p += DR * pitch;
-            if (ch >= CPR) {
-                ch -= CPR;
-                ++row;
-                p += pitch;
+                copy16(smem_u32(to), bytes ? at : base - (reinterpret_cast<uintptr_t>(base) & 15u), bytes);
             }
         }
     }

@@ -56,23 +56,20 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
         const Run<float, SH> gr(sm.g, run, in.g, in.ldg, t.t0);
         const Run<E, SH> xr(sm.x, run, x, in.ldx, t.t0), ir(sm.i, run, ig, in.ldi, t.t0);
         float a[RUN][V], u[RUN][V];
-#pragma unroll
-        for (int j = 0; j < RUN; ++j) {
+        gr.each([&](int j, const float *row) {
             float gv[V];
-            get<ADJ>(gr(j), l, gv);
-            get<ADJ>(xr(j), l, u[j]);
+            get<ADJ>(row, l, gv);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
-        }
-        if (ig) {
-#pragma unroll
-            for (int j = 0; j < RUN; ++j) {
+        });
+        xr.each([&](int j, const E *row) { get<ADJ>(row, l, u[j]); });
+        if (ig)
+            ir.each([&](int j, const E *row) {
                 float iv[V];
-                get<ADJ>(ir(j), l, iv);
+                get<ADJ>(row, l, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
-            }
-        }
+            });
         const Run<E, SH> hr(sm.dh, run, dh, lddh, t.t0);
         float P[V] = {1.f, 1.f}, F[V] = {0.f, 0.f}, B[V] = {0.f, 0.f};   // (P, F): of the states; (P, B): of the gradients
         by_kind(kind, [&](auto k) {
