@@ -475,39 +475,43 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
         meanwhile();
         constexpr int MOST = (GROUP - 1 + WARPS - 1) / WARPS;
         uint64_t w[MOST];
-        uint32_t from = 0;
-        bool ok = true;
+        const long long began = clock64();
+        const uint32_t *state = ch.state + static_cast<size_t>(grp) * ch.Dp + col0 + lane;
+        uint32_t from = warp == one && grp > 0 ? ld_relaxed(state) : 0u;
         // only what has not come yet is read again: words that many CTAs wait for are few enough as it is
 #pragma unroll
         for (int k = 0; k < MOST; ++k) w[k] = warp + k * WARPS < pos ? ~0ull : 0ull;
-        if (warp == one && grp > 0) from = ~0u;
-        const long long began = clock64();
         while (true) {
             bool all = true;
 #pragma unroll
             for (int k = 0; k < MOST; ++k)
                 if (__any_sync(0xffffffffu, w[k] == ~0ull)) w[k] = ld_relaxed(own - static_cast<size_t>(pos - warp - k * WARPS) * ch.Dp);
-            if (__any_sync(0xffffffffu, from == ~0u)) from = ld_relaxed(ch.state + static_cast<size_t>(grp) * ch.Dp + col0 + lane);
 #pragma unroll
             for (int k = 0; k < MOST; ++k) all = all && w[k] != ~0ull;
-            all = all && from != ~0u;
             if (__all_sync(0xffffffffu, all)) break;
             if (__any_sync(0xffffffffu, clock64() - began > SPIN)) {
-                ok = false;
+                sh.bad = 1;
                 break;
             }
         }
 #pragma unroll
         for (int k = 0; k < MOST; ++k)
             if (warp + k * WARPS < pos) sh.before[warp + k * WARPS][lane] = map_of(w[k]);
-        if (!ok) sh.bad = 1;
         __syncthreads();
         if (sh.bad) return false;
         if (warp == one) {
+            // the group's state may come last, and the next group's follows from it: no barrier stands in between
+            while (__any_sync(0xffffffffu, from == ~0u)) {
+                if (__any_sync(0xffffffffu, clock64() - began > SPIN)) {
+                    sh.bad = 1;
+                    break;
+                }
+                from = ld_relaxed(state);
+            }
             h = __uint_as_float(from);
 #pragma unroll 5
             for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
-            if (pos == ch.group - 1 && !last)
+            if (pos == ch.group - 1 && !last && !sh.bad)
                 st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(apply(make_float2(A, B), h)));
         }
     } else {
@@ -535,7 +539,7 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
         }
     }
     __syncthreads();
-    return true;
+    return sh.bad == 0;
 }
 
 // Walks the tiles of a CTA: load(tile, part) starts the copies of a tile in two parts, work(tile, bounds, release)
