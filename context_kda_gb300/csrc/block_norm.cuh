@@ -154,10 +154,11 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
     }
 };
 
-// U = 1: any rows.  A row is copied 16 bytes at a time with the 16 bytes it starts in, by all of its threads, so it is
-// read behind a barrier of them, from an offset.
-template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
+// U = 1: any rows; U = 2: D is even and rows start on pairs.  A row is copied 16 bytes at a time with the 16 bytes it
+// starts in, by all of its threads, so it is read behind a barrier of them, from an offset.
+template <typename X, int BLOCK, int NC, int U> struct Staged {
     static constexpr int NE = 8 * NC, SIZE = static_cast<int>(sizeof(X)), EPC = 16 / SIZE;
+    using Pair = typename std::conditional<SIZE == 4, uint2, uint32_t>::type;
     static constexpr int BYTES = BLOCK * (NE * SIZE + 4);     // of the CTA, per step: a row has four threads at least
     static __device__ __forceinline__ int place(int NT) { return static_cast<int>(threadIdx.x / NT) * (NT * NE * SIZE + 16); }
 
@@ -196,6 +197,17 @@ template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
     {
         const X *p = RING ? reinterpret_cast<const X *>(base + place(NT) + (reinterpret_cast<uintptr_t>(row) & 15u)) : row;
         const int some = in ? D : 0;
+        if constexpr (U == 2) {
+#pragma unroll
+            for (int j = 0; j < NE; j += 2) {
+                const int c = (ti + j / 2 * NT) * 2;
+                X e[2] = {from_f32<X>(0.f), from_f32<X>(0.f)};
+                if (c < some) *reinterpret_cast<Pair *>(e) = *reinterpret_cast<const Pair *>(p + c);
+                v[j] = to_f32(e[0]);
+                v[j + 1] = to_f32(e[1]);
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
             const int c = ti + j * NT;
@@ -204,11 +216,22 @@ template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> {
     }
     template <bool> static __device__ __forceinline__ void write(X *row, int ti, int NT, int D, bool, const float (&v)[NE])
     {
+        if constexpr (U == 2) {
+#pragma unroll
+            for (int j = 0; j < NE; j += 2) {
+                const int c = (ti + j / 2 * NT) * 2;
+                const X e[2] = {from_f32<X>(v[j]), from_f32<X>(v[j + 1])};
+                if (c < D) *reinterpret_cast<Pair *>(row + c) = *reinterpret_cast<const Pair *>(e);
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < NE; ++j)
             if (ti + j * NT < D) row[ti + j * NT] = from_f32<X>(v[j]);
     }
 };
+template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> : Staged<X, BLOCK, NC, 1> {};
+template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 2> : Staged<X, BLOCK, NC, 2> {};
 
 // Sums over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp take one barrier: the
 // warps' sums go to one of two buffers in turn.
@@ -351,7 +374,7 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
     static constexpr int STEP = RowR::BYTES + 2 * RowE::BYTES;
     static constexpr int CTAS = NC == 1 ? 1024 / BLOCK : 1;                       // of an SM
     static constexpr int FIT = 220 / CTAS * 1024 / STEP;
-    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U == 1 ? 0 : FIT;      // steps in the ring; 0: no ring
+    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U <= 2 ? 0 : FIT;      // steps in the ring; 0: no ring
     static constexpr int SMEM = S * STEP;
 };
 
@@ -422,7 +445,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
         };
-        if constexpr (S > 0 && U > 1) {
+        if constexpr (S > 0 && U > 2) {
             ahead();
             cp_wait<S - 1>();
         } else if constexpr (S > 0) {
@@ -505,7 +528,7 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
     static constexpr int STEP = 2 * RowR::BYTES + 3 * RowE::BYTES;
     static constexpr int CTAS = BLOCK == 256 ? 2 : 1;                             // of an SM
     static constexpr int FIT = 220 / CTAS * 1024 / STEP;
-    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U == 1 ? 0 : FIT;
+    static constexpr int S = FIT > 3 ? 3 : FIT == 1 && U <= 2 ? 0 : FIT;
     static constexpr int FOLD = BLOCK * NE * 4;      // the column sums of the CTA, folded at the end
     static constexpr int SMEM = S * STEP > FOLD ? S * STEP : FOLD;
 };
@@ -588,7 +611,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             fetch(slot == 0 ? S - 1 : slot - 1, t + (S - 1) * step);
             cp_commit();
         };
-        if constexpr (S > 0 && U > 1) {
+        if constexpr (S > 0 && U > 2) {
             ahead();
             cp_wait<S - 1>();
         } else if constexpr (S > 0) {
@@ -757,10 +780,10 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
 
 // ---- launches ---------------------------------------------------------------------------------------------
 
-// Every row of the tensor starts on 16 bytes.
-inline bool rows_on(const void *p, int64_t ld, int elem)
+// Every row of the tensor starts on 'on' bytes.
+inline bool rows_on(const void *p, int64_t ld, int elem, int on = 16)
 {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * elem & 15) == 0);
+    return !p || ((reinterpret_cast<uintptr_t>(p) & (on - 1)) == 0 && (ld * elem & (on - 1)) == 0);
 }
 
 // Threads of a row: as many as hold it in 8 nc channels each, and a group's where runs are short.
@@ -828,9 +851,14 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
                                  : run_forward<R, E, 1024, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream);
         return KDA_NORM_PICK(run_forward, R, E, WIDE<R>, s, a, r_out, ldro, y, ldy, stream);
     }
-    if (a.r && a.o && a.w_post && r_out && y && s.D <= 4096)
+    if (a.r && a.o && a.w_post && r_out && y && s.D <= 4096) {
+        if (s.D % 2 == 0 && rows_on(a.r, a.ldr, re, 2 * re) && rows_on(a.o, a.ldo, e, 2 * e) && rows_on(a.z, a.ldz, e, 2 * e) &&
+            rows_on(r_out, ldro, re, 2 * re) && rows_on(y, ldy, e, 2 * e))
+            return s.D <= 2048 ? run_forward<R, E, 256, 1, 2, true>(s, a, r_out, ldro, y, ldy, stream)
+                               : run_forward<R, E, 512, 1, 2, true>(s, a, r_out, ldro, y, ldy, stream);
         return s.D <= 2048 ? run_forward<R, E, 256, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream)
                            : run_forward<R, E, 512, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream);
+    }
     return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
 }
 
@@ -850,9 +878,15 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
                                  : run_backward<R, E, 512, 2, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return KDA_NORM_PICK(run_backward, R, E, WIDE<R>, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
-    if (a.w_pre && dro && a.o && a.w_post && s.D <= 4096)
+    if (a.w_pre && dro && a.o && a.w_post && s.D <= 4096) {
+        if (s.D % 2 == 0 && rows_on(a.r, a.ldr, re, 2 * re) && rows_on(dro, lddro, re, 2 * re) && rows_on(dy, lddy, e, 2 * e) &&
+            rows_on(a.o, a.ldo, e, 2 * e) && rows_on(a.z, a.ldz, e, 2 * e) && rows_on(g.dr, g.lddr, re, 2 * re) &&
+            rows_on(g.d_o, g.lddo, e, 2 * e) && rows_on(g.dz, g.lddz, e, 2 * e))
+            return s.D <= 2048 ? run_backward<R, E, 256, 1, 2, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                               : run_backward<R, E, 512, 1, 2, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
         return s.D <= 2048 ? run_backward<R, E, 256, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
                            : run_backward<R, E, 512, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
+    }
     return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
 }
 
