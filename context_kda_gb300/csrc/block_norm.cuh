@@ -80,7 +80,7 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
     }
 
     // Copies the row's channels below D to the slots at 'base'; 'row' is the row's first channel.
-    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *, int ti, int NT, int D)
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *, int ti, int NT, int D, bool)
     {
 #pragma unroll
         for (int q = 0; q < NU; ++q) {
@@ -90,7 +90,7 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
         }
     }
     // The same where D is a multiple of 8 (zeros from D on).
-    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *, int ti, int NT, int D)
+    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *, int ti, int NT, int D, bool)
     {
 #pragma unroll
         for (int q = 0; q < NU; ++q) {
@@ -162,12 +162,21 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
     static constexpr int BYTES = BLOCK * (NE * SIZE + 4);     // of the CTA, per step: a row has four threads at least
     static __device__ __forceinline__ int place(int NT) { return static_cast<int>(threadIdx.x / NT) * (NT * NE * SIZE + 16); }
 
-    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D)
+    // 'inner': 16 bytes before and behind the row belong to the tensor's rows, so whole copies may be read.
+    static __device__ __forceinline__ void fetch(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D, bool inner)
     {
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u), end = off + D * SIZE;
         const char *p = reinterpret_cast<const char *>(row) - off;
         base += place(NT);
+        if (inner) {
 #pragma unroll
+            for (int k = 0; k <= NE * SIZE / 16; ++k) {
+                const int at = (ti + k * NT) * 16;
+                if (at < end) copy16(base + at, p + at, 16);
+            }
+            return;
+        }
+#pragma unroll 1
         for (int k = 0; k <= NE * SIZE / 16; ++k) {
             const int at = (ti + k * NT) * 16;
             if (at >= end) break;
@@ -187,9 +196,9 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
         else
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const unsigned short *>(&v)) : "memory");
     }
-    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D)
+    static __device__ __forceinline__ void fetch_full(uint32_t base, const X *row, const X *tensor, int ti, int NT, int D, bool inner)
     {
-        fetch(base, row, tensor, ti, NT, D);
+        fetch(base, row, tensor, ti, NT, D, inner);
     }
     static __device__ __forceinline__ void fetch_none(uint32_t, const X *) {}
     template <bool RING>
@@ -400,14 +409,15 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * F::STEP;
         if (t < s.T) {
+            const bool inner = t >= 16 && t + 16 < s.T;      // rows are two bytes at least
             if constexpr (FULL) {
-                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D);
-                RowE::fetch_full(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D);
-                if (z) RowE::fetch_full(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D);
+                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D, inner);
+                RowE::fetch_full(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D, inner);
+                if (z) RowE::fetch_full(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D, inner);
             } else {
-                if (r) RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
-                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D);
-                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D);
+                if (r) RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D, inner);
+                if (o) RowE::fetch(b + RowR::BYTES, row_at(o, t, lo), o, ti, NT, D, inner);
+                if (z) RowE::fetch(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), z, ti, NT, D, inner);
             }
         } else {
             if (has_r) RowR::fetch_none(b, r);
@@ -561,20 +571,21 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     auto fetch = [&](int slot, uint32_t t) {
         const uint32_t b = base + slot * B::STEP;
         if (t < s.T) {
+            const bool inner = t >= 16 && t + 16 < s.T;      // rows are two bytes at least
             if constexpr (FULL) {
-                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D);
-                RowE::fetch_full(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D);
-                RowR::fetch_full(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D);
-                RowE::fetch_full(b + O_O, row_at(o, t, lo), o, ti, NT, D);
-                if (z) RowE::fetch_full(b + O_Z, row_at(z, t, lz), z, ti, NT, D);
+                RowR::fetch_full(b, row_at(r, t, lr), r, ti, NT, D, inner);
+                RowE::fetch_full(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D, inner);
+                RowR::fetch_full(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D, inner);
+                RowE::fetch_full(b + O_O, row_at(o, t, lo), o, ti, NT, D, inner);
+                if (z) RowE::fetch_full(b + O_Z, row_at(z, t, lz), z, ti, NT, D, inner);
             } else {
                 if (a.w_pre) {
-                    RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D);
-                    RowE::fetch(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D);
+                    RowR::fetch(b, row_at(r, t, lr), r, ti, NT, D, inner);
+                    RowE::fetch(b + O_DY, row_at(dy, t, ldy), dy, ti, NT, D, inner);
                 }
-                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D);
-                if (o) RowE::fetch(b + O_O, row_at(o, t, lo), o, ti, NT, D);
-                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz), z, ti, NT, D);
+                if (dro) RowR::fetch(b + O_DRO, row_at(dro, t, ldr), dro, ti, NT, D, inner);
+                if (o) RowE::fetch(b + O_O, row_at(o, t, lo), o, ti, NT, D, inner);
+                if (z) RowE::fetch(b + O_Z, row_at(z, t, lz), z, ti, NT, D, inner);
             }
         } else {
             if (has_pre) {

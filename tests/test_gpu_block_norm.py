@@ -273,3 +273,28 @@ def test_every_alignment(D, group, kind, res):
             want = ref.norm_backward(r_out.double().cpu().numpy(), *args, w["dr_out"], w["dy"])
             for name, a, b, k in zip(("dr", "do", "dz", "dw_post", "dls", "dw_pre"), got, want, (res, kind, kind, "f32", "f32", "f32")):
                 check(a, b, k, name)
+
+
+@pytest.mark.parametrize("kind,res", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("D,group", [(1, 0), (9, 0), (70, 0), (301, 0), (320, 64), (1002, 0)])
+def test_alignment_inside(D, group, kind, res):
+    """The same for rows that have 16 others on both sides, which are copied in whole pieces of 16 bytes."""
+    import torch
+    T = 70
+    d, w = _draw(T, D, kind, res, group=group)
+    args = (w["o"], w["z"], "sigmoid", group, w["w_post"], 0.7, w["ls"], w["w_pre"], EPS)
+    r_ref, y_ref = ref.norm_forward(w["r"], *args)
+    for first, pad in ((0, 1), (1, 0), (7, 2), (2, 2)):
+        moved = dict(d)
+        for name in ("r", "o", "z", "dr_out", "dy"):
+            ld = D + pad
+            flat = torch.full((T * ld + first,), float("nan"), dtype=d[name].dtype, device="cuda")
+            moved[name] = flat[first:first + T * ld].view(T, ld)[:, :D]
+            moved[name].copy_(d[name])
+        r_out, y = _forward(moved, T, D, kind, res, "sigmoid", group)
+        check(r_out, r_ref, res, "r_out")
+        check(y, y_ref, kind, "y")
+        got = _backward(moved, r_out, T, D, kind, res, "sigmoid", group)
+        want = ref.norm_backward(r_out.double().cpu().numpy(), *args, w["dr_out"], w["dy"])
+        for name, a, b, k in zip(("dr", "do", "dz", "dw_post", "dls", "dw_pre"), got, want, (res, kind, kind, "f32", "f32", "f32")):
+            check(a, b, k, name)

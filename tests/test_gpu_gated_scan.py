@@ -321,7 +321,7 @@ def test_every_alignment(D, kind):
     """Tensors that start at every element of 16 bytes, with rows of every length modulo 16 bytes; the values around
     them are NaN and stay out of the results."""
     import torch
-    per = 16 // torch.finfo(torch_type(kind)).bits * 8
+    per = 128 // torch.finfo(torch_type(kind)).bits
     cu, dev, w = _draw([140, 20], D, kind, seed=D)
     h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
     want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])
@@ -339,3 +339,28 @@ def test_every_alignment(D, kind):
             check(final, f_ref, "f32", "final")
             for name, a, b, k in zip(("dx", "di", "dg", "dh0"), _backward(cu, moved, states), want, (kind, kind, "f32", "f32")):
                 check(a, b, k, name)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lengths,D", [([300, 140], 34), ([300, 140], 65), ([900, 1, 320], 65), ([1290], 98)])
+def test_alignment_inside(lengths, D, kind):
+    """The same for tiles that have rows on both sides, which are copied in whole pieces of 16 bytes: by a cluster and
+    by a chain of tiles."""
+    import torch
+    per = 128 // torch.finfo(torch_type(kind)).bits
+    cu, dev, w = _draw(lengths, D, kind, seed=D)
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])
+    for first, pad in ((0, 1), (1, 0), (per - 1, 2), (2, 3)):
+        moved = dict(dev)
+        for name in ("x", "i", "g", "dh"):
+            ld = D + pad
+            flat = torch.full((cu[-1] * ld + first,), float("nan"), dtype=dev[name].dtype, device="cuda")
+            rows = flat[first:first + cu[-1] * ld].view(cu[-1], ld)[:, :D]
+            rows.copy_(dev[name])
+            moved[name] = rows
+        h, final, states = _forward(cu, moved)
+        check(h, h_ref, kind, "h")
+        check(final, f_ref, "f32", "final")
+        for name, a, b, k in zip(("dx", "di", "dg", "dh0"), _backward(cu, moved, states), want, (kind, kind, "f32", "f32")):
+            check(a, b, k, name)
