@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
         const int left = D - t.col0, rows = T - t.t0 - run * RUN, place = b.place();
         const int kind = kind_of(b, rows >= RUN && left >= C && pair);
         float h0[V] = {};
-        if (kind == ONE) seq_row<ADJ>(in.h0, b.first, D, t.col0, l, b.starts != 0, h0);
+        if (kind != ANY) seq_row<ADJ>(in.h0, b.first, D, t.col0, l, b.starts != 0, h0);
         const Run<float, SH> gr(sm.g, run, in.g, in.ldg, t.t0);
         const Run<E, SH> xr(sm.x, run, x, in.ldx, t.t0), ir(sm.i, run, ig, in.ldi, t.t0);
         float a[RUN][V], u[RUN][V];
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
             });
         // a becomes the product of the decays up to the token (ANY: -1 behind a start), u the state from zero, or from
         // its sequence's start
-        by_kind(kind, [&](auto k) {
+        by_inner_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
             float A[V] = {1.f, 1.f}, B[V] = {0.f, 0.f};
 #pragma unroll
@@ -89,17 +89,20 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
             constexpr int K = decltype(k)::value;
             E *at = row + chan<ADJ>(l, 0);
             float *fin = nullptr;
-            if constexpr (K == ONE)
+            if constexpr (K == ONE || K == EDGE)
                 if (final_state && place >= 1 && place <= RUN) fin = final_state + static_cast<int64_t>(b.first - 1) * D + t.col0;
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     s[v] = fmaf(a[j][v], h[v], u[j][v]);
-                    if constexpr (K == ONE) s[v] = j >= place ? u[j][v] : s[v];
+                    if constexpr (K == ONE || K == EDGE) s[v] = j >= place ? u[j][v] : s[v];
                     if constexpr (K == ANY) s[v] = a[j][v] < 0.f ? u[j][v] : s[v];
                 }
-                if constexpr (K == ANY) {
+                if constexpr (K == EDGE) {
+                    if (j < rows) put<ADJ>(at - chan<ADJ>(l, 0), l, s, left);
+                    if (fin && j + 1 == place) put<ADJ>(fin, l, s, left);
+                } else if constexpr (K == ANY) {
                     if (j < rows) put<ADJ>(at - chan<ADJ>(l, 0), l, s, left);
                     if ((b.mask >> (j + 1) & 1) && final_state) put<ADJ>(final_state + (b.seq(j + 1) - 1) * D + t.col0, l, s, left);
                 } else {

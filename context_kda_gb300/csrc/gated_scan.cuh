@@ -406,12 +406,14 @@ struct Bounds {
     __device__ __forceinline__ int place() const { return mask ? __ffs(mask) - 1 : 2 * RUN; }
 };
 // How a warp's two runs are worked.  Boundaries between sequences are rare, but later tiles wait for the tiles that
-// hold them: a run with one takes it by selections (its rows of h0 and dfinal are requested before anything else),
-// only runs with several, and those at the tensor's edges, look at every token.
-enum { PLAIN = 0, ONE = 1, ANY = 2 };
+// hold them: a run with one takes it by selections (its rows of h0 and dfinal are requested before anything else).
+// Runs at the tensor's edges do the same (tokens past the end leave a state as it is: their decay is one and their term
+// zero) and look at what they may write; only runs with several boundaries look at every token.
+enum { PLAIN = 0, ONE = 1, EDGE = 2, ANY = 3 };
 __device__ __forceinline__ int kind_of(const Bounds &b, bool inside)
 {
-    if (__any_sync(0xffffffffu, !inside || __popc(b.mask) > 1)) return ANY;
+    if (__any_sync(0xffffffffu, __popc(b.mask) > 1)) return ANY;
+    if (__any_sync(0xffffffffu, !inside)) return EDGE;
     return __any_sync(0xffffffffu, b.mask != 0) ? ONE : PLAIN;
 }
 template <int K> using Kind = std::integral_constant<int, K>;
@@ -419,7 +421,15 @@ template <typename F> __device__ __forceinline__ void by_kind(int kind, F f)
 {
     if (kind == PLAIN) f(Kind<PLAIN>{});
     else if (kind == ONE) f(Kind<ONE>{});
+    else if (kind == EDGE) f(Kind<EDGE>{});
     else f(Kind<ANY>{});
+}
+// The same for what writes nothing.
+template <typename F> __device__ __forceinline__ void by_inner_kind(int kind, F f)
+{
+    if (kind == PLAIN) f(Kind<PLAIN>{});
+    else if (kind == ANY) f(Kind<ANY>{});
+    else f(Kind<ONE>{});
 }
 // Row n of [N][D] at a lane's channels (zeros past D, without the tensor, or where it is not wanted).
 template <bool ADJ> __device__ __forceinline__ void seq_row(const float *p, int64_t n, int D, int col0, int l, bool wanted, float (&o)[V])

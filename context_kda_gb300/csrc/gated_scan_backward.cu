@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
         const uint32_t ends = b.mask >> 1;
         const int kind = kind_of(b, rows >= RUN && left >= C && pair);
         float h0[V] = {}, df[V] = {};
-        if (kind == ONE) {
+        if (kind != ANY) {
             seq_row<ADJ>(in.h0, b.first, D, t.col0, l, b.starts != 0, h0);
             seq_row<ADJ>(dfinal, b.first - 1, D, t.col0, l, ends != 0, df);
         }
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
             });
         const Run<E, SH> hr(sm.dh, run, dh, lddh, t.t0);
         float P[V] = {1.f, 1.f}, F[V] = {0.f, 0.f}, B[V] = {0.f, 0.f};   // (P, F): of the states; (P, B): of the gradients
-        by_kind(kind, [&](auto k) {
+        by_inner_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
             float f[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) f[v] = sm.fstate[run][chan<ADJ>(l, v)];
-            by_kind(kind, [&](auto k) {
+            by_inner_kind(kind, [&](auto k) {
                 constexpr int K = decltype(k)::value;
 #pragma unroll
                 for (int j = 0; j < RUN; ++j) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
         by_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
             float *first = nullptr;
-            if constexpr (K == ONE)
+            if constexpr (K == ONE || K == EDGE)
                 if (out.dh0 && b.starts) first = out.dh0 + static_cast<int64_t>(b.first) * D + t.col0;
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
                     if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, e);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) e[v] = j + 1 == place ? df[v] : e[v];
+                    if constexpr (K == ONE || K == EDGE) e[v] = j + 1 == place ? df[v] : e[v];
                     Gr[v] += e[v];
                     e[v] = a[j][v] * Gr[v];
                     gi[v] *= Gr[v];
@@ -168,13 +168,15 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
 #pragma unroll
                     for (int v = 0; v < V; ++v) gx[v] *= Gr[v];
                 }
-                if constexpr (K == ANY) {
+                if constexpr (K == ANY || K == EDGE) {
                     if (j < rows) {
                         put<ADJ>(px - chan<ADJ>(l, 0), l, gx, left);
                         if (di) put<ADJ>(pi - chan<ADJ>(l, 0), l, gi, left);
                         put<ADJ>(pg - chan<ADJ>(l, 0), l, gg, left);
                     }
-                    if ((b.starts >> j & 1) && out.dh0) put<ADJ>(out.dh0 + b.seq(j) * D + t.col0, l, e, left);
+                    if constexpr (K == EDGE) {
+                        if (first && j == place) put<ADJ>(first, l, e, left);
+                    } else if ((b.starts >> j & 1) && out.dh0) put<ADJ>(out.dh0 + b.seq(j) * D + t.col0, l, e, left);
                 } else {
                     put_all<ADJ>(px, gx);
                     if (di) put_all<ADJ>(pi, gi);
