@@ -130,17 +130,17 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
 
 // ---- one token --------------------------------------------------------------------------------------------
 
-// One token per row, each the next one of its slot's state (updated in place).  N channels a thread: four where all rows
-// start on four elements and D is a multiple of four, one otherwise; bound by memory (2048 x 4096 in bf16: see the
-// launch), or by the launch.
-constexpr int STEP_THREADS = 128;
-template <typename X> __device__ __forceinline__ void get_n(const X *p, float (&v)[1]) { v[0] = to_f32(*p); }
-__device__ __forceinline__ void get_n(const float *p, float (&v)[4])
+// One token per row, each the next one of its slot's state (updated in place).  Four channels a thread: adjacent ones
+// where all rows start on four elements and D is a multiple of four (VEC), else STEP_THREADS apart, so that a warp's
+// are adjacent.  Bound by memory, or by the launch (2048 x 4096 in bf16: 21 us, the rate of a copy; 27 us at 4095 channels;
+// with one channel a thread, too few loads in flight, 84 us).
+constexpr int STEP_THREADS = 128, STEP_N = 4;
+__device__ __forceinline__ void get_four(const float *p, float (&v)[4])
 {
     const float4 q = *reinterpret_cast<const float4 *>(p);
     v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
 }
-template <typename X> __device__ __forceinline__ void get_n(const X *p, float (&v)[4])
+template <typename X> __device__ __forceinline__ void get_four(const X *p, float (&v)[4])
 {
     const uint2 q = *reinterpret_cast<const uint2 *>(p);
     float w[2];
@@ -149,38 +149,56 @@ template <typename X> __device__ __forceinline__ void get_n(const X *p, float (&
     unpack(q.y, w, p);
     v[2] = w[0], v[3] = w[1];
 }
-template <typename X> __device__ __forceinline__ void put_n(X *p, const float (&v)[1]) { *p = from_f32<X>(v[0]); }
-__device__ __forceinline__ void put_n(float *p, const float (&v)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
-template <typename X> __device__ __forceinline__ void put_n(X *p, const float (&v)[4])
+__device__ __forceinline__ void put_four(float *p, const float (&v)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+template <typename X> __device__ __forceinline__ void put_four(X *p, const float (&v)[4])
 {
     X e[4] = {from_f32<X>(v[0]), from_f32<X>(v[1]), from_f32<X>(v[2]), from_f32<X>(v[3])};
     *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
 }
-template <typename E, int N>
+template <bool VEC, typename X> __device__ __forceinline__ void get_row(const X *row, int d, int D, float (&v)[STEP_N])
+{
+    if constexpr (VEC) {
+        get_four(row + d, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < STEP_N; ++k) v[k] = d + k * STEP_THREADS < D ? to_f32(row[d + k * STEP_THREADS]) : 0.f;
+    }
+}
+template <bool VEC, typename X> __device__ __forceinline__ void put_row(X *row, int d, int D, const float (&v)[STEP_N])
+{
+    if constexpr (VEC) {
+        put_four(row + d, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < STEP_N; ++k)
+            if (d + k * STEP_THREADS < D) row[d + k * STEP_THREADS] = from_f32<X>(v[k]);
+    }
+}
+template <typename E, bool VEC>
 __global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int D, const int32_t *slots, int num_slots, ScanIn in,
                                                           float *state, void *h_, int64_t ldh)
 {
-    const int d = (blockIdx.x * STEP_THREADS + threadIdx.x) * N;
+    const int d = blockIdx.x * (STEP_THREADS * STEP_N) + threadIdx.x * (VEC ? STEP_N : 1);
     if (d >= D) return;
     for (int64_t b = blockIdx.y; b < B; b += gridDim.y) {
         // the row's inputs are requested along with its slot, not after it
-        float g[N], u[N], i[N];
-        get_n(in.g + b * in.ldg + d, g);
-        get_n(static_cast<const E *>(in.x) + b * in.ldx + d, u);
-        if (in.i) get_n(static_cast<const E *>(in.i) + b * in.ldi + d, i);
+        float g[STEP_N], u[STEP_N], i[STEP_N];
+        get_row<VEC>(in.g + b * in.ldg, d, D, g);
+        get_row<VEC>(static_cast<const E *>(in.x) + b * in.ldx, d, D, u);
+        if (in.i) get_row<VEC>(static_cast<const E *>(in.i) + b * in.ldi, d, D, i);
         const int slot = slots ? slots[b] : static_cast<int>(b);
         const bool live = slot >= 0 && slot < num_slots;
-        float s[N] = {};
+        float s[STEP_N] = {};
         if (live) {
-            float *at = state + static_cast<int64_t>(slot) * D + d;
-            get_n(at, s);
+            float *at = state + static_cast<int64_t>(slot) * D;
+            get_row<VEC>(at, d, D, s);
 #pragma unroll
-            for (int j = 0; j < N; ++j) s[j] = fmaf(decay(g[j]), s[j], in.i ? u[j] * i[j] : u[j]);
-            put_n(at, s);
+            for (int j = 0; j < STEP_N; ++j) s[j] = fmaf(decay(g[j]), s[j], in.i ? u[j] * i[j] : u[j]);
+            put_row<VEC>(at, d, D, s);
         } else if (slot >= num_slots && d == 0) {
             record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         }
-        put_n(static_cast<E *>(h_) + b * ldh + d, s);
+        put_row<VEC>(static_cast<E *>(h_) + b * ldh, d, D, s);
     }
 }
 
@@ -212,10 +230,9 @@ cudaError_t launch_scan_step(int B, int D, int type, const int32_t *slots, int n
         };
         const bool four = D % 4 == 0 && on_four(in.x, in.ldx, sizeof(E)) && on_four(in.i, in.ldi, sizeof(E)) && on_four(in.g, in.ldg, 4) &&
                           on_four(state, 0, 4) && on_four(h, ldh, sizeof(E));
-        const int n = four ? 4 : 1;
-        const dim3 grid((D + STEP_THREADS * n - 1) / (STEP_THREADS * n), B < 65535 ? B : 65535);
-        if (four) scan_step<E, 4><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
-        else scan_step<E, 1><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
+        const dim3 grid((D + STEP_THREADS * STEP_N - 1) / (STEP_THREADS * STEP_N), B < 65535 ? B : 65535);
+        if (four) scan_step<E, true><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
+        else scan_step<E, false><<<grid, STEP_THREADS, 0, stream>>>(B, D, slots, num_slots, in, state, h, ldh);
         return cudaGetLastError();
     });
 }

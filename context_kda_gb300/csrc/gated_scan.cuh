@@ -50,8 +50,13 @@ constexpr int V = 2;                         // channels of a lane
 constexpr int WARPS = RUNS / 2, THREADS = WARPS * 32;
 // CTAs of an SM: four, or as many as their shared memory allows.
 template <typename Sh> constexpr int ctas_of() { return 233472 / (static_cast<int>(sizeof(Sh)) + 1024) < 4 ? 233472 / (static_cast<int>(sizeof(Sh)) + 1024) : 4; }
-constexpr int GROUP = 16, SHORT_GROUP = 8;   // tiles of a group: see run()
-constexpr int MAX_CLUSTER = 8;               // tiles that a cluster covers
+// Tiles of a group.  Narrow inputs wait for the state's way from group to group, which a long group shortens, at the cost
+// of more maps that a tile reads and folds (16384 tokens x 4096 and 49274 x 128 channels in bf16: groups of 8 110 and 40 us,
+// of 16 110 and 26 us, of 32 114 and 22 us).
+constexpr int GROUP = 16;
+// Tiles that a cluster covers: 512 tokens in bf16 take 4.9 us, by a chain 5.9 us, at 512 channels, and 6.3 and 7.0 us at 4096;
+// 1024 tokens 5.3 and 7.3 us, and 10.8 and 10.4 us.
+constexpr int MAX_CLUSTER = 8;
 constexpr long long SPIN = 4000000000LL;     // clocks of a wait: about two seconds
 
 __device__ int g_scan_status;
@@ -77,7 +82,7 @@ inline Layout layout_of(int64_t T, int D)
     Layout l;
     l.starts = 256;                                  // the ticket comes first
     l.state = up(l.starts + (nT + 1) * sizeof(Starts));
-    l.map = up(l.state + (nT / SHORT_GROUP + 1) * Dp * 4);
+    l.map = up(l.state + (nT / GROUP + 1) * Dp * 4);
     l.end = l.map + nT * Dp * 8;
     return l;
 }
@@ -86,14 +91,14 @@ struct Chain {
     Starts *starts;       // [tiles + 1]
     uint32_t *state;      // [groups][Dp], all ones until published
     uint64_t *map;        // [tiles][Dp], low word A, high word B
-    int Dp, group;        // padded channels; tiles of a group
+    int Dp;               // padded channels
 };
 inline Chain chain_of(void *ws, int64_t T, int D)
 {
     char *b = static_cast<char *>(ws);
     const Layout l = layout_of(T, D);
     return Chain{reinterpret_cast<int *>(b), reinterpret_cast<Starts *>(b + l.starts), reinterpret_cast<uint32_t *>(b + l.state),
-                 reinterpret_cast<uint64_t *>(b + l.map), padded(D), GROUP};
+                 reinterpret_cast<uint64_t *>(b + l.map), padded(D)};
 }
 
 __global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int grid, int *ticket, Starts *starts,
@@ -478,9 +483,9 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
         }
     }
     if constexpr (CHAIN) {
-        const int grp = rt / ch.group, pos = rt - grp * ch.group;
+        const int grp = rt / GROUP, pos = rt - grp * GROUP;
         uint64_t *own = ch.map + static_cast<size_t>(rt) * ch.Dp + col0 + lane;
-        if (warp == one && pos < ch.group - 1 && !last)      // the group's last tile publishes a state instead
+        if (warp == one && pos < GROUP - 1 && !last)      // the group's last tile publishes a state instead
             st_relaxed(own, static_cast<uint64_t>(word(B)) << 32 | __float_as_uint(A));
         meanwhile();
         constexpr int MOST = (GROUP - 1 + WARPS - 1) / WARPS;
@@ -521,7 +526,7 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
             h = __uint_as_float(from);
 #pragma unroll 5
             for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
-            if (pos == ch.group - 1 && !last && !sh.bad)
+            if (pos == GROUP - 1 && !last && !sh.bad)
                 st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(apply(make_float2(A, B), h)));
         }
     } else {
@@ -695,9 +700,6 @@ cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     } else {
         ch = chain_of(ws, T, D);
-        // A short group folds fewer maps a tile; a long one passes the state on less often, which is what bounds narrow
-        // inputs.
-        ch.group = nC >= 64 ? SHORT_GROUP : GROUP;
         const Layout l = layout_of(T, D);
         const size_t words = (l.end - l.state) / 16;
         const size_t want = (words + 4 * 256 - 1) / (4 * 256), most = 4 * static_cast<size_t>(sm_count());
