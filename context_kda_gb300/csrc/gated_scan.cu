@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
                 for (int v = 0; v < V; ++v) {
                     if constexpr (K == ONE) B[v] = j == place ? h0[v] : B[v];
                     u[j][v] = B[v] = fmaf(a[j][v], B[v], u[j][v]);
-                    a[j][v] = A[v] = K == ANY && A[v] < 0.f ? -1.f : A[v] * a[j][v];
+                    a[j][v] = A[v] = K == ANY && A[v] < 0.f ? -1.f : times(A[v], a[j][v]);
                 }
             }
         });

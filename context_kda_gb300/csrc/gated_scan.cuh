@@ -336,11 +336,14 @@ __device__ __forceinline__ float decay(float g) { return ex2_ftz(g * 1.442695040
 
 // ---- maps -----------------------------------------------------------------------------------------------
 
+// The product of two decays, which may be above one.  It stays finite, so that a state of zero stays zero (a decay that
+// is infinite by itself makes a NaN of the map's other half).
+__device__ __forceinline__ float times(float A, float a) { return fminf(A * a, 3.402823466e38f); }
 // One map more: (A, B) becomes (a, b) o (A, B).
 __device__ __forceinline__ void then(float &A, float &B, float a, float b)
 {
     B = a < 0.f ? b : fmaf(a, B, b);
-    A = a < 0.f || A < 0.f ? -1.f : A * a;
+    A = a < 0.f || A < 0.f ? -1.f : times(A, a);
 }
 __device__ __forceinline__ float apply(float2 m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
 

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     if constexpr (K == ONE) F[v] = j == place ? h0[v] : F[v];
-                    P[v] *= a[j][v];
+                    P[v] = times(P[v], a[j][v]);
                     F[v] = fmaf(a[j][v], F[v], u[j][v]);
                 }
             }

@@ -364,3 +364,22 @@ def test_alignment_inside(lengths, D, kind):
         check(final, f_ref, "f32", "final")
         for name, a, b, k in zip(("dx", "di", "dg", "dh0"), _backward(cu, moved, states), want, (kind, kind, "f32", "f32")):
             check(a, b, k, name)
+
+
+@pytest.mark.parametrize("lengths", [[400, 300], [1400, 300], [5, 400, 1]])
+def test_growing_decays_of_a_zero_state(lengths):
+    """exp(g) = e: the decays' product passes fp32's range long before the sequence ends, the state is zero all along."""
+    import torch
+    D = 70
+    cu, dev, _ = _draw(lengths, D, "bf16", seed=3, with_h0=False)
+    a, b = cu[-3], cu[-2]
+    dev["g"][a:b] = 1.0
+    dev["x"][a:b] = 0.0
+    dev["dh"][a:b] = 0.0
+    dev["dfinal"][-2] = 0.0
+    h, final, states = _forward(cu, dev)
+    assert not h[a:b].any() and not final[-2].any() and torch.isfinite(h).all() and torch.isfinite(final).all()
+    dx, di, dg, dh0 = _backward(cu, dev, states)
+    for t in (dx, di, dg):
+        assert not t[a:b].any() and torch.isfinite(t).all()
+    assert not dh0[-2].any() and torch.isfinite(dh0).all()
