@@ -21,7 +21,8 @@ namespace {
 constexpr int RT = 1024, STRANDS = RT / 32;   // threads: 32 columns x 32 strands of CTAs
 
 // Column c of [dw_post | dls | dw_pre] (G + 2 D of them): the CTAs' sums, strand by strand, the strands added up in order.
-// Its blocks are dispatched while the last of those CTAs fold their sums; every thread has all of its loads in flight.
+// Its blocks are dispatched while the last of those CTAs fold their sums; every thread has all of its loads in flight
+// (8192 x 2048 gradients 51.9 us, 53.8 us with 8 strands a column that load one after the other).
 __global__ void __launch_bounds__(RT) reduce(int ctas, int D, int G, const float *part, float *dw_post, float *dls, float *dw_pre)
 {
     __shared__ float s[STRANDS][33];

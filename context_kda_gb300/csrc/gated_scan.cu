@@ -73,10 +73,16 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan
                 for (int v = 0; v < V; ++v) {
                     if constexpr (K == ONE) B[v] = j == place ? h0[v] : B[v];
                     u[j][v] = B[v] = fmaf(a[j][v], B[v], u[j][v]);
-                    a[j][v] = A[v] = K == ANY && A[v] < 0.f ? -1.f : times(A[v], a[j][v]);
+                    a[j][v] = A[v] = K == ANY && A[v] < 0.f ? -1.f : A[v] * a[j][v];
                 }
             }
         });
+        if (__any_sync(0xffffffffu, !(a[RUN - 1][0] <= MOST) || !(a[RUN - 1][1] <= MOST))) {
+#pragma unroll
+            for (int j = 0; j < RUN; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[j][v] = fminf(a[j][v], MOST);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) sm.s.map[run][chan<ADJ>(l, v)] = make_float2(b.starts ? -1.f : a[RUN - 1][v], u[RUN - 1][v]);
         __syncthreads();

@@ -93,13 +93,14 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) sca
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     if constexpr (K == ONE) F[v] = j == place ? h0[v] : F[v];
-                    P[v] = times(P[v], a[j][v]);
+                    P[v] *= a[j][v];
                     F[v] = fmaf(a[j][v], F[v], u[j][v]);
                 }
             }
         });
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            P[v] = fminf(P[v], MOST);
             sm.s.map[run][chan<ADJ>(l, v)] = make_float2(ends ? -1.f : P[v], B[v]);
             sm.fmap[run][chan<ADJ>(l, v)] = make_float2(b.starts ? -1.f : P[v], F[v]);
         }
