@@ -14,18 +14,18 @@
 // all its rows, which are copied to a ring in shared memory (cp.async) one to three steps ahead.  Sums over a row take
 // one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
 // residual is fp32) where rows start on 16 bytes (a thread copies what it reads itself, without a barrier), else 2 where they
-// start on pairs and 1 anywhere (8192 rows in bf16, forward of 3970 channels: 89 us in pairs, 105 us one by one; gradients
-// of 1002 channels with an fp32 residual: 52 and 63 us).
+// start on pairs and 1 anywhere (8192 rows in bf16, forward of 3970 channels: 83 us in pairs, 92 us one by one; gradients
+// of 1002 channels with an fp32 residual: 50 and 55 us).
 // FULL instances are for the usual call: every part but the gate is there and, unless U = 1, D is a multiple of U and
 // outputs lie as inputs do.  They decide nothing about that per row, which is a third of the instructions of the
-// others and bounds them (16384 x 2048 gradients in bf16: 115 us, 95 us with FULL).
+// others and bounds them (16384 x 2048 gradients in bf16: 114 us, 92 us with FULL).
 // Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 //
 // Measured on the device (share of a copy's 6.79 TB/s): forward of 65536 x 4096 in bf16 with an fp32 residual 546 us (101 %),
 // of 16384 x 4096 all in bf16 84 us (94 %); gradients of 16384 x 4096 with an fp32 residual 227 us (96 %), of 16384 x 2048 in
 // bf16 92 us (86 %), of 8192 x 2048 51 us (77 %): the launches, the first rows' way in and the column sums take 6 us of
-// any call.  Unaligned rows are bound by instructions, gradients of 8198 x 1001 in fp32 64 us (60 %); above 4096 channels the weights
+// any call.  Unaligned rows are bound by instructions, gradients of 8198 x 1001 in fp32 56 us (69 %); above 4096 channels the weights
 // are read again for every row, 8192 x 8192 in bf16 117 us (84 %) and gradients 336 us (47 %: the column sums leave no registers
 // for the row, and some of it is kept in local memory).
 #pragma once
@@ -74,11 +74,20 @@ __device__ __forceinline__ void unpack(uint32_t w, float *v, const __half *)
 }
 __device__ __forceinline__ void unpack(uint32_t w, float *v, const float *) { v[0] = __uint_as_float(w); }
 
+// Channel j of a thread's NE of its row.  U > 2: runs of U, NT threads apart.  U <= 2: W threads take W NE adjacent channels,
+// their runs W threads apart, so that all but a thread's first are at offsets that the compiler knows; W is a warp, or half
+// of one for rows of up to 128 channels (gradients of 46838 x 113 in fp32: 32 us, 45 us with W = 32).
+template <int U, int NE, int W> __device__ __forceinline__ int channel_of(int ti, int NT, int j)
+{
+    if constexpr (U > 2) return (ti + j / U * NT) * U + j % U;
+    else return ti / W * (W * NE) + ti % W * U + j / U * (W * U) + j % U;
+}
+
 // A thread's channels of a row of X, in runs of U: run q starts at channel (ti + q NT) U.  U = 8, or 4 where the
 // residual is fp32: rows start on 16 bytes; every thread copies its own channels into its own slots.  A run is one
 // copy, so that a warp's copies and stores are adjacent bytes: with 8 channels of fp32 a thread, in two pieces each,
 // every sector moved twice (16384 x 2048 in fp32: 157 us, 109 us with 4).
-template <typename X, int BLOCK, int NC, int U> struct Row {
+template <typename X, int BLOCK, int NC, int U, int W> struct Row {
     static constexpr int NE = 8 * NC, NU = NE / U, RUN = U * static_cast<int>(sizeof(X));     // runs, bytes of a run
     static constexpr int BYTES = NE * static_cast<int>(sizeof(X)) * BLOCK;                    // of the CTA, per step
     static_assert(RUN == 16 || RUN == 8, "one copy a run");
@@ -137,7 +146,7 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
         } else {
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                const int c = (ti + j / U * NT) * U + j % U;
+                const int c = channel_of<U, NE, W>(ti, NT, j);
                 v[j] = in && c < D ? to_f32(row[c]) : 0.f;
             }
         }
@@ -165,10 +174,10 @@ template <typename X, int BLOCK, int NC, int U> struct Row {
 
 // U = 1: any rows; U = 2: D is even and rows start on pairs.  A row is copied 16 bytes at a time with the 16 bytes it
 // starts in, by all of its threads, so it is read behind a barrier of them, from an offset.
-template <typename X, int BLOCK, int NC, int U> struct Staged {
+template <typename X, int BLOCK, int NC, int U, int W> struct Staged {
     static constexpr int NE = 8 * NC, SIZE = static_cast<int>(sizeof(X)), EPC = 16 / SIZE;
     using Pair = typename std::conditional<SIZE == 4, uint2, uint32_t>::type;
-    static constexpr int BYTES = BLOCK * (NE * SIZE + 4);     // of the CTA, per step: a row has four threads at least
+    static constexpr int BYTES = BLOCK * NE * SIZE + BLOCK / W * 16;     // of the CTA, per step: a row has W threads at least
     static __device__ __forceinline__ int place(int NT) { return static_cast<int>(threadIdx.x / NT) * (NT * NE * SIZE + 16); }
 
     // 'inner': 16 bytes before and behind the row belong to the tensor's rows, so whole copies may be read.
@@ -218,7 +227,7 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
         if constexpr (U == 2) {
 #pragma unroll
             for (int j = 0; j < NE; j += 2) {
-                const int c = (ti + j / 2 * NT) * 2;
+                const int c = channel_of<U, NE, W>(ti, NT, j);
                 X e[2] = {from_f32<X>(0.f), from_f32<X>(0.f)};
                 if (c < some) *reinterpret_cast<Pair *>(e) = *reinterpret_cast<const Pair *>(p + c);
                 v[j] = to_f32(e[0]);
@@ -228,7 +237,7 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            const int c = ti + j * NT;
+            const int c = channel_of<U, NE, W>(ti, NT, j);
             v[j] = c < some ? to_f32(p[c]) : 0.f;
         }
     }
@@ -237,7 +246,7 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
         if constexpr (U == 2) {
 #pragma unroll
             for (int j = 0; j < NE; j += 2) {
-                const int c = (ti + j / 2 * NT) * 2;
+                const int c = channel_of<U, NE, W>(ti, NT, j);
                 const X e[2] = {from_f32<X>(v[j]), from_f32<X>(v[j + 1])};
                 if (c < D) *reinterpret_cast<Pair *>(row + c) = *reinterpret_cast<const Pair *>(e);
             }
@@ -245,11 +254,11 @@ template <typename X, int BLOCK, int NC, int U> struct Staged {
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j)
-            if (ti + j * NT < D) row[ti + j * NT] = from_f32<X>(v[j]);
+            if (channel_of<U, NE, W>(ti, NT, j) < D) row[channel_of<U, NE, W>(ti, NT, j)] = from_f32<X>(v[j]);
     }
 };
-template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 1> : Staged<X, BLOCK, NC, 1> {};
-template <typename X, int BLOCK, int NC> struct Row<X, BLOCK, NC, 2> : Staged<X, BLOCK, NC, 2> {};
+template <typename X, int BLOCK, int NC, int W> struct Row<X, BLOCK, NC, 1, W> : Staged<X, BLOCK, NC, 1, W> {};
+template <typename X, int BLOCK, int NC, int W> struct Row<X, BLOCK, NC, 2, W> : Staged<X, BLOCK, NC, 2, W> {};
 
 // Sums over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp take one barrier: the
 // warps' sums go to one of two buffers in turn.
@@ -309,26 +318,38 @@ template <typename X> __device__ __forceinline__ X *row_at(X *p, uint32_t t, uin
     return reinterpret_cast<X *>(reinterpret_cast<Byte *>(p) + static_cast<uint64_t>(t) * ld);
 }
 
-// Sums over each run's group of G channels (G < D), in place.  G spans G / U lanes of consecutive threads,
-// which may be several warps when runs are short (NT U is then at least G; buffers in turn as above, so an object serves one
-// sum a row).
-template <int BLOCK, int NU, int U> struct GroupSums {
-    float part[U < 8 ? 2 : 1][U < 8 ? NU : 1][BLOCK / 32];
+// Sums over each run's group of G channels (G < D), in place.  U > 2: G spans G / U lanes of consecutive threads, which
+// may be two warps when U = 4 (NT U is then at least G; buffers in turn as above, so an object serves one sum a row).  U <= 2: a
+// run's lanes, and several runs of its W threads where a run of them is less.
+template <int BLOCK, int NU, int U, int W> struct GroupSums {
+    float part[U == 4 ? 2 : 1][U == 4 ? NU : 1][BLOCK / 32];
     static __device__ __forceinline__ void fold(float (&v)[NU], int m)
     {
 #pragma unroll
         for (int q = 0; q < NU; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], m);
     }
+    // Sums of n adjacent runs.
+    static __device__ __forceinline__ void join(float (&v)[NU], int n)
+    {
+#pragma unroll
+        for (int m = 1; m < NU; m *= 2) {
+            if (m >= n) return;
+#pragma unroll
+            for (int q = 0; q < NU; ++q)
+                if (!(q & m)) v[q] = v[q | m] = v[q] + v[q | m];
+        }
+    }
     __device__ __forceinline__ void over_group(float (&v)[NU], int G, int turn)
     {
         const int lanes = G / U;
 #pragma unroll 1
-        for (int m = (lanes < 32 ? lanes : 32) >> 1; m > 8; m >>= 1) fold(v, m);
+        for (int m = (lanes < W ? lanes : W) >> 1; m > 8; m >>= 1) fold(v, m);
         if (lanes >= 16) fold(v, 8);
         if (lanes >= 8) fold(v, 4);
         fold(v, 2);        // a group is four lanes at least
         fold(v, 1);
-        if constexpr (U < 8) {
+        if constexpr (U <= 2) join(v, lanes / W);
+        if constexpr (U == 4) {
             if (lanes <= 32) return;
             const int warp = threadIdx.x >> 5, n = lanes >> 5, w0 = warp & ~(n - 1);
             if ((threadIdx.x & 31) == 0)
@@ -359,14 +380,14 @@ __device__ __forceinline__ float unit_grad_of_one(float e, float inv, float eps)
 
 // A weight's values at a thread's channels (1 where it is absent), times 'scale': kept in registers when they are few,
 // read again for every row otherwise, four at a time where the weight starts on 16 bytes ('wide') and D allows.
-template <int NE, int U, typename I>
+template <int NE, int U, int W, typename I>
 __device__ __forceinline__ void weights(const float *w, float scale, I index, int ti, int NT, int D, bool wide, float (&v)[NE])
 {
     if constexpr (U >= 4) {
         if (w && wide && D % U == 0) {
 #pragma unroll
             for (int j = 0; j < NE; j += 4) {
-                const int c = (ti + (j / U) * NT) * U + j % U;
+                const int c = channel_of<U, NE, W>(ti, NT, j);
                 const float4 f = c < D ? __ldg(reinterpret_cast<const float4 *>(w + index(c))) : make_float4(0.f, 0.f, 0.f, 0.f);
                 v[j] = scale * f.x;
                 v[j + 1] = scale * f.y;
@@ -378,16 +399,16 @@ __device__ __forceinline__ void weights(const float *w, float scale, I index, in
     }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-        const int c = (ti + (j / U) * NT) * U + j % U;
+        const int c = channel_of<U, NE, W>(ti, NT, j);
         v[j] = c < D ? scale * (w ? __ldg(w + index(c)) : 1.f) : 0.f;
     }
 }
 
 // ---- forward ----------------------------------------------------------------------------------------------
 
-template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
-    using RowR = Row<R, BLOCK, NC, U>;
-    using RowE = Row<E, BLOCK, NC, U>;
+template <typename R, typename E, int BLOCK, int NC, int U, int W> struct Forward {
+    using RowR = Row<R, BLOCK, NC, U, W>;
+    using RowE = Row<E, BLOCK, NC, U, W>;
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = RowR::BYTES + 2 * RowE::BYTES;
     static constexpr int CTAS = NC == 1 ? 1024 / BLOCK : 1;                       // of an SM
@@ -396,16 +417,16 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Forward {
     static constexpr int SMEM = S * STEP;
 };
 
-template <typename R, typename E, int BLOCK, int NC, int U, bool FULL>
-__global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL, int W>
+__global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U, W>::CTAS) forward(Shape s, NormIn a, R *r_out, int64_t ldro, E *y, int64_t ldy)
 {
-    using F = Forward<R, E, BLOCK, NC, U>;
+    using F = Forward<R, E, BLOCK, NC, U, W>;
     using RowR = typename F::RowR;
     using RowE = typename F::RowE;
     constexpr int NE = F::NE, NU = F::NU, S = F::S;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ Sums<BLOCK> sums;
-    __shared__ GroupSums<BLOCK, NU, U> groups;
+    __shared__ GroupSums<BLOCK, NU, U, W> groups;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
     const int D = s.D, G = s.G, NT = s.NT, ti = threadIdx.x & (NT - 1), rows = BLOCK / NT, rr = threadIdx.x / NT;
@@ -444,17 +465,17 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
     auto in_row = [&](int c) { return c; };
     float wl[NE], wr[NE];      // scale * ls * w_post, w_pre
     auto branch_weights = [&] {
-        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
+        weights<NE, U, W>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
         if (has_post) {
             float wg[NE];
-            weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
+            weights<NE, U, W>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
 #pragma unroll
             for (int j = 0; j < NE; ++j) wl[j] *= wg[j];
         }
     };
     if constexpr (NC == 1) {
         branch_weights();
-        if (has_y) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
+        if (has_y) weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
 #pragma unroll
             for (int j = 0; j < NE; ++j) ss += v[j] * v[j];
             const float inv = inv_rms(sums.over_row(ss, NT, turn) * inv_d, a.eps);
-            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
+            if constexpr (NC > 1) weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
             if (in) RowE::template write<FULL>(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E))), ti, NT, D, s.wide_a, v);
@@ -540,9 +561,9 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U>::CTAS) forw
 
 // ---- backward ---------------------------------------------------------------------------------------------
 
-template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
-    using RowR = Row<R, BLOCK, NC, U>;
-    using RowE = Row<E, BLOCK, NC, U>;
+template <typename R, typename E, int BLOCK, int NC, int U, int W> struct Backward {
+    using RowR = Row<R, BLOCK, NC, U, W>;
+    using RowE = Row<E, BLOCK, NC, U, W>;
     static constexpr int NE = 8 * NC, NU = NE / U;
     static constexpr int STEP = 2 * RowR::BYTES + 3 * RowE::BYTES;
     static constexpr int CTAS = BLOCK == 256 ? 2 : 1;                             // of an SM
@@ -553,17 +574,17 @@ template <typename R, typename E, int BLOCK, int NC, int U> struct Backward {
 };
 
 // part: [grid][G + 2 D], the CTA's sums for w_post, ls and w_pre.
-template <typename R, typename E, int BLOCK, int NC, int U, bool FULL>
-__global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) backward(Shape s, NormIn a, const R *dro, int64_t lddro,
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL, int W>
+__global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U, W>::CTAS) backward(Shape s, NormIn a, const R *dro, int64_t lddro,
                                                                                       const E *dy, int64_t lddy, NormGrads g, float *part)
 {
-    using B = Backward<R, E, BLOCK, NC, U>;
+    using B = Backward<R, E, BLOCK, NC, U, W>;
     using RowR = typename B::RowR;
     using RowE = typename B::RowE;
     constexpr int NE = B::NE, NU = B::NU, S = B::S;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ Sums<BLOCK> sums, sums_o, sums_e;
-    __shared__ GroupSums<BLOCK, NU, U> groups_o, groups_e;
+    __shared__ GroupSums<BLOCK, NU, U, W> groups_o, groups_e;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
     R *dr = static_cast<R *>(g.dr);
@@ -619,9 +640,9 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     for (int j = 0; j < NE; ++j) acc_g[j] = acc_l[j] = acc_r[j] = 0.f;
     float wg[NE], wl[NE], wr[NE];
     if constexpr (NC == 1) {
-        weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
-        weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
-        weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
+        weights<NE, U, W>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
+        weights<NE, U, W>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
+        weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
     }
     int slot = 0, turn = 0;
     for (; t0 < s.T; t0 += step) {
@@ -644,10 +665,11 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         float ov[NE], rv[NE], e[NE];
         float ss = 0.f, ev_r = 0.f;             // sums of r^2 and of e r over the row
         float so[NU];                           // of o^2 over the groups
+        auto inverse = [&](float sum) { return in ? inv_rms(sum * inv_g, a.eps) : 0.f; };     // no row: zeros, also with eps = 0
         if (has_pre) {
             RowR::template read<(S > 0)>(b, row_at(r, t, lr), ti, NT, D, in, rv);
             RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy), ti, NT, D, in, e);
-            if constexpr (NC > 1) weights<NE, U>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
+            if constexpr (NC > 1) weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
                 ss = fmaf(rv[j], rv[j], ss);
@@ -667,10 +689,14 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
                 }
                 if (G == D) {
                     all = sums_o.over_row(all, NT, turn);
+                    if constexpr (U <= 2) all = inverse(all);      // one for all of the thread's runs
 #pragma unroll
                     for (int q = 0; q < NU; ++q) so[q] = all;
                 } else {
                     groups_o.over_group(so, G, turn);
+                    if constexpr (U <= 2)
+#pragma unroll
+                        for (int q = 0; q < NU; ++q) so[q] = inverse(so[q]);
                 }
             }
         }
@@ -683,7 +709,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
         }
         if (has_pre) {
             sums.over_row(ss, ev_r, NT, turn);
-            const float inv = in ? inv_rms(ss * inv_d, a.eps) : 0.f, mean = ev_r * inv_d * inv;   // no row: zeros, also with eps = 0
+            const float inv = in ? inv_rms(ss * inv_d, a.eps) : 0.f, mean = ev_r * inv_d * inv;   // no row: as above
             if ((!FULL || U == 1) && D == 1) {
                 v[0] += unit_grad_of_one(e[0] * wr[0], inv, a.eps);
                 acc_r[0] = fmaf(e[0], rv[0] * inv, acc_r[0]);
@@ -701,13 +727,13 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
             float gz[NE];
             if (z) RowE::template read<(S > 0)>(b + O_Z, row_at(z, t, lz), ti, NT, D, in, gz);
             if constexpr (NC > 1) {
-                weights<NE, U>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
-                weights<NE, U>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
+                weights<NE, U, W>(a.w_post, 1.f, in_group, ti, NT, D, s.wide_w, wg);
+                weights<NE, U, W>(a.ls, a.scale, in_row, ti, NT, D, s.wide_w, wl);
             }
             float ev[NU], inv[NU];
 #pragma unroll
             for (int q = 0; q < NU; ++q) {
-                inv[q] = !has_post ? 1.f : in ? inv_rms(so[q] * inv_g, a.eps) : 0.f;
+                inv[q] = !has_post ? 1.f : U <= 2 ? so[q] : inverse(so[q]);
                 ev[q] = 0.f;
             }
             // channel j with the gate's value and derivative times v: v becomes the gradient of hat, ov becomes hat
@@ -769,7 +795,7 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U>::CTAS) bac
     auto put = [&](const float (&acc)[NE]) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NE; ++j) fold[(threadIdx.x / NT) * width + (ti + (j / U) * NT) * U + j % U] = acc[j];
+        for (int j = 0; j < NE; ++j) fold[(threadIdx.x / NT) * width + channel_of<U, NE, W>(ti, NT, j)] = acc[j];
         __syncthreads();
     };
     if (g.dw_post) {
@@ -806,22 +832,23 @@ inline bool rows_on(const void *p, int64_t ld, int elem, int on = 16)
     return !p || ((reinterpret_cast<uintptr_t>(p) & (on - 1)) == 0 && (ld * elem & (on - 1)) == 0);
 }
 
-// Threads of a row: as many as hold it in 8 nc channels each, and a group's where runs are short.
-inline int threads_of_row(int D, int G, int nc, int U)
+// Threads of a row: as many as hold it in 8 nc channels each; W at least where runs are short, a group's where they
+// are four channels.
+inline int threads_of_row(int D, int G, int nc, int U, int W)
 {
-    int nt = 4;
+    int nt = U <= 2 ? W : 4;
     while (static_cast<int64_t>(nt) * 8 * nc < D) nt *= 2;
-    if (G < D)
+    if (G < D && U > 2)
         while (nt * U < G) nt *= 2;
     return nt;
 }
 
-template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false>
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false, int W = 32>
 cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, void *y, int64_t ldy, cudaStream_t stream)
 {
-    using F = Forward<R, E, BLOCK, NC, U>;
-    s.NT = threads_of_row(s.D, s.G, NC, U);
-    auto fn = forward<R, E, BLOCK, NC, U, FULL>;
+    using F = Forward<R, E, BLOCK, NC, U, W>;
+    s.NT = threads_of_row(s.D, s.G, NC, U, W);
+    auto fn = forward<R, E, BLOCK, NC, U, FULL, W>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), F::SMEM)) return e;
     // With one barrier a row, fewer CTAs read and write the rows more nearly in order and are faster (16384 x 4096 with a
     // residual in fp32: 164 us on one CTA of 512 threads an SM, 177 us on two); with two barriers a row the second CTA
@@ -833,13 +860,13 @@ cudaError_t run_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, voi
     return cudaGetLastError();
 }
 
-template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false>
+template <typename R, typename E, int BLOCK, int NC, int U, bool FULL = false, int W = 32>
 cudaError_t run_backward(Shape s, const NormIn &a, const void *dro, int64_t lddro, const void *dy, int64_t lddy, const NormGrads &g,
                          float *part, int *grid, cudaStream_t stream)
 {
-    using B = Backward<R, E, BLOCK, NC, U>;
-    s.NT = threads_of_row(s.D, s.G, NC, U);
-    auto fn = backward<R, E, BLOCK, NC, U, FULL>;
+    using B = Backward<R, E, BLOCK, NC, U, W>;
+    s.NT = threads_of_row(s.D, s.G, NC, U, W);
+    auto fn = backward<R, E, BLOCK, NC, U, FULL, W>;
     if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), B::SMEM)) return e;
     const int64_t rows = BLOCK / s.NT, want = (s.T + rows - 1) / rows, full = B::CTAS * sm_count(), most = full < MAX_GRID ? full : MAX_GRID;
     *grid = static_cast<int>(want < most ? want : most);
@@ -875,9 +902,11 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
     if (a.r && a.o && a.w_post && r_out && y && s.D <= 4096) {
         if (s.D % 2 == 0 && rows_on(a.r, a.ldr, re, 2 * re) && rows_on(a.o, a.ldo, e, 2 * e) && rows_on(a.z, a.ldz, e, 2 * e) &&
             rows_on(r_out, ldro, re, 2 * re) && rows_on(y, ldy, e, 2 * e))
-            return s.D <= 2048 ? run_forward<R, E, 256, 1, 2, true>(s, a, r_out, ldro, y, ldy, stream)
+            return s.D <= 128    ? run_forward<R, E, 256, 1, 2, true, 16>(s, a, r_out, ldro, y, ldy, stream)
+                   : s.D <= 2048 ? run_forward<R, E, 256, 1, 2, true>(s, a, r_out, ldro, y, ldy, stream)
                                : run_forward<R, E, 512, 1, 2, true>(s, a, r_out, ldro, y, ldy, stream);
-        return s.D <= 2048 ? run_forward<R, E, 256, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream)
+        return s.D <= 128    ? run_forward<R, E, 256, 1, 1, true, 16>(s, a, r_out, ldro, y, ldy, stream)
+               : s.D <= 2048 ? run_forward<R, E, 256, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream)
                            : run_forward<R, E, 512, 1, 1, true>(s, a, r_out, ldro, y, ldy, stream);
     }
     return KDA_NORM_PICK(run_forward, R, E, 1, s, a, r_out, ldro, y, ldy, stream);
@@ -904,9 +933,11 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
         if (s.D % 2 == 0 && rows_on(a.r, a.ldr, re, 2 * re) && rows_on(dro, lddro, re, 2 * re) && rows_on(dy, lddy, e, 2 * e) &&
             rows_on(a.o, a.ldo, e, 2 * e) && rows_on(a.z, a.ldz, e, 2 * e) && rows_on(g.dr, g.lddr, re, 2 * re) &&
             rows_on(g.d_o, g.lddo, e, 2 * e) && rows_on(g.dz, g.lddz, e, 2 * e))
-            return s.D <= 2048 ? run_backward<R, E, 256, 1, 2, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+            return s.D <= 128    ? run_backward<R, E, 256, 1, 2, true, 16>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+                   : s.D <= 2048 ? run_backward<R, E, 256, 1, 2, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
                                : run_backward<R, E, 512, 1, 2, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
-        return s.D <= 2048 ? run_backward<R, E, 256, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+        return s.D <= 128    ? run_backward<R, E, 256, 1, 1, true, 16>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
+               : s.D <= 2048 ? run_backward<R, E, 256, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
                            : run_backward<R, E, 512, 1, 1, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream);
     }
     return KDA_NORM_PICK(run_backward, R, E, 1, s, a, dro, lddro, dy, lddy, g, part, grid, stream);
