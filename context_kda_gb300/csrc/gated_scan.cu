@@ -6,18 +6,18 @@ namespace {
 
 // ---- forward --------------------------------------------------------------------------------------------
 
-template <typename E, bool SH> struct __align__(16) ForwardShared {
+template <typename E, bool SH, int G> struct __align__(16) ForwardShared {
     Rows<float, SH> g;
     Rows<E, SH> x, i;
-    Shared s;
+    Shared<G> s;
 };
 
-template <typename E, bool SH, bool ADJ, bool CHAIN>
-__global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH>>()) scan_forward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch, void *h_,
+template <typename E, bool SH, bool ADJ, bool CHAIN, int G>
+__global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) scan_forward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch, void *h_,
                                                               int64_t ldh, float *final_state, float *states)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<ForwardShared<E, SH> *>(smem_raw);
+    auto &sm = *reinterpret_cast<ForwardShared<E, SH, G> *>(smem_raw);
     if (!plan_matches(plan, sig)) {
         if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         return;
@@ -219,9 +219,17 @@ cudaError_t launch_scan_forward(const int32_t *plan_host, const int32_t *plan_de
         using E = decltype(ev);
         return by_lie(Lie().with(in.x, in.ldx, sizeof(E)).with(in.i, in.ldi, sizeof(E)).with(in.g, in.ldg, 4), [&](auto shift, auto adj) {
             constexpr bool SH = decltype(shift)::value, ADJ = decltype(adj)::value;
-            using Sh = ForwardShared<E, SH>;
-            return run(scan_forward<E, SH, ADJ, false>, scan_forward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
-                       plan_dev, D, ws, stream, in, h, ldh, final_state, states);
+            auto form = [](auto chain, auto group) {
+                constexpr bool CHAIN = decltype(chain)::value;
+                constexpr int G = decltype(group)::value;
+                using Sh = ForwardShared<E, SH, G>;
+                using K = decltype(&scan_forward<E, SH, ADJ, CHAIN, G>);
+                return Form<K>{scan_forward<E, SH, ADJ, CHAIN, G>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>()};
+            };
+            using Wide = std::integral_constant<int, WIDE_GROUP>;
+            using Narrow = std::integral_constant<int, NARROW_GROUP>;
+            return run(form(std::false_type{}, Wide{}), form(std::true_type{}, Wide{}), form(std::true_type{}, Narrow{}), plan_host, plan_dev, D, ws,
+                       stream, in, h, ldh, final_state, states);
         });
     });
 }

@@ -14,8 +14,8 @@
 // kernel waits rather than computes (for copies, for other tiles' maps), so four CTAs share an SM, each in another phase;
 // a tile's copies are requested as soon as the last tile's have gone to registers.
 //
-// Measured on the device (bf16, share of a copy's 6.79 TB/s): wide inputs are bound by memory, 65536 x 4096 413 us (96 %),
-// 16384 x 4096 111 us (89 %; 119 us with two CTAs of 256 threads an SM) and its gradients 206 us (87 %; 277 us); what is
+// Measured on the device (bf16, share of a copy's 6.79 TB/s): wide inputs are bound by memory, 65536 x 4096 408 us (97 %),
+// 16384 x 4096 109 us (91 %; 119 us with two CTAs of 256 threads an SM) and its gradients 200 us (89 %; 277 us); what is
 // left is the first tiles' way in and the last ones' way out.  Narrow inputs are bound by the state's way along the
 // chain, about a microsecond a group: 49274 x 128 26 us (36 %), 16384 x 1024 37 us (67 %).  Rows that do not start on 16 bytes
 // are bound by instructions, 16384 x 1001 50 us (48 %) and its gradients 91 us (48 %); the smallest by the launch,
@@ -58,9 +58,10 @@ constexpr int WARPS = RUNS / 2, THREADS = WARPS * 32;
 // CTAs of an SM: four, or as many as their shared memory allows.
 template <typename Sh> constexpr int ctas_of() { return 233472 / (static_cast<int>(sizeof(Sh)) + 1024) < 4 ? 233472 / (static_cast<int>(sizeof(Sh)) + 1024) : 4; }
 // Tiles of a group.  Narrow inputs wait for the state's way from group to group, which a long group shortens, at the cost
-// of more maps that a tile reads and folds (16384 tokens x 4096 and 49274 x 128 channels in bf16: groups of 8 110 and 40 us,
-// of 16 110 and 26 us, of 32 114 and 22 us).
-constexpr int GROUP = 16;
+// of more maps that a tile reads and folds (bf16, groups of 8 / 16: 65536 tokens x 4096 channels, 128 ranges of channels, 408 / 414 us
+// and gradients of 16384 x 4096 200 / 206 us; 16384 x 1024, 32 ranges, 39 / 37 us; 49274 x 128, 4 ranges, 40 / 26 us; of 32, the
+// last takes 22 us and the others are slower than with 16).
+constexpr int WIDE_GROUP = 8, NARROW_GROUP = 16, WIDE_RANGES = 64;
 // Tiles that a cluster covers: 512 tokens in bf16 take 4.9 us, by a chain 5.9 us, at 512 channels, and 6.3 and 7.0 us at 4096;
 // 1024 tokens 5.3 and 7.3 us, and 10.8 and 10.4 us.
 constexpr int MAX_CLUSTER = 8;
@@ -89,7 +90,7 @@ inline Layout layout_of(int64_t T, int D)
     Layout l;
     l.starts = 256;                                  // the ticket comes first
     l.state = up(l.starts + (nT + 1) * sizeof(Starts));
-    l.map = up(l.state + (nT / GROUP + 1) * Dp * 4);
+    l.map = up(l.state + (nT / WIDE_GROUP + 1) * Dp * 4);
     l.end = l.map + nT * Dp * 8;
     return l;
 }
@@ -188,11 +189,11 @@ template <typename X, bool SH> struct Run {
         }
     }
 };
-// What the runs and tiles of a channel range pass on.
-struct Shared {
+// What the runs and tiles of a channel range pass on; G: tiles of a group.
+template <int G> struct Shared {
     float2 map[RUNS][C];           // the runs' maps
     float state[RUNS][C];          // the state that enters each run
-    float2 before[GROUP - 1][C];   // maps of the group's tiles before this one (cluster: this tile's in [0])
+    float2 before[G - 1][C];   // maps of the group's tiles before this one (cluster: this tile's in [0])
     Starts starts;                 // cluster: the tile's sequence starts
     uint32_t after;
     int next, bad;
@@ -480,8 +481,8 @@ __device__ __forceinline__ float2 map_of(uint64_t w)
 // runs' maps in sh.map, left in sh.state.  The warp 'one' does what one warp can, a channel a lane: it folds the maps, passes the
 // tile's on and folds the state that enters the tile.  meanwhile() runs once this tile's map is on its way and before
 // others are waited for.  False: a wait ran out.  All threads call it, behind a barrier after the maps were written.
-template <bool CHAIN, bool REVERSE, typename Meanwhile>
-__device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, int col0, bool last, Meanwhile meanwhile)
+template <bool CHAIN, bool REVERSE, int G, typename Meanwhile>
+__device__ __forceinline__ bool incoming(Shared<G> &sh, const Chain &ch, int rt, int col0, bool last, Meanwhile meanwhile)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int one = REVERSE ? 0 : WARPS - 1;
@@ -495,12 +496,12 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
         A = fminf(A, MOST);
     }
     if constexpr (CHAIN) {
-        const int grp = rt / GROUP, pos = rt - grp * GROUP;
+        const int grp = rt / G, pos = rt - grp * G;
         uint64_t *own = ch.map + static_cast<size_t>(rt) * ch.Dp + col0 + lane;
-        if (warp == one && pos < GROUP - 1 && !last)      // the group's last tile publishes a state instead
+        if (warp == one && pos < G - 1 && !last)      // the group's last tile publishes a state instead
             st_relaxed(own, static_cast<uint64_t>(word(B)) << 32 | __float_as_uint(A));
         meanwhile();
-        constexpr int WORDS = (GROUP - 1 + WARPS - 1) / WARPS;
+        constexpr int WORDS = (G - 1 + WARPS - 1) / WARPS;
         uint64_t w[WORDS];
         const long long began = clock64();
         const uint32_t *state = ch.state + static_cast<size_t>(grp) * ch.Dp + col0 + lane;
@@ -538,7 +539,7 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
             h = __uint_as_float(from);
 #pragma unroll 5
             for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
-            if (pos == GROUP - 1 && !last && !sh.bad)
+            if (pos == G - 1 && !last && !sh.bad)
                 st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(apply(make_float2(A, B), h)));
         }
     } else {
@@ -572,8 +573,8 @@ __device__ __forceinline__ bool incoming(Shared &sh, const Chain &ch, int rt, in
 // Walks the tiles of a CTA: load(tile, part) starts the copies of a tile in two parts, work(tile, bounds, release)
 // computes it; release runs within it, once part 0's copies may be overwritten, part 1's may when it is done.  work
 // returns false when a wait ran out.
-template <bool CHAIN, bool REVERSE, typename Load, typename Work>
-__device__ __forceinline__ void walk(Shared &sh, const Chain &ch, const PlanView &pv, int D, Load load, Work work)
+template <bool CHAIN, bool REVERSE, int G, typename Load, typename Work>
+__device__ __forceinline__ void walk(Shared<G> &sh, const Chain &ch, const PlanView &pv, int D, Load load, Work work)
 {
     const int T = pv.T(), nT = tiles_of(T), nC = (D + C - 1) / C;
     const int run = threadIdx.x / 16;
@@ -686,19 +687,24 @@ template <typename F> cudaError_t by_lie(const Lie &lie, F f)
     return f(std::true_type{}, std::false_type{});
 }
 
-// Runs a tile kernel in the form that the number of tiles asks for.  cluster / chain: the two instances.
+// A form of a tile kernel: a cluster for few tiles, chains with groups of either length.
+template <typename K> struct Form {
+    K fn;
+    int smem, ctas;         // shared memory, CTAs of an SM
+};
+// Runs a tile kernel in the form that the numbers of tiles and of channel ranges ask for.
 template <typename K, typename... Args>
-cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host, const int32_t *plan_dev, int D, void *ws, cudaStream_t stream,
+cudaError_t run(Form<K> cluster, Form<K> wide, Form<K> narrow, const int32_t *plan_host, const int32_t *plan_dev, int D, void *ws, cudaStream_t stream,
                 const ScanIn &in, Args... args)
 {
     const int T = plan_host[KDA_PH_T], nT = tiles_of(T), nC = (D + C - 1) / C;
     const PlanSig sig = plan_sig(plan_host);
-    K fn = nT <= MAX_CLUSTER ? cluster : chain;
-    if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(fn), smem)) return e;
+    const Form<K> form = nT <= MAX_CLUSTER ? cluster : nC >= WIDE_RANGES ? wide : narrow;
+    if (cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(form.fn), form.smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = form.smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -715,7 +721,7 @@ cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host
         const Layout l = layout_of(T, D);
         const size_t words = (l.end - l.state) / 16;
         const size_t want = (words + 4 * 256 - 1) / (4 * 256), most = 4 * static_cast<size_t>(sm_count());
-        const int64_t tiles = static_cast<int64_t>(nT) * nC, all = static_cast<int64_t>(ctas) * sm_count();
+        const int64_t tiles = static_cast<int64_t>(nT) * nC, all = static_cast<int64_t>(form.ctas) * sm_count();
         cfg.gridDim = dim3(static_cast<unsigned>(tiles < all ? tiles : all));
         chain_init<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
             plan_dev, sig, nT, static_cast<int>(cfg.gridDim.x), ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
@@ -723,7 +729,7 @@ cudaError_t run(K cluster, K chain, int smem, int ctas, const int32_t *plan_host
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
     }
-    return cudaLaunchKernelEx(&cfg, fn, plan_dev, sig, D, in, ch, args...);
+    return cudaLaunchKernelEx(&cfg, form.fn, plan_dev, sig, D, in, ch, args...);
 }
 
 }  // namespace

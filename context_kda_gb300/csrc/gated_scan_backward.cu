@@ -6,21 +6,21 @@ namespace {
 
 // ---- backward -------------------------------------------------------------------------------------------
 
-template <typename E, bool SH> struct __align__(16) BackwardShared {
+template <typename E, bool SH, int G> struct __align__(16) BackwardShared {
     Rows<float, SH> g;
     Rows<E, SH> x, i, dh;
     float2 fmap[RUNS][C];          // the runs' maps of the states, forwards
     float fstate[RUNS][C];         // the state that enters each run
-    Shared s;
+    Shared<G> s;
 };
 
-template <typename E, bool SH, bool ADJ, bool CHAIN>
-__global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH>>()) scan_backward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch,
+template <typename E, bool SH, bool ADJ, bool CHAIN, int G>
+__global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) scan_backward(const int32_t *plan, PlanSig sig, int D, ScanIn in, Chain ch,
                                                                                     const float *states, const void *dh_, int64_t lddh,
                                                                                     const float *dfinal, ScanGrads out)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<BackwardShared<E, SH> *>(smem_raw);
+    auto &sm = *reinterpret_cast<BackwardShared<E, SH, G> *>(smem_raw);
     if (!plan_matches(plan, sig)) {
         if (threadIdx.x == 0) record_status(&g_scan_status, KDA_ERR_INVALID_ARG);
         return;
@@ -210,9 +210,17 @@ cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_d
         const Lie lie = Lie().with(in.x, in.ldx, sizeof(E)).with(in.i, in.ldi, sizeof(E)).with(in.g, in.ldg, 4).with(dh, lddh, sizeof(E));
         return by_lie(lie, [&](auto shift, auto adj) {
             constexpr bool SH = decltype(shift)::value, ADJ = decltype(adj)::value;
-            using Sh = BackwardShared<E, SH>;
-            return run(scan_backward<E, SH, ADJ, false>, scan_backward<E, SH, ADJ, true>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>(), plan_host,
-                       plan_dev, D, ws, stream, in, states, dh, lddh, dfinal, out);
+            auto form = [](auto chain, auto group) {
+                constexpr bool CHAIN = decltype(chain)::value;
+                constexpr int G = decltype(group)::value;
+                using Sh = BackwardShared<E, SH, G>;
+                using K = decltype(&scan_backward<E, SH, ADJ, CHAIN, G>);
+                return Form<K>{scan_backward<E, SH, ADJ, CHAIN, G>, static_cast<int>(sizeof(Sh)), ctas_of<Sh>()};
+            };
+            using Wide = std::integral_constant<int, WIDE_GROUP>;
+            using Narrow = std::integral_constant<int, NARROW_GROUP>;
+            return run(form(std::false_type{}, Wide{}), form(std::true_type{}, Wide{}), form(std::true_type{}, Narrow{}), plan_host, plan_dev, D, ws,
+                       stream, in, states, dh, lddh, dfinal, out);
         });
     });
 }
