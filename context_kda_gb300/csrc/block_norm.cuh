@@ -18,15 +18,15 @@
 // of 1002 channels with an fp32 residual: 50 and 55 us).
 // FULL instances are for the usual call: every part but the gate is there and, unless U = 1, D is a multiple of U and
 // outputs lie as inputs do.  They decide nothing about that per row, which is a third of the instructions of the
-// others and bounds them (16384 x 2048 gradients in bf16: 114 us, 92 us with FULL).
+// others and bounds them (16384 x 2048 gradients in bf16: 114 us, 92 us with FULL, both in scalar instructions).
 // Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 //
 // Measured on the device (share of a copy's 6.79 TB/s): forward of 65536 x 4096 in bf16 with an fp32 residual 546 us (101 %),
-// of 16384 x 4096 all in bf16 84 us (94 %); gradients of 16384 x 4096 with an fp32 residual 227 us (96 %), of 16384 x 2048 in
-// bf16 92 us (86 %), of 8192 x 2048 51 us (77 %): the launches, the first rows' way in and the column sums take 6 us of
+// of 16384 x 4096 all in bf16 84 us (94 %); gradients of 16384 x 4096 with an fp32 residual 216 us (101 %), of 16384 x 2048 in
+// bf16 88 us (90 %), of 8192 x 2048 50 us (80 %): the launches, the first rows' way in and the column sums take 6 us of
 // any call.  Unaligned rows are bound by instructions, gradients of 8198 x 1001 in fp32 56 us (69 %); above 4096 channels the weights
-// are read again for every row, 8192 x 8192 in bf16 117 us (84 %) and gradients 336 us (47 %: the column sums leave no registers
+// are read again for every row, 8192 x 8192 in bf16 117 us (84 %) and gradients 346 us (46 %: the column sums leave no registers
 // for the row, and some of it is kept in local memory).
 #pragma once
 
@@ -375,6 +375,51 @@ __device__ __forceinline__ float rcp(float x)
 __device__ __forceinline__ float inv_rms(float mean_sq, float eps) { return rsqrtf(mean_sq + eps); }
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + tc::ex2_ftz(z * -1.4426950408889634f)); }   // exp = infinity: 0
 
+// Two channels in one instruction, each as the scalar one would round it (16384 x 2048 gradients in
+// bf16: 88 us, 92 us in scalar ones).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+template <int N> __device__ __forceinline__ float2 at(const float (&v)[N], int j) { return make_float2(v[j], v[j + 1]); }
+template <int N> __device__ __forceinline__ void set(float (&v)[N], int j, float2 p) { v[j] = p.x, v[j + 1] = p.y; }
+__device__ __forceinline__ float2 sigmoid2(float2 z)
+{
+    const float2 w = mul2(z, two(-1.4426950408889634f));
+    const float2 d = fma2(make_float2(tc::ex2_ftz(w.x), tc::ex2_ftz(w.y)), two(1.f), two(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+// Sums over runs of U of products that come in pairs of channels.
+template <int NE, int U> struct RunSums {
+    float2 s[U == 1 ? NE / 2 : NE / U];
+    __device__ __forceinline__ RunSums()
+    {
+#pragma unroll
+        for (float2 &p : s) p = two(0.f);
+    }
+    __device__ __forceinline__ void add(int j, float2 a, float2 b)
+    {
+        float2 &p = s[U == 1 ? j / 2 : j / U];
+        p = fma2(a, b, p);
+    }
+    __device__ __forceinline__ float run(int q) const { return U == 1 ? (q % 2 ? s[q / 2].y : s[q / 2].x) : s[q].x + s[q].y; }
+};
+
 // The gradient of a group of one channel from e, the gradient of hat = v inv.
 __device__ __forceinline__ float unit_grad_of_one(float e, float inv, float eps) { return e * (eps * inv) * (inv * inv); }
 
@@ -670,23 +715,24 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U, W>::CTAS) 
             RowR::template read<(S > 0)>(b, row_at(r, t, lr), ti, NT, D, in, rv);
             RowE::template read<(S > 0)>(b + O_DY, row_at(dy, t, ldy), ti, NT, D, in, e);
             if constexpr (NC > 1) weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
+            float2 s2 = two(0.f), e2 = two(0.f);
 #pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                ss = fmaf(rv[j], rv[j], ss);
-                ev_r = fmaf(e[j] * wr[j], rv[j], ev_r);
+            for (int j = 0; j < NE; j += 2) {
+                s2 = fma2(at(rv, j), at(rv, j), s2);
+                e2 = fma2(mul2(at(e, j), at(wr, j)), at(rv, j), e2);
             }
+            ss = s2.x + s2.y;
+            ev_r = e2.x + e2.y;
         }
         if (has_o) {
             RowE::template read<(S > 0)>(b + O_O, row_at(o, t, lo), ti, NT, D, in, ov);
             if (has_post) {
                 float all = 0.f;
+                RunSums<NE, U> o2;
 #pragma unroll
-                for (int q = 0; q < NU; ++q) {
-                    so[q] = 0.f;
+                for (int j = 0; j < NE; j += 2) o2.add(j, at(ov, j), at(ov, j));
 #pragma unroll
-                    for (int j = 0; j < U; ++j) so[q] = fmaf(ov[q * U + j], ov[q * U + j], so[q]);
-                    all += so[q];
-                }
+                for (int q = 0; q < NU; ++q) all += so[q] = o2.run(q);
                 if (G == D) {
                     all = sums_o.over_row(all, NT, turn);
                     if constexpr (U <= 2) all = inverse(all);      // one for all of the thread's runs
@@ -715,10 +761,10 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U, W>::CTAS) 
                 acc_r[0] = fmaf(e[0], rv[0] * inv, acc_r[0]);
             } else {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    const float hat = rv[j] * inv;
-                    acc_r[j] = fmaf(e[j], hat, acc_r[j]);
-                    v[j] = fmaf(inv, fmaf(-hat, mean, e[j] * wr[j]), v[j]);
+                for (int j = 0; j < NE; j += 2) {
+                    const float2 hat = mul2(at(rv, j), two(inv));
+                    set(acc_r, j, fma2(at(e, j), hat, at(acc_r, j)));
+                    set(v, j, fma2(two(inv), fma2(hat, two(-mean), mul2(at(e, j), at(wr, j))), at(v, j)));
                 }
             }
         }
@@ -732,36 +778,38 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U, W>::CTAS) 
             }
             float ev[NU], inv[NU];
 #pragma unroll
-            for (int q = 0; q < NU; ++q) {
-                inv[q] = !has_post ? 1.f : U <= 2 ? so[q] : inverse(so[q]);
-                ev[q] = 0.f;
-            }
-            // channel j with the gate's value and derivative times v: v becomes the gradient of hat, ov becomes hat
-            auto channel = [&](int j, float va, float vs) {
-                const float hat = ov[j] * inv[j / U], n = hat * wg[j], dn = va * wl[j];
-                acc_l[j] = fmaf(va, n, acc_l[j]);      // times the scale, at the end
-                acc_g[j] = fmaf(dn, hat, acc_g[j]);
-                gz[j] = vs * wl[j] * n;
-                v[j] = dn * wg[j];
-                ov[j] = hat;
-                ev[j / U] = fmaf(v[j], hat, ev[j / U]);
+            for (int q = 0; q < NU; ++q) inv[q] = !has_post ? 1.f : U <= 2 ? so[q] : inverse(so[q]);
+            auto inv2 = [&](int j) { return make_float2(inv[j / U], inv[(j + 1) / U]); };
+            RunSums<NE, U> e2;
+            // channels j and j + 1 with the gate's value and derivative times v: v becomes the gradient of hat, ov becomes hat
+            auto channels = [&](int j, float2 va, float2 vs) {
+                const float2 hat = mul2(at(ov, j), inv2(j)), n = mul2(hat, at(wg, j)), dn = mul2(va, at(wl, j));
+                set(acc_l, j, fma2(va, n, at(acc_l, j)));      // times the scale, at the end
+                set(acc_g, j, fma2(dn, hat, at(acc_g, j)));
+                set(gz, j, mul2(mul2(vs, at(wl, j)), n));
+                const float2 dhat = mul2(dn, at(wg, j));
+                set(v, j, dhat);
+                set(ov, j, hat);
+                e2.add(j, dhat, hat);
             };
             if (a.gate == KDA_GATE_SIGMOID) {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    const float p = sigmoid(gz[j]), va = v[j] * p;
-                    channel(j, va, fmaf(-va, p, va));
+                for (int j = 0; j < NE; j += 2) {
+                    const float2 p = sigmoid2(at(gz, j)), va = mul2(at(v, j), p);
+                    channels(j, va, mul2(va, fma2(p, two(-1.f), two(1.f))));
                 }
             } else if (a.gate == KDA_GATE_SILU) {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    const float p = sigmoid(gz[j]), va = v[j] * p;
-                    channel(j, va * gz[j], va * fmaf(gz[j], 1.f - p, 1.f));
+                for (int j = 0; j < NE; j += 2) {
+                    const float2 z2 = at(gz, j), p = sigmoid2(z2), va = mul2(at(v, j), p);
+                    channels(j, mul2(va, z2), mul2(va, fma2(z2, fma2(p, two(-1.f), two(1.f)), two(1.f))));
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) channel(j, v[j], 0.f);
+                for (int j = 0; j < NE; j += 2) channels(j, at(v, j), two(0.f));
             }
+#pragma unroll
+            for (int q = 0; q < NU; ++q) ev[q] = e2.run(q);
             if (dz && in) RowE::template write<FULL>(row_at(dz, t, static_cast<uint32_t>(g.lddz * sizeof(E))), ti, NT, D, s.wide_b, gz);
             if (has_post) {
                 if (G == D) {
@@ -778,7 +826,10 @@ __global__ void __launch_bounds__(BLOCK, Backward<R, E, BLOCK, NC, U, W>::CTAS) 
                     v[0] = unit_grad_of_one(v[0], inv[0], a.eps);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < NE; ++j) v[j] = inv[j / U] * fmaf(-ov[j], ev[j / U] * inv_g, v[j]);
+                    for (int q = 0; q < NU; ++q) ev[q] *= -inv_g;
+#pragma unroll
+                    for (int j = 0; j < NE; j += 2)
+                        set(v, j, mul2(inv2(j), fma2(at(ov, j), make_float2(ev[j / U], ev[(j + 1) / U]), at(v, j))));
                 }
             }
             if (in) RowE::template write<FULL>(row_at(d_o, t, static_cast<uint32_t>(g.lddo * sizeof(E))), ti, NT, D, s.wide_a, v);
@@ -922,7 +973,7 @@ cudaError_t pick_backward(Shape s, const NormIn &a, const void *dro, int64_t ldd
         s.wide_r = rows_on(g.dr, g.lddr, re);
         s.wide_a = rows_on(g.d_o, g.lddo, e);
         s.wide_b = rows_on(g.dz, g.lddz, e);
-        // above 4096 channels the other way round, registers being short: 336 us on 512 threads, 457 us on 1024
+        // above 4096 channels the other way round, registers being short: 346 us on 512 threads, 457 us on 1024
         if (a.w_pre && dro && a.o && a.w_post && s.wide_r && s.wide_a && s.wide_b && s.D % 8 == 0 && s.D <= 8192)
             return s.D <= 2048   ? run_backward<R, E, 256, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
                    : s.D <= 4096 ? run_backward<R, E, 512, 1, WIDE<R>, true>(s, a, dro, lddro, dy, lddy, g, part, grid, stream)
