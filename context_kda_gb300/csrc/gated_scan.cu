@@ -45,16 +45,14 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) s
         gr.each([&](int j, const float *row) {
             float gv[V];
             get<ADJ>(row, l, gv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
+            set(a[j], decay2(both(gv)));
         });
         xr.each([&](int j, const E *row) { get<ADJ>(row, l, u[j]); });
         if (ig)
             ir.each([&](int j, const E *row) {
                 float iv[V];
                 get<ADJ>(row, l, iv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
+                set(u[j], mul2(both(u[j]), both(iv)));
             });
         // a becomes the product of the decays up to the token (ANY: -1 behind a start), u the state from zero, or from
         // its sequence's start
@@ -69,12 +67,15 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) s
 #pragma unroll
                         for (int v = 0; v < V; ++v) A[v] = -1.f;
                     }
+                if constexpr (K == ONE)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) B[v] = j == place ? h0[v] : B[v];
-                    u[j][v] = B[v] = fmaf(a[j][v], B[v], u[j][v]);
-                    a[j][v] = A[v] = K == ANY && A[v] < 0.f ? -1.f : A[v] * a[j][v];
-                }
+                    for (int v = 0; v < V; ++v) B[v] = j == place ? h0[v] : B[v];
+                const float2 b2 = fma2(both(a[j]), both(B), both(u[j])), a2 = mul2(both(A), both(a[j]));
+                set(B, b2);
+                set(u[j], b2);
+                if constexpr (K == ANY) set(A, make_float2(A[0] < 0.f ? -1.f : a2.x, A[1] < 0.f ? -1.f : a2.y));
+                else set(A, a2);
+                set(a[j], both(A));
             }
         });
         if (__any_sync(0xffffffffu, !(a[RUN - 1][0] <= MOST) || !(a[RUN - 1][1] <= MOST))) {
@@ -99,9 +100,9 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) s
                 if (final_state && place >= 1 && place <= RUN) fin = final_state + static_cast<int64_t>(b.first - 1) * D + t.col0;
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
+                set(s, fma2(both(a[j]), both(h), both(u[j])));
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    s[v] = fmaf(a[j][v], h[v], u[j][v]);
                     if constexpr (K == ONE || K == EDGE) s[v] = j >= place ? u[j][v] : s[v];
                     if constexpr (K == ANY) s[v] = a[j][v] < 0.f ? u[j][v] : s[v];
                 }

@@ -59,16 +59,14 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) 
         gr.each([&](int j, const float *row) {
             float gv[V];
             get<ADJ>(row, l, gv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[j][v] = decay(gv[v]);
+            set(a[j], decay2(both(gv)));
         });
         xr.each([&](int j, const E *row) { get<ADJ>(row, l, u[j]); });
         if (ig)
             ir.each([&](int j, const E *row) {
                 float iv[V];
                 get<ADJ>(row, l, iv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) u[j][v] *= iv[v];
+                set(u[j], mul2(both(u[j]), both(iv)));
             });
         const Run<E, SH> hr(sm.dh, run, dh, lddh, t.t0);
         float P[V] = {1.f, 1.f}, F[V] = {0.f, 0.f}, B[V] = {0.f, 0.f};   // (P, F): of the states; (P, B): of the gradients
@@ -80,22 +78,20 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) 
                 get<ADJ>(hr(j), l, d);
                 if constexpr (K == ANY)
                     if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, B);
+                if constexpr (K == ONE)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) B[v] = j + 1 == place ? df[v] : B[v];
-                    B[v] = a[j][v] * (d[v] + B[v]);
-                }
+                    for (int v = 0; v < V; ++v) B[v] = j + 1 == place ? df[v] : B[v];
+                set(B, mul2(both(a[j]), add2(both(d), both(B))));
             }
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 if constexpr (K == ANY)
                     if (b.starts >> j & 1) seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, F);
+                if constexpr (K == ONE)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE) F[v] = j == place ? h0[v] : F[v];
-                    P[v] *= a[j][v];
-                    F[v] = fmaf(a[j][v], F[v], u[j][v]);
-                }
+                    for (int v = 0; v < V; ++v) F[v] = j == place ? h0[v] : F[v];
+                set(P, mul2(both(P), both(a[j])));
+                set(F, fma2(both(a[j]), both(F), both(u[j])));
             }
         });
 #pragma unroll
@@ -125,13 +121,12 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) 
                 for (int j = 0; j < RUN; ++j) {
                     if constexpr (K == ANY)
                         if (b.starts >> j & 1) seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, f);
+                    if constexpr (K == ONE)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if constexpr (K == ONE) f[v] = j == place ? h0[v] : f[v];
-                        const float next = fmaf(a[j][v], f[v], u[j][v]);
-                        u[j][v] = f[v];
-                        f[v] = next;
-                    }
+                        for (int v = 0; v < V; ++v) f[v] = j == place ? h0[v] : f[v];
+                    const float2 next = fma2(both(a[j]), both(f), both(u[j]));
+                    set(u[j], both(f));
+                    set(f, next);
                 }
             });
         };
@@ -155,19 +150,17 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) 
                 get<ADJ>(xr(j), l, gi);
                 if constexpr (K == ANY)
                     if (ends >> j & 1) seq_row<ADJ>(dfinal, b.seq(j + 1) - 1, D, t.col0, l, true, e);
+                if constexpr (K == ONE || K == EDGE)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE || K == EDGE) e[v] = j + 1 == place ? df[v] : e[v];
-                    Gr[v] += e[v];
-                    e[v] = a[j][v] * Gr[v];
-                    gi[v] *= Gr[v];
-                    gg[v] = u[j][v] * e[v];
-                    gx[v] = Gr[v];
-                }
+                    for (int v = 0; v < V; ++v) e[v] = j + 1 == place ? df[v] : e[v];
+                set(Gr, add2(both(Gr), both(e)));
+                set(e, mul2(both(a[j]), both(Gr)));
+                set(gi, mul2(both(gi), both(Gr)));
+                set(gg, mul2(both(u[j]), both(e)));
+                set(gx, both(Gr));
                 if (ig) {
                     get<ADJ>(ir(j), l, gx);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) gx[v] *= Gr[v];
+                    set(gx, mul2(both(gx), both(Gr)));
                 }
                 if constexpr (K == ANY || K == EDGE) {
                     if (j < rows) {
