@@ -383,3 +383,16 @@ def test_growing_decays_of_a_zero_state(lengths):
     for t in (dx, di, dg):
         assert not t[a:b].any() and torch.isfinite(t).all()
     assert not dh0[-2].any() and torch.isfinite(dh0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [2048, 2049, 2050])
+def test_groups_of_a_wide_input(D, kind):
+    """Wide inputs pass their state on in shorter groups of tiles: several of them, boundaries at and within tiles."""
+    _check_all([1500, 36, 1, 640], D, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("B,D", [(3, 511), (9, 513), (40, 1001), (7, 2046)])
+def test_step_of_unaligned_rows(B, D, kind):
+    test_step(B, D, True, kind)
