@@ -587,7 +587,7 @@ int kda_block_norm_forward(int64_t T, int32_t D, int32_t res_type, int32_t type,
  *   dr          out [T][D] gradient of r (and of r'), or NULL.    d_o  out [T][D], given iff o is.
  *   dz          out [T][D] or NULL (not written).
  *   dw_post     out fp32 [group], dls, dw_pre out fp32 [D], or NULL (not written).  Sums over the rows in
- *                   an order that depends on T and D only: the same call gives the same bits.
+ *                   an order that depends on sizes, types and alignments only: the same call gives the same bits.
  *   ws, ws_bytes    device workspace of at least kda_block_norm_workspace_bytes(D) bytes.
  * T = 0 writes zeros to the weight gradients.  dr may be dr_out itself (same address and stride).
  * Returns as the forward, or KDA_ERR_WORKSPACE.
