@@ -15,7 +15,7 @@
 // one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
 // residual is fp32) where rows start on 16 bytes (a thread copies what it reads itself, without a barrier), else 2 where they
 // start on pairs and 1 anywhere (8192 rows in bf16, forward of 3970 channels: 83 us in pairs, 92 us one by one; gradients
-// of 1002 channels with an fp32 residual: 50 and 55 us).
+// of 1002 channels with an fp32 residual: 50 and 55 us, all in scalar instructions).
 // FULL instances are for the usual call: every part but the gate is there and, unless U = 1, D is a multiple of U and
 // outputs lie as inputs do.  They decide nothing about that per row, which is a third of the instructions of the
 // others and bounds them (16384 x 2048 gradients in bf16: 114 us, 92 us with FULL, both in scalar instructions).
@@ -23,10 +23,10 @@
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 //
 // Measured on the device (share of a copy's 6.79 TB/s): forward of 65536 x 4096 in bf16 with an fp32 residual 546 us (101 %),
-// of 16384 x 4096 all in bf16 84 us (94 %); gradients of 16384 x 4096 with an fp32 residual 216 us (101 %), of 16384 x 2048 in
+// of 16384 x 4096 all in bf16 86 us (92 %); gradients of 16384 x 4096 with an fp32 residual 216 us (101 %), of 16384 x 2048 in
 // bf16 88 us (90 %), of 8192 x 2048 50 us (80 %): the launches, the first rows' way in and the column sums take 6 us of
 // any call.  Unaligned rows are bound by instructions, gradients of 8198 x 1001 in fp32 56 us (69 %); above 4096 channels the weights
-// are read again for every row, 8192 x 8192 in bf16 117 us (84 %) and gradients 346 us (46 %: the column sums leave no registers
+// are read again for every row, 8192 x 8192 in bf16 115 us (86 %) and gradients 346 us (46 %: the column sums leave no registers
 // for the row, and some of it is kept in local memory).
 #pragma once
 
@@ -373,9 +373,9 @@ __device__ __forceinline__ float rcp(float x)
     return r;
 }
 __device__ __forceinline__ float inv_rms(float mean_sq, float eps) { return rsqrtf(mean_sq + eps); }
-__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + tc::ex2_ftz(z * -1.4426950408889634f)); }   // exp = infinity: 0
 
-// Two channels in one instruction (16384 x 2048 gradients in bf16: 88 us, 92 us in scalar ones).
+// Two channels in one instruction (16384 x 2048 gradients in bf16: 88 us, 92 us in scalar ones; forward of 8192 x 3970
+// 80 and 83 us).
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 template <int N> __device__ __forceinline__ float2 at(const float (&v)[N], int j) { return make_float2(v[j], v[j + 1]); }
 template <int N> __device__ __forceinline__ void set(float (&v)[N], int j, float2 p) { v[j] = p.x, v[j + 1] = p.y; }
@@ -383,7 +383,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 z)
 {
     const float2 w = mul2(z, two(-1.4426950408889634f));
     const float2 d = fma2(make_float2(tc::ex2_ftz(w.x), tc::ex2_ftz(w.y)), two(1.f), two(1.f));
-    return make_float2(rcp(d.x), rcp(d.y));
+    return make_float2(rcp(d.x), rcp(d.y));      // exp = infinity: 0
 }
 // Sums over runs of U of products that come in pairs of channels.
 template <int NE, int U> struct RunSums {
@@ -535,19 +535,18 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U, W>::CTAS) f
             if (z) RowE::template read<(S > 0)>(b + RowR::BYTES + RowE::BYTES, row_at(z, t, lz), ti, NT, D, in, g);
             if (has_post) {
                 float ss[NU];
+                RunSums<NE, U> n2;
 #pragma unroll
-                for (int q = 0; q < NU; ++q) {
-                    ss[q] = 0.f;
+                for (int j = 0; j < NE; j += 2) n2.add(j, at(n, j), at(n, j));
 #pragma unroll
-                    for (int j = 0; j < U; ++j) ss[q] += n[q * U + j] * n[q * U + j];
-                }
+                for (int q = 0; q < NU; ++q) ss[q] = n2.run(q);
                 if (G == D) {
                     float all = 0.f;
 #pragma unroll
                     for (int q = 0; q < NU; ++q) all += ss[q];
                     const float inv = inv_rms(sums.over_row(all, NT, turn++) * inv_g, a.eps);
 #pragma unroll
-                    for (int j = 0; j < NE; ++j) n[j] *= inv;
+                    for (int j = 0; j < NE; j += 2) set(n, j, mul2(at(n, j), two(inv)));
                 } else {
                     groups.over_group(ss, G, turn);
 #pragma unroll
@@ -560,24 +559,25 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U, W>::CTAS) f
             }
             if (a.gate == KDA_GATE_SIGMOID) {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) n[j] *= sigmoid(g[j]);
+                for (int j = 0; j < NE; j += 2) set(n, j, mul2(at(n, j), sigmoid2(at(g, j))));
             } else if (a.gate == KDA_GATE_SILU) {
 #pragma unroll
-                for (int j = 0; j < NE; ++j) n[j] *= g[j] * sigmoid(g[j]);
+                for (int j = 0; j < NE; j += 2) set(n, j, mul2(at(n, j), mul2(at(g, j), sigmoid2(at(g, j)))));
             }
             if constexpr (NC > 1) branch_weights();
 #pragma unroll
-            for (int j = 0; j < NE; ++j) v[j] = fmaf(wl[j], n[j], v[j]);
+            for (int j = 0; j < NE; j += 2) set(v, j, fma2(at(wl, j), at(n, j), at(v, j)));
         }
         if (has_out && in) RowR::template write<FULL>(row_at(r_out, t, static_cast<uint32_t>(ldro * sizeof(R))), ti, NT, D, s.wide_r, v);
         if (has_y) {
-            float ss = 0.f;
+            float2 s2 = two(0.f);
 #pragma unroll
-            for (int j = 0; j < NE; ++j) ss += v[j] * v[j];
+            for (int j = 0; j < NE; j += 2) s2 = fma2(at(v, j), at(v, j), s2);
+            const float ss = s2.x + s2.y;
             const float inv = inv_rms(sums.over_row(ss, NT, turn) * inv_d, a.eps);
             if constexpr (NC > 1) weights<NE, U, W>(a.w_pre, 1.f, in_row, ti, NT, D, s.wide_w, wr);
 #pragma unroll
-            for (int j = 0; j < NE; ++j) v[j] *= inv * wr[j];
+            for (int j = 0; j < NE; j += 2) set(v, j, mul2(at(v, j), mul2(two(inv), at(wr, j))));
             if (in) RowE::template write<FULL>(row_at(y, t, static_cast<uint32_t>(ldy * sizeof(E))), ti, NT, D, s.wide_a, v);
         }
         ++turn;
@@ -924,7 +924,7 @@ cudaError_t pick_forward(Shape s, const NormIn &a, void *r_out, int64_t ldro, vo
     if (rows_on(a.r, a.ldr, re) && rows_on(a.o, a.ldo, e) && rows_on(a.z, a.ldz, e)) {
         s.wide_r = rows_on(r_out, ldro, re);
         s.wide_a = rows_on(y, ldy, e);
-        // above 4096 channels: 8192 x 8192 in bf16 117 us on one CTA of 1024 threads with 8 channels each, 162 us on 512 with 16
+        // above 4096 channels: 8192 x 8192 in bf16 115 us on one CTA of 1024 threads with 8 channels each, 162 us on 512 with 16
         if (a.r && a.o && a.w_post && r_out && y && s.wide_r && s.wide_a && s.D % 8 == 0 && s.D <= 8192)
             return s.D <= 2048   ? run_forward<R, E, 256, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
                    : s.D <= 4096 ? run_forward<R, E, 512, 1, WIDE<R>, true>(s, a, r_out, ldro, y, ldy, stream)
