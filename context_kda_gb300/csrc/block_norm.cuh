@@ -261,7 +261,9 @@ template <typename X, int BLOCK, int NC, int W> struct Row<X, BLOCK, NC, 1, W> :
 template <typename X, int BLOCK, int NC, int W> struct Row<X, BLOCK, NC, 2, W> : Staged<X, BLOCK, NC, 2, W> {};
 
 // Sums over a row's NT threads (a power of two); every thread gets them.  Rows wider than a warp take one barrier: the
-// warps' sums go to one of two buffers in turn.
+// warps' sums go to one of two buffers in turn, 'turn' being the number of the CTA's step.  An object serves one sum a
+// step, whichever others the call has: a warp writes a buffer again two steps later, behind the barrier of the step in
+// between, which no warp reaches before it has read what the first of them left.
 template <int BLOCK> struct Sums {
     float part[2][2][BLOCK / 32];
     static __device__ __forceinline__ float xor_add(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U, W>::CTAS) f
     using RowE = typename F::RowE;
     constexpr int NE = F::NE, NU = F::NU, S = F::S;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ Sums<BLOCK> sums;
+    __shared__ Sums<BLOCK> sums, sums_o;
     __shared__ GroupSums<BLOCK, NU, U, W> groups;
     const R *r = static_cast<const R *>(a.r);
     const E *o = static_cast<const E *>(a.o), *z = static_cast<const E *>(a.z);
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(BLOCK, Forward<R, E, BLOCK, NC, U, W>::CTAS) f
                     float all = 0.f;
 #pragma unroll
                     for (int q = 0; q < NU; ++q) all += ss[q];
-                    const float inv = inv_rms(sums.over_row(all, NT, turn++) * inv_g, a.eps);
+                    const float inv = inv_rms(sums_o.over_row(all, NT, turn) * inv_g, a.eps);
 #pragma unroll
                     for (int j = 0; j < NE; j += 2) set(n, j, mul2(at(n, j), two(inv)));
                 } else {

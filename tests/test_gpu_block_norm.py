@@ -298,3 +298,20 @@ def test_alignment_inside(D, group, kind, res):
         want = ref.norm_backward(r_out.double().cpu().numpy(), *args, w["dr_out"], w["dy"])
         for name, a, b, k in zip(("dr", "do", "dz", "dw_post", "dls", "dw_pre"), got, want, (res, kind, kind, "f32", "f32", "f32")):
             check(a, b, k, name)
+
+
+@pytest.mark.parametrize("kind,res,D,T", [("bf16", "bf16", 512, 9001), ("bf16", "f32", 512, 9001), ("f32", "f32", 1024, 5001), ("bf16", "bf16", 2048, 2501),
+                                          ("f16", "f32", 2048, 2501), ("bf16", "f32", 4096, 1301), ("bf16", "bf16", 8192, 901), ("f32", "f32", 8192, 701),
+                                          ("bf16", "bf16", 12288, 601), ("f32", "f32", 12288, 601)])
+@pytest.mark.parametrize("gate,r", [("sigmoid", False), ("none", True)], ids=["gated norm alone", "last residual"])
+def test_whole_row_norm_without_the_next_norm(kind, res, D, T, gate, r):
+    """w_pre absent: the sum of the norm after the block is the only one of a row and its barrier the only one.  Every CTA works
+    many rows, one after the other: no row may be normed with sums of the next, and the same call gives the same bits."""
+    import torch
+    d, w = _draw(T, D, kind, res, gate, ls=r, r=r, pre=False)
+    first, y = _forward(d, T, D, kind, res, gate, 0)
+    assert y is None
+    check(first, ref.norm_forward(w["r"], w["o"], w["z"], gate, 0, w["w_post"], 0.7, w["ls"], None, EPS)[0], res, "r_out")
+    for _ in range(5):
+        again, _ = _forward(d, T, D, kind, res, gate, 0)
+        assert torch.equal(first.view(torch.uint8), again.view(torch.uint8))
