@@ -23,8 +23,8 @@
 //   - Up to 8 tiles of tokens ('cluster'): the CTAs of a channel range are one cluster; they exchange the
 //     maps through distributed shared memory.  One launch and no workspace, for short inputs, where
 //     latency counts.
-//   - More ('chain'): CTAs draw tiles in time order from a ticket, so that a tile waits only for tiles drawn
-//     before it by CTAs that run.  A tile's incoming state is folded, always in the same order, from the
+//   - More ('chain'): CTAs draw all their tiles in time order from a ticket, so that a tile waits only for tiles drawn
+//     before it by CTAs that run, and progress needs one CTA on the device, not the grid.  A tile's incoming state is folded, always in the same order, from the
 //     state at its group's start and the maps of the group's earlier tiles; the group's last tile publishes
 //     the next group's state.  Only that last step is serial in time, once a group.  Published words
 //     carry their own validity (they are all ones until written, which no published value is), so that one
@@ -109,14 +109,14 @@ inline Chain chain_of(void *ws, int64_t T, int D)
                  reinterpret_cast<uint64_t *>(b + l.map), padded(D)};
 }
 
-__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int grid, int *ticket, Starts *starts,
+__global__ void __launch_bounds__(256) chain_init(const int32_t *plan, PlanSig sig, int nT, int *ticket, Starts *starts,
                                                   uint4 *words, size_t n)
 {
     tc::grid_dep_launch();
     const size_t id = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x, step = static_cast<size_t>(gridDim.x) * blockDim.x;
     if (!plan_matches(plan, sig)) return;   // the main kernel records it
     for (size_t j = id; j < n; j += step) words[j] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    if (id == 0) *ticket = grid;
+    if (id == 0) *ticket = 0;
     const PlanView pv{plan};
     const int32_t *cu = pv.cu();
     const int lane = threadIdx.x & 31, N = pv.N();
@@ -618,13 +618,16 @@ __device__ __forceinline__ void walk(Shared<G> &sh, const Chain &ch, const PlanV
         }
         cluster_wait();
     } else {
-        // A CTA's first tile goes by its index: its copies start before the kernel that sets the workspace is waited
-        // for (blocks are dispatched in the order of their indexes, and a wait that this failed would end by its
-        // limit).  The others go by tickets, drawn ahead (k: in work, k2: next, then the one drawn while k is in work), so that neither
-        // the draw nor a tile's starts are waited for.  A CTA works its tiles in the order drawn, so the lowest
-        // unfinished tile is always in work with nothing to wait for.
+        // Every tile goes by a ticket, the first one too, so a tile belongs to a CTA that runs, however few of the grid do (a
+        // kernel on another stream may hold the rest of the device for as long as it likes).  Later tickets are drawn ahead (k: in
+        // work, k2: next, then the one drawn while k is in work), so that neither the draw nor a tile's starts are waited
+        // for.  A CTA works its tiles in the order drawn, so the lowest unfinished tile is always in work, and all that it
+        // waits for has been published.
         const int n = nT * nC;
-        int drawn = 0, k = blockIdx.x;
+        grid_dep_wait();                     // the kernel before sets the ticket
+        if (threadIdx.x == 0) sh.next = atomicAdd(ch.ticket, 1);
+        __syncthreads();
+        int drawn = 0, k = sh.next;
         uint4 bits = {};
         uint32_t after = 0;
         int first = 0;
@@ -637,7 +640,6 @@ __device__ __forceinline__ void walk(Shared<G> &sh, const Chain &ch, const PlanV
             const Tile t = tile_of<REVERSE>(k, nT, nC);
             load(t, 0);
             load(t, 1);
-            grid_dep_wait();
             words(t);
             if (threadIdx.x == 0) drawn = atomicAdd(ch.ticket, 1);
         }
@@ -734,7 +736,7 @@ cudaError_t run(Form<K> cluster, Form<K> wide, Form<K> narrow, const int32_t *pl
         const int64_t tiles = static_cast<int64_t>(nT) * nC, all = static_cast<int64_t>(form.ctas) * sm_count();
         cfg.gridDim = dim3(static_cast<unsigned>(tiles < all ? tiles : all));
         chain_init<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
-            plan_dev, sig, nT, static_cast<int>(cfg.gridDim.x), ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
+            plan_dev, sig, nT, ch.ticket, ch.starts, reinterpret_cast<uint4 *>(ch.state), words);
         if (cudaError_t e = cudaGetLastError()) return e;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;

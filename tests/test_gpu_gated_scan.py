@@ -396,3 +396,31 @@ def test_groups_of_a_wide_input(D, kind):
 @pytest.mark.parametrize("B,D", [(3, 511), (9, 513), (40, 1001), (7, 2046)])
 def test_step_of_unaligned_rows(B, D, kind):
     test_step(B, D, True, kind)
+
+
+def test_two_streams_at_once():
+    """Chains of tiles on two streams of different priority share the device: neither needs its whole grid there at once."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    lens = [[9000, 40, 3000], [7000, 5000]]
+    draws = [_draw(lens[0], 1100, "bf16", seed=5), _draw(lens[1], 1024, "bf16", seed=6)]
+    want = [_forward(cu, dev) for cu, dev, _ in draws]
+    want_grads = [_backward(cu, dev, w[2]) for (cu, dev, _), w in zip(draws, want)]
+    for (cu, _, w), (h, final, _) in zip(draws, want):
+        h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+        check(h, h_ref, "bf16", "h")
+        check(final, f_ref, "f32", "final")
+    streams = [torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for n, (cu, dev, _) in enumerate(draws):
+            with torch.cuda.stream(streams[n]):
+                f = _forward(cu, dev)
+                got[n].append(f + _backward(cu, dev, f[2]))
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == kda.KDA_OK
+    for n in range(2):
+        for one in got[n]:
+            for a, b in zip(one, want[n] + want_grads[n]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
