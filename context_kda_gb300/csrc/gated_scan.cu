@@ -54,43 +54,61 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) s
                 get<ADJ>(row, l, iv);
                 set(u[j], mul2(both(u[j]), both(iv)));
             });
-        // a becomes the product of the decays up to the token (ANY: -1 behind a start), u the state from zero, or from
-        // its sequence's start
+        // a becomes the product of the decays up to the token (of no use from the first boundary on), u the state from zero, or
+        // from its sequence's start
         by_inner_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
             float A[V] = {1.f, 1.f}, B[V] = {0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 if constexpr (K == ANY)
-                    if (b.starts >> j & 1) {
-                        seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, B);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) A[v] = -1.f;
-                    }
+                    if (b.starts >> j & 1) seq_row<ADJ>(in.h0, b.seq(j), D, t.col0, l, true, B);
                 if constexpr (K == ONE)
 #pragma unroll
                     for (int v = 0; v < V; ++v) B[v] = j == place ? h0[v] : B[v];
                 const float2 b2 = fma2(both(a[j]), both(B), both(u[j])), a2 = mul2(both(A), both(a[j]));
                 set(B, b2);
                 set(u[j], b2);
-                if constexpr (K == ANY) set(A, make_float2(A[0] < 0.f ? -1.f : a2.x, A[1] < 0.f ? -1.f : a2.y));
-                else set(A, a2);
+                set(A, a2);
                 set(a[j], both(A));
             }
         });
-        if (__any_sync(0xffffffffu, !(a[RUN - 1][0] <= MOST) || !(a[RUN - 1][1] <= MOST))) {
 #pragma unroll
-            for (int j = 0; j < RUN; ++j)
+        for (int v = 0; v < V; ++v) sm.s.map[run][chan<ADJ>(l, v)] = make_float2(b.starts ? FORGET : a[RUN - 1][v], u[RUN - 1][v]);
+        // A product that leaves fp32's range is infinite, or NaN, from there on.  If that is before the run's first boundary, the
+        // products are made again from 2^-k instead of one, and the state that enters is multiplied by 2^k: both are exact, and
+        // what the one loses among the small products the other would lose in the state.
+        int far[V] = {};           // k
+        if (__any_sync(0xffffffffu, !(a[RUN - 1][0] <= MOST_RUN) || !(a[RUN - 1][1] <= MOST_RUN))) {
+            sm.s.far = t.rt;
+            double p[V];
+            far_products<ADJ>(gr, l, place < RUN ? place : RUN, p, far);
 #pragma unroll
-                for (int v = 0; v < V; ++v) a[j][v] = fminf(a[j][v], MOST);
+            for (int v = 0; v < V; ++v)
+                if (far[v] && !b.starts) sm.s.map[run][chan<ADJ>(l, v)].x = product_of(p[v]);
+            if (__any_sync(0xffffffffu, far[0] | far[1])) {
+                float A[V] = {two_to(-far[0]), two_to(-far[1])};
+                gr.each([&](int j, const float *row) {
+                    float gv[V];
+                    get<ADJ>(row, l, gv);
+                    set(a[j], decay2(both(gv)));
+                });
+#pragma unroll
+                for (int j = 0; j < RUN; ++j) {
+                    set(A, mul2(both(A), both(a[j])));
+#pragma unroll
+                    for (int v = 0; v < V; ++v) a[j][v] = fminf(A[v], MOST);
+                }
+            }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) sm.s.map[run][chan<ADJ>(l, v)] = make_float2(b.starts ? -1.f : a[RUN - 1][v], u[RUN - 1][v]);
         __syncthreads();
         if (!incoming<CHAIN, false>(sm.s, ch, t.rt, t.col0, t.tt == nT - 1, release)) return false;
         float h[V], s[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = sm.s.state[run][chan<ADJ>(l, v)];
+        for (int v = 0; v < V; ++v) {
+            h[v] = sm.s.state[run][chan<ADJ>(l, v)];
+            if (far[v]) h[v] *= two_to(far[v]);
+        }
         E *row = h_out + (static_cast<int64_t>(t.t0) + run * RUN) * ldh + t.col0;
         by_kind(kind, [&](auto k) {
             constexpr int K = decltype(k)::value;
@@ -101,11 +119,9 @@ __global__ void __launch_bounds__(THREADS, ctas_of<ForwardShared<E, SH, G>>()) s
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 set(s, fma2(both(a[j]), both(h), both(u[j])));
+                if constexpr (K != PLAIN)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if constexpr (K == ONE || K == EDGE) s[v] = j >= place ? u[j][v] : s[v];
-                    if constexpr (K == ANY) s[v] = a[j][v] < 0.f ? u[j][v] : s[v];
-                }
+                    for (int v = 0; v < V; ++v) s[v] = j >= place ? u[j][v] : s[v];
                 if constexpr (K == EDGE) {
                     if (j < rows) put<ADJ>(at - chan<ADJ>(l, 0), l, s, left);
                     if (fin && j + 1 == place) put<ADJ>(fin, l, s, left);

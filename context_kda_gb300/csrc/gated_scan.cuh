@@ -5,7 +5,8 @@
 // One pass over the data.  Over a run of tokens the recurrence is the map h -> A h + B with A the product
 // of the decays and B the run's state from zero, and maps compose as (A2, B2) o (A1, B1) = (A1 A2, A2 B1 + B2);
 // a run in which a sequence starts forgets what came before (h -> B, marked by A = -1: decays are not
-// negative), so nothing of another sequence, infinities and NaN included, is ever multiplied in.
+// negative), so nothing of another sequence, infinities and NaN included, is ever multiplied in.  Decays may be above one
+// and their product beyond fp32's range, where a state may still be small: such an A is kept scaled, as a negative number.
 //
 // The stream is cut into tiles of 128 tokens x 32 channels, a tile into 8 runs of 16 tokens (half a warp each, two
 // channels a lane).  A CTA of four warps copies a tile to shared memory (cp.async), folds each run in
@@ -197,6 +198,7 @@ template <int G> struct Shared {
     Starts starts;                 // cluster: the tile's sequence starts
     uint32_t after;
     int next, bad;
+    int far;                       // the last tile (its number, rt) that met great products
 };
 
 // ---- copies ---------------------------------------------------------------------------------------------
@@ -354,17 +356,74 @@ __device__ __forceinline__ float2 decay2(float2 g)
 
 // ---- maps -----------------------------------------------------------------------------------------------
 
-// Decays may be above one.  A product of them that has passed fp32's range is made finite again before a state is
-// multiplied by it, so that a state of zero stays zero (a decay that is infinite by itself makes a NaN of the map's
-// other half).
-constexpr float MOST = 3.402823466e38f;
-// One map more: (A, B) becomes (a, b) o (A, B).
-__device__ __forceinline__ void then(float &A, float &B, float a, float b)
+// A map's A as a float: a product of decays of up to fp32's largest number is itself, -1 marks a map that forgets, and a
+// greater product is scaled: minus its 2^-127th part, from -2 on.  Minus infinity stands for 2^254 and more, which takes every
+// state but zero (and fp32's denormal numbers) past fp32's range; zero stays zero (a decay that is infinite by itself makes a NaN
+// of the map's other half).
+constexpr float MOST = 3.402823466e38f, FORGET = -1.f;
+constexpr float MOST_RUN = 32768.f;     // the runs' products up to which a tile's is in range
+static_assert(RUNS == 8, "2^(15 * 8) < 2^128");
+__device__ __forceinline__ float product_of(double p)
 {
-    B = a < 0.f ? b : fmaf(a, B, b);
-    A = a < 0.f || A < 0.f ? -1.f : A * a;
+    return !(p > MOST) ? static_cast<float>(p) : p < 0x1p254 ? -static_cast<float>(p * 0x1p-127) : __int_as_float(static_cast<int>(0xFF800000u));
 }
+// A run whose products may leave fp32's range: the product of its first n decays, kept at 2^1000 beyond that, and, for a channel
+// whose products in fp32 do leave it, the k that brings all of them to 2^121 and less (126 at most; else 0).  Decays that are
+// infinite by themselves, or NaN, do not count: they leave NaN behind them, and must change nothing before them.
+template <bool ADJ, typename R> __device__ __forceinline__ void far_products(const R &rows, int l, int n, double (&p)[V], int (&k)[V])
+{
+    constexpr double MAX = 0x1p1000;
+    float q[V] = {1.f, 1.f};
+    double peak[V] = {1.0, 1.0};
+    bool over[V] = {};
+    p[0] = p[1] = 1.0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        float g[V];
+        get<ADJ>(rows(j), l, g);
+        set(g, decay2(both(g)));
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = g[v] <= MOST ? g[v] : 1.f;
+        set(q, mul2(both(q), both(g)));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            over[v] = over[v] || !(q[v] <= MOST);
+            p[v] = p[v] < MAX ? fmin(p[v] * g[v], MAX) : MAX;
+            peak[v] = fmax(peak[v], p[v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = over[v] ? max(0, min((__double2hiint(peak[v]) >> 20) - 1023 - 120, 126)) : 0;
+}
+__device__ __forceinline__ float two_to(int k) { return __int_as_float((127 + k) << 23); }     // |k| <= 126
+// A state behind a map.  Scaled ones (any_apply) are rare and the folds are what tiles wait for: who makes or fetches a map that
+// may lead to one leaves a mark, and folds go by 'apply' where there is none (65536 x 4096 in bf16: 428 us with the cases
+// looked at in every step, 421 us with a tile's product looked at behind its fold, 414 us).
 __device__ __forceinline__ float apply(float2 m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
+__device__ __forceinline__ bool scaled(float lowest) { return lowest < FORGET; }
+__device__ __forceinline__ float any_apply(float2 m, float h)
+{
+    if (!scaled(m.x)) return apply(m, h);
+    if (m.x < -MOST) return h == 0.f ? m.y : fmaf(h, -m.x, m.y);
+    return fmaf(0x1p64f * h * -m.x, 0x1p63f, m.y);      // neither product leaves the range before the result does
+}
+// One map more: (A, B) becomes m o (A, B).
+__device__ __forceinline__ void then(float &A, float &B, float2 m)
+{
+    B = apply(m, B);
+    A = m.x < 0.f || A < 0.f ? FORGET : A * m.x;
+}
+// (a call: its double arithmetic in the kernels' code costs gradients of 16384 x 4096 half a percent)
+__device__ __noinline__ float any_join(float A, float a)
+{
+    auto whole = [](float x) { return x < 0.f ? fmin(static_cast<double>(x) * -0x1p127, 0x1p600) : static_cast<double>(x); };
+    return A == FORGET || a == FORGET ? FORGET : product_of(whole(A) * whole(a));
+}
+__device__ __forceinline__ void any_then(float &A, float &B, float2 m)
+{
+    B = any_apply(m, B);
+    A = any_join(A, m.x);
+}
 
 // A float as a word that is not all ones (one NaN pattern gives way to another).
 __device__ __forceinline__ uint32_t word(float x)
@@ -497,13 +556,15 @@ __device__ __forceinline__ bool incoming(Shared<G> &sh, const Chain &ch, int rt,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int one = REVERSE ? 0 : WARPS - 1;
     float A = 1.f, B = 0.f, h = 0.f;
+    bool far = sh.far == rt;           // a map may be scaled
     if (warp == one) {
+        if (far) {
+#pragma unroll 1
+            for (int r = 0; r < RUNS; ++r) any_then(A, B, sh.map[REVERSE ? RUNS - 1 - r : r][lane]);
+        } else {
 #pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            const float2 m = sh.map[REVERSE ? RUNS - 1 - r : r][lane];
-            then(A, B, m.x, m.y);
+            for (int r = 0; r < RUNS; ++r) then(A, B, sh.map[REVERSE ? RUNS - 1 - r : r][lane]);
         }
-        A = fminf(A, MOST);
     }
     if constexpr (CHAIN) {
         const int grp = rt / G, pos = rt - grp * G;
@@ -534,8 +595,13 @@ __device__ __forceinline__ bool incoming(Shared<G> &sh, const Chain &ch, int rt,
         }
 #pragma unroll
         for (int k = 0; k < WORDS; ++k)
-            if (warp + k * WARPS < pos) sh.before[warp + k * WARPS][lane] = map_of(w[k]);
+            if (warp + k * WARPS < pos) {
+                const float2 m = map_of(w[k]);
+                sh.before[warp + k * WARPS][lane] = m;
+                if (scaled(m.x)) sh.far = rt;
+            }
         __syncthreads();
+        far = far || sh.far == rt;
         if (sh.bad) return false;
         if (warp == one) {
             // the group's state may come last, and the next group's follows from it: no barrier stands in between
@@ -547,10 +613,19 @@ __device__ __forceinline__ bool incoming(Shared<G> &sh, const Chain &ch, int rt,
                 from = ld_relaxed(state);
             }
             h = __uint_as_float(from);
+            auto pass_on = [&](auto f) {
+                if (pos == G - 1 && !last && !sh.bad)
+                    st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(f(make_float2(A, B), h)));
+            };
+            if (far) {
+#pragma unroll 1
+                for (int p = 0; p < pos; ++p) h = any_apply(sh.before[p][lane], h);
+                pass_on(any_apply);
+            } else {
 #pragma unroll 5
-            for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
-            if (pos == G - 1 && !last && !sh.bad)
-                st_relaxed(ch.state + static_cast<size_t>(grp + 1) * ch.Dp + col0 + lane, word(apply(make_float2(A, B), h)));
+                for (int p = 0; p < pos; ++p) h = apply(sh.before[p][lane], h);
+                pass_on(apply);
+            }
         }
     } else {
         if (warp == one) sh.before[0][lane] = make_float2(A, B);
@@ -562,18 +637,33 @@ __device__ __forceinline__ bool incoming(Shared<G> &sh, const Chain &ch, int rt,
 #pragma unroll
             for (int p = 0; p < MAX_CLUSTER - 1; ++p)
                 m[p] = p < rt ? ld_cluster(mapa(smem_u32(&sh.before[0][lane]), p)) : make_float2(1.f, 0.f);
+            float lowest = 0.f;
 #pragma unroll
-            for (int p = 0; p < MAX_CLUSTER - 1; ++p) h = p < rt ? apply(m[p], h) : h;
+            for (int p = 0; p < MAX_CLUSTER - 1; ++p) {
+                h = p < rt ? apply(m[p], h) : h;
+                lowest = fminf(lowest, m[p].x);
+            }
+            if (scaled(lowest)) {
+                h = 0.f;
+#pragma unroll
+                for (int p = 0; p < MAX_CLUSTER - 1; ++p) h = p < rt ? any_apply(m[p], h) : h;
+            }
         }
         cluster_arrive();   // paired with the wait at the kernel's end: no CTA leaves while its map is read
     }
     if (warp == one) {
-#pragma unroll
-        for (int k = 0; k < RUNS; ++k) {
+        auto fold = [&](int k, auto f) {
             const int r = REVERSE ? RUNS - 1 - k : k;
             const float2 m = sh.map[r][lane];
             sh.state[r][lane] = h;
-            h = apply(m, h);
+            h = f(m, h);
+        };
+        if (far) {
+#pragma unroll 1
+            for (int k = 0; k < RUNS; ++k) fold(k, any_apply);
+        } else {
+#pragma unroll
+            for (int k = 0; k < RUNS; ++k) fold(k, apply);
         }
     }
     __syncthreads();
@@ -588,7 +678,7 @@ __device__ __forceinline__ void walk(Shared<G> &sh, const Chain &ch, const PlanV
 {
     const int T = pv.T(), nT = tiles_of(T), nC = (D + C - 1) / C;
     const int run = threadIdx.x / 16;
-    if (threadIdx.x == 0) sh.bad = 0;
+    if (threadIdx.x == 0) sh.bad = 0, sh.far = -1;
     if constexpr (!CHAIN) {
         uint32_t cs, rank;
         asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));

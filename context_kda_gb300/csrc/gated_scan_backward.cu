@@ -94,21 +94,36 @@ __global__ void __launch_bounds__(THREADS, ctas_of<BackwardShared<E, SH, G>>()) 
                 set(F, fma2(both(a[j]), both(F), both(u[j])));
             }
         });
+        if (__any_sync(0xffffffffu, !(P[0] <= MOST_RUN) || !(P[1] <= MOST_RUN))) {
+            sm.s.far = t.rt;
+            double p[V];
+            int k[V];
+            far_products<ADJ>(gr, l, RUN, p, k);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (!(P[v] <= MOST)) P[v] = product_of(p[v]);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            P[v] = fminf(P[v], MOST);
-            sm.s.map[run][chan<ADJ>(l, v)] = make_float2(ends ? -1.f : P[v], B[v]);
-            sm.fmap[run][chan<ADJ>(l, v)] = make_float2(b.starts ? -1.f : P[v], F[v]);
+            sm.s.map[run][chan<ADJ>(l, v)] = make_float2(ends ? FORGET : P[v], B[v]);
+            sm.fmap[run][chan<ADJ>(l, v)] = make_float2(b.starts ? FORGET : P[v], F[v]);
         }
         __syncthreads();
         // While the tile's map travels: the states before each token, in place of the tokens' own terms.
         auto meanwhile = [&] {
             release();
             if (warp == WARPS - 1) {
-#pragma unroll
-                for (int r = 0; r < RUNS; ++r) {
+                auto fold = [&](int r, auto f) {
+                    const float2 m = sm.fmap[r][lane];
                     sm.fstate[r][lane] = f0;
-                    f0 = apply(sm.fmap[r][lane], f0);
+                    f0 = f(m, f0);
+                };
+                if (sm.s.far == t.rt) {
+#pragma unroll 1
+                    for (int r = 0; r < RUNS; ++r) fold(r, any_apply);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < RUNS; ++r) fold(r, apply);
                 }
             }
             __syncthreads();

@@ -499,9 +499,11 @@ enum { KDA_SCAN_TILE = 128 };
  *   plan, plan_dev  a plan of kda_plan_segments and its device copy; its segments do not matter here.
  *   D               channels (any number).
  *   x, i            activations [T][D]; i (the input gate's value) NULL: 1.
- *   g               fp32 [T][D] log-decays; any value (exp(g) is taken as it is).  Decays above one are
- *                   meant for states that stay small: where the product of up to KDA_SCAN_TILE adjacent
- *                   ones passes fp32's range, a state other than zero may become infinite early.
+ *   g               fp32 [T][D] log-decays; any value (exp(g) is taken as it is).  Decays may be above one: a
+ *                   state is right while it is within fp32's range, also where products of decays are not;
+ *                   one that passes 2^248 may be infinite or NaN up to 15 tokens before it leaves the range.
+ *                   A product of up to KDA_SCAN_TILE adjacent decays below 2^-126 may count as zero, also
+ *                   where later decays above one would bring the state back.
  *   h0              fp32 [N][D] or NULL (zeros).
  *   h           out [T][D].
  *   final_state out fp32 [N][D] (h after each sequence's last token) or NULL.

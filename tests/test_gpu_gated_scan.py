@@ -424,3 +424,83 @@ def test_two_streams_at_once():
         for one in got[n]:
             for a, b in zip(one, want[n] + want_grads[n]):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def _relative(got, want, bound, what):
+    """Every value within a share of itself (and fp32's smallest numbers)."""
+    x = got.double().cpu().numpy()
+    assert x.shape == want.shape and np.all(np.isfinite(x)), what
+    worst = float(np.max(np.abs(x - want) / (bound * np.abs(want) + 2.0 ** -126)))
+    assert worst <= 1.0, f"{what}: {worst:.3g} times the tolerance"
+
+
+# (lengths, (first token, tokens, log-decay) of the stretches whose decays are not one)
+GROWING = {"within a run": ([40], [(0, 15, 8.0)]), "two runs": ([60], [(20, 15, 8.0)]), "within a tile": ([400], [(4, 120, 1.0)]),
+           "over tiles": ([1000], [(100, 240, 0.5)]), "chain, a run": ([2500], [(200, 15, 8.0)]), "chain, over tiles": ([40, 2500, 7], [(300, 240, 0.5)]),
+           "several boundaries in a run": ([5, 4, 12, 3, 30, 2], [(9, 12, 10.0)]), "before a boundary": ([19, 40], [(3, 14, 8.5)]),
+           "and back": ([1500], [(16, 15, 8.0), (31, 60, -1.0)]), "and forgotten": ([300], [(16, 15, 8.0), (31, 1, -np.inf)])}
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 70])
+@pytest.mark.parametrize("case", GROWING, ids=lambda c: c.replace(" ", "-"))
+def test_growing_decays_of_a_small_state(case, D, kind):
+    """A state of 1e-25 that grows by e^120: the product of the decays passes fp32's range, the state does not (nor do the
+    gradients, whose last one is 1e-25 too, or 1e5 where they shrink before they grow).  Every decay is off by
+    2^-22 (the exponential) and 1.5 |g| 2^-24 (its argument), every product by 2^-24 of itself; these add up.  Channels whose
+    state is zero stay at zero next to it."""
+    lens, stretches = GROWING[case]
+    cu, dev, w = _draw(lens, D, kind, seed=D)
+    for name in ("x", "dh"):
+        dev[name].zero_()
+        w[name][:] = 0
+    steps = 60
+    for v in (dev["g"], w["g"]):
+        v[:] = 0
+        for first, n, g in stretches:
+            v[first:first + n] = g
+    for first, n, g in stretches:
+        steps += n * (4 + (1.5 * abs(g) if np.isfinite(g) else 0) + 2)
+    for name, size in (("h0", 1e-25), ("dfinal", 1e5 if case == "and back" else 1e-25)):
+        dev[name][:, ::3], w[name][:, ::3] = 0, 0
+        dev[name][:, 1::3], w[name][:, 1::3] = size, float(np.float32(size))
+        dev[name][:, 2::3], w[name][:, 2::3] = -size, -float(np.float32(size))
+    bound = 2.0 ** -24 * steps
+    h_ref, f_ref = ref.scan_forward(cu, w["x"], w["i"], w["g"], w["h0"])
+    assert 1e26 < np.abs(h_ref).max() < 1e30
+    h, final, states = _forward(cu, dev)
+    _relative(h, h_ref, bound + ref.ROUND[kind], "h")
+    _relative(final, f_ref, bound, "final")
+    _relative(states, ref.saved_states(h_ref), bound, "states")
+    assert not h[:, ::3].any() and not final[:, ::3].any()
+    got = _backward(cu, dev, states)
+    want = ref.scan_backward(cu, w["x"], w["i"], w["g"], w["h0"], w["dh"], w["dfinal"])
+    for name, a, b, k in zip(("dx", "di", "dg", "dh0"), got, want, (kind, kind, "f32", "f32")):
+        _relative(a, b, 2 * bound + 2 * ref.ROUND[k], name)
+
+
+@pytest.mark.parametrize("lens", [[9, 400, 5, 260], [9, 1600, 3, 2, 300]], ids=["cluster", "chain"])
+def test_growing_decays_of_one_channel_or_sequence(lens):
+    """Other channels and other sequences keep their bits."""
+    import torch
+    D = 70
+    cu, dev, _ = _draw(lens, D, "bf16", seed=11)
+    a = _forward(cu, dev)
+    ga = _backward(cu, dev, a[2])
+    first, last = cu[1], cu[2]
+    dev["g"][first:first + 20, 8] = 9.0
+    dev["g"][last - 20:last, 8] = 9.0
+    dev["g"][last - 40:last - 30, 9] = float("inf")
+    b = _forward(cu, dev)
+    gb = _backward(cu, dev, b[2])
+    same = lambda x, y: torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+    others = [c for c in range(D) if c not in (8, 9)]
+    for x, y in zip(a + ga, b + gb):
+        assert same(x[:, others], y[:, others])
+    assert same(a[0][first + 20:last - 40, 9], b[0][first + 20:last - 40, 9])     # also what comes before an infinite decay
+    for n in range(len(lens)):
+        if n != 1:
+            rows = slice(cu[n], cu[n + 1])
+            for x, y in ((a[0], b[0]), *zip(ga[:3], gb[:3])):
+                assert same(x[rows], y[rows])
+            assert same(a[1][n], b[1][n]) and same(ga[3][n], gb[3][n])
