@@ -577,7 +577,7 @@ int norm_in_ok(int64_t T, int32_t D, int32_t rtype, int32_t type, const kda::Nor
 
 extern "C" size_t kda_gated_scan_workspace_bytes(const int32_t *plan, int32_t D)
 {
-    return plan_ok(plan) && D >= 1 ? kda::scan_workspace_bytes(plan[KDA_PH_T], D) : 0;
+    return plan_ok(plan) && D >= 1 && D <= kda::SCAN_MAX_D ? kda::scan_workspace_bytes(plan[KDA_PH_T], D) : 0;
 }
 
 extern "C" int kda_gated_scan_forward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
@@ -589,6 +589,7 @@ extern "C" int kda_gated_scan_forward(const int32_t *plan, const int32_t *plan_d
     if (!plan_ok(plan) || !plan_dev || !scan_in_ok(D, type, in)) return KDA_ERR_INVALID_ARG;
     if (!rows_ok(h, ldh, D, kda::elem_bytes(type)) || !floats_ok_or_null(final_state) || !floats_ok_or_null(states))
         return KDA_ERR_INVALID_ARG;
+    if (D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;
     if (const int rc = scan_ws_ok(plan, D, ws, ws_bytes)) return rc;
     return cuda_status(kda::launch_scan_forward(plan, plan_dev, D, type, in, h, ldh, final_state, states, ws,
                                                 static_cast<cudaStream_t>(stream)));
@@ -609,6 +610,7 @@ extern "C" int kda_gated_scan_backward(const int32_t *plan, const int32_t *plan_
     if (!rows_ok(dx, lddx, D, e) || !rows_ok_or_null(di, lddi, D, e) || !rows_ok(dg, lddg, D, 4) || !floats_ok_or_null(dh0))
         return KDA_ERR_INVALID_ARG;
     if (di && !i) return KDA_ERR_INVALID_ARG;
+    if (D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;
     if (const int rc = scan_ws_ok(plan, D, ws, ws_bytes)) return rc;
     return cuda_status(kda::launch_scan_backward(plan, plan_dev, D, type, in, states, dh, lddh, dfinal, out, ws,
                                                  static_cast<cudaStream_t>(stream)));
@@ -624,6 +626,7 @@ extern "C" int kda_gated_scan_step(int32_t B, int32_t D, int32_t type, const int
     if (!scan_in_ok(D, type, in) || !state || !floats_ok_or_null(state) || !rows_ok(h, ldh, D, kda::elem_bytes(type)) ||
         (reinterpret_cast<uintptr_t>(slots) & 3u))
         return KDA_ERR_INVALID_ARG;
+    if (D > kda::SCAN_MAX_D) return KDA_ERR_UNSUPPORTED;
     return cuda_status(kda::launch_scan_step(B, D, type, slots, num_slots, in, state, h, ldh,
                                              static_cast<cudaStream_t>(stream)));
 }

@@ -218,8 +218,8 @@ __device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld,
         const int row = threadIdx.x / CPR, c = threadIdx.x % CPR * R::EPC;
         const X *p = src + (static_cast<int64_t>(t0) + row) * ld + c0 + c;
         const int64_t hop = STEP * ld;
-        const int left = (D - c0 - c) * static_cast<int>(sizeof(X));
-        const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+        const int left = D - c0 - c;
+        const int bytes = (left < 0 ? 0 : left > R::EPC ? R::EPC : left) * static_cast<int>(sizeof(X));
         const int rows = bytes ? T - t0 - row : 0;                 // of this thread, from its first on
         // the k-th row's place is a constant from the first's: steps never leave the first row's place within its run
         static_assert(STEP % RUN == 0 || RUN % STEP == 0, "whole runs a step or whole steps a run");
@@ -245,7 +245,7 @@ __device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld,
         const char *base = reinterpret_cast<const char *>(src);
         const int64_t pitch = ld * static_cast<int64_t>(sizeof(X));
         const char *tile = base + t0 * pitch + c0 * static_cast<int64_t>(sizeof(X));
-        if (t0 > 0 && t0 + L < T && c0 + C <= D) {
+        if (t0 > 0 && T - t0 > L && D - c0 >= C) {
             // rows before and after the tile's: whole copies stay within the tensor, their ends belong to other channels
             const int row = threadIdx.x / CPR, c = threadIdx.x % CPR;
             const uint32_t to = smem_u32(dst.row(row / RUN, row % RUN) + c * R::EPC);
@@ -266,7 +266,7 @@ __device__ __forceinline__ void fill(Rows<X, SH> &dst, const X *src, int64_t ld,
             const int row = k / (CPR + 1), ch = k % (CPR + 1);
             const char *p = tile + row * pitch;
             const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-            const int left = t0 + row < T ? off + width - ch * 16 : 0;
+            const int left = row < T - t0 ? off + width - ch * 16 : 0;
             const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
             const char *at = p - off + ch * 16;
             X *to = dst.row(row / RUN, row % RUN) + ch * R::EPC;

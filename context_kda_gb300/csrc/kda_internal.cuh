@@ -234,6 +234,7 @@ cudaError_t launch_scan_backward(const int32_t *plan_host, const int32_t *plan_d
                                  const ScanGrads &out, void *ws, cudaStream_t stream);
 cudaError_t launch_scan_step(int B, int D, int type, const int32_t *slots, int num_slots, const ScanIn &in,
                              float *state, void *h, int64_t ldh, cudaStream_t stream);
+constexpr int SCAN_MAX_D = 2147483136;   // 2^31 - 512: channel indexes of a whole block of threads are 32-bit numbers
 int take_scan_status();
 int take_scan_backward_status();
 

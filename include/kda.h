@@ -497,7 +497,7 @@ enum { KDA_SCAN_TILE = 128 };
  * kda_gated_scan_forward -- the gated linear recurrence of every sequence of the plan, per channel,
  *     h_t = exp(g_t) h_{t-1} + i_t x_t,     h before a sequence's first token = its h0.
  *   plan, plan_dev  a plan of kda_plan_segments and its device copy; its segments do not matter here.
- *   D               channels (any number).
+ *   D               channels (up to 2^31 - 512, else KDA_ERR_UNSUPPORTED).
  *   x, i            activations [T][D]; i (the input gate's value) NULL: 1.
  *   g               fp32 [T][D] log-decays; any value (exp(g) is taken as it is).  Decays may be above one: a
  *                   state is right while it is within fp32's range, also where products of decays are not;
@@ -512,7 +512,8 @@ enum { KDA_SCAN_TILE = 128 };
  *   ws, ws_bytes    device workspace of at least kda_gated_scan_workspace_bytes(plan, D) bytes (may be
  *                   NULL where that is 0).
  * A sequence never sees another's values, whatever they are.  Results do not depend on timing: the
- * same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_WORKSPACE or KDA_ERR_CUDA.
+ * same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED,
+ * KDA_ERR_WORKSPACE or KDA_ERR_CUDA.
  */
 int kda_gated_scan_forward(const int32_t *plan, const int32_t *plan_dev, int32_t D, int32_t type,
                            const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,
@@ -548,7 +549,7 @@ size_t kda_gated_scan_workspace_bytes(const int32_t *plan, int32_t D);
  *                   returns KDA_ERR_INVALID_ARG.
  *   state           in/out fp32 [num_slots][D].
  *   x, i, g, h      [B][D], as in the forward.
- * B = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG or KDA_ERR_CUDA.
+ * B = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
  */
 int kda_gated_scan_step(int32_t B, int32_t D, int32_t type, const int32_t *slots, int32_t num_slots,
                         const void *x, int64_t ldx, const void *i, int64_t ldi, const float *g, int64_t ldg,

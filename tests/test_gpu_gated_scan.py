@@ -504,3 +504,46 @@ def test_growing_decays_of_one_channel_or_sequence(lens):
             for x, y in ((a[0], b[0]), *zip(ga[:3], gb[:3])):
                 assert same(x[rows], y[rows])
             assert same(a[1][n], b[1][n]) and same(ga[3][n], gb[3][n])
+
+
+def test_widths_beyond_2_to_the_29():
+    """Bytes of a row that pass 2^31: h = exp(g) h0 + x with every value known, and its gradients."""
+    import math
+
+    import torch
+    from context_kda_gb300 import binding as kda
+    D = 2 ** 29 + 8
+    full = lambda v: torch.full((1, D), v, device="cuda")
+    plan = kda.kda_plan_segments([0, 1], 1)
+    plan_dev = kda.upload_plan(plan)
+    x, g, h0, h, final = full(1.0), full(math.log(0.5)), full(2.0), full(float("nan")), full(float("nan"))
+    states = full(float("nan"))
+    kda.kda_gated_scan_forward(plan, plan_dev, x, None, g, h0, h, final, states, None)
+    off = lambda t, v: float(t.sub_(v).abs_().max())
+    assert off(h, 2.0) <= 1e-5 and off(final, 2.0) <= 1e-5 and off(states, 0.0) == 0.0
+    dx, dg, dh0 = full(float("nan")), full(float("nan")), full(float("nan"))
+    kda.kda_gated_scan_backward(plan, plan_dev, x, None, g, h0, states, full(1.0), None, dx, None, dg, dh0, None)
+    assert off(dx, 1.0) == 0.0 and off(dg, 1.0) <= 1e-5 and off(dh0, 0.5) <= 1e-5
+
+
+def test_lengths_up_to_2_to_the_31():
+    """The last tile of a stream of 2^31 - 100 tokens would end beyond 32 bits; its rows start anywhere."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    T, tail = 2 ** 31 - 100, 300
+    plan = kda.kda_plan_segments([0, T], 1)
+    plan_dev = kda.upload_plan(plan)
+    x = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    g = torch.full((T, 1), -1.0, device="cuda")
+    gen = torch.Generator().manual_seed(8)
+    last = torch.randn(tail, 1, generator=gen).to(torch.bfloat16)
+    x[T - tail:] = last.cuda()
+    h = torch.empty_like(x)
+    ws = torch.empty(kda.kda_gated_scan_workspace_bytes(plan, 1), dtype=torch.uint8, device="cuda")
+    final = torch.empty(1, 1, device="cuda")
+    kda.kda_gated_scan_forward(plan, plan_dev, x, None, g, None, h, final, None, ws)
+    assert kda.kda_device_status() == kda.KDA_OK
+    h_ref, f_ref = ref.scan_forward([0, tail], last.double().numpy(), None, np.full((tail, 1), -1.0), None)
+    check(h[T - tail:], h_ref, "bf16", "h")
+    check(final, f_ref, "f32", "final")
+    assert not h[:T - tail].any()

@@ -124,3 +124,19 @@ def test_binding_refuses_tensors_that_do_not_fit(kda):
     with pytest.raises(kda.KDAError):
         kda.kda_decode_step(None, torch.zeros(1, 2, 128), torch.zeros(1, 2, 128), torch.zeros(1, 2, 128), torch.zeros(1, 2, 128),
                             torch.zeros(1, 2), 1.0, torch.zeros(1, 2, 128, 128), torch.zeros(1, 2, 128), 0)
+
+
+def test_gated_scan_refuses_more_channels_than_its_indexes_hold(kda):
+    lib, most = kda._lib, 2 ** 31 - 512
+    for D in (most + 1, 2 ** 31 - 1):
+        for cu in ([0, 1], [0, 3000]):
+            plan = kda.kda_plan_segments(cu, 1)
+            pp = plan.ctypes.data_as(ctypes.c_void_p)
+            assert kda.kda_gated_scan_workspace_bytes(plan, D) == 0
+            assert lib.kda_gated_scan_forward(pp, F, D, BF16, F, D, F, D, F, D, F, F, D, F, F, F, 1 << 62, None) == kda.KDA_ERR_UNSUPPORTED
+            assert lib.kda_gated_scan_backward(pp, F, D, BF16, F, D, F, D, F, D, F, F, F, D, F, F, D, F, D, F, D, F, F, 1 << 62,
+                                               None) == kda.KDA_ERR_UNSUPPORTED
+        assert lib.kda_gated_scan_step(1, D, BF16, F, 4, F, D, F, D, F, D, F, F, D, None) == kda.KDA_ERR_UNSUPPORTED
+    plan = kda.kda_plan_segments([0, 3000], 1)
+    tiles, states = 24, 4                                        # one state every 8 tiles, one more
+    assert kda.kda_gated_scan_workspace_bytes(plan, most) >= (tiles * 8 + states * 4) * most
