@@ -39,9 +39,20 @@ def _newest_input() -> float:
     return max(os.path.getmtime(p) for p in paths if os.path.exists(p))
 
 
+def _torch_dir():
+    """torch's folder, found without importing it; None where there is no torch with CUDA (the C library needs none)."""
+    spec = importlib.util.find_spec("torch")
+    for path in (spec.submodule_search_locations or ()) if spec else ():
+        if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")):
+            return path
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
-    """Compile csrc/ into context_kda_gb300/libkda.so unless it is up to date."""
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (LIB, OPS)):
+    """Compile csrc/ into context_kda_gb300/libkda.so and, where torch is found, _ops.so, unless they are up to date."""
+    torch = _torch_dir()
+    made = (LIB, OPS) if torch else (LIB,)
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in made):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -55,13 +66,13 @@ def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
         obj = os.path.join(BUILD, src + ".o")
         jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", *inc, "-c", os.path.join(CSRC, src), "-o", obj])
 
-    # torch's headers, found without importing it; its libraries are already loaded when the module is
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    # torch's libraries are already loaded when the marshalling module is
     ops_obj = os.path.join(BUILD, "torch_ops.cpp.o")
-    jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", os.path.join(torch, "include"), "-I",
-                 os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
-                 sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", ops_obj])
+    if torch:
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", os.path.join(torch, "include"), "-I",
+                     os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
+                     sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", ops_obj])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -77,8 +88,9 @@ def build(force: bool = False, verbose: bool = False, extra_nvcc=()) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    tmp = OPS + f".tmp{os.getpid()}"
-    run(["g++", "-shared", "-o", tmp, ops_obj, "-L", PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
-         "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
-    os.replace(tmp, OPS)
+    if torch:
+        tmp = OPS + f".tmp{os.getpid()}"
+        run(["g++", "-shared", "-o", tmp, ops_obj, "-L", PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
+             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+        os.replace(tmp, OPS)
     return LIB

@@ -292,6 +292,8 @@ def _marshal():
     global _ops
     if _ops is None:
         import torch  # noqa: F401  (its libraries have to be loaded first)
+        if not os.path.exists(os.path.join(_PKG, "_ops.so")):
+            raise ImportError("_ops.so is not built (it is where the build finds torch); run __graft_entry__.build() again")
         from . import _ops as module
         module.set_error(KDAError)
         _ops = module
