@@ -1,11 +1,12 @@
 // Argument marshalling of the operators around the KDA layer for Python: tensors in, the C entry points of
 // libkda.so called on the current stream.  These operators are called once a layer and token, where the
 // time to unpack fifteen arguments in Python (6 us) would exceed the call itself (4 us); here it takes
-// well under one.  Shapes, types and strides are checked here, everything else by the entry points; a refused call
+// well under one.  Shapes, types, strides and devices are checked here, everything else by the entry points; a refused call
 // raises the binding's KDAError.  Nothing is computed, allocated or kept.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -19,6 +20,7 @@ PyObject *g_error = nullptr;   // the binding's KDAError(fn, status, message)
 
 struct Refused {
     int status;
+    const char *why = nullptr;
 };
 
 struct Rows {
@@ -73,6 +75,15 @@ void need(bool ok)
     if (!ok) throw Refused{KDA_ERR_INVALID_ARG};
 }
 
+// The work goes to the current device: a tensor has to be there.
+thread_local int t_device = -1;    // of this call, once it is known
+void here(const at::Tensor &t)
+{
+    need(t.is_cuda());
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    if (t.device().index() != t_device) throw Refused{KDA_ERR_INVALID_ARG, "a tensor is on another device than the current one"};
+}
+
 int32_t i32(int64_t v)
 {
     need(v >= INT32_MIN && v <= INT32_MAX);
@@ -91,7 +102,8 @@ int type_code(at::ScalarType t)
 Rows rows_of(const at::Tensor *t, int64_t rows, int64_t width, at::ScalarType type)
 {
     if (!t) return Rows{nullptr, 0};
-    need(t->scalar_type() == type && t->is_cuda() && t->dim() >= 2 && t->size(0) == rows);
+    here(*t);
+    need(t->scalar_type() == type && t->dim() >= 2 && t->size(0) == rows);
     int64_t n = 1;
     for (int64_t d = t->dim() - 1; d > 0; --d) {
         need(t->size(d) == 1 || t->stride(d) == n);
@@ -104,7 +116,8 @@ Rows rows_of(const at::Tensor *t, int64_t rows, int64_t width, at::ScalarType ty
 template <typename T> T *flat(const at::Tensor *t, int64_t numel, at::ScalarType type)
 {
     if (!t) return nullptr;
-    need(t->scalar_type() == type && t->is_cuda() && t->numel() == numel && t->is_contiguous());
+    here(*t);
+    need(t->scalar_type() == type && t->numel() == numel && t->is_contiguous());
     return static_cast<T *>(t->data_ptr());
 }
 float *floats(const at::Tensor *t, int64_t numel) { return flat<float>(t, numel, at::kFloat); }
@@ -116,7 +129,8 @@ struct Bytes {
 Bytes workspace(const at::Tensor *t)
 {
     if (!t) return Bytes{nullptr, 0};
-    need(t->is_cuda() && t->is_contiguous());
+    here(*t);
+    need(t->is_contiguous());
     return Bytes{t->data_ptr(), static_cast<size_t>(t->numel()) * t->element_size()};
 }
 
@@ -132,7 +146,8 @@ struct Plan {
             const int64_t n = view.len / 4;
             need(n >= KDA_PLAN_HEADER_WORDS && words[KDA_PH_TOTAL] >= KDA_PLAN_HEADER_WORDS && n >= words[KDA_PH_TOTAL]);
             const at::Tensor *t = a.tensor(false);
-            need(t->scalar_type() == at::kInt && t->is_cuda() && t->is_contiguous() && t->numel() >= words[KDA_PH_TOTAL]);
+            here(*t);
+            need(t->scalar_type() == at::kInt && t->is_contiguous() && t->numel() >= words[KDA_PH_TOTAL]);
             dev = static_cast<const int32_t *>(t->data_ptr());
         } catch (...) {
             PyBuffer_Release(&view);
@@ -147,10 +162,13 @@ struct Plan {
 template <typename F> PyObject *call(const char *name, F f)
 {
     int status = KDA_ERR_INVALID_ARG;
+    const char *why = nullptr;
+    t_device = -1;
     try {
         status = f();
     } catch (const Refused &r) {
         status = r.status;
+        why = r.why;
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -159,7 +177,8 @@ template <typename F> PyObject *call(const char *name, F f)
     if (status == KDA_OK) Py_RETURN_NONE;
     PyObject *text = status == KDA_ERR_CUDA
                          ? PyUnicode_FromFormat("%s (cudaError %d)", kda_status_string(status), kda_last_cuda_error())
-                         : PyUnicode_FromString(kda_status_string(status));
+                     : why ? PyUnicode_FromFormat("%s (%s)", kda_status_string(status), why)
+                           : PyUnicode_FromString(kda_status_string(status));
     PyObject *e = text ? PyObject_CallFunction(g_error, "siO", name, status, text) : nullptr;
     Py_XDECREF(text);
     if (e) {
