@@ -138,7 +138,7 @@ def _nbytes(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # of the current device
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     return ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
 
 
