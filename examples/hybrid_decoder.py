@@ -155,25 +155,26 @@ class GatedScan(torch.autograd.Function):
 
 
 class BlockNorm(torch.autograd.Function):
-    """(r', y) of kda_block_norm_forward, with gradients for r, o, z and the weights."""
+    """(r', y) of kda_block_norm_forward, with gradients for r, o, z and the weights.  All but o may be None, as in the call
+    (z where the gate is "none"; without w_pre there is no y)."""
 
     @staticmethod
     def forward(ctx, gate, group, scale, r, o, z, w_post, ls, w_pre):
-        r_out, y = torch.empty_like(r), torch.empty_like(o)
+        r_out, y = torch.empty_like(o if r is None else r), None if w_pre is None else torch.empty_like(o)
         kda.kda_block_norm_forward(r, o, z, gate, group, w_post, scale, ls, w_pre, EPS, r_out, y)
-        ctx.how = gate, group, scale
+        ctx.how = gate, group, scale, r is not None
         ctx.save_for_backward(r_out, o, z, w_post, ls, w_pre)
         return r_out, y
 
     @staticmethod
     def backward(ctx, dr_out, dy):
-        gate, group, scale = ctx.how
+        gate, group, scale, has_r = ctx.how
         r_out, o, z, w_post, ls, w_pre = ctx.saved_tensors
-        dr, do, dz = torch.empty_like(r_out), torch.empty_like(o), torch.empty_like(z)
-        dw = [torch.empty_like(w) for w in (w_post, ls, w_pre)]
+        like = lambda t: None if t is None else torch.empty_like(t)
+        dr, do, dz, dw = like(r_out) if has_r else None, like(o), like(z), [like(w) for w in (w_post, ls, w_pre)]
         ws = _empty(kda.kda_block_norm_workspace_bytes(o.shape[1]), dtype=torch.uint8)
-        kda.kda_block_norm_backward(r_out, o, z, gate, group, w_post, scale, ls, w_pre, EPS, dr_out.contiguous(), dy.contiguous(), dr, do,
-                                    dz, *dw, ws)
+        kda.kda_block_norm_backward(r_out, o, z, gate, group, w_post, scale, ls, w_pre, EPS, dr_out.contiguous(),
+                                    None if w_pre is None else dy.contiguous(), dr, do, dz, *dw, ws)
         return None, None, None, dr, do, dz, *dw
 
 

@@ -60,3 +60,34 @@ def test_gradients_under_autograd(example):
         got, want = float((v[name].grad.double() * d).sum()), float((up - down) / (2 * eps))
         size = float((v[name].grad.double() * d).square().sum().sqrt())     # of a sum of terms of random sign
         assert abs(got - want) <= 1e-2 * max(abs(want), size), (name, got, want)
+
+
+@pytest.mark.parametrize("absent", [("z",), ("r",), ("w_post",), ("ls",), ("w_pre",), ("r", "w_pre"), ("z", "r", "ls", "w_pre")], ids="-".join)
+def test_block_norm_under_autograd_without_parts(example, absent):
+    """Any part but o may be None: gradients against autograd through the definition in 64 bits, within the tolerances of the
+    operators' own tests."""
+    import torch
+    import ops_reference as ref
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    T, D, G = 37, 128, 32
+    normal = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    parts = {"r": normal(T, D), "o": normal(T, D), "z": normal(T, D), "w_post": 1 + 0.1 * normal(G), "ls": 1 + 0.1 * normal(D), "w_pre": 1 + 0.1 * normal(D)}
+    parts = {k: None if k in absent else v for k, v in parts.items()}
+    gate = "none" if "z" in absent else "silu"
+    c1, c2 = normal(T, D), normal(T, D)
+    own = {k: None if v is None else v.clone().requires_grad_() for k, v in parts.items()}
+    wide = {k: None if v is None else v.double().requires_grad_() for k, v in parts.items()}
+    r, y = example.BlockNorm.apply(gate, G, 0.5, *own.values())
+    assert (y is None) == ("w_pre" in absent)
+    ((r * c1).sum() + (0 if y is None else (y * c2).sum())).backward()
+    unit = lambda v, n: v * torch.rsqrt(v.unflatten(1, (-1, n)).square().mean(-1, keepdim=True) + example.EPS).expand(-1, -1, n).reshape(T, D)
+    u = wide["o"] if wide["w_post"] is None else unit(wide["o"], G) * wide["w_post"].repeat(D // G)
+    u = u if wide["z"] is None else u * torch.nn.functional.silu(wide["z"])
+    r2 = (0 if wide["r"] is None else wide["r"]) + 0.5 * u * (1 if wide["ls"] is None else wide["ls"])
+    loss = (r2 * c1.double()).sum()
+    if wide["w_pre"] is not None:
+        loss = loss + (unit(r2, D) * wide["w_pre"] * c2.double()).sum()
+    loss.backward()
+    for name, v in own.items():
+        if v is not None:
+            ref.check(v.grad, wide[name].grad.cpu().numpy(), "f32", name)
