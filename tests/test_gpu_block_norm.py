@@ -315,3 +315,25 @@ def test_whole_row_norm_without_the_next_norm(kind, res, D, T, gate, r):
     for _ in range(5):
         again, _ = _forward(d, T, D, kind, res, gate, 0)
         assert torch.equal(first.view(torch.uint8), again.view(torch.uint8))
+
+
+def _steps(D):
+    """Rows that keep every CTA of the widest launch (four CTAs of 256 threads an SM up to 2048 channels, two of 512 up to 4096,
+    one above) at work for three steps and a bit."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    threads = 4
+    while threads * 8 < D:
+        threads *= 2
+    per = 4 * max(1, 256 // threads) if D <= 2048 else 2 if D <= 4096 else 1
+    return 3 * sms * per + 5
+
+
+@pytest.mark.parametrize("how", [dict(), dict(pre=False), dict(r=False, pre=False), dict(post=False), dict(ls=False, r=False), dict(o=False, gate="none")], ids=str)
+@pytest.mark.parametrize("D,group", [(96, 32), (300, 0), (301, 0), (384, 128), (1001, 0), (1024, 256), (2048, 0), (2048, 128), (2050, 0), (4096, 0), (4096, 128),
+                                     (4098, 0), (4099, 0), (6144, 0), (6144, 128), (6146, 0), (8192, 256), (12288, 0), (12288, 128), (12289, 0)])
+def test_many_rows_a_cta(D, group, how):
+    """Slots of the ring are filled again, the buffers of the row sums alternate, weights are read again for every row."""
+    pairs = (("bf16", "f32"), ("f32", "f32")) if how in (dict(), dict(pre=False)) else (("f16", "f16"),)
+    for kind, res in pairs:
+        _check_all(_steps(D), D, kind, res, group=group, **how)
