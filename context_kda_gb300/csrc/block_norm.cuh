@@ -11,8 +11,10 @@
 // Reciprocals and square roots are the hardware's approximations (about 2^-22 relative): fp32 results keep 1e-6.
 //
 // A CTA of BLOCK threads takes R rows at a time (NT threads a row, 8 NC channels a thread) and walks over
-// all its rows, which are copied to a ring in shared memory (cp.async) one to three steps ahead.  Sums over a row take
-// one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
+// all its rows, which are copied to a ring in shared memory (cp.async) up to two steps ahead, as many as fit.  With an fp32
+// residual above 8192 channels (gradients: 4096, and 8192 all in 16 bits) one step fits: none is ahead, and rows that do not start
+// on 16 bytes are read from memory as they are needed, as are all in gradients above 8192 channels with an fp32 residual.
+// Sums over a row take one barrier each (none when a row is a warp or less).  U is the run of adjacent channels of a thread: 8 (4 where the
 // residual is fp32) where rows start on 16 bytes (a thread copies what it reads itself, without a barrier), else 2 where they
 // start on pairs and 1 anywhere (8192 rows in bf16, forward of 3970 channels: 83 us in pairs, 92 us one by one; gradients
 // of 1002 channels with an fp32 residual: 50 and 55 us, all in scalar instructions).
@@ -22,12 +24,12 @@
 // Column sums (the weights' gradients) stay in registers over all rows of a CTA, are folded over its R rows
 // and its groups at the end, and a second kernel adds up the CTAs in order.
 //
-// Measured on the device (share of a copy's 6.79 TB/s): forward of 65536 x 4096 in bf16 with an fp32 residual 546 us (101 %),
-// of 16384 x 4096 all in bf16 86 us (92 %); gradients of 16384 x 4096 with an fp32 residual 216 us (101 %), of 16384 x 2048 in
+// Measured on the device (share of a copy's 6.79 TB/s): forward of 65536 x 4096 in bf16 with an fp32 residual 540 us (103 %),
+// of 16384 x 4096 all in bf16 84 us (95 %); gradients of 16384 x 4096 with an fp32 residual 216 us (101 %), of 16384 x 2048 in
 // bf16 88 us (90 %), of 8192 x 2048 50 us (80 %): the launches, the first rows' way in and the column sums take 6 us of
 // any call.  Unaligned rows are bound by instructions, gradients of 8198 x 1001 in fp32 56 us (69 %); above 4096 channels the weights
-// are read again for every row, 8192 x 8192 in bf16 115 us (86 %) and gradients 346 us (46 %: the column sums leave no registers
-// for the row, and some of it is kept in local memory).
+// are read again for every row, 8192 x 8192 in bf16 115 to 119 us (83 to 86 %) and gradients 346 us (46 %: the column sums leave
+// no registers for the row, and some of it is kept in local memory, most above 8192 channels: 4096 x 16384 1022 us, 15 %).
 #pragma once
 
 #include <type_traits>

@@ -15,11 +15,11 @@
 // kernel waits rather than computes (for copies, for other tiles' maps), so four CTAs share an SM, each in another phase;
 // a tile's copies are requested as soon as the last tile's have gone to registers.
 //
-// Measured on the device (bf16, share of a copy's 6.79 TB/s): wide inputs are bound by memory, 65536 x 4096 408 us (97 %),
-// 16384 x 4096 109 us (91 %; 119 us with two CTAs of 256 threads an SM) and its gradients 197 us (91 %; 277 us); what is
-// left is the first tiles' way in and the last ones' way out.  Narrow inputs are bound by the state's way along the
-// chain, about a microsecond a group: 49274 x 128 26 us (36 %), 16384 x 1024 37 us (67 %).  Rows that do not start on 16 bytes
-// are bound by instructions, 16384 x 1001 50 us (48 %) and its gradients 91 us (48 %); the smallest by the launch,
+// Measured on the device (bf16, share of a copy's 6.79 TB/s): wide inputs are bound by memory, 65536 x 4096 413 us (96 %),
+// 16384 x 4096 110 us (90 %) and its gradients 201 us (89 %), as first built with two CTAs of 256 threads an SM 119 and 277 us;
+// what is left is the first tiles' way in and the last ones' way out.  Narrow inputs are bound by the state's way along the
+// chain, about a microsecond a group: 49274 x 128 26 us (36 %), 16384 x 1024 38 us (66 %).  Rows that do not start on 16 bytes
+// are bound by instructions, 16384 x 1001 50 us (48 %) and its gradients 88 us (49 %); the smallest by the launch,
 // 1024 x 512 5.4 us.
 //   - Up to 8 tiles of tokens ('cluster'): the CTAs of a channel range are one cluster; they exchange the
 //     maps through distributed shared memory.  One launch and no workspace, for short inputs, where
@@ -59,12 +59,13 @@ constexpr int WARPS = RUNS / 2, THREADS = WARPS * 32;
 // CTAs of an SM: four, or as many as their shared memory allows.
 template <typename Sh> constexpr int ctas_of() { return 233472 / (static_cast<int>(sizeof(Sh)) + 1024) < 4 ? 233472 / (static_cast<int>(sizeof(Sh)) + 1024) : 4; }
 // Tiles of a group.  Narrow inputs wait for the state's way from group to group, which a long group shortens, at the cost
-// of more maps that a tile reads and folds (bf16, groups of 8 / 16: 65536 tokens x 4096 channels, 128 ranges of channels, 408 / 414 us
-// and gradients of 16384 x 4096 200 / 206 us; 16384 x 1024, 32 ranges, 39 / 37 us; 49274 x 128, 4 ranges, 40 / 26 us; of 32, the
-// last takes 22 us and the others are slower than with 16).
+// of more maps that a tile reads and folds (bf16, groups of 8 / 16: 65536 tokens x 4096 channels, 128 ranges of channels, 411 / 420 us
+// and gradients of 16384 x 4096 200 / 206 us; 16384 x 1024, 32 ranges, 39 / 37 us; 49274 x 128, 4 ranges, 39 / 26 us; of 32, the
+// last takes 22 us and the others are slower than with 16: a third length for a few ranges would take that, at the cost of another
+// instance of every kernel).
 constexpr int WIDE_GROUP = 8, NARROW_GROUP = 16, WIDE_RANGES = 64;
-// Tiles that a cluster covers: 512 tokens in bf16 take 4.9 us, by a chain 5.9 us, at 512 channels, and 6.3 and 7.0 us at 4096;
-// 1024 tokens 5.3 and 7.3 us, and 10.8 and 10.4 us.
+// Tiles that a cluster covers: 512 tokens in bf16 take 5.2 us, by a chain 6.7 us, at 512 channels, and 6.1 and 7.8 us at 4096;
+// 1024 tokens 5.4 and 6.8 us, and 10.6 and 10.9 us.
 constexpr int MAX_CLUSTER = 8;
 constexpr long long SPIN = 4000000000LL;     // clocks of a wait: about two seconds
 
@@ -340,11 +341,13 @@ template <typename X> __device__ __forceinline__ bool pairs(const X *p, int64_t 
     return (reinterpret_cast<uintptr_t>(p) & (2 * sizeof(X) - 1)) == 0 && (ld & 1) == 0;
 }
 
-// exp(g) as 2^(g log2 e): the product's rounding moves the result by |g| 2^-24 relative, which is below the
-// exponential's own 2^-22 for every g that leaves anything to remember.
+// exp(g) as 2^(g log2 e): the product's rounding moves the result by |g| 2^-24 relative, which is below the exponential's own
+// error for every g that leaves anything to remember.  That is 2^-22 at most; measured against 64 bits, in units of 2^-24: 1.4 for
+// g in -1e-7 .. -1e-3, where states are longest remembered, 2.1 down to -0.2, 3.8 down to -3 (torch's fp32 exponential 1.5, 1.8
+// and 2.4, a correctly rounded one 0.5 to 1).
 __device__ __forceinline__ float decay(float g) { return ex2_ftz(g * 1.4426950408889634f); }
 
-// A lane's two channels in one instruction (gradients of 16384 x 4096 in bf16: 197 us, 201 us in scalar ones).
+// A lane's two channels in one instruction (gradients of 16384 x 4096 in bf16: 4 us of 201 less than in scalar ones).
 static_assert(V == 2, "pairs");
 __device__ __forceinline__ float2 both(const float (&v)[V]) { return make_float2(v[0], v[1]); }
 __device__ __forceinline__ void set(float (&v)[V], float2 p) { v[0] = p.x, v[1] = p.y; }
@@ -398,7 +401,7 @@ template <bool ADJ, typename R> __device__ __forceinline__ void far_products(con
 __device__ __forceinline__ float two_to(int k) { return __int_as_float((127 + k) << 23); }     // |k| <= 126
 // A state behind a map.  Scaled ones (any_apply) are rare and the folds are what tiles wait for: who makes or fetches a map that
 // may lead to one leaves a mark, and folds go by 'apply' where there is none (65536 x 4096 in bf16: 428 us with the cases
-// looked at in every step, 421 us with a tile's product looked at behind its fold, 414 us).
+// looked at in every step, 421 us with a tile's product looked at behind its fold, 413 us).
 __device__ __forceinline__ float apply(float2 m, float h) { return m.x < 0.f ? m.y : fmaf(m.x, h, m.y); }
 __device__ __forceinline__ bool scaled(float lowest) { return lowest < FORGET; }
 __device__ __forceinline__ float any_apply(float2 m, float h)
