@@ -74,8 +74,15 @@ def _load():
     lib.kda_block_norm_workspace_bytes.argtypes = [I32]
     lib.kda_block_norm_workspace_bytes.restype = SZ
     lib.kda_decode_step.argtypes = [I32, I32, I32, P, I32, *R, *R, *R, *R, *R, F, P, *R, P]
+    lib.kda_rotary_phases.argtypes = [P, I32, P]
+    lib.kda_head_norm_rotary_forward.argtypes = [I64, I32, I32, I32, I32, *R, *R, I32, P, P, F, P, P, I32, I32, *R, *R, P]
+    lib.kda_head_norm_rotary_backward.argtypes = [I64, I32, I32, I32, I32, *R, *R, I32, P, P, F, P, P, I32, I32, *R, *R, *R, *R,
+                                                  P, P, P, SZ, P]
+    lib.kda_head_norm_rotary_workspace_bytes.argtypes = [I32]
+    lib.kda_head_norm_rotary_workspace_bytes.restype = SZ
     for name in ("kda_gated_scan_forward", "kda_gated_scan_backward", "kda_gated_scan_step", "kda_block_norm_forward",
-                 "kda_block_norm_backward", "kda_decode_step"):
+                 "kda_block_norm_backward", "kda_decode_step", "kda_rotary_phases", "kda_head_norm_rotary_forward",
+                 "kda_head_norm_rotary_backward"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("kda_plan_segments", "kda_plan_check", "kda_plan_segments_refined", "kda_workspace_layout", "kda_segment_forward", "kda_compose_summaries",
                  "kda_compose_summaries_blocked", "kda_apply_boundary", "kda_forward_segmented", "kda_forward_segmented_noalloc", "kda_backward_segmented",
@@ -345,3 +352,34 @@ def kda_decode_step(slots, q, k, v, g, beta, scale, state, o, stream=None):
     g [B, H, 128] and beta [B, H] fp32, state [num_slots, H, 128, 128] fp32 updated in place; slots (int32
     [B], negative: padding) may be None."""
     (_ops or _marshal()).decode_step(slots, q, k, v, g, beta, scale, state, o, stream)
+
+
+# ---- the attention layer beside the KDA layer ---------------------------------------------------------
+
+PAIRS = {"halves": 0, "adjacent": 1}
+
+
+def kda_rotary_phases(frequencies) -> np.ndarray:
+    """Frequencies (radians a position) as the 64-bit fractions of a turn that the head norms take (int64 words; upload them once)."""
+    f = np.ascontiguousarray(frequencies, dtype=np.float64)
+    out = np.zeros(f.size, dtype=np.int64)
+    _check("kda_rotary_phases", _lib.kda_rotary_phases(_hp(f), f.size, _hp(out)))
+    return out
+
+
+def kda_head_norm_rotary_workspace_bytes(d: int) -> int:
+    return int(_lib.kda_head_norm_rotary_workspace_bytes(int(d)))
+
+
+def kda_head_norm_rotary_forward(q, k, norm, w_q, w_k, eps, positions, phases, pairs, q_out, k_out, stream=None):
+    """The norms of the query and key heads with the rotation by position (see include/kda.h): q [T, H, d], k [T, Hk, d] or
+    None in one activation type, weights fp32 [d] or None, positions int32 [T] and phases int64 [rot / 2] (both None: no
+    rotation), pairs "halves" or "adjacent"."""
+    (_ops or _marshal()).head_norm_rotary_forward(q, k, norm, w_q, w_k, eps, positions, phases, PAIRS.get(pairs, -1), q_out, k_out, stream)
+
+
+def kda_head_norm_rotary_backward(q, k, norm, w_q, w_k, eps, positions, phases, pairs, dq_out, dk_out, dq, dk, dw_q, dw_k, ws, stream=None):
+    """The gradients of kda_head_norm_rotary_forward (see include/kda.h); q and k may be None where norm is false, dw_q, dw_k
+    and, without them, ws too."""
+    (_ops or _marshal()).head_norm_rotary_backward(q, k, norm, w_q, w_k, eps, positions, phases, PAIRS.get(pairs, -1), dq_out, dk_out,
+                                                   dq, dk, dw_q, dw_k, ws, stream)

@@ -4,6 +4,7 @@
 // rejects them; no call allocates, frees or synchronises.  There is no
 // fallback path (cuLA PR #110, "feat(cp): add opt-in NVSHMEM CP state handoff",
 // §Supported configuration: request an error instead of fallback).
+#include <cmath>
 #include <cstdint>
 #include <initializer_list>
 #include <mutex>
@@ -703,4 +704,85 @@ extern "C" int kda_decode_step(int32_t B, int32_t H, int32_t type, const int32_t
     const kda::DecodeIn in{q, k, v, g, beta, ldq, ldk, ldv, ldg, ldb};
     return cuda_status(kda::launch_decode_step(B, H, type, slots, num_slots, in, scale, state, o, ldo,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the attention layer beside the KDA layer -----------------------------------------------------------
+
+namespace {
+
+// What both directions of the head norms check of the arguments they share; 'x': whether q and k are read.
+int head_in_ok(const kda::HeadIn &a, int32_t type, int32_t pairs, bool x)
+{
+    const int e = kda::elem_bytes(type);
+    if (a.T < 0 || a.H < 1 || a.Hk < 0 || a.d < 1 || !e || a.rot < 0) return KDA_ERR_INVALID_ARG;
+    if ((a.norm != 0 && a.norm != 1) || (pairs != KDA_PAIRS_HALVES && pairs != KDA_PAIRS_ADJACENT)) return KDA_ERR_INVALID_ARG;
+    if (a.d != 32 && a.d != 64 && a.d != 128 && a.d != 256) return KDA_ERR_UNSUPPORTED;
+    if (a.rot > a.d || a.rot % 16) return KDA_ERR_UNSUPPORTED;
+    if (a.norm ? !(a.eps >= 0.f) : (a.w_q || a.w_k)) return KDA_ERR_INVALID_ARG;
+    if (!floats_ok_or_null(a.w_q) || !floats_ok_or_null(a.w_k) || (!a.Hk && a.w_k)) return KDA_ERR_INVALID_ARG;
+    if (a.T == 0) return KDA_OK;   // no rows: their addresses do not matter
+    if (a.rot && (!a.positions || (reinterpret_cast<uintptr_t>(a.positions) & 3u) || !a.phases || (reinterpret_cast<uintptr_t>(a.phases) & 7u)))
+        return KDA_ERR_INVALID_ARG;
+    const int64_t w = static_cast<int64_t>(a.H) * a.d, wk = static_cast<int64_t>(a.Hk) * a.d;
+    if (x && (!rows_ok(a.q, a.ldq, w, e) || (a.Hk ? !rows_ok(a.k, a.ldk, wk, e) : a.k != nullptr))) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+bool head_rows_ok(const kda::HeadIn &a, int32_t type, const kda::HeadOut &x)
+{
+    const int e = kda::elem_bytes(type);
+    return rows_ok(x.q, x.ldq, static_cast<int64_t>(a.H) * a.d, e) &&
+           (a.Hk ? rows_ok(x.k, x.ldk, static_cast<int64_t>(a.Hk) * a.d, e) : x.k == nullptr);
+}
+
+}  // namespace
+
+extern "C" int kda_rotary_phases(const double *frequencies, int32_t n, uint64_t *phases)
+{
+    if (n < 0 || (n && (!frequencies || !phases))) return KDA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i) {
+        if (!std::isfinite(frequencies[i])) return KDA_ERR_INVALID_ARG;
+        const double turns = frequencies[i] / 6.283185307179586476925286766559, part = turns - std::floor(turns);
+        // the fraction in two halves of 32 bits; one that rounds up to a whole turn is none
+        const double top = std::floor(std::ldexp(part, 32));
+        const uint64_t low = static_cast<uint64_t>(std::ldexp(part, 64) - std::ldexp(top, 32));
+        phases[i] = (static_cast<uint64_t>(top) << 32) + low;
+    }
+    return KDA_OK;
+}
+
+extern "C" size_t kda_head_norm_rotary_workspace_bytes(int32_t d)
+{
+    return d == 32 || d == 64 || d == 128 || d == 256 ? kda::head_workspace_bytes(d) : 0;
+}
+
+extern "C" int kda_head_norm_rotary_forward(int64_t T, int32_t H, int32_t Hk, int32_t d, int32_t type, const void *q, int64_t ldq,
+                                            const void *k, int64_t ldk, int32_t norm, const float *w_q, const float *w_k, float eps,
+                                            const int32_t *positions, const uint64_t *phases, int32_t rot, int32_t pairs, void *q_out,
+                                            int64_t ldq_out, void *k_out, int64_t ldk_out, void *stream)
+{
+    const kda::HeadIn in{q, k, ldq, ldk, T, w_q, w_k, positions, phases, H, Hk, d, rot, pairs, norm, eps};
+    const kda::HeadOut out{q_out, k_out, ldq_out, ldk_out};
+    const int rc = head_in_ok(in, type, pairs, true);
+    if (rc != KDA_OK || T == 0) return rc;
+    if (!head_rows_ok(in, type, out)) return KDA_ERR_INVALID_ARG;
+    return cuda_status(kda::launch_head_forward(in, type, out, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_head_norm_rotary_backward(int64_t T, int32_t H, int32_t Hk, int32_t d, int32_t type, const void *q, int64_t ldq,
+                                             const void *k, int64_t ldk, int32_t norm, const float *w_q, const float *w_k, float eps,
+                                             const int32_t *positions, const uint64_t *phases, int32_t rot, int32_t pairs,
+                                             const void *dq_out, int64_t lddq_out, const void *dk_out, int64_t lddk_out, void *dq,
+                                             int64_t lddq, void *dk, int64_t lddk, float *dw_q, float *dw_k, void *ws, size_t ws_bytes,
+                                             void *stream)
+{
+    const kda::HeadIn in{q, k, ldq, ldk, T, w_q, w_k, positions, phases, H, Hk, d, rot, pairs, norm, eps};
+    const kda::HeadOut g{const_cast<void *>(dq_out), const_cast<void *>(dk_out), lddq_out, lddk_out}, dx{dq, dk, lddq, lddk};
+    if (const int rc = head_in_ok(in, type, pairs, norm != 0)) return rc;
+    if ((dw_q && !w_q) || (dw_k && !w_k) || !floats_ok_or_null(dw_q) || !floats_ok_or_null(dw_k)) return KDA_ERR_INVALID_ARG;
+    if (T > 0 && (!head_rows_ok(in, type, g) || !head_rows_ok(in, type, dx))) return KDA_ERR_INVALID_ARG;
+    if (dw_q || dw_k) {
+        if (!ws || !aligned16(ws)) return KDA_ERR_INVALID_ARG;
+        if (ws_bytes < kda::head_workspace_bytes(d)) return KDA_ERR_WORKSPACE;
+    }
+    return cuda_status(kda::launch_head_backward(in, type, g, dx, dw_q, dw_k, ws, static_cast<cudaStream_t>(stream)));
 }

@@ -266,4 +266,23 @@ cudaError_t launch_decode_step(int B, int H, int type, const int32_t *slots, int
                                float *state, void *o, int64_t ldo, cudaStream_t stream);
 int take_decode_status();
 
+// The attention layer beside the KDA layer (head_rotary.cu, window_attention*.cu, window_cache.cu).
+struct HeadIn {
+    const void *q, *k;                // [T][H][d], [T][Hk][d] (null, Hk 0: absent)
+    int64_t ldq, ldk, T;
+    const float *w_q, *w_k;           // [d], null: 1
+    const int32_t *positions;         // [T]
+    const uint64_t *phases;           // [rot / 2]
+    int H, Hk, d, rot, adjacent, norm;
+    float eps;
+};
+struct HeadOut {
+    void *q, *k;
+    int64_t ldq, ldk;
+};
+size_t head_workspace_bytes(int d);
+cudaError_t launch_head_forward(const HeadIn &in, int type, const HeadOut &out, cudaStream_t stream);
+cudaError_t launch_head_backward(const HeadIn &in, int type, const HeadOut &g, const HeadOut &dx, float *dw_q, float *dw_k, void *ws,
+                                 cudaStream_t stream);
+
 }  // namespace kda

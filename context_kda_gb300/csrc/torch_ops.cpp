@@ -335,6 +335,72 @@ PyObject *decode_step(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
+// The heads of a token are adjacent: [T][heads][d] (or [T][heads * d] rows) with a token stride.
+struct Heads {
+    const at::Tensor *t;
+    int64_t T, H, d;
+    explicit Heads(const at::Tensor *x) : t(x), T(0), H(0), d(0)
+    {
+        if (!x) return;
+        need(x->dim() == 3);
+        T = x->size(0), H = x->size(1), d = x->size(2);
+    }
+};
+
+// What both directions of the head norms take first; the shapes come from q or, where it is absent, from the gradients.
+struct HeadArgs {
+    const at::Tensor *q, *k;
+    int64_t norm;
+    const at::Tensor *w_q, *w_k;
+    float eps;
+    const at::Tensor *positions, *phases;
+    int64_t pairs, rot;
+    explicit HeadArgs(Args &a)
+        : q(a.tensor()), k(a.tensor()), norm(a.integer()), w_q(a.tensor()), w_k(a.tensor()), eps(a.real()), positions(a.tensor()),
+          phases(a.tensor()), pairs(a.integer()), rot(phases ? 2 * phases->numel() : 0)
+    {
+        need((positions != nullptr) == (phases != nullptr));
+    }
+    const uint64_t *phase_words() const { return reinterpret_cast<const uint64_t *>(flat<int64_t>(phases, rot / 2, at::kLong)); }
+};
+
+PyObject *head_norm_rotary_forward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_head_norm_rotary_forward", [&] {
+        Args a(args, n, 12);
+        const HeadArgs p(a);
+        const Heads q(p.q), k(p.k);
+        need(p.q && (!p.k || k.d == q.d));
+        const at::ScalarType ty = p.q->scalar_type();
+        const int64_t T = q.T, w = q.H * q.d, wk = k.H * q.d;
+        const Rows rq = rows_of(p.q, T, w, ty), rk = rows_of(p.k, T, wk, ty), oq = rows_of(a.tensor(false), T, w, ty), ok = rows_of(a.tensor(), T, wk, ty);
+        return kda_head_norm_rotary_forward(T, i32(q.H), i32(k.H), i32(q.d), type_code(ty), rq.p, rq.ld, rk.p, rk.ld, i32(p.norm), floats(p.w_q, q.d),
+                                            floats(p.w_k, q.d), p.eps, flat<int32_t>(p.positions, T, at::kInt), p.phase_words(), i32(p.rot),
+                                            i32(p.pairs), oq.p, oq.ld, ok.p, ok.ld, a.stream());
+    });
+}
+
+PyObject *head_norm_rotary_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_head_norm_rotary_backward", [&] {
+        Args a(args, n, 17);
+        const HeadArgs p(a);
+        const at::Tensor *gq = a.tensor(false), *gk = a.tensor();
+        const Heads q(gq), k(gk);
+        need(!gk || k.d == q.d);
+        const at::ScalarType ty = gq->scalar_type();
+        const int64_t T = q.T, w = q.H * q.d, wk = k.H * q.d;
+        const Rows rq = rows_of(p.q, T, w, ty), rk = rows_of(p.k, T, wk, ty), rgq = rows_of(gq, T, w, ty), rgk = rows_of(gk, T, wk, ty);
+        const Rows dq = rows_of(a.tensor(false), T, w, ty), dk = rows_of(a.tensor(), T, wk, ty);
+        float *dw_q = floats(a.tensor(), q.d), *dw_k = floats(a.tensor(), q.d);
+        const Bytes ws = workspace(a.tensor());
+        return kda_head_norm_rotary_backward(T, i32(q.H), i32(k.H), i32(q.d), type_code(ty), rq.p, rq.ld, rk.p, rk.ld, i32(p.norm),
+                                             floats(p.w_q, q.d), floats(p.w_k, q.d), p.eps, flat<int32_t>(p.positions, T, at::kInt),
+                                             p.phase_words(), i32(p.rot), i32(p.pairs), rgq.p, rgq.ld, rgk.p, rgk.ld, dq.p, dq.ld, dk.p, dk.ld,
+                                             dw_q, dw_k, ws.p, ws.n, a.stream());
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -345,6 +411,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(gated_scan_forward), FAST(gated_scan_backward), FAST(gated_scan_step),
                            FAST(block_norm_forward), FAST(block_norm_backward), FAST(decode_step),
+                           FAST(head_norm_rotary_forward), FAST(head_norm_rotary_backward),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", "Argument marshalling of the operators around the KDA layer.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -620,6 +620,61 @@ int kda_decode_step(int32_t B, int32_t H, int32_t type, const int32_t *slots, in
                     int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const float *g, int64_t ldg,
                     const float *beta, int64_t ldb, float scale, float *state, void *o, int64_t ldo, void *stream);
 
+/* ---- The attention layer beside the KDA layer --------------------------------------------------------
+ *
+ * Hybrid decoders put a layer of local attention between their recurrent ones.  Conventions as for the
+ * operators above; heads of a token are adjacent, [T][heads][d], with the token stride 'ld' in elements. */
+
+enum { KDA_PAIRS_HALVES = 0, KDA_PAIRS_ADJACENT = 1 };
+
+/*
+ * kda_head_norm_rotary_forward -- the norm of every query and key head and the rotation by position, in one pass:
+ *     n = x / sqrt(mean(x^2) + eps) * w          (norm 0: n = x; w NULL: 1)
+ *     (a, b) -> (a cos - b sin, a sin + b cos)   for every pair of the first 'rot' channels of n,
+ * the angle positions[t] times the pair's frequency.  w = d^-1/2 gives heads of unit length, as KDA's q and k.
+ *   T, H, Hk, d     tokens, heads of q and of k (Hk 0: k is NULL), channels of a head: 32, 64, 128 or 256 (others:
+ *                   KDA_ERR_UNSUPPORTED).
+ *   q, k            [T][H][d], [T][Hk][d] of 'type'; token strides ldq, ldk (>= heads * d).
+ *   w_q, w_k        fp32 [d] or NULL (NULL where norm is 0).
+ *   positions       device int32 [T]; phases  device [rot / 2] of kda_rotary_phases; both may be NULL where rot is 0.
+ *   rot             rotated channels: a multiple of 16 up to d (others: KDA_ERR_UNSUPPORTED); 0: no rotation.
+ *   pairs           KDA_PAIRS_HALVES: channels i and i + rot / 2; KDA_PAIRS_ADJACENT: 2 i and 2 i + 1.
+ *   q_out, k_out out as q, k; may be q, k themselves (same address and stride).
+ * T = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
+ */
+int kda_head_norm_rotary_forward(int64_t T, int32_t H, int32_t Hk, int32_t d, int32_t type, const void *q, int64_t ldq,
+                                 const void *k, int64_t ldk, int32_t norm, const float *w_q, const float *w_k, float eps,
+                                 const int32_t *positions, const uint64_t *phases, int32_t rot, int32_t pairs, void *q_out,
+                                 int64_t ldq_out, void *k_out, int64_t ldk_out, void *stream);
+
+/*
+ * kda_head_norm_rotary_backward -- the gradients of kda_head_norm_rotary_forward from those of its outputs.
+ *   q, k and the rest   the forward's (q and k may be NULL where norm is 0: they are not read).
+ *   dq_out, dk_out  [T][H][d], [T][Hk][d] of 'type'.
+ *   dq, dk      out as q, k; may be dq_out, dk_out themselves (same address and stride).
+ *   dw_q, dw_k  out fp32 [d] or NULL (not written; NULL where the weight is).  Sums over tokens and heads in an order that
+ *                   depends on sizes only: the same call gives the same bits.  T = 0 writes zeros.
+ *   ws, ws_bytes    device workspace of at least kda_head_norm_rotary_workspace_bytes(d) bytes (may be NULL where dw_q and
+ *                   dw_k are).
+ * Returns as the forward, or KDA_ERR_WORKSPACE.
+ */
+int kda_head_norm_rotary_backward(int64_t T, int32_t H, int32_t Hk, int32_t d, int32_t type, const void *q, int64_t ldq,
+                                  const void *k, int64_t ldk, int32_t norm, const float *w_q, const float *w_k, float eps,
+                                  const int32_t *positions, const uint64_t *phases, int32_t rot, int32_t pairs,
+                                  const void *dq_out, int64_t lddq_out, const void *dk_out, int64_t lddk_out, void *dq,
+                                  int64_t lddq, void *dk, int64_t lddk, float *dw_q, float *dw_k, void *ws, size_t ws_bytes,
+                                  void *stream);
+
+/* Device workspace bytes of kda_head_norm_rotary_backward (0: d is none of its widths). */
+size_t kda_head_norm_rotary_workspace_bytes(int32_t d);
+
+/*
+ * kda_rotary_phases -- host: n frequencies (radians a position, any finite values) as 64-bit fractions of a turn, the form in
+ * which the calls above take them: position * phase modulo 2^64 is then the angle's fraction of a turn, and far positions
+ * lose nothing.  Returns KDA_OK or KDA_ERR_INVALID_ARG.
+ */
+int kda_rotary_phases(const double *frequencies, int32_t n, uint64_t *phases);
+
 #ifdef __cplusplus
 }
 #endif
