@@ -80,9 +80,10 @@ def _load():
                                                   P, P, P, SZ, P]
     lib.kda_head_norm_rotary_workspace_bytes.argtypes = [I32]
     lib.kda_head_norm_rotary_workspace_bytes.restype = SZ
+    lib.kda_window_attention_forward.argtypes = [P, P, I32, I32, I32, I32, *R, *R, *R, F, I32, I32, *R, P, P]
     for name in ("kda_gated_scan_forward", "kda_gated_scan_backward", "kda_gated_scan_step", "kda_block_norm_forward",
                  "kda_block_norm_backward", "kda_decode_step", "kda_rotary_phases", "kda_head_norm_rotary_forward",
-                 "kda_head_norm_rotary_backward"):
+                 "kda_head_norm_rotary_backward", "kda_window_attention_forward"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("kda_plan_segments", "kda_plan_check", "kda_plan_segments_refined", "kda_workspace_layout", "kda_segment_forward", "kda_compose_summaries",
                  "kda_compose_summaries_blocked", "kda_apply_boundary", "kda_forward_segmented", "kda_forward_segmented_noalloc", "kda_backward_segmented",
@@ -373,7 +374,7 @@ def kda_head_norm_rotary_workspace_bytes(d: int) -> int:
 
 def kda_head_norm_rotary_forward(q, k, norm, w_q, w_k, eps, positions, phases, pairs, q_out, k_out, stream=None):
     """The norms of the query and key heads with the rotation by position (see include/kda.h): q [T, H, d], k [T, Hk, d] or
-    None in one activation type, weights fp32 [d] or None, positions int32 [T] and phases int64 [rot / 2] (both None: no
+    None in one activation type, weights fp32 [d] or None, positions int32 [T] and phases int64 [rot / 2] (phases None: no
     rotation), pairs "halves" or "adjacent"."""
     (_ops or _marshal()).head_norm_rotary_forward(q, k, norm, w_q, w_k, eps, positions, phases, PAIRS.get(pairs, -1), q_out, k_out, stream)
 
@@ -383,3 +384,9 @@ def kda_head_norm_rotary_backward(q, k, norm, w_q, w_k, eps, positions, phases, 
     and, without them, ws too."""
     (_ops or _marshal()).head_norm_rotary_backward(q, k, norm, w_q, w_k, eps, positions, phases, PAIRS.get(pairs, -1), dq_out, dk_out,
                                                    dq, dk, dw_q, dw_k, ws, stream)
+
+
+def kda_window_attention_forward(plan, plan_dev, q, k, v, scale, window, sinks, o, lse, stream=None):
+    """Softmax attention over a sliding window with sinks, of every sequence of the plan (see include/kda.h): q, o [T, H, d],
+    k, v [T, Hk, d] in bf16 or fp16, lse fp32 [H, T] or None."""
+    (_ops or _marshal()).window_attention_forward(_words(plan), plan_dev, q, k, v, scale, window, sinks, o, lse, stream)

@@ -181,7 +181,7 @@ extern "C" int kda_device_status(void)
     int worst = KDA_OK;
     for (int st : {kda::take_prep_status(), kda::take_state_status(), kda::take_compose_status(),
                    kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status(),
-                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status()})
+                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status(), kda::take_window_status()})
         if (st != KDA_OK && worst == KDA_OK) worst = st;
     return worst;
 }
@@ -785,4 +785,43 @@ extern "C" int kda_head_norm_rotary_backward(int64_t T, int32_t H, int32_t Hk, i
         if (ws_bytes < kda::head_workspace_bytes(d)) return KDA_ERR_WORKSPACE;
     }
     return cuda_status(kda::launch_head_backward(in, type, g, dx, dw_q, dw_k, ws, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Rows on 16 bytes: what the copies of the attention's tiles take.
+bool rows16_ok(const void *p, int64_t ld, int64_t width) { return p && aligned16(p) && ld >= width && ld % 8 == 0; }
+
+int window_shape_ok(const kda::WindowIn &in, int32_t type)
+{
+    if (in.H < 1 || in.Hk < 1 || in.H % in.Hk || in.d < 1 || !kda::elem_bytes(type) || in.W < 1 || in.S < 0) return KDA_ERR_INVALID_ARG;
+    const float c = in.scale * 1.44269504088896340736f;
+    if (!(c > 0.f) || !std::isnormal(c)) return KDA_ERR_INVALID_ARG;
+    if (type == KDA_TYPE_F32 || (in.d != 64 && in.d != 128) || in.S > KDA_WINDOW_MAX_SINKS) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// What the forward and the backward check of the arguments they share.
+int window_in_ok(const int32_t *plan, const int32_t *plan_dev, const kda::WindowIn &in, int32_t type)
+{
+    if (!plan_ok(plan) || !plan_dev) return KDA_ERR_INVALID_ARG;
+    if (const int rc = window_shape_ok(in, type)) return rc;
+    const int64_t w = static_cast<int64_t>(in.H) * in.d, wk = static_cast<int64_t>(in.Hk) * in.d;
+    if (!rows16_ok(in.q, in.ldq, w) || !rows16_ok(in.k, in.ldk, wk) || !rows16_ok(in.v, in.ldv, wk)) return KDA_ERR_INVALID_ARG;
+    // a head's tiles of 128 tokens, and one more for each sequence, are blocks of one grid
+    const int64_t T = plan[KDA_PH_T], N = plan[KDA_PH_N];
+    if (T > kda::WINDOW_MAX_T || (T / 128 + N) * in.H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
+                                            const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                            float scale, int32_t window, int32_t sinks, void *o, int64_t ldo, float *lse, void *stream)
+{
+    const kda::WindowIn in{q, k, v, ldq, ldk, ldv, H, Hk, d, window, sinks, scale};
+    if (const int rc = window_in_ok(plan, plan_dev, in, type)) return rc;
+    if (!rows16_ok(o, ldo, static_cast<int64_t>(H) * d) || !floats_ok_or_null(lse)) return KDA_ERR_INVALID_ARG;
+    return cuda_status(kda::launch_window_forward(plan, plan_dev, type, in, o, ldo, lse, static_cast<cudaStream_t>(stream)));
 }

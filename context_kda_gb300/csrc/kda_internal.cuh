@@ -285,4 +285,15 @@ cudaError_t launch_head_forward(const HeadIn &in, int type, const HeadOut &out, 
 cudaError_t launch_head_backward(const HeadIn &in, int type, const HeadOut &g, const HeadOut &dx, float *dw_q, float *dw_k, void *ws,
                                  cudaStream_t stream);
 
+struct WindowIn {
+    const void *q, *k, *v;            // [T][H][d], [T][Hk][d] twice
+    int64_t ldq, ldk, ldv;
+    int H, Hk, d, W, S;
+    float scale;
+};
+cudaError_t launch_window_forward(const int32_t *plan_host, const int32_t *plan_dev, int type, const WindowIn &in, void *o, int64_t ldo,
+                                  float *lse, cudaStream_t stream);
+constexpr int WINDOW_MAX_T = INT32_MAX - 512;    // a tile's rows behind the last token are 32-bit numbers too
+int take_window_status();
+
 }  // namespace kda

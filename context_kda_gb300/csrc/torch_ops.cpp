@@ -359,7 +359,7 @@ struct HeadArgs {
         : q(a.tensor()), k(a.tensor()), norm(a.integer()), w_q(a.tensor()), w_k(a.tensor()), eps(a.real()), positions(a.tensor()),
           phases(a.tensor()), pairs(a.integer()), rot(phases ? 2 * phases->numel() : 0)
     {
-        need((positions != nullptr) == (phases != nullptr));
+        need(positions || !phases);
     }
     const uint64_t *phase_words() const { return reinterpret_cast<const uint64_t *>(flat<int64_t>(phases, rot / 2, at::kLong)); }
 };
@@ -401,6 +401,41 @@ PyObject *head_norm_rotary_backward(PyObject *, PyObject *const *args, Py_ssize_
     });
 }
 
+// q, k and v of the window attention.
+struct WindowArgs {
+    Heads q, k;
+    at::ScalarType ty;
+    Rows rq, rk, rv;
+    float scale;
+    int32_t window, sinks;
+    WindowArgs(Args &a, int64_t T) : q(a.tensor(false)), k(a.tensor(false)), ty(q.t->scalar_type())
+    {
+        need(q.T == T && k.d == q.d);
+        rq = rows_of(q.t, T, q.H * q.d, ty);
+        rk = rows_of(k.t, T, k.H * q.d, ty);
+        const Heads v(a.tensor(false));
+        need(v.H == k.H && v.d == q.d);
+        rv = rows_of(v.t, T, k.H * q.d, ty);
+        scale = a.real();
+        window = i32(a.integer());
+        sinks = i32(a.integer());
+    }
+};
+
+PyObject *window_attention_forward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_window_attention_forward", [&] {
+        Args a(args, n, 11);
+        const Plan plan(a);
+        const int64_t T = plan.words[KDA_PH_T];
+        const WindowArgs p(a, T);
+        const Rows o = rows_of(a.tensor(false), T, p.q.H * p.q.d, p.ty);
+        float *lse = floats(a.tensor(), p.q.H * T);
+        return kda_window_attention_forward(plan.words, plan.dev, i32(p.q.H), i32(p.k.H), i32(p.q.d), type_code(p.ty), p.rq.p, p.rq.ld, p.rk.p,
+                                            p.rk.ld, p.rv.p, p.rv.ld, p.scale, p.window, p.sinks, o.p, o.ld, lse, a.stream());
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -412,6 +447,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 PyMethodDef g_methods[] = {FAST(gated_scan_forward), FAST(gated_scan_backward), FAST(gated_scan_step),
                            FAST(block_norm_forward), FAST(block_norm_backward), FAST(decode_step),
                            FAST(head_norm_rotary_forward), FAST(head_norm_rotary_backward),
+                           FAST(window_attention_forward),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", "Argument marshalling of the operators around the KDA layer.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,434 @@
+// Attention over a sliding window with sinks, forward: o = softmax(scale q k^T) v over the visible keys, one pass over the
+// keys with the running maximum and sum of every row.
+//
+// A CTA works two tiles of 128 query rows against the same tiles of keys: two heads that share a key head, or else two
+// neighbouring tiles of one head.  Warp 0 fetches (TMA), warp 1 issues the products (tcgen05), warps 2 and 3 look
+// after the values (below), and four warps a row tile do its softmax, a thread a row.  Scores S = Q K^T lie in TMEM; a row's
+// probabilities take the scores' place there as the A operand of O += P V.  While one row tile's probabilities are
+// computed, the tensor cores work for the other.
+// A row's maximum is followed lazily: O is multiplied up only when the maximum has grown by more than 2^8 since, which
+// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so there always is a maximum.
+// Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
+// the values before rounding.
+//
+// Values behind a masked place are multiplied by a probability of zero, which an infinity or NaN would survive.  Warps
+// 2 and 3 therefore look through the value tiles that some row sees only a part of, put zeros in the place of such values (and of the rows
+// behind the sequence's end) and leave a mark; the rows that do see one add it at the end, from memory.
+#include "window_attention.cuh"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+__device__ int g_window_status;
+
+constexpr int THREADS = 384;
+constexpr float LAZY = 8.f;               // growth of a row's maximum, in powers of two, that O is not corrected for
+
+template <int D> struct Smem {
+    static constexpr uint32_t T_BYTES = D / 64 * BOX;
+    static constexpr int KS = D == 128 ? 3 : 4, VS = D == 128 ? 2 : 4;
+    static constexpr uint32_t Q = 0, K = 2 * T_BYTES, V = K + KS * T_BYTES, BYTES = V + VS * T_BYTES, ALLOC = BYTES + 1024;
+    static_assert(ALLOC <= 227 * 1024, "shared memory");
+};
+
+// TMEM columns: scores (probabilities in their first half), outputs
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+
+// What the roles know of a CTA's work: its row tiles x = 0, 1 and the key tiles, from the diagonal down, the sinks' last.
+struct Plan {
+    int rows[2], t0[2], head[2];          // rows that exist, first row in the sequence
+    int lo[2], hi[2];                     // key tiles of the window; none: lo > hi
+    bool sink[2];
+    int top, n_win, n;                    // highest key tile, tiles of the windows, all tiles
+
+    __device__ bool is_sink(int i) const { return i >= n_win; }
+    __device__ int tile(int i) const { return i < n_win ? top - i : 0; }
+    __device__ bool active(int x, int i) const { return is_sink(i) ? sink[x] : tile(i) >= lo[x] && tile(i) <= hi[x]; }
+    // Keys [a, b] of tile i that row r of row tile x sees.
+    __device__ void visible(int x, int i, int r, int W, int S, int &a, int &b) const
+    {
+        const int row = t0[x] + r, j0 = tile(i) * TILE;
+        a = is_sink(i) ? 0 : max(0, row - W + 1 - j0);           // (row - W is above -2^31)
+        b = is_sink(i) ? min(S - 1, row - W) : min(TILE - 1, row - j0);
+    }
+    // Whether some row of x sees only a part of tile i, or the tile passes the sequence's end.
+    __device__ bool masked(int x, int i, int len, int W) const
+    {
+        const int j0 = tile(i) * TILE;
+        return is_sink(i) || j0 + TILE - 1 > t0[x] || j0 < t0[x] + TILE - W || j0 + TILE > len;
+    }
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    window_forward(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const Shape p, bool two_heads, const E *v_rows, int64_t ldv, E *o, int64_t ldo, float *lse)
+{
+    using L = Smem<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_vfix[L::VS], s_s[2], s_p[2], s_o[2], s_end;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (!plan_matches(p.plan, p.sig)) {
+        if (tid == 0 && blockIdx.x == 0) record_status(&g_window_status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    Place at;
+    const int span = two_heads ? TILE : 2 * TILE;
+    const int works = two_heads ? p.H / 2 : p.H, slot = (gridDim.x - 1 - blockIdx.x) / works, work = (gridDim.x - 1 - blockIdx.x) % works;
+    if (!find_tile(p, slot, span, at)) return;      // the last rows of a sequence, which see the most, come first
+    Plan w;
+    const int g = p.H / p.Hk;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        w.head[x] = two_heads ? 2 * work + x : work;
+        w.t0[x] = at.t0 + (two_heads ? 0 : x * TILE);
+        w.rows[x] = min(TILE, at.len - w.t0[x]);
+        w.hi[x] = w.rows[x] > 0 ? w.t0[x] / TILE : -1;
+        w.lo[x] = max(0, w.t0[x] - p.W + 1) / TILE;
+        w.sink[x] = w.rows[x] > 0 && p.S > 0 && w.t0[x] + w.rows[x] - 1 >= p.W;
+    }
+    w.top = max(w.hi[0], w.hi[1]);
+    w.n_win = w.top - w.lo[0] + 1;
+    w.n = w.n_win + (w.sink[0] || w.sink[1]);
+    const int hk = w.head[0] / g;
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *const basep = smem_raw + (base - smem_u32(smem_raw));
+    if (tid == 0) {
+        mbar_init(smem_u32(&s_q), 1);
+        for (int i = 0; i < L::KS; ++i) mbar_init(smem_u32(&s_kfull[i]), 1), mbar_init(smem_u32(&s_kfree[i]), 1);
+        for (int i = 0; i < L::VS; ++i) mbar_init(smem_u32(&s_vfull[i]), 1), mbar_init(smem_u32(&s_vfree[i]), 1), mbar_init(smem_u32(&s_vfix[i]), 2);
+        for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&s_s[x]), 1), mbar_init(smem_u32(&s_p[x]), 4), mbar_init(smem_u32(&s_o[x]), 1);
+        mbar_init(smem_u32(&s_end), 1);
+        s_abort = 0;
+        s_bad = 0;
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&s_tmem), TM_COLS);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *const abort_flag = &s_abort;
+    auto give_up = [&] {
+        record_status(&g_window_status, KDA_ERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    int fetched[2] = {0, 0};              // (the fetching thread) tiles of keys and of values
+    if (warp == 0) {
+        // ---- fetch
+        if (lane == 0) {
+            auto load = [&](const CUtensorMap &m, uint32_t dst, int head, int row, uint32_t bar) {
+                for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, head, at.start + row, bar);
+            };
+            const uint32_t bq = smem_u32(&s_q);
+            mbar_arrive_expect_tx(bq, (w.rows[1] > 0 ? 2 : 1) * L::T_BYTES);
+            load(mq, base + L::Q, w.head[0], w.t0[0], bq);
+            if (w.rows[1] > 0) load(mq, base + L::Q + L::T_BYTES, w.head[1], w.t0[1], bq);
+            bool ok = true;
+            int &ks = fetched[0], &vs = fetched[1];
+            for (int i = 0; i <= w.n && ok; ++i) {       // keys a tile ahead of the values
+                if (i < w.n) {
+                    const int s = i % L::KS;
+                    if (i >= L::KS) ok = mbar_wait(smem_u32(&s_kfree[s]), (i / L::KS - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(smem_u32(&s_kfull[s]), L::T_BYTES);
+                    load(mk, base + L::K + s * L::T_BYTES, hk, w.tile(i) * TILE, smem_u32(&s_kfull[s]));
+                    ++ks;
+                }
+                if (i > 0) {
+                    const int s = (i - 1) % L::VS;
+                    if (i - 1 >= L::VS) ok = mbar_wait(smem_u32(&s_vfree[s]), ((i - 1) / L::VS - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(smem_u32(&s_vfull[s]), L::T_BYTES);
+                    load(mv, base + L::V + s * L::T_BYTES, hk, w.tile(i - 1) * TILE, smem_u32(&s_vfull[s]));
+                    ++vs;
+                }
+            }
+            if (!ok) give_up();
+        }
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t ID_S = idesc<E>(TILE, TILE, 0), ID_O = idesc<E>(TILE, D, 1);
+            auto scores = [&](int x, int i) {
+                const uint32_t q = base + L::Q + x * L::T_BYTES, k = base + L::K + (i % L::KS) * L::T_BYTES;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = (s / 4) * BOX + (s % 4) * 32;
+                    mma_bf16(tmem + TM_S + x * 128, sdesc_sw128(q + off), sdesc_sw128(k + off), ID_S, s > 0);
+                }
+                commit(smem_u32(&s_s[x]));
+            };
+            bool ok = mbar_wait(smem_u32(&s_q), 0) && mbar_wait(smem_u32(&s_kfull[0]), 0);
+            int done[2] = {0, 0};
+            if (ok) {
+                fence_after();
+                for (int x = 0; x < 2; ++x)
+                    if (w.active(x, 0)) scores(x, 0);
+                commit(smem_u32(&s_kfree[0]));
+            }
+            for (int i = 0; i < w.n && ok; ++i) {
+                const uint32_t v = base + L::V + (i % L::VS) * L::T_BYTES;
+                const bool more = i + 1 < w.n;
+                ok = mbar_wait(smem_u32(&s_vfix[i % L::VS]), (i / L::VS) & 1);
+                if (ok && more) ok = mbar_wait(smem_u32(&s_kfull[(i + 1) % L::KS]), ((i + 1) / L::KS) & 1);
+                for (int x = 0; x < 2 && ok; ++x) {
+                    if (w.active(x, i)) {
+                        ok = mbar_wait(smem_u32(&s_p[x]), done[x] & 1);
+                        if (!ok) break;
+                        fence_after();
+                        // of the sinks' tile only the rows that hold sinks
+                        const int steps = w.is_sink(i) ? (p.S + 15) / 16 : TILE / 16;
+                        for (int s = 0; s < steps; ++s)
+                            mma_bf16_ta(tmem + TM_O + x * D, tmem + TM_S + x * 128 + s * 8, sdesc_mn_sw128(v + s * 2048, BOX), ID_O,
+                                        done[x] > 0 || s > 0);
+                        ++done[x];
+                    }
+                    if (more && w.active(x, i + 1)) scores(x, i + 1);
+                }
+                commit(smem_u32(&s_vfree[i % L::VS]));
+                if (more) commit(smem_u32(&s_kfree[(i + 1) % L::KS]));
+            }
+            if (ok) {
+                commit(smem_u32(&s_o[0]));
+                commit(smem_u32(&s_o[1]));
+            } else {
+                give_up();
+                commit(smem_u32(&s_end));          // the products in flight end before the memory is given back
+                mbar_wait(smem_u32(&s_end), 0);
+            }
+        }
+    } else if (warp < 4) {
+        // ---- values behind masked places
+        const int half = warp - 2;
+        bool ok = true;
+        for (int i = 0; i < w.n && ok; ++i) {
+            ok = mbar_wait_warp(smem_u32(&s_vfull[i % L::VS]), (i / L::VS) & 1);
+            if (!ok) break;
+            if (!((w.active(0, i) && w.masked(0, i, at.len, p.W)) || (w.active(1, i) && w.masked(1, i, at.len, p.W)))) {
+                if (lane == 0) mbar_arrive(smem_u32(&s_vfix[i % L::VS]));
+                continue;
+            }
+            unsigned char *const v = basep + L::V + (i % L::VS) * L::T_BYTES;
+            const int real = at.len - w.tile(i) * TILE;     // rows of the sequence
+            constexpr uint32_t INF = Pair<E>::INF;
+            bool bad = false;
+            for (int r = half * 64; r < half * 64 + 64; r += 4)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const int row = r + lane / 8;
+                    uint4 *const at16 = reinterpret_cast<uint4 *>(v + c * BOX + row * 128 + (lane & 7) * 16);
+                    uint4 x = *at16;
+                    uint32_t *const e = reinterpret_cast<uint32_t *>(&x);
+                    bool hit = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = (e[j] & INF) == INF ? 0xFFFFu : 0u, hi = (e[j] & (INF << 16)) == (INF << 16) ? 0xFFFF0000u : 0u;
+                        hit |= (lo | hi) != 0;
+                        e[j] &= ~(lo | hi);
+                    }
+                    if (row >= real) *at16 = make_uint4(0, 0, 0, 0);
+                    else if (hit) *at16 = x, bad = true;
+                }
+            bad = __any_sync(0xffffffffu, bad);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (bad) *static_cast<volatile int *>(&s_bad) = 1;
+                __threadfence_block();
+                mbar_arrive(smem_u32(&s_vfix[i % L::VS]));
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    } else {
+        // ---- softmax, a thread a row
+        const int x = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + TM_S + x * 128, to = tmem + lanes + TM_O + x * D;
+        float m = -INFINITY, sum = 0.f;      // the row's maximum (of the scores) and sum of probabilities
+        int n = 0;
+        bool ok = true;
+        for (int i = 0; i < w.n; ++i) {
+            if (!w.active(x, i)) continue;
+            ok = mbar_wait_warp(smem_u32(&s_s[x]), n & 1);
+            if (!ok) break;
+            fence_after();
+            uint32_t u[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + c * 32, u[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reg_fence32(u[c]);
+            if (w.masked(x, i, at.len, p.W)) {
+                int a, b;
+                w.visible(x, i, r, p.W, p.S, a, b);
+                const unsigned len = b >= a ? b - a + 1 : 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (static_cast<unsigned>(c * 32 + j - a) >= len) u[c][j] = 0xFF800000u;
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(u[c][j]));
+            const float new_m = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            if (n == 0) {
+                m = new_m;
+            } else if (__any_sync(0xffffffffu, (new_m - m) * p.c > LAZY)) {
+                // the products before this tile's scores are complete, O among them
+                const float f = ex2_ftz((m - new_m) * p.c);
+                m = new_m;
+                sum *= f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t t[32];
+                    tmem_ld32_nowait(to + c * 32, t);
+                    tmem_wait_ld();
+                    reg_fence32(t);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) t[j] = __float_as_uint(__uint_as_float(t[j]) * f);
+                    tmem_st32_nowait(to + c * 32, t);
+                }
+            }
+            const float2 cc = make_float2(p.c, p.c), mc = make_float2(-m * p.c, -m * p.c);
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t e[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float2 v = fma2(make_float2(__uint_as_float(u[c][2 * j]), __uint_as_float(u[c][2 * j + 1])), cc, mc);
+                    v.x = ex2_ftz(v.x);
+                    v.y = ex2_ftz(v.y);
+                    s2[j & 1] = add2(s2[j & 1], v);
+                    e[j] = Pair<E>::pack(v.x, v.y);
+                }
+                tmem_st16_nowait(ts + c * 16, e);
+            }
+            sum += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
+            ++n;
+        }
+        if (ok && n > 0) ok = mbar_wait_warp(smem_u32(&s_o[x]), 0);
+        if (!ok && lane == 0) give_up();
+        if (ok && n > 0) {
+            fence_after();
+            const int64_t token = at.start + w.t0[x] + r;
+            const bool real = r < w.rows[x];
+            if (lse && real) lse[static_cast<int64_t>(w.head[x]) * p.T + token] = (fmaf(m, p.c, log2f(sum))) * 0.69314718055994530942f;
+            const float inv = 1.f / sum;
+            const int bad = *static_cast<volatile int *>(&s_bad);
+            unsigned char *const out = basep + L::Q + x * L::T_BYTES;      // the queries are no longer needed: rows of D, chunks swizzled
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t t[32];
+                tmem_ld32_nowait(to + c * 32, t);
+                tmem_wait_ld();
+                reg_fence32(t);
+                float f[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(t[j]) * inv;
+                if (bad && real) {
+                    // values that are infinite or NaN: what the row sees of them
+                    for (int i = 0; i < w.n; ++i) {
+                        if (!w.active(x, i)) continue;
+                        int a, b;
+                        w.visible(x, i, r, p.W, p.S, a, b);
+                        for (int j = a; j <= b; ++j) {
+                            const E *const v = v_rows + (at.start + w.tile(i) * TILE + j) * ldv + hk * D + c * 32;
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) {
+                                const float val = to_f32(v[q]);
+                                if (!isfinite(val)) f[q] += val;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int chunk = c * 4 + q;
+                    uint4 y;
+                    y.x = Pair<E>::pack(f[8 * q], f[8 * q + 1]);
+                    y.y = Pair<E>::pack(f[8 * q + 2], f[8 * q + 3]);
+                    y.z = Pair<E>::pack(f[8 * q + 4], f[8 * q + 5]);
+                    y.w = Pair<E>::pack(f[8 * q + 6], f[8 * q + 7]);
+                    *reinterpret_cast<uint4 *>(out + r * (2 * D) + ((chunk ^ (r & 7)) << 4)) = y;
+                }
+            }
+            __syncwarp();
+            constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte pieces of a row, rows of one store of the warp
+            const int r0 = (warp & 3) * 32, ch = lane % CH;
+            E *const dst = o + (static_cast<int64_t>(at.start) + w.t0[x]) * ldo + w.head[x] * D + ch * 8;
+#pragma unroll 4
+            for (int k = 0; k < 32; k += RPI) {
+                const int row = r0 + k + lane / CH;
+                if (row < w.rows[x])
+                    *reinterpret_cast<uint4 *>(dst + row * ldo) = *reinterpret_cast<const uint4 *>(out + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0) {
+        if (s_abort && lane == 0) {     // the copies in flight end before the memory is given back
+            mbar_wait(smem_u32(&s_q), 0);
+            for (int i = 0; i < L::KS && i < fetched[0]; ++i) mbar_wait(smem_u32(&s_kfull[i]), ((fetched[0] - 1 - i) / L::KS) & 1);
+            for (int i = 0; i < L::VS && i < fetched[1]; ++i) mbar_wait(smem_u32(&s_vfull[i]), ((fetched[1] - 1 - i) / L::VS) & 1);
+        }
+        __syncwarp();
+        tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+template <typename E, int D>
+cudaError_t forward(const Shape &p, const WindowIn &in, void *o, int64_t ldo, float *lse, cudaStream_t stream)
+{
+    CUtensorMap mq, mk, mv;
+    const bool bf16 = Pair<E>::BF16;
+    if (!encode_heads(&mq, in.q, bf16, D, p.H, p.T, in.ldq, TILE) || !encode_heads(&mk, in.k, bf16, D, p.Hk, p.T, in.ldk, TILE) ||
+        !encode_heads(&mv, in.v, bf16, D, p.Hk, p.T, in.ldv, TILE))
+        return cudaErrorInvalidValue;
+    const void *fn = reinterpret_cast<const void *>(&window_forward<E, D>);
+    const cudaError_t e = set_dynamic_smem(fn, Smem<D>::ALLOC);
+    if (e != cudaSuccess) return e;
+    const bool two_heads = p.H / p.Hk % 2 == 0;
+    const int64_t grid = static_cast<int64_t>(two_heads ? p.H / 2 : p.H) * tile_slots(p.T, p.N, two_heads ? TILE : 2 * TILE);
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    window_forward<E, D><<<static_cast<int>(grid), THREADS, Smem<D>::ALLOC, stream>>>(mq, mk, mv, p, two_heads, static_cast<const E *>(in.v), in.ldv,
+                                                                    static_cast<E *>(o), ldo, lse);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_forward(const int32_t *plan_host, const int32_t *plan_dev, int type, const WindowIn &in, void *o, int64_t ldo,
+                                  float *lse, cudaStream_t stream)
+{
+    const Shape p = window_shape(plan_host, plan_dev, in);
+    if (type == KDA_TYPE_F16)
+        return in.d == 64 ? forward<__half, 64>(p, in, o, ldo, lse, stream) : forward<__half, 128>(p, in, o, ldo, lse, stream);
+    return in.d == 64 ? forward<__nv_bfloat16, 64>(p, in, o, ldo, lse, stream) : forward<__nv_bfloat16, 128>(p, in, o, ldo, lse, stream);
+}
+
+int take_window_status()
+{
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_window_status, sizeof(int)) != cudaSuccess) return KDA_ERR_CUDA;
+    if (v != 0 && cudaMemcpyToSymbol(g_window_status, &z, sizeof(int)) != cudaSuccess) return KDA_ERR_CUDA;
+    return v;
+}
+
+}  // namespace kda

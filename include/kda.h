@@ -675,6 +675,33 @@ size_t kda_head_norm_rotary_workspace_bytes(int32_t d);
  */
 int kda_rotary_phases(const double *frequencies, int32_t n, uint64_t *phases);
 
+/* The most sinks of the window attention. */
+enum { KDA_WINDOW_MAX_SINKS = 128 };
+
+/*
+ * kda_window_attention_forward -- softmax attention over a sliding window, with sinks, of every sequence of the plan:
+ *     o_i = sum_j p_ij v_j,   p_i = softmax over the visible j of scale q_i . k_j,
+ * where query i sees key j of its own sequence if j <= i and either i - j < window or j is one of the sequence's first
+ * 'sinks' tokens.  A window of the longest length or more is plain causal attention.
+ *   plan, plan_dev  a plan of kda_plan_segments and its device copy; its segments do not matter here.
+ *   H, Hk, d        query heads, key heads (H a multiple of Hk: query head h reads key head h / (H / Hk)), channels of a
+ *                   head: 64 or 128 (others: KDA_ERR_UNSUPPORTED).
+ *   type            KDA_TYPE_BF16 or KDA_TYPE_F16 (KDA_TYPE_F32: KDA_ERR_UNSUPPORTED).
+ *   q, k, v         [T][H][d], [T][Hk][d] twice; every row on 16 bytes (address and token stride).
+ *   scale           of the scores; above zero, so that scale log2(e) is a normal fp32 number.
+ *   window          at least 1.   sinks   0 to KDA_WINDOW_MAX_SINKS (more: KDA_ERR_UNSUPPORTED).
+ *   o           out [T][H][d], rows on 16 bytes.
+ *   lse         out fp32 [H][T] or NULL: log sum_j exp(scale q_i . k_j), what the backward needs.
+ * Scores, maxima and sums are fp32; probabilities are rounded to 'type' for their product with v.  A value (or score) that a
+ * query does not see has no part in its row, also where it is infinite or NaN; no sequence sees another's.  The same call
+ * gives the same bits.  T up to 2^31 - 513 (more, or more than 2^31 - 1 blocks of the grid: KDA_ERR_UNSUPPORTED).
+ * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA; a bounded wait that gave up is reported by
+ * kda_device_status() as KDA_ERR_TIMEOUT.
+ */
+int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
+                                 const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
+                                 int32_t window, int32_t sinks, void *o, int64_t ldo, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

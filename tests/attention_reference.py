@@ -36,3 +36,50 @@ def head_backward(x, norm, w, eps, positions, frequencies, pairs, g):
     dw = None if w is None else (g * hat).sum((0, 1))
     e = g if w is None else g * w
     return (e - hat * (e * hat).mean(-1, keepdims=True)) / size, dw
+
+
+def visible(n, window, sinks):
+    """[n, n]: whether row i of a sequence of n tokens sees key j."""
+    i, j = np.arange(n)[:, None], np.arange(n)[None, :]
+    return (j <= i) & ((i - j < window) | (j < sinks))
+
+
+def window_forward(cu, q, k, v, scale, window, sinks):
+    """o [T, H, d], lse [H, T] and sum p |v|, which the rounding of the probabilities goes by."""
+    T, H, d = q.shape
+    g = H // k.shape[1]
+    o, size, lse = np.zeros(q.shape), np.zeros(q.shape), np.zeros((H, T))
+    for a, b in zip(cu[:-1], cu[1:]):
+        seen = visible(b - a, window, sinks)
+        for h in range(H):
+            s = np.where(seen, scale * (q[a:b, h] @ k[a:b, h // g].T), -np.inf)
+            m = s.max(-1, keepdims=True)
+            p = np.exp(s - m)
+            l = p.sum(-1, keepdims=True)
+            lse[h, a:b] = (m + np.log(l))[:, 0]
+            o[a:b, h], size[a:b, h] = p / l @ v[a:b, h // g], p / l @ np.abs(v[a:b, h // g])
+    return o, lse, size
+
+
+def window_backward(cu, q, k, v, scale, window, sinks, do):
+    """dq, dk, dv, and for each the sum of the magnitudes that the rounding of p and ds goes by."""
+    H = q.shape[1]
+    g = H // k.shape[1]
+    out = [np.zeros(x.shape) for x in (q, k, v)]
+    size = [np.zeros(x.shape) for x in (q, k, v)]
+    for a, b in zip(cu[:-1], cu[1:]):
+        seen = visible(b - a, window, sinks)
+        for h in range(H):
+            Q, K, V, D = q[a:b, h], k[a:b, h // g], v[a:b, h // g], do[a:b, h]
+            s = np.where(seen, scale * (Q @ K.T), -np.inf)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            dp = D @ V.T
+            delta = (p * dp).sum(-1, keepdims=True)
+            ds = scale * p * (dp - delta)
+            mag = scale * p * (np.abs(dp) + np.abs(delta))     # what the difference is formed from
+            for n, (x, m) in enumerate(((ds @ K, mag @ np.abs(K)), (ds.T @ Q, mag.T @ np.abs(Q)), (p.T @ D, p.T @ np.abs(D)))):
+                at = (slice(a, b), h) if n == 0 else (slice(a, b), h // g)
+                out[n][at] += x
+                size[n][at] += m
+    return (*out, *size)

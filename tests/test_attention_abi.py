@@ -57,3 +57,39 @@ def test_binding_refuses_heads_that_do_not_fit(kda):  # noqa: F811
     assert e.value.status == kda.KDA_ERR_INVALID_ARG
     with pytest.raises(kda.KDAError):
         kda.kda_head_norm_rotary_forward(q[:, 0], None, True, None, None, 1e-6, None, None, "halves", q, None, 0)
+
+
+WINDOW = "plan plan_dev H Hk d type q ldq k ldk v ldv scale window sinks".split()
+
+
+def _window_good(kda):  # noqa: F811
+    plan = kda.kda_plan_segments([0, 300, 333], 1)
+    return plan, dict(plan=plan.ctypes.data_as(ctypes.c_void_p), plan_dev=F, H=8, Hk=2, d=64, type=BF16, q=F, ldq=512, k=F, ldk=128, v=F, ldv=128,
+                      scale=0.125, window=100, sinks=4, stream=None)
+
+
+WINDOW_BAD = [dict(plan=None), dict(plan_dev=None), dict(H=0), dict(Hk=0), dict(Hk=3), dict(d=0), dict(type=5), dict(q=None), dict(q=F + 8),
+              dict(ldq=511), dict(ldq=516), dict(k=None), dict(k=F + 2), dict(ldk=120), dict(ldk=132), dict(v=None), dict(v=F + 4), dict(ldv=64),
+              dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-39), dict(window=0),
+              dict(window=-5), dict(sinks=-1)]
+WINDOW_UNSUPPORTED = [dict(type=F32), dict(d=32), dict(d=256, ldq=2048, ldk=512, ldv=512), dict(d=96, ldq=768, ldk=192, ldv=192), dict(sinks=129),
+                      dict(H=2 ** 29, Hk=1, ldq=2 ** 40)]
+
+
+def test_window_forward_refusals(kda):  # noqa: F811
+    plan, good = _window_good(kda)
+    names = WINDOW + "o ldo lse stream".split()
+    good.update(o=F, ldo=512, lse=F)
+    _refusals(kda._lib.kda_window_attention_forward, names, good,
+              WINDOW_BAD + [dict(o=None), dict(o=F + 8), dict(ldo=504), dict(ldo=514), dict(lse=F + 2)], kda.KDA_ERR_INVALID_ARG)
+    _refusals(kda._lib.kda_window_attention_forward, names, good, WINDOW_UNSUPPORTED, kda.KDA_ERR_UNSUPPORTED)
+
+
+def test_window_forward_refuses_more_tokens_than_its_rows_count(kda):  # noqa: F811
+    """A plan that long has too many chunk records to be built here; its header alone would not pass the plan's check."""
+    plan, good = _window_good(kda)
+    bad = plan.copy()
+    bad[3] = 2 ** 31 - 100
+    good.update(o=F, ldo=512, lse=None, plan=bad.ctypes.data_as(ctypes.c_void_p))
+    names = WINDOW + "o ldo lse stream".split()
+    assert kda._lib.kda_window_attention_forward(*(good[n] for n in names)) == kda.KDA_ERR_INVALID_ARG

@@ -154,6 +154,17 @@ def test_bad_values_stay_in_their_head():
         assert changed == {(3, 1, 5), (3, 1, 21), (4, 2, 50)}
 
 
+def test_positions_without_phases():
+    """Nothing to rotate: positions are not looked at."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    dev, w = _draw(6, 2, 1, 64, "f32")
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    qo, ko = torch.empty_like(dev["q"]), torch.empty_like(dev["k"])
+    kda.kda_head_norm_rotary_forward(dev["q"], dev["k"], True, None, None, EPS, pos, None, "halves", qo, ko)
+    check(qo, ref.head_forward(w["q"], True, None, EPS, np.zeros(6), np.zeros(0), "halves"), "f32", "q")
+
+
 def test_no_rows():
     import torch
     from context_kda_gb300 import binding as kda
