@@ -81,9 +81,11 @@ def _load():
     lib.kda_head_norm_rotary_workspace_bytes.argtypes = [I32]
     lib.kda_head_norm_rotary_workspace_bytes.restype = SZ
     lib.kda_window_attention_forward.argtypes = [P, P, I32, I32, I32, I32, *R, *R, *R, F, I32, I32, *R, P, P]
+    lib.kda_window_cache_fill.argtypes = [P, P, I32, I32, I32, P, I32, *R, *R, I32, I32, P, P, P]
+    lib.kda_window_attention_step.argtypes = [I32, I32, I32, I32, I32, P, I32, P, *R, *R, *R, F, I32, I32, P, P, *R, P]
     for name in ("kda_gated_scan_forward", "kda_gated_scan_backward", "kda_gated_scan_step", "kda_block_norm_forward",
                  "kda_block_norm_backward", "kda_decode_step", "kda_rotary_phases", "kda_head_norm_rotary_forward",
-                 "kda_head_norm_rotary_backward", "kda_window_attention_forward"):
+                 "kda_head_norm_rotary_backward", "kda_window_attention_forward", "kda_window_cache_fill", "kda_window_attention_step"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("kda_plan_segments", "kda_plan_check", "kda_plan_segments_refined", "kda_workspace_layout", "kda_segment_forward", "kda_compose_summaries",
                  "kda_compose_summaries_blocked", "kda_apply_boundary", "kda_forward_segmented", "kda_forward_segmented_noalloc", "kda_backward_segmented",
@@ -390,3 +392,16 @@ def kda_window_attention_forward(plan, plan_dev, q, k, v, scale, window, sinks, 
     """Softmax attention over a sliding window with sinks, of every sequence of the plan (see include/kda.h): q, o [T, H, d],
     k, v [T, Hk, d] in bf16 or fp16, lse fp32 [H, T] or None."""
     (_ops or _marshal()).window_attention_forward(_words(plan), plan_dev, q, k, v, scale, window, sinks, o, lse, stream)
+
+
+def kda_window_cache_fill(plan, plan_dev, slots, k, v, window, sinks, cache_k, cache_v, stream=None):
+    """What the next tokens need of packed sequences into their slots' ring caches (see include/kda.h): k, v [T, Hk, d],
+    cache_k, cache_v [num_slots, Hk, sinks + window, d]; slots (int32 [N], negative: left out) may be None."""
+    (_ops or _marshal()).window_cache_fill(_words(plan), plan_dev, slots, k, v, window, sinks, cache_k, cache_v, stream)
+
+
+def kda_window_attention_step(slots, lengths, q, k, v, scale, window, sinks, cache_k, cache_v, o, stream=None):
+    """One token of the window attention for each of B slots (see include/kda.h): q, o [B, H, d], k, v [B, Hk, d], lengths int32
+    [B] (tokens before this one), the ring caches [num_slots, Hk, sinks + window, d] updated in place; slots (int32 [B],
+    negative: padding) may be None."""
+    (_ops or _marshal()).window_attention_step(slots, lengths, q, k, v, scale, window, sinks, cache_k, cache_v, o, stream)

@@ -181,7 +181,7 @@ extern "C" int kda_device_status(void)
     int worst = KDA_OK;
     for (int st : {kda::take_prep_status(), kda::take_state_status(), kda::take_compose_status(),
                    kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status(),
-                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status(), kda::take_window_status()})
+                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status(), kda::take_window_status(), kda::take_cache_status()})
         if (st != KDA_OK && worst == KDA_OK) worst = st;
     return worst;
 }
@@ -824,4 +824,49 @@ extern "C" int kda_window_attention_forward(const int32_t *plan, const int32_t *
     if (const int rc = window_in_ok(plan, plan_dev, in, type)) return rc;
     if (!rows16_ok(o, ldo, static_cast<int64_t>(H) * d) || !floats_ok_or_null(lse)) return KDA_ERR_INVALID_ARG;
     return cuda_status(kda::launch_window_forward(plan, plan_dev, type, in, o, ldo, lse, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// A ring cache's rows are counted in 32 bits.
+bool cache_ok(const void *k, const void *v, int32_t window, int32_t sinks)
+{
+    return k && v && aligned16(k) && aligned16(v) && window <= INT32_MAX - sinks;
+}
+
+}  // namespace
+
+extern "C" int kda_window_cache_fill(const int32_t *plan, const int32_t *plan_dev, int32_t Hk, int32_t d, int32_t type, const int32_t *slots,
+                                     int32_t num_slots, const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t window,
+                                     int32_t sinks, void *cache_k, void *cache_v, void *stream)
+{
+    const kda::WindowIn shape{nullptr, k, v, 0, ldk, ldv, Hk, Hk, d, window, sinks, 1.f};
+    if (!plan_ok(plan) || !plan_dev) return KDA_ERR_INVALID_ARG;
+    if (const int rc = window_shape_ok(shape, type)) return rc;
+    const int64_t wk = static_cast<int64_t>(Hk) * d;
+    if (num_slots < 0 || (!slots && plan[KDA_PH_N] > num_slots) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return KDA_ERR_INVALID_ARG;
+    if (!rows16_ok(k, ldk, wk) || !rows16_ok(v, ldv, wk) || !cache_ok(cache_k, cache_v, window, sinks)) return KDA_ERR_INVALID_ARG;
+    if (wk > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    const kda::FillIn in{k, v, ldk, ldv, slots, num_slots, Hk, d, window, sinks};
+    return cuda_status(kda::launch_window_fill(plan, plan_dev, in, cache_k, cache_v, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int kda_window_attention_step(int32_t B, int32_t H, int32_t Hk, int32_t d, int32_t type, const int32_t *slots, int32_t num_slots,
+                                         const int32_t *lengths, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                                         int64_t ldv, float scale, int32_t window, int32_t sinks, void *cache_k, void *cache_v, void *o,
+                                         int64_t ldo, void *stream)
+{
+    const kda::WindowIn shape{q, k, v, ldq, ldk, ldv, H, Hk, d, window, sinks, scale};
+    if (B < 0 || num_slots < 0 || (!slots && B > num_slots)) return KDA_ERR_INVALID_ARG;
+    if (const int rc = window_shape_ok(shape, type)) return rc;
+    if (B == 0) return KDA_OK;
+    const int64_t w = static_cast<int64_t>(H) * d, wk = static_cast<int64_t>(Hk) * d;
+    if ((reinterpret_cast<uintptr_t>(slots) & 3u) || !lengths || (reinterpret_cast<uintptr_t>(lengths) & 3u)) return KDA_ERR_INVALID_ARG;
+    if (!rows16_ok(q, ldq, w) || !rows16_ok(k, ldk, wk) || !rows16_ok(v, ldv, wk) || !rows16_ok(o, ldo, w) ||
+        !cache_ok(cache_k, cache_v, window, sinks))
+        return KDA_ERR_INVALID_ARG;
+    const int64_t blocks = (H / Hk + 7) / 8;
+    if (static_cast<int64_t>(B) * Hk > INT32_MAX / (8 * blocks)) return KDA_ERR_UNSUPPORTED;
+    const kda::StepIn in{q, k, v, ldq, ldk, ldv, slots, lengths, B, num_slots, H, Hk, d, window, sinks, scale};
+    return cuda_status(kda::launch_window_step(type, in, cache_k, cache_v, o, ldo, static_cast<cudaStream_t>(stream)));
 }

@@ -296,4 +296,21 @@ cudaError_t launch_window_forward(const int32_t *plan_host, const int32_t *plan_
 constexpr int WINDOW_MAX_T = INT32_MAX - 512;    // a tile's rows behind the last token are 32-bit numbers too
 int take_window_status();
 
+struct StepIn {
+    const void *q, *k, *v;            // [B][H][d], [B][Hk][d] twice
+    int64_t ldq, ldk, ldv;
+    const int32_t *slots, *lengths;
+    int B, num_slots, H, Hk, d, W, S;
+    float scale;
+};
+cudaError_t launch_window_step(int type, const StepIn &in, void *cache_k, void *cache_v, void *o, int64_t ldo, cudaStream_t stream);
+struct FillIn {
+    const void *k, *v;                // [T][Hk][d] of a 16-bit type
+    int64_t ldk, ldv;
+    const int32_t *slots;
+    int num_slots, Hk, d, W, S;
+};
+cudaError_t launch_window_fill(const int32_t *plan_host, const int32_t *plan_dev, const FillIn &in, void *cache_k, void *cache_v, cudaStream_t stream);
+int take_cache_status();
+
 }  // namespace kda

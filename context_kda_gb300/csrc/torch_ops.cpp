@@ -44,6 +44,12 @@ struct Args {
         if (!THPVariable_Check(o)) throw Refused{KDA_ERR_INVALID_ARG};
         return &THPVariable_Unpack(o);
     }
+    const at::Tensor *next_is_tensor()      // without taking it
+    {
+        const at::Tensor *t = tensor(false);
+        --at;
+        return t;
+    }
     int64_t integer()
     {
         const long long v = PyLong_AsLongLong(next());
@@ -436,6 +442,54 @@ PyObject *window_attention_forward(PyObject *, PyObject *const *args, Py_ssize_t
     });
 }
 
+// A ring cache [slots][Hk][sinks + window][d]; its number of slots.
+void *ring(const at::Tensor *t, int64_t Hk, int64_t rows, int64_t d, at::ScalarType ty, int64_t *slots)
+{
+    here(*t);
+    need(t->scalar_type() == ty && t->is_contiguous() && t->dim() == 4 && t->size(1) == Hk && t->size(2) == rows && t->size(3) == d);
+    if (*slots < 0) *slots = t->size(0);
+    need(t->size(0) == *slots);
+    return t->data_ptr();
+}
+
+PyObject *window_cache_fill(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_window_cache_fill", [&] {
+        Args a(args, n, 10);
+        const Plan plan(a);
+        const int64_t T = plan.words[KDA_PH_T], N = plan.words[KDA_PH_N];
+        const int32_t *slots = flat<int32_t>(a.tensor(), N, at::kInt);
+        const Heads k(a.tensor(false)), v(a.tensor(false));
+        const at::ScalarType ty = k.t->scalar_type();
+        need(v.H == k.H && v.d == k.d);
+        const Rows rk = rows_of(k.t, T, k.H * k.d, ty), rv = rows_of(v.t, T, k.H * k.d, ty);
+        const int32_t window = i32(a.integer()), sinks = i32(a.integer());
+        int64_t pool = -1;
+        void *ck = ring(a.tensor(false), k.H, static_cast<int64_t>(window) + sinks, k.d, ty, &pool);
+        void *cv = ring(a.tensor(false), k.H, static_cast<int64_t>(window) + sinks, k.d, ty, &pool);
+        return kda_window_cache_fill(plan.words, plan.dev, i32(k.H), i32(k.d), type_code(ty), slots, i32(pool), rk.p, rk.ld, rv.p, rv.ld, window,
+                                     sinks, ck, cv, a.stream());
+    });
+}
+
+PyObject *window_attention_step(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_window_attention_step", [&] {
+        Args a(args, n, 12);
+        const at::Tensor *slots = a.tensor(), *lengths = a.tensor(false), *q = a.next_is_tensor();
+        need(q->dim() == 3);
+        const int64_t B = q->size(0);
+        const WindowArgs p(a, B);
+        int64_t pool = -1;
+        void *ck = ring(a.tensor(false), p.k.H, static_cast<int64_t>(p.window) + p.sinks, p.q.d, p.ty, &pool);
+        void *cv = ring(a.tensor(false), p.k.H, static_cast<int64_t>(p.window) + p.sinks, p.q.d, p.ty, &pool);
+        const Rows o = rows_of(a.tensor(false), B, p.q.H * p.q.d, p.ty);
+        return kda_window_attention_step(i32(B), i32(p.q.H), i32(p.k.H), i32(p.q.d), type_code(p.ty), flat<int32_t>(slots, B, at::kInt), i32(pool),
+                                         flat<int32_t>(lengths, B, at::kInt), p.rq.p, p.rq.ld, p.rk.p, p.rk.ld, p.rv.p, p.rv.ld, p.scale, p.window,
+                                         p.sinks, ck, cv, o.p, o.ld, a.stream());
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -447,7 +501,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 PyMethodDef g_methods[] = {FAST(gated_scan_forward), FAST(gated_scan_backward), FAST(gated_scan_step),
                            FAST(block_norm_forward), FAST(block_norm_backward), FAST(decode_step),
                            FAST(head_norm_rotary_forward), FAST(head_norm_rotary_backward),
-                           FAST(window_attention_forward),
+                           FAST(window_attention_forward), FAST(window_cache_fill), FAST(window_attention_step),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", "Argument marshalling of the operators around the KDA layer.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -702,6 +702,40 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
                                  const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
                                  int32_t window, int32_t sinks, void *o, int64_t ldo, float *lse, void *stream);
 
+/*
+ * The ring cache of the window attention: for every slot and key head the last 'window' keys (and values) and the first 'sinks',
+ *     cache_k, cache_v   [num_slots][Hk][sinks + window][d] of 'type', contiguous, 16-byte aligned;
+ * position p is in row p if p < sinks, else in row sinks + (p - sinks) mod window.  sinks + window < 2^31.
+ *
+ * kda_window_cache_fill -- what the next tokens need of packed sequences: sequence n of the plan goes to slot slots[n] (device
+ * int32 [N], or NULL: slot n; then N <= num_slots), as if its tokens had come one at a time into an empty slot.  Rows of positions that the
+ * sequence does not have stay as they were.  A negative slot is left out; one >= num_slots too, and recorded:
+ * kda_device_status() then returns KDA_ERR_INVALID_ARG.  No slot may occur twice.
+ *   Hk, d, type, window, sinks as in kda_window_attention_forward;   k, v  [T][Hk][d], rows on 16 bytes.
+ */
+int kda_window_cache_fill(const int32_t *plan, const int32_t *plan_dev, int32_t Hk, int32_t d, int32_t type, const int32_t *slots,
+                          int32_t num_slots, const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t window,
+                          int32_t sinks, void *cache_k, void *cache_v, void *stream);
+
+/*
+ * kda_window_attention_step -- one token for each of B slots: its key and value go into the slot's cache, and its queries
+ * attend to what the cache then holds,
+ *     o_b = softmax(scale q_b . k) v   over the last 'window' positions up to its own and the first 'sinks'.
+ *   slots           device int32 [B], or NULL (row b's slot is b; then B <= num_slots).  No slot may occur twice.  A negative
+ *                   slot marks padding: its o row is zeros, no cache is touched.  A slot >= num_slots and a negative length are
+ *                   treated as padding and recorded: kda_device_status() then returns KDA_ERR_INVALID_ARG.
+ *   lengths         device int32 [B]: tokens that the slot has had before this one, which is its position; not changed.
+ *   q, o            [B][H][d];   k, v  [B][Hk][d]; rows on 16 bytes.   H, Hk, d, type, scale, window, sinks as in
+ *                   kda_window_attention_forward.
+ *   cache_k, cache_v  in/out, above.  Rows that no token has been put into are not read.
+ * B = 0 is a call without work.  The same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (as
+ * the forward; also more than 2^31 - 1 blocks, 8 B Hk ceil(H / Hk / 8)) or KDA_ERR_CUDA.
+ */
+int kda_window_attention_step(int32_t B, int32_t H, int32_t Hk, int32_t d, int32_t type, const int32_t *slots, int32_t num_slots,
+                              const int32_t *lengths, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                              int64_t ldv, float scale, int32_t window, int32_t sinks, void *cache_k, void *cache_v, void *o,
+                              int64_t ldo, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -83,3 +83,37 @@ def window_backward(cu, q, k, v, scale, window, sinks, do):
                 out[n][at] += x
                 size[n][at] += m
     return (*out, *size)
+
+
+def ring_row(p, window, sinks):
+    return p if p < sinks else sinks + (p - sinks) % window
+
+
+def cache_fill(cu, slots, k, v, window, sinks, cache_k, cache_v):
+    cache_k, cache_v = cache_k.copy(), cache_v.copy()
+    for n, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        if 0 <= slots[n] < len(cache_k):
+            for p in range(b - a):
+                cache_k[slots[n], :, ring_row(p, window, sinks)] = k[a + p]
+                cache_v[slots[n], :, ring_row(p, window, sinks)] = v[a + p]
+    return cache_k, cache_v
+
+
+def window_step(slots, lengths, q, k, v, scale, window, sinks, cache_k, cache_v):
+    """o, sum p |v| and the caches after it; a padding row's o is zeros."""
+    B, H, d = q.shape
+    g = H // k.shape[1]
+    cache_k, cache_v = cache_k.copy(), cache_v.copy()
+    o, size = np.zeros(q.shape), np.zeros(q.shape)
+    for b in range(B):
+        s, n = slots[b], lengths[b]
+        if not 0 <= s < len(cache_k) or n < 0:
+            continue
+        cache_k[s, :, ring_row(n, window, sinks)], cache_v[s, :, ring_row(n, window, sinks)] = k[b], v[b]
+        rows = min(n + 1, window + sinks)
+        for h in range(H):
+            x = scale * (cache_k[s, h // g, :rows] @ q[b, h])
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            o[b, h], size[b, h] = p @ cache_v[s, h // g, :rows], p @ np.abs(cache_v[s, h // g, :rows])
+    return o, size, cache_k, cache_v

@@ -93,3 +93,27 @@ def test_window_forward_refuses_more_tokens_than_its_rows_count(kda):  # noqa: F
     good.update(o=F, ldo=512, lse=None, plan=bad.ctypes.data_as(ctypes.c_void_p))
     names = WINDOW + "o ldo lse stream".split()
     assert kda._lib.kda_window_attention_forward(*(good[n] for n in names)) == kda.KDA_ERR_INVALID_ARG
+
+
+def test_window_step_refusals(kda):  # noqa: F811
+    names = "B H Hk d type slots num_slots lengths q ldq k ldk v ldv scale window sinks ck cv o ldo stream".split()
+    _, good = _window_good(kda)
+    good.update(B=3, slots=F, num_slots=7, lengths=F, ck=F, cv=F, o=F, ldo=512)
+    bad = [x for x in WINDOW_BAD if not set(x) & {"plan", "plan_dev"}]
+    bad += [dict(B=-1), dict(num_slots=-1), dict(slots=F + 2), dict(slots=None, num_slots=2), dict(lengths=None), dict(lengths=F + 1), dict(ck=None),
+            dict(ck=F + 8), dict(cv=None), dict(cv=F + 8), dict(o=None), dict(o=F + 8), dict(ldo=511), dict(window=2 ** 31 - 1, sinks=1)]
+    step = kda._lib.kda_window_attention_step
+    _refusals(step, names, good, bad, kda.KDA_ERR_INVALID_ARG)
+    _refusals(step, names, good, WINDOW_UNSUPPORTED[:-1] + [dict(B=2 ** 30, num_slots=2 ** 30)], kda.KDA_ERR_UNSUPPORTED)
+    _refusals(step, names, good, [dict(B=0), dict(B=0, q=None, lengths=None)], kda.KDA_OK)
+
+
+def test_window_fill_refusals(kda):  # noqa: F811
+    names = "plan plan_dev Hk d type slots num_slots k ldk v ldv window sinks ck cv stream".split()
+    _, good = _window_good(kda)
+    good.update(slots=F, num_slots=2, ck=F, cv=F)
+    bad = [x for x in WINDOW_BAD if not set(x) & {"H", "q", "ldq", "scale"} and x != dict(Hk=3)]
+    bad += [dict(num_slots=-1), dict(slots=F + 2), dict(slots=None, num_slots=1), dict(ck=None), dict(ck=F + 8), dict(cv=None), dict(cv=F + 8),
+            dict(window=2 ** 31 - 1, sinks=1)]
+    _refusals(kda._lib.kda_window_cache_fill, names, good, bad, kda.KDA_ERR_INVALID_ARG)
+    _refusals(kda._lib.kda_window_cache_fill, names, good, [dict(type=F32), dict(d=32), dict(sinks=129)], kda.KDA_ERR_UNSUPPORTED)
