@@ -173,6 +173,7 @@ def _plan(s, t):
             s["out"], s["lse_out"] = like("q"), torch.empty(s["H"], s["T"], device="cuda")
         else:
             s["dq"], s["dk"], s["dv"] = like("q"), like("k"), like("v")
+            s["o"] = s["o"].contiguous()      # as the forward call returns it
             n = kda.kda_window_attention_workspace_bytes(s["plan"], s["H"], s["Hk"], s["d"], s["W"], s["S"])
             s["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
 
