@@ -19,7 +19,7 @@ _BINDING_NAMES = ("kda_status_string", "kda_plan_segments", "kda_plan_check", "k
                   "kda_gated_scan_backward", "kda_gated_scan_workspace_bytes", "kda_gated_scan_step", "kda_block_norm_forward",
                   "kda_block_norm_backward", "kda_block_norm_workspace_bytes", "kda_decode_step", "kda_rotary_phases",
                   "kda_head_norm_rotary_forward", "kda_head_norm_rotary_backward", "kda_head_norm_rotary_workspace_bytes",
-                  "kda_window_attention_forward", "kda_window_cache_fill", "kda_window_attention_step", "upload_plan", "KDAError", "LIB_PATH")
+                  "kda_window_attention_forward", "kda_window_attention_backward", "kda_window_attention_workspace_bytes", "kda_window_cache_fill", "kda_window_attention_step", "upload_plan", "KDAError", "LIB_PATH")
 
 
 def __getattr__(name):

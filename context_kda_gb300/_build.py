@@ -19,7 +19,7 @@ OPS = os.path.join(PKG, "_ops.so")     # the marshalling module of binding.py (c
 ROOT = os.path.dirname(PKG)
 
 CUDA_SOURCES = ["api.cu", "chunk_prep.cu", "chunk_state.cu", "compose.cu", "boundary.cu", "noalloc.cu", "backward.cu", "reverse.cu",
-                "gated_scan.cu", "gated_scan_backward.cu", "decode.cu", "head_rotary.cu", "window_attention.cu", "window_cache.cu", "block_norm.cu",
+                "gated_scan.cu", "gated_scan_backward.cu", "decode.cu", "head_rotary.cu", "window_attention.cu", "window_attention_backward.cu", "window_cache.cu", "block_norm.cu",
                 "block_norm_forward_bf16.cu", "block_norm_forward_f16.cu", "block_norm_backward_bf16.cu",
                 "block_norm_backward_f16.cu"]
 CXX_SOURCES = ["plan.cpp"]

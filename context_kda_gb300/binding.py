@@ -83,9 +83,12 @@ def _load():
     lib.kda_window_attention_forward.argtypes = [P, P, I32, I32, I32, I32, *R, *R, *R, F, I32, I32, *R, P, P]
     lib.kda_window_cache_fill.argtypes = [P, P, I32, I32, I32, P, I32, *R, *R, I32, I32, P, P, P]
     lib.kda_window_attention_step.argtypes = [I32, I32, I32, I32, I32, P, I32, P, *R, *R, *R, F, I32, I32, P, P, *R, P]
+    lib.kda_window_attention_backward.argtypes = [P, P, I32, I32, I32, I32, *R, *R, *R, F, I32, I32, *R, P, *R, *R, *R, *R, P, SZ, P]
+    lib.kda_window_attention_workspace_bytes.argtypes = [P, I32, I32, I32, I32, I32]
+    lib.kda_window_attention_workspace_bytes.restype = SZ
     for name in ("kda_gated_scan_forward", "kda_gated_scan_backward", "kda_gated_scan_step", "kda_block_norm_forward",
                  "kda_block_norm_backward", "kda_decode_step", "kda_rotary_phases", "kda_head_norm_rotary_forward",
-                 "kda_head_norm_rotary_backward", "kda_window_attention_forward", "kda_window_cache_fill", "kda_window_attention_step"):
+                 "kda_head_norm_rotary_backward", "kda_window_attention_forward", "kda_window_attention_backward", "kda_window_cache_fill", "kda_window_attention_step"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("kda_plan_segments", "kda_plan_check", "kda_plan_segments_refined", "kda_workspace_layout", "kda_segment_forward", "kda_compose_summaries",
                  "kda_compose_summaries_blocked", "kda_apply_boundary", "kda_forward_segmented", "kda_forward_segmented_noalloc", "kda_backward_segmented",
@@ -392,6 +395,15 @@ def kda_window_attention_forward(plan, plan_dev, q, k, v, scale, window, sinks, 
     """Softmax attention over a sliding window with sinks, of every sequence of the plan (see include/kda.h): q, o [T, H, d],
     k, v [T, Hk, d] in bf16 or fp16, lse fp32 [H, T] or None."""
     (_ops or _marshal()).window_attention_forward(_words(plan), plan_dev, q, k, v, scale, window, sinks, o, lse, stream)
+
+
+def kda_window_attention_workspace_bytes(plan, H: int, Hk: int, d: int, window: int, sinks: int) -> int:
+    return int(_lib.kda_window_attention_workspace_bytes(_hp(_words(plan)), int(H), int(Hk), int(d), int(window), int(sinks)))
+
+
+def kda_window_attention_backward(plan, plan_dev, q, k, v, scale, window, sinks, o, lse, d_o, dq, dk, dv, ws, stream=None):
+    """The gradients of kda_window_attention_forward from that of o (see include/kda.h); o and lse are what it returned."""
+    (_ops or _marshal()).window_attention_backward(_words(plan), plan_dev, q, k, v, scale, window, sinks, o, lse, d_o, dq, dk, dv, ws, stream)
 
 
 def kda_window_cache_fill(plan, plan_dev, slots, k, v, window, sinks, cache_k, cache_v, stream=None):

@@ -181,7 +181,8 @@ extern "C" int kda_device_status(void)
     int worst = KDA_OK;
     for (int st : {kda::take_prep_status(), kda::take_state_status(), kda::take_compose_status(),
                    kda::take_boundary_status(), kda::take_backward_status(), kda::take_reverse_status(),
-                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status(), kda::take_window_status(), kda::take_cache_status()})
+                   kda::take_scan_status(), kda::take_scan_backward_status(), kda::take_decode_status(), kda::take_window_status(), kda::take_window_back_status(),
+                   kda::take_cache_status()})
         if (st != KDA_OK && worst == KDA_OK) worst = st;
     return worst;
 }
@@ -869,4 +870,27 @@ extern "C" int kda_window_attention_step(int32_t B, int32_t H, int32_t Hk, int32
     if (static_cast<int64_t>(B) * Hk > INT32_MAX / (8 * blocks)) return KDA_ERR_UNSUPPORTED;
     const kda::StepIn in{q, k, v, ldq, ldk, ldv, slots, lengths, B, num_slots, H, Hk, d, window, sinks, scale};
     return cuda_status(kda::launch_window_step(type, in, cache_k, cache_v, o, ldo, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t kda_window_attention_workspace_bytes(const int32_t *plan, int32_t H, int32_t Hk, int32_t d, int32_t window, int32_t sinks)
+{
+    const kda::WindowIn shape{nullptr, nullptr, nullptr, 0, 0, 0, H, Hk, d, window, sinks, 1.f};
+    if (!plan_ok(plan) || window_shape_ok(shape, KDA_TYPE_BF16) != KDA_OK) return 0;
+    return kda::window_workspace_bytes(plan[KDA_PH_T], plan[KDA_PH_N], H, Hk, d, window, sinks);
+}
+
+extern "C" int kda_window_attention_backward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
+                                             const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
+                                             int32_t window, int32_t sinks, const void *o, int64_t ldo, const float *lse, const void *d_o,
+                                             int64_t lddo, void *dq, int64_t lddq, void *dk, int64_t lddk, void *dv, int64_t lddv, void *ws,
+                                             size_t ws_bytes, void *stream)
+{
+    const kda::WindowIn in{q, k, v, ldq, ldk, ldv, H, Hk, d, window, sinks, scale};
+    const kda::WindowGrads g{o, d_o, ldo, lddo, lse, dq, dk, dv, lddq, lddk, lddv};
+    if (const int rc = window_in_ok(plan, plan_dev, in, type)) return rc;
+    const int64_t w = static_cast<int64_t>(H) * d, wk = static_cast<int64_t>(Hk) * d;
+    if (!rows16_ok(o, ldo, w) || !rows16_ok(d_o, lddo, w) || !lse || !floats_ok_or_null(lse)) return KDA_ERR_INVALID_ARG;
+    if (!rows16_ok(dq, lddq, w) || !rows16_ok(dk, lddk, wk) || !rows16_ok(dv, lddv, wk) || !ws || !aligned16(ws)) return KDA_ERR_INVALID_ARG;
+    if (ws_bytes < kda::window_workspace_bytes(plan[KDA_PH_T], plan[KDA_PH_N], H, Hk, d, window, sinks)) return KDA_ERR_WORKSPACE;
+    return cuda_status(kda::launch_window_backward(plan, plan_dev, type, in, g, ws, static_cast<cudaStream_t>(stream)));
 }

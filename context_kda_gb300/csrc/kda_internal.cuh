@@ -293,6 +293,17 @@ struct WindowIn {
 };
 cudaError_t launch_window_forward(const int32_t *plan_host, const int32_t *plan_dev, int type, const WindowIn &in, void *o, int64_t ldo,
                                   float *lse, cudaStream_t stream);
+struct WindowGrads {
+    const void *o, *d_o;              // [T][H][d]
+    int64_t ldo, lddo;
+    const float *lse;                 // [H][T]
+    void *dq, *dk, *dv;               // as q, k, v
+    int64_t lddq, lddk, lddv;
+};
+size_t window_workspace_bytes(int T, int N, int H, int Hk, int d, int W, int S);
+cudaError_t launch_window_backward(const int32_t *plan_host, const int32_t *plan_dev, int type, const WindowIn &in, const WindowGrads &g, void *ws,
+                                   cudaStream_t stream);
+int take_window_back_status();
 constexpr int WINDOW_MAX_T = INT32_MAX - 512;    // a tile's rows behind the last token are 32-bit numbers too
 int take_window_status();
 

@@ -442,6 +442,25 @@ PyObject *window_attention_forward(PyObject *, PyObject *const *args, Py_ssize_t
     });
 }
 
+PyObject *window_attention_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call("kda_window_attention_backward", [&] {
+        Args a(args, n, 16);
+        const Plan plan(a);
+        const int64_t T = plan.words[KDA_PH_T];
+        const WindowArgs p(a, T);
+        const int64_t w = p.q.H * p.q.d, wk = p.k.H * p.q.d;
+        const Rows o = rows_of(a.tensor(false), T, w, p.ty);
+        const float *lse = floats(a.tensor(false), p.q.H * T);
+        const Rows d_o = rows_of(a.tensor(false), T, w, p.ty), dq = rows_of(a.tensor(false), T, w, p.ty);
+        const Rows dk = rows_of(a.tensor(false), T, wk, p.ty), dv = rows_of(a.tensor(false), T, wk, p.ty);
+        const Bytes ws = workspace(a.tensor(false));
+        return kda_window_attention_backward(plan.words, plan.dev, i32(p.q.H), i32(p.k.H), i32(p.q.d), type_code(p.ty), p.rq.p, p.rq.ld, p.rk.p,
+                                             p.rk.ld, p.rv.p, p.rv.ld, p.scale, p.window, p.sinks, o.p, o.ld, lse, d_o.p, d_o.ld, dq.p, dq.ld,
+                                             dk.p, dk.ld, dv.p, dv.ld, ws.p, ws.n, a.stream());
+    });
+}
+
 // A ring cache [slots][Hk][sinks + window][d]; its number of slots.
 void *ring(const at::Tensor *t, int64_t Hk, int64_t rows, int64_t d, at::ScalarType ty, int64_t *slots)
 {
@@ -501,7 +520,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 PyMethodDef g_methods[] = {FAST(gated_scan_forward), FAST(gated_scan_backward), FAST(gated_scan_step),
                            FAST(block_norm_forward), FAST(block_norm_backward), FAST(decode_step),
                            FAST(head_norm_rotary_forward), FAST(head_norm_rotary_backward),
-                           FAST(window_attention_forward), FAST(window_cache_fill), FAST(window_attention_step),
+                           FAST(window_attention_forward), FAST(window_attention_backward), FAST(window_cache_fill), FAST(window_attention_step),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", "Argument marshalling of the operators around the KDA layer.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -65,7 +65,7 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo)
 // The sequence and tile of slot 'slot'.  Sequence n has its tiles of 'rows' tokens from slot cu[n] / rows + n on, which
 // leaves room for all of them without a prefix sum; a slot behind a sequence's last tile is empty (false).  Whole warps call it.
 struct Place {
-    int start, len, t0;                   // first token and length of the sequence, first row of the tile in it
+    int seq, start, len, t0;              // the sequence, its first token and length, first row of the tile in it
 };
 __device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Place &at)
 {
@@ -80,6 +80,7 @@ __device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Pl
         count = min(stride, count - last * stride);
         if (stride == 1) break;
     }
+    at.seq = lo;
     at.start = cu[lo];
     at.len = cu[lo + 1] - at.start;
     at.t0 = (slot - (at.start / rows + lo)) * rows;

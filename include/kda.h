@@ -703,6 +703,25 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
                                  int32_t window, int32_t sinks, void *o, int64_t ldo, float *lse, void *stream);
 
 /*
+ * kda_window_attention_backward -- the gradients of kda_window_attention_forward for L = sum <do, o>.
+ *   q ... sinks     the forward's inputs.   o, lse  what it returned.   d_o  [T][H][d], rows on 16 bytes.
+ *   dq, dk, dv  out as q, k, v, rows on 16 bytes.  dk and dv are the sums over the heads of each group.
+ *   ws, ws_bytes    device workspace of at least kda_window_attention_workspace_bytes bytes, 16-byte aligned.
+ * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products (fp16: kept times powers of two, so that
+ * they neither overflow nor fade).  No sequence sees another's values, whatever they are; an infinity or NaN of a sequence may reach all
+ * of that sequence's gradients.  The same call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
+ */
+int kda_window_attention_backward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
+                                  const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
+                                  int32_t window, int32_t sinks, const void *o, int64_t ldo, const float *lse, const void *d_o,
+                                  int64_t lddo, void *dq, int64_t lddq, void *dk, int64_t lddk, void *dv, int64_t lddv, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* Device workspace bytes of kda_window_attention_backward (0: the plan or a size is invalid): 4 H T bytes and, where sinks leave
+ * windows, (T / 1024 + 2 N) 8 sinks Hk d. */
+size_t kda_window_attention_workspace_bytes(const int32_t *plan, int32_t H, int32_t Hk, int32_t d, int32_t window, int32_t sinks);
+
+/*
  * The ring cache of the window attention: for every slot and key head the last 'window' keys (and values) and the first 'sinks',
  *     cache_k, cache_v   [num_slots][Hk][sinks + window][d] of 'type', contiguous, 16-byte aligned;
  * position p is in row p if p < sinks, else in row sinks + (p - sinks) mod window.  sinks + window < 2^31.

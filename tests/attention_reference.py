@@ -62,7 +62,8 @@ def window_forward(cu, q, k, v, scale, window, sinks):
 
 
 def window_backward(cu, q, k, v, scale, window, sinks, do):
-    """dq, dk, dv, and for each the sum of the magnitudes that the rounding of p and ds goes by."""
+    """dq, dk, dv, and for each the sum of the magnitudes that the rounding of p, of ds and of the output in D = do . o goes by
+    (o is off by u of sum p |v| and of itself, so D by u of 'loose')."""
     H = q.shape[1]
     g = H // k.shape[1]
     out = [np.zeros(x.shape) for x in (q, k, v)]
@@ -77,7 +78,8 @@ def window_backward(cu, q, k, v, scale, window, sinks, do):
             dp = D @ V.T
             delta = (p * dp).sum(-1, keepdims=True)
             ds = scale * p * (dp - delta)
-            mag = scale * p * (np.abs(dp) + np.abs(delta))     # what the difference is formed from
+            loose = (np.abs(D) * (p @ np.abs(V) + np.abs(p @ V))).sum(-1, keepdims=True)
+            mag = scale * p * (np.abs(dp - delta) + loose)
             for n, (x, m) in enumerate(((ds @ K, mag @ np.abs(K)), (ds.T @ Q, mag.T @ np.abs(Q)), (p.T @ D, p.T @ np.abs(D)))):
                 at = (slice(a, b), h) if n == 0 else (slice(a, b), h // g)
                 out[n][at] += x

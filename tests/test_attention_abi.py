@@ -117,3 +117,20 @@ def test_window_fill_refusals(kda):  # noqa: F811
             dict(window=2 ** 31 - 1, sinks=1)]
     _refusals(kda._lib.kda_window_cache_fill, names, good, bad, kda.KDA_ERR_INVALID_ARG)
     _refusals(kda._lib.kda_window_cache_fill, names, good, [dict(type=F32), dict(d=32), dict(sinks=129)], kda.KDA_ERR_UNSUPPORTED)
+
+
+def test_window_backward_refusals(kda):  # noqa: F811
+    plan, good = _window_good(kda)
+    names = WINDOW + "o ldo lse do lddo dq lddq dk lddk dv lddv ws ws_bytes stream".split()
+    need = kda.kda_window_attention_workspace_bytes(plan, 8, 2, 64, 100, 4)
+    good.update(o=F, ldo=512, lse=F, do=F, lddo=512, dq=F, lddq=512, dk=F, lddk=128, dv=F, lddv=128, ws=F, ws_bytes=need)
+    bad = WINDOW_BAD + [dict(lse=None), dict(lse=F + 1), dict(ws=None), dict(ws=F + 8)]
+    for n, ld in (("o", "ldo"), ("do", "lddo"), ("dq", "lddq"), ("dk", "lddk"), ("dv", "lddv")):
+        bad += [{n: None}, {n: F + 8}, {ld: good[ld] - 8}, {ld: good[ld] + 4}]
+    fn = kda._lib.kda_window_attention_backward
+    _refusals(fn, names, good, bad, kda.KDA_ERR_INVALID_ARG)
+    _refusals(fn, names, good, WINDOW_UNSUPPORTED, kda.KDA_ERR_UNSUPPORTED)
+    _refusals(fn, names, good, [dict(ws_bytes=need - 1)], kda.KDA_ERR_WORKSPACE)
+    size = lambda *a: kda.kda_window_attention_workspace_bytes(plan, *a)
+    assert size(8, 3, 64, 100, 4) == size(8, 2, 32, 100, 4) == size(8, 2, 64, 0, 4) == size(8, 2, 64, 100, 129) == 0
+    assert size(8, 2, 64, 333, 4) < need      # no sink leaves a window of that length
