@@ -24,6 +24,7 @@ using namespace attn;
 __device__ int g_window_status;
 
 constexpr int THREADS = 384;
+constexpr int REGS_OTHER = 72, REGS_SOFTMAX = 216;     // of 168 at the launch: 128 x 72 + 256 x 216 = 384 x 168
 constexpr float LAZY = 8.f;               // growth of a row's maximum, in powers of two, that O is not corrected for
 
 template <int D> struct Smem {
@@ -37,27 +38,29 @@ template <int D> struct Smem {
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
 // What the roles know of a CTA's work: its row tiles x = 0, 1 and the key tiles, from the diagonal down, the sinks' last.
-struct Plan {
-    int rows[2], t0[2], head[2];          // rows that exist, first row in the sequence
-    int lo[2], hi[2];                     // key tiles of the window; none: lo > hi
-    bool sink[2];
+struct Rows {
+    int count, t0, head;                  // rows that exist, first row in the sequence
+    int lo, hi;                           // key tiles of the window; none: lo > hi
+    bool sink;
+};
+struct Tiles {
     int top, n_win, n;                    // highest key tile, tiles of the windows, all tiles
 
-    __device__ bool is_sink(int i) const { return i >= n_win; }
-    __device__ int tile(int i) const { return i < n_win ? top - i : 0; }
-    __device__ bool active(int x, int i) const { return is_sink(i) ? sink[x] : tile(i) >= lo[x] && tile(i) <= hi[x]; }
-    // Keys [a, b] of tile i that row r of row tile x sees.
-    __device__ void visible(int x, int i, int r, int W, int S, int &a, int &b) const
+    __device__ __forceinline__ bool is_sink(int i) const { return i >= n_win; }
+    __device__ __forceinline__ int tile(int i) const { return i < n_win ? top - i : 0; }
+    __device__ __forceinline__ bool active(const Rows &x, int i) const { return is_sink(i) ? x.sink : tile(i) >= x.lo && tile(i) <= x.hi; }
+    // Keys [a, b] of tile i that row r of x sees.
+    __device__ __forceinline__ void visible(const Rows &x, int i, int r, int W, int S, int &a, int &b) const
     {
-        const int row = t0[x] + r, j0 = tile(i) * TILE;
+        const int row = x.t0 + r, j0 = tile(i) * TILE;
         a = is_sink(i) ? 0 : max(0, row - W + 1 - j0);           // (row - W is above -2^31)
         b = is_sink(i) ? min(S - 1, row - W) : min(TILE - 1, row - j0);
     }
     // Whether some row of x sees only a part of tile i, or the tile passes the sequence's end.
-    __device__ bool masked(int x, int i, int len, int W) const
+    __device__ __forceinline__ bool masked(const Rows &x, int i, int len, int W) const
     {
         const int j0 = tile(i) * TILE;
-        return is_sink(i) || j0 + TILE - 1 > t0[x] || j0 < t0[x] + TILE - W || j0 + TILE > len;
+        return is_sink(i) || j0 + TILE - 1 > x.t0 || j0 < x.t0 + TILE - W || j0 + TILE > len;
     }
 };
 
@@ -81,21 +84,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int span = two_heads ? TILE : 2 * TILE;
     const int works = two_heads ? p.H / 2 : p.H, slot = (gridDim.x - 1 - blockIdx.x) / works, work = (gridDim.x - 1 - blockIdx.x) % works;
     if (!find_tile(p, slot, span, at)) return;      // the last rows of a sequence, which see the most, come first
-    Plan w;
-    const int g = p.H / p.Hk;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        w.head[x] = two_heads ? 2 * work + x : work;
-        w.t0[x] = at.t0 + (two_heads ? 0 : x * TILE);
-        w.rows[x] = min(TILE, at.len - w.t0[x]);
-        w.hi[x] = w.rows[x] > 0 ? w.t0[x] / TILE : -1;
-        w.lo[x] = max(0, w.t0[x] - p.W + 1) / TILE;
-        w.sink[x] = w.rows[x] > 0 && p.S > 0 && w.t0[x] + w.rows[x] - 1 >= p.W;
-    }
-    w.top = max(w.hi[0], w.hi[1]);
-    w.n_win = w.top - w.lo[0] + 1;
-    w.n = w.n_win + (w.sink[0] || w.sink[1]);
-    const int hk = w.head[0] / g;
+    auto make_rows = [&](int x) {
+        Rows y;
+        y.head = two_heads ? 2 * work + x : work;
+        y.t0 = at.t0 + (two_heads ? 0 : x * TILE);
+        y.count = min(TILE, at.len - y.t0);
+        y.hi = y.count > 0 ? y.t0 / TILE : -1;
+        y.lo = max(0, y.t0 - p.W + 1) / TILE;
+        y.sink = y.count > 0 && p.S > 0 && y.t0 + y.count - 1 >= p.W;
+        return y;
+    };
+    const Rows x0 = make_rows(0), x1 = make_rows(1);
+    Tiles w;
+    w.top = max(x0.hi, x1.hi);
+    w.n_win = w.top - x0.lo + 1;
+    w.n = w.n_win + (x0.sink || x1.sink);
+    const int hk = x0.head / (p.H / p.Hk);
+    auto look_after = [&](int i) {        // tile i's values
+        return (w.active(x0, i) && w.masked(x0, i, at.len, p.W)) || (w.active(x1, i) && w.masked(x1, i, at.len, p.W));
+    };
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const basep = smem_raw + (base - smem_u32(smem_raw));
@@ -120,6 +127,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
 
     int fetched[2] = {0, 0};              // (the fetching thread) tiles of keys and of values
+    if (warp < 4) fewer_registers<REGS_OTHER>();
     if (warp == 0) {
         // ---- fetch
         if (lane == 0) {
@@ -127,9 +135,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, head, at.start + row, bar);
             };
             const uint32_t bq = smem_u32(&s_q);
-            mbar_arrive_expect_tx(bq, (w.rows[1] > 0 ? 2 : 1) * L::T_BYTES);
-            load(mq, base + L::Q, w.head[0], w.t0[0], bq);
-            if (w.rows[1] > 0) load(mq, base + L::Q + L::T_BYTES, w.head[1], w.t0[1], bq);
+            mbar_arrive_expect_tx(bq, (x1.count > 0 ? 2 : 1) * L::T_BYTES);
+            load(mq, base + L::Q, x0.head, x0.t0, bq);
+            if (x1.count > 0) load(mq, base + L::Q + L::T_BYTES, x1.head, x1.t0, bq);
             bool ok = true;
             int &ks = fetched[0], &vs = fetched[1];
             for (int i = 0; i <= w.n && ok; ++i) {       // keys a tile ahead of the values
@@ -169,8 +177,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             int done[2] = {0, 0};
             if (ok) {
                 fence_after();
-                for (int x = 0; x < 2; ++x)
-                    if (w.active(x, 0)) scores(x, 0);
+                if (w.active(x0, 0)) scores(0, 0);
+                if (w.active(x1, 0)) scores(1, 0);
                 commit(smem_u32(&s_kfree[0]));
             }
             for (int i = 0; i < w.n && ok; ++i) {
@@ -178,10 +186,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool more = i + 1 < w.n;
                 ok = mbar_wait(smem_u32(&s_vfix[i % L::VS]), (i / L::VS) & 1);
                 if (ok && more) ok = mbar_wait(smem_u32(&s_kfull[(i + 1) % L::KS]), ((i + 1) / L::KS) & 1);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (w.active(x, i)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const Rows &rows = x ? x1 : x0;
+                    if (!ok) continue;
+                    if (w.active(rows, i)) {
                         ok = mbar_wait(smem_u32(&s_p[x]), done[x] & 1);
-                        if (!ok) break;
+                        if (!ok) continue;
                         fence_after();
                         // of the sinks' tile only the rows that hold sinks
                         const int steps = w.is_sink(i) ? (p.S + 15) / 16 : TILE / 16;
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                         done[x] > 0 || s > 0);
                         ++done[x];
                     }
-                    if (more && w.active(x, i + 1)) scores(x, i + 1);
+                    if (more && w.active(rows, i + 1)) scores(x, i + 1);
                 }
                 commit(smem_u32(&s_vfree[i % L::VS]));
                 if (more) commit(smem_u32(&s_kfree[(i + 1) % L::KS]));
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < w.n && ok; ++i) {
             ok = mbar_wait_warp(smem_u32(&s_vfull[i % L::VS]), (i / L::VS) & 1);
             if (!ok) break;
-            if (!((w.active(0, i) && w.masked(0, i, at.len, p.W)) || (w.active(1, i) && w.masked(1, i, at.len, p.W)))) {
+            if (!look_after(i)) {
                 if (lane == 0) mbar_arrive(smem_u32(&s_vfix[i % L::VS]));
                 continue;
             }
@@ -248,14 +259,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok && lane == 0) give_up();
     } else {
         // ---- softmax, a thread a row
+        more_registers<REGS_SOFTMAX>();
         const int x = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
+        const Rows rows = make_rows(x);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + TM_S + x * 128, to = tmem + lanes + TM_O + x * D;
         float m = -INFINITY, sum = 0.f;      // the row's maximum (of the scores) and sum of probabilities
         int n = 0;
         bool ok = true;
         for (int i = 0; i < w.n; ++i) {
-            if (!w.active(x, i)) continue;
+            if (!w.active(rows, i)) continue;
             ok = mbar_wait_warp(smem_u32(&s_s[x]), n & 1);
             if (!ok) break;
             fence_after();
@@ -265,9 +278,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) reg_fence32(u[c]);
-            if (w.masked(x, i, at.len, p.W)) {
+            if (w.masked(rows, i, at.len, p.W)) {
                 int a, b;
-                w.visible(x, i, r, p.W, p.S, a, b);
+                w.visible(rows, i, r, p.W, p.S, a, b);
                 const unsigned len = b >= a ? b - a + 1 : 0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -325,9 +338,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok && lane == 0) give_up();
         if (ok && n > 0) {
             fence_after();
-            const int64_t token = at.start + w.t0[x] + r;
-            const bool real = r < w.rows[x];
-            if (lse && real) lse[static_cast<int64_t>(w.head[x]) * p.T + token] = (fmaf(m, p.c, log2f(sum))) * 0.69314718055994530942f;
+            const int64_t token = at.start + rows.t0 + r;
+            const bool real = r < rows.count;
+            if (lse && real) lse[static_cast<int64_t>(rows.head) * p.T + token] = (fmaf(m, p.c, log2f(sum))) * 0.69314718055994530942f;
             const float inv = 1.f / sum;
             const int bad = *static_cast<volatile int *>(&s_bad);
             unsigned char *const out = basep + L::Q + x * L::T_BYTES;      // the queries are no longer needed: rows of D, chunks swizzled
@@ -343,9 +356,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (bad && real) {
                     // values that are infinite or NaN: what the row sees of them
                     for (int i = 0; i < w.n; ++i) {
-                        if (!w.active(x, i)) continue;
+                        if (!w.active(rows, i)) continue;
                         int a, b;
-                        w.visible(x, i, r, p.W, p.S, a, b);
+                        w.visible(rows, i, r, p.W, p.S, a, b);
                         for (int j = a; j <= b; ++j) {
                             const E *const v = v_rows + (at.start + w.tile(i) * TILE + j) * ldv + hk * D + c * 32;
 #pragma unroll
@@ -370,11 +383,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte pieces of a row, rows of one store of the warp
             const int r0 = (warp & 3) * 32, ch = lane % CH;
-            E *const dst = o + (static_cast<int64_t>(at.start) + w.t0[x]) * ldo + w.head[x] * D + ch * 8;
+            E *const dst = o + (static_cast<int64_t>(at.start) + rows.t0) * ldo + rows.head * D + ch * 8;
 #pragma unroll 4
             for (int k = 0; k < 32; k += RPI) {
                 const int row = r0 + k + lane / CH;
-                if (row < w.rows[x])
+                if (row < rows.count)
                     *reinterpret_cast<uint4 *>(dst + row * ldo) = *reinterpret_cast<const uint4 *>(out + row * (2 * D) + ((ch ^ (row & 7)) << 4));
             }
         }

@@ -26,6 +26,10 @@ struct Shape {
     float scale;
 };
 
+// Registers of a warpgroup's threads, after the launch gave every thread the same.
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 inline Shape window_shape(const int32_t *plan_host, const int32_t *plan_dev, const WindowIn &in)
 {
     return Shape{plan_dev, plan_sig(plan_host), plan_host[KDA_PH_N], plan_host[KDA_PH_OFF_CU], plan_host[KDA_PH_T], in.H, in.Hk, in.W, in.S,

@@ -5,11 +5,12 @@
 // min(p + 1, S + W), its own among them, in whatever order; attention does not ask for it.
 //
 // The step is bound by memory: every visible row is read once, for all heads of its group.  A cluster of CTAs shares
-// the rows of one (token, key head); a warp takes 16 rows at a time from memory to registers, 16 bytes a lane, with no
-// stop in shared memory: the products (mma, whose rate does not matter here) may take channels and rows in any
-// order, so a lane's 16 bytes of keys are its part of two K steps, and its 16 bytes each of four rows of values, interleaved, are its part of eight
-// N tiles.  Scores leave the first product where the second one wants its A operand.  Each warp keeps its own running maximum, sum and
-// outputs; they are joined in shared memory and then over the cluster, in a fixed order.
+// the rows of one (token, key head); a warp takes 16 rows at a time, 16 bytes a lane.  The products (mma, whose rate does
+// not matter here) may take channels and rows in any order, so a lane's 16 bytes of keys are its part of two K steps, and its 16
+// bytes each of four rows of values, interleaved, are its part of eight N tiles: no lane needs another's bytes.  So shared memory is
+// only a queue of copies (cp.async) for each lane, STAGES deep, without a barrier.  Scores leave the first product where the
+// second one wants its A operand.  Each warp keeps its own running maximum, sum and outputs; they are joined in shared memory
+// and then over the cluster, in a fixed order.
 // The new token's row comes from the arguments, and the CTA that would have read it from the cache writes it there.
 #include "elem.cuh"
 #include "kda_internal.cuh"
@@ -23,6 +24,17 @@ __device__ int g_cache_status;
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int ROWS = 16;                  // of a warp's step
 constexpr int MAX_SPLIT = 8;              // CTAs of a cluster
+constexpr int STAGES = 3;                 // of a lane's queue, 16 rows each: two CTAs an SM have 128 KiB on their way
+
+template <int D> constexpr int PIECES = D / 8;                                   // 16-byte pieces of a lane in 16 rows of keys and values
+template <int D> constexpr uint32_t QUEUE = STAGES * PIECES<D> * 512;            // of a warp
+template <int D, int HG> constexpr uint32_t SMEM = WARPS * (QUEUE<D> > HG * D * 4 ? QUEUE<D> : HG * D * 4);
+
+// 16 bytes, or zeros where 'real' is false, into this lane's place.
+__device__ __forceinline__ void fetch16(uint32_t dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
 
 template <typename E>
 __device__ __forceinline__ void mma(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -79,10 +91,12 @@ struct Step {
 
 // HG: query heads worked together, 8 or 16 (the product's M).
 template <typename E, int D, int HG>
-__global__ void __launch_bounds__(THREADS) window_step(const Step p, E *cache_k, E *cache_v, E *o)
+__global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache_k, E *cache_v, E *o)
 {
     constexpr int KC = D / 32, VC = D / 64;       // 16-byte pieces of a lane: of a row of keys, of a row of values
-    __shared__ float s_o[WARPS][HG][D], s_m[WARPS][HG], s_l[WARPS][HG], s_mc[HG], s_lc[HG];
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto s_o = reinterpret_cast<float (*)[HG][D]>(smem);      // [WARPS], once the queues are empty
+    __shared__ float s_m[WARPS][HG], s_l[WARPS][HG], s_mc[HG], s_lc[HG];
     const StepIn &in = p.in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = lane >> 2, c4 = lane & 3;
     const int part = blockIdx.x % p.split;
@@ -125,39 +139,50 @@ __global__ void __launch_bounds__(THREADS) window_step(const Step p, E *cache_k,
         if constexpr (HG == 16) acc2[i][0] = acc2[i][1] = 0.f;
     }
 
-    uint4 kr[2][KC];
-    auto load_k = [&](int r0) {           // rows r0 + hd and r0 + 8 + hd
+    const uint32_t queue = tc::smem_u32(smem) + warp * QUEUE<D> + lane * 16;
+    const unsigned char *const mine = smem + warp * QUEUE<D> + lane * 16;
+    auto fetch = [&](int r0, int stage) {       // keys of rows r0 + hd, + 8; values of rows r0 + 2 c4, + 1, + 8, + 9
+        const uint32_t to = queue + stage * PIECES<D> * 512;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int r = r0 + t * 8 + hd;
-            const E *const src = (r == fresh ? k_new : cache_k + (first + r) * D) + c4 * 8;
+            const bool real = r < hi;
+            const E *const src = (r == fresh ? k_new : cache_k + (first + (real ? r : lo)) * D) + c4 * 8;
 #pragma unroll
-            for (int i = 0; i < KC; ++i) kr[t][i] = r < hi ? *reinterpret_cast<const uint4 *>(src + i * 32) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < KC; ++i) fetch16(to + (t * KC + i) * 512, src + i * 32, real);
         }
-    };
-    int r0 = lo + warp * ROWS;
-    if (r0 < hi) load_k(r0);
-    for (; r0 < hi; r0 += WARPS * ROWS) {
-        uint4 vr[4][VC];                  // rows r0 + 2 c4, + 1, + 8, + 9
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int r = r0 + (t >> 1) * 8 + c4 * 2 + (t & 1);
-            const E *const src = (r == fresh ? v_new : cache_v + (first + r) * D) + hd * 8;
+            const bool real = r < hi;
+            const E *const src = (r == fresh ? v_new : cache_v + (first + (real ? r : lo)) * D) + hd * 8;
 #pragma unroll
-            for (int i = 0; i < VC; ++i) vr[t][i] = r < hi ? *reinterpret_cast<const uint4 *>(src + i * 64) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < VC; ++i) fetch16(to + (2 * KC + t * VC + i) * 512, src + i * 64, real);
         }
+    };
+    int ahead = lo + warp * ROWS, r0 = ahead;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s, ahead += WARPS * ROWS) {
+        if (ahead < hi) fetch(ahead, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int stage = 0; r0 < hi; r0 += WARPS * ROWS, ahead += WARPS * ROWS, stage = stage == STAGES - 1 ? 0 : stage + 1) {
+        if (ahead < hi) fetch(ahead, stage == 0 ? STAGES - 1 : stage - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        const uint4 *const x = reinterpret_cast<const uint4 *>(mine + stage * PIECES<D> * 512);
         float s[2][4] = {};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
-                const uint32_t b0[4] = {kr[t][i].x, kr[t][i].y, kr[t][i].z, kr[t][i].w};
+                const uint4 y = x[(t * KC + i) * 32];
+                const uint32_t b0[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     mma<E>(s[t][0], s[t][1], s[t][2], s[t][3], qa[i][2 * h], HG == 16 ? qb[HG == 16 ? i : 0][2 * h] : 0u, qa[i][2 * h + 1],
                            HG == 16 ? qb[HG == 16 ? i : 0][2 * h + 1] : 0u, b0[2 * h], b0[2 * h + 1]);
             }
-        if (r0 + WARPS * ROWS < hi) load_k(r0 + WARPS * ROWS);
         // s[t][0, 1]: head hd, rows r0 + 8 t + 2 c4, + 1;  s[t][2, 3]: head hd + 8
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -189,22 +214,28 @@ __global__ void __launch_bounds__(THREADS) window_step(const Step p, E *cache_k,
         const uint32_t a0 = pack2(s[0][0], s[0][1], E()), a2 = pack2(s[1][0], s[1][1], E());
         const uint32_t a1 = HG == 16 ? pack2(s[0][2], s[0][3], E()) : 0u, a3 = HG == 16 ? pack2(s[1][2], s[1][3], E()) : 0u;
 #pragma unroll
-        for (int i = 0; i < VC; ++i)
+        for (int i = 0; i < VC; ++i) {
+            uint4 vr[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) vr[t] = x[(2 * KC + t * VC + i) * 32];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t x[4];
+                uint32_t y[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) x[t] = w == 0 ? vr[t][i].x : w == 1 ? vr[t][i].y : w == 2 ? vr[t][i].z : vr[t][i].w;
+                for (int t = 0; t < 4; ++t) y[t] = w == 0 ? vr[t].x : w == 1 ? vr[t].y : w == 2 ? vr[t].z : vr[t].w;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {     // channel 2 w + h of the lane's 8
-                    const uint32_t b0 = __byte_perm(x[0], x[1], h ? 0x7632 : 0x5410), b1 = __byte_perm(x[2], x[3], h ? 0x7632 : 0x5410);
+                    const uint32_t b0 = __byte_perm(y[0], y[1], h ? 0x7632 : 0x5410), b1 = __byte_perm(y[2], y[3], h ? 0x7632 : 0x5410);
                     const int j = i * 8 + 2 * w + h;
                     float d2 = 0.f, d3 = 0.f;
                     if constexpr (HG == 16) mma<E>(acc[j][0], acc[j][1], acc2[j][0], acc2[j][1], a0, a1, a2, a3, b0, b1);
                     else mma<E>(acc[j][0], acc[j][1], d2, d3, a0, 0u, a2, 0u, b0, b1);
                 }
             }
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
     // ---- the new row into the cache, by the CTA whose rows it is among
     if (block == 0 && fresh >= lo && fresh < hi && tid < 2 * D / 8) {
         const int ch = tid % (D / 8) * 8;
@@ -271,9 +302,12 @@ cudaError_t step(Step p, void *cache_k, void *cache_v, void *o, cudaStream_t str
     // enough CTAs for every SM, but none with fewer than 64 rows of a full cache (its way in and out would take longer)
     p.split = 1;
     while (p.split < MAX_SPLIT && units * p.split < 4 * sm_count() && (in.W + in.S) / (2 * p.split) >= 64) p.split *= 2;
+    const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(&window_step<E, D, HG>), SMEM<D, HG>);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM<D, HG>;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
