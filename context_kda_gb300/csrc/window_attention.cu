@@ -2,12 +2,15 @@
 // keys with the running maximum and sum of every row.
 //
 // A CTA works two tiles of 128 query rows against the same tiles of keys: two heads that share a key head, or else two
-// neighbouring tiles of one head.  Warp 0 fetches (TMA), warp 1 issues the products (tcgen05), warps 2 and 3 look
-// after the values (below), and four warps a row tile do its softmax, a thread a row.  Scores S = Q K^T lie in TMEM; a row's
-// probabilities take the scores' place there as the A operand of O += P V.  While one row tile's probabilities are
-// computed, the tensor cores work for the other.
+// neighbouring tiles of one head.  Warp 0 fetches (TMA), warp 1 issues the products (tcgen05), warp 2 looks after the
+// values (below), and four warps a row tile do its softmax, a thread a row.  Scores S = Q K^T lie in
+// TMEM; a row's probabilities take the scores' place there as the A operand of O += P V, and the first half of them is
+// multiplied while the second half is computed.  While one row tile's probabilities are computed, the tensor cores work for the other.  They take the next product hardly before
+// the last is done, so whatever the issuing warp waits for stands still: it waits for probabilities only, and warp 2 adds
+// its arrival to theirs once the tile's values and the next keys are there.  One warp issues for both row tiles in turn; two
+// warps that issue as they can drift into step, and both row tiles' softmax then meets idle tensor cores (329 us for 261).
 // A row's maximum is followed lazily: O is multiplied up only when the maximum has grown by more than 2^8 since, which
-// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so there always is a maximum.
+// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so that there always is a maximum.
 // Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
 // the values before rounding.
 //
@@ -31,7 +34,7 @@ template <int D> struct Smem {
     static constexpr uint32_t T_BYTES = D / 64 * BOX;
     static constexpr int KS = D == 128 ? 3 : 4, VS = D == 128 ? 2 : 4;
     static constexpr uint32_t Q = 0, K = 2 * T_BYTES, V = K + KS * T_BYTES, BYTES = V + VS * T_BYTES, ALLOC = BYTES + 1024;
-    static_assert(ALLOC <= 227 * 1024, "shared memory");
+    static_assert(ALLOC + 2048 <= 227 * 1024, "shared memory");      // with the static part
 };
 
 // TMEM columns: scores (probabilities in their first half), outputs
@@ -71,11 +74,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     using L = Smem<D>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_vfix[L::VS], s_s[2], s_p[2], s_o[2], s_end;
+    __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_s[2], s_p[2][2], s_o[2], s_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    if (tid == 0) prefetch_map(mq), prefetch_map(mk), prefetch_map(mv);
     if (!plan_matches(p.plan, p.sig)) {
         if (tid == 0 && blockIdx.x == 0) record_status(&g_window_status, KDA_ERR_INVALID_ARG);
         return;
@@ -106,14 +110,35 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const basep = smem_raw + (base - smem_u32(smem_raw));
+    int fetched[2] = {0, 0};              // (the fetching thread) tiles of keys and of values
+    auto load = [&](const CUtensorMap &m, uint32_t dst, int head, int row, uint32_t bar) {
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, head, at.start + row, bar);
+    };
+    auto fetch = [&](const CUtensorMap &m, uint32_t to, int i, uint64_t &full) {      // tile i of keys or values
+        mbar_arrive_expect_tx(smem_u32(&full), L::T_BYTES);
+        load(m, base + to, hk, w.tile(i) * TILE, smem_u32(&full));
+    };
     if (tid == 0) {
         mbar_init(smem_u32(&s_q), 1);
         for (int i = 0; i < L::KS; ++i) mbar_init(smem_u32(&s_kfull[i]), 1), mbar_init(smem_u32(&s_kfree[i]), 1);
-        for (int i = 0; i < L::VS; ++i) mbar_init(smem_u32(&s_vfull[i]), 1), mbar_init(smem_u32(&s_vfree[i]), 1), mbar_init(smem_u32(&s_vfix[i]), 2);
-        for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&s_s[x]), 1), mbar_init(smem_u32(&s_p[x]), 4), mbar_init(smem_u32(&s_o[x]), 1);
+        for (int i = 0; i < L::VS; ++i) mbar_init(smem_u32(&s_vfull[i]), 1), mbar_init(smem_u32(&s_vfree[i]), 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&s_s[x]), 1);
+            mbar_init(smem_u32(&s_p[x][0]), 5);
+            mbar_init(smem_u32(&s_p[x][1]), 4);
+            mbar_init(smem_u32(&s_o[x]), 1);
+        }
         mbar_init(smem_u32(&s_end), 1);
         s_abort = 0;
         s_bad = 0;
+        // the first tiles are on their way before anything else
+        const uint32_t bq = smem_u32(&s_q);
+        mbar_arrive_expect_tx(bq, (x1.count > 0 ? 2 : 1) * L::T_BYTES);
+        load(mq, base + L::Q, x0.head, x0.t0, bq);
+        fetch(mk, L::K, 0, s_kfull[0]);
+        if (x1.count > 0) load(mq, base + L::Q + L::T_BYTES, x1.head, x1.t0, bq);
+        fetch(mv, L::V, 0, s_vfull[0]);
+        fetched[0] = fetched[1] = 1;
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), TM_COLS);
     fence_before();
@@ -126,116 +151,143 @@ __global__ void __launch_bounds__(THREADS, 1)
         *abort_flag = 1;
     };
 
-    int fetched[2] = {0, 0};              // (the fetching thread) tiles of keys and of values
     if (warp < 4) fewer_registers<REGS_OTHER>();
     if (warp == 0) {
         // ---- fetch
         if (lane == 0) {
-            auto load = [&](const CUtensorMap &m, uint32_t dst, int head, int row, uint32_t bar) {
-                for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, head, at.start + row, bar);
-            };
-            const uint32_t bq = smem_u32(&s_q);
-            mbar_arrive_expect_tx(bq, (x1.count > 0 ? 2 : 1) * L::T_BYTES);
-            load(mq, base + L::Q, x0.head, x0.t0, bq);
-            if (x1.count > 0) load(mq, base + L::Q + L::T_BYTES, x1.head, x1.t0, bq);
             bool ok = true;
-            int &ks = fetched[0], &vs = fetched[1];
-            for (int i = 0; i <= w.n && ok; ++i) {       // keys a tile ahead of the values
+            for (int i = 1; i <= w.n; ++i) {             // keys a tile ahead of the values
                 if (i < w.n) {
                     const int s = i % L::KS;
-                    if (i >= L::KS) ok = mbar_wait(smem_u32(&s_kfree[s]), (i / L::KS - 1) & 1);
+                    if (i >= L::KS) ok = wait_thread(smem_u32(&s_kfree[s]), (i / L::KS - 1) & 1);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(smem_u32(&s_kfull[s]), L::T_BYTES);
-                    load(mk, base + L::K + s * L::T_BYTES, hk, w.tile(i) * TILE, smem_u32(&s_kfull[s]));
-                    ++ks;
+                    fetch(mk, L::K + s * L::T_BYTES, i, s_kfull[s]);
+                    ++fetched[0];
                 }
-                if (i > 0) {
+                if (i > 1) {
                     const int s = (i - 1) % L::VS;
-                    if (i - 1 >= L::VS) ok = mbar_wait(smem_u32(&s_vfree[s]), ((i - 1) / L::VS - 1) & 1);
+                    if (i - 1 >= L::VS) ok = wait_thread(smem_u32(&s_vfree[s]), ((i - 1) / L::VS - 1) & 1);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(smem_u32(&s_vfull[s]), L::T_BYTES);
-                    load(mv, base + L::V + s * L::T_BYTES, hk, w.tile(i - 1) * TILE, smem_u32(&s_vfull[s]));
-                    ++vs;
+                    fetch(mv, L::V + s * L::T_BYTES, i - 1, s_vfull[s]);
+                    ++fetched[1];
                 }
             }
             if (!ok) give_up();
         }
     } else if (warp == 1) {
-        // ---- products
-        if (lane == 0) {
-            constexpr uint32_t ID_S = idesc<E>(TILE, TILE, 0), ID_O = idesc<E>(TILE, D, 1);
-            auto scores = [&](int x, int i) {
-                const uint32_t q = base + L::Q + x * L::T_BYTES, k = base + L::K + (i % L::KS) * L::T_BYTES;
+        // ---- products.  TMEM addresses start at 0: the CTA has all of it
+        constexpr uint32_t ID_S = idesc<E>(TILE, TILE, 0), ID_O = idesc<E>(TILE, D, 1);
+        auto scores = [&](int x, int stage) {
+            const uint32_t qd = desc_k(base + L::Q + x * L::T_BYTES), kd = desc_k(base + L::K + stage * L::T_BYTES);
+            if (elect()) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (s / 4) * BOX + (s % 4) * 32;
-                    mma_bf16(tmem + TM_S + x * 128, sdesc_sw128(q + off), sdesc_sw128(k + off), ID_S, s > 0);
+                    const uint32_t off = ((s / 4) * BOX + (s % 4) * 32) >> 4;
+                    product(TM_S + x * 128, qd + off, kd + off, ID_S, s > 0);
                 }
                 commit(smem_u32(&s_s[x]));
-            };
-            bool ok = mbar_wait(smem_u32(&s_q), 0) && mbar_wait(smem_u32(&s_kfull[0]), 0);
-            int done[2] = {0, 0};
-            if (ok) {
-                fence_after();
-                if (w.active(x0, 0)) scores(0, 0);
-                if (w.active(x1, 0)) scores(1, 0);
-                commit(smem_u32(&s_kfree[0]));
             }
-            for (int i = 0; i < w.n && ok; ++i) {
-                const uint32_t v = base + L::V + (i % L::VS) * L::T_BYTES;
-                const bool more = i + 1 < w.n;
-                ok = mbar_wait(smem_u32(&s_vfix[i % L::VS]), (i / L::VS) & 1);
-                if (ok && more) ok = mbar_wait(smem_u32(&s_kfull[(i + 1) % L::KS]), ((i + 1) / L::KS) & 1);
+            __syncwarp();
+        };
+        auto signal = [&](uint64_t &bar) {
+            if (elect()) commit(smem_u32(&bar));
+            __syncwarp();
+        };
+        bool ok = wait_warp(smem_u32(&s_q), 0) && wait_warp(smem_u32(&s_kfull[0]), 0);
+        if (ok) {
+            fence_after();
+            if (w.active(x0, 0)) scores(0, 0);
+            if (w.active(x1, 0)) scores(1, 0);
+            signal(s_kfree[0]);
+        }
+        int ks = 1 % L::KS, kp = 1 / L::KS & 1, vs = 0;      // stage (and parity) of the next keys and values
+        int done[2] = {0, 0};
+        for (int i = 0; i < w.n && ok; ++i) {
+            const bool more = i + 1 < w.n;
+            // of the sinks' tile only the rows that hold sinks
+            const int steps = w.is_sink(i) ? (p.S + 15) / 16 : TILE / 16;
+            const uint32_t vd = desc_mn(base + L::V + vs * L::T_BYTES, BOX);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const Rows &rows = x ? x1 : x0;
-                    if (!ok) continue;
-                    if (w.active(rows, i)) {
-                        ok = mbar_wait(smem_u32(&s_p[x]), done[x] & 1);
+            for (int x = 0; x < 2; ++x) {
+                const Rows &rows = x ? x1 : x0;
+                const bool next = more && w.active(rows, i + 1);
+                if (w.active(rows, i)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && wait_warp(smem_u32(&s_p[x][h]), done[x] & 1);
                         if (!ok) continue;
                         fence_after();
-                        // of the sinks' tile only the rows that hold sinks
-                        const int steps = w.is_sink(i) ? (p.S + 15) / 16 : TILE / 16;
-                        for (int s = 0; s < steps; ++s)
-                            mma_bf16_ta(tmem + TM_O + x * D, tmem + TM_S + x * 128 + s * 8, sdesc_mn_sw128(v + s * 2048, BOX), ID_O,
-                                        done[x] > 0 || s > 0);
-                        ++done[x];
+                        if (elect()) {
+#pragma unroll
+                            for (int s = h * 4; s < h * 4 + 4; ++s)
+                                if (s < steps) product_ta(TM_O + x * D, TM_S + x * 128 + s * 8, vd + s * (2048 >> 4), ID_O, done[x] > 0 || s > 0);
+                        }
+                        __syncwarp();
                     }
-                    if (more && w.active(rows, i + 1)) scores(x, i + 1);
+                    ++done[x];
+                } else if (next) {
+                    ok = ok && wait_warp(smem_u32(&s_kfull[ks]), kp);
+                    fence_after();
                 }
-                commit(smem_u32(&s_vfree[i % L::VS]));
-                if (more) commit(smem_u32(&s_kfree[(i + 1) % L::KS]));
+                if (ok && next) scores(x, ks);
             }
-            if (ok) {
-                commit(smem_u32(&s_o[0]));
-                commit(smem_u32(&s_o[1]));
-            } else {
-                give_up();
-                commit(smem_u32(&s_end));          // the products in flight end before the memory is given back
-                mbar_wait(smem_u32(&s_end), 0);
-            }
+            if (!ok) break;
+            signal(s_vfree[vs]);
+            if (++vs == L::VS) vs = 0;
+            if (more) signal(s_kfree[ks]);
+            if (++ks == L::KS) ks = 0, kp ^= 1;
         }
-    } else if (warp < 4) {
-        // ---- values behind masked places
-        const int half = warp - 2;
+        if (ok) {
+            signal(s_o[0]);
+            signal(s_o[1]);
+        } else {
+            if (lane == 0) give_up();
+            signal(s_end);                     // the products in flight end before the memory is given back
+            wait_warp(smem_u32(&s_end), 0);
+        }
+    } else if (warp == 2) {
+        // ---- values behind masked places; tells the products that a tile's values and the next keys are there
         bool ok = true;
+        int seen[2] = {0, 0};
+        auto there = [&](int i) {
+            if (i + 1 < w.n) ok = wait_warp(smem_u32(&s_kfull[(i + 1) % L::KS]), ((i + 1) / L::KS) & 1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || !w.active(x ? x1 : x0, i)) continue;
+                ok = wait_warp(smem_u32(&s_s[x]), seen[x]++ & 1);     // the last round's arrivals are complete
+                if (ok && lane == 0) mbar_arrive(smem_u32(&s_p[x][0]));
+            }
+        };
         for (int i = 0; i < w.n && ok; ++i) {
-            ok = mbar_wait_warp(smem_u32(&s_vfull[i % L::VS]), (i / L::VS) & 1);
+            ok = wait_warp(smem_u32(&s_vfull[i % L::VS]), (i / L::VS) & 1);
             if (!ok) break;
             if (!look_after(i)) {
-                if (lane == 0) mbar_arrive(smem_u32(&s_vfix[i % L::VS]));
+                there(i);
                 continue;
             }
             unsigned char *const v = basep + L::V + (i % L::VS) * L::T_BYTES;
             const int real = at.len - w.tile(i) * TILE;     // rows of the sequence
-            constexpr uint32_t INF = Pair<E>::INF;
-            bool bad = false;
-            for (int r = half * 64; r < half * 64 + 64; r += 4)
+            // times zero, added up: NaN where one is infinite or NaN
+            uint4 *const mine = reinterpret_cast<uint4 *>(v + (lane / 8) * 128 + (lane & 7) * 16);
+            uint32_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const int row = r + lane / 8;
-                    uint4 *const at16 = reinterpret_cast<uint4 *>(v + c * BOX + row * 128 + (lane & 7) * 16);
-                    uint4 x = *at16;
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll 8
+                for (int r = 0; r < 32; ++r) {
+                    const uint4 x = mine[c * (BOX / 16) + r * 32];
+                    sum[0] = Pair<E>::times_zero(x.x, sum[0]);
+                    sum[1] = Pair<E>::times_zero(x.y, sum[1]);
+                    sum[2] = Pair<E>::times_zero(x.z, sum[2]);
+                    sum[3] = Pair<E>::times_zero(x.w, sum[3]);
+                }
+            bool bad = ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0;
+            if (__any_sync(0xffffffffu, bad) || real < TILE) {
+                constexpr uint32_t INF = Pair<E>::INF;
+                bad = false;
+#pragma unroll 1
+                for (int i = 0; i < D / 64 * 32; ++i) {
+                    const int r = i % 32;
+                    uint4 x = mine[i / 32 * (BOX / 16) + r * 32];
                     uint32_t *const e = reinterpret_cast<uint32_t *>(&x);
                     bool hit = false;
 #pragma unroll
@@ -244,20 +296,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                         hit |= (lo | hi) != 0;
                         e[j] &= ~(lo | hi);
                     }
-                    if (row >= real) *at16 = make_uint4(0, 0, 0, 0);
-                    else if (hit) *at16 = x, bad = true;
+                    if (r * 4 + lane / 8 >= real) mine[i / 32 * (BOX / 16) + r * 32] = make_uint4(0, 0, 0, 0);
+                    else if (hit) mine[i / 32 * (BOX / 16) + r * 32] = x, bad = true;
                 }
-            bad = __any_sync(0xffffffffu, bad);
+                bad = __any_sync(0xffffffffu, bad);
+            }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                if (bad) *static_cast<volatile int *>(&s_bad) = 1;
+            if (lane == 0 && bad) {
+                *static_cast<volatile int *>(&s_bad) = 1;
                 __threadfence_block();
-                mbar_arrive(smem_u32(&s_vfix[i % L::VS]));
             }
+            there(i);
         }
         if (!ok && lane == 0) give_up();
-    } else {
+    } else if (warp > 3) {
         // ---- softmax, a thread a row
         more_registers<REGS_SOFTMAX>();
         const int x = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
@@ -269,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int i = 0; i < w.n; ++i) {
             if (!w.active(rows, i)) continue;
-            ok = mbar_wait_warp(smem_u32(&s_s[x]), n & 1);
+            ok = wait_warp(smem_u32(&s_s[x]), n & 1);
             if (!ok) break;
             fence_after();
             uint32_t u[4][32];
@@ -281,19 +334,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (w.masked(rows, i, at.len, p.W)) {
                 int a, b;
                 w.visible(rows, i, r, p.W, p.S, a, b);
-                const unsigned len = b >= a ? b - a + 1 : 0;
+                if (__any_sync(0xffffffffu, a > 0)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int j = 0; j < TILE; ++j)
+                        if (j < a) u[j / 32][j % 32] = 0xFF800000u;
+                }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (static_cast<unsigned>(c * 32 + j - a) >= len) u[c][j] = 0xFF800000u;
+                for (int j = 0; j < TILE; ++j)
+                    if (j > b) u[j / 32][j % 32] = 0xFF800000u;
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 32; j += 2)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(u[c][j]));
-            const float new_m = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                for (int c = 0; c < 4; ++c) top[c] = max3(top[c], __uint_as_float(u[c][j]), __uint_as_float(u[c][j + 1]));
+            const float new_m = max3(m, fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             if (n == 0) {
                 m = new_m;
             } else if (__any_sync(0xffffffffu, (new_m - m) * p.c > LAZY)) {
@@ -315,26 +370,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float2 cc = make_float2(p.c, p.c), mc = make_float2(-m * p.c, -m * p.c);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t e[16];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t e[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float2 v = fma2(make_float2(__uint_as_float(u[c][2 * j]), __uint_as_float(u[c][2 * j + 1])), cc, mc);
+                for (int j = 0; j < 32; ++j) {
+                    const int k = h * 64 + 2 * j;
+                    float2 v = fma2(make_float2(__uint_as_float(u[k / 32][k % 32]), __uint_as_float(u[k / 32][k % 32 + 1])), cc, mc);
                     v.x = ex2_ftz(v.x);
                     v.y = ex2_ftz(v.y);
                     s2[j & 1] = add2(s2[j & 1], v);
                     e[j] = Pair<E>::pack(v.x, v.y);
                 }
-                tmem_st16_nowait(ts + c * 16, e);
+                tmem_st32_nowait(ts + h * 32, e);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_p[x][h]));
             }
             sum += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-            tmem_wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
             ++n;
         }
-        if (ok && n > 0) ok = mbar_wait_warp(smem_u32(&s_o[x]), 0);
+        if (ok && n > 0) ok = wait_warp(smem_u32(&s_o[x]), 0);
         if (!ok && lane == 0) give_up();
         if (ok && n > 0) {
             fence_after();
@@ -344,15 +400,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float inv = 1.f / sum;
             const int bad = *static_cast<volatile int *>(&s_bad);
             unsigned char *const out = basep + L::Q + x * L::T_BYTES;      // the queries are no longer needed: rows of D, chunks swizzled
+            uint32_t t[D / 32][32];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(to + c * 32, t[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) reg_fence32(t[c]);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-                uint32_t t[32];
-                tmem_ld32_nowait(to + c * 32, t);
-                tmem_wait_ld();
-                reg_fence32(t);
                 float f[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(t[j]) * inv;
+                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(t[c][j]) * inv;
                 if (bad && real) {
                     // values that are infinite or NaN: what the row sees of them
                     for (int i = 0; i < w.n; ++i) {
@@ -384,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr int CH = D / 8, RPI = 32 / CH;     // 16-byte pieces of a row, rows of one store of the warp
             const int r0 = (warp & 3) * 32, ch = lane % CH;
             E *const dst = o + (static_cast<int64_t>(at.start) + rows.t0) * ldo + rows.head * D + ch * 8;
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < 32; k += RPI) {
                 const int row = r0 + k + lane / CH;
                 if (row < rows.count)

@@ -26,6 +26,25 @@ struct Shape {
     float scale;
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Named barrier 'id' over 'threads' threads with an OR of v: everyone gets the same answer.
+__device__ __forceinline__ bool bar_or(int id, uint32_t threads, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap &m) { asm volatile("prefetch.tensormap [%0];" ::"l"(&m) : "memory"); }
+
 // Registers of a warpgroup's threads, after the launch gave every thread the same.
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -36,15 +55,27 @@ inline Shape window_shape(const int32_t *plan_host, const int32_t *plan_dev, con
                  in.scale * 1.44269504088896340736f, in.scale};
 }
 
-template <typename E> struct Pair;        // two values rounded to a packed pair (a in the low half)
+template <typename E> struct Pair;        // two values rounded to a packed pair (a in the low half); x 0 + c of such pairs
 template <> struct Pair<__nv_bfloat16> {
     static constexpr bool BF16 = true;
     static constexpr uint32_t INF = 0x7F80u;
+    static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t c)
+    {
+        uint32_t d;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(c));
+        return d;
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return bf16x2_bits(a, b); }
 };
 template <> struct Pair<__half> {
     static constexpr bool BF16 = false;
     static constexpr uint32_t INF = 0x7C00u;
+    static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t c)
+    {
+        uint32_t d;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(c));
+        return d;
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
         const __half2 v = __floats2half2_rn(a, b);
@@ -58,12 +89,52 @@ template <typename E> __host__ __device__ constexpr uint32_t idesc(int M, int N,
     return idesc_bf16(M, N, 0, b_mn) & (Pair<E>::BF16 ? ~0u : ~((1u << 7) | (1u << 10)));
 }
 
-// Descriptor of an MN-major operand in the 128-byte swizzle layout: rows (the contraction index) of 128 bytes, 8-row groups
-// 1024 bytes apart, the next 64 columns 'lbo' bytes on.  A K step of 16 rows advances the start by 2048 bytes.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo)
+// Shared-memory descriptors in the 128-byte swizzle layout, by halves: rows of 128 bytes, 8-row groups 1024 bytes apart (the
+// upper half: that, version 1, the swizzle).  K-major operands: a K step of 16 columns advances the start by 32 bytes.  MN-major
+// ones (rows are the contraction index): the next 64 columns are 'lbo' bytes on, and a K step of 16 rows advances the start
+// by 2048 bytes.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4 << 16); }
+
+// The products are issued by a whole warp whose values are the same in every lane, so that they stay in uniform registers, one
+// elected lane doing it: a lone thread's products took 100 cycles each to issue, twice what the tensor cores need for them.
+__device__ __forceinline__ bool elect()
 {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+// D[tmem] (+)= A B^T, one K step: A in shared memory, or (ta) in TMEM.
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\nsetp.ne.b32 p, %5, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+                 "r"(a), "r"(b), "n"(DESC_HI), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)));
+}
+__device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %3};\nsetp.ne.b32 p, %5, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+                 "r"(a), "r"(b), "n"(DESC_HI), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)));
+}
+
+// A bounded wait of a whole warp, the same answer in every lane.  One lane polls; the clock is read only where the first look fails.
+__device__ __forceinline__ bool look(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity) { return look(bar, parity) || mbar_wait(bar, parity); }
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity)
+{
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = wait_thread(bar, parity);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // The sequence and tile of slot 'slot'.  Sequence n has its tiles of 'rows' tokens from slot cu[n] / rows + n on, which
@@ -88,6 +159,11 @@ __device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Pl
     at.start = cu[lo];
     at.len = cu[lo + 1] - at.start;
     at.t0 = (slot - (at.start / rows + lo)) * rows;
+    // the same in every lane; said so that the compiler knows
+    at.seq = __shfl_sync(0xffffffffu, at.seq, 0);
+    at.start = __shfl_sync(0xffffffffu, at.start, 0);
+    at.len = __shfl_sync(0xffffffffu, at.len, 0);
+    at.t0 = __shfl_sync(0xffffffffu, at.t0, 0);
     return at.t0 < at.len;
 }
 inline int tile_slots(int T, int N, int rows) { return T / rows + N; }

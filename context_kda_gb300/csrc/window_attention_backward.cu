@@ -62,17 +62,6 @@ __device__ __forceinline__ float ds_factor(float most_do, float most_v)
     return exp2f(static_cast<float>(min(max(15 - e, -100), 100)));
 }
 
-__device__ __forceinline__ bool bar_or(int id, uint32_t threads, bool v)      // everyone gets the same answer
-{
-    uint32_t r;
-    asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
-        : "memory");
-    return r != 0;
-}
-
 // KEYS: the CTA owns keys (dk, dv); else queries (dq).
 template <typename E, int D, bool KEYS>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -187,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             for (int i = 0; i < n; ++i) {
                 const int s = i % STAGES;
-                if (i >= STAGES) ok = mbar_wait(smem_u32(&s_free[s]), (i / STAGES - 1) & 1);
+                if (i >= STAGES) ok = wait_thread(smem_u32(&s_free[s]), (i / STAGES - 1) & 1);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[s]);
                 mbar_arrive_expect_tx(bar, 2 * L::Y_BYTES);
@@ -200,57 +189,68 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) give_up();
         }
     } else if (warp == 1) {
-        // ---- products
-        if (lane == 0) {
-            constexpr uint32_t ID_S = idesc<E>(TILE, SUB, 0), ID_A = idesc<E>(TILE, D, 1);
-            auto scores = [&](int i) {
-                const uint32_t d = tmem + (i & 1) * 128, x = base + L::X, y = y1(i);
+        // ---- products.  TMEM addresses start at 0: the CTA has all of it
+        constexpr uint32_t ID_S = idesc<E>(TILE, SUB, 0), ID_A = idesc<E>(TILE, D, 1);
+        const uint32_t xd = desc_k(base + L::X);
+        auto scores = [&](int buf, uint32_t y) {
+            const uint32_t yd = desc_k(y);
+            if (elect()) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        mma_bf16(d + w * SUB, sdesc_sw128(x + w * L::X_BYTES + (s / 4) * BOX + (s % 4) * 32),
-                                 sdesc_sw128(y + w * L::Y_BYTES + (s / 4) * SBOX + (s % 4) * 32), ID_S, s > 0);
-                commit(smem_u32(&s_s[i & 1]));
-            };
-            auto wait_y = [&](int i) { return mbar_wait(smem_u32(&s_fix[i % STAGES]), (i / STAGES) & 1); };
-            bool ok = mbar_wait(smem_u32(&s_x), 0);
-            for (int i = 0; i < 2 && i < n && ok; ++i) {
-                ok = wait_y(i);
-                if (!ok) break;
-                fence_after();
-                scores(i);
+                        product(buf * 128 + w * SUB, xd + ((w * L::X_BYTES + (s / 4) * BOX + (s % 4) * 32) >> 4),
+                                yd + ((w * L::Y_BYTES + (s / 4) * SBOX + (s % 4) * 32) >> 4), ID_S, s > 0);
+                commit(smem_u32(&s_s[buf]));
             }
-            for (int i = 0; i < n && ok; ++i) {
-                ok = mbar_wait(smem_u32(&s_p[i & 1]), (i >> 1) & 1);
-                if (!ok) break;
-                fence_after();
-                const uint32_t d = tmem + (i & 1) * 128, y = y1(i);
+            __syncwarp();
+        };
+        bool ok = wait_warp(smem_u32(&s_x), 0);
+        int next = 0, next_parity = 0;              // stage and parity of the next tile to be multiplied
+        auto step_next = [&] {
+            if (++next == STAGES) next = 0, next_parity ^= 1;
+        };
+        for (int i = 0; i < 2 && i < n && ok; ++i) {
+            ok = wait_warp(smem_u32(&s_fix[next]), next_parity);
+            if (!ok) break;
+            fence_after();
+            scores(i, base + L::Y + next * 2 * L::Y_BYTES);
+            step_next();
+        }
+        int stage = 0;
+        for (int i = 0; i < n && ok; ++i) {
+            ok = wait_warp(smem_u32(&s_p[i & 1]), (i >> 1) & 1);
+            if (!ok) break;
+            fence_after();
+            const uint32_t d = (i & 1) * 128, y = base + L::Y + stage * 2 * L::Y_BYTES, y1d = desc_mn(y, SBOX), y2d = desc_mn(y + L::Y_BYTES, SBOX);
+            if (elect()) {
                 if (i >= dry)
 #pragma unroll
-                    for (int s = 0; s < SUB / 16; ++s)
-                        mma_bf16_ta(tmem + TM_ACC, d + SUB + s * 8, sdesc_mn_sw128(y + s * 2048, SBOX), ID_A, i > dry || s > 0);
+                    for (int s = 0; s < SUB / 16; ++s) product_ta(TM_ACC, d + SUB + s * 8, y1d + s * (2048 >> 4), ID_A, i > dry || s > 0);
                 if (KEYS)
 #pragma unroll
-                    for (int s = 0; s < SUB / 16; ++s)
-                        mma_bf16_ta(tmem + TM_ACC + D, d + s * 8, sdesc_mn_sw128(y + L::Y_BYTES + s * 2048, SBOX), ID_A, i > 0 || s > 0);
-                commit(smem_u32(&s_free[i % STAGES]));
-                if (i + 2 < n) {
-                    ok = wait_y(i + 2);
-                    if (!ok) break;
-                    fence_after();
-                    scores(i + 2);
-                }
+                    for (int s = 0; s < SUB / 16; ++s) product_ta(TM_ACC + D, d + s * 8, y2d + s * (2048 >> 4), ID_A, i > 0 || s > 0);
+                commit(smem_u32(&s_free[stage]));
             }
-            if (!ok) give_up();
-            commit(smem_u32(&s_end));
-            if (!ok) mbar_wait(smem_u32(&s_end), 0);     // the products in flight end before the memory is given back
+            __syncwarp();
+            if (++stage == STAGES) stage = 0;
+            if (i + 2 < n) {
+                ok = wait_warp(smem_u32(&s_fix[next]), next_parity);
+                if (!ok) break;
+                fence_after();
+                scores(i & 1, base + L::Y + next * 2 * L::Y_BYTES);
+                step_next();
+            }
         }
+        if (!ok && lane == 0) give_up();
+        if (elect()) commit(smem_u32(&s_end));
+        __syncwarp();
+        if (!ok) wait_warp(smem_u32(&s_end), 0);     // the products in flight end before the memory is given back
     } else if (warp < 4) {
         // ---- rows behind the sequence's end: zeros, so that a factor of zero meets no infinity or NaN there
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
-            ok = mbar_wait_warp(smem_u32(&s_full[i % STAGES]), (i / STAGES) & 1);
+            ok = wait_warp(smem_u32(&s_full[i % STAGES]), (i / STAGES) & 1);
             if (!ok) break;
             const int real = at.len - tile(i) * SUB;
             if (real < SUB) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const int turn = (i >> 1) & 1;
             if (KEYS) reinterpret_cast<float *>(s_row[x][turn])[(t & 63) / 4 * 8 + (t >> 6) * 4 + (t & 3)] = next;
-            ok = mbar_wait_warp(smem_u32(&s_s[x]), turn);
+            ok = wait_warp(smem_u32(&s_s[x]), turn);
             if (KEYS) ok = !bar_or(1 + x, 128, !ok);
             if (!ok) break;
             if (KEYS && i + 2 < n) next = row_value(i + 2);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
         }
         if (!KEYS && dry > 0 && !corrected && !correct(ok)) ok = false;      // a wait gave up in the dry steps, or no step of this group's follows
-        if (ok) ok = mbar_wait_warp(smem_u32(&s_end), 0);
+        if (ok) ok = wait_warp(smem_u32(&s_end), 0);
         if (!ok && lane == 0) give_up();
         // ---- the sums: the first group writes dk or dq, the second dv; rounded once, rows by way of shared memory (the own rows are
         // no longer needed), the sinks' in fp32 into the workspace
