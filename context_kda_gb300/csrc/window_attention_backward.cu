@@ -4,15 +4,19 @@
 //
 // Three kernels, and no atomics on sums, so that the same call gives the same bits: the rows' D; a kernel whose CTAs own 128
 // queries and go over their keys (dq); and one whose CTAs own 128 keys and go over the queries that see them, of all heads of
-// the group (dk, dv).  Scores and dp are computed in both: seven products for each pair of tiles where one kernel with a shared dq would take five.
+// the group (dk, dv).  Scores and dp are computed in both: seven products for each pair of tiles where one kernel with a shared dq
+// would take five.
 // The last two are one kernel of two kinds.  Its own rows X1, X2 (keys and values, or queries and do) stay in shared
-// memory; tiles of 64 of the other side, Y1, Y2, come by TMA four deep:
-//     S = X1 Y1^T,  P' = X2 Y2^T           to TMEM, two buffers that alternate between two groups of four warps,
-//     p, ds                                 a thread a row, back to TMEM in their places, as A operands of
-//     A2 += ds Y1  (dk or dq),   A1 += p Y2  (dv).
+// memory; tiles of 128 of the other side, Y1, Y2, come by TMA.  Per pair of tiles
+//     S = X1 Y1^T, P' = X2 Y2^T             to TMEM,
+//     p, then ds                            two threads a row; both back to TMEM in the places of S and P', as A operands of
+//     A2 += p Y2 (dv), A1 += ds Y1 (dk or dq).
+// The tensor cores run A2(i), S(i+1), A1(i), P'(i+1) in turn: p(i+1) is computed during A1(i) and P'(i+1), ds(i) during A2(i) and
+// S(i+1), so one buffer each is enough and neither side waits for long.  (Tiles of 64 with two buffers fit too, but products with
+// N = 64 are bound by shared memory: 57 cycles where 32 would do.)
 //
 // D_i from the output carries that output's rounding.  Where a row sees many keys the rest hides it, where it sees few it would be as large as
-// the rounding of ds.  Queries whose tiles are DRY or fewer (the first rows of a sequence, narrow windows) go over them twice: sum_j ds_ij,
+// the rounding of ds.  The first queries of a sequence, and all with a narrow window, go over their tiles twice: sum_j ds_ij,
 // which is zero with the right D, corrects D first, and the corrected D is left for the keys.
 //
 // Sinks are seen by every later query of their sequence.  Their tile's window part is worked as any other; the rest is cut into
@@ -30,19 +34,19 @@ using namespace attn;
 __device__ int g_window_back_status;
 
 constexpr int THREADS = 384;
-constexpr int SUB = 64;                   // rows of a tile of the other side
-constexpr int STAGES = 4;
-constexpr int DRY = 3;                    // tiles of the other side that queries go over twice
+constexpr int REGS_OTHER = 72, REGS_SOFTMAX = 216;     // of 168 at the launch: 128 x 72 + 256 x 216 = 384 x 168
+constexpr int HALF = TILE / 2;            // columns of a thread
+constexpr int NARROW = 32;                // windows up to this are narrow
 constexpr int CHUNK = 1024;               // queries of a piece of the sinks' work
-constexpr uint32_t SBOX = SUB * 128;      // 64 rows of 64 columns
 
 template <int D> struct Smem {
-    static constexpr uint32_t X_BYTES = D / 64 * BOX, Y_BYTES = D / 64 * SBOX;
-    static constexpr uint32_t X = 0, Y = 2 * X_BYTES, BYTES = Y + STAGES * 2 * Y_BYTES, ALLOC = BYTES + 1024;
-    static_assert(ALLOC <= 227 * 1024, "shared memory");
+    static constexpr uint32_t T_BYTES = D / 64 * BOX;
+    static constexpr int N1 = 3, N2 = 2;      // stages of Y1 (read first and last in a round) and of Y2
+    static constexpr uint32_t X = 0, Y1 = 2 * T_BYTES, Y2 = Y1 + N1 * T_BYTES, BYTES = Y2 + N2 * T_BYTES, ALLOC = BYTES + 1024;
+    static_assert(ALLOC + 2048 <= 227 * 1024, "shared memory");      // with the static part
 };
-// TMEM columns: two buffers of S and P', then the sums
-constexpr uint32_t TM_ACC = 256, TM_COLS = 512;
+// TMEM columns: S (p), P' (ds), the sums
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_ACC = 256, TM_COLS = 512;
 
 struct Back {
     const float *lse;                     // [H][T]
@@ -72,13 +76,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool F16 = !Pair<E>::BF16;
     constexpr float P_EXP = F16 ? 10.f : 0.f;            // p is kept times 2^P_EXP
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_x, s_full[STAGES], s_fix[STAGES], s_free[STAGES], s_s[2], s_p[2], s_end;
-    __shared__ float4 s_row[2][2][SUB / 4][2];           // (KEYS) the queries' lse and D, by group and buffer
-    __shared__ float s_dry[KEYS ? 1 : 2][KEYS ? 1 : TILE];
+    __shared__ uint64_t s_x, s_y1[L::N1], s_free1[L::N1], s_y2[L::N2], s_free2[L::N2], s_go, s_s, s_pp, s_a, s_b, s_end;
+    __shared__ float4 s_row[2][HALF / 4][2];             // KEYS: the queries' lse and D, by group of warps; else: sums of ds
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    if (tid == 0) prefetch_map(mx1), prefetch_map(mx2), prefetch_map(my1), prefetch_map(my2);
     if (!plan_matches(p.plan, p.sig)) {
         if (tid == 0 && blockIdx.x == 0) record_status(&g_window_back_status, KDA_ERR_INVALID_ARG);
         return;
@@ -101,55 +105,87 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     const int W = min(p.W, at.len), x0 = sinks ? 0 : at.t0, rows = min(TILE, at.len - x0);      // own rows [x0, x0 + rows)
     const bool has_sinks = p.S > 0 && W < at.len;        // some query has left a sink behind its window
-    // tiles of the other side: [lo, hi], then (queries) those of the sinks
+    // tiles of the other side: [lo, hi], then (queries) that of the sinks
     int lo, hi, extra = 0;
     if (KEYS) {
-        lo = (sinks ? max(at.t0, W) : x0) / SUB;
-        hi = (sinks ? min(at.t0 + CHUNK, at.len) - 1 : static_cast<int>(min(static_cast<int64_t>(x0) + TILE - 1 + W, static_cast<int64_t>(at.len)) - 1)) / SUB;
+        const int64_t end = sinks ? at.t0 + CHUNK : static_cast<int64_t>(x0) + TILE - 1 + W;
+        lo = (sinks ? max(at.t0, W) : x0) / TILE;
+        hi = static_cast<int>((min(end, static_cast<int64_t>(at.len)) - 1) / TILE);
         if (sinks && (!has_sinks || lo > hi)) return;
     } else {
-        lo = max(0, x0 - W + 1) / SUB;
-        hi = (x0 + rows - 1) / SUB;
-        if (has_sinks && x0 + rows - 1 >= W) extra = (p.S + SUB - 1) / SUB;
+        lo = max(0, x0 - W + 1) / TILE;
+        hi = x0 / TILE;
+        extra = has_sinks && x0 + rows - 1 >= W;
     }
-    const int per_head = hi - lo + 1, tiles = KEYS ? g * per_head : per_head + extra;
-    const int dry = !KEYS && tiles <= DRY ? tiles : 0, n = dry + tiles;      // steps, the first 'dry' of them for D alone
+    const int tiles = KEYS ? g * (hi - lo + 1) : hi - lo + 1 + extra;
+    const int dry = !KEYS && (tiles == 1 || W <= NARROW) ? tiles : 0, n = dry + tiles;      // steps, the first 'dry' of them for D alone
     const int xh = head, yh = KEYS ? head * g : head / g;                        // heads of the own rows and of the other side
-    auto tile = [&](int i) {
-        if (KEYS) return lo + i % per_head;
-        if (i >= dry) i -= dry;
-        return i < per_head ? hi - i : i - per_head;
+    // The steps in order: keys go over the tiles of each query head from lo up; queries from the diagonal down, the sinks last.
+    struct Iter {
+        int tile, head;
+        bool sink;
     };
-    auto y_head = [&](int i) { return KEYS ? yh + i / per_head : yh; };
-    auto is_sink = [&](int i) { return KEYS ? sinks : (i >= dry ? i - dry : i) >= per_head; };
-    // whether all own rows and all rows of tile i see each other
-    auto whole = [&](int i) {
-        const int y0 = tile(i) * SUB;
-        if (is_sink(i)) return false;
-        if (KEYS) return y0 >= x0 + TILE - 1 && y0 + SUB - 1 - x0 < W && y0 + SUB <= at.len;
-        return y0 + SUB - 1 <= x0 && x0 + TILE - 1 - y0 < W;
-    };
-    // columns [a, b] of tile i that go with own row r
-    auto visible = [&](int i, int r, int &a, int &b) {
-        const int y0 = tile(i) * SUB, x = x0 + r;
+    auto first = [&] { return Iter{KEYS ? lo : hi, yh, KEYS && sinks}; };
+    auto advance = [&](Iter &i) {
         if (KEYS) {
-            a = is_sink(i) ? (x < p.S ? x + W - y0 : SUB) : x - y0;
-            b = min(SUB - 1, (is_sink(i) ? at.len - 1 : static_cast<int>(min(static_cast<int64_t>(x) + W, static_cast<int64_t>(at.len)) - 1)) - y0);
+            if (++i.tile > hi) i.tile = lo, ++i.head;
+        } else if (i.sink || (i.tile == lo && !extra)) {
+            i = first();
+        } else if (i.tile == lo) {
+            i.tile = 0, i.sink = true;
         } else {
-            a = is_sink(i) ? 0 : x - W + 1 - y0;
-            b = min(SUB - 1, (is_sink(i) ? min(p.S - 1, x - W) : x) - y0);
+            --i.tile;
         }
-        a = max(a, 0);
+    };
+    // whether all own rows and all rows of the tile see each other
+    auto whole = [&](const Iter &i) {
+        const int y0 = i.tile * TILE;
+        if (i.sink) return false;
+        if (KEYS) return y0 >= x0 + TILE - 1 && y0 + TILE - 1 - x0 < W && y0 + TILE <= at.len;
+        return y0 + TILE - 1 <= x0 && x0 + TILE - 1 - y0 < W;
+    };
+    // columns [a, b] of the tile that go with own row r
+    auto visible = [&](const Iter &i, int r, int &a, int &b) {
+        const int y0 = i.tile * TILE, x = x0 + r;
+        if (KEYS) {
+            a = i.sink ? (x < p.S ? x + W - y0 : TILE) : x - y0;
+            b = (i.sink ? at.len - 1 : static_cast<int>(min(static_cast<int64_t>(x) + W, static_cast<int64_t>(at.len)) - 1)) - y0;
+        } else {
+            a = i.sink ? 0 : x - W + 1 - y0;
+            b = (i.sink ? min(p.S - 1, x - W) : x) - y0;
+        }
     };
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const basep = smem_raw + (base - smem_u32(smem_raw));
+    int fetched[2] = {0, 0};                             // (the fetching thread) tiles of Y1 and of Y2
+    auto load = [&](const CUtensorMap &m, uint32_t dst, int h, int row, uint32_t bar) {
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, h, at.start + row, bar);
+    };
+    auto fetch = [&](const CUtensorMap &m, uint32_t to, const Iter &i, uint64_t &full) {
+        mbar_arrive_expect_tx(smem_u32(&full), L::T_BYTES);
+        load(m, base + to, i.head, i.tile * TILE, smem_u32(&full));
+    };
     if (tid == 0) {
         mbar_init(smem_u32(&s_x), 1);
-        for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&s_full[i]), 1), mbar_init(smem_u32(&s_fix[i]), 2), mbar_init(smem_u32(&s_free[i]), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s_s[i]), 1), mbar_init(smem_u32(&s_p[i]), 4);
+        for (int i = 0; i < L::N1; ++i) mbar_init(smem_u32(&s_y1[i]), 1), mbar_init(smem_u32(&s_free1[i]), 1);
+        for (int i = 0; i < L::N2; ++i) mbar_init(smem_u32(&s_y2[i]), 1), mbar_init(smem_u32(&s_free2[i]), 1);
+        mbar_init(smem_u32(&s_go), 1);
+        mbar_init(smem_u32(&s_s), 1);
+        mbar_init(smem_u32(&s_pp), 1);
+        mbar_init(smem_u32(&s_a), 9);
+        mbar_init(smem_u32(&s_b), 9);
         mbar_init(smem_u32(&s_end), 1);
         s_abort = 0;
+        // the first tiles are on their way before anything else
+        const uint32_t bx = smem_u32(&s_x);
+        mbar_arrive_expect_tx(bx, 2 * L::T_BYTES);
+        load(mx1, base + L::X, xh, x0, bx);
+        const Iter i = first();
+        fetch(my1, L::Y1, i, s_y1[0]);
+        load(mx2, base + L::X + L::T_BYTES, xh, x0, bx);
+        fetch(my2, L::Y2, i, s_y2[0]);
+        fetched[0] = fetched[1] = 1;
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), TM_COLS);
     fence_before();
@@ -161,237 +197,283 @@ __global__ void __launch_bounds__(THREADS, 1)
         record_status(&g_window_back_status, KDA_ERR_TIMEOUT);
         *abort_flag = 1;
     };
-    auto y1 = [&](int i) { return base + L::Y + (i % STAGES) * 2 * L::Y_BYTES; };
-    int fetched = 0;
+    if (warp < 4) fewer_registers<REGS_OTHER>();
 
     if (warp == 0) {
         // ---- fetch
         if (lane == 0) {
-            const uint32_t bx = smem_u32(&s_x);
-            mbar_arrive_expect_tx(bx, 2 * L::X_BYTES);
-            for (int c = 0; c < D / 64; ++c) {
-                tma_load_3d(base + L::X + c * BOX, &mx1, c * 64, xh, at.start + x0, bx);
-                tma_load_3d(base + L::X + L::X_BYTES + c * BOX, &mx2, c * 64, xh, at.start + x0, bx);
-            }
             bool ok = true;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % STAGES;
-                if (i >= STAGES) ok = wait_thread(smem_u32(&s_free[s]), (i / STAGES - 1) & 1);
+            Iter it = first();
+            for (int i = 1, s1 = 1, s2 = 1 % L::N2, r1 = 0, r2 = 0; i < n; ++i) {      // stages, and rounds through them
+                advance(it);
+                if (i >= L::N1) ok = wait_thread(smem_u32(&s_free1[s1]), (r1 - 1) & 1);
                 if (!ok) break;
-                const uint32_t bar = smem_u32(&s_full[s]);
-                mbar_arrive_expect_tx(bar, 2 * L::Y_BYTES);
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_3d(y1(i) + c * SBOX, &my1, c * 64, y_head(i), at.start + tile(i) * SUB, bar);
-                    tma_load_3d(y1(i) + L::Y_BYTES + c * SBOX, &my2, c * 64, y_head(i), at.start + tile(i) * SUB, bar);
-                }
-                ++fetched;
+                fetch(my1, L::Y1 + s1 * L::T_BYTES, it, s_y1[s1]);
+                ++fetched[0];
+                if (i >= L::N2) ok = wait_thread(smem_u32(&s_free2[s2]), (r2 - 1) & 1);
+                if (!ok) break;
+                fetch(my2, L::Y2 + s2 * L::T_BYTES, it, s_y2[s2]);
+                ++fetched[1];
+                if (++s1 == L::N1) s1 = 0, ++r1;
+                if (++s2 == L::N2) s2 = 0, ++r2;
             }
             if (!ok) give_up();
         }
     } else if (warp == 1) {
         // ---- products.  TMEM addresses start at 0: the CTA has all of it
-        constexpr uint32_t ID_S = idesc<E>(TILE, SUB, 0), ID_A = idesc<E>(TILE, D, 1);
-        const uint32_t xd = desc_k(base + L::X);
-        auto scores = [&](int buf, uint32_t y) {
-            const uint32_t yd = desc_k(y);
+        constexpr uint32_t ID_S = idesc<E>(TILE, TILE, 0), ID_A = idesc<E>(TILE, D, 1);
+        auto scores = [&](uint32_t to, uint32_t x, uint32_t y, uint64_t &bar) {
+            const uint32_t xd = desc_k(x), yd = desc_k(y);
             if (elect()) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        product(buf * 128 + w * SUB, xd + ((w * L::X_BYTES + (s / 4) * BOX + (s % 4) * 32) >> 4),
-                                yd + ((w * L::Y_BYTES + (s / 4) * SBOX + (s % 4) * 32) >> 4), ID_S, s > 0);
-                commit(smem_u32(&s_s[buf]));
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = ((s / 4) * BOX + (s % 4) * 32) >> 4;
+                    product(to, xd + off, yd + off, ID_S, s > 0);
+                }
+                commit(smem_u32(&bar));
             }
             __syncwarp();
         };
-        bool ok = wait_warp(smem_u32(&s_x), 0);
-        int next = 0, next_parity = 0;              // stage and parity of the next tile to be multiplied
-        auto step_next = [&] {
-            if (++next == STAGES) next = 0, next_parity ^= 1;
+        auto add = [&](uint32_t to, uint32_t from, uint32_t y, bool more) {
+            const uint32_t yd = desc_mn(y, BOX);
+            if (elect()) {
+#pragma unroll
+                for (int s = 0; s < TILE / 16; ++s)
+                    product_ta(to, from + (s / 4) * HALF + (s % 4) * 8, yd + s * (2048 >> 4), ID_A, more || s > 0);
+            }
+            __syncwarp();
         };
-        for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = wait_warp(smem_u32(&s_fix[next]), next_parity);
-            if (!ok) break;
+        auto signal = [&](uint64_t &bar) {
+            if (elect()) commit(smem_u32(&bar));
+            __syncwarp();
+        };
+        bool ok = wait_warp(smem_u32(&s_x), 0) && wait_warp(smem_u32(&s_go), 0);
+        if (ok) {
             fence_after();
-            scores(i, base + L::Y + next * 2 * L::Y_BYTES);
-            step_next();
+            scores(TM_S, base + L::X, base + L::Y1, s_s);
+            scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2, s_pp);
+            if (!KEYS) signal(s_free2[0]);
         }
-        int stage = 0;
+        int c1 = 0, c2 = 0;                              // stages of step i
         for (int i = 0; i < n && ok; ++i) {
-            ok = wait_warp(smem_u32(&s_p[i & 1]), (i >> 1) & 1);
+            const int d1 = c1 + 1 == L::N1 ? 0 : c1 + 1, d2 = c2 + 1 == L::N2 ? 0 : c2 + 1;
+            const bool next = i + 1 < n;
+            ok = wait_warp(smem_u32(&s_a), i & 1);       // S(i) is read (and p in its place); Y1(i + 1) is there
             if (!ok) break;
             fence_after();
-            const uint32_t d = (i & 1) * 128, y = base + L::Y + stage * 2 * L::Y_BYTES, y1d = desc_mn(y, SBOX), y2d = desc_mn(y + L::Y_BYTES, SBOX);
-            if (elect()) {
-                if (i >= dry)
-#pragma unroll
-                    for (int s = 0; s < SUB / 16; ++s) product_ta(TM_ACC, d + SUB + s * 8, y1d + s * (2048 >> 4), ID_A, i > dry || s > 0);
-                if (KEYS)
-#pragma unroll
-                    for (int s = 0; s < SUB / 16; ++s) product_ta(TM_ACC + D, d + s * 8, y2d + s * (2048 >> 4), ID_A, i > 0 || s > 0);
-                commit(smem_u32(&s_free[stage]));
+            if (KEYS) {
+                add(TM_ACC + D, TM_S, base + L::Y2 + c2 * L::T_BYTES, i > 0);
+                signal(s_free2[c2]);
             }
-            __syncwarp();
-            if (++stage == STAGES) stage = 0;
-            if (i + 2 < n) {
-                ok = wait_warp(smem_u32(&s_fix[next]), next_parity);
-                if (!ok) break;
-                fence_after();
-                scores(i & 1, base + L::Y + next * 2 * L::Y_BYTES);
-                step_next();
+            if (next) scores(TM_S, base + L::X, base + L::Y1 + d1 * L::T_BYTES, s_s);
+            ok = wait_warp(smem_u32(&s_b), i & 1);       // ds in the place of P'(i); Y2(i + 1) is there
+            if (!ok) break;
+            fence_after();
+            if (i >= dry) add(TM_ACC, TM_P, base + L::Y1 + c1 * L::T_BYTES, i > dry);
+            signal(s_free1[c1]);
+            if (next) {
+                scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2 + d2 * L::T_BYTES, s_pp);
+                if (!KEYS) signal(s_free2[d2]);
             }
+            c1 = d1;
+            c2 = d2;
         }
         if (!ok && lane == 0) give_up();
-        if (elect()) commit(smem_u32(&s_end));
-        __syncwarp();
-        if (!ok) wait_warp(smem_u32(&s_end), 0);     // the products in flight end before the memory is given back
-    } else if (warp < 4) {
-        // ---- rows behind the sequence's end: zeros, so that a factor of zero meets no infinity or NaN there
+        signal(s_end);
+        if (!ok) wait_warp(smem_u32(&s_end), 0);         // the products in flight end before the memory is given back
+    } else if (warp == 2) {
+        // ---- rows behind the sequence's end: zeros, so that a factor of zero meets no infinity or NaN there.  Tells the products
+        // when the next tiles are there
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            ok = wait_warp(smem_u32(&s_full[i % STAGES]), (i / STAGES) & 1);
-            if (!ok) break;
-            const int real = at.len - tile(i) * SUB;
-            if (real < SUB) {
-                unsigned char *const y = basep + (y1(i) - base) + (warp - 2) * L::Y_BYTES;
-                for (int r = real + lane / 8; r < SUB; r += 4)
-                    for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint4 *>(y + c * SBOX + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-            }
+        Iter it = first();
+        int s1 = 0, s2 = 0, r1 = 0, r2 = 0;
+        auto there = [&](uint64_t &full, int round, uint32_t to) {
+            ok = wait_warp(smem_u32(&full), round & 1);
+            const int real = at.len - it.tile * TILE;
+            if (!ok || real >= TILE) return;
+            for (int r = real + lane / 8; r < TILE; r += 4)
+                for (int c = 0; c < D / 64; ++c)
+                    *reinterpret_cast<uint4 *>(basep + to + c * BOX + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_fix[i % STAGES]));
+        };
+        there(s_y1[0], 0, L::Y1);
+        if (ok) there(s_y2[0], 0, L::Y2);
+        if (ok && lane == 0) mbar_arrive(smem_u32(&s_go));
+        for (int i = 0; i < n && ok; ++i) {
+            if (++s1 == L::N1) s1 = 0, ++r1;
+            if (++s2 == L::N2) s2 = 0, ++r2;
+            advance(it);
+            // (an arrival waits for the step's scores: those of the step before are complete then)
+            if (i + 1 < n) there(s_y1[s1], r1, L::Y1 + s1 * L::T_BYTES);
+            ok = ok && wait_warp(smem_u32(&s_s), i & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(smem_u32(&s_a));
+            if (i + 1 < n) there(s_y2[s2], r2, L::Y2 + s2 * L::T_BYTES);
+            ok = ok && wait_warp(smem_u32(&s_pp), i & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(smem_u32(&s_b));
         }
         if (!ok && lane == 0) give_up();
-    } else {
-        // ---- p and ds, a thread a row; the two groups take turns
+    } else if (warp > 3) {
+        // ---- p and ds, two threads a row
+        more_registers<REGS_SOFTMAX>();
         const int x = (warp >> 2) - 1, t = tid & 127, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + x * 128, tp = ts + SUB;
+        const uint32_t ts = tmem + lanes + TM_S + x * HALF, tp = tmem + lanes + TM_P + x * HALF;
+        grid_dep_wait();                                 // D (and what goes with it) is the kernel's before
         const float factor = F16 ? ds_factor(k.most[KEYS ? head : yh], k.most[p.Hk + (KEYS ? head : yh)]) : 1.f;
         const float ds_mul = factor * (F16 ? 0x1p-10f : 1.f);
         const float2 cc = make_float2(p.c, p.c), ff = make_float2(ds_mul, ds_mul);
-        // KEYS: thread t holds lse (t < 64) or D of query t % 64 of the group's next tile; else every thread those of its own row
-        auto row_value = [&](int i) {
-            const int y = tile(i) * SUB + (t & 63);
-            const int64_t at_row = static_cast<int64_t>(y_head(i)) * p.T + at.start + y;
-            if (y >= at.len) return 0.f;
-            return t < 64 ? P_EXP - k.lse[at_row] * 1.44269504088896340736f : -k.delta[at_row];
+        constexpr float LOG2E = 1.44269504088896340736f;
+        // KEYS: thread t fetches lse (t < 64) or D of query t % 64 of the group's columns of the next tile, a step ahead; else
+        // every thread those of its own row
+        auto row_value = [&](const Iter &i) {
+            const int y = i.tile * TILE + x * HALF + (t & 63);
+            const float *const from = (t < 64 ? k.lse : k.delta) + static_cast<int64_t>(i.head) * p.T + at.start + y;
+            float v = 0.f;
+            if (y < at.len) v = *from;
+            return v;
         };
-        float next = 0.f;
+        Iter it = first(), ahead = it;
+        float raw = 0.f;
         float2 l2 = make_float2(0.f, 0.f), d2 = make_float2(0.f, 0.f);
         if (KEYS) {
-            if (x < n) next = row_value(x);
+            raw = row_value(it);
         } else if (r < rows) {
             const int64_t at_row = static_cast<int64_t>(head) * p.T + at.start + x0 + r;
-            l2.x = l2.y = P_EXP - k.lse[at_row] * 1.44269504088896340736f;
+            l2.x = l2.y = P_EXP - k.lse[at_row] * LOG2E;
             d2.x = d2.y = -k.delta[at_row];
         }
-        bool ok = true;
-        float off = 0.f;                                // (dry steps) sum of ds
-        bool corrected = false;
-        auto correct = [&](bool ok) {                    // D by what both groups have found; everyone of them comes here once
-            s_dry[x][r] = off * (F16 ? 0x1p-10f : 1.f);
-            if (bar_or(3, 256, !ok)) return false;
-            d2.x -= s_dry[0][r] + s_dry[1][r];
-            d2.y = d2.x;
-            if (x == 0 && r < rows) k.delta[static_cast<int64_t>(head) * p.T + at.start + x0 + r] = -d2.x;
-            return true;
-        };
-        for (int i = x; i < n; i += 2) {
-            if (!KEYS && i >= dry && dry > 0 && !corrected) {
+        bool ok = true, corrected = false;
+        float off = 0.f;                                 // (dry steps) sum of ds
+        float *const s_dry = reinterpret_cast<float *>(s_row);
+        for (int i = 0; i < n; ++i, advance(it)) {
+            if (!KEYS && dry > 0 && i == dry) {          // D by what both threads of the row have found
                 corrected = true;
-                ok = correct(true);
-                if (!ok) break;
+                s_dry[x * TILE + r] = off * (F16 ? 0x1p-10f : 1.f);
+                bar_or(3, 256, false);
+                d2.x -= s_dry[r] + s_dry[TILE + r];
+                d2.y = d2.x;
+                if (x == 0 && r < rows) k.delta[static_cast<int64_t>(head) * p.T + at.start + x0 + r] = -d2.x;
             }
-            const int turn = (i >> 1) & 1;
-            if (KEYS) reinterpret_cast<float *>(s_row[x][turn])[(t & 63) / 4 * 8 + (t >> 6) * 4 + (t & 3)] = next;
-            ok = wait_warp(smem_u32(&s_s[x]), turn);
+            const bool all = whole(it);
+            int a = 0, b = TILE - 1;
+            if (!all) visible(it, r, a, b);
+            a = max(a - x * HALF, 0);
+            b = min(b - x * HALF, HALF - 1);
+            const unsigned len = b >= a ? b - a + 1 : 0;
+            if (KEYS) reinterpret_cast<float *>(s_row[x])[(t & 63) / 4 * 8 + (t >> 6) * 4 + (t & 3)] = t < 64 ? fmaf(-raw, LOG2E, P_EXP) : -raw;
+            ok = wait_warp(smem_u32(&s_s), i & 1);
             if (KEYS) ok = !bar_or(1 + x, 128, !ok);
             if (!ok) break;
-            if (KEYS && i + 2 < n) next = row_value(i + 2);
             fence_after();
-            int a = 0, b = SUB - 1;
-            const bool all = whole(i);
-            if (!all) visible(i, r, a, b);
-            const unsigned len = b >= a ? b - a + 1 : 0;
-            if (!KEYS && i < dry) {
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t s[32], q[32];
-                    tmem_ld32_nowait(ts + c * 32, s);
-                    tmem_ld32_nowait(tp + c * 32, q);
-                    tmem_wait_ld();
-                    reg_fence32(s);
-                    reg_fence32(q);
+            uint32_t u[2][32];
+            tmem_ld32_nowait(ts, u[0]);
+            tmem_ld32_nowait(ts + 32, u[1]);
+            tmem_wait_ld();
+            reg_fence32(u[0]);
+            reg_fence32(u[1]);
+            if (KEYS) {
+                if (i + 1 < n) {
+                    advance(ahead);
+                    raw = row_value(ahead);
+                }
+            } else {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_a));
+            }
+            float2 pr[HALF / 2];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (static_cast<unsigned>(c * 32 + e - a) < len)
-                            off = fmaf(ex2_ftz(fmaf(__uint_as_float(s[e]), p.c, l2.x)), __uint_as_float(q[e]) + d2.x, off);
+            for (int j = 0; j < HALF; j += 4) {
+                float4 l4 = make_float4(l2.x, l2.y, l2.x, l2.y);
+                if (KEYS) l4 = s_row[x][j / 4][0];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = j + 2 * h;
+                    float2 v = fma2(make_float2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])), cc,
+                                    h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                    v.x = ex2_ftz(v.x);
+                    v.y = ex2_ftz(v.y);
+                    pr[e / 2] = v;
+                }
+            }
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < HALF; ++e)
+                    if (static_cast<unsigned>(e - a) >= len) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+            }
+            if (KEYS) {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < HALF / 2; ++e) w[e] = Pair<E>::pack(pr[e].x, pr[e].y);
+                tmem_st32_nowait(ts, w);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_a));
+            }
+            ok = wait_warp(smem_u32(&s_pp), i & 1);
+            if (ok) {
+                fence_after();
+                tmem_ld32_nowait(tp, u[0]);
+                tmem_ld32_nowait(tp + 32, u[1]);
+                tmem_wait_ld();
+                reg_fence32(u[0]);
+                reg_fence32(u[1]);
+                if (!KEYS && i < dry) {
+#pragma unroll
+                    for (int e = 0; e < HALF; ++e)
+                        if (static_cast<unsigned>(e - a) < len)
+                            off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
+                } else {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < HALF; j += 4) {
+                        float4 d4 = make_float4(d2.x, d2.y, d2.x, d2.y);
+                        if (KEYS) d4 = s_row[x][j / 4][1];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int e = j + 2 * h;
+                            float2 v = add2(make_float2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])),
+                                            h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
+                            if (F16) v = mul2(v, ff);
+                            v = mul2(v, pr[e / 2]);
+                            if (!all) {
+                                if (static_cast<unsigned>(e - a) >= len) v.x = 0.f;
+                                if (static_cast<unsigned>(e + 1 - a) >= len) v.y = 0.f;
+                            }
+                            w[e / 2] = Pair<E>::pack(v.x, v.y);
+                        }
+                    }
+                    tmem_st32_nowait(tp, w);
+                    tmem_wait_st();
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
-                continue;
+                if (lane == 0) mbar_arrive(smem_u32(&s_b));
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t s[32], q[32];
-                tmem_ld32_nowait(ts + c * 32, s);
-                tmem_ld32_nowait(tp + c * 32, q);
-                tmem_wait_ld();
-                reg_fence32(s);
-                reg_fence32(q);
-                uint32_t ep[16], es[16];
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    float2 lj[2] = {l2, l2}, dj[2] = {d2, d2};
-                    if (KEYS) {
-                        const float4 l4 = s_row[x][turn][c * 8 + j / 4][0], d4 = s_row[x][turn][c * 8 + j / 4][1];
-                        lj[0] = make_float2(l4.x, l4.y), lj[1] = make_float2(l4.z, l4.w);
-                        dj[0] = make_float2(d4.x, d4.y), dj[1] = make_float2(d4.z, d4.w);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int e = j + 2 * h;
-                        float2 v = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, lj[h]);
-                        v.x = ex2_ftz(v.x);
-                        v.y = ex2_ftz(v.y);
-                        float2 w = add2(make_float2(__uint_as_float(q[e]), __uint_as_float(q[e + 1])), dj[h]);
-                        if (F16) w = mul2(w, ff);
-                        w = mul2(w, v);
-                        if (!all) {
-                            if (static_cast<unsigned>(c * 32 + e - a) >= len) v.x = w.x = 0.f;
-                            if (static_cast<unsigned>(c * 32 + e + 1 - a) >= len) v.y = w.y = 0.f;
-                        }
-                        if (KEYS) ep[e / 2] = Pair<E>::pack(v.x, v.y);
-                        es[e / 2] = Pair<E>::pack(w.x, w.y);
-                    }
-                }
-                if (KEYS) tmem_st16_nowait(ts + c * 16, ep);
-                tmem_st16_nowait(tp + c * 16, es);
-            }
-            tmem_wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
+            if (KEYS) ok = !bar_or(1 + x, 128, !ok);     // the queries' values have been read
+            if (!ok) break;
         }
-        if (!KEYS && dry > 0 && !corrected && !correct(ok)) ok = false;      // a wait gave up in the dry steps, or no step of this group's follows
+        if (!KEYS && dry > 0 && !corrected) bar_or(3, 256, true);       // a wait gave up: whoever waits for this warp goes on
         if (ok) ok = wait_warp(smem_u32(&s_end), 0);
         if (!ok && lane == 0) give_up();
-        // ---- the sums: the first group writes dk or dq, the second dv; rounded once, rows by way of shared memory (the own rows are
-        // no longer needed), the sinks' in fp32 into the workspace
-        if (ok && (KEYS || x == 0)) {
+        // ---- the sums: keys: the first group writes dk, the second dv; queries: half of dq's columns each.  Rounded once, rows by way of
+        // shared memory (the own rows are no longer needed), the sinks' in fp32 into the workspace
+        if (ok) {
+            constexpr int COLS = KEYS ? D : D / 2, CH = COLS / 8, RPI = 32 / CH, SWZ = CH < 8 ? CH - 1 : 7;
             fence_after();
-            const float mul = x == 0 ? p.scale / factor : F16 ? 0x1p-10f : 1.f;
-            unsigned char *const stage = basep + L::X + x * L::X_BYTES;
+            const float mul = KEYS && x == 1 ? (F16 ? 0x1p-10f : 1.f) : p.scale / factor;
+            unsigned char *const stage = basep + L::X + x * L::T_BYTES;
             const int keep = KEYS && has_sinks && x0 == 0 ? min(p.S, rows) : 0;      // rows that go into the workspace
             float *const part = sinks ? k.rest + ((static_cast<int64_t>(slot) * p.Hk + head) * 2 + x) * p.S * D
                                       : k.first + ((static_cast<int64_t>(at.seq) * p.Hk + head) * 2 + x) * p.S * D;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < COLS / 32; ++c) {
                 uint32_t v[32];
-                tmem_ld32_nowait(tmem + lanes + TM_ACC + x * D + c * 32, v);
+                tmem_ld32_nowait(tmem + lanes + TM_ACC + x * COLS + c * 32, v);
                 tmem_wait_ld();
                 reg_fence32(v);
                 float f[32];
@@ -408,20 +490,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     y.y = Pair<E>::pack(f[8 * q + 2], f[8 * q + 3]);
                     y.z = Pair<E>::pack(f[8 * q + 4], f[8 * q + 5]);
                     y.w = Pair<E>::pack(f[8 * q + 6], f[8 * q + 7]);
-                    *reinterpret_cast<uint4 *>(stage + r * (2 * D) + (((c * 4 + q) ^ (r & 7)) << 4)) = y;
+                    *reinterpret_cast<uint4 *>(stage + r * (2 * COLS) + (((c * 4 + q) ^ (r & SWZ)) << 4)) = y;
                 }
             }
             __syncwarp();
             if (!sinks) {
-                constexpr int CH = D / 8, RPI = 32 / CH;
                 const int ch = lane % CH;
-                const int64_t ld = x == 0 ? ld1 : ld2;
-                E *const dst = (x == 0 ? out1 : out2) + (static_cast<int64_t>(at.start) + x0) * ld + head * D + ch * 8;
-#pragma unroll 4
+                const int64_t ld = KEYS && x == 1 ? ld2 : ld1;
+                E *const dst = (KEYS && x == 1 ? out2 : out1) + (static_cast<int64_t>(at.start) + x0) * ld + head * D + (KEYS ? 0 : x * COLS) + ch * 8;
+#pragma unroll
                 for (int j = 0; j < 32; j += RPI) {
                     const int row = (warp & 3) * 32 + j + lane / CH;
                     if (row >= keep && row < rows)
-                        *reinterpret_cast<uint4 *>(dst + row * ld) = *reinterpret_cast<const uint4 *>(stage + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+                        *reinterpret_cast<uint4 *>(dst + row * ld) = *reinterpret_cast<const uint4 *>(stage + row * (2 * COLS) + ((ch ^ (row & SWZ)) << 4));
                 }
             }
         }
@@ -429,10 +510,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_before();
     __syncthreads();
     fence_after();
+    grid_dep_launch();
     if (warp == 0) {
         if (s_abort && lane == 0) {     // the copies in flight end before the memory is given back
             mbar_wait(smem_u32(&s_x), 0);
-            for (int i = 0; i < STAGES && i < fetched; ++i) mbar_wait(smem_u32(&s_full[i]), ((fetched - 1 - i) / STAGES) & 1);
+            for (int i = 0; i < L::N1 && i < fetched[0]; ++i) mbar_wait(smem_u32(&s_y1[i]), ((fetched[0] - 1 - i) / L::N1) & 1);
+            for (int i = 0; i < L::N2 && i < fetched[1]; ++i) mbar_wait(smem_u32(&s_y2[i]), ((fetched[1] - 1 - i) / L::N2) & 1);
         }
         __syncwarp();
         tmem_dealloc(tmem, TM_COLS);
@@ -476,23 +559,27 @@ __global__ void __launch_bounds__(256) window_delta(const Shape p, const E *o, i
             }
         }
     }
+    grid_dep_launch();
 }
 
 // The sinks' rows of dk and dv: the window's part and the pieces', in order.
 template <typename E>
-__global__ void __launch_bounds__(256) window_sinks(const Shape p, const Back k, int D, E *dk, int64_t lddk, E *dv, int64_t lddv)
+__global__ void __launch_bounds__(128) window_sinks(const Shape p, const Back k, int D, E *dk, int64_t lddk, E *dv, int64_t lddv)
 {
+    grid_dep_wait();
     if (!plan_matches(p.plan, p.sig)) return;
     const int32_t *cu = p.plan + p.off_cu;
     const int seq = blockIdx.x / p.Hk, head = blockIdx.x % p.Hk, start = cu[seq], len = cu[seq + 1] - start;
     if (len <= p.W) return;
     const int keep = min(p.S, len), slot0 = start / CHUNK + seq;
-    const int64_t size = static_cast<int64_t>(p.S) * D;
-    for (int i = threadIdx.x; i < 2 * keep * D; i += blockDim.x) {
+    const int64_t size = static_cast<int64_t>(p.S) * D, step = static_cast<int64_t>(p.Hk) * 2 * size;
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < 2 * keep * D; i += gridDim.y * blockDim.x) {
         const int x = i / (keep * D), e = i - x * keep * D;
         float sum = k.first[((static_cast<int64_t>(seq) * p.Hk + head) * 2 + x) * size + e];
-        for (int c = p.W / CHUNK; c <= (len - 1) / CHUNK; ++c)
-            sum += k.rest[((static_cast<int64_t>(slot0 + c) * p.Hk + head) * 2 + x) * size + e];
+        const float *const rest = k.rest + ((static_cast<int64_t>(slot0) * p.Hk + head) * 2 + x) * size + e;
+        const int last = (len - 1) / CHUNK;
+#pragma unroll 8
+        for (int c = p.W / CHUNK; c <= last; ++c) sum += rest[c * step];
         E *const to = x == 0 ? dk + (static_cast<int64_t>(start) + e / D) * lddk : dv + (static_cast<int64_t>(start) + e / D) * lddv;
         to[head * D + e % D] = from_f32<E>(sum);
     }
@@ -525,14 +612,10 @@ cudaError_t backward(const Shape &p, const WindowIn &in, const WindowGrads &g, v
     if (slots * p.H > INT32_MAX || slots * p.Hk + pieces > INT32_MAX || static_cast<int64_t>(p.N) * p.Hk > INT32_MAX)
         return cudaErrorInvalidConfiguration;
     k.window_blocks = static_cast<int>(slots * p.Hk);
-    CUtensorMap m[8];      // queries, do, keys, values: tiles of 128 rows, then of 64
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t rows = i ? SUB : TILE;
-        if (!encode_heads(&m[4 * i], in.q, bf16, D, p.H, p.T, in.ldq, rows) || !encode_heads(&m[4 * i + 1], g.d_o, bf16, D, p.H, p.T, g.lddo, rows) ||
-            !encode_heads(&m[4 * i + 2], in.k, bf16, D, p.Hk, p.T, in.ldk, rows) ||
-            !encode_heads(&m[4 * i + 3], in.v, bf16, D, p.Hk, p.T, in.ldv, rows))
-            return cudaErrorInvalidValue;
-    }
+    CUtensorMap mq, mdo, mk, mv;
+    if (!encode_heads(&mq, in.q, bf16, D, p.H, p.T, in.ldq, TILE) || !encode_heads(&mdo, g.d_o, bf16, D, p.H, p.T, g.lddo, TILE) ||
+        !encode_heads(&mk, in.k, bf16, D, p.Hk, p.T, in.ldk, TILE) || !encode_heads(&mv, in.v, bf16, D, p.Hk, p.T, in.ldv, TILE))
+        return cudaErrorInvalidValue;
     cudaError_t e;
     if (!bf16 && (e = cudaMemsetAsync(k.most, 0, static_cast<size_t>(2) * p.Hk * 4, stream)) != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.T) * (p.H + (bf16 ? 0 : p.Hk)) * (D / 8);
@@ -542,14 +625,16 @@ cudaError_t backward(const Shape &p, const WindowIn &in, const WindowGrads &g, v
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const void *fk = reinterpret_cast<const void *>(&window_back<E, D, true>), *fq = reinterpret_cast<const void *>(&window_back<E, D, false>);
     if ((e = set_dynamic_smem(fk, Smem<D>::ALLOC)) != cudaSuccess || (e = set_dynamic_smem(fq, Smem<D>::ALLOC)) != cudaSuccess) return e;
-    window_back<E, D, false><<<static_cast<int>(slots * p.H), THREADS, Smem<D>::ALLOC, stream>>>(
-        m[0], m[1], m[6], m[7], p, k, static_cast<E *>(g.dq), g.lddq, nullptr, 0);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    window_back<E, D, true><<<static_cast<int>(slots * p.Hk + pieces), THREADS, Smem<D>::ALLOC, stream>>>(
-        m[2], m[3], m[4], m[5], p, k, static_cast<E *>(g.dk), g.lddk, static_cast<E *>(g.dv), g.lddv);
-    if ((e = cudaGetLastError()) != cudaSuccess || !sinks) return e;
-    window_sinks<E><<<p.N * p.Hk, 256, 0, stream>>>(p, k, D, static_cast<E *>(g.dk), g.lddk, static_cast<E *>(g.dv), g.lddv);
-    return cudaGetLastError();
+    // each of the others begins while the last CTAs of the one before it end
+    e = launch_dependent(window_back<E, D, false>, dim3(static_cast<unsigned>(slots * p.H)), dim3(THREADS), Smem<D>::ALLOC, stream, mq, mdo, mk, mv, p, k,
+                         static_cast<E *>(g.dq), g.lddq, static_cast<E *>(nullptr), static_cast<int64_t>(0));
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(window_back<E, D, true>, dim3(static_cast<unsigned>(slots * p.Hk + pieces)), dim3(THREADS), Smem<D>::ALLOC, stream, mk, mv, mq,
+                         mdo, p, k, static_cast<E *>(g.dk), g.lddk, static_cast<E *>(g.dv), g.lddv);
+    if (e != cudaSuccess || !sinks) return e;
+    const unsigned share = static_cast<unsigned>(min(16, (2 * p.S * D + 127) / 128));      // blocks of a sequence and head
+    return launch_dependent(window_sinks<E>, dim3(p.N * p.Hk, share), dim3(128), 0, stream, p, k, D, static_cast<E *>(g.dk), g.lddk,
+                            static_cast<E *>(g.dv), g.lddv);
 }
 
 }  // namespace
