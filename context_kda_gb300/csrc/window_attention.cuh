@@ -119,7 +119,6 @@ __device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint32_t b, u
                  "r"(a), "r"(b), "n"(DESC_HI), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)));
 }
 
-// A bounded wait of a whole warp, the same answer in every lane.  One lane polls; the clock is read only where the first look fails.
 __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -130,11 +129,15 @@ __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 __device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity) { return look(bar, parity) || mbar_wait(bar, parity); }
+// A bounded wait of a whole warp, the same answer in every lane; the clock is read only where the first look fails.  All lanes
+// look: a branch to one lane and back costs more than the look itself.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity)
 {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = wait_thread(bar, parity);
-    return __all_sync(0xffffffffu, ok);
+    if (__all_sync(0xffffffffu, look(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, look(bar, parity)))
+        if (__any_sync(0xffffffffu, clock64() - t0 > 4000000000LL)) return false;
+    return true;
 }
 
 // The sequence and tile of slot 'slot'.  Sequence n has its tiles of 'rows' tokens from slot cu[n] / rows + n on, which

@@ -42,8 +42,8 @@ constexpr int CHUNK = 1024;               // queries of a piece of the sinks' wo
 template <int D> struct Smem {
     static constexpr uint32_t T_BYTES = D / 64 * BOX;
     static constexpr int N1 = 3, N2 = 2;      // stages of Y1 (read first and last in a round) and of Y2
-    static constexpr uint32_t X = 0, Y1 = 2 * T_BYTES, Y2 = Y1 + N1 * T_BYTES, BYTES = Y2 + N2 * T_BYTES, ALLOC = BYTES + 1024;
-    static_assert(ALLOC + 2048 <= 227 * 1024, "shared memory");      // with the static part
+    static constexpr uint32_t X = 0, Y1 = 2 * T_BYTES, Y2 = Y1 + N1 * T_BYTES, BYTES = Y2 + N2 * T_BYTES;
+    static_assert(BYTES + 3072 <= 227 * 1024, "shared memory");      // with the static part
 };
 // TMEM columns: S (p), P' (ds), the sums
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_ACC = 256, TM_COLS = 512;
@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     using L = Smem<D>;
     constexpr bool F16 = !Pair<E>::BF16;
     constexpr float P_EXP = F16 ? 10.f : 0.f;            // p is kept times 2^P_EXP
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_x, s_y1[L::N1], s_free1[L::N1], s_y2[L::N2], s_free2[L::N2], s_go, s_s, s_pp, s_a, s_b, s_end;
-    __shared__ float4 s_row[2][HALF / 4][2];             // KEYS: the queries' lse and D, by group of warps; else: sums of ds
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint64_t s_x, s_y1[L::N1], s_free1[L::N1], s_y2[L::N2], s_free2[L::N2], s_go, s_s, s_pp, s_a, s_b, s_rows[2], s_end;
+    __shared__ float4 s_row[2][TILE / 4][2];             // KEYS: four queries' lse, then D, of two tiles; else: sums of ds
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -156,8 +156,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     };
 
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    unsigned char *const basep = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t base = smem_u32(smem);
+    unsigned char *const basep = smem;
+    if (base & 1023u) {                                  // the swizzle counts from there
+        if (tid == 0) record_status(&g_window_back_status, KDA_ERR_UNSUPPORTED);
+        return;
+    }
     int fetched[2] = {0, 0};                             // (the fetching thread) tiles of Y1 and of Y2
     auto load = [&](const CUtensorMap &m, uint32_t dst, int h, int row, uint32_t bar) {
         for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BOX, &m, c * 64, h, at.start + row, bar);
@@ -175,6 +179,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(smem_u32(&s_pp), 1);
         mbar_init(smem_u32(&s_a), 9);
         mbar_init(smem_u32(&s_b), 9);
+        mbar_init(smem_u32(&s_rows[0]), 1);
+        mbar_init(smem_u32(&s_rows[1]), 1);
         mbar_init(smem_u32(&s_end), 1);
         s_abort = 0;
         // the first tiles are on their way before anything else
@@ -315,34 +321,48 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(smem_u32(&s_b));
         }
         if (!ok && lane == 0) give_up();
+    } else if (warp == 3 && KEYS) {
+        // ---- the queries' lse and D, a tile ahead
+        grid_dep_wait();
+        bool ok = true;
+        Iter it = first();
+        for (int i = 0; i < n; ++i, advance(it)) {
+            float v[2][TILE / 32];
+#pragma unroll
+            for (int j = 0; j < TILE / 32; ++j) {
+                const int y = it.tile * TILE + j * 32 + lane;
+                const int64_t row = static_cast<int64_t>(it.head) * p.T + at.start + y;
+                v[0][j] = v[1][j] = 0.f;
+                if (y < at.len) v[0][j] = k.lse[row], v[1][j] = k.delta[row];
+            }
+            // the tile before last has been read by all
+            if (i > 1) ok = wait_warp(smem_u32(&s_b), i & 1);
+            if (!ok) break;
+            float *const to = reinterpret_cast<float *>(s_row[i & 1]) + lane / 4 * 8 + (lane & 3);
+#pragma unroll
+            for (int j = 0; j < TILE / 32; ++j) {
+                to[j * 64] = fmaf(-v[0][j], 1.44269504088896340736f, P_EXP);
+                to[j * 64 + 4] = -v[1][j];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_rows[i & 1]));
+        }
+        if (!ok && lane == 0) give_up();
     } else if (warp > 3) {
         // ---- p and ds, two threads a row
         more_registers<REGS_SOFTMAX>();
-        const int x = (warp >> 2) - 1, t = tid & 127, r = (warp & 3) * 32 + lane;
+        const int x = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + TM_S + x * HALF, tp = tmem + lanes + TM_P + x * HALF;
         grid_dep_wait();                                 // D (and what goes with it) is the kernel's before
         const float factor = F16 ? ds_factor(k.most[KEYS ? head : yh], k.most[p.Hk + (KEYS ? head : yh)]) : 1.f;
         const float ds_mul = factor * (F16 ? 0x1p-10f : 1.f);
         const float2 cc = make_float2(p.c, p.c), ff = make_float2(ds_mul, ds_mul);
-        constexpr float LOG2E = 1.44269504088896340736f;
-        // KEYS: thread t fetches lse (t < 64) or D of query t % 64 of the group's columns of the next tile, a step ahead; else
-        // every thread those of its own row
-        auto row_value = [&](const Iter &i) {
-            const int y = i.tile * TILE + x * HALF + (t & 63);
-            const float *const from = (t < 64 ? k.lse : k.delta) + static_cast<int64_t>(i.head) * p.T + at.start + y;
-            float v = 0.f;
-            if (y < at.len) v = *from;
-            return v;
-        };
-        Iter it = first(), ahead = it;
-        float raw = 0.f;
-        float2 l2 = make_float2(0.f, 0.f), d2 = make_float2(0.f, 0.f);
-        if (KEYS) {
-            raw = row_value(it);
-        } else if (r < rows) {
+        Iter it = first();
+        float2 l2 = make_float2(0.f, 0.f), d2 = make_float2(0.f, 0.f);      // queries: of the thread's own row
+        if (!KEYS && r < rows) {
             const int64_t at_row = static_cast<int64_t>(head) * p.T + at.start + x0 + r;
-            l2.x = l2.y = P_EXP - k.lse[at_row] * LOG2E;
+            l2.x = l2.y = P_EXP - k.lse[at_row] * 1.44269504088896340736f;
             d2.x = d2.y = -k.delta[at_row];
         }
         bool ok = true, corrected = false;
@@ -363,10 +383,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             a = max(a - x * HALF, 0);
             b = min(b - x * HALF, HALF - 1);
             const unsigned len = b >= a ? b - a + 1 : 0;
-            if (KEYS) reinterpret_cast<float *>(s_row[x])[(t & 63) / 4 * 8 + (t >> 6) * 4 + (t & 3)] = t < 64 ? fmaf(-raw, LOG2E, P_EXP) : -raw;
-            ok = wait_warp(smem_u32(&s_s), i & 1);
-            if (KEYS) ok = !bar_or(1 + x, 128, !ok);
+            ok = (!KEYS || wait_warp(smem_u32(&s_rows[i & 1]), i >> 1 & 1)) && wait_warp(smem_u32(&s_s), i & 1);
             if (!ok) break;
+            const float4 (*const row)[2] = s_row[i & 1] + x * (HALF / 4);
             fence_after();
             uint32_t u[2][32];
             tmem_ld32_nowait(ts, u[0]);
@@ -374,12 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_wait_ld();
             reg_fence32(u[0]);
             reg_fence32(u[1]);
-            if (KEYS) {
-                if (i + 1 < n) {
-                    advance(ahead);
-                    raw = row_value(ahead);
-                }
-            } else {
+            if (!KEYS) {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_a));
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < HALF; j += 4) {
                 float4 l4 = make_float4(l2.x, l2.y, l2.x, l2.y);
-                if (KEYS) l4 = s_row[x][j / 4][0];
+                if (KEYS) l4 = row[j / 4][0];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int e = j + 2 * h;
@@ -415,47 +429,44 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&s_a));
             }
             ok = wait_warp(smem_u32(&s_pp), i & 1);
-            if (ok) {
-                fence_after();
-                tmem_ld32_nowait(tp, u[0]);
-                tmem_ld32_nowait(tp + 32, u[1]);
-                tmem_wait_ld();
-                reg_fence32(u[0]);
-                reg_fence32(u[1]);
-                if (!KEYS && i < dry) {
-#pragma unroll
-                    for (int e = 0; e < HALF; ++e)
-                        if (static_cast<unsigned>(e - a) < len)
-                            off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
-                } else {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int j = 0; j < HALF; j += 4) {
-                        float4 d4 = make_float4(d2.x, d2.y, d2.x, d2.y);
-                        if (KEYS) d4 = s_row[x][j / 4][1];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int e = j + 2 * h;
-                            float2 v = add2(make_float2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])),
-                                            h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
-                            if (F16) v = mul2(v, ff);
-                            v = mul2(v, pr[e / 2]);
-                            if (!all) {
-                                if (static_cast<unsigned>(e - a) >= len) v.x = 0.f;
-                                if (static_cast<unsigned>(e + 1 - a) >= len) v.y = 0.f;
-                            }
-                            w[e / 2] = Pair<E>::pack(v.x, v.y);
-                        }
-                    }
-                    tmem_st32_nowait(tp, w);
-                    tmem_wait_st();
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s_b));
-            }
-            if (KEYS) ok = !bar_or(1 + x, 128, !ok);     // the queries' values have been read
             if (!ok) break;
+            fence_after();
+            tmem_ld32_nowait(tp, u[0]);
+            tmem_ld32_nowait(tp + 32, u[1]);
+            tmem_wait_ld();
+            reg_fence32(u[0]);
+            reg_fence32(u[1]);
+            if (!KEYS && i < dry) {
+#pragma unroll
+                for (int e = 0; e < HALF; ++e)
+                    if (static_cast<unsigned>(e - a) < len)
+                        off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
+            } else {
+                uint32_t w[32];
+#pragma unroll
+                for (int j = 0; j < HALF; j += 4) {
+                    float4 d4 = make_float4(d2.x, d2.y, d2.x, d2.y);
+                    if (KEYS) d4 = row[j / 4][1];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = j + 2 * h;
+                        float2 v = add2(make_float2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])),
+                                        h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
+                        if (F16) v = mul2(v, ff);
+                        v = mul2(v, pr[e / 2]);
+                        if (!all) {
+                            if (static_cast<unsigned>(e - a) >= len) v.x = 0.f;
+                            if (static_cast<unsigned>(e + 1 - a) >= len) v.y = 0.f;
+                        }
+                        w[e / 2] = Pair<E>::pack(v.x, v.y);
+                    }
+                }
+                tmem_st32_nowait(tp, w);
+                tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_b));
         }
         if (!KEYS && dry > 0 && !corrected) bar_or(3, 256, true);       // a wait gave up: whoever waits for this warp goes on
         if (ok) ok = wait_warp(smem_u32(&s_end), 0);
@@ -624,12 +635,12 @@ cudaError_t backward(const Shape &p, const WindowIn &in, const WindowGrads &g, v
                                                  static_cast<const E *>(in.v), in.ldv, k);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const void *fk = reinterpret_cast<const void *>(&window_back<E, D, true>), *fq = reinterpret_cast<const void *>(&window_back<E, D, false>);
-    if ((e = set_dynamic_smem(fk, Smem<D>::ALLOC)) != cudaSuccess || (e = set_dynamic_smem(fq, Smem<D>::ALLOC)) != cudaSuccess) return e;
+    if ((e = set_dynamic_smem(fk, Smem<D>::BYTES)) != cudaSuccess || (e = set_dynamic_smem(fq, Smem<D>::BYTES)) != cudaSuccess) return e;
     // each of the others begins while the last CTAs of the one before it end
-    e = launch_dependent(window_back<E, D, false>, dim3(static_cast<unsigned>(slots * p.H)), dim3(THREADS), Smem<D>::ALLOC, stream, mq, mdo, mk, mv, p, k,
+    e = launch_dependent(window_back<E, D, false>, dim3(static_cast<unsigned>(slots * p.H)), dim3(THREADS), Smem<D>::BYTES, stream, mq, mdo, mk, mv, p, k,
                          static_cast<E *>(g.dq), g.lddq, static_cast<E *>(nullptr), static_cast<int64_t>(0));
     if (e != cudaSuccess) return e;
-    e = launch_dependent(window_back<E, D, true>, dim3(static_cast<unsigned>(slots * p.Hk + pieces)), dim3(THREADS), Smem<D>::ALLOC, stream, mk, mv, mq,
+    e = launch_dependent(window_back<E, D, true>, dim3(static_cast<unsigned>(slots * p.Hk + pieces)), dim3(THREADS), Smem<D>::BYTES, stream, mk, mv, mq,
                          mdo, p, k, static_cast<E *>(g.dk), g.lddk, static_cast<E *>(g.dv), g.lddv);
     if (e != cudaSuccess || !sinks) return e;
     const unsigned share = static_cast<unsigned>(min(16, (2 * p.S * D + 127) / 128));      // blocks of a sequence and head
