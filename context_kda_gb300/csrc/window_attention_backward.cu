@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (!all) {
+                __syncwarp();      // (a branch: without it every tile would pay for the selections)
 #pragma unroll
                 for (int e = 0; e < HALF; ++e)
                     if (static_cast<unsigned>(e - a) >= len) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (static_cast<unsigned>(e - a) < len)
                         off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
             } else {
-                uint32_t w[32];
+                float2 ds[HALF / 2];
 #pragma unroll
                 for (int j = 0; j < HALF; j += 4) {
                     float4 d4 = make_float4(d2.x, d2.y, d2.x, d2.y);
@@ -453,14 +454,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                         float2 v = add2(make_float2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])),
                                         h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
                         if (F16) v = mul2(v, ff);
-                        v = mul2(v, pr[e / 2]);
-                        if (!all) {
-                            if (static_cast<unsigned>(e - a) >= len) v.x = 0.f;
-                            if (static_cast<unsigned>(e + 1 - a) >= len) v.y = 0.f;
-                        }
-                        w[e / 2] = Pair<E>::pack(v.x, v.y);
+                        ds[e / 2] = mul2(v, pr[e / 2]);
                     }
                 }
+                if (!all) {
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < HALF; ++e)
+                        if (static_cast<unsigned>(e - a) >= len) (e & 1 ? ds[e / 2].y : ds[e / 2].x) = 0.f;
+                }
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < HALF / 2; ++e) w[e] = Pair<E>::pack(ds[e].x, ds[e].y);
                 tmem_st32_nowait(tp, w);
                 tmem_wait_st();
             }
