@@ -719,6 +719,7 @@ int head_in_ok(const kda::HeadIn &a, int32_t type, int32_t pairs, bool x)
     if ((a.norm != 0 && a.norm != 1) || (pairs != KDA_PAIRS_HALVES && pairs != KDA_PAIRS_ADJACENT)) return KDA_ERR_INVALID_ARG;
     if (a.d != 32 && a.d != 64 && a.d != 128 && a.d != 256) return KDA_ERR_UNSUPPORTED;
     if (a.rot > a.d || a.rot % 16) return KDA_ERR_UNSUPPORTED;
+    if (a.H > INT32_MAX / a.d || a.Hk > INT32_MAX / a.d) return KDA_ERR_UNSUPPORTED;     // a row's channels are counted in 32 bits
     if (a.norm ? !(a.eps >= 0.f) : (a.w_q || a.w_k)) return KDA_ERR_INVALID_ARG;
     if (!floats_ok_or_null(a.w_q) || !floats_ok_or_null(a.w_k) || (!a.Hk && a.w_k)) return KDA_ERR_INVALID_ARG;
     if (a.T == 0) return KDA_OK;   // no rows: their addresses do not matter

@@ -24,7 +24,7 @@ __device__ int g_cache_status;
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int ROWS = 16;                  // of a warp's step
 constexpr int MAX_SPLIT = 8;              // CTAs of a cluster
-constexpr int STAGES = 3;                 // of a lane's queue, 16 rows each: two CTAs an SM have 128 KiB on their way
+constexpr int STAGES = 2;                 // of a lane's queue, 16 rows each: three CTAs an SM have up to 192 KiB on their way
 
 template <int D> constexpr int PIECES = D / 8;                                   // 16-byte pieces of a lane in 16 rows of keys and values
 template <int D> constexpr uint32_t QUEUE = STAGES * PIECES<D> * 512;            // of a warp
@@ -91,7 +91,7 @@ struct Step {
 
 // HG: query heads worked together, 8 or 16 (the product's M).
 template <typename E, int D, int HG>
-__global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache_k, E *cache_v, E *o)
+__global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache_k, E *cache_v, E *o)
 {
     constexpr int KC = D / 32, VC = D / 64;       // 16-byte pieces of a lane: of a row of keys, of a row of values
     extern __shared__ __align__(16) unsigned char smem[];
@@ -299,9 +299,10 @@ cudaError_t step(Step p, void *cache_k, void *cache_v, void *o, cudaStream_t str
     const StepIn &in = p.in;
     p.blocks = (p.g + HG - 1) / HG;
     const int64_t units = static_cast<int64_t>(in.B) * in.Hk * p.blocks;
-    // enough CTAs for every SM, but none with fewer than 64 rows of a full cache (its way in and out would take longer)
+    // two rounds of CTAs and more, since lengths differ, but none with fewer than 64 rows of a full cache (its way in and out would
+    // take longer): 64 tokens x 8 key heads over up to 4100 rows 168 us, with one round 174 us
     p.split = 1;
-    while (p.split < MAX_SPLIT && units * p.split < 4 * sm_count() && (in.W + in.S) / (2 * p.split) >= 64) p.split *= 2;
+    while (p.split < MAX_SPLIT && units * p.split < 6 * sm_count() && (in.W + in.S) / (2 * p.split) >= 64) p.split *= 2;
     const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(&window_step<E, D, HG>), SMEM<D, HG>);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

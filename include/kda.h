@@ -633,7 +633,7 @@ enum { KDA_PAIRS_HALVES = 0, KDA_PAIRS_ADJACENT = 1 };
  *     (a, b) -> (a cos - b sin, a sin + b cos)   for every pair of the first 'rot' channels of n,
  * the angle positions[t] times the pair's frequency.  w = d^-1/2 gives heads of unit length, as KDA's q and k.
  *   T, H, Hk, d     tokens, heads of q and of k (Hk 0: k is NULL), channels of a head: 32, 64, 128 or 256 (others:
- *                   KDA_ERR_UNSUPPORTED).
+ *                   KDA_ERR_UNSUPPORTED); heads * d < 2^31.
  *   q, k            [T][H][d], [T][Hk][d] of 'type'; token strides ldq, ldk (>= heads * d).
  *   w_q, w_k        fp32 [d] or NULL (NULL where norm is 0).
  *   positions       device int32 [T]; phases  device [rot / 2] of kda_rotary_phases; both may be NULL where rot is 0.

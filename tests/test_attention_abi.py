@@ -18,7 +18,8 @@ def test_head_norm_rotary_refusals(kda):  # noqa: F811
               dict(eps=-1.0), dict(eps=float("nan")), dict(norm=0), dict(w_q=F + 2), dict(w_k=F + 1), dict(positions=None),
               dict(positions=F + 2), dict(phases=None), dict(phases=F + 4), dict(q=None), dict(q=F + 1), dict(ldq=511), dict(k=None),
               dict(k=F + 1), dict(ldk=127), dict(Hk=0)]
-    unsupported = [dict(d=48, rot=16), dict(d=512, rot=16), dict(rot=80), dict(rot=8), dict(rot=24)]
+    unsupported = [dict(d=48, rot=16), dict(d=512, rot=16), dict(rot=80), dict(rot=8), dict(rot=24),
+                   dict(H=2 ** 25, ldq=2 ** 40, ldq_out=2 ** 40, ldgq=2 ** 40, lddq=2 ** 40)]
     _refusals(lib.kda_head_norm_rotary_forward, names, good,
               common + [dict(q_out=None), dict(q_out=F + 1), dict(ldq_out=511), dict(k_out=None), dict(ldk_out=5),
                         dict(Hk=0, k=None, w_k=None), dict(Hk=0, k=None, k_out=None)], kda.KDA_ERR_INVALID_ARG)
@@ -60,6 +61,14 @@ def test_binding_refuses_heads_that_do_not_fit(kda):  # noqa: F811
 
 
 WINDOW = "plan plan_dev H Hk d type q ldq k ldk v ldv scale window sinks".split()
+
+
+def test_heads_of_a_row_that_32_bits_still_count(kda):  # noqa: F811
+    """One head fewer than refused goes on to the next check (an output that is not there)."""
+    names = "T H Hk d type q ldq k ldk norm w_q w_k eps positions phases rot pairs q_out ldq_out k_out ldk_out stream".split()
+    good = dict(T=4, H=2 ** 25 - 1, Hk=0, d=64, type=BF16, q=F, ldq=2 ** 40, k=None, ldk=0, norm=0, w_q=None, w_k=None, eps=0.0, positions=None, phases=None,
+                rot=0, pairs=0, q_out=None, ldq_out=2 ** 40, k_out=None, ldk_out=0, stream=None)
+    assert kda._lib.kda_head_norm_rotary_forward(*(good[n] for n in names)) == kda.KDA_ERR_INVALID_ARG
 
 
 def _window_good(kda):  # noqa: F811
