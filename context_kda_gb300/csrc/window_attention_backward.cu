@@ -11,9 +11,10 @@
 //     S = X1 Y1^T, P' = X2 Y2^T             to TMEM,
 //     p, then ds                            two threads a row; both back to TMEM in the places of S and P', as A operands of
 //     A2 += p Y2 (dv), A1 += ds Y1 (dk or dq).
-// The tensor cores run A2(i), S(i+1), A1(i), P'(i+1) in turn: p(i+1) is computed during A1(i) and P'(i+1), ds(i) during A2(i) and
-// S(i+1), so one buffer each is enough and neither side waits for long.  (Tiles of 64 with two buffers fit too, but products with
-// N = 64 are bound by shared memory: 57 cycles where 32 would do.)
+// For keys the tensor cores run A2(i), S(i+1), A1(i), P'(i+1) in turn: p(i+1) is computed during A1(i) and P'(i+1), ds(i) during
+// A2(i) and S(i+1), so one buffer each is enough.  Queries have one sum and room for a second P': S(i+1), P'(i+1), A1(i), and p and ds
+// of a step are computed while the scores of the next are.  (Tiles of 64 with two buffers of everything fit too, but products
+// with N = 64 are bound by shared memory: 57 cycles where 32 would do.)
 //
 // D_i from the output carries that output's rounding.  Where a row sees many keys the rest hides it, where it sees few it would be as large as
 // the rounding of ds.  The first queries of a sequence, and all with a narrow window, go over their tiles twice: sum_j ds_ij,
@@ -46,7 +47,7 @@ template <int D> struct Smem {
     static_assert(BYTES + 3072 <= 227 * 1024, "shared memory");      // with the static part
 };
 // TMEM columns: S (p), P' (ds), the sums
-constexpr uint32_t TM_S = 0, TM_P = 128, TM_ACC = 256, TM_COLS = 512;
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_ACC = 256, TM_P2 = 384, TM_COLS = 512;      // (queries: TM_P2 for odd steps)
 
 struct Back {
     const float *lse;                     // [H][T]
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool F16 = !Pair<E>::BF16;
     constexpr float P_EXP = F16 ? 10.f : 0.f;            // p is kept times 2^P_EXP
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ uint64_t s_x, s_y1[L::N1], s_free1[L::N1], s_y2[L::N2], s_free2[L::N2], s_go, s_s, s_pp, s_a, s_b, s_rows[2], s_end;
+    __shared__ uint64_t s_x, s_y1[L::N1], s_free1[L::N1], s_y2[L::N2], s_free2[L::N2], s_go, s_s, s_pp[2], s_a, s_b[2], s_rows[2], s_rfree[2], s_end;
     __shared__ float4 s_row[2][TILE / 4][2];             // KEYS: four queries' lse, then D, of two tiles; else: sums of ds
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -176,11 +177,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < L::N2; ++i) mbar_init(smem_u32(&s_y2[i]), 1), mbar_init(smem_u32(&s_free2[i]), 1);
         mbar_init(smem_u32(&s_go), 1);
         mbar_init(smem_u32(&s_s), 1);
-        mbar_init(smem_u32(&s_pp), 1);
+        for (int i = 0; i < 2; ++i) {                    // of even and odd steps: nobody can fall a whole round behind
+            mbar_init(smem_u32(&s_pp[i]), 1);
+            mbar_init(smem_u32(&s_b[i]), KEYS ? 9 : 8);
+            mbar_init(smem_u32(&s_rows[i]), 1);
+            mbar_init(smem_u32(&s_rfree[i]), 8);
+        }
         mbar_init(smem_u32(&s_a), 9);
-        mbar_init(smem_u32(&s_b), 9);
-        mbar_init(smem_u32(&s_rows[0]), 1);
-        mbar_init(smem_u32(&s_rows[1]), 1);
         mbar_init(smem_u32(&s_end), 1);
         s_abort = 0;
         // the first tiles are on their way before anything else
@@ -257,14 +260,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok) {
             fence_after();
             scores(TM_S, base + L::X, base + L::Y1, s_s);
-            scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2, s_pp);
+            scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2, s_pp[0]);
             if (!KEYS) signal(s_free2[0]);
         }
         int c1 = 0, c2 = 0;                              // stages of step i
         for (int i = 0; i < n && ok; ++i) {
             const int d1 = c1 + 1 == L::N1 ? 0 : c1 + 1, d2 = c2 + 1 == L::N2 ? 0 : c2 + 1;
             const bool next = i + 1 < n;
-            ok = wait_warp(smem_u32(&s_a), i & 1);       // S(i) is read (and p in its place); Y1(i + 1) is there
+            const uint32_t p_now = KEYS || !(i & 1) ? TM_P : TM_P2, p_next = KEYS || (i & 1) ? TM_P : TM_P2;
+            ok = wait_warp(smem_u32(&s_a), i & 1);       // S(i) is read (keys: and p in its place); Y1(i + 1), for queries Y2(i + 1) too, is there
             if (!ok) break;
             fence_after();
             if (KEYS) {
@@ -272,15 +276,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 signal(s_free2[c2]);
             }
             if (next) scores(TM_S, base + L::X, base + L::Y1 + d1 * L::T_BYTES, s_s);
-            ok = wait_warp(smem_u32(&s_b), i & 1);       // ds in the place of P'(i); Y2(i + 1) is there
+            if (next && !KEYS) {
+                scores(p_next, base + L::X + L::T_BYTES, base + L::Y2 + d2 * L::T_BYTES, s_pp[(i + 1) & 1]);
+                signal(s_free2[d2]);
+            }
+            ok = wait_warp(smem_u32(&s_b[i & 1]), i >> 1 & 1);       // ds in the place of P'(i); keys: Y2(i + 1) is there
             if (!ok) break;
             fence_after();
-            if (i >= dry) add(TM_ACC, TM_P, base + L::Y1 + c1 * L::T_BYTES, i > dry);
+            if (i >= dry) add(TM_ACC, p_now, base + L::Y1 + c1 * L::T_BYTES, i > dry);
             signal(s_free1[c1]);
-            if (next) {
-                scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2 + d2 * L::T_BYTES, s_pp);
-                if (!KEYS) signal(s_free2[d2]);
-            }
+            if (next && KEYS) scores(TM_P, base + L::X + L::T_BYTES, base + L::Y2 + d2 * L::T_BYTES, s_pp[(i + 1) & 1]);
             c1 = d1;
             c2 = d2;
         }
@@ -310,15 +315,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (++s1 == L::N1) s1 = 0, ++r1;
             if (++s2 == L::N2) s2 = 0, ++r2;
             advance(it);
-            // (an arrival waits for the step's scores: those of the step before are complete then)
+            // (an arrival waits for the step's scores, which are issued when the arrivals of the step before are complete; queries'
+            // P'(i + 1) does not wait for s_b(i), so there is no arrival here)
             if (i + 1 < n) there(s_y1[s1], r1, L::Y1 + s1 * L::T_BYTES);
+            if (!KEYS && ok && i + 1 < n) there(s_y2[s2], r2, L::Y2 + s2 * L::T_BYTES);
             ok = ok && wait_warp(smem_u32(&s_s), i & 1);
             if (!ok) break;
             if (lane == 0) mbar_arrive(smem_u32(&s_a));
+            if (!KEYS) continue;
             if (i + 1 < n) there(s_y2[s2], r2, L::Y2 + s2 * L::T_BYTES);
-            ok = ok && wait_warp(smem_u32(&s_pp), i & 1);
+            ok = ok && wait_warp(smem_u32(&s_pp[i & 1]), i >> 1 & 1);
             if (!ok) break;
-            if (lane == 0) mbar_arrive(smem_u32(&s_b));
+            if (lane == 0) mbar_arrive(smem_u32(&s_b[i & 1]));
         }
         if (!ok && lane == 0) give_up();
     } else if (warp == 3 && KEYS) {
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (y < at.len) v[0][j] = k.lse[row], v[1][j] = k.delta[row];
             }
             // the tile before last has been read by all
-            if (i > 1) ok = wait_warp(smem_u32(&s_b), i & 1);
+            if (i > 1) ok = wait_warp(smem_u32(&s_rfree[i & 1]), (i >> 1) - 1 & 1);
             if (!ok) break;
             float *const to = reinterpret_cast<float *>(s_row[i & 1]) + lane / 4 * 8 + (lane & 3);
 #pragma unroll
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         more_registers<REGS_SOFTMAX>();
         const int x = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + TM_S + x * HALF, tp = tmem + lanes + TM_P + x * HALF;
+        const uint32_t ts = tmem + lanes + TM_S + x * HALF;
         grid_dep_wait();                                 // D (and what goes with it) is the kernel's before
         const float factor = F16 ? ds_factor(k.most[KEYS ? head : yh], k.most[p.Hk + (KEYS ? head : yh)]) : 1.f;
         const float ds_mul = factor * (F16 ? 0x1p-10f : 1.f);
@@ -380,9 +388,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool all = whole(it);
             int a = 0, b = TILE - 1;
             if (!all) visible(it, r, a, b);
-            a = max(a - x * HALF, 0);
-            b = min(b - x * HALF, HALF - 1);
-            const unsigned len = b >= a ? b - a + 1 : 0;
+            a -= x * HALF;
+            b -= x * HALF;
+            const uint32_t tp = tmem + lanes + (KEYS || !(i & 1) ? TM_P : TM_P2) + x * HALF;
             ok = (!KEYS || wait_warp(smem_u32(&s_rows[i & 1]), i >> 1 & 1)) && wait_warp(smem_u32(&s_s), i & 1);
             if (!ok) break;
             const float4 (*const row)[2] = s_row[i & 1] + x * (HALF / 4);
@@ -414,10 +422,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (!all) {
-                __syncwarp();      // (a branch: without it every tile would pay for the selections)
+                // a bound that no row of the warp meets costs nothing.  (ds is zero where p is: the other side's rows are finite
+                // behind the sequence's end)
+                if (__any_sync(0xffffffffu, a > 0)) {
 #pragma unroll
-                for (int e = 0; e < HALF; ++e)
-                    if (static_cast<unsigned>(e - a) >= len) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                    for (int e = 0; e < HALF; ++e)
+                        if (e < a) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                }
+                if (__any_sync(0xffffffffu, b < HALF - 1)) {
+#pragma unroll
+                    for (int e = 0; e < HALF; ++e)
+                        if (e > b) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                }
             }
             if (KEYS) {
                 uint32_t w[32];
@@ -429,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_a));
             }
-            ok = wait_warp(smem_u32(&s_pp), i & 1);
+            ok = wait_warp(smem_u32(&s_pp[i & 1]), i >> 1 & 1);
             if (!ok) break;
             fence_after();
             tmem_ld32_nowait(tp, u[0]);
@@ -440,8 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!KEYS && i < dry) {
 #pragma unroll
                 for (int e = 0; e < HALF; ++e)
-                    if (static_cast<unsigned>(e - a) < len)
-                        off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
+                    off = fmaf(e & 1 ? pr[e / 2].y : pr[e / 2].x, __uint_as_float(u[e / 32][e % 32]) + d2.x, off);
             } else {
                 float2 ds[HALF / 2];
 #pragma unroll
@@ -457,12 +472,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ds[e / 2] = mul2(v, pr[e / 2]);
                     }
                 }
-                if (!all) {
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < HALF; ++e)
-                        if (static_cast<unsigned>(e - a) >= len) (e & 1 ? ds[e / 2].y : ds[e / 2].x) = 0.f;
-                }
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < HALF / 2; ++e) w[e] = Pair<E>::pack(ds[e].x, ds[e].y);
@@ -471,7 +480,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_b));
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s_b[i & 1]));
+                if (KEYS) mbar_arrive(smem_u32(&s_rfree[i & 1]));
+            }
         }
         if (!KEYS && dry > 0 && !corrected) bar_or(3, 256, true);       // a wait gave up: whoever waits for this warp goes on
         if (ok) ok = wait_warp(smem_u32(&s_end), 0);
