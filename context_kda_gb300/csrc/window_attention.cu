@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) prefetch_map(mq), prefetch_map(mk), prefetch_map(mv);
-    if (!plan_matches(p.plan, p.sig)) {
+    // A device plan of another launch: nothing is written.  Where the starts come with the launch nothing depends on it before.
+    const bool right = plan_matches(p.plan, p.sig);
+    if (p.N > FEW && !right) {
         if (tid == 0 && blockIdx.x == 0) record_status(&g_window_status, KDA_ERR_INVALID_ARG);
         return;
     }
@@ -395,7 +397,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok && n > 0) {
             fence_after();
             const int64_t token = at.start + rows.t0 + r;
-            const bool real = r < rows.count;
+            const bool real = r < rows.count && right;
+            if (!right && lane == 0) record_status(&g_window_status, KDA_ERR_INVALID_ARG);
             if (lse && real) lse[static_cast<int64_t>(rows.head) * p.T + token] = (fmaf(m, p.c, log2f(sum))) * 0.69314718055994530942f;
             const float inv = 1.f / sum;
             const int bad = *static_cast<volatile int *>(&s_bad);
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 32; k += RPI) {
                 const int row = r0 + k + lane / CH;
-                if (row < rows.count)
+                if (row < rows.count && right)
                     *reinterpret_cast<uint4 *>(dst + row * ldo) = *reinterpret_cast<const uint4 *>(out + row * (2 * D) + ((ch ^ (row & 7)) << 4));
             }
         }

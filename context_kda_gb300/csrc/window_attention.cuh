@@ -17,10 +17,15 @@ using namespace tc;
 constexpr int TILE = 128;                 // rows of a tile, of queries and of keys
 constexpr uint32_t BOX = TILE * 128;      // 128 rows of 64 16-bit columns, as a box with the 128-byte swizzle lands
 
+// Sequences whose starts come with the launch.  Finding a tile in the device plan takes three trips to the L2 cache, 2300 cycles
+// before a CTA knows what to fetch; from the launch's constants it is hardly any.
+constexpr int FEW = 32;
+
 struct Shape {
     const int32_t *plan;
     PlanSig sig;
     int N, off_cu, T;                     // of the plan
+    int32_t cu[FEW + 1];                  // the host plan's, where N <= FEW
     int H, Hk, W, S;
     float c;                              // scale * log2(e): scores to exponents of two
     float scale;
@@ -51,8 +56,10 @@ template <int N> __device__ __forceinline__ void more_registers() { asm volatile
 
 inline Shape window_shape(const int32_t *plan_host, const int32_t *plan_dev, const WindowIn &in)
 {
-    return Shape{plan_dev, plan_sig(plan_host), plan_host[KDA_PH_N], plan_host[KDA_PH_OFF_CU], plan_host[KDA_PH_T], in.H, in.Hk, in.W, in.S,
-                 in.scale * 1.44269504088896340736f, in.scale};
+    Shape p{plan_dev, plan_sig(plan_host), plan_host[KDA_PH_N], plan_host[KDA_PH_OFF_CU], plan_host[KDA_PH_T], {}, in.H, in.Hk, in.W, in.S,
+            in.scale * 1.44269504088896340736f, in.scale};
+    for (int n = 0; n <= p.N && p.N <= FEW; ++n) p.cu[n] = plan_host[p.off_cu + n];
+    return p;
 }
 
 template <typename E> struct Pair;        // two values rounded to a packed pair (a in the low half); x 0 + c of such pairs
@@ -147,20 +154,26 @@ struct Place {
 };
 __device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Place &at)
 {
-    const int32_t *cu = p.plan + p.off_cu;
     const int lane = threadIdx.x & 31;
-    int lo = 0, count = p.N;
-    while (true) {                        // 32 candidates at a time, evenly spread over the rest
-        const int stride = (count + 31) / 32, n = lo + lane * stride;
-        const bool in = lane * stride < count && cu[n] / rows + n <= slot;
-        const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
-        lo += last * stride;
-        count = min(stride, count - last * stride);
-        if (stride == 1) break;
+    int lo = 0;
+    if (p.N <= FEW) {
+        lo = __popc(__ballot_sync(0xffffffffu, lane < p.N && p.cu[lane] / rows + lane <= slot)) - 1;
+        at.start = p.cu[lo];
+        at.len = p.cu[lo + 1] - at.start;
+    } else {
+        const int32_t *cu = p.plan + p.off_cu;
+        for (int count = p.N;;) {         // 32 candidates at a time, evenly spread over the rest
+            const int stride = (count + 31) / 32, n = lo + lane * stride;
+            const bool in = lane * stride < count && cu[n] / rows + n <= slot;
+            const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+            lo += last * stride;
+            count = min(stride, count - last * stride);
+            if (stride == 1) break;
+        }
+        at.start = cu[lo];
+        at.len = cu[lo + 1] - at.start;
     }
     at.seq = lo;
-    at.start = cu[lo];
-    at.len = cu[lo + 1] - at.start;
     at.t0 = (slot - (at.start / rows + lo)) * rows;
     // the same in every lane; said so that the compiler knows
     at.seq = __shfl_sync(0xffffffffu, at.seq, 0);

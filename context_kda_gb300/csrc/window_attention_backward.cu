@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) prefetch_map(mx1), prefetch_map(mx2), prefetch_map(my1), prefetch_map(my2);
-    if (!plan_matches(p.plan, p.sig)) {
+    // A device plan of another launch: no gradient is written.  Where the starts come with the launch nothing depends on it before.
+    const bool right = plan_matches(p.plan, p.sig);
+    if (p.N > FEW && !right) {
         if (tid == 0 && blockIdx.x == 0) record_status(&g_window_back_status, KDA_ERR_INVALID_ARG);
         return;
     }
@@ -490,7 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok && lane == 0) give_up();
         // ---- the sums: keys: the first group writes dk, the second dv; queries: half of dq's columns each.  Rounded once, rows by way of
         // shared memory (the own rows are no longer needed), the sinks' in fp32 into the workspace
-        if (ok) {
+        if (!right && lane == 0) record_status(&g_window_back_status, KDA_ERR_INVALID_ARG);
+        if (ok && right) {
             constexpr int COLS = KEYS ? D : D / 2, CH = COLS / 8, RPI = 32 / CH, SWZ = CH < 8 ? CH - 1 : 7;
             fence_after();
             const float mul = KEYS && x == 1 ? (F16 ? 0x1p-10f : 1.f) : p.scale / factor;
@@ -557,33 +560,48 @@ __global__ void __launch_bounds__(256) window_delta(const Shape p, const E *o, i
     constexpr int LANES = D / 8;
     const int lane = threadIdx.x & 31, l = lane % LANES;
     const int heads = p.H + (Pair<E>::BF16 ? 0 : p.Hk);      // the value heads behind the query heads
-    const int64_t n = static_cast<int64_t>(p.T) * heads, all = (n * LANES + 31) / 32 * 32;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / LANES, t = row / heads;
-        const int h = static_cast<int>(row - t * heads);
-        float dot = 0.f, sq = 0.f;
-        if (row < n) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(h < p.H ? d_o + t * lddo + h * D + l * 8 : v + t * ldv + (h - p.H) * D + l * 8);
-            const uint4 b = h < p.H ? *reinterpret_cast<const uint4 *>(o + t * ldo + h * D + l * 8) : a;
-            const E *const x = reinterpret_cast<const E *>(&a), *const y = reinterpret_cast<const E *>(&b);
+    const int64_t n = static_cast<int64_t>(p.T) * heads;
+    constexpr int U = 4, ROWS = 32 / LANES;                  // steps in flight, rows of a warp's step
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x / 32;
+    for (int64_t first = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32 * ROWS; first < n; first += U * warps * ROWS) {
+        uint4 a[U], b[U];
+        int64_t t[U];
+        int h[U];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = to_f32(x[j]);
-                dot = fmaf(u, to_f32(y[j]), dot);
-                if (!Pair<E>::BF16) sq = fmaf(u, u, sq);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = first + u * warps * ROWS + lane / LANES;
+            t[u] = row / heads;
+            h[u] = row < n ? static_cast<int>(row - t[u] * heads) : -1;
+            a[u] = b[u] = make_uint4(0, 0, 0, 0);
+            if (h[u] >= p.H) {
+                a[u] = b[u] = *reinterpret_cast<const uint4 *>(v + t[u] * ldv + (h[u] - p.H) * D + l * 8);
+            } else if (h[u] >= 0) {
+                a[u] = *reinterpret_cast<const uint4 *>(d_o + t[u] * lddo + h[u] * D + l * 8);
+                b[u] = *reinterpret_cast<const uint4 *>(o + t[u] * ldo + h[u] * D + l * 8);
             }
         }
 #pragma unroll
-        for (int m = LANES / 2; m; m >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, m);
-            if (!Pair<E>::BF16) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-        }
-        if (l == 0 && row < n) {
-            if (h < p.H) k.delta[static_cast<int64_t>(h) * p.T + t] = dot;
-            if (!Pair<E>::BF16 && isfinite(sq)) {      // numbers above zero compare as their bits do
-                int *const to = reinterpret_cast<int *>(k.most) + (h < p.H ? h / (p.H / p.Hk) : p.Hk + h - p.H);
-                const int bits = __float_as_int(sqrtf(sq));
-                if (bits > *static_cast<volatile int *>(to)) atomicMax(to, bits);
+        for (int u = 0; u < U; ++u) {
+            const E *const x = reinterpret_cast<const E *>(&a[u]), *const y = reinterpret_cast<const E *>(&b[u]);
+            float dot = 0.f, sq = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float w = to_f32(x[j]);
+                dot = fmaf(w, to_f32(y[j]), dot);
+                if (!Pair<E>::BF16) sq = fmaf(w, w, sq);
+            }
+#pragma unroll
+            for (int m = LANES / 2; m; m >>= 1) {
+                dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                if (!Pair<E>::BF16) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+            }
+            if (l == 0 && h[u] >= 0) {
+                if (h[u] < p.H) k.delta[static_cast<int64_t>(h[u]) * p.T + t[u]] = dot;
+                if (!Pair<E>::BF16 && isfinite(sq)) {      // numbers above zero compare as their bits do
+                    int *const to = reinterpret_cast<int *>(k.most) + (h[u] < p.H ? h[u] / (p.H / p.Hk) : p.Hk + h[u] - p.H);
+                    const int bits = __float_as_int(sqrtf(sq));
+                    if (bits > *static_cast<volatile int *>(to)) atomicMax(to, bits);
+                }
             }
         }
     }
@@ -647,7 +665,7 @@ cudaError_t backward(const Shape &p, const WindowIn &in, const WindowGrads &g, v
     cudaError_t e;
     if (!bf16 && (e = cudaMemsetAsync(k.most, 0, static_cast<size_t>(2) * p.Hk * 4, stream)) != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.T) * (p.H + (bf16 ? 0 : p.Hk)) * (D / 8);
-    const int grid = static_cast<int>(min((rows + 255) / 256, static_cast<int64_t>(sm_count()) * 16));
+    const int grid = static_cast<int>(min((rows + 1023) / 1024, static_cast<int64_t>(sm_count()) * 8));
     window_delta<E, D><<<grid, 256, 0, stream>>>(p, static_cast<const E *>(g.o), g.ldo, static_cast<const E *>(g.d_o), g.lddo,
                                                  static_cast<const E *>(in.v), in.ldv, k);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
