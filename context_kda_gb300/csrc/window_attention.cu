@@ -4,8 +4,8 @@
 // A CTA works two tiles of 128 query rows against the same tiles of keys: two heads that share a key head, or else two
 // neighbouring tiles of one head.  Warp 0 fetches (TMA), warp 1 issues the products (tcgen05), warp 2 looks after the
 // values (below), and four warps a row tile do its softmax, a thread a row.  Scores S = Q K^T lie in
-// TMEM; a row's probabilities take the scores' place there as the A operand of O += P V, and the first half of them is
-// multiplied while the second half is computed.  While one row tile's probabilities are computed, the tensor cores work for the other.  They take the next product hardly before
+// TMEM; a row's probabilities take the scores' place there as the A operand of O += P V.  While one row tile's
+// probabilities are computed, the tensor cores work for the other.  They take the next product hardly before
 // the last is done, so whatever the issuing warp waits for stands still: it waits for probabilities only, and warp 2 adds
 // its arrival to theirs once the tile's values and the next keys are there.  One warp issues for both row tiles in turn; two
 // warps that issue as they can drift into step, and both row tiles' softmax then meets idle tensor cores (329 us for 261).
@@ -14,9 +14,9 @@
 // Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
 // the values before rounding.
 //
-// Values behind a masked place are multiplied by a probability of zero, which an infinity or NaN would survive.  Warps
-// 2 and 3 therefore look through the value tiles that some row sees only a part of, put zeros in the place of such values (and of the rows
-// behind the sequence's end) and leave a mark; the rows that do see one add it at the end, from memory.
+// Values behind a masked place are multiplied by a probability of zero, which an infinity or NaN would survive.  Warp 2
+// therefore looks through the value tiles that some row sees only a part of, puts zeros in the place of such values (and of the rows
+// behind the sequence's end) and leaves a mark; the rows that do see one add it at the end, from memory.
 #include "window_attention.cuh"
 
 namespace kda {
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     using L = Smem<D>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_s[2], s_p[2][2], s_o[2], s_end;
+    __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_s[2], s_p[2], s_o[2], s_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -87,9 +87,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         return;
     }
     Place at;
-    const int span = two_heads ? TILE : 2 * TILE;
     const int works = two_heads ? p.H / 2 : p.H, slot = (gridDim.x - 1 - blockIdx.x) / works, work = (gridDim.x - 1 - blockIdx.x) % works;
-    if (!find_tile(p, slot, span, at)) return;      // the last rows of a sequence, which see the most, come first
+    if (!find_tile(p, slot, two_heads ? 7 : 8, at)) return;      // the last rows of a sequence, which see the most, come first
     auto make_rows = [&](int x) {
         Rows y;
         y.head = two_heads ? 2 * work + x : work;
@@ -126,8 +125,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < L::VS; ++i) mbar_init(smem_u32(&s_vfull[i]), 1), mbar_init(smem_u32(&s_vfree[i]), 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&s_s[x]), 1);
-            mbar_init(smem_u32(&s_p[x][0]), 5);
-            mbar_init(smem_u32(&s_p[x][1]), 4);
+            mbar_init(smem_u32(&s_p[x]), 5);
             mbar_init(smem_u32(&s_o[x]), 1);
         }
         mbar_init(smem_u32(&s_end), 1);
@@ -179,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // ---- products.  TMEM addresses start at 0: the CTA has all of it
         constexpr uint32_t ID_S = idesc<E>(TILE, TILE, 0), ID_O = idesc<E>(TILE, D, 1);
-        auto scores = [&](int x, int stage) {
+        auto scores = [&](int x, int stage, bool last) {      // last: of this tile of keys
             const uint32_t qd = desc_k(base + L::Q + x * L::T_BYTES), kd = desc_k(base + L::K + stage * L::T_BYTES);
             if (elect()) {
 #pragma unroll
@@ -188,6 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     product(TM_S + x * 128, qd + off, kd + off, ID_S, s > 0);
                 }
                 commit(smem_u32(&s_s[x]));
+                if (last) commit(smem_u32(&s_kfree[stage]));
             }
             __syncwarp();
         };
@@ -198,9 +197,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = wait_warp(smem_u32(&s_q), 0) && wait_warp(smem_u32(&s_kfull[0]), 0);
         if (ok) {
             fence_after();
-            if (w.active(x0, 0)) scores(0, 0);
-            if (w.active(x1, 0)) scores(1, 0);
-            signal(s_kfree[0]);
+            if (w.active(x0, 0)) scores(0, 0, !w.active(x1, 0));
+            if (w.active(x1, 0)) scores(1, 0, true);
         }
         int ks = 1 % L::KS, kp = 1 / L::KS & 1, vs = 0;      // stage (and parity) of the next keys and values
         int done[2] = {0, 0};
@@ -213,30 +211,28 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int x = 0; x < 2; ++x) {
                 const Rows &rows = x ? x1 : x0;
                 const bool next = more && w.active(rows, i + 1);
+                // the last of the two that work a tile gives its stage back
+                const bool last = x == 1 || !w.active(x1, i), last_next = x == 1 || !(more && w.active(x1, i + 1));
                 if (w.active(rows, i)) {
+                    ok = ok && wait_warp(smem_u32(&s_p[x]), done[x] & 1);
+                    if (!ok) continue;
+                    fence_after();
+                    if (elect()) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && wait_warp(smem_u32(&s_p[x][h]), done[x] & 1);
-                        if (!ok) continue;
-                        fence_after();
-                        if (elect()) {
-#pragma unroll
-                            for (int s = h * 4; s < h * 4 + 4; ++s)
-                                if (s < steps) product_ta(TM_O + x * D, TM_S + x * 128 + s * 8, vd + s * (2048 >> 4), ID_O, done[x] > 0 || s > 0);
-                        }
-                        __syncwarp();
+                        for (int s = 0; s < TILE / 16; ++s)
+                            if (s < steps) product_ta(TM_O + x * D, TM_S + x * 128 + s * 8, vd + s * (2048 >> 4), ID_O, done[x] > 0 || s > 0);
+                        if (last) commit(smem_u32(&s_vfree[vs]));
                     }
+                    __syncwarp();
                     ++done[x];
                 } else if (next) {
                     ok = ok && wait_warp(smem_u32(&s_kfull[ks]), kp);
                     fence_after();
                 }
-                if (ok && next) scores(x, ks);
+                if (ok && next) scores(x, ks, last_next);
             }
             if (!ok) break;
-            signal(s_vfree[vs]);
             if (++vs == L::VS) vs = 0;
-            if (more) signal(s_kfree[ks]);
             if (++ks == L::KS) ks = 0, kp ^= 1;
         }
         if (ok) {
@@ -257,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int x = 0; x < 2; ++x) {
                 if (!ok || !w.active(x ? x1 : x0, i)) continue;
                 ok = wait_warp(smem_u32(&s_s[x]), seen[x]++ & 1);     // the last round's arrivals are complete
-                if (ok && lane == 0) mbar_arrive(smem_u32(&s_p[x][0]));
+                if (ok && lane == 0) mbar_arrive(smem_u32(&s_p[x]));
             }
         };
         for (int i = 0; i < w.n && ok; ++i) {
@@ -384,11 +380,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     e[j] = Pair<E>::pack(v.x, v.y);
                 }
                 tmem_st32_nowait(ts + h * 32, e);
-                tmem_wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s_p[x][h]));
             }
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_p[x]));
             sum += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
             ++n;
         }

@@ -147,24 +147,24 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity)
     return true;
 }
 
-// The sequence and tile of slot 'slot'.  Sequence n has its tiles of 'rows' tokens from slot cu[n] / rows + n on, which
+// The sequence and tile of slot 'slot'.  Sequence n has its tiles of 'rows' = 2^log_rows tokens from slot cu[n] / rows + n on, which
 // leaves room for all of them without a prefix sum; a slot behind a sequence's last tile is empty (false).  Whole warps call it.
 struct Place {
     int seq, start, len, t0;              // the sequence, its first token and length, first row of the tile in it
 };
-__device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Place &at)
+__device__ __forceinline__ bool find_tile(const Shape &p, int slot, int log_rows, Place &at)
 {
     const int lane = threadIdx.x & 31;
     int lo = 0;
     if (p.N <= FEW) {
-        lo = __popc(__ballot_sync(0xffffffffu, lane < p.N && p.cu[lane] / rows + lane <= slot)) - 1;
+        lo = __popc(__ballot_sync(0xffffffffu, lane < p.N && (p.cu[lane] >> log_rows) + lane <= slot)) - 1;
         at.start = p.cu[lo];
         at.len = p.cu[lo + 1] - at.start;
     } else {
         const int32_t *cu = p.plan + p.off_cu;
         for (int count = p.N;;) {         // 32 candidates at a time, evenly spread over the rest
             const int stride = (count + 31) / 32, n = lo + lane * stride;
-            const bool in = lane * stride < count && cu[n] / rows + n <= slot;
+            const bool in = lane * stride < count && (cu[n] >> log_rows) + n <= slot;
             const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
             lo += last * stride;
             count = min(stride, count - last * stride);
@@ -174,7 +174,7 @@ __device__ __forceinline__ bool find_tile(const Shape &p, int slot, int rows, Pl
         at.len = cu[lo + 1] - at.start;
     }
     at.seq = lo;
-    at.t0 = (slot - (at.start / rows + lo)) * rows;
+    at.t0 = (slot - ((at.start >> log_rows) + lo)) << log_rows;
     // the same in every lane; said so that the compiler knows
     at.seq = __shfl_sync(0xffffffffu, at.seq, 0);
     at.start = __shfl_sync(0xffffffffu, at.start, 0);

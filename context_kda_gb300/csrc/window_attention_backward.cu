@@ -38,7 +38,7 @@ constexpr int THREADS = 384;
 constexpr int REGS_OTHER = 72, REGS_SOFTMAX = 216;     // of 168 at the launch: 128 x 72 + 256 x 216 = 384 x 168
 constexpr int HALF = TILE / 2;            // columns of a thread
 constexpr int NARROW = 32;                // windows up to this are narrow
-constexpr int CHUNK = 1024;               // queries of a piece of the sinks' work
+constexpr int CHUNK = 1024;               // queries of a piece of the sinks' work (tiles and pieces are found by shifts: 2^7, 2^10)
 
 template <int D> struct Smem {
     static constexpr uint32_t T_BYTES = D / 64 * BOX;
@@ -100,11 +100,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         sinks = true;
         head = i % p.Hk;
         slot = i / p.Hk;
-        if (!find_tile(p, slot, CHUNK, at)) return;
+        if (!find_tile(p, slot, 10, at)) return;
     } else {
         const int works = KEYS ? p.Hk : p.H, i = (KEYS ? k.window_blocks : static_cast<int>(gridDim.x)) - 1 - blockIdx.x;
         head = i % works;
-        if (!find_tile(p, i / works, TILE, at)) return;
+        if (!find_tile(p, i / works, 7, at)) return;
     }
     const int W = min(p.W, at.len), x0 = sinks ? 0 : at.t0, rows = min(TILE, at.len - x0);      // own rows [x0, x0 + rows)
     const bool has_sinks = p.S > 0 && W < at.len;        // some query has left a sink behind its window
@@ -426,15 +426,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!all) {
                 // a bound that no row of the warp meets costs nothing.  (ds is zero where p is: the other side's rows are finite
                 // behind the sequence's end)
-                if (__any_sync(0xffffffffu, a > 0)) {
 #pragma unroll
-                    for (int e = 0; e < HALF; ++e)
-                        if (e < a) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
-                }
-                if (__any_sync(0xffffffffu, b < HALF - 1)) {
+                for (int c = 0; c < HALF; c += 32) {
+                    if (__any_sync(0xffffffffu, a > c)) {
 #pragma unroll
-                    for (int e = 0; e < HALF; ++e)
-                        if (e > b) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                        for (int e = c; e < c + 32; ++e)
+                            if (e < a) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                    }
+                    if (__any_sync(0xffffffffu, b < c + 31)) {
+#pragma unroll
+                        for (int e = c; e < c + 32; ++e)
+                            if (e > b) (e & 1 ? pr[e / 2].y : pr[e / 2].x) = 0.f;
+                    }
                 }
             }
             if (KEYS) {
