@@ -794,12 +794,15 @@ namespace {
 // Rows on 16 bytes: what the copies of the attention's tiles take.
 bool rows16_ok(const void *p, int64_t ld, int64_t width) { return p && aligned16(p) && ld >= width && ld % 8 == 0; }
 
+bool map_stride_ok(int64_t ld) { return ld < (int64_t(1) << 39); }
+
 int window_shape_ok(const kda::WindowIn &in, int32_t type)
 {
     if (in.H < 1 || in.Hk < 1 || in.H % in.Hk || in.d < 1 || !kda::elem_bytes(type) || in.W < 1 || in.S < 0) return KDA_ERR_INVALID_ARG;
     const float c = in.scale * 1.44269504088896340736f;
     if (!(c > 0.f) || !std::isnormal(c)) return KDA_ERR_INVALID_ARG;
     if (type == KDA_TYPE_F32 || (in.d != 64 && in.d != 128) || in.S > KDA_WINDOW_MAX_SINKS) return KDA_ERR_UNSUPPORTED;
+    if (in.H > INT32_MAX / in.d) return KDA_ERR_UNSUPPORTED;      // a token's channels are counted in 32 bits
     return KDA_OK;
 }
 
@@ -810,9 +813,11 @@ int window_in_ok(const int32_t *plan, const int32_t *plan_dev, const kda::Window
     if (const int rc = window_shape_ok(in, type)) return rc;
     const int64_t w = static_cast<int64_t>(in.H) * in.d, wk = static_cast<int64_t>(in.Hk) * in.d;
     if (!rows16_ok(in.q, in.ldq, w) || !rows16_ok(in.k, in.ldk, wk) || !rows16_ok(in.v, in.ldv, wk)) return KDA_ERR_INVALID_ARG;
-    // a head's tiles of 128 tokens, and one more for each sequence, are blocks of one grid
+    // a head's tiles of 128 tokens, and one more for each sequence, are blocks of one grid, with the sinks' pieces at most twice as many;
+    // tensor maps hold strides below 2^40 bytes
     const int64_t T = plan[KDA_PH_T], N = plan[KDA_PH_N];
-    if (T > kda::WINDOW_MAX_T || (T / 128 + N) * in.H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (T > kda::WINDOW_MAX_T || (T / 128 + N) * in.H > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
+    if (!map_stride_ok(in.ldq) || !map_stride_ok(in.ldk) || !map_stride_ok(in.ldv)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -830,10 +835,10 @@ extern "C" int kda_window_attention_forward(const int32_t *plan, const int32_t *
 
 namespace {
 
-// A ring cache's rows are counted in 32 bits.
+// A ring cache's rows are counted in 32 bits, up to two rounds of a CTA's warps behind the last one.
 bool cache_ok(const void *k, const void *v, int32_t window, int32_t sinks)
 {
-    return k && v && aligned16(k) && aligned16(v) && window <= INT32_MAX - sinks;
+    return k && v && aligned16(k) && aligned16(v) && window <= INT32_MAX - 512 - sinks;
 }
 
 }  // namespace
@@ -892,6 +897,7 @@ extern "C" int kda_window_attention_backward(const int32_t *plan, const int32_t 
     const int64_t w = static_cast<int64_t>(H) * d, wk = static_cast<int64_t>(Hk) * d;
     if (!rows16_ok(o, ldo, w) || !rows16_ok(d_o, lddo, w) || !lse || !floats_ok_or_null(lse)) return KDA_ERR_INVALID_ARG;
     if (!rows16_ok(dq, lddq, w) || !rows16_ok(dk, lddk, wk) || !rows16_ok(dv, lddv, wk) || !ws || !aligned16(ws)) return KDA_ERR_INVALID_ARG;
+    if (!map_stride_ok(lddo)) return KDA_ERR_UNSUPPORTED;
     if (ws_bytes < kda::window_workspace_bytes(plan[KDA_PH_T], plan[KDA_PH_N], H, Hk, d, window, sinks)) return KDA_ERR_WORKSPACE;
     return cuda_status(kda::launch_window_backward(plan, plan_dev, type, in, g, ws, static_cast<cudaStream_t>(stream)));
 }

@@ -694,7 +694,8 @@ enum { KDA_WINDOW_MAX_SINKS = 128 };
  *   lse         out fp32 [H][T] or NULL: log sum_j exp(scale q_i . k_j), what the backward needs.
  * Scores, maxima and sums are fp32; probabilities are rounded to 'type' for their product with v.  A value (or score) that a
  * query does not see has no part in its row, also where it is infinite or NaN; no sequence sees another's.  The same call
- * gives the same bits.  T up to 2^31 - 513 (more, or more than 2^31 - 1 blocks of the grid: KDA_ERR_UNSUPPORTED).
+ * gives the same bits.  T up to 2^31 - 513, (T / 128 + N) H below 2^30, H d below 2^31, token strides below 2^39 (others:
+ * KDA_ERR_UNSUPPORTED).
  * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA; a bounded wait that gave up is reported by
  * kda_device_status() as KDA_ERR_TIMEOUT.
  */
@@ -708,8 +709,9 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
  *   dq, dk, dv  out as q, k, v, rows on 16 bytes.  dk and dv are the sums over the heads of each group.
  *   ws, ws_bytes    device workspace of at least kda_window_attention_workspace_bytes bytes, 16-byte aligned.
  * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products (fp16: kept times powers of two, so that
- * they neither overflow nor fade).  No sequence sees another's values, whatever they are; an infinity or NaN of a sequence may reach all
- * of that sequence's gradients.  The same call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
+ * they neither overflow nor fade; that of ds goes by the longest finite rows of do and v of all sequences, |ds| from 2^-29 of their product
+ * up keeps its bits).  No sequence sees another's values otherwise; an infinity or NaN of a sequence may reach all of that
+ * sequence's gradients.  The same call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
  */
 int kda_window_attention_backward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
                                   const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
@@ -724,7 +726,7 @@ size_t kda_window_attention_workspace_bytes(const int32_t *plan, int32_t H, int3
 /*
  * The ring cache of the window attention: for every slot and key head the last 'window' keys (and values) and the first 'sinks',
  *     cache_k, cache_v   [num_slots][Hk][sinks + window][d] of 'type', contiguous, 16-byte aligned;
- * position p is in row p if p < sinks, else in row sinks + (p - sinks) mod window.  sinks + window < 2^31.
+ * position p is in row p if p < sinks, else in row sinks + (p - sinks) mod window.  sinks + window < 2^31 - 512.
  *
  * kda_window_cache_fill -- what the next tokens need of packed sequences: sequence n of the plan goes to slot slots[n] (device
  * int32 [N], or NULL: slot n; then N <= num_slots), as if its tokens had come one at a time into an empty slot.  Rows of positions that the

@@ -82,7 +82,7 @@ WINDOW_BAD = [dict(plan=None), dict(plan_dev=None), dict(H=0), dict(Hk=0), dict(
               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-39), dict(window=0),
               dict(window=-5), dict(sinks=-1)]
 WINDOW_UNSUPPORTED = [dict(type=F32), dict(d=32), dict(d=256, ldq=2048, ldk=512, ldv=512), dict(d=96, ldq=768, ldk=192, ldv=192), dict(sinks=129),
-                      dict(H=2 ** 29, Hk=1, ldq=2 ** 40)]
+                      dict(H=2 ** 25, Hk=1, ldq=2 ** 38), dict(ldq=2 ** 39), dict(ldk=2 ** 39), dict(ldv=2 ** 40)]
 
 
 def test_window_forward_refusals(kda):  # noqa: F811
@@ -110,10 +110,10 @@ def test_window_step_refusals(kda):  # noqa: F811
     good.update(B=3, slots=F, num_slots=7, lengths=F, ck=F, cv=F, o=F, ldo=512)
     bad = [x for x in WINDOW_BAD if not set(x) & {"plan", "plan_dev"}]
     bad += [dict(B=-1), dict(num_slots=-1), dict(slots=F + 2), dict(slots=None, num_slots=2), dict(lengths=None), dict(lengths=F + 1), dict(ck=None),
-            dict(ck=F + 8), dict(cv=None), dict(cv=F + 8), dict(o=None), dict(o=F + 8), dict(ldo=511), dict(window=2 ** 31 - 1, sinks=1)]
+            dict(ck=F + 8), dict(cv=None), dict(cv=F + 8), dict(o=None), dict(o=F + 8), dict(ldo=511), dict(window=2 ** 31 - 1, sinks=1), dict(window=2 ** 31 - 512, sinks=0)]
     step = kda._lib.kda_window_attention_step
     _refusals(step, names, good, bad, kda.KDA_ERR_INVALID_ARG)
-    _refusals(step, names, good, WINDOW_UNSUPPORTED[:-1] + [dict(B=2 ** 30, num_slots=2 ** 30)], kda.KDA_ERR_UNSUPPORTED)
+    _refusals(step, names, good, WINDOW_UNSUPPORTED[:-4] + [dict(H=2 ** 25, Hk=1, ldq=2 ** 38, ldo=2 ** 38), dict(B=2 ** 30, num_slots=2 ** 30)], kda.KDA_ERR_UNSUPPORTED)
     _refusals(step, names, good, [dict(B=0), dict(B=0, q=None, lengths=None)], kda.KDA_OK)
 
 
@@ -138,7 +138,7 @@ def test_window_backward_refusals(kda):  # noqa: F811
         bad += [{n: None}, {n: F + 8}, {ld: good[ld] - 8}, {ld: good[ld] + 4}]
     fn = kda._lib.kda_window_attention_backward
     _refusals(fn, names, good, bad, kda.KDA_ERR_INVALID_ARG)
-    _refusals(fn, names, good, WINDOW_UNSUPPORTED, kda.KDA_ERR_UNSUPPORTED)
+    _refusals(fn, names, good, WINDOW_UNSUPPORTED[:-4] + WINDOW_UNSUPPORTED[-3:] + [dict(lddo=2 ** 39)], kda.KDA_ERR_UNSUPPORTED)
     _refusals(fn, names, good, [dict(ws_bytes=need - 1)], kda.KDA_ERR_WORKSPACE)
     size = lambda *a: kda.kda_window_attention_workspace_bytes(plan, *a)
     assert size(8, 3, 64, 100, 4) == size(8, 2, 32, 100, 4) == size(8, 2, 64, 0, 4) == size(8, 2, 64, 100, 129) == 0

@@ -237,6 +237,13 @@ def test_many_short_sequences():
     _case(lengths, 1, 1, 64, "bf16", 9, 1)
 
 
+@pytest.mark.parametrize("count", [31, 32, 33, 64, 65])
+def test_sequences_around_the_number_whose_starts_come_with_the_launch(count):
+    lengths = [1 + (i * 37) % 300 for i in range(count)]
+    _case(lengths, 2, 1, 64, "bf16", 100, 2)
+    _case(lengths, 1, 1, 128, "f16", BIG, 0)
+
+
 def test_a_device_plan_of_another_launch_is_refused():
     import torch
     from context_kda_gb300 import binding as kda

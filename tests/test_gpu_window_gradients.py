@@ -150,6 +150,24 @@ def test_many_short_sequences():
     _case(lengths, 1, 1, 64, "bf16", 9, 1)
 
 
+@pytest.mark.parametrize("count", [32, 33])
+def test_sequences_around_the_number_whose_starts_come_with_the_launch(count):
+    lengths = [1 + (i * 37) % 300 for i in range(count)]
+    _case(lengths, 2, 1, 64, "bf16", 100, 2)
+
+
+def test_the_same_bits_many_times():
+    """The roles of a CTA meet at barriers only: whatever their timing, every run gives the same bits."""
+    import torch
+    for lengths, H, Hk, d, kind, window, sinks in (((2050,), 1, 1, 64, "f16", 1025, 1), ((900, 333, 64), 4, 2, 128, "bf16", 200, 3)):
+        plan = _plan(lengths)
+        dev, _ = _draw(lengths, H, Hk, d, kind, names=("q", "k", "v", "do"))
+        want = _backward(plan, dev, 0.1, window, sinks)
+        for _ in range(30):
+            for a, b in zip(_backward(plan, dev, 0.1, window, sinks), want):
+                assert torch.equal(a, b)
+
+
 def test_against_differences():
     """The formula in 64 bits against central differences of the 64-bit forward, step 1e-4: error of order 1e-8 and 1e-16 / 1e-4.  (The
     kernel is compared with that formula above.)"""
