@@ -44,7 +44,7 @@ template <int D> struct Smem {
     static constexpr uint32_t T_BYTES = D / 64 * BOX;
     static constexpr int N1 = 3, N2 = 2;      // stages of Y1 (read first and last in a round) and of Y2
     static constexpr uint32_t X = 0, Y1 = 2 * T_BYTES, Y2 = Y1 + N1 * T_BYTES, BYTES = Y2 + N2 * T_BYTES;
-    static_assert(BYTES + 3072 <= 227 * 1024, "shared memory");      // with the static part
+    static_assert(BYTES + 3 * 1024 <= 227 * 1024, "shared memory");      // with the static part
 };
 // TMEM columns: S (p), P' (ds), the sums
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_ACC = 256, TM_P2 = 384, TM_COLS = 512;      // (queries: TM_P2 for odd steps)

@@ -5,13 +5,17 @@
 // min(p + 1, S + W), its own among them, in whatever order; attention does not ask for it.
 //
 // The step is bound by memory: every visible row is read once, for all heads of its group.  A cluster of CTAs shares
-// the rows of one (token, key head); a warp takes 16 rows at a time, 16 bytes a lane.  The products (mma, whose rate does
-// not matter here) may take channels and rows in any order, so a lane's 16 bytes of keys are its part of two K steps, and its 16
-// bytes each of four rows of values, interleaved, are its part of eight N tiles: no lane needs another's bytes.  So shared memory is
-// only a queue of copies (cp.async) for each lane, STAGES deep, without a barrier.  Scores leave the first product where the
+// the rows of one (token, key head); a warp takes 16 rows at a time, which are contiguous, as one bulk copy of keys and one of
+// values, STAGES of them in turn, each warp with its own barriers.  How the bytes are asked for is what decides: without any work on
+// them, the 807 MB of 64 tokens x 8 key heads over up to 4100 rows of 128 take 133 us as bulk copies of 4 KB, 160 us a row at a time and
+// 180 us with 16 bytes a lane (cp.async).  With the work and as separate calls 127 to 134 us, 6.0 to 6.3 TB/s, where a copy runs at 6.8.
+// The products (mma, whose rate does not matter here) may take channels and rows in any order, so a lane's 16 bytes of keys are
+// its part of two K steps, and its 16 bytes each of four rows of values, interleaved, are its part of eight N tiles: no lane needs
+// another's bytes.  Rows follow one another without a gap, so lanes of odd rows take their pieces in another order and swap them
+// afterwards: keys without bank conflicts, values (128 channels) with two to a bank.  Scores leave the first product where the
 // second one wants its A operand.  Each warp keeps its own running maximum, sum and outputs; they are joined in shared memory
 // and then over the cluster, in a fixed order.
-// The new token's row comes from the arguments, and the CTA that would have read it from the cache writes it there.
+// The new token's row is laid over the cache's in shared memory, and the CTA whose rows it is among writes it to the cache.
 #include "elem.cuh"
 #include "kda_internal.cuh"
 #include "tc.cuh"
@@ -24,16 +28,21 @@ __device__ int g_cache_status;
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int ROWS = 16;                  // of a warp's step
 constexpr int MAX_SPLIT = 8;              // CTAs of a cluster
-constexpr int STAGES = 2;                 // of a lane's queue, 16 rows each: three CTAs an SM have up to 192 KiB on their way
+constexpr int STAGES = 3;                 // of a warp's queue, 16 rows each: two CTAs an SM have up to 192 KiB on their way
 
-template <int D> constexpr int PIECES = D / 8;                                   // 16-byte pieces of a lane in 16 rows of keys and values
-template <int D> constexpr uint32_t QUEUE = STAGES * PIECES<D> * 512;            // of a warp
-template <int D, int HG> constexpr uint32_t SMEM = WARPS * (QUEUE<D> > HG * D * 4 ? QUEUE<D> : HG * D * 4);
+template <int D> constexpr uint32_t STAGE = 2 * ROWS * D * 2;      // bytes: 16 rows of keys, 16 of values
+template <int D> constexpr uint32_t QUEUE = STAGES * STAGE<D>;     // of a warp
+// A warp's sums, for the join: channel ch of a head at at_ch(ch), heads PITCH apart, so that its 8 heads x 4 groups of channels meet 32 banks.
+template <int D> constexpr int PITCH = D + 33;
+template <int D> __device__ __forceinline__ int at_ch(int ch) { return ch + 8 * (ch / (D / 4)); }
+template <int D, int HG> constexpr uint32_t SUMS = HG * PITCH<D> * 4;
+template <int D, int HG> constexpr uint32_t SMEM = WARPS * (QUEUE<D> > SUMS<D, HG> ? QUEUE<D> : SUMS<D, HG>);
 
-// 16 bytes, or zeros where 'real' is false, into this lane's place.
-__device__ __forceinline__ void fetch16(uint32_t dst, const void *src, bool real)
+__device__ __forceinline__ void swap_if(bool yes, uint4 &a, uint4 &b)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+    const uint4 x = a;
+    a.x = yes ? b.x : a.x, a.y = yes ? b.y : a.y, a.z = yes ? b.z : a.z, a.w = yes ? b.w : a.w;
+    b.x = yes ? x.x : b.x, b.y = yes ? x.y : b.y, b.z = yes ? x.z : b.z, b.w = yes ? x.w : b.w;
 }
 
 template <typename E>
@@ -91,12 +100,13 @@ struct Step {
 
 // HG: query heads worked together, 8 or 16 (the product's M).
 template <typename E, int D, int HG>
-__global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache_k, E *cache_v, E *o)
+__global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache_k, E *cache_v, E *o)
 {
     constexpr int KC = D / 32, VC = D / 64;       // 16-byte pieces of a lane: of a row of keys, of a row of values
     extern __shared__ __align__(16) unsigned char smem[];
-    auto s_o = reinterpret_cast<float (*)[HG][D]>(smem);      // [WARPS], once the queues are empty
+    auto s_o = reinterpret_cast<float (*)[HG][PITCH<D>]>(smem);      // [WARPS], once the queues are empty
     __shared__ float s_m[WARPS][HG], s_l[WARPS][HG], s_mc[HG], s_lc[HG];
+    __shared__ alignas(8) uint64_t s_full[WARPS][STAGES];
     const StepIn &in = p.in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = lane >> 2, c4 = lane & 3;
     const int part = blockIdx.x % p.split;
@@ -139,50 +149,66 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
         if constexpr (HG == 16) acc2[i][0] = acc2[i][1] = 0.f;
     }
 
-    const uint32_t queue = tc::smem_u32(smem) + warp * QUEUE<D> + lane * 16;
-    const unsigned char *const mine = smem + warp * QUEUE<D> + lane * 16;
-    auto fetch = [&](int r0, int stage) {       // keys of rows r0 + hd, + 8; values of rows r0 + 2 c4, + 1, + 8, + 9
-        const uint32_t to = queue + stage * PIECES<D> * 512;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int r = r0 + t * 8 + hd;
-            const bool real = r < hi;
-            const E *const src = (r == fresh ? k_new : cache_k + (first + (real ? r : lo)) * D) + c4 * 8;
-#pragma unroll
-            for (int i = 0; i < KC; ++i) fetch16(to + (t * KC + i) * 512, src + i * 32, real);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int r = r0 + (t >> 1) * 8 + c4 * 2 + (t & 1);
-            const bool real = r < hi;
-            const E *const src = (r == fresh ? v_new : cache_v + (first + (real ? r : lo)) * D) + hd * 8;
-#pragma unroll
-            for (int i = 0; i < VC; ++i) fetch16(to + (2 * KC + t * VC + i) * 512, src + i * 64, real);
-        }
+    const uint32_t full = tc::smem_u32(&s_full[warp][0]), queue = tc::smem_u32(smem) + warp * QUEUE<D>;
+    unsigned char *const mine = smem + warp * QUEUE<D>;
+    if (lane == 0)
+        for (int s = 0; s < STAGES; ++s) tc::mbar_init(full + s * 8, 1);
+    auto fetch = [&](int r0, int stage) {         // by lane 0
+        const uint32_t bytes = min(ROWS, hi - r0) * D * 2, to = queue + stage * STAGE<D>;
+        tc::mbar_arrive_expect_tx(full + stage * 8, 2 * bytes);
+        tc::bulk_g2s(to, cache_k + (first + r0) * D, bytes, full + stage * 8);
+        tc::bulk_g2s(to + STAGE<D> / 2, cache_v + (first + r0) * D, bytes, full + stage * 8);
     };
-    int ahead = lo + warp * ROWS, r0 = ahead;
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s, ahead += WARPS * ROWS) {
-        if (ahead < hi) fetch(ahead, s);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    for (int stage = 0; r0 < hi; r0 += WARPS * ROWS, ahead += WARPS * ROWS, stage = stage == STAGES - 1 ? 0 : stage + 1) {
-        if (ahead < hi) fetch(ahead, stage == 0 ? STAGES - 1 : stage - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        const uint4 *const x = reinterpret_cast<const uint4 *>(mine + stage * PIECES<D> * 512);
+    constexpr int STRIDE = WARPS * ROWS;
+    int r0 = lo + warp * ROWS;
+    if (lane == 0)
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (r0 + s * STRIDE < hi) fetch(r0 + s * STRIDE, s);
+    __syncwarp();
+    uint32_t parity = 0;
+    for (int stage = 0; r0 < hi; r0 += STRIDE, stage = stage == STAGES - 1 ? 0 : stage + 1) {
+        __syncwarp();                             // the stage before this one has been read
+        if (lane == 0 && r0 + (STAGES - 1) * STRIDE < hi) fetch(r0 + (STAGES - 1) * STRIDE, stage == 0 ? STAGES - 1 : stage - 1);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(full + stage * 8, parity >> stage & 1))) {
+            if (lane == 0) record_status(&g_cache_status, KDA_ERR_TIMEOUT);
+            for (int i = 0, s = stage; i < STAGES; ++i, s = s == STAGES - 1 ? 0 : s + 1)      // copies on their way, before this memory is used again
+                if (r0 + i * STRIDE < hi) tc::mbar_wait(full + s * 8, parity >> s & 1);
+            l = l2 = NAN;
+            break;
+        }
+        parity ^= 1u << stage;
+        unsigned char *const rows = mine + stage * STAGE<D>;
+        if (fresh >= r0 && fresh < r0 + ROWS && fresh < hi) {
+            if (lane < 2 * D / 8) {
+                const bool is_v = lane >= D / 8;
+                const int ch = lane % (D / 8) * 8;
+                *reinterpret_cast<uint4 *>(rows + is_v * (STAGE<D> / 2) + ((fresh - r0) * D + ch) * 2) = *reinterpret_cast<const uint4 *>((is_v ? v_new : k_new) + ch);
+            }
+            tc::fence_async_smem();               // before the next copy to this place
+        }
+        if (r0 + ROWS > hi)                       // no values there: a probability of zero, but what lies there may be NaN
+            for (int i = (hi - r0) * (D / 8) + lane; i < ROWS * D / 8; i += 32)
+                *reinterpret_cast<uint4 *>(rows + STAGE<D> / 2 + i * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
         float s[2][4] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {             // keys of rows r0 + hd, + 8
+            uint4 kr[KC];
+#pragma unroll
+            for (int i = 0; i < KC; ++i) kr[i] = *reinterpret_cast<const uint4 *>(rows + (t * 8 + hd) * D * 2 + (c4 + 4 * (i ^ (hd & 1))) * 16);
+#pragma unroll
+            for (int i = 0; i < KC; i += 2) swap_if(hd & 1, kr[i], kr[i + 1]);
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
-                const uint4 y = x[(t * KC + i) * 32];
+                const uint4 y = kr[i];
                 const uint32_t b0[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     mma<E>(s[t][0], s[t][1], s[t][2], s[t][3], qa[i][2 * h], HG == 16 ? qb[HG == 16 ? i : 0][2 * h] : 0u, qa[i][2 * h + 1],
                            HG == 16 ? qb[HG == 16 ? i : 0][2 * h + 1] : 0u, b0[2 * h], b0[2 * h + 1]);
             }
+        }
         // s[t][0, 1]: head hd, rows r0 + 8 t + 2 c4, + 1;  s[t][2, 3]: head hd + 8
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -213,16 +239,21 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
         if constexpr (HG == 16) follow(m2, l2, acc2, 2);
         const uint32_t a0 = pack2(s[0][0], s[0][1], E()), a2 = pack2(s[1][0], s[1][1], E());
         const uint32_t a1 = HG == 16 ? pack2(s[0][2], s[0][3], E()) : 0u, a3 = HG == 16 ? pack2(s[1][2], s[1][3], E()) : 0u;
+        uint4 vr[VC][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {             // values of rows r0 + 2 c4, + 1, + 8, + 9
+            const unsigned char *const row = rows + STAGE<D> / 2 + ((t >> 1) * 8 + c4 * 2 + (t & 1)) * D * 2 + hd * VC * 16;
+#pragma unroll
+            for (int i = 0; i < VC; ++i) vr[i][t] = *reinterpret_cast<const uint4 *>(row + (VC == 1 ? 0 : (i ^ (c4 & 1)) * 16));
+            if constexpr (VC == 2) swap_if(c4 & 1, vr[0][t], vr[1][t]);
+        }
 #pragma unroll
         for (int i = 0; i < VC; ++i) {
-            uint4 vr[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) vr[t] = x[(2 * KC + t * VC + i) * 32];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 uint32_t y[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) y[t] = w == 0 ? vr[t].x : w == 1 ? vr[t].y : w == 2 ? vr[t].z : vr[t].w;
+                for (int t = 0; t < 4; ++t) y[t] = w == 0 ? vr[i][t].x : w == 1 ? vr[i][t].y : w == 2 ? vr[i][t].z : vr[i][t].w;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {     // channel 2 w + h of the lane's 8
                     const uint32_t b0 = __byte_perm(y[0], y[1], h ? 0x7632 : 0x5410), b1 = __byte_perm(y[2], y[3], h ? 0x7632 : 0x5410);
@@ -234,7 +265,6 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
             }
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     // ---- the new row into the cache, by the CTA whose rows it is among
     if (block == 0 && fresh >= lo && fresh < hi && tid < 2 * D / 8) {
@@ -248,9 +278,9 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (c4 == 0) s_m[warp][head] = m, s_l[warp][head] = l;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)           // n = 2 c4 + e is channel (n + 8 (j / 8)) * 8 + j % 8
+        for (int j = 0; j < D / 8; ++j)           // n = 2 c4 + e is channel (n VC + j / 8) * 8 + j % 8
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s_o[warp][head][(2 * c4 + e + j / 8 * 8) * 8 + j % 8] = a[j][e];
+            for (int e = 0; e < 2; ++e) s_o[warp][head][at_ch<D>(((2 * c4 + e) * VC + j / 8) * 8 + j % 8)] = a[j][e];
     };
     leave(hd, m, l, acc);
     if constexpr (HG == 16) leave(hd + 8, m2, l2, acc2);
@@ -264,10 +294,10 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
         for (int w = 0; w < WARPS; ++w) {
             const float f = s_m[w][h] == -INFINITY && !(s_l[w][h] > 0.f || s_l[w][h] != s_l[w][h]) ? 0.f : tc::ex2_ftz(s_m[w][h] - top);
             sum = fmaf(f, s_l[w][h], sum);
-            v = fmaf(f, s_o[w][h][ch], v);
+            v = fmaf(f, s_o[w][h][at_ch<D>(ch)], v);
         }
         if (p.split == 1) out[i] = from_f32<E>(v / sum);
-        else s_o[0][h][ch] = v;
+        else s_o[0][h][at_ch<D>(ch)] = v;
         if (ch == 0) s_mc[h] = top, s_lc[h] = sum;
     }
     if (p.split == 1) return;
@@ -278,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 3) window_step(const Step p, E *cache
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r)
             if (r < p.split) {
-                ms[r] = load_rank(&s_mc[h], r), ls[r] = load_rank(&s_lc[h], r), vs[r] = load_rank(&s_o[0][h][ch], r);
+                ms[r] = load_rank(&s_mc[h], r), ls[r] = load_rank(&s_lc[h], r), vs[r] = load_rank(&s_o[0][h][at_ch<D>(ch)], r);
                 top = fmaxf(top, ms[r]);
             }
 #pragma unroll
@@ -299,8 +329,9 @@ cudaError_t step(Step p, void *cache_k, void *cache_v, void *o, cudaStream_t str
     const StepIn &in = p.in;
     p.blocks = (p.g + HG - 1) / HG;
     const int64_t units = static_cast<int64_t>(in.B) * in.Hk * p.blocks;
-    // two rounds of CTAs and more, since lengths differ, but none with fewer than 64 rows of a full cache (its way in and out would
-    // take longer): 64 tokens x 8 key heads over up to 4100 rows 168 us, with one round 174 us
+    // three rounds of CTAs (two an SM) and more, since lengths differ, but none with fewer than 64 rows of a full cache (its way in and out
+    // would take longer): 64 tokens x 8 key heads over up to 4100 rows of 128, any length, 127 to 134 us, with half as many CTAs 138 us,
+    // twice as many 130 us; with all caches full, where nothing is uneven, 170, 158 and 172 us.  2 tokens x 4 over 1028 rows: 8.2 us
     p.split = 1;
     while (p.split < MAX_SPLIT && units * p.split < 6 * sm_count() && (in.W + in.S) / (2 * p.split) >= 64) p.split *= 2;
     const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(&window_step<E, D, HG>), SMEM<D, HG>);

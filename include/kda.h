@@ -748,9 +748,10 @@ int kda_window_cache_fill(const int32_t *plan, const int32_t *plan_dev, int32_t 
  *   lengths         device int32 [B]: tokens that the slot has had before this one, which is its position; not changed.
  *   q, o            [B][H][d];   k, v  [B][Hk][d]; rows on 16 bytes.   H, Hk, d, type, scale, window, sinks as in
  *                   kda_window_attention_forward.
- *   cache_k, cache_v  in/out, above.  Rows that no token has been put into are not read.
+ *   cache_k, cache_v  in/out, above.  Rows that no token has been put into have no part in it.
  * B = 0 is a call without work.  The same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (as
- * the forward; also more than 2^31 - 1 blocks, 8 B Hk ceil(H / Hk / 8)) or KDA_ERR_CUDA.
+ * the forward; also more than 2^31 - 1 blocks, 8 B Hk ceil(H / Hk / 8)) or KDA_ERR_CUDA; a bounded wait that gave up is
+ * reported by kda_device_status() as KDA_ERR_TIMEOUT.
  */
 int kda_window_attention_step(int32_t B, int32_t H, int32_t Hk, int32_t d, int32_t type, const int32_t *slots, int32_t num_slots,
                               const int32_t *lengths, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
