@@ -10,8 +10,9 @@
 // fixed lane away (halves).  The angles of a token are the same for all its heads: they are made once a token, two or so
 // a lane, and go through shared memory.  Few tokens are cut into parts of their heads, so that a decoding step
 // fills more than a few warps.
-// Bound by memory: 65536 tokens x 40 heads of 128 in bf16 take 236 us (84 % of a copy), gradients of 8192 x 32 heads 60 us (50 %: 16
-// warps an SM is what their registers allow), 8 tokens 6 us.
+// Bound by memory: 65536 tokens x 40 heads of 128 in bf16 take 236 us (84 % of a copy), gradients of 8192 x 32 heads 58 us (51 %: 16
+// warps an SM is what their registers allow), 8 tokens 6 us.  Neither is short of bytes on their way: chunks fetched ahead by bulk copies (as in
+// the attention's step) leave the gradients at 59 us, and the forward, whose registers they take, at 327 us.
 #include "elem.cuh"
 #include "kda_internal.cuh"
 #include "tc.cuh"
@@ -137,6 +138,34 @@ __device__ __forceinline__ void rotate(const Turn &t, float (&x)[V])
     }
 }
 
+// The same of values as they came: the others' come in their own type, half as many shuffles for 16 bits.
+template <typename E> __device__ __forceinline__ void rotate(const Turn &t, const Raw<E> &r, float (&x)[V])
+{
+    widen<E>(r, x);
+    if (t.partner < 0) {
+        rotate(t, x);
+        return;
+    }
+    Raw<E> other;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) {
+        other.v[i].x = __shfl_sync(0xffffffffu, r.v[i].x, t.partner);
+        other.v[i].y = __shfl_sync(0xffffffffu, r.v[i].y, t.partner);
+        other.v[i].z = __shfl_sync(0xffffffffu, r.v[i].z, t.partner);
+        other.v[i].w = __shfl_sync(0xffffffffu, r.v[i].w, t.partner);
+    }
+    float o[V];
+    widen<E>(other, o);
+    if (t.on) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 y = fma2(make_float2(o[j], o[j + 1]), make_float2(t.s[j], t.s[j + 1]),
+                                  mul2(make_float2(x[j], x[j + 1]), make_float2(t.c[j], t.c[j + 1])));
+            x[j] = y.x, x[j + 1] = y.y;
+        }
+    }
+}
+
 template <int D> __device__ __forceinline__ float head_sum(float v)
 {
 #pragma unroll
@@ -232,29 +261,37 @@ __device__ __forceinline__ void backward_heads(const HeadIn &in, const E *x, con
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u >= hi) break;
+            // (a step behind the last one is worked on zeros, as in the forward; the weights get nothing from it)
             const int h = (i + u) * HEADS + lane / LANES;
+            const bool real = i + u < hi && h < n;
             float e[V];
-            widen<E>(rg[u], e);
-            if (in.rot) rotate(turn, e);
+            if (in.rot) rotate<E>(turn, rg[u], e);
+            else widen<E>(rg[u], e);
             if (in.norm) {
-                float v[V], ss = 0.f, dot = 0.f;
+                float v[V];
                 widen<E>(rx[u], v);
+                float2 ew[V / 2], ss = make_float2(0.f, 0.f), dot = ss;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    ss = fmaf(v[j], v[j], ss);
-                    dot = fmaf(e[j] * w[j], v[j], dot);
+                for (int j = 0; j < V; j += 2) {
+                    const float2 x2 = make_float2(v[j], v[j + 1]);
+                    ew[j / 2] = mul2(make_float2(e[j], e[j + 1]), make_float2(w[j], w[j + 1]));
+                    ss = fma2(x2, x2, ss);
+                    dot = fma2(ew[j / 2], x2, dot);
                 }
-                const float inv = rsqrtf(fmaf(head_sum<D>(ss), 1.f / D, in.eps));
-                const float mean = head_sum<D>(dot) * inv * (1.f / D);        // of e w x / rms
+                const float square = head_sum<D>(ss.x + ss.y);        // (by all lanes)
+                const float inv = real ? rsqrtf(fmaf(square, 1.f / D, in.eps)) : 0.f;
+                const float mean = head_sum<D>(dot.x + dot.y) * inv * (1.f / D);        // of e w x / rms
+                const float2 inv2 = make_float2(inv, inv), less = make_float2(-mean, -mean);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float hat = v[j] * inv;
-                    dw[j] = fmaf(e[j], hat, dw[j]);
-                    e[j] = inv * fmaf(-hat, mean, e[j] * w[j]);
+                for (int j = 0; j < V; j += 2) {
+                    const float2 hat = mul2(make_float2(v[j], v[j + 1]), inv2);
+                    const float2 s = fma2(make_float2(e[j], e[j + 1]), hat, make_float2(dw[j], dw[j + 1]));
+                    dw[j] = s.x, dw[j + 1] = s.y;
+                    const float2 d = mul2(inv2, fma2(hat, less, ew[j / 2]));
+                    e[j] = d.x, e[j + 1] = d.y;
                 }
             }
-            if (h < n) store<E, ALIGNED>(dx + h * D + at, e);
+            if (real) store<E, ALIGNED>(dx + h * D + at, e);
         }
     }
 }
@@ -341,14 +378,15 @@ bool on16(const void *p, int64_t ld, int64_t T, int e)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (T < 2 || (ld * e & 15) == 0);
 }
 
-// How many warps share a token: one, unless that leaves the device's 'warps' fewer than eight tokens each, the last of which
-// would leave many of them idle.  A part is four steps at least where there are enough tokens for all warps: each part makes its angles anew.
+// How many warps share a token: one, unless that leaves the device's 'warps' fewer than six tokens each, the last of which
+// would leave many of them idle.  A part is four steps at least where there are enough tokens for all warps: each part makes its angles anew
+// (gradients of 8192 x 32 heads: two parts 58 us, three, which is what eight tokens each would ask for, 61 us).
 Work make_work(const HeadIn &in, int heads, int64_t warps)
 {
     Work p{in, in.T, 1, 0, 0};
     p.steps = (in.H + heads - 1) / heads + (in.Hk + heads - 1) / heads;
-    if (in.T < 8 * warps)
-        p.parts = static_cast<int>(min(static_cast<int64_t>(in.T < warps ? p.steps : (p.steps + 3) / 4), (8 * warps + in.T - 1) / in.T));
+    if (in.T < 6 * warps)
+        p.parts = static_cast<int>(min(static_cast<int64_t>(in.T < warps ? p.steps : (p.steps + 3) / 4), (6 * warps + in.T - 1) / in.T));
     p.per_part = (p.steps + p.parts - 1) / p.parts;
     p.parts = (p.steps + p.per_part - 1) / p.per_part;
     p.tasks = in.T * p.parts;
