@@ -10,7 +10,8 @@
 // its arrival to theirs once the tile's values and the next keys are there.  One warp issues for both row tiles in turn; two
 // warps that issue as they can drift into step, and both row tiles' softmax then meets idle tensor cores (329 us for 261).
 // A row's maximum is followed lazily: O is multiplied up only when the maximum has grown by more than 2^8 since, which
-// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so that there always is a maximum.
+// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so that there always is a maximum (minus
+// infinity where a row's scores are).
 // Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
 // the values before rounding.
 // Bound by the tensor cores' issue where much is visible: 8192 tokens x 16 heads (4 key heads) of 128, all visible, 201 us, 73 % of the dense
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 m = new_m;
             } else if (__any_sync(0xffffffffu, (new_m - m) * p.c > LAZY)) {
                 // the products before this tile's scores are complete, O among them
-                const float f = ex2_ftz((m - new_m) * p.c);
+                const float f = new_m == -INFINITY ? 1.f : ex2_ftz((m - new_m) * p.c);
                 m = new_m;
                 sum *= f;
 #pragma unroll
@@ -368,7 +369,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_st32_nowait(to + c * 32, t);
                 }
             }
-            const float2 cc = make_float2(p.c, p.c), mc = make_float2(-m * p.c, -m * p.c);
+            // (a row whose scores have all been minus infinity so far has probabilities of zero, and no maximum to subtract)
+            const float less = m == -INFINITY ? 0.f : -m * p.c;
+            const float2 cc = make_float2(p.c, p.c), mc = make_float2(less, less);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

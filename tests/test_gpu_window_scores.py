@@ -1,0 +1,61 @@
+"""GPU tests of the window attention where scores are extreme.  Tolerances of test_gpu_window_attention.py; where they differ, the reason
+stands with the test."""
+import numpy as np
+import pytest
+
+import attention_reference as ref
+from ops_reference import ROUND, TOL32
+from test_gpu_window_attention import BIG, _check_forward, _cu, _draw, _forward, _plan, _within
+from test_gpu_window_gradients import _backward
+
+pytestmark = pytest.mark.gpu
+
+
+def _values(x):
+    return x.double().cpu().numpy()
+
+
+def _hide(dev, keys, how):
+    """The score of every query with the given keys becomes minus infinity, by an infinite entry or by finite ones whose product passes
+    fp32 (bf16 only); all other scores stay finite."""
+    dev["q"][..., 0] = 1.0 if how == "infinite" else 2e19
+    dev["k"][..., 0] = 0.0
+    dev["k"][keys, :, 0] = float("-inf") if how == "infinite" else -3e19
+
+
+@pytest.mark.parametrize("kind,how", [("bf16", "infinite"), ("bf16", "finite"), ("f16", "infinite")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (2, 1)])
+@pytest.mark.parametrize("window,sinks", [(BIG, 0), (100, 3)])
+def test_a_visible_score_of_minus_infinity(window, sinks, H, Hk, d, kind, how):
+    """Its probability is zero and the row's others are as without it: also where it is the only key of its tile that a row sees (128, 256),
+    and where it is all that a warp's rows see in their first tile."""
+    lengths = (300, 150)
+    dev, _ = _draw(lengths, H, Hk, d, kind)
+    _hide(dev, [5, 128, 129, 130, 140, 256, 299, 301, 428], how)
+    w = {n: _values(dev[n]) for n in ("q", "k", "v")}
+    o, lse = _forward(_plan(lengths), dev, 0.125, window, sinks)
+    _check_forward(o, lse, lengths, w, kind, 0.125, window, sinks)
+
+
+def test_a_row_whose_scores_are_all_minus_infinity():
+    """0 / 0, as the formula has it, in that row alone."""
+    import torch
+    dev, _ = _draw((300,), 1, 1, 64, "bf16")
+    _hide(dev, [0], "infinite")
+    o, lse = _forward(_plan((300,)), dev, 0.125, BIG, 0)
+    assert bool(torch.isnan(o[0]).all()) and float(lse[0, 0]) == float("-inf")
+    assert bool(torch.isfinite(o[1:].float()).all()) and bool(torch.isfinite(lse[0, 1:]).all())
+
+
+def test_gradients_beside_scores_of_minus_infinity():
+    """Finite entries whose products pass fp32 hide their keys; the gradients of all other channels are those of the formula."""
+    lengths, window, sinks = (300, 150), 100, 3
+    dev, _ = _draw(lengths, 2, 1, 64, "bf16", names=("q", "k", "v", "do"))
+    _hide(dev, [5, 128, 129, 130, 140, 256, 299, 301, 428], "finite")
+    w = {n: _values(x) for n, x in dev.items()}
+    outs = _backward(_plan(lengths), dev, 0.125, window, sinks)
+    want = ref.window_backward(_cu(lengths), w["q"], w["k"], w["v"], 0.125, window, sinks, w["do"])
+    for n, got, x, size in zip(("dq", "dk", "dv"), outs, want[:3], want[3:]):
+        x, size = x[..., 1:], size[..., 1:]
+        _within(got[..., 1:], x, ROUND["bf16"] * 1.001 * (size + np.abs(x)) + TOL32 * (size + 1e-2 * np.abs(x).max() + 1e-3), n)
