@@ -227,11 +227,12 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
                 for (int i = 0; i < D / 8; ++i) a[i][0] *= f, a[i][1] *= f;
                 m = top;
             }
+            const float less = m == -INFINITY ? 0.f : m;      // (no maximum yet: scores of minus infinity alone, probabilities of zero)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    s[t][j + k] = tc::ex2_ftz(fmaf(s[t][j + k], p.c, -m));
+                    s[t][j + k] = tc::ex2_ftz(fmaf(s[t][j + k], p.c, -less));
                     l += s[t][j + k];
                 }
         };

@@ -7,6 +7,7 @@ import attention_reference as ref
 from ops_reference import ROUND, TOL32
 from test_gpu_window_attention import BIG, _check_forward, _cu, _draw, _forward, _plan, _within
 from test_gpu_window_gradients import _backward
+from test_gpu_window_step import _check as _check_step, _draw as _draw_step, _step
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,21 @@ def test_gradients_beside_scores_of_minus_infinity():
     for n, got, x, size in zip(("dq", "dk", "dv"), outs, want[:3], want[3:]):
         x, size = x[..., 1:], size[..., 1:]
         _within(got[..., 1:], x, ROUND["bf16"] * 1.001 * (size + np.abs(x)) + TOL32 * (size + 1e-2 * np.abs(x).max() + 1e-3), n)
+
+
+@pytest.mark.parametrize("kind,how", [("bf16", "infinite"), ("bf16", "finite"), ("f16", "infinite")])
+@pytest.mark.parametrize("B,H,Hk,d", [(2, 4, 1, 64), (1, 2, 2, 128), (1, 20, 1, 128)])
+@pytest.mark.parametrize("window,sinks", [(20, 1), (900, 2)])
+def test_a_visible_score_of_minus_infinity_in_the_step(window, sinks, B, H, Hk, d, kind, how):
+    """Whole groups of 16 rows, a warp's first ones among them, and single rows."""
+    cap = window + sinks
+    dev, _ = _draw_step(B, H, Hk, d, kind, window, sinks, B)
+    dev["k"][..., 0] = dev["cache_k"][..., 0] = 0.0
+    dev["q"][..., 0] = 1.0 if how == "infinite" else 2e19
+    hidden = list(range(0, 16)) + [17] + list(range(64, min(cap, 96))) + list(range(128, min(cap, 800)))
+    dev["cache_k"][:, :, [r for r in hidden if r < cap], 0] = float("-inf") if how == "infinite" else -3e19
+    w = {n: _values(x) for n, x in dev.items()}
+    for n in (cap - 1, 3 * cap):
+        d2 = {m: x.clone() for m, x in dev.items()}
+        o = _step(d2, None, [n] * B, 0.125, window, sinks)
+        _check_step(o, d2, w, list(range(B)), [n] * B, 0.125, window, sinks, kind)
