@@ -351,12 +351,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) top[c] = max3(top[c], __uint_as_float(u[c][j]), __uint_as_float(u[c][j + 1]));
             const float new_m = max3(m, fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            // each row by its own growth, whatever the warp's others do: rows share a warp with other sequences' too
+            const bool grown = (new_m - m) * p.c > LAZY;
             if (n == 0) {
                 m = new_m;
-            } else if (__any_sync(0xffffffffu, (new_m - m) * p.c > LAZY)) {
+            } else if (__any_sync(0xffffffffu, grown)) {
                 // the products before this tile's scores are complete, O among them
-                const float f = new_m == -INFINITY ? 1.f : ex2_ftz((m - new_m) * p.c);
-                m = new_m;
+                const float f = grown ? ex2_ftz((m - new_m) * p.c) : 1.f;
+                m = grown ? new_m : m;
                 sum *= f;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {

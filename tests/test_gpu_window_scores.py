@@ -78,3 +78,23 @@ def test_a_visible_score_of_minus_infinity_in_the_step(window, sinks, B, H, Hk, 
         d2 = {m: x.clone() for m, x in dev.items()}
         o = _step(d2, None, [n] * B, 0.125, window, sinks)
         _check_step(o, d2, w, list(range(B)), [n] * B, 0.125, window, sinks, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 2)])
+def test_a_row_keeps_its_bits_beside_any_other(H, Hk, kind):
+    """Rows share a warp with rows of their own sequence and, in its last tile, of the next one.  Those rows' scores, here grown
+    thirty times, have no part in a row's, whatever they do to their own maxima."""
+    import torch
+    lengths, d = (333, 333), 64
+    dev, _ = _draw(lengths, H, Hk, d, kind)
+    alone, lse1 = _forward(_plan(lengths[:1]), {n: x[:333].contiguous() for n, x in dev.items()}, 0.125, BIG, 0)
+    packed, lse2 = _forward(_plan(lengths), dev, 0.125, BIG, 0)
+    assert torch.equal(alone, packed[:333]) and torch.equal(lse1, lse2[:, :333])
+    for rows in (slice(333, 666), slice(300, 333, 2), slice(130, 256, 3)):
+        q = dev["q"].clone()
+        q[rows] *= 30
+        got, lse = _forward(_plan(lengths), dict(dev, q=q), 0.125, BIG, 0)
+        keep = torch.ones(666, dtype=torch.bool)
+        keep[rows] = False
+        assert torch.equal(got[keep], packed[keep]) and torch.equal(lse[:, keep], lse2[:, keep]), rows
