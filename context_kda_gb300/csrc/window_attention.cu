@@ -33,6 +33,7 @@ __device__ int g_window_status;
 constexpr int THREADS = 384;
 constexpr int REGS_OTHER = 72, REGS_SOFTMAX = 216;     // of 168 at the launch: 128 x 72 + 256 x 216 = 384 x 168
 constexpr float LAZY = 8.f;               // growth of a row's maximum, in powers of two, that O is not corrected for
+constexpr float FAR = 65536.f;            // exponents that are not made from products of their own: off by 2^-8 at most below
 
 template <int D> struct Smem {
     static constexpr uint32_t T_BYTES = D / 64 * BOX;
@@ -371,8 +372,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_st32_nowait(to + c * 32, t);
                 }
             }
-            // (a row whose scores have all been minus infinity so far has probabilities of zero, and no maximum to subtract)
-            const float less = m == -INFINITY ? 0.f : -m * p.c;
+            // Exponents (s - m) c come as s c - m c in one instruction, off by half a step of m c for all of the row, which cancels; where m c
+            // is far from zero, so that this would pass fp32's range (2^32) or fp16's, the difference is taken first.  (So it is
+            // where all scores have been minus infinity: probabilities of zero.)
+            const bool far = fabsf(m * p.c) > FAR;
+            if (__any_sync(0xffffffffu, far)) {
+                const float less = far && m != -INFINITY ? m : 0.f;
+#pragma unroll
+                for (int j = 0; j < TILE; ++j) u[j / 32][j % 32] = __float_as_uint(__uint_as_float(u[j / 32][j % 32]) - less);
+            }
+            const float less = far ? 0.f : -m * p.c;
             const float2 cc = make_float2(p.c, p.c), mc = make_float2(less, less);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import attention_reference as ref
-from ops_reference import ROUND, TOL32
+from ops_reference import ROUND, TOL32, torch_type
 from test_gpu_window_attention import BIG, _check_forward, _cu, _draw, _forward, _plan, _within
 from test_gpu_window_gradients import _backward
 from test_gpu_window_step import _check as _check_step, _draw as _draw_step, _step
@@ -98,3 +98,37 @@ def test_a_row_keeps_its_bits_beside_any_other(H, Hk, kind):
         keep = torch.ones(666, dtype=torch.bool)
         keep[rows] = False
         assert torch.equal(got[keep], packed[keep]) and torch.equal(lse[:, keep], lse2[:, keep]), rows
+
+
+@pytest.mark.parametrize("kind,gain,scale", [("bf16", 1e6, 1.0), ("bf16", 6e17, 8.0), ("f16", 100.0, 64.0), ("f16", 1000.0, 1.0)])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (2, 1)])
+def test_far_scores(H, Hk, kind, gain, scale):
+    """Scores from 2^24 on, where an exponent of two in fp32 is off by one and more: o is the winner's value all the same.  Only rows whose
+    two largest scores are further apart than 64 additions in fp32 are off (64 2^-24 of the largest) have a winner."""
+    import torch
+    lengths, d, window = (300,), 64, 40
+    dev, _ = _draw(lengths, H, Hk, d, kind, seed=11)
+    t = torch_type(kind)
+    gen = torch.Generator().manual_seed(3)
+    sign = lambda shape: torch.randint(0, 2, shape, generator=gen) * 2.0 - 1
+    dev["q"] = (sign(dev["q"].shape) * gain).to(t).cuda()
+    dev["k"] = (sign(dev["k"].shape) * gain * (1 + torch.arange(300).view(-1, 1, 1) % 61 / 64.0)).to(t).cuda()      # a size a key
+    w = {n: _values(dev[n]) for n in ("q", "k", "v")}
+    seen = ref.visible(300, window, 0)
+    far = 0
+    o, lse = _forward(_plan(lengths), dev, scale, window, 0)
+    o_ref, lse_ref, size = ref.window_forward(_cu(lengths), w["q"], w["k"], w["v"], scale, window, 0)
+    clear = np.zeros((300, H), dtype=bool)
+    for h in range(H):
+        s = w["q"][:, h] @ w["k"][:, h * Hk // H].T
+        for i in range(300):
+            x = np.sort(s[i, seen[i]])
+            clear[i, h] = len(x) == 1 or x[-1] - x[-2] > 64 * 2.0 ** -24 * 4 * np.abs(s[i]).max()
+        far = max(far, scale * np.abs(s).max())
+    assert far > 2.0 ** 24 and clear.mean() > 0.8
+    assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
+    got = _values(o)
+    bound = ROUND[kind] * 1.001 * (size + np.abs(o_ref)) + TOL32 * (size + 1e-3)
+    assert np.all(np.abs(got - o_ref)[clear] <= bound[clear])
+    got, want = lse.double().cpu().numpy().T[clear], lse_ref.T[clear]
+    assert np.all(np.abs(got - want) <= TOL32 * (1 + np.abs(want)))
