@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
             float top = fmaxf(fmaxf(s[0][j], s[0][j + 1]), fmaxf(s[1][j], s[1][j + 1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            top = fmaxf(top * p.c, m);
+            top = fmaxf(top, m);
             if (__any_sync(0xffffffffu, top > m)) {
-                const float f = m == -INFINITY ? 0.f : tc::ex2_ftz(m - top);
+                const float f = m == -INFINITY ? 0.f : tc::ex2_ftz((m - top) * p.c);
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) a[i][0] *= f, a[i][1] *= f;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    s[t][j + k] = tc::ex2_ftz(fmaf(s[t][j + k], p.c, -less));
+                    s[t][j + k] = tc::ex2_ftz((s[t][j + k] - less) * p.c);      // (the difference first: scores may be of any size)
                     l += s[t][j + k];
                 }
         };
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
         for (int w = 1; w < WARPS; ++w) top = fmaxf(top, s_m[w][h]);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const float f = s_m[w][h] == -INFINITY && !(s_l[w][h] > 0.f || s_l[w][h] != s_l[w][h]) ? 0.f : tc::ex2_ftz(s_m[w][h] - top);
+            const float f = s_m[w][h] == -INFINITY && !(s_l[w][h] > 0.f || s_l[w][h] != s_l[w][h]) ? 0.f : tc::ex2_ftz((s_m[w][h] - top) * p.c);
             sum = fmaf(f, s_l[w][h], sum);
             v = fmaf(f, s_o[w][h][at_ch<D>(ch)], v);
         }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r)
             if (r < p.split) {
-                const float f = ms[r] == -INFINITY && ls[r] == 0.f ? 0.f : tc::ex2_ftz(ms[r] - top);
+                const float f = ms[r] == -INFINITY && ls[r] == 0.f ? 0.f : tc::ex2_ftz((ms[r] - top) * p.c);
                 sum = fmaf(f, ls[r], sum);
                 v = fmaf(f, vs[r], v);
             }

@@ -132,3 +132,22 @@ def test_far_scores(H, Hk, kind, gain, scale):
     assert np.all(np.abs(got - o_ref)[clear] <= bound[clear])
     got, want = lse.double().cpu().numpy().T[clear], lse_ref.T[clear]
     assert np.all(np.abs(got - want) <= TOL32 * (1 + np.abs(want)))
+
+
+@pytest.mark.parametrize("kind,gain,scale", [("bf16", 1e6, 1.0), ("bf16", 2e18, 8.0), ("f16", 4000.0, 4.0), ("f16", 6000.0, 1.0)])
+@pytest.mark.parametrize("H", [2, 12])
+def test_far_scores_in_the_step(H, kind, gain, scale):
+    """Every score is one product; the largest times scale log2(e) passes fp32 in the second case."""
+    import torch
+    window, sinks, d, n = 700, 2, 64, 702
+    dev, _ = _draw_step(1, H, 1, d, kind, window, sinks, 1)
+    t = torch_type(kind)
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(4))
+    dev["q"].zero_()
+    dev["q"][..., 3] = gain
+    dev["k"][..., 3] = 0.0
+    dev["cache_k"][0, 0, :, 3] = (gain * 8 * (0.25 + order / n)).to(t).cuda()
+    dev["cache_k"][0, 0, int(order.argmax()), 3] = gain * 10.5      # above all others, which may be equal
+    w = {m: _values(x) for m, x in dev.items()}
+    o = _step(dev, None, [n - 1], scale, window, sinks)
+    _check_step(o, dev, w, [0], [n - 1], scale, window, sinks, kind)
