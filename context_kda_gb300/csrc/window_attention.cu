@@ -13,7 +13,8 @@
 // fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so that there always is a maximum (minus
 // infinity where a row's scores are).
 // Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
-// the values before rounding.
+// the values before rounding.  fp16 has no numbers below 2^-24, and very many small probabilities count: there they are kept
+// times 2^7, each off by half a step or 2^-32 of the row's largest.
 // Bound by the tensor cores' issue where much is visible: 8192 tokens x 16 heads (4 key heads) of 128, all visible, 201 us, 73 % of the dense
 // bf16 rate counted over visible pairs; by the way in and out of a CTA where little is: 32768 tokens in 24 sequences, window 1024, 260 us
 // (38 %); 1024 x 8 heads 19 us.
@@ -33,6 +34,7 @@ __device__ int g_window_status;
 constexpr int THREADS = 384;
 constexpr int REGS_OTHER = 72, REGS_SOFTMAX = 216;     // of 168 at the launch: 128 x 72 + 256 x 216 = 384 x 168
 constexpr float LAZY = 8.f;               // growth of a row's maximum, in powers of two, that O is not corrected for
+constexpr float F16_EXP = 7.f;            // 2^LAZY times that is 2^15, fp16's last power of two
 constexpr float FAR = 65536.f;            // exponents that are not made from products of their own: off by 2^-8 at most below
 
 template <int D> struct Smem {
@@ -78,6 +80,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                    const Shape p, bool two_heads, const E *v_rows, int64_t ldv, E *o, int64_t ldo, float *lse)
 {
     using L = Smem<D>;
+    constexpr float P_EXP = Pair<E>::BF16 ? 0.f : F16_EXP;      // probabilities are kept times 2^P_EXP
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t s_q, s_kfull[L::KS], s_kfree[L::KS], s_vfull[L::VS], s_vfree[L::VS], s_s[2], s_p[2], s_o[2], s_end;
     __shared__ uint32_t s_tmem;
@@ -381,8 +384,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < TILE; ++j) u[j / 32][j % 32] = __float_as_uint(__uint_as_float(u[j / 32][j % 32]) - less);
             }
-            const float less = far ? 0.f : -m * p.c;
-            const float2 cc = make_float2(p.c, p.c), mc = make_float2(less, less);
+            const float off = far ? P_EXP : fmaf(-m, p.c, P_EXP);
+            const float2 cc = make_float2(p.c, p.c), mc = make_float2(off, off);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t token = at.start + rows.t0 + r;
             const bool real = r < rows.count && right;
             if (!right && lane == 0) record_status(&g_window_status, KDA_ERR_INVALID_ARG);
-            if (lse && real) lse[static_cast<int64_t>(rows.head) * p.T + token] = (fmaf(m, p.c, log2f(sum))) * 0.69314718055994530942f;
+            if (lse && real) lse[static_cast<int64_t>(rows.head) * p.T + token] = fmaf(m, p.c, log2f(sum) - P_EXP) * 0.69314718055994530942f;
             const float inv = 1.f / sum;
             const int bad = *static_cast<volatile int *>(&s_bad);
             unsigned char *const out = basep + L::Q + x * L::T_BYTES;      // the queries are no longer needed: rows of D, chunks swizzled

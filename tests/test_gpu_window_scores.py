@@ -151,3 +151,21 @@ def test_far_scores_in_the_step(H, kind, gain, scale):
     w = {m: _values(x) for m, x in dev.items()}
     o = _step(dev, None, [n - 1], scale, window, sinks)
     _check_step(o, dev, w, [0], [n - 1], scale, window, sinks, kind)
+
+
+def test_very_many_small_probabilities_in_fp16():
+    """One key 17.5 nats above 65,535 others whose values are all that counts.  A probability of 2^-25.2 is below fp16's numbers; the
+    kernel keeps probabilities times a power of two, 2^7 at least: each is off by 2^-25 2^-7 of the largest at most."""
+    import torch
+    T, d = 65536, 64
+    q = torch.zeros(T, 1, d, dtype=torch.float16, device="cuda")
+    k, v = torch.zeros_like(q), torch.full_like(q, 8.0)
+    q[..., 0], k[T - 100, 0, 0], v[T - 100] = 4.0, 4.375, 0.0
+    o, lse = _forward(_plan((T,)), dict(q=q, k=k, v=v), 1.0, BIG, 0)
+    rows = np.arange(T - 99, T)
+    small = rows * np.exp(-17.5)                 # of all others together
+    want = 8 * small / (1 + small)
+    got = _values(o)[rows, 0]
+    bound = 2 * ROUND["f16"] * want + TOL32 * want + 2.0 ** -32 * 8 * T
+    assert np.all(np.abs(got - want[:, None]) <= bound[:, None])
+    assert np.all(np.abs(_values(lse)[0, rows] - (17.5 + np.log1p(small))) <= TOL32 * 18)
