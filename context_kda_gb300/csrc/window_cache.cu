@@ -14,8 +14,11 @@
 // another's bytes.  Rows follow one another without a gap, so lanes of odd rows take their pieces in another order and swap them
 // afterwards: keys without bank conflicts, values (128 channels) with two to a bank.  Scores leave the first product where the
 // second one wants its A operand.  Each warp keeps its own running maximum, sum and outputs; they are joined in shared memory
-// and then over the cluster, in a fixed order.
+// and then over the cluster, in a fixed order.  Probabilities are rounded to the activations' type for their product; in fp16, which has no
+// numbers below 2^-24, they are kept times 2^15, since very many small ones count.
 // The new token's row is laid over the cache's in shared memory, and the CTA whose rows it is among writes it to the cache.
+#include <type_traits>
+
 #include "elem.cuh"
 #include "kda_internal.cuh"
 #include "tc.cuh"
@@ -103,6 +106,7 @@ template <typename E, int D, int HG>
 __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache_k, E *cache_v, E *o)
 {
     constexpr int KC = D / 32, VC = D / 64;       // 16-byte pieces of a lane: of a row of keys, of a row of values
+    constexpr float P_EXP = std::is_same<E, __half>::value ? 15.f : 0.f;      // probabilities (one at most) are kept times 2^P_EXP
     extern __shared__ __align__(16) unsigned char smem[];
     auto s_o = reinterpret_cast<float (*)[HG][PITCH<D>]>(smem);      // [WARPS], once the queues are empty
     __shared__ float s_m[WARPS][HG], s_l[WARPS][HG], s_mc[HG], s_lc[HG];
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 2) window_step(const Step p, E *cache
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    s[t][j + k] = tc::ex2_ftz((s[t][j + k] - less) * p.c);      // (the difference first: scores may be of any size)
+                    s[t][j + k] = tc::ex2_ftz(fmaf(s[t][j + k] - less, p.c, P_EXP));      // (the difference first: scores may be of any size)
                     l += s[t][j + k];
                 }
         };

@@ -169,3 +169,19 @@ def test_very_many_small_probabilities_in_fp16():
     bound = 2 * ROUND["f16"] * want + TOL32 * want + 2.0 ** -32 * 8 * T
     assert np.all(np.abs(got - want[:, None]) <= bound[:, None])
     assert np.all(np.abs(_values(lse)[0, rows] - (17.5 + np.log1p(small))) <= TOL32 * 18)
+
+
+@pytest.mark.parametrize("H", [1, 12])
+def test_very_many_small_probabilities_in_fp16_in_the_step(H):
+    """The same in a cache; the step keeps probabilities times 2^14 at least."""
+    import torch
+    n, d = 65536, 64
+    ck = torch.zeros(1, 1, n, d, dtype=torch.float16, device="cuda")
+    cv = torch.full_like(ck, 64.0)
+    q = torch.zeros(1, H, d, dtype=torch.float16, device="cuda")
+    q[..., 0], ck[0, 0, 0, 0], cv[0, 0, 0] = 4.0, 4.375, 0.0
+    k, v = torch.zeros(1, 1, d, dtype=torch.float16, device="cuda"), torch.full((1, 1, d), 64.0, dtype=torch.float16, device="cuda")
+    o = _step(dict(q=q, k=k, v=v, cache_k=ck, cache_v=cv), None, [n - 1], 1.0, n, 0)
+    small = (n - 1) * np.exp(-17.5)
+    want = 64 * small / (1 + small)
+    assert np.all(np.abs(_values(o) - want) <= 2 * ROUND["f16"] * want + TOL32 * want + 2.0 ** -39 * 64 * n)
