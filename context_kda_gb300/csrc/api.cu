@@ -738,16 +738,24 @@ bool head_rows_ok(const kda::HeadIn &a, int32_t type, const kda::HeadOut &x)
 
 }  // namespace
 
+// A frequency over 2 pi as two doubles, 107 bits of it: with 53 alone the fraction of a turn is off by 2^-53 of itself, which the position
+// multiplies.  Each of the two is cut into 32-bit halves exactly (a remainder and a difference without rounding), of either sign.
 extern "C" int kda_rotary_phases(const double *frequencies, int32_t n, uint64_t *phases)
 {
     if (n < 0 || (n && (!frequencies || !phases))) return KDA_ERR_INVALID_ARG;
+    constexpr double inv_high = 0x1.45f306dc9c883p-3, inv_low = -0x1.6b01ec5417056p-57;      // 1 / (2 pi)
     for (int32_t i = 0; i < n; ++i) {
-        if (!std::isfinite(frequencies[i])) return KDA_ERR_INVALID_ARG;
-        const double turns = frequencies[i] / 6.283185307179586476925286766559, part = turns - std::floor(turns);
-        // the fraction in two halves of 32 bits; one that rounds up to a whole turn is none
-        const double top = std::floor(std::ldexp(part, 32));
-        const uint64_t low = static_cast<uint64_t>(std::ldexp(part, 64) - std::ldexp(top, 32));
-        phases[i] = (static_cast<uint64_t>(top) << 32) + low;
+        const double f = frequencies[i];
+        if (!std::isfinite(f)) return KDA_ERR_INVALID_ARG;
+        const double turns = f * inv_high, rest = std::fma(f, inv_low, std::fma(f, inv_high, -turns));
+        uint64_t high = 0;
+        double low = 0.0;
+        for (const double x : {turns, rest}) {
+            const double part = std::fmod(x, 1.0), top = std::trunc(std::ldexp(part, 32));
+            high += static_cast<uint64_t>(static_cast<int64_t>(top));
+            low += std::ldexp(part, 64) - std::ldexp(top, 32);
+        }
+        phases[i] = (high << 32) + static_cast<uint64_t>(static_cast<int64_t>(std::llrint(low)));
     }
     return KDA_OK;
 }

@@ -670,8 +670,9 @@ size_t kda_head_norm_rotary_workspace_bytes(int32_t d);
 
 /*
  * kda_rotary_phases -- host: n frequencies (radians a position, any finite values) as 64-bit fractions of a turn, the form in
- * which the calls above take them: position * phase modulo 2^64 is then the angle's fraction of a turn, and far positions
- * lose nothing.  Returns KDA_OK or KDA_ERR_INVALID_ARG.
+ * which the calls above take them, to the nearest (above 2^42 radians as far as 107 bits go): position * phase modulo 2^64 is then the
+ * angle's fraction of a turn, off by the position times 2^-65, 2^-34 of a turn at the farthest.  The calls use its first 32 bits.
+ * Returns KDA_OK or KDA_ERR_INVALID_ARG.
  */
 int kda_rotary_phases(const double *frequencies, int32_t n, uint64_t *phases);
 
