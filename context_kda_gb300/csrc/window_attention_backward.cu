@@ -60,7 +60,7 @@ struct Back {
     int window_blocks;                    // blocks of windows' tiles; the others are the sinks' pieces
 };
 
-// ds is kept times this in fp16: 2 |do| |v| becomes 2^14 to 2^15.
+// ds is kept times this in fp16: 2 |do| |v| becomes 2^14 to 2^15, so that |ds| from 2^-27 of |do| |v| up is a normal number (2^-14).
 __device__ __forceinline__ float ds_factor(float most_do, float most_v)
 {
     const float bound = 2.f * most_do * most_v;

@@ -710,7 +710,7 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
  *   dq, dk, dv  out as q, k, v, rows on 16 bytes.  dk and dv are the sums over the heads of each group.
  *   ws, ws_bytes    device workspace of at least kda_window_attention_workspace_bytes bytes, 16-byte aligned.
  * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products (fp16: kept times powers of two, so that
- * they neither overflow nor fade; that of ds goes by the longest finite rows of do and v of all sequences, |ds| from 2^-29 of their product
+ * they neither overflow nor fade; that of ds goes by the longest finite rows of do and v of all sequences, |ds| from 2^-27 of their product
  * up keeps its bits).  No sequence sees another's values otherwise; an infinity or NaN of a sequence may reach all of that
  * sequence's gradients.  The same call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
  */
