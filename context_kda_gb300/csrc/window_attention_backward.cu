@@ -16,9 +16,13 @@
 // of a step are computed while the scores of the next are.  (Tiles of 64 with two buffers of everything fit too, but products
 // with N = 64 are bound by shared memory: 57 cycles where 32 would do.)
 //
-// D_i from the output carries that output's rounding.  Where a row sees many keys the rest hides it, where it sees few it would be as large as
-// the rounding of ds.  The first queries of a sequence, and all with a narrow window, go over their tiles twice: sum_j ds_ij,
-// which is zero with the right D, corrects D first, and the corrected D is left for the keys.
+// D_i from the output carries that output's rounding (and that of its probabilities): u sum_c |do_c| (sum_j p_ij |v_jc| + |o_ic|) at most,
+// and ds_ij is off by p_ij times that.  In a row that spreads its weight over many keys the rounding of ds itself is larger; in one that
+// sees few, or puts nearly all its weight on few of many, ds is next to nothing and the error stays: it is the larger one
+// there.  Rows that see few can be told beforehand: the first queries of a sequence, and all with a narrow window, go over their
+// tiles twice: sum_j ds_ij, which is zero with the right D, corrects D first, and the corrected D is left for the keys.  The others keep
+// the output's D, since a second pass over all tiles is two products more for seven.  dq of random rows of 2000 keys in bf16 is off by 0.24 %
+// against 64 bits, as with an exact D; with scores 4 times as wide by 0.37 % (exact 0.24 %), 16 times 0.67 %.
 //
 // Sinks are seen by every later query of their sequence.  Their tile's window part is worked as any other; the rest is cut into
 // pieces of CHUNK queries, each a CTA's, which leave sums in fp32 in the workspace, and a last kernel adds those in order.

@@ -693,9 +693,10 @@ enum { KDA_WINDOW_MAX_SINKS = 128 };
  *   window          at least 1.   sinks   0 to KDA_WINDOW_MAX_SINKS (more: KDA_ERR_UNSUPPORTED).
  *   o           out [T][H][d], rows on 16 bytes.
  *   lse         out fp32 [H][T] or NULL: log sum_j exp(scale q_i . k_j), what the backward needs.
- * Scores, maxima and sums are fp32; probabilities are rounded to 'type' for their product with v.  A value (or score) that a
- * query does not see has no part in its row, also where it is infinite or NaN; no sequence sees another's.  The same call
- * gives the same bits.  T up to 2^31 - 513, (T / 128 + N) H below 2^30, H d below 2^31, token strides below 2^39 (others:
+ * Scores, maxima and sums are fp32; probabilities are rounded to 'type' for their product with v (fp16: kept times 2^7, so that each is
+ * off by half a step or 2^-32 of the row's largest).  Scores may have any size, minus infinity too where a row has others.  A value (or
+ * score) that a query does not see has no part in its row, also where it is infinite or NaN; no sequence sees another's.  The same
+ * call gives the same bits.  T up to 2^31 - 513, (T / 128 + N) H below 2^30, H d below 2^31, token strides below 2^39 (others:
  * KDA_ERR_UNSUPPORTED).
  * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA; a bounded wait that gave up is reported by
  * kda_device_status() as KDA_ERR_TIMEOUT.
@@ -709,10 +710,13 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
  *   q ... sinks     the forward's inputs.   o, lse  what it returned.   d_o  [T][H][d], rows on 16 bytes.
  *   dq, dk, dv  out as q, k, v, rows on 16 bytes.  dk and dv are the sums over the heads of each group.
  *   ws, ws_bytes    device workspace of at least kda_window_attention_workspace_bytes bytes, 16-byte aligned.
- * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products (fp16: kept times powers of two, so that
- * they neither overflow nor fade; that of ds goes by the longest finite rows of do and v of all sequences, |ds| from 2^-27 of their product
- * up keeps its bits).  No sequence sees another's values otherwise; an infinity or NaN of a sequence may reach all of that
- * sequence's gradients.  The same call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
+ * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products.  do . o carries the rounding of o, which is
+ * what dq and dk are off by where nearly all of a row's weight is on few of many keys.  p is made from lse and is off by 2^-23 |lse| of
+ * itself: scores beyond 2^20 have no gradients to speak of, beyond 2^28 they may be infinite or NaN.
+ * fp16: p and ds are kept times powers of two, so that they neither overflow nor fade; that of ds goes by the longest finite rows of do
+ * and v of a key head in all sequences, and |ds| from 2^-27 of their product up keeps its bits.
+ * No sequence sees another's values otherwise; an infinity or NaN of a sequence may reach all of that sequence's gradients.  The same
+ * call gives the same bits.  Returns as the forward, or KDA_ERR_WORKSPACE.
  */
 int kda_window_attention_backward(const int32_t *plan, const int32_t *plan_dev, int32_t H, int32_t Hk, int32_t d, int32_t type,
                                   const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, float scale,
