@@ -821,10 +821,8 @@ int window_in_ok(const int32_t *plan, const int32_t *plan_dev, const kda::Window
     if (const int rc = window_shape_ok(in, type)) return rc;
     const int64_t w = static_cast<int64_t>(in.H) * in.d, wk = static_cast<int64_t>(in.Hk) * in.d;
     if (!rows16_ok(in.q, in.ldq, w) || !rows16_ok(in.k, in.ldk, wk) || !rows16_ok(in.v, in.ldv, wk)) return KDA_ERR_INVALID_ARG;
-    // a head's tiles of 128 tokens, and one more for each sequence, are blocks of one grid, with the sinks' pieces at most twice as many;
+    if (!kda::window_sizes_ok(plan[KDA_PH_T], plan[KDA_PH_N], in.H)) return KDA_ERR_UNSUPPORTED;
     // tensor maps hold strides below 2^40 bytes
-    const int64_t T = plan[KDA_PH_T], N = plan[KDA_PH_N];
-    if (T > kda::WINDOW_MAX_T || (T / 128 + N) * in.H > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
     if (!map_stride_ok(in.ldq) || !map_stride_ok(in.ldk) || !map_stride_ok(in.ldv)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

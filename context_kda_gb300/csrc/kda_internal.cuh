@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/kda.h"
+#include "window_limits.h"
 
 namespace kda {
 
@@ -304,7 +305,6 @@ size_t window_workspace_bytes(int T, int N, int H, int Hk, int d, int W, int S);
 cudaError_t launch_window_backward(const int32_t *plan_host, const int32_t *plan_dev, int type, const WindowIn &in, const WindowGrads &g, void *ws,
                                    cudaStream_t stream);
 int take_window_back_status();
-constexpr int WINDOW_MAX_T = INT32_MAX - 512;    // a tile's rows behind the last token are 32-bit numbers too
 int take_window_status();
 
 struct StepIn {
