@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool right = plan_matches(p.plan, p.sig);
     if (p.N > FEW && !right) {
         if (tid == 0 && blockIdx.x == 0) record_status(&g_window_back_status, KDA_ERR_INVALID_ARG);
+        grid_dep_wait();                                 // the rows' D is still being written: the call ends when that has
         return;
     }
     // ---- the CTA's work
