@@ -131,3 +131,33 @@ def test_fill_refuses_a_device_plan_of_another_launch():
     kda.kda_window_cache_fill(plan, other, s, k, v, 50, 4, *got)
     assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
     assert all(torch.equal(a, b) for a, b in zip(got, empty))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_rows_whose_offsets_pass_32_bits(kind):
+    """Every tensor a column range of rows 2^24 elements apart: the last ones start behind 2^31 elements."""
+    import torch
+    from context_kda_gb300 import binding as kda
+    lengths, H, Hk, d, window, sinks = (100, 41), 4, 2, 64, 50, 3
+    T = sum(lengths)
+    t = torch_type(kind)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    wide = torch.empty(T, 2 ** 24, dtype=t, device="cuda")
+    shapes = dict(q=H, k=Hk, v=Hk, o=H, do=H, dq=H, dk=Hk, dv=Hk)
+    far = {n: wide[:, 4096 * i:4096 * i + h * d].unflatten(1, (h, d)) for i, (n, h) in enumerate(shapes.items())}
+    near = {n: torch.randn(T, h, d, generator=gen, device="cuda").to(t) for n, h in shapes.items()}
+    for n in ("q", "k", "v", "do"):
+        far[n].copy_(near[n])
+    plan = kda.kda_plan_segments(_cu(lengths), 1)
+    plan_dev = kda.upload_plan(plan)
+    ws = torch.empty(kda.kda_window_attention_workspace_bytes(plan, H, Hk, d, window, sinks), dtype=torch.uint8, device="cuda")
+    for x in (near, far):
+        lse = torch.empty(H, T, device="cuda")
+        kda.kda_window_attention_forward(plan, plan_dev, x["q"], x["k"], x["v"], 0.125, window, sinks, x["o"], lse)
+        kda.kda_window_attention_backward(plan, plan_dev, x["q"], x["k"], x["v"], 0.125, window, sinks, x["o"], lse, x["do"],
+                                          x["dq"], x["dk"], x["dv"], ws)
+        x["cache"] = [torch.zeros(2, Hk, window + sinks, d, dtype=t, device="cuda") for _ in range(2)]
+        kda.kda_window_cache_fill(plan, plan_dev, None, x["k"], x["v"], window, sinks, *x["cache"])
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(near[n], far[n]), n
+    assert all(torch.equal(a, b) for a, b in zip(near["cache"], far["cache"]))
