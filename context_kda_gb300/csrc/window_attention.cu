@@ -9,14 +9,14 @@
 // the last is done, so whatever the issuing warp waits for stands still: it waits for probabilities only, and warp 2 adds
 // its arrival to theirs once the tile's values and the next keys are there.  One warp issues for both row tiles in turn; two
 // warps that issue as they can drift into step, and both row tiles' softmax then meets idle tensor cores (329 us for 261).
-// A row's maximum is followed lazily: O is multiplied up only when the maximum has grown by more than 2^8 since, which
-// fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes first, so that there always is a maximum (minus
-// infinity where a row's scores are).
+// A row's maximum is followed lazily (a published method for this hardware, as two row tiles in turn are): O is multiplied up only when
+// the maximum has grown by more than 2^8 since, which fp32 sums and 16-bit probabilities hold easily; the diagonal tile comes
+// first, so that there always is a maximum (minus infinity where a row's scores are).
 // Probabilities are rounded to the activations' type (half a step of it relative, as the output itself); their sum is kept in fp32 from
 // the values before rounding.  fp16 has no numbers below 2^-24, and very many small probabilities count: there they are kept
 // times 2^7, each off by half a step or 2^-32 of the row's largest.
 // Bound by the tensor cores' issue where much is visible: 8192 tokens x 16 heads (4 key heads) of 128, all visible, 201 us, 73 % of the dense
-// bf16 rate counted over visible pairs; by the way in and out of a CTA where little is: 32768 tokens in 24 sequences, window 1024, 260 us
+// bf16 rate counted over visible pairs; by the way in and out of a CTA where little is: 32768 tokens in 24 sequences, window 1024, 258 us
 // (38 %); 1024 x 8 heads 19 us.
 //
 // Values behind a masked place are multiplied by a probability of zero, which an infinity or NaN would survive.  Warp 2

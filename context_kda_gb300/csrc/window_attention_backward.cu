@@ -27,8 +27,11 @@
 // Sinks are seen by every later query of their sequence.  Their tile's window part is worked as any other; the rest is cut into
 // pieces of CHUNK queries, each a CTA's, which leave sums in fp32 in the workspace, and a last kernel adds those in order.
 //
-// Bound by the products and, beside them, p and ds: 8192 tokens x 16 heads (4 key heads) of 128, window 1024, bf16, 240 us, 36 % of the dense rate
-// (half of it, counting the two products done twice); 8 heads of 64 in fp16, documents of any length, 155 to 165 us (16 %).
+// Bound by the products and, beside them, p and ds, and by the ends of the two launches: 8192 tokens x 16 heads (4 key heads) of 128, window 1024,
+// bf16, 240 us, 36 % of the dense rate (half of it, counting the two products done twice); 8 heads of 64 in fp16, documents of any length, 150 to
+// 180 us (14 to 16 %).  Tiles are launched last to first.  For queries that is most work first; for keys it is the reverse: the first ones are
+// seen by the most queries and start last, and with shared key heads a CTA walks all heads of its group.  A list schedule of the documents'
+// keys takes 46 to 62 steps where 40 to 47 are the mean, of 8192 x (16, 4) heads with everything visible 363 for 221.
 //
 // fp16 has a narrow range: p is kept times 2^10, ds times a power of two for each key head, from the longest rows of do and v
 // (|ds| <= 2 |do| |v|), so that it neither overflows nor fades.  bf16 needs neither.

@@ -8,7 +8,7 @@
 // the rows of one (token, key head); a warp takes 16 rows at a time, which are contiguous, as one bulk copy of keys and one of
 // values, STAGES of them in turn, each warp with its own barriers.  How the bytes are asked for is what decides: without any work on
 // them, the 807 MB of 64 tokens x 8 key heads over up to 4100 rows of 128 take 133 us as bulk copies of 4 KB, 160 us a row at a time and
-// 180 us with 16 bytes a lane (cp.async).  With the work and as separate calls 127 to 134 us, 6.0 to 6.3 TB/s, where a copy runs at 6.8.
+// 180 us with 16 bytes a lane (cp.async).  With the work and as separate calls 123 to 131 us, 6.1 to 6.5 TB/s, where a copy runs at 6.8.
 // The products (mma, whose rate does not matter here) may take channels and rows in any order, so a lane's 16 bytes of keys are
 // its part of two K steps, and its 16 bytes each of four rows of values, interleaved, are its part of eight N tiles: no lane needs
 // another's bytes.  Rows follow one another without a gap, so lanes of odd rows take their pieces in another order and swap them
@@ -335,7 +335,7 @@ cudaError_t step(Step p, void *cache_k, void *cache_v, void *o, cudaStream_t str
     p.blocks = (p.g + HG - 1) / HG;
     const int64_t units = static_cast<int64_t>(in.B) * in.Hk * p.blocks;
     // three rounds of CTAs (two an SM) and more, since lengths differ, but none with fewer than 64 rows of a full cache (its way in and out
-    // would take longer): 64 tokens x 8 key heads over up to 4100 rows of 128, any length, 127 to 134 us, with half as many CTAs 138 us,
+    // would take longer): 64 tokens x 8 key heads over up to 4100 rows of 128, any length, 123 to 134 us, with half as many CTAs 138 us,
     // twice as many 130 us; with all caches full, where nothing is uneven, 170, 158 and 172 us.  2 tokens x 4 over 1028 rows: 8.2 us
     p.split = 1;
     while (p.split < MAX_SPLIT && units * p.split < 6 * sm_count() && (in.W + in.S) / (2 * p.split) >= 64) p.split *= 2;

@@ -640,6 +640,7 @@ enum { KDA_PAIRS_HALVES = 0, KDA_PAIRS_ADJACENT = 1 };
  *   rot             rotated channels: a multiple of 16 up to d (others: KDA_ERR_UNSUPPORTED); 0: no rotation.
  *   pairs           KDA_PAIRS_HALVES: channels i and i + rot / 2; KDA_PAIRS_ADJACENT: 2 i and 2 i + 1.
  *   q_out, k_out out as q, k; may be q, k themselves (same address and stride).
+ * Computed in fp32, sums of squares too (a head whose sum passes 2^128 has a norm of zeros), and rounded once.
  * T = 0 is a call without work.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
  */
 int kda_head_norm_rotary_forward(int64_t T, int32_t H, int32_t Hk, int32_t d, int32_t type, const void *q, int64_t ldq,
@@ -754,6 +755,7 @@ int kda_window_cache_fill(const int32_t *plan, const int32_t *plan_dev, int32_t 
  *   q, o            [B][H][d];   k, v  [B][Hk][d]; rows on 16 bytes.   H, Hk, d, type, scale, window, sinks as in
  *                   kda_window_attention_forward.
  *   cache_k, cache_v  in/out, above.  Rows that no token has been put into have no part in it.
+ * Numerics as the forward's (fp16: probabilities are kept times 2^15).
  * B = 0 is a call without work.  The same call gives the same bits.  Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (as
  * the forward; also more than 2^31 - 1 blocks, 8 B Hk ceil(H / Hk / 8)) or KDA_ERR_CUDA; a bounded wait that gave up is
  * reported by kda_device_status() as KDA_ERR_TIMEOUT.
