@@ -713,7 +713,7 @@ int kda_window_attention_forward(const int32_t *plan, const int32_t *plan_dev, i
  *   ws, ws_bytes    device workspace of at least kda_window_attention_workspace_bytes bytes, 16-byte aligned.
  * Sums are fp32; p and ds = p (do . v - do . o) are rounded to 'type' for their products.  do . o carries the rounding of o, which is
  * what dq and dk are off by where nearly all of a row's weight is on few of many keys.  p is made from lse and is off by 2^-23 |lse| of
- * itself: scores beyond 2^20 have no gradients to speak of, beyond 2^28 they may be infinite or NaN.
+ * itself: scores beyond 2^20 have no gradients to speak of, beyond 2^24 they may be infinite or NaN.
  * fp16: p and ds are kept times powers of two, so that they neither overflow nor fade; that of ds goes by the longest finite rows of do
  * and v of a key head in all sequences, and |ds| from 2^-27 of their product up keeps its bits.
  * No sequence sees another's values otherwise; an infinity or NaN of a sequence may reach all of that sequence's gradients.  The same
